@@ -15,9 +15,19 @@ The three steps (crate alice-llm 2.0.0, module sparse_attention):
 * :func:`sa_forward_combine` - steps 2 and 3 on a built index (one fused
   kernel for batches of one query per sequence);
 * :func:`sa_attention` - the three on one stream without a host sync.
+
+Around them, for serving:
+
+* :func:`sa_store_kv` - new tokens' K/V into the paged cache (f32, bf16, or 8
+  bits with a scale per page and kv head);
+* :func:`sa_block_bounds` - the smallest and largest key per channel of the
+  blocks that got new tokens;
+* :func:`sa_select_blocks` - each query's topk blocks by those bounds: the
+  ``selected`` of the steps above.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from dataclasses import dataclass
 
@@ -25,13 +35,14 @@ import numpy as np
 import torch
 
 from . import _native
-from ._native import (DTYPE_BF16, DTYPE_F32, PATH_AUTO, PATH_CUDA_CORE, PATH_CUDA_CORE_GENERAL,
+from ._native import (DTYPE_BF16, DTYPE_E4M3, DTYPE_F32, DTYPE_INT8, PATH_AUTO, PATH_CUDA_CORE, PATH_CUDA_CORE_GENERAL,
                       PATH_FUSED_DECODE, PATH_TENSOR_CORE, PATH_TENSOR_CORE_TF32, STATUS_NAMES)
 
 __all__ = ["SAError", "Index", "sa_index_query_sizes", "sa_build_index",
            "sa_build_index_no_alloc", "sa_forward", "sa_forward_combine", "sa_forward_kernel_name",
            "sa_attention_kernel_name", "PATH_FUSED_DECODE",
-           "sa_combine", "sa_attention", "sa_get_status", "sa_clear_status", "sa_status_string",
+           "sa_combine", "sa_attention", "sa_store_kv", "sa_block_bounds", "sa_select_blocks",
+           "allocate_select_workspace", "sa_get_status", "sa_clear_status", "sa_status_string",
            "sa_version", "allocate_index", "PATH_AUTO", "PATH_CUDA_CORE", "PATH_TENSOR_CORE",
            "PATH_TENSOR_CORE_TF32",
            "PATH_CUDA_CORE_GENERAL", "AttentionGraph", "sa_debug_stall", "sa_debug_cta_stats", "STALL_NONE",
@@ -474,6 +485,190 @@ class AttentionGraph:
     def replay(self):
         self.graph.replay()
         return self.out, self.lse
+
+
+def _on(dev):
+    """The device of the call's tensors as the current one, where it is not."""
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
+_CACHE_DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16,
+                 torch.float8_e4m3fn: DTYPE_E4M3, torch.int8: DTYPE_INT8}
+_ACT_DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+
+
+def _cache_dtype(pages, name):
+    if not isinstance(pages, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if pages.dtype not in _CACHE_DTYPES:
+        raise TypeError(f"{name} must be float32, bfloat16, float8_e4m3fn or int8, got {pages.dtype}")
+    if pages.dim() != 4:
+        raise ValueError(f"{name} must be [num_pages, hkv, page_size, head_dim]")
+    return _CACHE_DTYPES[pages.dtype]
+
+
+def _scales(scales, pages, name):
+    """The scales [num_pages, hkv] of an 8-bit cache (None for the others)."""
+    if pages.dtype not in (torch.float8_e4m3fn, torch.int8):
+        if scales is not None:
+            raise ValueError(f"{name}: a {pages.dtype} cache has no scales")
+        return None
+    if scales is None:
+        raise ValueError(f"{name} [num_pages, hkv] are needed with a {pages.dtype} cache")
+    _require(scales, torch.float32, name, pages.device)
+    if tuple(scales.shape) != tuple(pages.shape[:2]):
+        raise ValueError(f"{name} must be {tuple(pages.shape[:2])}, got {tuple(scales.shape)}")
+    return scales
+
+
+def _batch_args(cu_seqlens_q_host, cu_seqlens_q, used_kv_lens, tables, dev, name):
+    """Host prefix lengths after the checks that sequences and tables agree."""
+    cu_h = _host_i64(cu_seqlens_q_host)
+    batch = cu_h.size - 1
+    _require(cu_seqlens_q, torch.int64, "cu_seqlens_q", dev)
+    _require(used_kv_lens, torch.int32, "used_kv_lens", dev)
+    if cu_seqlens_q.numel() != cu_h.size or used_kv_lens.numel() != batch:
+        raise ValueError("cu_seqlens_q [batch + 1] and used_kv_lens [batch] disagree with "
+                         "cu_seqlens_q_host")
+    for t, n in zip(tables, name):
+        _require(t, torch.int32, n, dev)
+        if t.dim() != 2 or t.shape[0] != batch:
+            raise ValueError(f"{n} must have a row for each of the {batch} sequences")
+    return cu_h, batch
+
+
+def _status_word(status, dev):
+    if status is not None:
+        _require(status, torch.int64, "status", dev)
+    return _ptr(status)
+
+
+def sa_store_kv(k, v, k_pages, v_pages, block_tables, cu_seqlens_q_host, cu_seqlens_q,
+                used_kv_lens, k_scales=None, v_scales=None, status=None, stream=None) -> None:
+    """Store new tokens' K/V rows in the paged cache.  ``k``, ``v`` [tq, hkv,
+    d] float32 or bfloat16, channels contiguous (slices of a fused projection
+    will do); ``used_kv_lens`` the lengths with the new tokens, which take each
+    sequence's last positions.  A float8_e4m3fn or int8 cache has ``k_scales``
+    and ``v_scales`` [num_pages, hkv], renewed with the pages (powers of two;
+    see sa.h).  ``status``: a zeroed int64 CUDA tensor that keeps the first
+    device-detected error."""
+    code = _cache_dtype(k_pages, "k_pages")
+    dev = k_pages.device
+    _require(k_pages, k_pages.dtype, "k_pages", dev)
+    _require(v_pages, k_pages.dtype, "v_pages", dev)
+    if v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages and v_pages must have one shape")
+    num_pages, hkv, page_size, d = (int(x) for x in k_pages.shape)
+    for t, name in ((k, "k"), (v, "v")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype not in _ACT_DTYPES or t.dtype != k.dtype:
+            raise TypeError(f"{name} must be float32 or bfloat16 (both alike), got {t.dtype}")
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+        if t.dim() != 3 or tuple(t.shape) != (k.shape[0], hkv, d):
+            raise ValueError(f"{name} must be [tq, {hkv}, {d}], got {tuple(t.shape)}")
+        if t.numel() and t.stride(2) != 1:
+            raise ValueError(f"{name}: channels must be contiguous")
+    ks, vs = _scales(k_scales, k_pages, "k_scales"), _scales(v_scales, v_pages, "v_scales")
+    cu_h, batch = _batch_args(cu_seqlens_q_host, cu_seqlens_q, used_kv_lens, (block_tables,), dev,
+                              ("block_tables",))
+    with _on(dev):
+        _check(_native.load().sa_store_kv(
+            _ptr(k), _ptr(v), _ACT_DTYPES[k.dtype], k.stride(0), k.stride(1), v.stride(0),
+            v.stride(1), _ptr(k_pages), _ptr(v_pages), _ptr(ks), _ptr(vs), num_pages, code,
+            _ptr(block_tables), int(block_tables.shape[1]), cu_h.ctypes.data_as(ctypes.c_void_p),
+            _ptr(cu_seqlens_q), batch, int(k.shape[0]), _ptr(used_kv_lens), hkv, d, page_size,
+            _status_word(status, dev), _stream(stream, dev)), "sa_store_kv")
+
+
+def _check_bounds(bounds, hkv, d, dev):
+    _require(bounds, torch.bfloat16, "bounds", dev)
+    if bounds.dim() != 4 or tuple(bounds.shape[1:]) != (hkv, 2, d):
+        raise ValueError(f"bounds must be [rows, {hkv}, 2, {d}], got {tuple(bounds.shape)}")
+
+
+def sa_block_bounds(k_pages, block_tables, cu_seqlens_q_host, cu_seqlens_q, used_kv_lens, bounds,
+                    bound_tables, block_size, k_scales=None, status=None, stream=None):
+    """Renew the bounds of every block that holds a new token: ``bounds``
+    [rows, hkv, 2, d] bfloat16 (smallest, largest key per channel), row
+    ``bound_tables[b, j]`` (int32 [batch, msb], -1 = skip) for block j of
+    sequence b.  Returns ``bounds``."""
+    code = _cache_dtype(k_pages, "k_pages")
+    dev = k_pages.device
+    _require(k_pages, k_pages.dtype, "k_pages", dev)
+    num_pages, hkv, page_size, d = (int(x) for x in k_pages.shape)
+    ks = _scales(k_scales, k_pages, "k_scales")
+    _check_bounds(bounds, hkv, d, dev)
+    cu_h, batch = _batch_args(cu_seqlens_q_host, cu_seqlens_q, used_kv_lens,
+                              (block_tables, bound_tables), dev, ("block_tables", "bound_tables"))
+    with _on(dev):
+        _check(_native.load().sa_block_bounds(
+            _ptr(k_pages), _ptr(ks), num_pages, code, _ptr(block_tables),
+            int(block_tables.shape[1]), cu_h.ctypes.data_as(ctypes.c_void_p), _ptr(cu_seqlens_q),
+            batch, int(cu_h[-1]), _ptr(used_kv_lens), hkv, d, int(block_size), page_size,
+            _ptr(bound_tables), int(bound_tables.shape[1]), int(bounds.shape[0]), _ptr(bounds),
+            _status_word(status, dev), _stream(stream, dev)), "sa_block_bounds")
+    return bounds
+
+
+def allocate_select_workspace(tq, batch, hkv, head_dim, msb, device) -> torch.Tensor:
+    """Scratch for :func:`sa_select_blocks` over these sizes (msb: columns of
+    the bound tables), to be kept from call to call."""
+    n = ctypes.c_size_t(0)
+    _check(_native.load().sa_select_workspace_size(tq, batch, hkv, head_dim, msb, ctypes.byref(n)),
+           "sa_select_workspace_size")
+    return torch.empty(n.value + 256, dtype=torch.uint8, device=device)
+
+
+def sa_select_blocks(q, bounds, bound_tables, cu_seqlens_q_host, cu_seqlens_q, used_kv_lens,
+                     block_size, topk, causal, sink_blocks=0, local_blocks=0, selected=None,
+                     workspace=None, status=None, stream=None):
+    """Each (query, kv head)'s ``topk`` blocks with the highest upper bound of
+    q.k summed over the GQA lanes: ``selected`` [tq, hkv, topk] int32,
+    ascending, -1 behind the last.  ``q`` [tq, hq, d] float32 or bfloat16;
+    ``bounds`` and ``bound_tables`` as in :func:`sa_block_bounds`;
+    ``sink_blocks`` first and ``local_blocks`` last blocks always come in."""
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    if q.dtype not in _ACT_DTYPES:
+        raise TypeError(f"q must be float32 or bfloat16, got {q.dtype}")
+    _require(q, q.dtype, "q")
+    dev = q.device
+    if q.dim() != 3 or not isinstance(bounds, torch.Tensor) or bounds.dim() != 4:
+        raise ValueError("q must be [tq, hq, d], bounds [rows, hkv, 2, d]")
+    tq, hq, d = (int(x) for x in q.shape)
+    hkv = int(bounds.shape[1])
+    _check_bounds(bounds, hkv, d, dev)
+    cu_h, batch = _batch_args(cu_seqlens_q_host, cu_seqlens_q, used_kv_lens, (bound_tables,), dev,
+                              ("bound_tables",))
+    msb = int(bound_tables.shape[1])
+    if selected is None:
+        selected = torch.empty((tq, hkv, int(topk)), dtype=torch.int32, device=dev)
+    else:
+        _require(selected, torch.int32, "selected", dev)
+        if tuple(selected.shape) != (tq, hkv, int(topk)):
+            raise ValueError(f"selected must be {(tq, hkv, int(topk))}, got {tuple(selected.shape)}")
+    if workspace is None:
+        workspace = allocate_select_workspace(tq, batch, hkv, d, msb, dev)
+        if stream is not None:
+            workspace.record_stream(stream)
+            selected.record_stream(stream)
+    else:
+        _require(workspace, torch.uint8, "workspace", dev)
+    base = workspace.data_ptr()
+    aligned = (base + 255) & ~255
+    with _on(dev):
+        _check(_native.load().sa_select_blocks(
+            _ptr(q), _ACT_DTYPES[q.dtype], tq, hq, hkv, d, _ptr(bounds), int(bounds.shape[0]),
+            _ptr(bound_tables), msb, cu_h.ctypes.data_as(ctypes.c_void_p), _ptr(cu_seqlens_q),
+            batch, _ptr(used_kv_lens), int(block_size), int(topk), _causal(causal),
+            int(sink_blocks), int(local_blocks), _ptr(selected), ctypes.c_void_p(aligned),
+            max(workspace.numel() - (aligned - base), 0), _status_word(status, dev),
+            _stream(stream, dev)), "sa_select_blocks")
+    return selected
 
 
 def sa_get_status(index: Index, stream=None) -> int:

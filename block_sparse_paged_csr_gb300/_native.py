@@ -14,7 +14,7 @@ STATUS_NAMES = {
     5: "SELECTED_RANGE", 6: "HEAD_DIM", 7: "EMPTY", 8: "CUDA", 9: "DEVICE_TIMEOUT",
     10: "UNSUPPORTED", 11: "INVALID_ARGUMENT",
 }
-DTYPE_F32, DTYPE_BF16 = 0, 1
+DTYPE_F32, DTYPE_BF16, DTYPE_E4M3, DTYPE_INT8 = 0, 1, 2, 3
 PATH_AUTO, PATH_CUDA_CORE, PATH_TENSOR_CORE, PATH_CUDA_CORE_GENERAL, PATH_FUSED_DECODE = 0, 1, 2, 3, 4
 PATH_TENSOR_CORE_TF32 = 5
 
@@ -24,7 +24,8 @@ EXPORTS = ("sa_status_string", "sa_version", "sa_index_query_sizes", "sa_index_w
            "sa_build_index_no_alloc", "sa_forward", "sa_forward_ex", "sa_forward_combine",
            "sa_forward_combine_ex", "sa_forward_kernel_name", "sa_attention_kernel_name",
            "sa_combine", "sa_combine_ex", "sa_attention", "sa_attention_ex", "sa_get_status",
-           "sa_clear_status", "sa_debug_stall", "sa_debug_cta_stats")
+           "sa_clear_status", "sa_store_kv", "sa_block_bounds", "sa_select_workspace_size",
+           "sa_select_blocks", "sa_debug_stall", "sa_debug_cta_stats")
 
 
 class SaIndex(ctypes.Structure):
@@ -123,6 +124,18 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.sa_get_status.restype = st
     lib.sa_clear_status.argtypes = [ctypes.POINTER(SaIndex), p]
     lib.sa_clear_status.restype = st
+    lib.sa_store_kv.argtypes = [p, p, st, i64, i64, i64, i64, p, p, p, p, i64, st, p, i32, p, p,
+                                i32, i64, p, i32, i32, i32, p, p]
+    lib.sa_store_kv.restype = st
+    lib.sa_block_bounds.argtypes = [p, p, i64, st, p, i32, p, p, i32, i64, p, i32, i32, i32, i32,
+                                    p, i32, i64, p, p, p]
+    lib.sa_block_bounds.restype = st
+    lib.sa_select_workspace_size.argtypes = [i64, i32, i32, i32, i32,
+                                             ctypes.POINTER(ctypes.c_size_t)]
+    lib.sa_select_workspace_size.restype = st
+    lib.sa_select_blocks.argtypes = [p, st, i64, i32, i32, i32, p, i64, p, i32, p, p, i32, p, i32,
+                                     i32, i32, i32, i32, p, p, ctypes.c_size_t, p, p]
+    lib.sa_select_blocks.restype = st
     lib.sa_debug_stall.argtypes = [i32, ctypes.c_uint32]
     lib.sa_debug_stall.restype = st
     lib.sa_debug_cta_stats.argtypes = [p, i32]

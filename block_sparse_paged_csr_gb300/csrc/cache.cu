@@ -1,0 +1,595 @@
+// Writing the paged K/V cache and the bounds of its blocks.
+//
+// sa_store_kv puts the rows of new tokens into the cache's pages, in any of
+// the cache's types.  The 8-bit types hold a scale for each (page, kv head):
+// s = 2^e, the smallest that brings the page's largest magnitude to the
+// type's range, so that x / s and code * s are exact and only the rounding to
+// a code loses anything.  A page that already holds rows of its sequence and
+// gets a larger value takes the larger scale, and its old codes are rounded to
+// it once (for e4m3 a power of two moves the exponent only, exact but for
+// subnormal codes).
+//
+// sa_block_bounds takes the smallest and the largest key per channel of every
+// block that holds a new token.
+#include <algorithm>
+#include <cstdint>
+
+#include "internal.h"
+#include "seq_common.cuh"
+
+namespace sa {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+
+enum CacheType { kF32 = 0, kBf16 = 1, kE4m3 = 2, kInt8 = 3 };
+
+// ------------------------------------------------------------------ store
+
+struct StoreArgs {
+  const void* src[2];                  // K, V rows of the new tokens
+  int64_t token_stride[2], head_stride[2];   // elements
+  void* pages[2];
+  float* scales[2];
+  int64_t num_pages;
+  const int32_t* block_tables;
+  const int64_t* cu;
+  const int32_t* used;
+  int64_t tq, slots;
+  int32_t batch, hkv, head_dim, page_size, max_pages;
+  int64_t* status;
+};
+
+// 8 consecutive source elements as f32.
+template <bool kSrcBf16>
+__device__ __forceinline__ void load8(const void* src, int64_t off, float (&x)[8]) {
+  if constexpr (kSrcBf16) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(src) + off));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  } else {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(src) + off);
+    const float4 a = __ldg(p), b = __ldg(p + 1);
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  }
+}
+
+// Largest finite magnitude's bits (order-preserving as unsigned).
+__device__ __forceinline__ uint32_t amax_bits(uint32_t m, const float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t u = __float_as_uint(x[i]) & 0x7FFFFFFFu;
+    m = max(m, u < 0x7F800000u ? u : 0u);
+  }
+  return m;
+}
+
+// The smallest power of two s >= 2^-126 with amax <= QMAX * s (0 for amax 0).
+// QMAX = 448 = 1.75 * 2^8 (e4m3) or 127 = 1.984375 * 2^6 (int8): the exponent
+// of amax less 8 or 6, one more where its mantissa lies above QMAX's.
+template <int kType>
+__device__ __forceinline__ float scale_of(uint32_t amax) {
+  if (amax == 0u) return 0.f;
+  const int e = static_cast<int>(amax >> 23) - (kType == kInt8 ? 6 : 8) +
+                ((amax & 0x7FFFFFu) > (kType == kInt8 ? 0x7E0000u : 0x600000u) ? 1 : 0);
+  return __uint_as_float(static_cast<uint32_t>(max(e, 1)) << 23);
+}
+
+// x / s for the page's scale: by the exact reciprocal where s is a power of
+// two (every scale this kernel makes), by division for a caller's own.
+struct Quant {
+  float s, inv;
+  bool pow2;
+  __device__ __forceinline__ explicit Quant(float scale) : s(scale) {
+    const uint32_t u = __float_as_uint(scale);
+    pow2 = (u & 0x7FFFFFu) == 0u && u != 0u;
+    // 2^-e has the exponent field 254 - e; e = 254 (2^127) leaves the
+    // subnormal 2^-127
+    const uint32_t e = u >> 23;
+    inv = pow2 ? (e < 254u ? __uint_as_float((254u - e) << 23) : __uint_as_float(0x00400000u)) : 0.f;
+  }
+  __device__ __forceinline__ float operator()(float x) const {
+    return s == 0.f ? (x == x ? 0.f : x) : (pow2 ? x * inv : __fdiv_rn(x, s));
+  }
+};
+
+// Two values to codes, round to nearest even, beyond the range to its end;
+// NaN stays NaN in e4m3 and becomes 0 in int8.
+template <int kType>
+__device__ __forceinline__ uint32_t to_code2(float x0, float x1) {
+  if constexpr (kType == kE4m3) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(x1), "f"(x0));
+    return r;
+  } else {
+    const int a = __float2int_rn(fminf(fmaxf(x0 == x0 ? x0 : 0.f, -127.f), 127.f));
+    const int b = __float2int_rn(fminf(fmaxf(x1 == x1 ? x1 : 0.f, -127.f), 127.f));
+    return (static_cast<uint32_t>(a) & 0xFFu) | ((static_cast<uint32_t>(b) & 0xFFu) << 8);
+  }
+}
+
+template <int kType>
+__device__ __forceinline__ void store8(void* pages, int64_t off, const float (&x)[8],
+                                       const Quant& qz) {
+  if constexpr (kType == kF32) {
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(pages) + off);
+    p[0] = make_float4(x[0], x[1], x[2], x[3]);
+    p[1] = make_float4(x[4], x[5], x[6], x[7]);
+  } else if constexpr (kType == kBf16) {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(pages) + off) =
+        make_uint4(pack_bf16x2_rn(x[0], x[1]), pack_bf16x2_rn(x[2], x[3]),
+                   pack_bf16x2_rn(x[4], x[5]), pack_bf16x2_rn(x[6], x[7]));
+  } else {
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = to_code2<kType>(qz(x[2 * i]), qz(x[2 * i + 1]));
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(pages) + off) =
+        make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+  }
+}
+
+// One item: the new rows of one (page, kv head) of K or of V, by a warp
+// (kItemWarps = 1: decode steps, a row or a few) or by the whole CTA (prompts:
+// up to a page of rows).  A thread takes 8 elements at a time and keeps its
+// first kHeld pieces in registers between the pass that finds the largest
+// magnitude and the pass that writes codes, so a page of 64 x 128 is read
+// once.
+template <int kType, bool kSrcBf16, int kItemWarps>
+__global__ void __launch_bounds__(kThreads) store_kv_kernel(const StoreArgs a) {
+  constexpr bool kCodes = kType == kE4m3 || kType == kInt8;
+  constexpr int kT = kItemWarps * 32;                 // threads per item
+  constexpr int kHeld = kItemWarps == 1 ? 2 : 4;
+  __shared__ uint32_t s_amax[kWarps];
+  const int lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
+  const int t = kItemWarps == 1 ? lane : static_cast<int>(threadIdx.x);
+  const int64_t item = kItemWarps == 1 ? static_cast<int64_t>(blockIdx.x) * kWarps + warp
+                                       : static_cast<int64_t>(blockIdx.x);
+  const int64_t u = item / (2 * a.hkv);
+  const int rest = static_cast<int>(item - u * (2 * a.hkv));
+  const int h = rest >> 1;
+  const int kv = rest & 1;                            // 0: K, 1: V
+  if (u >= a.slots) return;
+  const int b = warp_slot_sequence(a.cu, a.batch, a.page_size, u, lane);
+  const NewRange nr = new_range(a.cu, a.used, b, a.tq);
+  const int64_t page0 = nr.p0 / a.page_size;
+  const int64_t pg = page0 + (u - slot_base(a.cu[b], b, a.page_size));
+  const int64_t base = pg * a.page_size;
+  if (pg < page0 || base >= nr.p1 || pg >= a.max_pages) return;   // the same for the whole item
+  const int id = a.block_tables[static_cast<int64_t>(b) * a.max_pages + pg];
+  if (id < 0 || id >= a.num_pages) {
+    if (id >= 0 && t == 0) report(a.status, SA_ERR_SHAPE);
+    return;
+  }
+  const int r0 = static_cast<int>(max(nr.p0 - base, int64_t{0}));
+  const int r1 = static_cast<int>(min(nr.p1 - base, static_cast<int64_t>(a.page_size)));
+  // the new tokens end at cu0 + (p1 - p0): a sequence shorter than its new
+  // tokens stores the first of them
+  const int64_t tok0 = nr.cu0 + (base + r0 - nr.p0);
+  const int per_row = a.head_dim >> 3;                // 8-element pieces of a row
+  const int n = (r1 - r0) * per_row;
+  const void* src = a.src[kv];
+  const int64_t ts = a.token_stride[kv];
+  const int64_t src0 = tok0 * ts + h * a.head_stride[kv];
+  void* pages = a.pages[kv];
+  const int64_t dst0 = ((static_cast<int64_t>(id) * a.hkv + h) * a.page_size + r0) * a.head_dim;
+  auto src_at = [&](int i) -> int64_t {
+    const int r = i / per_row;
+    return src0 + r * ts + (i - r * per_row) * 8;
+  };
+
+  float held[kHeld][8];
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < kHeld; ++j)
+    if (t + j * kT < n) load8<kSrcBf16>(src, src_at(t + j * kT), held[j]);
+  float* scale_at = nullptr;
+  float s_old = 0.f;
+  if constexpr (kCodes) {
+    scale_at = a.scales[kv] + static_cast<int64_t>(id) * a.hkv + h;
+    if (r0 > 0) {
+      s_old = *scale_at;
+      if (!(s_old > 0.f && s_old < INFINITY)) s_old = 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j)
+      if (t + j * kT < n) m = amax_bits(m, held[j]);
+    for (int i = t + kHeld * kT; i < n; i += kT) {
+      float x[8];
+      load8<kSrcBf16>(src, src_at(i), x);
+      m = amax_bits(m, x);
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    if constexpr (kItemWarps > 1) {
+      if (lane == 0) s_amax[warp] = m;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kItemWarps; ++w) m = max(m, s_amax[w]);
+    }
+  }
+  const float s_new = kCodes ? fmaxf(s_old, scale_of<kType>(m)) : 1.f;
+  const Quant qz(s_new);
+#pragma unroll
+  for (int j = 0; j < kHeld; ++j)
+    if (t + j * kT < n)
+      store8<kType>(pages, dst0 + static_cast<int64_t>(t + j * kT) * 8, held[j], qz);
+  for (int i = t + kHeld * kT; i < n; i += kT) {
+    float x[8];
+    load8<kSrcBf16>(src, src_at(i), x);
+    store8<kType>(pages, dst0 + static_cast<int64_t>(i) * 8, x, qz);
+  }
+  if constexpr (kCodes) {
+    if (r0 > 0 && s_new > s_old) {
+      // the page's earlier rows to the larger scale
+      const float ratio = __fdiv_rn(s_old, s_new);
+      const Quant one(1.f);
+      uint8_t* old = static_cast<uint8_t*>(pages) + dst0 - static_cast<int64_t>(r0) * a.head_dim;
+      for (int i = t; i < r0 * per_row; i += kT) {
+        const uint2 w = *reinterpret_cast<const uint2*>(old + static_cast<int64_t>(i) * 8);
+        uint32_t f[4];
+        codes4_to_f16<kType == kInt8>(w.x, f[0], f[1]);
+        codes4_to_f16<kType == kInt8>(w.y, f[2], f[3]);
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 v = f16x2_to_f32(f[j]);
+          x[2 * j] = v.x * ratio;
+          x[2 * j + 1] = v.y * ratio;
+        }
+        store8<kType>(old, static_cast<int64_t>(i) * 8, x, one);
+      }
+    }
+    // every thread of the item read the old scale before the reduction above
+    if (t == 0) *scale_at = s_new;
+  }
+}
+
+template <int kType, bool kSrcBf16>
+cudaError_t launch_store(const StoreArgs& a, bool by_warp, cudaStream_t stream) {
+  const int64_t items = a.slots * a.hkv * 2;
+  const int64_t grid = by_warp ? (items + kWarps - 1) / kWarps : items;
+  if (grid > 0x7FFFFFFF) return cudaErrorNotSupported;
+  if (by_warp)
+    store_kv_kernel<kType, kSrcBf16, 1><<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(a);
+  else
+    store_kv_kernel<kType, kSrcBf16, kWarps>
+        <<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <int kType>
+cudaError_t launch_store_src(const StoreArgs& a, bool src_bf16, bool by_warp, cudaStream_t s) {
+  return src_bf16 ? launch_store<kType, true>(a, by_warp, s)
+                  : launch_store<kType, false>(a, by_warp, s);
+}
+
+// ------------------------------------------------------------------ bounds
+
+struct BoundsArgs {
+  const void* k_pages;
+  const float* k_scales;
+  int64_t num_pages;
+  const int32_t* block_tables;
+  const int64_t* cu;
+  const int32_t* used;
+  const int32_t* bound_tables;
+  int64_t num_bounds;
+  uint16_t* bounds;                    // [num_bounds, hkv, 2, head_dim] bf16
+  int64_t tq, slots;
+  int32_t batch, hkv, head_dim, block_size, page_size, max_pages, msb;
+  int64_t* status;
+};
+
+// Elements of a 16-byte piece.
+template <int kType> struct Piece { static constexpr int n = kType == kF32 ? 4 : kType == kBf16 ? 8 : 16; };
+
+// One CTA per (block, kv head).  A thread owns one 16-byte piece of a row (its
+// channels) and every kRows-th row of the block; the codes' minima and maxima
+// are kept as packed f16 (exact) and multiplied by the scale where the page
+// changes; threads of the same channels meet in shared memory.
+template <int kType>
+__global__ void __launch_bounds__(kThreads) block_bounds_kernel(const BoundsArgs a) {
+  constexpr int kN = Piece<kType>::n;
+  constexpr bool kCodes = kType == kE4m3 || kType == kInt8;
+  extern __shared__ float s_part[];                    // [groups][2][head_dim]
+  const int tid = threadIdx.x;
+  const int lane = tid & 31;
+  const int64_t u = blockIdx.x / a.hkv;
+  const int h = static_cast<int>(blockIdx.x - u * a.hkv);
+  const int b = warp_slot_sequence(a.cu, a.batch, a.block_size, u, lane);
+  const NewRange nr = new_range(a.cu, a.used, b, a.tq);
+  const int64_t blk0 = nr.p0 / a.block_size;
+  const int64_t blk = blk0 + (u - slot_base(a.cu[b], b, a.block_size));
+  const int64_t base = blk * a.block_size;
+  if (blk < blk0 || base >= nr.p1 || nr.p0 >= nr.p1 || blk >= a.msb) return;
+  const int row = a.bound_tables[static_cast<int64_t>(b) * a.msb + blk];
+  if (row < 0 || row >= a.num_bounds) {
+    if (row >= 0 && tid == 0) report(a.status, SA_ERR_SHAPE);
+    return;
+  }
+  const int d = a.head_dim;
+  const int per_row = d / kN;                          // pieces of a row
+  const int groups = kThreads / per_row;               // rows taken at a time
+  const int c = tid % per_row;
+  const int g = tid / per_row;
+  const int keys = static_cast<int>(min(nr.p1 - base, static_cast<int64_t>(a.block_size)));
+  const int ps = a.page_size;
+  const int32_t* bt = a.block_tables + static_cast<int64_t>(b) * a.max_pages;
+  const int64_t pg0 = blk * (a.block_size / ps);
+
+  float lo[kN], hi[kN];
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    lo[i] = INFINITY;
+    hi[i] = -INFINITY;
+  }
+  if (g < groups) {
+    // each group of threads takes a contiguous run of keys, so that pages
+    // change as rarely as possible
+    const int run = (a.block_size + groups - 1) / groups;
+    const int k1 = min((g + 1) * run, keys);
+    int k = g * run;
+    while (k < k1) {
+      const int p = k / ps;
+      const int end = min((p + 1) * ps, k1);
+      const int64_t pg = pg0 + p;
+      const int id = pg < a.max_pages ? bt[pg] : -1;
+      if (id < 0 || id >= a.num_pages) {
+        if (id >= 0 && c == 0) report(a.status, SA_ERR_SHAPE);
+        k = end;
+        continue;
+      }
+      const int64_t off = ((static_cast<int64_t>(id) * a.hkv + h) * ps + (k - p * ps)) * d + c * kN;
+      if constexpr (kCodes) {
+        const uint4* at = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.k_pages) + off);
+        const float s = a.k_scales[static_cast<int64_t>(id) * a.hkv + h];
+        __half2 l2[8], h2[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          l2[i] = __half2half2(__ushort_as_half(0x7C00));
+          h2[i] = __half2half2(__ushort_as_half(0xFC00));
+        }
+        const int step = d / 16;
+#pragma unroll 4
+        for (int r = k; r < end; ++r, at += step) {
+          const uint4 w = __ldg(at);
+          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t f0, f1;
+            codes4_to_f16<kType == kInt8>(ww[i], f0, f1);
+            const __half2 x0 = *reinterpret_cast<const __half2*>(&f0);
+            const __half2 x1 = *reinterpret_cast<const __half2*>(&f1);
+            l2[2 * i] = __hmin2(l2[2 * i], x0);
+            h2[2 * i] = __hmax2(h2[2 * i], x0);
+            l2[2 * i + 1] = __hmin2(l2[2 * i + 1], x1);
+            h2[2 * i + 1] = __hmax2(h2[2 * i + 1], x1);
+          }
+        }
+        // (a NaN product, of a scale that is 0 and a channel with NaN keys
+        // only, leaves the other operand)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 l = __half22float2(l2[i]);
+          const float2 m = __half22float2(h2[i]);
+          lo[2 * i] = fminf(lo[2 * i], l.x * s);
+          lo[2 * i + 1] = fminf(lo[2 * i + 1], l.y * s);
+          hi[2 * i] = fmaxf(hi[2 * i], m.x * s);
+          hi[2 * i + 1] = fmaxf(hi[2 * i + 1], m.y * s);
+        }
+      } else if constexpr (kType == kBf16) {
+        const uint16_t* at = static_cast<const uint16_t*>(a.k_pages) + off;
+#pragma unroll 4
+        for (int r = k; r < end; ++r, at += d) {
+          const uint4 w = __ldg(reinterpret_cast<const uint4*>(at));
+          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float x0 = __uint_as_float(ww[i] << 16);
+            const float x1 = __uint_as_float(ww[i] & 0xFFFF0000u);
+            lo[2 * i] = fminf(lo[2 * i], x0);
+            hi[2 * i] = fmaxf(hi[2 * i], x0);
+            lo[2 * i + 1] = fminf(lo[2 * i + 1], x1);
+            hi[2 * i + 1] = fmaxf(hi[2 * i + 1], x1);
+          }
+        }
+      } else {
+        const float* at = static_cast<const float*>(a.k_pages) + off;
+#pragma unroll 4
+        for (int r = k; r < end; ++r, at += d) {
+          const float4 w = __ldg(reinterpret_cast<const float4*>(at));
+          lo[0] = fminf(lo[0], w.x);
+          hi[0] = fmaxf(hi[0], w.x);
+          lo[1] = fminf(lo[1], w.y);
+          hi[1] = fmaxf(hi[1], w.y);
+          lo[2] = fminf(lo[2], w.z);
+          hi[2] = fmaxf(hi[2], w.z);
+          lo[3] = fminf(lo[3], w.w);
+          hi[3] = fmaxf(hi[3], w.w);
+        }
+      }
+      k = end;
+    }
+    float* mine = s_part + static_cast<int64_t>(g) * 2 * d + c * kN;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      mine[i] = lo[i];
+      mine[d + i] = hi[i];
+    }
+  }
+  __syncthreads();
+  uint16_t* out = a.bounds + (static_cast<int64_t>(row) * a.hkv + h) * 2 * d;
+  for (int x = tid; x < 2 * d; x += kThreads) {
+    const bool is_hi = x >= d;
+    float v = s_part[x];
+    for (int g2 = 1; g2 < groups; ++g2) {
+      const float y = s_part[static_cast<int64_t>(g2) * 2 * d + x];
+      v = is_hi ? fmaxf(v, y) : fminf(v, y);
+    }
+    out[x] = static_cast<uint16_t>(is_hi ? bf16_up(v) : bf16_down(v));
+  }
+}
+
+template <int kType>
+cudaError_t launch_bounds(const BoundsArgs& a, cudaStream_t stream) {
+  const int64_t grid = a.slots * a.hkv;
+  if (grid > 0x7FFFFFFF) return cudaErrorNotSupported;
+  const int groups = kThreads / (a.head_dim / Piece<kType>::n);
+  const size_t smem = static_cast<size_t>(groups) * 2 * a.head_dim * sizeof(float);
+  block_bounds_kernel<kType><<<static_cast<unsigned>(grid), kThreads, smem, stream>>>(a);
+  return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------ checks
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+bool known_type(sa_dtype t) { return t >= SA_DTYPE_F32 && t <= SA_DTYPE_INT8; }
+
+bool eight_bit(sa_dtype t) { return t == SA_DTYPE_E4M3 || t == SA_DTYPE_INT8; }
+
+sa_status check_lengths(const int64_t* cu_host, int32_t batch, int64_t tq) {
+  if (cu_host == nullptr || batch < 1 || cu_host[0] != 0) return SA_ERR_CU_SEQLENS;
+  for (int32_t b = 1; b <= batch; ++b)
+    if (cu_host[b] < cu_host[b - 1]) return SA_ERR_CU_SEQLENS;
+  return cu_host[batch] == tq ? SA_OK : SA_ERR_SHAPE;
+}
+
+}  // namespace
+
+}  // namespace sa
+
+extern "C" {
+
+sa_status sa_store_kv(const void* k, const void* v, sa_dtype src_dtype, int64_t k_token_stride,
+                      int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                      void* k_pages, void* v_pages, float* k_scales, float* v_scales,
+                      int64_t num_pages, sa_dtype kv_dtype, const int32_t* block_tables,
+                      int32_t max_pages, const int64_t* cu_seqlens_q_host,
+                      const int64_t* cu_seqlens_q, int32_t batch, int64_t tq,
+                      const int32_t* used_kv_lens, int32_t hkv, int32_t head_dim,
+                      int32_t page_size, int64_t* status, void* stream) {
+  if (hkv <= 0) return SA_ERR_HEAD_COUNT;
+  if (head_dim <= 0 || page_size <= 0) return SA_ERR_BLOCK_PAGE;
+  sa_status st = sa::check_lengths(cu_seqlens_q_host, batch, tq);
+  if (st != SA_OK) return st;
+  if (num_pages < 0 || max_pages < 0) return SA_ERR_SHAPE;
+  if (src_dtype != SA_DTYPE_F32 && src_dtype != SA_DTYPE_BF16) return SA_ERR_INVALID_ARGUMENT;
+  if (!sa::known_type(kv_dtype)) return SA_ERR_INVALID_ARGUMENT;
+  if (head_dim % (sa::eight_bit(kv_dtype) ? 16 : 8) != 0 || head_dim > 256)
+    return SA_ERR_UNSUPPORTED;
+  if (tq == 0) return SA_OK;
+  if (!k || !v || !k_pages || !v_pages || !block_tables || !cu_seqlens_q || !used_kv_lens)
+    return SA_ERR_INVALID_ARGUMENT;
+  if (sa::eight_bit(kv_dtype) && (!k_scales || !v_scales)) return SA_ERR_INVALID_ARGUMENT;
+  if (!sa::aligned16(k) || !sa::aligned16(v) || !sa::aligned16(k_pages) || !sa::aligned16(v_pages))
+    return SA_ERR_INVALID_ARGUMENT;
+  const int64_t unit = src_dtype == SA_DTYPE_BF16 ? 8 : 4;      // elements of 16 bytes
+  if (k_token_stride % unit || k_head_stride % unit || v_token_stride % unit ||
+      v_head_stride % unit)
+    return SA_ERR_INVALID_ARGUMENT;
+
+  sa::StoreArgs a{};
+  a.src[0] = k;
+  a.src[1] = v;
+  a.token_stride[0] = k_token_stride;
+  a.token_stride[1] = v_token_stride;
+  a.head_stride[0] = k_head_stride;
+  a.head_stride[1] = v_head_stride;
+  a.pages[0] = k_pages;
+  a.pages[1] = v_pages;
+  a.scales[0] = k_scales;
+  a.scales[1] = v_scales;
+  a.num_pages = num_pages;
+  a.block_tables = block_tables;
+  a.cu = cu_seqlens_q;
+  a.used = used_kv_lens;
+  a.tq = tq;
+  a.slots = sa::slot_base(tq, batch, page_size);
+  a.batch = batch;
+  a.hkv = hkv;
+  a.head_dim = head_dim;
+  a.page_size = page_size;
+  a.max_pages = max_pages;
+  a.status = status;
+  int64_t longest = 0;
+  for (int32_t b = 0; b < batch; ++b)
+    longest = std::max(longest, cu_seqlens_q_host[b + 1] - cu_seqlens_q_host[b]);
+  // a warp per item while an item is at most eight 8-element pieces a lane
+  const int64_t rows = std::min<int64_t>(longest, page_size);
+  const bool by_warp = rows * head_dim <= 32 * 8 * 8;
+  const bool bf = src_dtype == SA_DTYPE_BF16;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t err;
+  switch (kv_dtype) {
+    case SA_DTYPE_F32: err = sa::launch_store_src<sa::kF32>(a, bf, by_warp, s); break;
+    case SA_DTYPE_BF16: err = sa::launch_store_src<sa::kBf16>(a, bf, by_warp, s); break;
+    case SA_DTYPE_E4M3: err = sa::launch_store_src<sa::kE4m3>(a, bf, by_warp, s); break;
+    default: err = sa::launch_store_src<sa::kInt8>(a, bf, by_warp, s); break;
+  }
+  if (err == cudaErrorNotSupported) return SA_ERR_UNSUPPORTED;
+  return err == cudaSuccess ? SA_OK : SA_ERR_CUDA;
+}
+
+sa_status sa_block_bounds(const void* k_pages, const float* k_scales, int64_t num_pages,
+                          sa_dtype kv_dtype, const int32_t* block_tables, int32_t max_pages,
+                          const int64_t* cu_seqlens_q_host, const int64_t* cu_seqlens_q,
+                          int32_t batch, int64_t tq, const int32_t* used_kv_lens, int32_t hkv,
+                          int32_t head_dim, int32_t block_size, int32_t page_size,
+                          const int32_t* bound_tables, int32_t msb, int64_t num_bounds,
+                          void* bounds, int64_t* status, void* stream) {
+  if (hkv <= 0) return SA_ERR_HEAD_COUNT;
+  if (head_dim <= 0 || block_size <= 0 || page_size <= 0 || block_size % page_size != 0)
+    return SA_ERR_BLOCK_PAGE;
+  sa_status st = sa::check_lengths(cu_seqlens_q_host, batch, tq);
+  if (st != SA_OK) return st;
+  if (num_pages < 0 || max_pages < 0 || msb < 0 || num_bounds < 0) return SA_ERR_SHAPE;
+  if (!sa::known_type(kv_dtype)) return SA_ERR_INVALID_ARGUMENT;
+  if (head_dim % (sa::eight_bit(kv_dtype) ? 16 : 8) != 0 || head_dim > 256)
+    return SA_ERR_UNSUPPORTED;
+  if (tq == 0) return SA_OK;
+  if (!k_pages || !block_tables || !cu_seqlens_q || !used_kv_lens || !bound_tables || !bounds)
+    return SA_ERR_INVALID_ARGUMENT;
+  if (sa::eight_bit(kv_dtype) && !k_scales) return SA_ERR_INVALID_ARGUMENT;
+  if (!sa::aligned16(k_pages) || !sa::aligned16(bounds)) return SA_ERR_INVALID_ARGUMENT;
+
+  sa::BoundsArgs a{};
+  a.k_pages = k_pages;
+  a.k_scales = k_scales;
+  a.num_pages = num_pages;
+  a.block_tables = block_tables;
+  a.cu = cu_seqlens_q;
+  a.used = used_kv_lens;
+  a.bound_tables = bound_tables;
+  a.num_bounds = num_bounds;
+  a.bounds = static_cast<uint16_t*>(bounds);
+  a.tq = tq;
+  a.slots = sa::slot_base(tq, batch, block_size);
+  a.batch = batch;
+  a.hkv = hkv;
+  a.head_dim = head_dim;
+  a.block_size = block_size;
+  a.page_size = page_size;
+  a.max_pages = max_pages;
+  a.msb = msb;
+  a.status = status;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t err;
+  switch (kv_dtype) {
+    case SA_DTYPE_F32: err = sa::launch_bounds<sa::kF32>(a, s); break;
+    case SA_DTYPE_BF16: err = sa::launch_bounds<sa::kBf16>(a, s); break;
+    case SA_DTYPE_E4M3: err = sa::launch_bounds<sa::kE4m3>(a, s); break;
+    default: err = sa::launch_bounds<sa::kInt8>(a, s); break;
+  }
+  if (err == cudaErrorNotSupported) return SA_ERR_UNSUPPORTED;
+  return err == cudaSuccess ? SA_OK : SA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -64,7 +64,9 @@ typedef enum sa_status {
 
 typedef enum sa_dtype {
   SA_DTYPE_F32 = 0,
-  SA_DTYPE_BF16 = 1
+  SA_DTYPE_BF16 = 1,
+  SA_DTYPE_E4M3 = 2,           /* 8-bit float (4 exponent, 3 mantissa bits), K/V only  */
+  SA_DTYPE_INT8 = 3            /* 8-bit integer codes -127..127, K/V only              */
 } sa_dtype;
 
 /* Forward kernel choice (sa_forward / sa_attention `path`). */
@@ -472,6 +474,124 @@ sa_status sa_attention_ex(const float *q, const void *k_pages, const void *v_pag
                           int32_t causal, int32_t split_edges, sa_index *idx,
                           sa_dtype partial_dtype, void *o_partial, float *m_partial,
                           float *l_partial, float *out, float *lse, sa_path path, void *stream);
+
+/*
+ * Writing the paged cache.  The rows of new tokens go to the cache's pages:
+ * new token t of sequence b (row cu_seqlens_q[b] + t of k and v) to position
+ * lk_b - qo_b + t, where lk_b = used_kv_lens[b] is the length WITH the new
+ * tokens and qo_b their number (the positions the right-aligned causal rule
+ * gives the queries of the same call); a sequence with lk_b < qo_b stores its
+ * first lk_b tokens at positions 0.. .  Position p is row p % page_size of
+ * page block_tables[b, p / page_size].
+ *
+ *   k, v          [tq, hkv, head_dim] of src_dtype (f32 or bf16); channels
+ *                 contiguous, tokens and heads at the given strides (elements;
+ *                 multiples of 16 bytes: slices of a fused projection do)
+ *   k_pages,
+ *   v_pages       [num_pages, hkv, page_size, head_dim] of kv_dtype (any)
+ *   k_scales,
+ *   v_scales      [num_pages, hkv] f32 for the 8-bit types, else ignored
+ *   block_tables  [batch, max_pages]; -1: the page's tokens are dropped
+ *   used_kv_lens  [batch] int32, required
+ *   status        a device status word (as sa_index.totals[3]: int64, 0 =
+ *                 none, first error kept) or NULL; the call does not clear it
+ *
+ * f32 rows are rounded to nearest even where the cache is bf16.  The 8-bit
+ * types hold codes and, per (page, kv head), a scale: value = code * scale.
+ * The scale is a power of two, the smallest >= 2^-126 that brings the largest
+ * finite magnitude to at most 448 (e4m3) or 127 (int8); 0 for rows of zeros.
+ * Codes are rounded to nearest even; infinities take the end of the range,
+ * NaN stays NaN in e4m3 and becomes 0 in int8.  Where rows of the page come
+ * before the first new one, the page's scale never falls: the larger of the
+ * old scale (one that is not positive and finite counts as 0) and the new
+ * rows', and where it grows the old rows' codes are rounded to it.  Rows
+ * behind the new ones are left as they were.  Two new positions of one call
+ * must not share a page through different table entries (which of them ends
+ * up in a shared row, or in the scale, is then unspecified; every access stays
+ * in bounds).
+ *
+ * Supported: head_dim a multiple of 8 (16 for the 8-bit types), at most 256.
+ * Checks, in order: HEAD_COUNT, BLOCK_PAGE, CU_SEQLENS, SHAPE
+ * (cu_seqlens_q_host[batch] != tq), INVALID_ARGUMENT (types), UNSUPPORTED,
+ * INVALID_ARGUMENT (NULL, alignment, strides); on device: SHAPE (page id >=
+ * num_pages).  tq == 0 is SA_OK.  Enqueues one kernel.
+ */
+sa_status sa_store_kv(const void *k, const void *v, sa_dtype src_dtype, int64_t k_token_stride,
+                      int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                      void *k_pages, void *v_pages, float *k_scales, float *v_scales,
+                      int64_t num_pages, sa_dtype kv_dtype, const int32_t *block_tables,
+                      int32_t max_pages, const int64_t *cu_seqlens_q_host,
+                      const int64_t *cu_seqlens_q, int32_t batch, int64_t tq,
+                      const int32_t *used_kv_lens, int32_t hkv, int32_t head_dim,
+                      int32_t page_size, int64_t *status, void *stream);
+
+/*
+ * The bounds of every block that holds a new token (positions as for
+ * sa_store_kv): per (block, kv head, channel) the smallest and the largest
+ * key among the block's live keys (below the sequence's length, on a page that
+ * is there), taken over the whole block, also where only some of it is new.
+ *
+ *   bounds        [num_bounds, hkv, 2, head_dim] bf16: smallest, then largest,
+ *                 rounded down and up (exact for bf16 keys and for 8-bit codes
+ *                 under power-of-two scales)
+ *   bound_tables  [batch, msb] int32: row of `bounds` for block j of sequence
+ *                 b; -1: the block is skipped
+ *   k_scales      [num_pages, hkv] for the 8-bit types, else ignored
+ *
+ * NaN keys do not count.  A block without a live key gets (+inf, -inf), which
+ * sa_select_blocks takes as "no block here".  Shapes, checks and errors as for
+ * sa_store_kv, and BLOCK_PAGE for block_size % page_size != 0; on device also
+ * SHAPE (bounds row >= num_bounds).  Enqueues one kernel.
+ */
+sa_status sa_block_bounds(const void *k_pages, const float *k_scales, int64_t num_pages,
+                          sa_dtype kv_dtype, const int32_t *block_tables, int32_t max_pages,
+                          const int64_t *cu_seqlens_q_host, const int64_t *cu_seqlens_q,
+                          int32_t batch, int64_t tq, const int32_t *used_kv_lens, int32_t hkv,
+                          int32_t head_dim, int32_t block_size, int32_t page_size,
+                          const int32_t *bound_tables, int32_t msb, int64_t num_bounds,
+                          void *bounds, int64_t *status, void *stream);
+
+/* Bytes of device memory (256-byte aligned) that sa_select_blocks needs. */
+sa_status sa_select_workspace_size(int64_t tq, int32_t batch, int32_t hkv, int32_t head_dim,
+                                   int32_t msb, size_t *bytes);
+
+/*
+ * Block selection: selected[tq, hkv, topk] for sa_build_index / sa_attention.
+ * For query i and kv head h, with qhead = hq / hkv lanes,
+ *   score(block) = sum over lanes g and channels c of
+ *                  max(q[i, h qhead + g, c] lo[c], q[i, h qhead + g, c] hi[c]),
+ * lo and hi the block's bounds: no key of the block adds up to more over the
+ * lanes.  The candidates are the blocks with a key that query i may see
+ * (causal as in sa_forward: 0 every block below the sequence's length, 1 up to
+ * its own position right-aligned, 2 left-aligned) whose bounds row is there
+ * and holds lo[0] <= hi[0].  The topk candidates with the highest scores are
+ * written in ascending order, then -1.  Ties go to the lower block; a score
+ * that is NaN ranks behind all others.  The first sink_blocks and the last
+ * local_blocks of the blocks in sight come in before any other (sink_blocks +
+ * local_blocks <= topk).  The result is that of exactly computed scores: f32
+ * decides where its error cannot matter, f64 elsewhere.
+ *
+ *   q             [tq, hq, head_dim] of q_dtype (f32 or bf16), 16-byte aligned
+ *   bounds, bound_tables, msb, num_bounds   as for sa_block_bounds
+ *   used_kv_lens  [batch] int32, required
+ *   workspace     device memory of sa_select_workspace_size bytes; nothing is
+ *                 kept in it from call to call, and calls that overlap on the
+ *                 GPU need one each
+ *
+ * Supported: head_dim a multiple of 8, at most 256; msb <= 16384; tq * hkv *
+ * topk < 2^31.  Checks, in order: HEAD_COUNT, BLOCK_PAGE, EMPTY, SHAPE
+ * (negative sizes), CU_SEQLENS, SHAPE, INVALID_ARGUMENT (types, causal, sink +
+ * local > topk), UNSUPPORTED, INVALID_ARGUMENT (NULL, alignment, workspace);
+ * on device: SHAPE (bounds row >= num_bounds, taken as no block).
+ */
+sa_status sa_select_blocks(const void *q, sa_dtype q_dtype, int64_t tq, int32_t hq, int32_t hkv,
+                           int32_t head_dim, const void *bounds, int64_t num_bounds,
+                           const int32_t *bound_tables, int32_t msb,
+                           const int64_t *cu_seqlens_q_host, const int64_t *cu_seqlens_q,
+                           int32_t batch, const int32_t *used_kv_lens, int32_t block_size,
+                           int32_t topk, int32_t causal, int32_t sink_blocks,
+                           int32_t local_blocks, int32_t *selected, void *workspace,
+                           size_t workspace_bytes, int64_t *status, void *stream);
 
 /*
  * Test hook for the bounded device waits (the pages have no counterpart:
