@@ -254,11 +254,52 @@ def _kv_dtype(k):
     raise TypeError(f"k_pages/v_pages must be float32 or bfloat16, got {k.dtype}")
 
 
+_DTYPE_NAMES = {"f32": DTYPE_F32, "bf16": DTYPE_BF16, "e4m3": DTYPE_E4M3, "int8": DTYPE_INT8}
+
+
+@dataclass
+class _Scaled:
+    """An 8-bit cache's part of a call: types and scale pointers."""
+
+    kv_code: int
+    q_code: int
+    out_dtype: torch.dtype
+    scales: tuple
+
+    def head(self, q, k_pages, v_pages, num_pages):
+        return (_ptr(q), self.q_code, _ptr(k_pages), _ptr(v_pages), *self.scales, num_pages,
+                self.kv_code)
+
+
+def _scaled(q, k_pages, v_pages, k_scales, v_scales):
+    """Checks of a call over an 8-bit cache; None for the other cache types,
+    which take no scales."""
+    if k_pages.dtype not in (torch.float8_e4m3fn, torch.int8):
+        if k_scales is not None or v_scales is not None:
+            raise ValueError(f"a {k_pages.dtype} cache has no scales")
+        return None
+    code = _cache_dtype(k_pages, "k_pages")
+    if q.dtype not in _ACT_DTYPES:
+        raise TypeError(f"q must be float32 or bfloat16, got {q.dtype}")
+    _require(q, q.dtype, "q")
+    _require(k_pages, k_pages.dtype, "k_pages", q.device)
+    _require(v_pages, k_pages.dtype, "v_pages", q.device)
+    if v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages and v_pages must have one shape")
+    ks, vs = _scales(k_scales, k_pages, "k_scales"), _scales(v_scales, v_pages, "v_scales")
+    return _Scaled(code, _ACT_DTYPES[q.dtype], q.dtype, (_ptr(ks), _ptr(vs)))
+
+
+def _check_out(out, dtype):
+    if out is not None and out.dtype != dtype:
+        raise TypeError(f"out must be {dtype}, got {out.dtype}")
+
+
 def sa_forward_kernel_name(tq, batch, hkv, hq, head_dim, block_size, page_size, kv_dtype="f32",
                            path=PATH_AUTO):
     """Name of the kernel sa_forward launches for this problem shape, or None
     where sa_forward would refuse it.  Host only."""
-    dt = {"f32": DTYPE_F32, "bf16": DTYPE_BF16}[kv_dtype]
+    dt = _DTYPE_NAMES[kv_dtype]
     name = _native.load().sa_forward_kernel_name(int(tq), int(batch), hq, hkv, head_dim,
                                                  block_size, page_size, dt, int(path))
     return None if name is None else name.decode()
@@ -269,7 +310,7 @@ def sa_attention_kernel_name(cu_seqlens_q_host, num_pages, hkv, hq, head_dim, bl
     """The kernel sa_attention runs for steps 2 and 3 ("fused_dec_kernel" on
     the fused decode path), or None where it would refuse the call."""
     cu = _host_i64(cu_seqlens_q_host)
-    dt = {"f32": DTYPE_F32, "bf16": DTYPE_BF16}[kv_dtype]
+    dt = _DTYPE_NAMES[kv_dtype]
     name = _native.load().sa_attention_kernel_name(
         int(cu[-1]), len(cu) - 1, cu.ctypes.data, int(num_pages), hq, hkv, head_dim, block_size,
         page_size, dt, _causal(causal), int(path))
@@ -306,15 +347,19 @@ def partial_rows(index: Index, hq: int) -> int:
 def sa_forward(q, k_pages, v_pages, index: Index, block_tables, cu_seqlens_q, used_kv_lens, hq,
                hkv, head_dim, block_size, page_size, softmax_scale, causal, o_partial=None,
                m_partial=None, l_partial=None, path=PATH_AUTO, stream=None, partial_dtype=None,
-               q_scratch=None):
+               q_scratch=None, k_scales=None, v_scales=None):
     """Step 2.  Returns (o_partial, m_partial, l_partial); the first
     totals[0] * qhead rows are valid.  ``partial_dtype="bf16"`` (or a
     bfloat16 ``o_partial``) stores o in bf16; ``q_scratch`` (a tensor of at
     least tq * hq * head_dim * 2 bytes, e.g. the combine's ``out``) lets the
-    tensor-core kernel gather Q from a bf16 copy (both: sa_forward_ex)."""
-    _require(q, torch.float32, "q")
+    tensor-core kernel gather Q from a bf16 copy (both: sa_forward_ex).  An
+    8-bit cache needs ``k_scales`` and ``v_scales`` [num_pages, hkv]; ``q`` may
+    then be bfloat16 (sa_forward_scaled)."""
+    x = _scaled(q, k_pages, v_pages, k_scales, v_scales)
+    if x is None:
+        _require(q, torch.float32, "q")
+        kvd = _kv_dtype(k_pages)
     dev = q.device
-    kvd = _kv_dtype(k_pages)
     _require(k_pages, k_pages.dtype, "k_pages", dev)
     _require(v_pages, k_pages.dtype, "v_pages", dev)
     _require(block_tables, torch.int32, "block_tables", dev)
@@ -332,10 +377,17 @@ def sa_forward(q, k_pages, v_pages, index: Index, block_tables, cu_seqlens_q, us
     if l_partial is None:
         l_partial = torch.empty(rows, dtype=torch.float32, device=dev)
     L = _native.load()
-    head = (_ptr(q), _ptr(k_pages), _ptr(v_pages), num_pages, kvd, ctypes.byref(index.c),
-            _ptr(block_tables), _ptr(cu_seqlens_q), _ptr(used_kv_lens), hq, hkv, head_dim,
-            block_size, page_size, softmax_scale, _causal(causal))
+    mid = (ctypes.byref(index.c), _ptr(block_tables), _ptr(cu_seqlens_q), _ptr(used_kv_lens), hq,
+           hkv, head_dim, block_size, page_size, softmax_scale, _causal(causal))
     tail = (_ptr(o_partial), _ptr(m_partial), _ptr(l_partial), path, _stream(stream, dev))
+    if x is not None:
+        if q_scratch is not None:
+            raise ValueError("q_scratch does not apply to an 8-bit cache")
+        with _on(dev):
+            _check(L.sa_forward_scaled(*x.head(q, k_pages, v_pages, num_pages), *mid, ocode, *tail),
+                   "sa_forward_scaled")
+        return o_partial, m_partial, l_partial
+    head = (_ptr(q), _ptr(k_pages), _ptr(v_pages), num_pages, kvd, *mid)
     if q_scratch is not None:
         need = index.c.tq * hq * head_dim * 2
         if q_scratch.device != dev or q_scratch.numel() * q_scratch.element_size() < need:
@@ -371,13 +423,19 @@ def sa_combine(index: Index, o_partial, m_partial, l_partial, hq, head_dim, out=
 def sa_forward_combine(q, k_pages, v_pages, index: Index, selected, cu_seqlens_q_host,
                        cu_seqlens_q, used_kv_lens, block_tables, hq, head_dim, block_size,
                        page_size, softmax_scale, causal, split_edges=0, partials=None, out=None,
-                       lse=None, with_lse=True, path=PATH_AUTO, stream=None, partial_dtype=None):
+                       lse=None, with_lse=True, path=PATH_AUTO, stream=None, partial_dtype=None,
+                       k_scales=None, v_scales=None):
     """Steps 2 and 3 on a built index (the fused decode kernel where it
     applies).  Returns (out, lse, (o, m, l)).  ``partial_dtype="bf16"`` (or a
-    bfloat16 o in ``partials``): 16-bit o partials."""
-    _require(q, torch.float32, "q")
+    bfloat16 o in ``partials``): 16-bit o partials.  ``k_scales``, ``v_scales``:
+    see :func:`sa_attention`."""
+    x = _scaled(q, k_pages, v_pages, k_scales, v_scales)
+    if x is None:
+        _require(q, torch.float32, "q")
+        kvd = _kv_dtype(k_pages)
+    else:
+        _check_out(out, x.out_dtype)
     dev = q.device
-    kvd = _kv_dtype(k_pages)
     c = index.c
     hkv = c.hkv
     cu_h = _host_i64(cu_seqlens_q_host)
@@ -388,18 +446,23 @@ def sa_forward_combine(q, k_pages, v_pages, index: Index, selected, cu_seqlens_q
                     torch.empty(rows, dtype=torch.float32, device=dev),
                     torch.empty(rows, dtype=torch.float32, device=dev))
     if out is None:
-        out = torch.empty((c.tq, hq, head_dim), dtype=torch.float32, device=dev)
+        out = torch.empty((c.tq, hq, head_dim), dtype=q.dtype, device=dev)
     if lse is None and with_lse:
         lse = torch.empty((c.tq, hq), dtype=torch.float32, device=dev)
     page_elems = hkv * page_size * head_dim
     num_pages = k_pages.numel() // page_elems if page_elems > 0 else 0
     o, m, l = partials
     L = _native.load()
-    head = (_ptr(q), _ptr(k_pages), _ptr(v_pages), num_pages, kvd, ctypes.byref(c),
-            _ptr(selected), cu_h.ctypes.data_as(ctypes.c_void_p), _ptr(cu_seqlens_q),
-            _ptr(used_kv_lens), _ptr(block_tables), hq, head_dim, block_size, page_size,
-            softmax_scale, _causal(causal), split_edges)
+    mid = (ctypes.byref(c), _ptr(selected), cu_h.ctypes.data_as(ctypes.c_void_p),
+           _ptr(cu_seqlens_q), _ptr(used_kv_lens), _ptr(block_tables), hq, head_dim, block_size,
+           page_size, softmax_scale, _causal(causal), split_edges)
     tail = (_ptr(o), _ptr(m), _ptr(l), _ptr(out), _ptr(lse), path, _stream(stream, dev))
+    if x is not None:
+        with _on(dev):
+            _check(L.sa_forward_combine_scaled(*x.head(q, k_pages, v_pages, num_pages), *mid, ocode,
+                                               *tail), "sa_forward_combine_scaled")
+        return out, lse, partials
+    head = (_ptr(q), _ptr(k_pages), _ptr(v_pages), num_pages, kvd, *mid)
     if ocode:
         _check(L.sa_forward_combine_ex(*head, ocode, *tail), "sa_forward_combine_ex")
     else:
@@ -410,14 +473,21 @@ def sa_forward_combine(q, k_pages, v_pages, index: Index, selected, cu_seqlens_q
 def sa_attention(q, k_pages, v_pages, selected, cu_seqlens_q_host, cu_seqlens_q, used_kv_lens,
                  block_tables, hq, hkv, head_dim, block_size, page_size, softmax_scale, causal,
                  split_edges=0, index: Index | None = None, partials=None, out=None, lse=None,
-                 with_lse=True, path=PATH_AUTO, stream=None, partial_dtype=None):
+                 with_lse=True, path=PATH_AUTO, stream=None, partial_dtype=None, k_scales=None,
+                 v_scales=None):
     """Steps 1-3 in one call.  Returns (out, lse, index, (o, m, l)).  Pass
     ``index`` / ``partials`` / ``out`` back in to reuse their memory.
     ``partial_dtype="bf16"`` (or a bfloat16 o in ``partials``): 16-bit o
-    partials (sa_attention_ex)."""
-    _require(q, torch.float32, "q")
+    partials (sa_attention_ex).  A float8_e4m3fn or int8 cache needs
+    ``k_scales`` and ``v_scales`` [num_pages, hkv] (see :func:`sa_store_kv`);
+    ``q`` may then be bfloat16, and ``out`` has its type (sa_attention_scaled)."""
+    x = _scaled(q, k_pages, v_pages, k_scales, v_scales)
+    if x is None:
+        _require(q, torch.float32, "q")
+        kvd = _kv_dtype(k_pages)
+    else:
+        _check_out(out, x.out_dtype)
     dev = q.device
-    kvd = _kv_dtype(k_pages)
     tq, hkv_s, topk = (int(x) for x in selected.shape)
     cu_h = _host_i64(cu_seqlens_q_host)
     batch = cu_h.size - 1
@@ -432,18 +502,23 @@ def sa_attention(q, k_pages, v_pages, selected, cu_seqlens_q_host, cu_seqlens_q,
                     torch.empty(rows, dtype=torch.float32, device=dev),
                     torch.empty(rows, dtype=torch.float32, device=dev))
     if out is None:
-        out = torch.empty((tq, hq, head_dim), dtype=torch.float32, device=dev)
+        out = torch.empty((tq, hq, head_dim), dtype=q.dtype, device=dev)
     if lse is None and with_lse:
         lse = torch.empty((tq, hq), dtype=torch.float32, device=dev)
     page_elems = hkv * page_size * head_dim
     num_pages = k_pages.numel() // page_elems if page_elems > 0 else 0
     o, m, l = partials
     L = _native.load()
-    head = (_ptr(q), _ptr(k_pages), _ptr(v_pages), num_pages, kvd, _ptr(selected), tq, topk,
-            cu_h.ctypes.data_as(ctypes.c_void_p), _ptr(cu_seqlens_q), batch, _ptr(used_kv_lens),
-            _ptr(block_tables), max_pages, hq, hkv, head_dim, block_size, page_size,
-            softmax_scale, _causal(causal), split_edges, ctypes.byref(index.c))
+    mid = (_ptr(selected), tq, topk, cu_h.ctypes.data_as(ctypes.c_void_p), _ptr(cu_seqlens_q),
+           batch, _ptr(used_kv_lens), _ptr(block_tables), max_pages, hq, hkv, head_dim, block_size,
+           page_size, softmax_scale, _causal(causal), split_edges, ctypes.byref(index.c))
     tail = (_ptr(o), _ptr(m), _ptr(l), _ptr(out), _ptr(lse), path, _stream(stream, dev))
+    if x is not None:
+        with _on(dev):
+            _check(L.sa_attention_scaled(*x.head(q, k_pages, v_pages, num_pages), *mid, ocode,
+                                         *tail), "sa_attention_scaled")
+        return out, lse, index, partials
+    head = (_ptr(q), _ptr(k_pages), _ptr(v_pages), num_pages, kvd, *mid)
     if ocode:
         _check(L.sa_attention_ex(*head, ocode, *tail), "sa_attention_ex")
     else:
@@ -466,10 +541,11 @@ class AttentionGraph:
 
     def __init__(self, q, k_pages, v_pages, selected, cu_seqlens_q_host, cu_seqlens_q,
                  used_kv_lens, block_tables, hq, hkv, head_dim, block_size, page_size,
-                 softmax_scale, causal, split_edges=0, path=PATH_AUTO, partial_dtype=None):
+                 softmax_scale, causal, split_edges=0, path=PATH_AUTO, partial_dtype=None,
+                 k_scales=None, v_scales=None):
         args = (q, k_pages, v_pages, selected, cu_seqlens_q_host, cu_seqlens_q, used_kv_lens,
                 block_tables, hq, hkv, head_dim, block_size, page_size, softmax_scale, causal)
-        kw = dict(split_edges=split_edges, path=path)
+        kw = dict(split_edges=split_edges, path=path, k_scales=k_scales, v_scales=v_scales)
         # one eager call first: buffers, library load and kernel attributes
         self.out, self.lse, self.index, self.partials = sa_attention(
             *args, partial_dtype=partial_dtype, **kw)

@@ -24,7 +24,8 @@ EXPORTS = ("sa_status_string", "sa_version", "sa_index_query_sizes", "sa_index_w
            "sa_build_index_no_alloc", "sa_forward", "sa_forward_ex", "sa_forward_combine",
            "sa_forward_combine_ex", "sa_forward_kernel_name", "sa_attention_kernel_name",
            "sa_combine", "sa_combine_ex", "sa_attention", "sa_attention_ex", "sa_get_status",
-           "sa_clear_status", "sa_store_kv", "sa_block_bounds", "sa_select_workspace_size",
+           "sa_clear_status", "sa_forward_scaled", "sa_forward_combine_scaled",
+           "sa_attention_scaled", "sa_store_kv", "sa_block_bounds", "sa_select_workspace_size",
            "sa_select_blocks", "sa_debug_stall", "sa_debug_cta_stats")
 
 
@@ -124,6 +125,17 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.sa_get_status.restype = st
     lib.sa_clear_status.argtypes = [ctypes.POINTER(SaIndex), p]
     lib.sa_clear_status.restype = st
+    lib.sa_forward_scaled.argtypes = [p, st, p, p, p, p, i64, st, ctypes.POINTER(SaIndex), p, p, p,
+                                      i32, i32, i32, i32, i32, f32, i32, st, p, p, p, st, p]
+    lib.sa_forward_scaled.restype = st
+    lib.sa_forward_combine_scaled.argtypes = [p, st, p, p, p, p, i64, st, ctypes.POINTER(SaIndex),
+                                              p, p, p, p, p, i32, i32, i32, i32, f32, i32, i32, st,
+                                              p, p, p, p, p, st, p]
+    lib.sa_forward_combine_scaled.restype = st
+    lib.sa_attention_scaled.argtypes = [p, st, p, p, p, p, i64, st, p, i64, i32, p, p, i32, p, p,
+                                        i32, i32, i32, i32, i32, i32, f32, i32, i32,
+                                        ctypes.POINTER(SaIndex), st, p, p, p, p, p, st, p]
+    lib.sa_attention_scaled.restype = st
     lib.sa_store_kv.argtypes = [p, p, st, i64, i64, i64, i64, p, p, p, p, i64, st, p, i32, p, p,
                                 i32, i64, p, i32, i32, i32, p, p]
     lib.sa_store_kv.restype = st

@@ -66,19 +66,36 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 
 enum class FwdKernel { kNone, kGeneral, kDecode, kDecodeMma, kTensor };
 
+// What the entry points with scales add to a call: an 8-bit cache's scales and
+// the type of q (and of out).  `scaled` is false for the others.
+struct KvExtra {
+  bool scaled = false;
+  const float* k_scales = nullptr;
+  const float* v_scales = nullptr;
+  sa_dtype q_dtype = SA_DTYPE_F32;
+};
+
+bool kv_eight_bit(sa_dtype t) { return t == SA_DTYPE_E4M3 || t == SA_DTYPE_INT8; }
+
+// The types a call may have: 8-bit K/V exactly where scales come with it.
+bool types_ok(sa_dtype kv_dtype, const KvExtra& x) {
+  if (!x.scaled) return kv_dtype == SA_DTYPE_F32 || kv_dtype == SA_DTYPE_BF16;
+  return kv_eight_bit(kv_dtype) && (x.q_dtype == SA_DTYPE_F32 || x.q_dtype == SA_DTYPE_BF16);
+}
+
 // The forward kernel a call takes.  Decode-shaped problems (tq at most twice
 // the batch: about one query per sequence, so few rows per work split) go to
 // the per-warp decode kernels (warp-level MMA for bf16 K/V, f32 FMA
 // otherwise); problems whose units gather many rows go to the tcgen05
 // kernel; the general f32 kernel takes whatever the others do not support.
 FwdKernel choose_forward(int64_t tq, int32_t batch, int32_t qhead, int32_t head_dim,
-                         int32_t block_size, int32_t page_size, int kv_bf16, sa_path path) {
+                         int32_t block_size, int32_t page_size, int kv_type, sa_path path) {
   const bool decode_like = tq <= 2 * static_cast<int64_t>(batch);
   const bool tc_ok = sa::forward_tc_supported(head_dim, block_size, page_size, qhead);
   const bool mma_ok =
-      sa::forward_dec_mma_supported(head_dim, block_size, page_size, qhead, kv_bf16);
-  const bool dec_ok = sa::forward_dec_supported(head_dim, block_size, page_size, qhead, kv_bf16);
-  const bool cc_ok = sa::forward_cc_supported(head_dim, block_size, kv_bf16);
+      sa::forward_dec_mma_supported(head_dim, block_size, page_size, qhead, kv_type);
+  const bool dec_ok = sa::forward_dec_supported(head_dim, block_size, page_size, qhead, kv_type);
+  const bool cc_ok = sa::forward_cc_supported(head_dim, block_size, kv_type);
   switch (path) {
     case SA_PATH_TENSOR_CORE:
     case SA_PATH_TENSOR_CORE_TF32:
@@ -105,9 +122,9 @@ FwdKernel choose_forward(int64_t tq, int32_t batch, int32_t qhead, int32_t head_
 // and the shape is one the kernel supports.
 bool fused_eligible(int64_t tq, int32_t batch, const int64_t* cu_host, int64_t num_pages,
                     int32_t hq, int32_t hkv, int32_t head_dim, int32_t block_size,
-                    int32_t page_size, int kv_bf16) {
+                    int32_t page_size, int kv_type) {
   if (cu_host == nullptr || batch < 1 || tq < 1 || hkv < 1 || hq % hkv != 0) return false;
-  if (!sa::fused_dec_supported(head_dim, block_size, page_size, hq / hkv, kv_bf16)) return false;
+  if (!sa::fused_dec_supported(head_dim, block_size, page_size, hq / hkv, kv_type)) return false;
   if (num_pages < 1 || num_pages > sa::kFusedMaxRows / (static_cast<int64_t>(hkv) * page_size))
     return false;
   if (tq * hq * 4 > sa::kFusedMaxRows) return false;
@@ -362,13 +379,14 @@ bool index_scratch(const sa_index* idx, unsigned char** ws, size_t* bytes) {
 // 16-byte aligned, not overlapping q, that the tensor-core kernel may fill
 // with Q rounded to bf16 and gather from (half the bytes of the f32 rows, no
 // conversion per gather); its content afterwards is unspecified.
-sa_status forward_impl(const float* q, const void* k_pages, const void* v_pages,
+sa_status forward_impl(const void* q, const void* k_pages, const void* v_pages,
                        int64_t num_pages, sa_dtype kv_dtype, const sa_index* idx,
                        const int32_t* block_tables, const int64_t* cu_seqlens_q,
                        const int32_t* used_kv_lens, int32_t hq, int32_t hkv, int32_t head_dim,
                        int32_t block_size, int32_t page_size, float softmax_scale, int32_t causal,
                        sa_dtype partial_dtype, void* o_partial, float* m_partial,
-                       float* l_partial, sa_path path, void* stream, void* q16_scratch) {
+                       float* l_partial, sa_path path, void* stream, void* q16_scratch,
+                       const KvExtra& x = KvExtra()) {
   if (hkv <= 0 || hq <= 0 || hq % hkv != 0) return SA_ERR_HEAD_COUNT;
   if (head_dim <= 0 || block_size <= 0 || page_size <= 0 || block_size % page_size != 0)
     return SA_ERR_BLOCK_PAGE;
@@ -377,30 +395,34 @@ sa_status forward_impl(const float* q, const void* k_pages, const void* v_pages,
       idx->block_size != block_size || idx->page_size != page_size)
     return SA_ERR_SHAPE;
   if (num_pages < 0) return SA_ERR_SHAPE;
-  if (kv_dtype != SA_DTYPE_F32 && kv_dtype != SA_DTYPE_BF16) return SA_ERR_INVALID_ARGUMENT;
+  if (!types_ok(kv_dtype, x)) return SA_ERR_INVALID_ARGUMENT;
   if (partial_dtype != SA_DTYPE_F32 && partial_dtype != SA_DTYPE_BF16)
     return SA_ERR_INVALID_ARGUMENT;
   if (causal < 0 || causal > 2) return SA_ERR_INVALID_ARGUMENT;
-  const int kv_bf16 = kv_dtype == SA_DTYPE_BF16 ? 1 : 0;
+  const int kv_type = static_cast<int>(kv_dtype);
   if (path == SA_PATH_FUSED_DECODE) return SA_ERR_UNSUPPORTED;   // writes no partials
   if (path != SA_PATH_AUTO && path != SA_PATH_CUDA_CORE && path != SA_PATH_CUDA_CORE_GENERAL &&
       path != SA_PATH_TENSOR_CORE && path != SA_PATH_TENSOR_CORE_TF32)
     return SA_ERR_INVALID_ARGUMENT;
   const FwdKernel kernel = choose_forward(idx->tq, idx->batch, hq / hkv, head_dim, block_size,
-                                          page_size, kv_bf16, path);
+                                          page_size, kv_type, path);
   if (kernel == FwdKernel::kNone) return SA_ERR_UNSUPPORTED;
   if (!q || !k_pages || !v_pages || !block_tables || !cu_seqlens_q || !o_partial || !m_partial ||
       !l_partial)
     return SA_ERR_INVALID_ARGUMENT;
+  if (x.scaled && (!x.k_scales || !x.v_scales)) return SA_ERR_INVALID_ARGUMENT;
   if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o_partial))
     return SA_ERR_INVALID_ARGUMENT;
 
   sa::ForwardArgs a{};
-  a.q = q;
+  a.q = static_cast<const float*>(q);
+  a.q_bf16 = x.q_dtype == SA_DTYPE_BF16 ? 1 : 0;
+  a.k_scales = x.k_scales;
+  a.v_scales = x.v_scales;
   a.k_pages = k_pages;
   a.v_pages = v_pages;
   a.num_pages = num_pages;
-  a.kv_bf16 = kv_bf16;
+  a.kv_type = kv_type;
   a.block_tables = block_tables;
   a.cu = cu_seqlens_q;
   a.used = used_kv_lens;
@@ -446,10 +468,13 @@ sa_status forward_impl(const float* q, const void* k_pages, const void* v_pages,
   }
   if (kernel == FwdKernel::kTensor) sa::debug_cta_stats(&a.cta_stats, &a.cta_stats_len);
   // tf32 scores for f32 K/V where asked for; bf16 operands otherwise
-  a.tf32 = kernel == FwdKernel::kTensor && !kv_bf16 && path == SA_PATH_TENSOR_CORE_TF32;
-  if (kernel == FwdKernel::kTensor && !a.tf32 && q16_scratch != nullptr) {
+  a.tf32 = kernel == FwdKernel::kTensor && kv_dtype == SA_DTYPE_F32 &&
+           path == SA_PATH_TENSOR_CORE_TF32;
+  if (a.q_bf16) {
+    a.q16 = static_cast<const uint16_t*>(q);   // the tensor-core kernel's bf16 rows as they are
+  } else if (kernel == FwdKernel::kTensor && !a.tf32 && q16_scratch != nullptr) {
     const int64_t n = idx->tq * static_cast<int64_t>(hq) * head_dim;
-    err = sa::launch_q_to_bf16(q, static_cast<uint16_t*>(q16_scratch), n, s);
+    err = sa::launch_q_to_bf16(a.q, static_cast<uint16_t*>(q16_scratch), n, s);
     if (err != cudaSuccess) return SA_ERR_CUDA;
     a.q16 = static_cast<const uint16_t*>(q16_scratch);
   }
@@ -509,24 +534,24 @@ const char* sa_forward_kernel_name(int64_t tq, int32_t batch, int32_t hq, int32_
   if (hkv <= 0 || hq <= 0 || hq % hkv != 0) return nullptr;
   if (head_dim <= 0 || block_size <= 0 || page_size <= 0 || block_size % page_size != 0)
     return nullptr;
-  if (kv_dtype != SA_DTYPE_F32 && kv_dtype != SA_DTYPE_BF16) return nullptr;
+  if (kv_dtype < SA_DTYPE_F32 || kv_dtype > SA_DTYPE_INT8) return nullptr;
   return forward_kernel_name(choose_forward(tq, batch, hq / hkv, head_dim, block_size, page_size,
-                                            kv_dtype == SA_DTYPE_BF16 ? 1 : 0, path));
+                                            static_cast<int>(kv_dtype), path));
 }
 
 const char* sa_attention_kernel_name(int64_t tq, int32_t batch, const int64_t* cu_seqlens_q_host,
                                      int64_t num_pages, int32_t hq, int32_t hkv,
                                      int32_t head_dim, int32_t block_size, int32_t page_size,
                                      sa_dtype kv_dtype, int32_t causal, sa_path path) {
-  if (kv_dtype != SA_DTYPE_F32 && kv_dtype != SA_DTYPE_BF16) return nullptr;
+  if (kv_dtype < SA_DTYPE_F32 || kv_dtype > SA_DTYPE_INT8) return nullptr;
   if (causal < 0 || causal > 2) return nullptr;
-  const int kv_bf16 = kv_dtype == SA_DTYPE_BF16 ? 1 : 0;
+  const int kv_type = static_cast<int>(kv_dtype);
   if ((path == SA_PATH_AUTO || path == SA_PATH_FUSED_DECODE) && causal != 2) {
     if (hkv > 0 && hq > 0 && hq % hkv == 0 && head_dim > 0 && block_size > 0 && page_size > 0 &&
         block_size % page_size == 0 && validate_cu_host(cu_seqlens_q_host, batch) == SA_OK &&
         cu_seqlens_q_host[batch] == tq &&
         fused_eligible(tq, batch, cu_seqlens_q_host, num_pages, hq, hkv, head_dim, block_size,
-                       page_size, kv_bf16))
+                       page_size, kv_type))
       return "fused_dec_kernel";
   }
   if (path == SA_PATH_FUSED_DECODE) return nullptr;
@@ -534,9 +559,13 @@ const char* sa_attention_kernel_name(int64_t tq, int32_t batch, const int64_t* c
                                 path);
 }
 
-sa_status sa_combine_ex(const sa_index* idx, sa_dtype partial_dtype, const void* o_partial,
-                        const float* m_partial, const float* l_partial, int32_t hq,
-                        int32_t head_dim, float* out, float* lse, void* stream) {
+namespace {
+
+// Step 3, with out in f32 or bf16.
+sa_status combine_impl(const sa_index* idx, sa_dtype partial_dtype, const void* o_partial,
+                       const float* m_partial, const float* l_partial, int32_t hq,
+                       int32_t head_dim, void* out, sa_dtype out_dtype, float* lse,
+                       void* stream) {
   if (idx == nullptr) return SA_ERR_INVALID_ARGUMENT;
   if (partial_dtype != SA_DTYPE_F32 && partial_dtype != SA_DTYPE_BF16)
     return SA_ERR_INVALID_ARGUMENT;
@@ -558,9 +587,19 @@ sa_status sa_combine_ex(const sa_index* idx, sa_dtype partial_dtype, const void*
   a.qhead = hq / idx->hkv;
   a.head_dim = head_dim;
   a.out = out;
+  a.out_bf16 = out_dtype == SA_DTYPE_BF16 ? 1 : 0;
   a.lse = lse;
   const cudaError_t err = sa::launch_combine(a, static_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? SA_OK : SA_ERR_CUDA;
+}
+
+}  // namespace
+
+sa_status sa_combine_ex(const sa_index* idx, sa_dtype partial_dtype, const void* o_partial,
+                        const float* m_partial, const float* l_partial, int32_t hq,
+                        int32_t head_dim, float* out, float* lse, void* stream) {
+  return combine_impl(idx, partial_dtype, o_partial, m_partial, l_partial, hq, head_dim, out,
+                      SA_DTYPE_F32, lse, stream);
 }
 
 sa_status sa_combine(const sa_index* idx, const float* o_partial, const float* m_partial,
@@ -575,15 +614,16 @@ namespace {
 // Steps 2 and 3.  `behind_build`: the index build that made `idx` was the
 // last launch on `stream` (sa_attention), so the fused decode kernel may be
 // launched as its programmatic dependent.
-sa_status forward_combine_impl(const float* q, const void* k_pages, const void* v_pages,
+sa_status forward_combine_impl(const void* q, const void* k_pages, const void* v_pages,
                                int64_t num_pages, sa_dtype kv_dtype, const sa_index* idx,
                                const int32_t* selected, const int64_t* cu_seqlens_q_host,
                                const int64_t* cu_seqlens_q, const int32_t* used_kv_lens,
                                const int32_t* block_tables, int32_t hq, int32_t head_dim,
                                int32_t block_size, int32_t page_size, float softmax_scale,
                                int32_t causal, int32_t split_edges, sa_dtype partial_dtype,
-                               void* o_partial, float* m_partial, float* l_partial, float* out,
-                               float* lse, sa_path path, void* stream, bool behind_build) {
+                               void* o_partial, float* m_partial, float* l_partial, void* out,
+                               float* lse, sa_path path, void* stream, bool behind_build,
+                               const KvExtra& x = KvExtra()) {
   if (idx == nullptr) return SA_ERR_INVALID_ARGUMENT;
   if (partial_dtype != SA_DTYPE_F32 && partial_dtype != SA_DTYPE_BF16)
     return SA_ERR_INVALID_ARGUMENT;
@@ -592,10 +632,10 @@ sa_status forward_combine_impl(const float* q, const void* k_pages, const void* 
   if (head_dim <= 0 || block_size <= 0 || page_size <= 0 || block_size % page_size != 0)
     return SA_ERR_BLOCK_PAGE;
   if (idx->block_size != block_size || idx->page_size != page_size) return SA_ERR_SHAPE;
-  if (kv_dtype != SA_DTYPE_F32 && kv_dtype != SA_DTYPE_BF16) return SA_ERR_INVALID_ARGUMENT;
+  if (!types_ok(kv_dtype, x)) return SA_ERR_INVALID_ARGUMENT;
   if (split_edges < 0) return SA_ERR_INVALID_ARGUMENT;
   if (causal < 0 || causal > 2) return SA_ERR_INVALID_ARGUMENT;
-  const int kv_bf16 = kv_dtype == SA_DTYPE_BF16 ? 1 : 0;
+  const int kv_type = static_cast<int>(kv_dtype);
   const int64_t tq = idx->tq;
   const int32_t batch = idx->batch;
   bool fused = false;
@@ -604,7 +644,7 @@ sa_status forward_combine_impl(const float* q, const void* k_pages, const void* 
     if (causal != 2 && validate_cu_host(cu_seqlens_q_host, batch) == SA_OK &&
         cu_seqlens_q_host[batch] == tq)
       fused = fused_eligible(tq, batch, cu_seqlens_q_host, num_pages, hq, hkv, head_dim,
-                             block_size, page_size, kv_bf16);
+                             block_size, page_size, kv_type);
     if (path == SA_PATH_FUSED_DECODE && !fused) return SA_ERR_UNSUPPORTED;
   }
   if (!fused) {
@@ -612,7 +652,8 @@ sa_status forward_combine_impl(const float* q, const void* k_pages, const void* 
     // keep a bf16 copy of Q there (in its first half), unless out and q
     // share memory.
     const size_t qbytes = static_cast<size_t>(tq) * hq * head_dim * sizeof(float);
-    void* q16 = (out != nullptr && q != nullptr && qbytes > 0 && head_dim % 8 == 0 &&
+    // (Queries that are bf16 already need none.)
+    void* q16 = (x.q_dtype == SA_DTYPE_F32 && out != nullptr && q != nullptr && qbytes > 0 && head_dim % 8 == 0 &&
                  aligned16(out) && !overlaps(q, qbytes, out, qbytes))
                     ? static_cast<void*>(out)
                     : nullptr;
@@ -620,14 +661,15 @@ sa_status forward_combine_impl(const float* q, const void* k_pages, const void* 
                                       block_tables, cu_seqlens_q, used_kv_lens, hq, hkv, head_dim,
                                       block_size, page_size, softmax_scale, causal,
                                       partial_dtype, o_partial, m_partial, l_partial, path,
-                                      stream, q16);
+                                      stream, q16, x);
     if (st != SA_OK) return st;
-    return sa_combine_ex(idx, partial_dtype, o_partial, m_partial, l_partial, hq, head_dim, out,
-                         lse, stream);
+    return combine_impl(idx, partial_dtype, o_partial, m_partial, l_partial, hq, head_dim, out,
+                        x.q_dtype, lse, stream);
   }
   if (!q || !k_pages || !v_pages || !block_tables || !cu_seqlens_q || !selected || !o_partial ||
       !m_partial || !l_partial || !out || !idx->inv || !idx->totals)
     return SA_ERR_INVALID_ARGUMENT;
+  if (x.scaled && (!x.k_scales || !x.v_scales)) return SA_ERR_INVALID_ARGUMENT;
   // The per-(query, kv head) piece counters live in the index's scratch,
   // cleared by the build that made the index.
   unsigned char* ws = nullptr;
@@ -640,11 +682,14 @@ sa_status forward_combine_impl(const float* q, const void* k_pages, const void* 
     return SA_ERR_INVALID_ARGUMENT;
   if (idx->msb <= 0) return SA_ERR_SHAPE;   // a built index over these sizes addresses blocks
   sa::FusedDecArgs a{};
-  a.q = q;
+  a.q = static_cast<const float*>(q);
+  a.q_bf16 = x.q_dtype == SA_DTYPE_BF16 ? 1 : 0;
+  a.k_scales = x.k_scales;
+  a.v_scales = x.v_scales;
   a.k_pages = k_pages;
   a.v_pages = v_pages;
   a.num_pages = num_pages;
-  a.kv_bf16 = kv_bf16;
+  a.kv_type = kv_type;
   a.block_tables = block_tables;
   a.cu = cu_seqlens_q;
   a.used = used_kv_lens;
@@ -692,6 +737,7 @@ sa_status forward_combine_impl(const float* q, const void* k_pages, const void* 
   a.part_m = m_partial;
   a.part_l = l_partial;
   a.out = out;
+  a.out_bf16 = a.q_bf16;
   a.lse = lse;
   a.pdl = behind_build ? 1 : 0;
   (void)causal;   // a no-op for one query per sequence (its position is lk - 1)
@@ -734,32 +780,35 @@ sa_status sa_forward_combine(const float* q, const void* k_pages, const void* v_
                                lse, path, stream);
 }
 
-sa_status sa_attention_ex(const float* q, const void* k_pages, const void* v_pages,
-                          int64_t num_pages, sa_dtype kv_dtype, const int32_t* selected, int64_t tq,
-                          int32_t topk, const int64_t* cu_seqlens_q_host,
-                          const int64_t* cu_seqlens_q, int32_t batch, const int32_t* used_kv_lens,
-                          const int32_t* block_tables, int32_t max_pages, int32_t hq, int32_t hkv,
-                          int32_t head_dim, int32_t block_size, int32_t page_size,
-                          float softmax_scale, int32_t causal, int32_t split_edges, sa_index* idx,
-                          sa_dtype partial_dtype, void* o_partial, float* m_partial,
-                          float* l_partial, float* out, float* lse, sa_path path, void* stream) {
+namespace {
+
+sa_status attention_impl(const void* q, const void* k_pages, const void* v_pages,
+                         int64_t num_pages, sa_dtype kv_dtype, const int32_t* selected, int64_t tq,
+                         int32_t topk, const int64_t* cu_seqlens_q_host,
+                         const int64_t* cu_seqlens_q, int32_t batch, const int32_t* used_kv_lens,
+                         const int32_t* block_tables, int32_t max_pages, int32_t hq, int32_t hkv,
+                         int32_t head_dim, int32_t block_size, int32_t page_size,
+                         float softmax_scale, int32_t causal, int32_t split_edges, sa_index* idx,
+                         sa_dtype partial_dtype, void* o_partial, float* m_partial,
+                         float* l_partial, void* out, float* lse, sa_path path, void* stream,
+                         const KvExtra& x) {
   if (hkv <= 0 || hq <= 0 || hq % hkv != 0) return SA_ERR_HEAD_COUNT;
   if (head_dim <= 0 || block_size <= 0 || page_size <= 0 || block_size % page_size != 0)
     return SA_ERR_BLOCK_PAGE;
-  if (kv_dtype != SA_DTYPE_F32 && kv_dtype != SA_DTYPE_BF16) return SA_ERR_INVALID_ARGUMENT;
+  if (!types_ok(kv_dtype, x)) return SA_ERR_INVALID_ARGUMENT;
   if (partial_dtype != SA_DTYPE_F32 && partial_dtype != SA_DTYPE_BF16)
     return SA_ERR_INVALID_ARGUMENT;
   if (causal < 0 || causal > 2) return SA_ERR_INVALID_ARGUMENT;
-  const int kv_bf16 = kv_dtype == SA_DTYPE_BF16 ? 1 : 0;
+  const int kv_type = static_cast<int>(kv_dtype);
   // Shape checks of the forward step, before any device work.
   bool fused = false;
   if (path == SA_PATH_AUTO || path == SA_PATH_FUSED_DECODE) {
     if (causal != 2 && tq > 0 && validate_cu_host(cu_seqlens_q_host, batch) == SA_OK)
       fused = fused_eligible(tq, batch, cu_seqlens_q_host, num_pages, hq, hkv, head_dim,
-                             block_size, page_size, kv_bf16);
+                             block_size, page_size, kv_type);
     if (path == SA_PATH_FUSED_DECODE && !fused) return SA_ERR_UNSUPPORTED;
   }
-  if (!fused && !sa::forward_cc_supported(head_dim, block_size, kv_bf16) &&
+  if (!fused && !sa::forward_cc_supported(head_dim, block_size, kv_type) &&
       !((path == SA_PATH_TENSOR_CORE || path == SA_PATH_TENSOR_CORE_TF32) &&
         sa::forward_tc_supported(head_dim, block_size, page_size, hq / hkv)))
     return SA_ERR_UNSUPPORTED;
@@ -779,12 +828,82 @@ sa_status sa_attention_ex(const float* q, const void* k_pages, const void* v_pag
                                cu_seqlens_q_host, cu_seqlens_q, used_kv_lens, block_tables, hq,
                                head_dim, block_size, page_size, softmax_scale, causal,
                                split_edges, partial_dtype, o_partial, m_partial, l_partial, out,
-                               lse, path, stream, side == nullptr);
+                               lse, path, stream, side == nullptr, x);
   if (forked && (cudaEventRecord(side->join, side->s) != cudaSuccess ||
                           cudaStreamWaitEvent(static_cast<cudaStream_t>(stream), side->join, 0) !=
                               cudaSuccess))
     return SA_ERR_CUDA;
   return st2;
+}
+
+}  // namespace
+
+sa_status sa_attention_ex(const float* q, const void* k_pages, const void* v_pages,
+                          int64_t num_pages, sa_dtype kv_dtype, const int32_t* selected, int64_t tq,
+                          int32_t topk, const int64_t* cu_seqlens_q_host,
+                          const int64_t* cu_seqlens_q, int32_t batch, const int32_t* used_kv_lens,
+                          const int32_t* block_tables, int32_t max_pages, int32_t hq, int32_t hkv,
+                          int32_t head_dim, int32_t block_size, int32_t page_size,
+                          float softmax_scale, int32_t causal, int32_t split_edges, sa_index* idx,
+                          sa_dtype partial_dtype, void* o_partial, float* m_partial,
+                          float* l_partial, float* out, float* lse, sa_path path, void* stream) {
+  return attention_impl(q, k_pages, v_pages, num_pages, kv_dtype, selected, tq, topk,
+                        cu_seqlens_q_host, cu_seqlens_q, batch, used_kv_lens, block_tables,
+                        max_pages, hq, hkv, head_dim, block_size, page_size, softmax_scale, causal,
+                        split_edges, idx, partial_dtype, o_partial, m_partial, l_partial, out, lse,
+                        path, stream, KvExtra());
+}
+
+sa_status sa_forward_scaled(const void* q, sa_dtype q_dtype, const void* k_pages,
+                            const void* v_pages, const float* k_scales, const float* v_scales,
+                            int64_t num_pages, sa_dtype kv_dtype, const sa_index* idx,
+                            const int32_t* block_tables, const int64_t* cu_seqlens_q,
+                            const int32_t* used_kv_lens, int32_t hq, int32_t hkv,
+                            int32_t head_dim, int32_t block_size, int32_t page_size,
+                            float softmax_scale, int32_t causal, sa_dtype partial_dtype,
+                            void* o_partial, float* m_partial, float* l_partial, sa_path path,
+                            void* stream) {
+  return forward_impl(q, k_pages, v_pages, num_pages, kv_dtype, idx, block_tables, cu_seqlens_q,
+                      used_kv_lens, hq, hkv, head_dim, block_size, page_size, softmax_scale,
+                      causal, partial_dtype, o_partial, m_partial, l_partial, path, stream,
+                      nullptr, KvExtra{true, k_scales, v_scales, q_dtype});
+}
+
+sa_status sa_forward_combine_scaled(const void* q, sa_dtype q_dtype, const void* k_pages,
+                                    const void* v_pages, const float* k_scales,
+                                    const float* v_scales, int64_t num_pages, sa_dtype kv_dtype,
+                                    const sa_index* idx, const int32_t* selected,
+                                    const int64_t* cu_seqlens_q_host, const int64_t* cu_seqlens_q,
+                                    const int32_t* used_kv_lens, const int32_t* block_tables,
+                                    int32_t hq, int32_t head_dim, int32_t block_size,
+                                    int32_t page_size, float softmax_scale, int32_t causal,
+                                    int32_t split_edges, sa_dtype partial_dtype, void* o_partial,
+                                    float* m_partial, float* l_partial, void* out, float* lse,
+                                    sa_path path, void* stream) {
+  return forward_combine_impl(q, k_pages, v_pages, num_pages, kv_dtype, idx, selected,
+                              cu_seqlens_q_host, cu_seqlens_q, used_kv_lens, block_tables, hq,
+                              head_dim, block_size, page_size, softmax_scale, causal, split_edges,
+                              partial_dtype, o_partial, m_partial, l_partial, out, lse, path,
+                              stream, false, KvExtra{true, k_scales, v_scales, q_dtype});
+}
+
+sa_status sa_attention_scaled(const void* q, sa_dtype q_dtype, const void* k_pages,
+                              const void* v_pages, const float* k_scales, const float* v_scales,
+                              int64_t num_pages, sa_dtype kv_dtype, const int32_t* selected,
+                              int64_t tq, int32_t topk, const int64_t* cu_seqlens_q_host,
+                              const int64_t* cu_seqlens_q, int32_t batch,
+                              const int32_t* used_kv_lens, const int32_t* block_tables,
+                              int32_t max_pages, int32_t hq, int32_t hkv, int32_t head_dim,
+                              int32_t block_size, int32_t page_size, float softmax_scale,
+                              int32_t causal, int32_t split_edges, sa_index* idx,
+                              sa_dtype partial_dtype, void* o_partial, float* m_partial,
+                              float* l_partial, void* out, float* lse, sa_path path,
+                              void* stream) {
+  return attention_impl(q, k_pages, v_pages, num_pages, kv_dtype, selected, tq, topk,
+                        cu_seqlens_q_host, cu_seqlens_q, batch, used_kv_lens, block_tables,
+                        max_pages, hq, hkv, head_dim, block_size, page_size, softmax_scale, causal,
+                        split_edges, idx, partial_dtype, o_partial, m_partial, l_partial, out, lse,
+                        path, stream, KvExtra{true, k_scales, v_scales, q_dtype});
 }
 
 sa_status sa_attention(const float* q, const void* k_pages, const void* v_pages,

@@ -109,13 +109,13 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(CombineArgs a) {
     for (int off = 16; off; off >>= 1) big_l += __shfl_xor_sync(0xffffffffu, big_l, off);
   }
   const float inv_l = big_l > 0.f ? 1.f / big_l : 0.f;
-  float4* orow = reinterpret_cast<float4*>(a.out + row * d);
 #pragma unroll
   for (int c = 0; c < kChunks; ++c) {
     const int ch = lane + 32 * c;
     if (ch < nc)
-      orow[ch] = make_float4(acc[c].x * inv_l, acc[c].y * inv_l, acc[c].z * inv_l,
-                             acc[c].w * inv_l);
+      store_o4(a.out, a.out_bf16, row * d + 4 * ch,
+               make_float4(acc[c].x * inv_l, acc[c].y * inv_l, acc[c].z * inv_l,
+                           acc[c].w * inv_l));
   }
   if (a.lse && lane == 0) a.lse[row] = big_l > 0.f ? big_m + logf(big_l) : -INFINITY;
 }
@@ -226,15 +226,16 @@ __global__ void __launch_bounds__(kThreads) combine_bf16_kernel(CombineArgs a) {
   }
   const float inv_l = big_l > 0.f ? 1.f / big_l : 0.f;
   if (half == 0) {
-    float4* orow = reinterpret_cast<float4*>(a.out + row * d);
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
       const int ch = hl + 16 * c;
       if (ch < n8) {
-        orow[2 * ch] = make_float4(acc[c][0] * inv_l, acc[c][1] * inv_l, acc[c][2] * inv_l,
-                                   acc[c][3] * inv_l);
-        orow[2 * ch + 1] = make_float4(acc[c][4] * inv_l, acc[c][5] * inv_l, acc[c][6] * inv_l,
-                                       acc[c][7] * inv_l);
+        store_o4(a.out, a.out_bf16, row * d + 8 * ch,
+                 make_float4(acc[c][0] * inv_l, acc[c][1] * inv_l, acc[c][2] * inv_l,
+                             acc[c][3] * inv_l));
+        store_o4(a.out, a.out_bf16, row * d + 8 * ch + 4,
+                 make_float4(acc[c][4] * inv_l, acc[c][5] * inv_l, acc[c][6] * inv_l,
+                             acc[c][7] * inv_l));
       }
     }
   }

@@ -13,11 +13,15 @@
 //   PV       one thread per (row, 4 output dims), p broadcast from shared.
 // Masked keys (past the sequence's length, absent pages, right-aligned
 // causal limit) score -inf; a row with no live key writes (0, -inf, 0).
+// 8-bit K/V: codes are staged as they are; the page's scales meet K on the
+// scores and V on p, and keys with p = 0 are left out of PV (rows behind a
+// sequence's end may hold NaN codes).
 #include <cfloat>
 #include <cstdint>
 
 #include "internal.h"
 #include "sa_common.cuh"
+#include "seq_common.cuh"
 
 namespace sa {
 
@@ -30,14 +34,20 @@ constexpr int kMaxDim = 256;
 
 struct SmemPlan {
   size_t kv_bytes;   // one of K or V
-  size_t k_off, v_off, q_off, p_off, pos_off, lim_off, total;
+  size_t k_off, v_off, q_off, p_off, pos_off, lim_off, sc_off, total;
 };
 
 __host__ __device__ inline size_t align128(size_t x) { return (x + 127) & ~static_cast<size_t>(127); }
 
-__host__ __device__ inline SmemPlan plan_smem(int block_size, int head_dim, int kv_bf16) {
+__host__ __device__ constexpr bool is_q8(int t) { return t == SA_DTYPE_E4M3 || t == SA_DTYPE_INT8; }
+
+__host__ __device__ constexpr size_t elt_bytes(int t) {
+  return t == SA_DTYPE_F32 ? 4 : t == SA_DTYPE_BF16 ? 2 : 1;
+}
+
+__host__ __device__ inline SmemPlan plan_smem(int block_size, int head_dim, int kv_type) {
   SmemPlan p{};
-  const size_t elt = kv_bf16 ? 2 : 4;
+  const size_t elt = elt_bytes(kv_type);
   p.kv_bytes = static_cast<size_t>(block_size) * head_dim * elt;
   p.k_off = 128;  // [0, 16) holds the mbarrier
   p.v_off = align128(p.k_off + p.kv_bytes);
@@ -45,14 +55,22 @@ __host__ __device__ inline SmemPlan plan_smem(int block_size, int head_dim, int 
   p.p_off = align128(p.q_off + sizeof(float) * kRows * head_dim);
   p.pos_off = align128(p.p_off + sizeof(float) * kRows * block_size);
   p.lim_off = align128(p.pos_off + sizeof(int32_t) * block_size);
-  p.total = align128(p.lim_off + sizeof(int32_t) * kRows);
+  p.sc_off = align128(p.lim_off + sizeof(int32_t) * kRows);
+  p.total = is_q8(kv_type) ? align128(p.sc_off + 2 * sizeof(float) * block_size) : p.sc_off;
   return p;
 }
 
-template <bool kBf16>
+template <int kT>
 __device__ __forceinline__ float4 load4(const unsigned char* base, int row, int chunk,
                                         int head_dim) {
-  if constexpr (kBf16) {
+  if constexpr (is_q8(kT)) {
+    uint32_t h0, h1;
+    codes4_to_f16<kT == SA_DTYPE_INT8>(
+        *reinterpret_cast<const uint32_t*>(base + static_cast<size_t>(row) * head_dim + 4 * chunk),
+        h0, h1);
+    const float2 x = f16x2_to_f32(h0), y = f16x2_to_f32(h1);
+    return make_float4(x.x, x.y, y.x, y.y);
+  } else if constexpr (kT == SA_DTYPE_BF16) {
     const uint2 u = *reinterpret_cast<const uint2*>(
         base + (static_cast<size_t>(row) * head_dim + 4 * chunk) * 2);
     return bf16x4_to_f32(u);
@@ -62,11 +80,11 @@ __device__ __forceinline__ float4 load4(const unsigned char* base, int row, int 
   }
 }
 
-template <bool kBf16>
+template <int kT>
 __global__ void __launch_bounds__(kThreads)
 forward_cc_kernel(ForwardArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
-  const SmemPlan plan = plan_smem(a.block_size, a.head_dim, kBf16 ? 1 : 0);
+  const SmemPlan plan = plan_smem(a.block_size, a.head_dim, kT);
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem);
   unsigned char* ks = smem + plan.k_off;
   unsigned char* vs = smem + plan.v_off;
@@ -74,6 +92,8 @@ forward_cc_kernel(ForwardArgs a) {
   float* ps = reinterpret_cast<float*>(smem + plan.p_off);
   int32_t* kpos = reinterpret_cast<int32_t*>(smem + plan.pos_off);
   int32_t* rlim = reinterpret_cast<int32_t*>(smem + plan.lim_off);
+  float* ksc = reinterpret_cast<float*>(smem + plan.sc_off);   // 8-bit: scales per key
+  float* vsc = ksc + a.block_size;
   __shared__ uint32_t s_bytes;
 
   const int tid = threadIdx.x;
@@ -84,7 +104,7 @@ forward_cc_kernel(ForwardArgs a) {
   const int bs = a.block_size;
   const int ps_ = a.page_size;
   const int qhead = a.qhead;
-  const size_t elt = kBf16 ? 2 : 4;
+  const size_t elt = elt_bytes(kT);
   const size_t page_bytes = static_cast<size_t>(ps_) * d * elt;
   int64_t* status = a.totals + 3;
 
@@ -133,7 +153,13 @@ forward_cc_kernel(ForwardArgs a) {
       int32_t live = -1;
       if (p < block_end) {
         const int32_t pid = bt_row[t / ps_];
-        if (pid >= 0 && pid < a.num_pages) live = static_cast<int32_t>(p);
+        if (pid >= 0 && pid < a.num_pages) {
+          live = static_cast<int32_t>(p);
+          if constexpr (is_q8(kT)) {
+            ksc[t] = __ldg(a.k_scales + static_cast<int64_t>(pid) * a.hkv + h);
+            vsc[t] = __ldg(a.v_scales + static_cast<int64_t>(pid) * a.hkv + h);
+          }
+        }
       }
       kpos[t] = live;
     }
@@ -188,8 +214,13 @@ forward_cc_kernel(ForwardArgs a) {
         const int64_t e = w.z + row / qhead;
         const int qh = row % qhead;
         const int64_t qi = a.edges[2 * e];
-        const float4 v = *reinterpret_cast<const float4*>(
-            a.q + (qi * a.hq + static_cast<int64_t>(h) * qhead + qh) * d + 4 * c);
+        const int64_t qoff = (qi * a.hq + static_cast<int64_t>(h) * qhead + qh) * d + 4 * c;
+        float4 v;
+        if (is_q8(kT) && a.q_bf16)
+          v = bf16x4_to_f32(*reinterpret_cast<const uint2*>(
+              reinterpret_cast<const uint16_t*>(a.q) + qoff));
+        else
+          v = *reinterpret_cast<const float4*>(a.q + qoff);
         reinterpret_cast<float4*>(qs + r * d)[c] = v;
         if (c == 0) {
           int64_t lim = INT32_MAX;
@@ -212,7 +243,7 @@ forward_cc_kernel(ForwardArgs a) {
           float acc = 0.f;
           int c = t % nc;
           for (int cc = 0; cc < nc; ++cc) {
-            const float4 kv = load4<kBf16>(ks, t, c, d);
+            const float4 kv = load4<kT>(ks, t, c, d);
             const float4 qv = qrow[c];
             acc = fmaf(qv.x, kv.x, acc);
             acc = fmaf(qv.y, kv.y, acc);
@@ -221,6 +252,7 @@ forward_cc_kernel(ForwardArgs a) {
             if (++c == nc) c = 0;
           }
           s = acc * a.scale;
+          if constexpr (is_q8(kT)) s *= ksc[t];
         }
         ps[r * bs + t] = s;
       }
@@ -235,7 +267,7 @@ forward_cc_kernel(ForwardArgs a) {
         for (int t = lane; t < bs; t += 32) {
           const float s = ps[r * bs + t];
           const float p = (m == -INFINITY || s == -INFINITY) ? 0.f : __expf(s - m);
-          ps[r * bs + t] = p;
+          ps[r * bs + t] = is_q8(kT) && p != 0.f ? p * vsc[t] : p;
           l += p;
         }
 #pragma unroll
@@ -254,7 +286,8 @@ forward_cc_kernel(ForwardArgs a) {
         const float* prow = ps + r * bs;
         for (int t = 0; t < bs; ++t) {
           const float p = prow[t];
-          const float4 vv = load4<kBf16>(vs, t, c, d);
+          if (is_q8(kT) && p == 0.f) continue;
+          const float4 vv = load4<kT>(vs, t, c, d);
           acc.x = fmaf(p, vv.x, acc.x);
           acc.y = fmaf(p, vv.y, acc.y);
           acc.z = fmaf(p, vv.z, acc.z);
@@ -269,19 +302,20 @@ forward_cc_kernel(ForwardArgs a) {
 
 }  // namespace
 
-bool forward_cc_supported(int head_dim, int block_size, int kv_bf16) {
+bool forward_cc_supported(int head_dim, int block_size, int kv_type) {
   if (head_dim <= 0 || head_dim > kMaxDim) return false;
-  if (head_dim % (kv_bf16 ? 8 : 4) != 0) return false;
+  if (head_dim % static_cast<int>(16 / elt_bytes(kv_type)) != 0) return false;
   if (block_size <= 0) return false;
-  const SmemPlan p = plan_smem(block_size, head_dim, kv_bf16);
+  const SmemPlan p = plan_smem(block_size, head_dim, kv_type);
   return p.kv_bytes * 2 <= 160 * 1024 && p.total <= 227 * 1024;
 }
 
-cudaError_t launch_forward_cc(const ForwardArgs& a, cudaStream_t stream) {
-  if (!forward_cc_supported(a.head_dim, a.block_size, a.kv_bf16)) return cudaErrorNotSupported;
-  const SmemPlan p = plan_smem(a.block_size, a.head_dim, a.kv_bf16);
-  const void* fn = a.kv_bf16 ? reinterpret_cast<const void*>(forward_cc_kernel<true>)
-                             : reinterpret_cast<const void*>(forward_cc_kernel<false>);
+namespace {
+
+template <int kT>
+cudaError_t launch_cc(const ForwardArgs& a, cudaStream_t stream) {
+  const SmemPlan p = plan_smem(a.block_size, a.head_dim, kT);
+  const void* fn = reinterpret_cast<const void*>(forward_cc_kernel<kT>);
   cudaError_t err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(p.total));
   if (err != cudaSuccess) return err;
@@ -295,11 +329,20 @@ cudaError_t launch_forward_cc(const ForwardArgs& a, cudaStream_t stream) {
   int64_t grid = static_cast<int64_t>(device_sm_count()) * per_sm;
   if (grid > a.max_splits) grid = a.max_splits;
   if (grid < 1) grid = 1;
-  if (a.kv_bf16)
-    forward_cc_kernel<true><<<static_cast<unsigned>(grid), kThreads, p.total, stream>>>(a);
-  else
-    forward_cc_kernel<false><<<static_cast<unsigned>(grid), kThreads, p.total, stream>>>(a);
+  forward_cc_kernel<kT><<<static_cast<unsigned>(grid), kThreads, p.total, stream>>>(a);
   return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_forward_cc(const ForwardArgs& a, cudaStream_t stream) {
+  if (!forward_cc_supported(a.head_dim, a.block_size, a.kv_type)) return cudaErrorNotSupported;
+  switch (a.kv_type) {
+    case SA_DTYPE_F32: return launch_cc<SA_DTYPE_F32>(a, stream);
+    case SA_DTYPE_BF16: return launch_cc<SA_DTYPE_BF16>(a, stream);
+    case SA_DTYPE_E4M3: return launch_cc<SA_DTYPE_E4M3>(a, stream);
+    default: return launch_cc<SA_DTYPE_INT8>(a, stream);
+  }
 }
 
 }  // namespace sa

@@ -343,7 +343,7 @@ forward_dec_kernel(ForwardArgs a) {
 
 template <int R, bool kBf16, int NST, int WARPS>
 cudaError_t launch_dec(const ForwardArgs& a, cudaStream_t stream) {
-  const WarpPlan p = warp_plan(R, a.kv_bf16, NST);
+  const WarpPlan p = warp_plan(R, a.kv_type == SA_DTYPE_BF16, NST);
   const size_t smem = p.warp_bytes * WARPS;
   if (smem > 227 * 1024) return cudaErrorNotSupported;
   const void* fn = reinterpret_cast<const void*>(forward_dec_kernel<R, kBf16, NST, WARPS>);
@@ -364,8 +364,8 @@ cudaError_t launch_dec(const ForwardArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-bool forward_dec_supported(int head_dim, int block_size, int page_size, int qhead, int kv_bf16) {
-  (void)kv_bf16;
+bool forward_dec_supported(int head_dim, int block_size, int page_size, int qhead, int kv_type) {
+  if (kv_type != SA_DTYPE_F32 && kv_type != SA_DTYPE_BF16) return false;
   if (head_dim != kD) return false;
   // at least two chunks per block keeps the Q buffers of the ring apart
   if (block_size % kKC != 0 || block_size < 2 * kKC) return false;
@@ -378,11 +378,11 @@ bool forward_dec_supported(int head_dim, int block_size, int page_size, int qhea
 }
 
 cudaError_t launch_forward_dec(const ForwardArgs& a, cudaStream_t stream) {
-  if (!forward_dec_supported(a.head_dim, a.block_size, a.page_size, a.qhead, a.kv_bf16))
+  if (!forward_dec_supported(a.head_dim, a.block_size, a.page_size, a.qhead, a.kv_type))
     return cudaErrorNotSupported;
   if (a.qhead <= 4)
-    return a.kv_bf16 ? launch_dec<4, true, 4, 5>(a, stream) : launch_dec<4, false, 3, 4>(a, stream);
-  return a.kv_bf16 ? launch_dec<8, true, 3, 6>(a, stream) : launch_dec<8, false, 3, 3>(a, stream);
+    return a.kv_type == SA_DTYPE_BF16 ? launch_dec<4, true, 4, 5>(a, stream) : launch_dec<4, false, 3, 4>(a, stream);
+  return a.kv_type == SA_DTYPE_BF16 ? launch_dec<8, true, 3, 6>(a, stream) : launch_dec<8, false, 3, 3>(a, stream);
 }
 
 }  // namespace sa

@@ -428,8 +428,8 @@ cudaError_t launch_dec_mma(const ForwardArgs& a, cudaStream_t stream) {
 }  // namespace
 
 bool forward_dec_mma_supported(int head_dim, int block_size, int page_size, int qhead,
-                               int kv_bf16) {
-  if (!kv_bf16 || head_dim != kD) return false;
+                               int kv_type) {
+  if (kv_type != SA_DTYPE_BF16 || head_dim != kD) return false;
   // at least two chunks per block keeps the two Q buffers apart
   if (block_size % kKC != 0 || block_size < 2 * kKC) return false;
   if (page_size <= 0 || block_size % page_size || block_size / page_size > kMaxPages) return false;
@@ -437,7 +437,7 @@ bool forward_dec_mma_supported(int head_dim, int block_size, int page_size, int 
 }
 
 cudaError_t launch_forward_dec_mma(const ForwardArgs& a, cudaStream_t stream) {
-  if (!forward_dec_mma_supported(a.head_dim, a.block_size, a.page_size, a.qhead, a.kv_bf16))
+  if (!forward_dec_mma_supported(a.head_dim, a.block_size, a.page_size, a.qhead, a.kv_type))
     return cudaErrorNotSupported;
   if (a.qhead <= 8)
     return a.o_bf16 ? launch_dec_mma<8, 3, 6, true>(a, stream)

@@ -17,7 +17,7 @@
 //              every unit with its global addresses at hand; an end-of-work
 //              unit stops the other roles;
 //   warps 1-14 loaders: per unit, the block's K and V rows (through the
-//              block table, f32 or bf16) converted to bf16 once, both as
+//              block table, any K/V type) converted to bf16 once, both as
 //              [keys x 128] rows with the 128-byte swizzle: K-major for S,
 //              MN-major for O (two unit buffers, so the next unit loads
 //              while this one computes); per tile, the rows' Q in the same
@@ -46,6 +46,7 @@
 
 #include "internal.h"
 #include "sa_common.cuh"
+#include "seq_common.cuh"
 
 namespace sa {
 
@@ -253,10 +254,18 @@ __device__ __forceinline__ uint32_t sw128_offset(int rows, int r, int k) {
   return static_cast<uint32_t>(panel * rows * 128 + r * 128 + ((chunk ^ (r & 7)) << 4) + within);
 }
 
-// Four K/V elements (f32 or bf16) as packed bf16 (round to nearest even).
-template <bool kBf16>
-__device__ __forceinline__ uint2 ld_kv4_bf16(const void* pages, int64_t elem_off) {
-  if constexpr (kBf16) {
+// Four K/V elements as packed bf16 (round to nearest even); 8-bit codes times
+// the scale of their page (exact in bf16 under a power-of-two scale).
+template <int kT>
+__device__ __forceinline__ uint2 ld_kv4_bf16(const void* pages, int64_t elem_off, float scale) {
+  if constexpr (kT == SA_DTYPE_E4M3 || kT == SA_DTYPE_INT8) {
+    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(pages) + elem_off));
+    uint32_t h0, h1;
+    codes4_to_f16<kT == SA_DTYPE_INT8>(w, h0, h1);
+    const float2 x = f16x2_to_f32(h0), y = f16x2_to_f32(h1);
+    return make_uint2(pack_bf16x2_rn(x.x * scale, x.y * scale),
+                      pack_bf16x2_rn(y.x * scale, y.y * scale));
+  } else if constexpr (kT == SA_DTYPE_BF16) {
     return __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(pages) + elem_off));
   } else {
     const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(pages) + elem_off));
@@ -510,7 +519,7 @@ __device__ void tc_scheduler(const ForwardArgs& a, unsigned char* smem, const Tc
 
 // ------------------------------------------------------------------ loaders
 
-template <int BS, bool kBf16, bool kTf32>
+template <int BS, int kT, bool kTf32>
 __device__ void tc_loader(const ForwardArgs& a, unsigned char* smem, const TcPlan& P,
                           const TcBars& B, int lw, int lane) {
   constexpr int KVB = TcCfg<BS, kTf32>::KVB;
@@ -596,8 +605,17 @@ __device__ void tc_loader(const ForwardArgs& a, unsigned char* smem, const TcPla
           const int r = lw + (q0 + q) * kLoaders;
           const int key = r < BS ? r : r - BS;
           const int64_t off = q0 + q < kRows && r < 2 * BS ? koff[key] : -1;
-          kr[q] = off >= 0 ? ld_kv4_bf16<kBf16>(r < BS ? a.k_pages : a.v_pages, off + 4 * lane)
-                           : make_uint2(0u, 0u);
+          float sc = 1.f;
+          if constexpr (kT == SA_DTYPE_E4M3 || kT == SA_DTYPE_INT8) {
+            // off / (page_size * 128) numbers the (page, kv head); a pool of
+            // 2^32 rows of 128 codes would not fit the device
+            if (off >= 0)
+              sc = __ldg((r < BS ? a.k_scales : a.v_scales) +
+                         static_cast<uint32_t>(off >> 7) / static_cast<uint32_t>(a.page_size));
+          }
+          kr[q] = off >= 0
+                      ? ld_kv4_bf16<kT>(r < BS ? a.k_pages : a.v_pages, off + 4 * lane, sc)
+                      : make_uint2(0u, 0u);
         }
 #pragma unroll
         for (int q = 0; q < kKvBatch; ++q) {
@@ -1212,7 +1230,7 @@ __device__ void tc_softmax(const ForwardArgs& a, const CUtensorMap* omap, unsign
 
 // ------------------------------------------------------------------ kernel
 
-template <int BS, bool kBf16, bool kTf32>
+template <int BS, int kT, bool kTf32>
 __global__ void __launch_bounds__(TcWarps<BS>::kThreads, 1)
 forward_tc_kernel(const __grid_constant__ CUtensorMap omap, ForwardArgs a) {
   constexpr int KVB = TcCfg<BS, kTf32>::KVB;
@@ -1304,7 +1322,7 @@ forward_tc_kernel(const __grid_constant__ CUtensorMap omap, ForwardArgs a) {
     } else if (warp == kSchedWarp) {
       tc_scheduler<BS>(a, smem, P, B, unit_base, n_units, lane);
     } else {
-      tc_loader<BS, kBf16, kTf32>(a, smem, P, B, warp - kLoaderWarp0, lane);
+      tc_loader<BS, kT, kTf32>(a, smem, P, B, warp - kLoaderWarp0, lane);
     }
   }
   tc_fence_before();
@@ -1422,11 +1440,11 @@ __global__ void __launch_bounds__(kOrderThreads) unit_order_kernel(ForwardArgs a
   if (c >= 0) a.unit_order[wcnt[warp][c] + rank] = static_cast<int32_t>(u);
 }
 
-template <int BS, bool kBf16, bool kTf32>
+template <int BS, int kT, bool kTf32>
 cudaError_t launch_tc(const ForwardArgs& a, cudaStream_t stream) {
   const TcPlan p = tc_plan<BS, kTf32>();
   if (p.total > 227 * 1024) return cudaErrorNotSupported;
-  const void* fn = reinterpret_cast<const void*>(forward_tc_kernel<BS, kBf16, kTf32>);
+  const void* fn = reinterpret_cast<const void*>(forward_tc_kernel<BS, kT, kTf32>);
   cudaError_t err =
       cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(p.total));
   if (err != cudaSuccess) return err;
@@ -1473,7 +1491,7 @@ cudaError_t launch_tc(const ForwardArgs& a, cudaStream_t stream) {
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  forward_tc_kernel<BS, kBf16, kTf32>
+  forward_tc_kernel<BS, kT, kTf32>
       <<<static_cast<unsigned>(grid), TcWarps<BS>::kThreads, p.total, stream>>>(omap, args);
   return cudaGetLastError();
 }
@@ -1519,13 +1537,25 @@ cudaError_t launch_forward_tc(const ForwardArgs& a, cudaStream_t stream) {
   if (!forward_tc_supported(a.head_dim, a.block_size, a.page_size, a.qhead) || a.hkv > 200)
     return cudaErrorNotSupported;
   // tf32 operands only for f32 K/V (bf16 K/V are exact in bf16)
-  const bool tf32 = a.tf32 && !a.kv_bf16;
-  if (a.block_size == 64) {
-    if (a.kv_bf16) return launch_tc<64, true, false>(a, stream);
-    return tf32 ? launch_tc<64, false, true>(a, stream) : launch_tc<64, false, false>(a, stream);
+  const bool tf32 = a.tf32 && a.kv_type == SA_DTYPE_F32;
+  const bool wide = a.block_size == 128;
+  switch (a.kv_type) {
+    case SA_DTYPE_F32:
+      if (tf32)
+        return wide ? launch_tc<128, SA_DTYPE_F32, true>(a, stream)
+                    : launch_tc<64, SA_DTYPE_F32, true>(a, stream);
+      return wide ? launch_tc<128, SA_DTYPE_F32, false>(a, stream)
+                  : launch_tc<64, SA_DTYPE_F32, false>(a, stream);
+    case SA_DTYPE_BF16:
+      return wide ? launch_tc<128, SA_DTYPE_BF16, false>(a, stream)
+                  : launch_tc<64, SA_DTYPE_BF16, false>(a, stream);
+    case SA_DTYPE_E4M3:
+      return wide ? launch_tc<128, SA_DTYPE_E4M3, false>(a, stream)
+                  : launch_tc<64, SA_DTYPE_E4M3, false>(a, stream);
+    default:
+      return wide ? launch_tc<128, SA_DTYPE_INT8, false>(a, stream)
+                  : launch_tc<64, SA_DTYPE_INT8, false>(a, stream);
   }
-  if (a.kv_bf16) return launch_tc<128, true, false>(a, stream);
-  return tf32 ? launch_tc<128, false, true>(a, stream) : launch_tc<128, false, false>(a, stream);
 }
 
 }  // namespace sa

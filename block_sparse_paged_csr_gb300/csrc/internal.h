@@ -86,11 +86,14 @@ cudaError_t launch_clear_for_build(void* workspace, size_t bytes, int64_t* statu
                                    cudaStream_t stream);
 
 struct ForwardArgs {
-  const float* q;
+  const float* q;           // bf16 values when q_bf16 (8-bit K/V only)
+  int q_bf16;
   const void* k_pages;
   const void* v_pages;
   int64_t num_pages;
-  int kv_bf16;
+  int kv_type;              // an sa_dtype
+  const float* k_scales;    // [num_pages, hkv], 8-bit K/V only
+  const float* v_scales;
   const int32_t* block_tables;
   const int64_t* cu;
   const int32_t* used;      // nullable
@@ -129,7 +132,7 @@ struct ForwardArgs {
 
 // Returns cudaErrorNotSupported when the shape has no kernel.
 cudaError_t launch_forward_cc(const ForwardArgs& a, cudaStream_t stream);
-bool forward_cc_supported(int head_dim, int block_size, int kv_bf16);
+bool forward_cc_supported(int head_dim, int block_size, int kv_type);
 
 // Tensor-core (tcgen05) forward for units with many gathered rows.
 cudaError_t launch_forward_tc(const ForwardArgs& a, cudaStream_t stream);
@@ -141,20 +144,23 @@ bool forward_tc_supported(int head_dim, int block_size, int page_size, int qhead
 // Decode-shaped forward with bf16 K/V on warp-level tensor-core MMA.
 cudaError_t launch_forward_dec_mma(const ForwardArgs& a, cudaStream_t stream);
 bool forward_dec_mma_supported(int head_dim, int block_size, int page_size, int qhead,
-                               int kv_bf16);
+                               int kv_type);
 
 // Pipelined decode-shaped forward (head_dim 128, few rows per split).
 cudaError_t launch_forward_dec(const ForwardArgs& a, cudaStream_t stream);
-bool forward_dec_supported(int head_dim, int block_size, int page_size, int qhead, int kv_bf16);
+bool forward_dec_supported(int head_dim, int block_size, int page_size, int qhead, int kv_type);
 
 // Fused decode attention (forward and combine in one kernel) for batches in
 // which every sequence holds at most one query.
 struct FusedDecArgs {
-  const float* q;
+  const float* q;           // bf16 values when q_bf16 (8-bit K/V only)
+  int q_bf16;
   const void* k_pages;
   const void* v_pages;
   int64_t num_pages;
-  int kv_bf16;
+  int kv_type;              // an sa_dtype
+  const float* k_scales;    // [num_pages, hkv], 8-bit K/V only
+  const float* v_scales;
   const int32_t* block_tables;
   const int64_t* cu;
   const int32_t* used;      // nullable
@@ -173,7 +179,8 @@ struct FusedDecArgs {
   int part_bf16;            // o rows f32, or bf16 when part_bf16
   float* part_m;
   float* part_l;
-  float* out;
+  void* out;                // f32, or bf16 when out_bf16
+  int out_bf16;
   float* lse;               // nullable
   int pdl;                  // launched right behind the index kernel that built the
                             // index: it may start while that kernel runs (it reads
@@ -184,7 +191,7 @@ struct FusedDecArgs {
 
 // Whether the fused decode kernel supports this shape (the caller also checks
 // that every sequence holds at most one query and the pool size limits).
-bool fused_dec_supported(int head_dim, int block_size, int page_size, int qhead, int kv_bf16);
+bool fused_dec_supported(int head_dim, int block_size, int page_size, int qhead, int kv_type);
 // Largest pool (num_pages * hkv * page_size key rows) the kernel addresses.
 constexpr int64_t kFusedMaxRows = (int64_t{1} << 31) - 1;
 cudaError_t launch_fused_dec(const FusedDecArgs& a, cudaStream_t stream);
@@ -198,7 +205,8 @@ struct CombineArgs {
   const float* l_partial;
   int64_t tq;
   int32_t hkv, topk, qhead, head_dim;
-  float* out;
+  void* out;                // f32, or bf16 when out_bf16
+  int out_bf16;
   float* lse;               // nullable
 };
 

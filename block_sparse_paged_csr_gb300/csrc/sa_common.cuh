@@ -176,9 +176,9 @@ __device__ __forceinline__ uint32_t pack_bf16x2_rn(float lo, float hi) {
   return r;
 }
 
-// Four consecutive elements of a partial o buffer, starting at element `off`
-// (a multiple of 4): f32, or bf16 rounded to nearest even when the caller
-// asked for 16-bit o partials.
+// Four consecutive elements of a partial o (or output) buffer, starting at
+// element `off` (a multiple of 4): f32, or bf16 rounded to nearest even when
+// the caller asked for 16-bit o partials (or gave bf16 queries).
 __device__ __forceinline__ void store_o4(void* o, int bf16, int64_t off, float4 v) {
   if (bf16)
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(o) + off) =

@@ -476,6 +476,65 @@ sa_status sa_attention_ex(const float *q, const void *k_pages, const void *v_pag
                           float *l_partial, float *out, float *lse, sa_path path, void *stream);
 
 /*
+ * sa_forward_ex, sa_forward_combine_ex and sa_attention_ex over a cache held in
+ * 8 bits (sa_store_kv): kv_dtype SA_DTYPE_E4M3 or SA_DTYPE_INT8, key =
+ * code * k_scales[page, kv head], value = code * v_scales[page, kv head]; the
+ * entry points without scales refuse these types, and these refuse the others
+ * (SA_ERR_INVALID_ARGUMENT).
+ *
+ *   q             [tq, hq, head_dim] of q_dtype: float32 or bf16; `out` has the
+ *                 same type (lse and the partials' m and l stay float32)
+ *   k_scales,
+ *   v_scales      [num_pages, hkv] f32, finite; any values, powers of two or not
+ *
+ * Kernels: batches of one query per sequence take the fused decode path under
+ * the conditions given at sa_attention (8-bit: page_size a power of two of at
+ * least 16, qhead <= 16), with products exact to 2^-21 and f32 sums; other
+ * problems the tcgen05 kernel where it is supported (keys, values, queries and
+ * P rounded to bf16: code * scale is exact there under a power-of-two scale),
+ * decode-shaped ones and the rest the general f32 FMA kernel.  SA_PATH_CUDA_CORE
+ * means the general kernel.  head_dim: a multiple of 16, at most 256.  Codes
+ * behind a sequence's length or on absent pages are never used, whatever they
+ * hold; a NaN code at a key that only the causal mask hides may reach the
+ * outputs of the tcgen05 kernel.  Checks as for the entry points above;
+ * INVALID_ARGUMENT also for NULL scales.
+ */
+sa_status sa_forward_scaled(const void *q, sa_dtype q_dtype, const void *k_pages,
+                            const void *v_pages, const float *k_scales, const float *v_scales,
+                            int64_t num_pages, sa_dtype kv_dtype, const sa_index *idx,
+                            const int32_t *block_tables, const int64_t *cu_seqlens_q,
+                            const int32_t *used_kv_lens, int32_t hq, int32_t hkv,
+                            int32_t head_dim, int32_t block_size, int32_t page_size,
+                            float softmax_scale, int32_t causal, sa_dtype partial_dtype,
+                            void *o_partial, float *m_partial, float *l_partial, sa_path path,
+                            void *stream);
+
+sa_status sa_forward_combine_scaled(const void *q, sa_dtype q_dtype, const void *k_pages,
+                                    const void *v_pages, const float *k_scales,
+                                    const float *v_scales, int64_t num_pages, sa_dtype kv_dtype,
+                                    const sa_index *idx, const int32_t *selected,
+                                    const int64_t *cu_seqlens_q_host, const int64_t *cu_seqlens_q,
+                                    const int32_t *used_kv_lens, const int32_t *block_tables,
+                                    int32_t hq, int32_t head_dim, int32_t block_size,
+                                    int32_t page_size, float softmax_scale, int32_t causal,
+                                    int32_t split_edges, sa_dtype partial_dtype, void *o_partial,
+                                    float *m_partial, float *l_partial, void *out, float *lse,
+                                    sa_path path, void *stream);
+
+sa_status sa_attention_scaled(const void *q, sa_dtype q_dtype, const void *k_pages,
+                              const void *v_pages, const float *k_scales, const float *v_scales,
+                              int64_t num_pages, sa_dtype kv_dtype, const int32_t *selected,
+                              int64_t tq, int32_t topk, const int64_t *cu_seqlens_q_host,
+                              const int64_t *cu_seqlens_q, int32_t batch,
+                              const int32_t *used_kv_lens, const int32_t *block_tables,
+                              int32_t max_pages, int32_t hq, int32_t hkv, int32_t head_dim,
+                              int32_t block_size, int32_t page_size, float softmax_scale,
+                              int32_t causal, int32_t split_edges, sa_index *idx,
+                              sa_dtype partial_dtype, void *o_partial, float *m_partial,
+                              float *l_partial, void *out, float *lse, sa_path path,
+                              void *stream);
+
+/*
  * Writing the paged cache.  The rows of new tokens go to the cache's pages:
  * new token t of sequence b (row cu_seqlens_q[b] + t of k and v) to position
  * lk_b - qo_b + t, where lk_b = used_kv_lens[b] is the length WITH the new

@@ -153,3 +153,94 @@ def test_binding_refusals():
         sa._scales(torch.zeros((3, 2)), codes.float(), "k_scales")
     with pytest.raises(TypeError):
         sa.sa_select_blocks(x.half(), None, None, [0, 2], None, None, 16, 2, True)
+
+
+def test_scaled_attention_refusals(lib):  # noqa: F811
+    """The entry points with scales: 8-bit K/V only, scales required, the other
+    checks as for the entry points without; those refuse 8-bit K/V."""
+    from block_sparse_paged_csr_gb300 import _native
+
+    n = _names()
+    cu = np.array([0, 1, 2, 3, 4], np.int64)
+    pcu = cu.ctypes.data_as(ctypes.c_void_p)
+
+    def index(**kw):
+        a = dict(hkv=2, pages_per_block=4, block_size=64, page_size=16, tq=4, topk=2, batch=4, msb=2)
+        a.update(kw)
+        return _native.SaIndex(**a)
+
+    def fwd(idx=None, qt=0, kv=2, ks=P, vs=P, hq=4, hkv=2, d=128, bs=64, ps=16, causal=0, path=0,
+            pdt=0, q=P):
+        idx = index() if idx is None else idx
+        return lib.sa_forward_scaled(q, qt, P, P, ks, vs, 16, kv, ctypes.byref(idx), P, P, None, hq,
+                                     hkv, d, bs, ps, 0.1, causal, pdt, P, P, P, path, None)
+
+    assert fwd(hq=3) == n["HEAD_COUNT"]
+    assert fwd(bs=24) == n["BLOCK_PAGE"]
+    assert fwd(bs=32) == n["SHAPE"]
+    assert fwd(kv=0) == n["INVALID_ARGUMENT"]
+    assert fwd(kv=1) == n["INVALID_ARGUMENT"]
+    assert fwd(kv=4) == n["INVALID_ARGUMENT"]
+    assert fwd(qt=2) == n["INVALID_ARGUMENT"]
+    assert fwd(pdt=2) == n["INVALID_ARGUMENT"]
+    assert fwd(causal=3) == n["INVALID_ARGUMENT"]
+    assert fwd(path=4) == n["UNSUPPORTED"]
+    assert fwd(d=40) == n["UNSUPPORTED"]
+    assert fwd(ks=None) == n["INVALID_ARGUMENT"]
+    assert fwd(vs=None) == n["INVALID_ARGUMENT"]
+    assert fwd(q=ODD) == n["INVALID_ARGUMENT"]
+
+    def both(kv=2, ks=P, vs=P, path=0, hq=4, q=P, ws=P, cu_host=pcu):
+        idx = index(workspace=4096, workspace_bytes=1 << 20, inv=4096, totals=4096)
+        if ws is None:
+            idx.workspace = None
+        return lib.sa_forward_combine_scaled(q, 0, P, P, ks, vs, 16, kv, ctypes.byref(idx), P,
+                                             cu_host, P, None, P, hq, 128, 64, 16, 0.1, 1, 0, 0, P, P,
+                                             P, P, P, path, None)
+
+    assert both(kv=1) == n["INVALID_ARGUMENT"]
+    assert both(hq=3) == n["HEAD_COUNT"]
+    assert both(ks=None) == n["INVALID_ARGUMENT"]
+    assert both(q=ODD) == n["INVALID_ARGUMENT"]
+    assert both(ws=None) == n["INVALID_ARGUMENT"]      # the fused path's counters
+    assert both(hq=34, path=4) == n["UNSUPPORTED"]     # 17 lanes
+
+    def att(kv=3, hq=4, d=128, bs=64, causal=1, path=0, sel=None):
+        idx = _native.SaIndex()
+        return lib.sa_attention_scaled(P, 0, P, P, P, P, 16, kv, sel, 4, 2, pcu, P, 4, None, P, 8, hq,
+                                       2, d, bs, 16, 0.1, causal, 0, ctypes.byref(idx), 0, P, P, P, P,
+                                       P, path, None)
+
+    assert att(kv=0) == n["INVALID_ARGUMENT"]
+    assert att(hq=5) == n["HEAD_COUNT"]
+    assert att(bs=40) == n["BLOCK_PAGE"]
+    assert att(d=24) == n["UNSUPPORTED"]
+    assert att(causal=7) == n["INVALID_ARGUMENT"]
+    assert att(path=4, causal=2) == n["UNSUPPORTED"]
+    assert att() == n["INVALID_ARGUMENT"]              # no selection, no index arrays
+    # without scales: the 8-bit types are refused as before
+    idx = index()
+    assert lib.sa_forward(P, P, P, 16, 2, ctypes.byref(idx), P, P, None, 4, 2, 128, 64, 16, 0.1, 0,
+                          P, P, P, 0, None) == n["INVALID_ARGUMENT"]
+
+
+def test_scaled_kernel_choice():
+    import block_sparse_paged_csr_gb300 as sa
+
+    one = np.array([0, 1, 1, 2, 3], np.int64)
+    many = np.array([0, 40, 80], np.int64)
+    name = sa.sa_attention_kernel_name
+    for kind in ("e4m3", "int8"):
+        assert name(one, 1000, 8, 32, 128, 64, 16, kind) == "fused_dec_kernel"
+        assert name(one, 1000, 2, 32, 128, 64, 16, kind) == "fused_dec_kernel"
+        assert name(one, 1000, 1, 32, 128, 64, 16, kind) == "forward_cc_kernel"   # 32 lanes
+        assert name(one, 1000, 8, 32, 128, 64, 8, kind) == "forward_cc_kernel"    # pages of 8
+        assert name(one, 1000, 8, 32, 64, 64, 16, kind) == "forward_cc_kernel"
+        assert name(one, 1000, 8, 32, 128, 64, 16, kind, causal=2) == "forward_cc_kernel"
+        assert name(many, 1000, 8, 64, 128, 128, 64, kind) == "forward_tc_kernel"
+        assert name(many, 1000, 8, 64, 64, 128, 64, kind) == "forward_cc_kernel"
+        assert name(many, 1000, 8, 64, 72, 128, 64, kind) is None
+        assert sa.sa_forward_kernel_name(80, 2, 8, 64, 128, 128, 64, kind,
+                                         sa.PATH_TENSOR_CORE) == "forward_tc_kernel"
+        assert sa.sa_forward_kernel_name(80, 2, 8, 64, 128, 128, 64, kind,
+                                         sa.PATH_CUDA_CORE) == "forward_cc_kernel"

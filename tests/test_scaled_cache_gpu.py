@@ -1,0 +1,351 @@
+"""Attention over a cache held in 8 bits (e4m3, int8; a scale per page and kv
+head) against the oracle in 64 bits on the values the codes stand for.
+
+Tolerances (row-normalised, as in the other parity tests): the fused decode
+and general kernels take codes exactly and split Q and P into two f16 parts or
+keep them in f32, so they are held to the f32 class, 1e-4; a bf16 output adds
+its rounding of 2^-8; the tensor-core kernel rounds Q, P and K/V to bf16, 2e-2 for keys of unit size.
+There the error is that of the scores: rounding q and k moves a score by at most
+2 * 2^-8 * scale * sum |q_d k_d|, which is proportional to the keys' size, and p
+with it.  The keys here are up to several times larger (their scales are what is
+tested), so the class is multiplied by their root mean square where that is
+above 1."""
+import math
+from dataclasses import replace
+
+import numpy as np
+import pytest
+import torch
+
+import _gpu
+import block_sparse_paged_csr_gb300 as sa
+import inputs
+import oracle
+
+pytestmark = pytest.mark.gpu
+
+TORCH = {"e4m3": torch.float8_e4m3fn, "int8": torch.int8}
+HALF_BF16 = 2.0 ** -8
+
+
+def scaled_workload(w, kind, act="f32", scales="pow2", seed=0, dirty=True):
+    """Device tensors of workload `w` with K/V in 8 bits, and the f32 values
+    they stand for.  Rows that no sequence reaches hold NaN codes (e4m3) or
+    large ones."""
+    rng = np.random.default_rng(seed + 77)
+    t = _gpu.device_workload(replace(w, kv_dtype="f32"))
+    t["q"] = t["q"].to(torch.bfloat16) if act == "bf16" else t["q"]
+    live = np.zeros((w.num_pages, w.page_size), bool)
+    for b in range(w.batch):
+        n = int(w.used_kv_lens[b]) if w.pass_used else w.msb * w.block_size
+        for p in range(min(-(-n // w.page_size), w.max_pages)):
+            page = w.block_tables[b, p]
+            if 0 <= page < w.num_pages:
+                live[page, :max(0, min(n - p * w.page_size, w.page_size))] = True
+    vals = {}
+    for name in ("k", "v"):
+        x = t[name].view(w.num_pages, w.hkv, w.page_size, w.head_dim)
+        shape = (w.num_pages, w.hkv)
+        if scales == "pow2":
+            s = 2.0 ** rng.integers(-6, -3, shape)
+        elif scales == "any":
+            s = rng.uniform(0.02, 0.1, shape)
+        elif scales == "wide":                   # of V: those of K set the scores' size
+            s = 2.0 ** (rng.integers(-16, 5, shape) if name == "v" else rng.integers(-6, -3, shape))
+        else:                                    # some pages stand for zeros
+            s = np.where(rng.random(shape) < 0.3, 0.0, 0.04)
+        s = torch.from_numpy(s.astype(np.float32)).cuda()
+        gain = 30.0 if kind == "int8" else 90.0
+        codes = (x * gain).round() if kind == "int8" else x * gain
+        codes = codes.clamp(-127, 127).to(TORCH[kind])
+        v = (codes.float() * s[:, :, None, None]).cpu().numpy()
+        if dirty:
+            dead = torch.from_numpy(~live).cuda()[:, None, :, None].expand_as(codes)
+            raw = codes.view(torch.uint8)
+            raw[dead] = 0x7F
+        t[name], t[name + "s"] = codes, s
+        v[~np.broadcast_to(live[:, None, :, None], v.shape)] = 0.0
+        vals[name] = v
+    return t, vals
+
+
+def reference(w, t, vals):
+    return oracle.attention(t["q"].float().cpu().numpy(), vals["k"], vals["v"], w.selected,
+                            w.block_tables, w.cu_seqlens_q, w.used, w.hq, w.head_dim, w.block_size,
+                            w.page_size, w.softmax_scale, w.causal)
+
+
+def attend(w, t, **kw):
+    out, lse, idx, parts = sa.sa_attention(
+        t["q"], t["k"], t["v"], t["selected"], w.cu_seqlens_q, t["cu"], t["used"], t["bt"], w.hq,
+        w.hkv, w.head_dim, w.block_size, w.page_size, w.softmax_scale, w.causal,
+        k_scales=t["ks"], v_scales=t["vs"], **kw)
+    assert sa.sa_get_status(idx) == 0
+    assert out.dtype == t["q"].dtype and lse.dtype == torch.float32
+    return out, lse, idx, parts
+
+
+def kernel(w, kind):
+    return sa.sa_attention_kernel_name(w.cu_seqlens_q, w.num_pages, w.hkv, w.hq, w.head_dim,
+                                       w.block_size, w.page_size, kind, causal=w.causal)
+
+
+def tc_tol(vals):
+    k = vals["k"][vals["k"] != 0]
+    return _gpu.TOL_TC * max(1.0, float(np.sqrt(np.mean(k.astype(np.float64) ** 2))))
+
+
+def check(w, t, vals, tol, name="", **kw):
+    out, lse, idx, parts = attend(w, t, **kw)
+    ref, ref_lse, _, _ = reference(w, t, vals)
+    got = out.float().cpu().numpy()
+    assert np.isfinite(got).all()
+    if t["q"].dtype == torch.bfloat16:
+        tol += HALF_BF16
+    _gpu.report(f"8-bit {name}", "out", got, ref)
+    assert _gpu.row_error(got, ref) <= tol
+    _gpu.compare_lse(lse.cpu().numpy(), ref_lse, min(tol, 1e-4) if tol < 1e-2 else tol)
+    return out, lse
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("name", ["gqa_decode", "long_decode"])
+def test_fused_decode(kind, act, name):
+    w = inputs.small(name, seed=31)
+    assert kernel(w, kind) == "fused_dec_kernel"
+    t, vals = scaled_workload(w, kind, act)
+    check(w, t, vals, _gpu.TOL_F32, f"{name} {kind} {act}")
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("hq,hkv,ps,bs,topk", [
+    (1, 1, 16, 64, 3), (6, 2, 16, 16, 5), (8, 1, 32, 32, 4), (15, 3, 16, 128, 3),
+    (32, 2, 64, 64, 6), (12, 1, 16, 64, 7), (18, 2, 128, 128, 2), (16, 1, 16, 32, 9),
+    (4, 4, 256, 256, 2), (8, 8, 16, 64, 80)])
+def test_fused_decode_geometries(kind, hq, hkv, ps, bs, topk):
+    """Group sizes 1 to 16, pages of 16 to 256 keys, blocks of a page and of
+    several, more ranks than a piece holds."""
+    w = inputs.gqa_decode(41, batch=5, kv_min=max(bs * topk, 300), kv_max=max(bs * topk, 300) + 777,
+                          hq=hq, hkv=hkv, page_size=ps, block_size=bs, topk=topk)
+    assert kernel(w, kind) == "fused_dec_kernel"
+    t, vals = scaled_workload(w, kind)
+    check(w, t, vals, _gpu.TOL_F32, f"fused {hq}/{hkv} {ps}/{bs} {kind}")
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("scales", ["any", "wide", "zeros"])
+@pytest.mark.parametrize("hq", [8, 24])
+def test_fused_decode_scales(kind, scales, hq):
+    w = inputs.gqa_decode(43, batch=4, kv_min=700, kv_max=1500, hq=hq, hkv=2, topk=8)
+    t, vals = scaled_workload(w, kind, scales=scales)
+    check(w, t, vals, _gpu.TOL_F32, f"fused scales {scales} {kind}")
+
+
+@pytest.mark.parametrize("split", [1, 3, 64])
+@pytest.mark.parametrize("partial", [None, "bf16"])
+def test_fused_decode_pieces(split, partial):
+    w = inputs.small("long_decode", seed=33)
+    t, vals = scaled_workload(w, "e4m3", "bf16")
+    check(w, t, vals, _gpu.TOL_F32 if partial is None else HALF_BF16, f"pieces {split} {partial}",
+          split_edges=split, partial_dtype=partial)
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("act,qscale", [("f32", 1e-20), ("f32", 100.0), ("bf16", 1e-6), ("f32", 0.0)])
+def test_fused_decode_query_range(kind, act, qscale):
+    """Queries far from 1 (split into f16 parts after a power of two)."""
+    w = inputs.small("gqa_decode", seed=35)
+    w = replace(w, softmax_scale=w.softmax_scale / (qscale if qscale > 0 else 1.0))
+    t, vals = scaled_workload(w, kind)
+    t["q"] = (t["q"] * qscale).to(torch.bfloat16 if act == "bf16" else torch.float32)
+    check(w, t, vals, _gpu.TOL_F32, f"q x {qscale} {kind}")
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+def test_empty_rows_and_missing_pages(kind):
+    """A sequence of length 0, one of a single key, one whose ranks are all
+    empty, missing pages inside a block, and queries of fewer sequences than
+    the batch."""
+    w = inputs.gqa_decode(45, batch=6, kv_min=300, kv_max=900, hq=8, hkv=2, topk=5)
+    lens = w.used_kv_lens.copy()
+    lens[0], lens[1] = 0, 1
+    sel = w.selected.copy()
+    sel[1] = -1
+    sel[1, :, 2] = 0
+    sel[2] = -1
+    bt = w.block_tables.copy()
+    bt[3, ::3] = -1
+    bt[4, :] = -1
+    qo = w.qo_lens.copy()
+    qo[5] = 0
+    w = replace(w, used_kv_lens=lens, selected=sel[:5].copy(), block_tables=bt, qo_lens=qo)
+    t, vals = scaled_workload(w, kind)
+    out, lse = check(w, t, vals, _gpu.TOL_F32, f"empty {kind}")
+    for i in (0, 2, 4):
+        assert (out[i] == 0).all() and (lse[i] == -math.inf).all()
+
+
+GENERAL = [  # batch, qo, kv, hq, hkv, d, ps, bs, topk
+    (2, 3, 200, 6, 2, 64, 16, 32, 4), (1, 1, 90, 4, 4, 32, 4, 16, 6), (2, 2, 130, 5, 1, 48, 8, 48, 2),
+    (1, 5, 300, 2, 1, 256, 16, 64, 3), (3, 1, 70, 3, 3, 16, 2, 8, 5), (2, 2, 500, 8, 2, 128, 16, 64, 5)]
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("batch,qo,kv,hq,hkv,d,ps,bs,topk", GENERAL)
+def test_general_kernel(kind, act, batch, qo, kv, hq, hkv, d, ps, bs, topk):
+    w = inputs.chunked_prefill(51, batch=batch, qo_len=qo, kv_len=kv, hq=hq, hkv=hkv, head_dim=d,
+                               page_size=ps, block_size=bs, topk=topk)
+    t, vals = scaled_workload(w, kind, act, scales="any")
+    check(w, t, vals, _gpu.TOL_F32, f"general {d} {ps}/{bs} {kind} {act}",
+          path=sa.PATH_CUDA_CORE)
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("name", ["chunked_prefill", "skewed"])
+def test_tensor_cores(kind, act, name):
+    w = inputs.small(name, seed=53)
+    assert kernel(w, kind) == "forward_tc_kernel"
+    t, vals = scaled_workload(w, kind, act)
+    check(w, t, vals, tc_tol(vals), f"{name} {kind} {act}")
+    check(w, t, vals, tc_tol(vals), f"{name} {kind} {act} bf16 partials", partial_dtype="bf16")
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+def test_tensor_cores_odd_lengths(kind):
+    """Lengths that end inside pages, rows of padding, scales of any value."""
+    w = inputs.skewed(55, batch=3, qo_len=37, kv_len=1999, hq=16, hkv=2, topk=6)
+    w = replace(w, used_kv_lens=np.array([1999, 1003, 64], np.int32))
+    t, vals = scaled_workload(w, kind, "bf16", scales="any")
+    check(w, t, vals, tc_tol(vals), f"odd {kind}")
+
+
+@pytest.mark.parametrize("path", [sa.PATH_AUTO, sa.PATH_CUDA_CORE])
+def test_steps_one_by_one(path):
+    """sa_forward and sa_combine, and sa_forward_combine, on a built index."""
+    w = inputs.small("chunked_prefill", seed=57)
+    t, vals = scaled_workload(w, "int8", "f32")
+    ref, ref_lse, _, _ = reference(w, t, vals)
+    tol = tc_tol(vals) if path == sa.PATH_AUTO else _gpu.TOL_F32
+    idx = sa.sa_build_index(t["selected"], w.cu_seqlens_q, t["cu"], t["used"], w.max_pages,
+                            w.block_size, w.page_size)
+    kw = dict(k_scales=t["ks"], v_scales=t["vs"], path=path)
+    o, m, l = sa.sa_forward(t["q"], t["k"], t["v"], idx, t["bt"], t["cu"], t["used"], w.hq, w.hkv,
+                            w.head_dim, w.block_size, w.page_size, w.softmax_scale, w.causal, **kw)
+    out, lse = sa.sa_combine(idx, o, m, l, w.hq, w.head_dim)
+    assert _gpu.row_error(out.cpu().numpy(), ref) <= tol
+    out2, lse2, _ = sa.sa_forward_combine(
+        t["q"], t["k"], t["v"], idx, t["selected"], w.cu_seqlens_q, t["cu"], t["used"], t["bt"],
+        w.hq, w.head_dim, w.block_size, w.page_size, w.softmax_scale, w.causal, **kw)
+    assert sa.sa_get_status(idx) == 0
+    assert _gpu.row_error(out2.cpu().numpy(), ref) <= tol
+    _gpu.compare_lse(lse2.cpu().numpy(), ref_lse, tol)
+
+
+def test_arguments():
+    w = inputs.small("gqa_decode", seed=59)
+    t, _ = scaled_workload(w, "int8")
+    with pytest.raises(ValueError):
+        attend(w, dict(t, ks=None))
+    with pytest.raises(ValueError):
+        attend(w, dict(t, vs=t["vs"][:-1].contiguous()))
+    with pytest.raises(TypeError):
+        attend(w, dict(t, ks=t["ks"].double()))
+    with pytest.raises(TypeError):
+        attend(w, dict(t, q=t["q"].half()))
+    with pytest.raises(TypeError):
+        attend(w, t, out=torch.empty_like(t["q"], dtype=torch.bfloat16))
+    with pytest.raises(TypeError):
+        attend(w, dict(t, v=t["v"].float()))
+    f = _gpu.device_workload(w)
+    with pytest.raises(ValueError):
+        attend(w, dict(f, ks=t["ks"], vs=t["vs"]))
+    with pytest.raises(sa.SAError):      # one query per sequence only
+        w2 = inputs.small("chunked_prefill", seed=59)
+        t2, _ = scaled_workload(w2, "int8")
+        attend(w2, t2, path=sa.PATH_FUSED_DECODE)
+
+
+@pytest.mark.parametrize("name", ["gqa_decode", "chunked_prefill"])
+def test_graph_and_streams(name):
+    """A captured step replayed on new contents, and a call on a stream of the
+    caller's, give what an eager call gives, bit for bit."""
+    w = inputs.small(name, seed=61)
+    t, _ = scaled_workload(w, "e4m3", "bf16")
+    args = (t["q"], t["k"], t["v"], t["selected"], w.cu_seqlens_q, t["cu"], t["used"], t["bt"], w.hq,
+            w.hkv, w.head_dim, w.block_size, w.page_size, w.softmax_scale, w.causal)
+    g = sa.AttentionGraph(*args, k_scales=t["ks"], v_scales=t["vs"])
+    for seed in range(2):
+        t["q"].copy_(torch.randn(t["q"].shape, device="cuda"))
+        t["ks"].mul_(2.0)
+        ref, ref_lse, _, _ = attend(w, t)
+        out, lse = g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        out, lse, _, _ = attend(w, t)
+    side.synchronize()
+    assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+def test_serving_steps(kind, act):
+    """The operators in the order a server calls them: a prompt is stored,
+    its blocks' bounds taken, each query's blocks selected and attended to,
+    then single tokens, step by step.  Every step's output against the oracle
+    on the cache's values and the selection that was made."""
+    batch, hkv, g, d, ps, bs, topk = 3, 2, 4, 128, 16, 64, 5
+    hq = hkv * g
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    prompt = np.array([200, 513, 64])
+    steps = 4
+    cols = -(-int(prompt.max() + steps) // bs)
+    max_pages = cols * (bs // ps)
+    perm = np.random.default_rng(4).permutation(batch * max_pages).astype(np.int32)
+    bt = torch.from_numpy(perm.reshape(batch, max_pages)).cuda()
+    rows = torch.arange(batch * cols, dtype=torch.int32, device="cuda").view(batch, cols)
+    shape = (batch * max_pages, hkv, ps, d)
+    kp = torch.full(shape, 0x7F, dtype=torch.uint8, device="cuda").view(TORCH[kind])
+    vp = kp.clone()
+    ks, vs = torch.zeros(shape[:2], device="cuda"), torch.zeros(shape[:2], device="cuda")
+    bounds = torch.zeros((batch * cols, hkv, 2, d), dtype=torch.bfloat16, device="cuda")
+    status = torch.zeros(1, dtype=torch.int64, device="cuda")
+    lens = prompt.copy()
+    qo = prompt.copy()
+    for step in range(steps):
+        cu = np.concatenate([[0], np.cumsum(qo)]).astype(np.int64)
+        tq = int(cu[-1])
+        cud = torch.from_numpy(cu).cuda()
+        used = torch.from_numpy(lens.astype(np.int32)).cuda()
+        qkv = torch.randn((tq, hq + 2 * hkv, d), generator=gen, device="cuda")
+        qkv = qkv.to(torch.bfloat16 if act == "bf16" else torch.float32)
+        q = qkv[:, :hq].contiguous()
+        sa.sa_store_kv(qkv[:, hq:hq + hkv], qkv[:, hq + hkv:], kp, vp, bt, cu, cud, used,
+                       k_scales=ks, v_scales=vs, status=status)
+        sa.sa_block_bounds(kp, bt, cu, cud, used, bounds, rows, bs, k_scales=ks, status=status)
+        sel = sa.sa_select_blocks(q, bounds, rows, cu, cud, used, bs, topk, True, sink_blocks=1,
+                                  local_blocks=1, status=status)
+        out, lse, idx, _ = sa.sa_attention(q, kp, vp, sel, cu, cud, used, bt, hq, hkv, d, bs, ps,
+                                           1 / math.sqrt(d), True, k_scales=ks, v_scales=vs)
+        assert sa.sa_get_status(idx) == 0 and int(status) == 0
+        selected = sel.cpu().numpy()
+        for b in range(batch):
+            pos = np.arange(lens[b] - qo[b], lens[b])
+            own = pos // bs
+            s = selected[cu[b]:cu[b + 1]]
+            assert (s[:, :, 0] == 0).all()
+            assert (s.max(2) == own[:, None]).all()
+            assert (((s >= 0).sum(2)) == np.minimum(own + 1, topk)[:, None]).all()
+        kf = np.nan_to_num((kp.float() * ks[:, :, None, None]).cpu().numpy())
+        vf = np.nan_to_num((vp.float() * vs[:, :, None, None]).cpu().numpy())
+        ref, ref_lse, _, _ = oracle.attention(q.float().cpu().numpy(), kf, vf, selected,
+                                              bt.cpu().numpy(), cu, used.cpu().numpy(), hq, d, bs,
+                                              ps, 1 / math.sqrt(d), True)
+        tol = (_gpu.TOL_TC if step == 0 else _gpu.TOL_F32) + (HALF_BF16 if act == "bf16" else 0.0)
+        assert _gpu.row_error(out.float().cpu().numpy(), ref) <= tol
+        lens = lens + 1
+        qo = np.ones(batch, np.int64)
