@@ -124,7 +124,12 @@ bool fused_eligible(int64_t tq, int32_t batch, const int64_t* cu_host, int64_t n
                     int32_t hq, int32_t hkv, int32_t head_dim, int32_t block_size,
                     int32_t page_size, int kv_type) {
   if (cu_host == nullptr || batch < 1 || tq < 1 || hkv < 1 || hq % hkv != 0) return false;
-  if (!sa::fused_dec_supported(head_dim, block_size, page_size, hq / hkv, kv_type)) return false;
+  const bool ok =
+      kv_type >= SA_DTYPE_E4M3
+          ? sa::fused_dec_q8_supported(head_dim, block_size, page_size, hq / hkv)
+          : sa::fused_dec_supported(head_dim, block_size, page_size, hq / hkv,
+                                    kv_type == SA_DTYPE_BF16);
+  if (!ok) return false;
   if (num_pages < 1 || num_pages > sa::kFusedMaxRows / (static_cast<int64_t>(hkv) * page_size))
     return false;
   if (tq * hq * 4 > sa::kFusedMaxRows) return false;
@@ -683,13 +688,10 @@ sa_status forward_combine_impl(const void* q, const void* k_pages, const void* v
   if (idx->msb <= 0) return SA_ERR_SHAPE;   // a built index over these sizes addresses blocks
   sa::FusedDecArgs a{};
   a.q = static_cast<const float*>(q);
-  a.q_bf16 = x.q_dtype == SA_DTYPE_BF16 ? 1 : 0;
-  a.k_scales = x.k_scales;
-  a.v_scales = x.v_scales;
   a.k_pages = k_pages;
   a.v_pages = v_pages;
   a.num_pages = num_pages;
-  a.kv_type = kv_type;
+  a.kv_bf16 = kv_type == SA_DTYPE_BF16 ? 1 : 0;
   a.block_tables = block_tables;
   a.cu = cu_seqlens_q;
   a.used = used_kv_lens;
@@ -736,12 +738,24 @@ sa_status forward_combine_impl(const void* q, const void* k_pages, const void* v
   a.part_bf16 = partial_dtype == SA_DTYPE_BF16 ? 1 : 0;
   a.part_m = m_partial;
   a.part_l = l_partial;
-  a.out = out;
-  a.out_bf16 = a.q_bf16;
+  a.out = static_cast<float*>(out);
   a.lse = lse;
   a.pdl = behind_build ? 1 : 0;
   (void)causal;   // a no-op for one query per sequence (its position is lk - 1)
-  const cudaError_t err = sa::launch_fused_dec(a, static_cast<cudaStream_t>(stream));
+  cudaError_t err;
+  if (x.scaled) {
+    sa::FusedQ8Args q8{};
+    q8.base = a;
+    q8.int8 = kv_dtype == SA_DTYPE_INT8 ? 1 : 0;
+    q8.q = q;
+    q8.out = out;
+    q8.act_bf16 = x.q_dtype == SA_DTYPE_BF16 ? 1 : 0;
+    q8.k_scales = x.k_scales;
+    q8.v_scales = x.v_scales;
+    err = sa::launch_fused_dec_q8(q8, static_cast<cudaStream_t>(stream));
+  } else {
+    err = sa::launch_fused_dec(a, static_cast<cudaStream_t>(stream));
+  }
   if (err == cudaErrorNotSupported) return SA_ERR_UNSUPPORTED;
   return err == cudaSuccess ? SA_OK : SA_ERR_CUDA;
 }

@@ -39,32 +39,23 @@
 // conflicts and hold no Q in registers.  bf16 K/V: 4 consumer warps x 16 keys
 // on warp-level MMA (m16n8k16), Q and P split into bf16 high parts and
 // remainders; with at most 8 q-heads per kv head the remainders ride in the
-// tile's otherwise empty rows 8-15, so the split costs no extra MMA.  8-bit
-// K/V (e4m3, int8; a scale per page and kv head): see consumer_q8.
+// tile's otherwise empty rows 8-15, so the split costs no extra MMA.
 //
 // Shared-memory layout of a stage (a 1024-byte aligned region per tensor):
 //   f32:  [key][quarter of head_dim][32 floats], one 128-byte row per
 //         (key, quarter), 16-byte chunks XOR-swizzled by (4 key + quarter) & 7;
 //   bf16: [half of head_dim][key][64 bf16], one 128-byte row per (half, key),
-//         chunks swizzled by key & 7;
-//   8-bit: [key][128 codes], one 128-byte row per key, chunks swizzled by
-//         key & 7.
-// All make the consumers' shared loads (and ldmatrix) bank-conflict free.
+//         chunks swizzled by key & 7.
+// Both make the consumers' shared loads (and ldmatrix) bank-conflict free.
 #include <cstdint>
 #include <cuda.h>
 
 #include "internal.h"
 #include "sa_common.cuh"
-#include "seq_common.cuh"
 
 namespace sa {
 
 namespace {
-
-// K/V types (the kT of the templates): the values of sa_dtype.
-constexpr int kTF32 = 0, kTBf16 = 1, kTE4m3 = 2, kTInt8 = 3;
-__host__ __device__ constexpr bool is_q8(int t) { return t >= kTE4m3; }
-__host__ __device__ constexpr int elt_bytes(int t) { return t == kTF32 ? 4 : t == kTBf16 ? 2 : 1; }
 
 constexpr int kD = 128;
 constexpr int kCK = 64;              // keys per stage
@@ -92,49 +83,34 @@ struct StageHdr {
   int32_t item, k, pad0, pad1, pad2;
 };
 
+template <bool kBf16> struct Cfg;
 // NC consumer warps (keys of a stage split between them), NL load warps
 // (stages round-robin: one warp's copy issue alone does not keep HBM busy).
-template <int kT, int R> struct Cfg;
-template <int R> struct Cfg<kTF32, R> { static constexpr int NC = 8, NL = 2; };   // 8 keys per consumer
-template <int R> struct Cfg<kTBf16, R> { static constexpr int NC = 4, NL = 3; };  // 16 keys per consumer
-// 8-bit: 16 keys per consumer; with 8 query rows two groups of four consumers
-// take alternate stages (a stage arrives in half the time of a bf16 one), with
-// 16 rows (twice the registers) one group takes all
-template <int R> struct Cfg<kTE4m3, R> { static constexpr int NC = R == 8 ? 8 : 4, NL = 3; };
-template <int R> struct Cfg<kTInt8, R> { static constexpr int NC = R == 8 ? 8 : 4, NL = 3; };
-
-// Scales of a stage's four 16-key groups, and of a piece's pages (8-bit K/V).
-struct StageScales { float k[4], v[4]; };
-struct PieceScales { float k[kMaxEP][kMaxPPB], v[kMaxEP][kMaxPPB]; };
+template <> struct Cfg<false> { static constexpr int NC = 8, NL = 2; };   // 8 keys per consumer
+template <> struct Cfg<true> { static constexpr int NC = 4, NL = 3; };    // 16 keys per consumer
 
 struct Layout {
   uint32_t tensor;     // bytes of K (or V) of one stage
   uint32_t stage;      // K + V
-  uint32_t q, hdr, mo, mm, ml, desc, bars, flag, ssc, psc, total;
+  uint32_t q, hdr, mo, mm, ml, desc, bars, flag, total;
 };
 
 __host__ __device__ constexpr uint32_t up_to(uint32_t x, uint32_t a) { return (x + a - 1) / a * a; }
 
-template <int kT, int R, int S>
+template <bool kBf16, int R, int S>
 __host__ __device__ constexpr Layout fused_layout() {
-  constexpr int NC = Cfg<kT, R>::NC;
   Layout L{};
-  L.tensor = kCK * kD * elt_bytes(kT);
+  L.tensor = kCK * kD * (kBf16 ? 2 : 4);
   L.stage = 2 * L.tensor;
   L.q = S * L.stage;                                          // Q slots [S][R][128] f32
   L.hdr = L.q + S * R * kD * 4;                               // StageHdr[S]
   L.mo = up_to(L.hdr + S * static_cast<uint32_t>(sizeof(StageHdr)), 16);
-  L.mm = L.mo + NC * R * kD * 4;                              // merge rows [NC][R][128]
-  L.ml = L.mm + NC * R * 4;
-  L.desc = up_to(L.ml + NC * R * 4, 16);
+  L.mm = L.mo + Cfg<kBf16>::NC * R * kD * 4;                  // merge rows [NC][R][128]
+  L.ml = L.mm + Cfg<kBf16>::NC * R * 4;
+  L.desc = up_to(L.ml + Cfg<kBf16>::NC * R * 4, 16);
   L.bars = up_to(L.desc + kDescs * static_cast<uint32_t>(sizeof(PieceDesc)), 8);
   L.flag = L.bars + (2 * S + 2 * kDescs + 2) * 8;           // merge info: item, k
   L.total = L.flag + 16;
-  if (is_q8(kT)) {
-    L.ssc = up_to(L.total, 16);                               // StageScales[S]
-    L.psc = L.ssc + S * static_cast<uint32_t>(sizeof(StageScales));
-    L.total = L.psc + kDescs * static_cast<uint32_t>(sizeof(PieceScales));
-  }
   return L;
 }
 
@@ -154,8 +130,6 @@ struct Smem {
   uint64_t* mready;     // consumers -> merge warp: the piece's states are in mo/mm/ml
   uint64_t* mfree;      // merge warp -> consumers: the states have been read
   volatile int* minfo;  // item, k of the piece being merged (-1: no more pieces)
-  StageScales* ssc;     // 8-bit K/V only
-  PieceScales* psc;
 };
 
 // ------------------------------------------------------------------ metadata
@@ -177,7 +151,6 @@ __device__ __forceinline__ int warp_batch_of(const int64_t* cu, int batch, int64
   return lo;
 }
 
-template <bool kScales>
 __device__ void meta_warp(const FusedDecArgs& a, const Smem& sm, int64_t n_pieces, int lane) {
   uint32_t n = 0;
   for (int64_t g = blockIdx.x;; g += gridDim.x, ++n) {
@@ -246,11 +219,6 @@ __device__ void meta_warp(const FusedDecArgs& a, const Smem& sm, int64_t n_piece
             if (id < 0) id = -1;
           }
           d.pid[pos][p] = id;
-          if constexpr (kScales) {
-            const int64_t at = static_cast<int64_t>(max(id, 0)) * a.hkv + h;
-            sm.psc[slot].k[pos][p] = id >= 0 ? __ldg(a.k_scales + at) : 0.f;
-            sm.psc[slot].v[pos][p] = id >= 0 ? __ldg(a.v_scales + at) : 0.f;
-          }
         }
       }
       nkept += __popc(km);
@@ -271,17 +239,17 @@ __device__ void meta_warp(const FusedDecArgs& a, const Smem& sm, int64_t n_piece
 // ------------------------------------------------------------------ loads
 
 // Load warp lw of NL: fills the stages whose running index is lw modulo NL.
-template <int kT, int R, int S>
+template <bool kBf16, int R, int S>
 __device__ void load_warp(const TmaMaps& maps, const FusedDecArgs& a, const Smem& sm, int lw,
                           int lane) {
-  constexpr Layout L = fused_layout<kT, R, S>();
-  constexpr uint32_t NL = Cfg<kT, R>::NL;
+  constexpr Layout L = fused_layout<kBf16, R, S>();
+  constexpr uint32_t NL = Cfg<kBf16>::NL;
   const int ck = a.block_size < kCK ? a.block_size : kCK;           // keys per chunk
   const int cpb = a.block_size / ck;                                // chunks per block
   const int kb = a.page_size < ck ? a.page_size : ck;               // keys per page box
   const int nbox = ck / kb;
-  const uint32_t box_bytes = static_cast<uint32_t>(kb) * kD * elt_bytes(kT);
-  const uint32_t q_bytes = static_cast<uint32_t>(a.qhead) * kD * (is_q8(kT) && a.q_bf16 ? 2 : 4);
+  const uint32_t box_bytes = static_cast<uint32_t>(kb) * kD * (kBf16 ? 2 : 4);
+  const uint32_t q_bytes = static_cast<uint32_t>(a.qhead) * kD * 4;
   uint32_t n = 0, xs = 0;
   bool ok = true;
   if (a.stall) return;   // test hook: no stage is ever filled, so every wait on one runs out
@@ -345,22 +313,9 @@ __device__ void load_warp(const TmaMaps& maps, const FusedDecArgs& a, const Smem
         }
       }
       const unsigned pm = __ballot_sync(0xffffffffu, present);
-      const bool with_q = kT != kTF32 ? (first && nr > 0) : nr > 0;
+      const bool with_q = kBf16 ? (first && nr > 0) : nr > 0;
       const uint32_t tx =
           static_cast<uint32_t>(__popc(pm)) * 2u * box_bytes + (with_q ? q_bytes : 0u);
-      if constexpr (is_q8(kT)) {
-        // the scales of the chunk's 16-key groups (each within one page)
-        if (lane < 8) {
-          const int g16 = (lane & 3) * 16;
-          float sc = 0.f;
-          if (nr > 0 && g16 < ck) {
-            const int p = (c * ck + g16) / a.page_size;
-            sc = lane < 4 ? sm.psc[slot].k[j][p] : sm.psc[slot].v[j][p];
-          }
-          (lane < 4 ? sm.ssc[s].k : sm.ssc[s].v)[lane & 3] = sc;
-        }
-        __syncwarp();
-      }
       if (lane == 0) {
         StageHdr& hd = sm.hdr[s];
         hd.flags = (first ? kFirst : 0u) | (last ? kLast : 0u);
@@ -373,11 +328,7 @@ __device__ void load_warp(const TmaMaps& maps, const FusedDecArgs& a, const Smem
       __syncwarp();
       unsigned char* st = sm.base + s * L.stage;
       if (present) {
-        if constexpr (is_q8(kT)) {
-          const uint32_t off = static_cast<uint32_t>(lane * kb) * 128u;
-          tma_load_2d(st + off, &maps.k[0], 0, row0, sm.full + s);
-          tma_load_2d(st + L.tensor + off, &maps.v[0], 0, row0, sm.full + s);
-        } else if constexpr (kT == kTBf16) {
+        if constexpr (kBf16) {
           const uint32_t off = static_cast<uint32_t>(lane * kb) * 128u;
           tma_load_2d(st + off, &maps.k[0], 0, row0, sm.full + s);
           tma_load_2d(st + kCK * 128 + off, &maps.k[1], 0, row0, sm.full + s);
@@ -391,11 +342,7 @@ __device__ void load_warp(const TmaMaps& maps, const FusedDecArgs& a, const Smem
       }
       if (with_q && lane == 31) {
         const int64_t qrow = static_cast<int64_t>(d.i) * a.hq + static_cast<int64_t>(h) * a.qhead;
-        if constexpr (is_q8(kT))
-          bulk_g2s(sm.qs + s * R * kD,
-                   reinterpret_cast<const unsigned char*>(a.q) + qrow * kD * (a.q_bf16 ? 2 : 4),
-                   q_bytes, sm.full + s);
-        else if constexpr (kT == kTBf16)
+        if constexpr (kBf16)
           bulk_g2s(sm.qs + s * R * kD, a.q + qrow * kD, q_bytes, sm.full + s);
         else
           tma_load_2d(sm.qs + s * R * kD, &maps.q, 0, static_cast<int>(qrow * 4), sm.full + s);
@@ -420,8 +367,8 @@ __device__ void load_warp(const TmaMaps& maps, const FusedDecArgs& a, const Smem
 __device__ __forceinline__ void write_row(const FusedDecArgs& a, int64_t row, int d4, float m2,
                                           float l, float4 o) {
   const float inv = l > 0.f ? 1.f / l : 0.f;
-  store_o4(a.out, a.out_bf16, row * kD + 4 * d4,
-           make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+  reinterpret_cast<float4*>(a.out + row * kD)[d4] =
+      make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
   if (a.lse && d4 == 0) a.lse[row] = l > 0.f ? (m2 + log2f(l)) * kLn2 : -INFINITY;
 }
 
@@ -437,18 +384,13 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
-// Where the 8-bit consumers put 16-byte chunk `c` of row r of a merge row: a
-// consumer's lanes hold (row, 32 consecutive dims), which without the XOR all
-// fall on the same banks.
-__device__ __forceinline__ int merge_chunk(int c, int r) { return c ^ (c >> 3) ^ ((r & 1) << 2); }
-
 // The merge warp.  Per piece: merge the NC consumer warps' states (m in the
 // log2 domain) row by row, lane = 4 dims; release the state buffer; then
 // either write the output rows (one piece per pair) or the piece's scratch
 // rows, and if this piece is the pair's last to finish (a counter per pair),
 // merge the pair's scratch rows into the output.  It runs beside the
 // consumers, which only wait for it when they hand over their next piece.
-template <int NC, int R, bool kSwz>
+template <int NC, int R>
 __device__ void merge_warp(const FusedDecArgs& a, const Smem& sm, int lane) {
   const int qhead = a.qhead;
   for (uint32_t np = 0;; ++np) {
@@ -476,8 +418,7 @@ __device__ void merge_warp(const FusedDecArgs& a, const Smem& sm, int lane) {
         for (int w = 0; w < NC; ++w) {
           const float e = exp2f(sm.mm[w * R + r] - M);
           l = fmaf(e, sm.ml[w * R + r], l);
-          const float4 v = reinterpret_cast<const float4*>(
-              sm.mo + (w * R + r) * kD)[kSwz ? merge_chunk(lane, r) : lane];
+          const float4 v = reinterpret_cast<const float4*>(sm.mo + (w * R + r) * kD)[lane];
           o.x = fmaf(e, v.x, o.x);
           o.y = fmaf(e, v.y, o.y);
           o.z = fmaf(e, v.z, o.z);
@@ -580,7 +521,7 @@ __device__ __forceinline__ void handoff_signal(const Smem& sm, int w, int lane, 
 
 template <int R, int S>
 __device__ void consumer_f32(const FusedDecArgs& a, const Smem& sm, int w, int lane) {
-  constexpr Layout L = fused_layout<kTF32, R, S>();
+  constexpr Layout L = fused_layout<false, R, S>();
   const int ck = a.block_size < kCK ? a.block_size : kCK;
   const int kb = a.page_size < ck ? a.page_size : ck;
   const int lkb = __ffs(kb) - 1;                  // kb is a power of two
@@ -752,7 +693,7 @@ __device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_
 template <int R, int S>
 __device__ void consumer_bf16(const FusedDecArgs& a, const Smem& sm, int w, int lane) {
   static_assert(R == 16, "rows g and g + 8 of the m16 tile are both query rows");
-  constexpr Layout L = fused_layout<kTBf16, R, S>();
+  constexpr Layout L = fused_layout<true, R, S>();
   const int g = lane >> 2, c = lane & 3;          // fragment row (and + 8), column pair
   const int mi = lane >> 3, ri = lane & 7;        // ldmatrix matrix and row
   // K rows for S = Q K^T: matrices (keys 0-7 | 8-15) x (dims lo | hi 8 of 16).
@@ -930,7 +871,7 @@ __device__ void consumer_bf16(const FusedDecArgs& a, const Smem& sm, int w, int 
 template <int S>
 __device__ void consumer_bf16_packed(const FusedDecArgs& a, const Smem& sm, int w, int lane) {
   constexpr int R = 8;
-  constexpr Layout L = fused_layout<kTBf16, R, S>();
+  constexpr Layout L = fused_layout<true, R, S>();
   const int g = lane >> 2, c = lane & 3;          // fragment row, column pair
   const int mi = lane >> 3, ri = lane & 7;        // ldmatrix matrix and row
   const uint32_t krow = static_cast<uint32_t>(16 * w + (mi >> 1) * 8 + ri) * 128u;
@@ -1077,308 +1018,15 @@ __device__ void consumer_bf16_packed(const FusedDecArgs& a, const Smem& sm, int 
   }
 }
 
-// ------------------------------------------------------------------ 8-bit consumers
-
-__device__ __forceinline__ void mma16816_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                             uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
-      "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Two values as f16 high parts and f16 remainders (22 bits together).
-__device__ __forceinline__ void split2h(float x0, float x1, uint32_t& hi, uint32_t& lo) {
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(x1), "f"(x0));
-  const float2 h = f16x2_to_f32(hi);
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(x1 - h.y), "f"(x0 - h.x));
-}
-
-// 8-bit K/V: warp-level MMA (m16n8k16) on f16 operands.  Codes of both types
-// are exact in f16; Q (its row scaled by a power of two into f16's range) and P
-// are split into f16 high parts and remainders, so products lose no more than
-// 2^-22.  The scale of a 16-key group's page meets K on the scores and V on the
-// group's product (o += vs * (P Vcodes): a fresh accumulator per group, since
-// neighbouring groups may lie in pages of other scales).
-//
-// No transposition and no repacking of bytes through shared memory: a
-// fragment's k index may stand for any channel (scores) and its n index for
-// any channel (output) as long as both operands agree.
-//   scores: lane (g, c) reads the 16-byte chunks c and c + 4 of key g's row
-//     and serves them as the k-steps' B fragments, 4 codes each; Q's fragments
-//     hold the same channels.
-//   output: lane (g, c) reads chunk g (channels 16 g ..) of the four keys its
-//     fragment's k indices stand for, interleaves the keys' bytes and serves
-//     channel 16 g + j as n-tile j.
-// Both reads are free of bank conflicts under the 128-byte swizzle.
-//
-// R = 8 (at most 8 query rows): rows g + 8 of the m16 tile carry the
-// remainders of rows g.  R = 16: remainders in products of their own.
-template <int kT, int R, int S>
-__device__ void consumer_q8(const FusedDecArgs& a, const Smem& sm, int warp, int lane) {
-  constexpr Layout L = fused_layout<kT, R, S>();
-  constexpr bool kI8 = kT == kTInt8;
-  constexpr int kGroups = Cfg<kT, R>::NC / 4;     // warp groups, alternate stages
-  constexpr int NR = R / 8;                       // query rows per lane: g (and g + 8)
-  // P is kept 2^10 times larger than exp2(s - m) so that its f16 parts stay
-  // clear of f16's subnormals for the 2^-24 that still matter
-  constexpr float kShift = 10.f;
-  const int w = warp & 3;                         // the warp's 16 keys of a stage
-  const int g = lane >> 2, c = lane & 3;
-  const uint32_t k_row = static_cast<uint32_t>(16 * w + g) * 128u;
-  const uint32_t k_lo = static_cast<uint32_t>(((c + 4 * (g & 1)) ^ g) << 4);   // read first
-  const uint32_t k_hi = k_lo ^ 64u;                                            // chunk + 4
-  const bool swap = (g & 1) != 0;
-  const uint32_t v_row = static_cast<uint32_t>(16 * w + 2 * c) * 128u;
-  const uint32_t v_c0 = static_cast<uint32_t>((g ^ (2 * c)) << 4);
-  const uint32_t v_c1 = static_cast<uint32_t>((g ^ (2 * c + 1)) << 4);
-
-  float m_run[NR], l_part[NR], sfac[NR];
-  float o[16][2 * NR];               // [n-tile j][rows g, g + 8: columns 2c, 2c + 1]
-  uint32_t qa[8][4];                 // R = 8: high parts | remainders; R = 16: high parts
-  uint32_t ql[R == 16 ? 8 : 1][4];   // R = 16: remainders
-#pragma unroll
-  for (int j = 0; j < 16; ++j)
-#pragma unroll
-    for (int e = 0; e < 2 * NR; ++e) o[j][e] = 0.f;
-#pragma unroll
-  for (int r = 0; r < NR; ++r) {
-    m_run[r] = -INFINITY;
-    l_part[r] = 0.f;
-    sfac[r] = 0.f;
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      qa[j][e] = 0u;
-      if constexpr (R == 16) ql[j][e] = 0u;
-    }
-
-  uint32_t xc = 0, handed = 0;
-  for (;;) {
-    const int s = static_cast<int>(xc % S);
-    if (!mbar_wait_bounded(sm.full + s, (xc / S) & 1u, sm.spin)) {
-      if (lane == 0) report(a.status, SA_ERR_DEVICE_TIMEOUT);
-      return;
-    }
-    const StageHdr hd = sm.hdr[s];
-    if (hd.flags & kDone) {
-      if (handoff_wait(sm, handed)) handoff_signal(sm, warp, lane, -1, 0);
-      return;
-    }
-    if (hd.flags & kFirst) {
-      // Q rows g (and g + 8): lane's channels of k-step j are 4 consecutive
-      // ones of chunk c (j < 4) or c + 4
-#pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        const int row = g + 8 * r;
-        const float* q32 = sm.qs + s * R * kD + row * kD;
-        const uint16_t* q16 = reinterpret_cast<const uint16_t*>(sm.qs + s * R * kD) + row * kD;
-        float4 x[8];
-        float am = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int ch = 16 * (c + 4 * (j >> 2)) + 4 * (j & 3);
-          x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (row < a.qhead)
-            x[j] = a.q_bf16 ? bf16x4_to_f32(*reinterpret_cast<const uint2*>(q16 + ch))
-                            : *reinterpret_cast<const float4*>(q32 + ch);
-          am = fmaxf(am, fmaxf(fmaxf(fabsf(x[j].x), fabsf(x[j].y)),
-                               fmaxf(fabsf(x[j].z), fabsf(x[j].w))));
-        }
-        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
-        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
-        // largest magnitude to [2^10, 2^11); f = 2^(137 - E) with E the
-        // biased exponent, both factors kept normal
-        const int ex = min(max(static_cast<int>(__float_as_uint(am) >> 23), 11), 253);
-        const float f = __uint_as_float(static_cast<uint32_t>(min(264 - ex, 254)) << 23);
-        const float inv = __uint_as_float(static_cast<uint32_t>(max(ex - 10, 1)) << 23);
-        sfac[r] = a.scale * kLog2e * inv;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          uint32_t h0, l0, h1, l1;
-          split2h(x[j].x * f, x[j].y * f, h0, l0);
-          split2h(x[j].z * f, x[j].w * f, h1, l1);
-          if constexpr (R == 8) {
-            qa[j][0] = h0;
-            qa[j][1] = l0;
-            qa[j][2] = h1;
-            qa[j][3] = l1;
-          } else {
-            qa[j][r] = h0;
-            qa[j][2 + r] = h1;
-            ql[j][r] = l0;
-            ql[j][2 + r] = l1;
-          }
-        }
-        m_run[r] = -INFINITY;
-        l_part[r] = 0.f;
-      }
-#pragma unroll
-      for (int j = 0; j < 16; ++j)
-#pragma unroll
-        for (int e = 0; e < 2 * NR; ++e) o[j][e] = 0.f;
-    }
-    const bool mine = kGroups == 1 || static_cast<int>(xc & 1u) == warp >> 2;
-    const uint32_t mk =
-        mine ? (w < 2 ? hd.mask_lo >> (16 * w) : hd.mask_hi >> (16 * (w - 2))) & 0xFFFFu : 0u;
-    if (mk) {
-      const unsigned char* kt = sm.base + s * L.stage;
-      const unsigned char* vt = kt + L.tensor;
-      const float ks = sm.ssc[s].k[w], vs = sm.ssc[s].v[w];
-      // ---- S = Q K^T for the warp's 16 keys (two n-tiles of 8) ----
-      float sc[NR][2][2];
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        const uint4 u0 = *reinterpret_cast<const uint4*>(kt + k_row + nt * 1024u + k_lo);
-        const uint4 u1 = *reinterpret_cast<const uint4*>(kt + k_row + nt * 1024u + k_hi);
-        const uint32_t x0[4] = {u0.x, u0.y, u0.z, u0.w}, x1[4] = {u1.x, u1.y, u1.z, u1.w};
-        float part[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint32_t codes = ((j < 4) != swap) ? x0[j & 3] : x1[j & 3];
-          uint32_t b0, b1;
-          codes4_to_f16<kI8>(codes, b0, b1);
-          mma16816_f16(part[j & 1], qa[j], b0, b1);
-          if constexpr (R == 16) mma16816_f16(part[j & 1], ql[j], b0, b1);
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          if constexpr (R == 8) {
-            sc[0][nt][e] = (part[0][e] + part[1][e]) + (part[0][e + 2] + part[1][e + 2]);
-          } else {
-            sc[0][nt][e] = part[0][e] + part[1][e];
-            sc[NR - 1][nt][e] = part[0][e + 2] + part[1][e + 2];
-          }
-        }
-      }
-      // ---- online softmax ----
-      uint32_t pa[4], pl[R == 16 ? 4 : 1];
-      float alpha[NR];
-      bool moved = false;
-#pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        const float f = sfac[r] * ks;
-        float cm = -INFINITY;
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int kk = 8 * nt + 2 * c + e;
-            sc[r][nt][e] = ((mk >> kk) & 1u) ? sc[r][nt][e] * f : -INFINITY;
-            cm = fmaxf(cm, sc[r][nt][e]);
-          }
-        cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, 1));
-        cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, 2));
-        const float m_new = fmaxf(m_run[r], cm);         // finite: the warp has a key
-        alpha[r] = exp2f(m_run[r] - m_new);
-        moved = moved || alpha[r] != 1.f;
-        const float sub = m_new - kShift;
-        float pv[2][2];
-        float lsum = 0.f;
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            pv[nt][e] = exp2f(sc[r][nt][e] - sub);
-            lsum += pv[nt][e];
-          }
-        l_part[r] = fmaf(l_part[r], alpha[r], lsum);
-        m_run[r] = m_new;
-        if constexpr (R == 8) {
-          split2h(pv[0][0], pv[0][1], pa[0], pa[1]);
-          split2h(pv[1][0], pv[1][1], pa[2], pa[3]);
-        } else {
-          split2h(pv[0][0], pv[0][1], pa[r], pl[r]);
-          split2h(pv[1][0], pv[1][1], pa[2 + r], pl[2 + r]);
-        }
-      }
-      if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-#pragma unroll
-          for (int e = 0; e < 2 * NR; ++e) o[j][e] *= alpha[e / 2];
-      }
-      // ---- o += vs * (P V) (n-tile j: channels 16 n + j) ----
-      // rows behind the sequence's end hold anything (NaN codes too): zeros
-      const bool whole = mk == 0xFFFFu;
-      const uint32_t z0 = whole || ((mk >> (2 * c)) & 1u) ? 0xFFFFFFFFu : 0u;
-      const uint32_t z1 = whole || ((mk >> (2 * c + 1)) & 1u) ? 0xFFFFFFFFu : 0u;
-      const uint32_t z2 = whole || ((mk >> (2 * c + 8)) & 1u) ? 0xFFFFFFFFu : 0u;
-      const uint32_t z3 = whole || ((mk >> (2 * c + 9)) & 1u) ? 0xFFFFFFFFu : 0u;
-      const uint4 v0 = *reinterpret_cast<const uint4*>(vt + v_row + v_c0);
-      const uint4 v1 = *reinterpret_cast<const uint4*>(vt + v_row + 128u + v_c1);
-      const uint4 v2 = *reinterpret_cast<const uint4*>(vt + v_row + 1024u + v_c0);
-      const uint4 v3 = *reinterpret_cast<const uint4*>(vt + v_row + 1152u + v_c1);
-      const uint32_t y0[4] = {v0.x, v0.y, v0.z, v0.w}, y1[4] = {v1.x, v1.y, v1.z, v1.w};
-      const uint32_t y2[4] = {v2.x, v2.y, v2.z, v2.w}, y3[4] = {v3.x, v3.y, v3.z, v3.w};
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t t0 = y0[q] & z0, t1 = y1[q] & z1, t2 = y2[q] & z2, t3 = y3[q] & z3;
-        uint32_t b[4][2];
-        codes4_to_f16<kI8>(__byte_perm(t0, t1, 0x5140), b[0][0], b[1][0]);
-        codes4_to_f16<kI8>(__byte_perm(t0, t1, 0x7362), b[2][0], b[3][0]);
-        codes4_to_f16<kI8>(__byte_perm(t2, t3, 0x5140), b[0][1], b[1][1]);
-        codes4_to_f16<kI8>(__byte_perm(t2, t3, 0x7362), b[2][1], b[3][1]);
-#pragma unroll
-        for (int jj = 0; jj < 4; ++jj) {
-          const int j = 4 * q + jj;
-          float t[4] = {0.f, 0.f, 0.f, 0.f};
-          mma16816_f16(t, pa, b[jj][0], b[jj][1]);
-          if constexpr (R == 16) {
-            mma16816_f16(t, pl, b[jj][0], b[jj][1]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[j][e] = fmaf(vs, t[e], o[j][e]);
-          } else {
-            o[j][0] = fmaf(vs, t[0] + t[2], o[j][0]);
-            o[j][1] = fmaf(vs, t[1] + t[3], o[j][1]);
-          }
-        }
-      }
-    }
-    mbar_arrive(sm.empty + s);
-    if (hd.flags & kLast) {
-      if (!handoff_wait(sm, handed)) {
-        if (lane == 0) report(a.status, SA_ERR_DEVICE_TIMEOUT);
-        return;
-      }
-#pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        float l = l_part[r];
-        l += __shfl_xor_sync(0xffffffffu, l, 1);
-        l += __shfl_xor_sync(0xffffffffu, l, 2);
-        const int row = g + 8 * r;
-        float4* dst = reinterpret_cast<float4*>(sm.mo + (warp * R + row) * kD);
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            dst[merge_chunk(4 * (2 * c + e) + q, row)] =
-                make_float4(o[4 * q][2 * r + e], o[4 * q + 1][2 * r + e], o[4 * q + 2][2 * r + e],
-                            o[4 * q + 3][2 * r + e]);
-        if (c == 0) {
-          sm.mm[warp * R + row] = m_run[r] - kShift;
-          sm.ml[warp * R + row] = l;
-        }
-      }
-      handoff_signal(sm, warp, lane, hd.item, hd.k);
-      ++handed;
-    }
-    ++xc;
-  }
-}
-
 // ------------------------------------------------------------------ kernel
 
-template <int kT, int R, int S>
-__global__ void __launch_bounds__((2 + Cfg<kT, R>::NL + Cfg<kT, R>::NC) * 32, 1)
+template <bool kBf16, int R, int S>
+__global__ void __launch_bounds__((2 + Cfg<kBf16>::NL + Cfg<kBf16>::NC) * 32, 1)
 fused_dec_kernel(const __grid_constant__ TmaMaps maps, const FusedDecArgs a) {
   extern __shared__ unsigned char smem_raw[];
-  constexpr Layout L = fused_layout<kT, R, S>();
-  constexpr int NC = Cfg<kT, R>::NC;
-  constexpr int NL = Cfg<kT, R>::NL;
+  constexpr Layout L = fused_layout<kBf16, R, S>();
+  constexpr int NC = Cfg<kBf16>::NC;
+  constexpr int NL = Cfg<kBf16>::NL;
   unsigned char* base = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   Smem sm;
@@ -1397,8 +1045,6 @@ fused_dec_kernel(const __grid_constant__ TmaMaps maps, const FusedDecArgs a) {
   sm.mready = sm.dempty + kDescs;
   sm.mfree = sm.mready + 1;
   sm.minfo = reinterpret_cast<volatile int*>(base + L.flag);
-  sm.ssc = reinterpret_cast<StageScales*>(base + L.ssc);
-  sm.psc = reinterpret_cast<PieceScales*>(base + L.psc);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -1408,7 +1054,7 @@ fused_dec_kernel(const __grid_constant__ TmaMaps maps, const FusedDecArgs a) {
     }
     for (int d = 0; d < kDescs; ++d) {
       mbar_init(sm.dfull + d, 32);
-      mbar_init(sm.dempty + d, 32 * NL);
+      mbar_init(sm.dempty + d, 32 * Cfg<kBf16>::NL);
     }
     mbar_init(sm.mready, NC * 32);
     mbar_init(sm.mfree, 32);
@@ -1423,14 +1069,12 @@ fused_dec_kernel(const __grid_constant__ TmaMaps maps, const FusedDecArgs a) {
 
   const int64_t n_pieces = a.whole_items + (a.tq * a.hkv - a.whole_items) * a.pieces;
   if (warp == 0) {
-    meta_warp<is_q8(kT)>(a, sm, n_pieces, lane);
+    meta_warp(a, sm, n_pieces, lane);
   } else if (warp <= NL) {
-    load_warp<kT, R, S>(maps, a, sm, warp - 1, lane);
+    load_warp<kBf16, R, S>(maps, a, sm, warp - 1, lane);
   } else if (warp == NL + 1) {
-    merge_warp<NC, R, is_q8(kT)>(a, sm, lane);
-  } else if constexpr (is_q8(kT)) {
-    consumer_q8<kT, R, S>(a, sm, warp - NL - 2, lane);
-  } else if constexpr (kT == kTBf16) {
+    merge_warp<NC, R>(a, sm, lane);
+  } else if constexpr (kBf16) {
     if constexpr (R == 8)
       consumer_bf16_packed<S>(a, sm, warp - NL - 2, lane);
     else
@@ -1467,21 +1111,10 @@ EncodeTiledFn encode_fn() {
 //   f32:  3-D (32 floats, 4 quarters, rows), box (32, 4, kb);
 //   bf16: 2-D (64 bf16 of one half, rows) with row stride 256 bytes, one map
 //         per half (base + 128 bytes for the high half), box (64, kb).
-//   8-bit: 2-D (128 codes, rows), box (128, kb).
-bool encode_pool(const void* pool, int64_t rows, int kb, int type, CUtensorMap* maps) {
+bool encode_pool(const void* pool, int64_t rows, int kb, bool bf16, CUtensorMap* maps) {
   EncodeTiledFn enc = encode_fn();
   if (enc == nullptr) return false;
-  if (is_q8(type)) {
-    const cuuint64_t dims[2] = {kD, static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {kD};
-    const cuuint32_t box[2] = {kD, static_cast<cuuint32_t>(kb)};
-    const cuuint32_t estr[2] = {1, 1};
-    return enc(maps, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(pool), dims, strides, box,
-               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-  }
-  if (type == kTBf16) {
+  if (bf16) {
     for (int half = 0; half < 2; ++half) {
       const cuuint64_t dims[2] = {64, static_cast<cuuint64_t>(rows)};
       const cuuint64_t strides[1] = {256};
@@ -1504,21 +1137,21 @@ bool encode_pool(const void* pool, int64_t rows, int kb, int type, CUtensorMap* 
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kT, int R, int S>
+template <bool kBf16, int R, int S>
 cudaError_t launch_fused(const FusedDecArgs& a, cudaStream_t stream) {
-  constexpr Layout L = fused_layout<kT, R, S>();
-  constexpr int NC = Cfg<kT, R>::NC;
-  constexpr int NL = Cfg<kT, R>::NL;
+  constexpr Layout L = fused_layout<kBf16, R, S>();
+  constexpr int NC = Cfg<kBf16>::NC;
+  constexpr int NL = Cfg<kBf16>::NL;
   const size_t smem = L.total + 1024;
   if (smem > 227 * 1024) return cudaErrorNotSupported;
   const int ck = a.block_size < kCK ? a.block_size : kCK;
   const int kb = a.page_size < ck ? a.page_size : ck;
   const int64_t rows = a.num_pages * a.hkv * a.page_size;
   TmaMaps maps;
-  if (!encode_pool(a.k_pages, rows, kb, kT, maps.k) ||
-      !encode_pool(a.v_pages, rows, kb, kT, maps.v))
+  if (!encode_pool(a.k_pages, rows, kb, kBf16, maps.k) ||
+      !encode_pool(a.v_pages, rows, kb, kBf16, maps.v))
     return cudaErrorNotSupported;
-  if constexpr (kT == kTF32) {
+  if constexpr (!kBf16) {
     // q [tq, hq, 128] as rows of 32 floats; box = the qhead rows of one kv head.
     const int64_t qrows = a.tq * a.hq * 4;
     const cuuint64_t dims[2] = {32, static_cast<cuuint64_t>(qrows)};
@@ -1534,7 +1167,7 @@ cudaError_t launch_fused(const FusedDecArgs& a, cudaStream_t stream) {
   } else {
     maps.q = maps.k[0];   // unused
   }
-  const void* fn = reinterpret_cast<const void*>(fused_dec_kernel<kT, R, S>);
+  const void* fn = reinterpret_cast<const void*>(fused_dec_kernel<kBf16, R, S>);
   cudaError_t err =
       cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (err != cudaSuccess) return err;
@@ -1556,12 +1189,12 @@ cudaError_t launch_fused(const FusedDecArgs& a, cudaStream_t stream) {
   int site = kStallNone;
   debug_stall_setting(&site, &args.spin_limit);
   args.stall = site == kStallFusedCopies;
-  return cudaLaunchKernelEx(&cfg, fused_dec_kernel<kT, R, S>, maps, args);
+  return cudaLaunchKernelEx(&cfg, fused_dec_kernel<kBf16, R, S>, maps, args);
 }
 
 }  // namespace
 
-bool fused_dec_supported(int head_dim, int block_size, int page_size, int qhead, int kv_type) {
+bool fused_dec_supported(int head_dim, int block_size, int page_size, int qhead, int kv_bf16) {
   if (head_dim != kD) return false;
   // page boxes: a power of two of at least 8 rows (the swizzle period)
   if (page_size < 8 || (page_size & (page_size - 1)) != 0) return false;
@@ -1569,14 +1202,12 @@ bool fused_dec_supported(int head_dim, int block_size, int page_size, int qhead,
   if (block_size / page_size > kMaxPPB) return false;
   const int ck = block_size < kCK ? block_size : kCK;
   if (block_size % ck != 0) return false;
-  // a 16-key step of the 8-bit consumers lies in one page (one scale)
-  if (is_q8(kv_type)) return page_size >= 16 && qhead >= 1 && qhead <= 16;
-  if (kv_type == kTBf16) return qhead >= 1 && qhead <= 16;
+  if (kv_bf16) return qhead >= 1 && qhead <= 16;
   return qhead >= 1 && qhead <= 4;
 }
 
 cudaError_t launch_fused_dec(const FusedDecArgs& a, cudaStream_t stream) {
-  if (!fused_dec_supported(kD, a.block_size, a.page_size, a.qhead, a.kv_type))
+  if (!fused_dec_supported(kD, a.block_size, a.page_size, a.qhead, a.kv_bf16))
     return cudaErrorNotSupported;
   if (a.ranks_per_piece < 1 || a.ranks_per_piece > kMaxEP || a.pieces < 1 ||
       static_cast<int64_t>(a.pieces) * a.ranks_per_piece < a.topk || a.whole_items < 0 ||
@@ -1584,18 +1215,9 @@ cudaError_t launch_fused_dec(const FusedDecArgs& a, cudaStream_t stream) {
     return cudaErrorInvalidValue;
   if (a.num_pages < 1 || a.num_pages * a.hkv * a.page_size > kFusedMaxRows)
     return cudaErrorNotSupported;
-  switch (a.kv_type) {
-    case kTF32: return launch_fused<kTF32, 4, 3>(a, stream);
-    case kTBf16:
-      return a.qhead <= 8 ? launch_fused<kTBf16, 8, 5>(a, stream)
-                          : launch_fused<kTBf16, 16, 4>(a, stream);
-    case kTE4m3:
-      return a.qhead <= 8 ? launch_fused<kTE4m3, 8, 8>(a, stream)
-                          : launch_fused<kTE4m3, 16, 6>(a, stream);
-    default:
-      return a.qhead <= 8 ? launch_fused<kTInt8, 8, 8>(a, stream)
-                          : launch_fused<kTInt8, 16, 6>(a, stream);
-  }
+  if (!a.kv_bf16) return launch_fused<false, 4, 3>(a, stream);
+  if (a.qhead <= 8) return launch_fused<true, 8, 5>(a, stream);
+  return launch_fused<true, 16, 4>(a, stream);
 }
 
 }  // namespace sa

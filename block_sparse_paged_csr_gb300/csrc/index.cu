@@ -952,6 +952,11 @@ cudaError_t launch_build_index(const IndexArgs& a, int64_t chunks_per_head,
     err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, index_kernel<true>, kThreads, smem);
     if (err != cudaSuccess) return err;
     if (seg_ctas > static_cast<int64_t>(per_sm) * sms) args.small = 0;
+    // beside a fused decode kernel: an SM keeps one split of L1 and shared
+    // memory for all its CTAs, so this kernel asks for the fused kernel's
+    err = cudaFuncSetAttribute(index_kernel<true>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared);
+    if (err != cudaSuccess) return err;
   }
   const void* fn = reinterpret_cast<const void*>(index_kernel<true>);
   int64_t grid = 0;

@@ -153,14 +153,11 @@ bool forward_dec_supported(int head_dim, int block_size, int page_size, int qhea
 // Fused decode attention (forward and combine in one kernel) for batches in
 // which every sequence holds at most one query.
 struct FusedDecArgs {
-  const float* q;           // bf16 values when q_bf16 (8-bit K/V only)
-  int q_bf16;
+  const float* q;
   const void* k_pages;
   const void* v_pages;
   int64_t num_pages;
-  int kv_type;              // an sa_dtype
-  const float* k_scales;    // [num_pages, hkv], 8-bit K/V only
-  const float* v_scales;
+  int kv_bf16;
   const int32_t* block_tables;
   const int64_t* cu;
   const int32_t* used;      // nullable
@@ -179,8 +176,7 @@ struct FusedDecArgs {
   int part_bf16;            // o rows f32, or bf16 when part_bf16
   float* part_m;
   float* part_l;
-  void* out;                // f32, or bf16 when out_bf16
-  int out_bf16;
+  float* out;
   float* lse;               // nullable
   int pdl;                  // launched right behind the index kernel that built the
                             // index: it may start while that kernel runs (it reads
@@ -191,10 +187,24 @@ struct FusedDecArgs {
 
 // Whether the fused decode kernel supports this shape (the caller also checks
 // that every sequence holds at most one query and the pool size limits).
-bool fused_dec_supported(int head_dim, int block_size, int page_size, int qhead, int kv_type);
+bool fused_dec_supported(int head_dim, int block_size, int page_size, int qhead, int kv_bf16);
 // Largest pool (num_pages * hkv * page_size key rows) the kernel addresses.
 constexpr int64_t kFusedMaxRows = (int64_t{1} << 31) - 1;
 cudaError_t launch_fused_dec(const FusedDecArgs& a, cudaStream_t stream);
+
+// The fused decode kernel over an 8-bit cache (fused_dec_q8.cu): the fields of
+// `base` as above except q, kv_bf16 and out, whose types vary.
+struct FusedQ8Args {
+  FusedDecArgs base;
+  int int8;                 // codes: int8, else e4m3
+  const void* q;            // f32, or bf16 when act_bf16
+  void* out;                // of q's type
+  int act_bf16;
+  const float* k_scales;    // [num_pages, hkv]
+  const float* v_scales;
+};
+bool fused_dec_q8_supported(int head_dim, int block_size, int page_size, int qhead);
+cudaError_t launch_fused_dec_q8(const FusedQ8Args& a, cudaStream_t stream);
 
 struct CombineArgs {
   const int32_t* inv;

@@ -59,14 +59,6 @@ __device__ __forceinline__ NewRange new_range(const int64_t* cu, const int32_t* 
   return r;
 }
 
-// Two 8-bit codes to packed f16 (exact for both types).  e4m3: the hardware
-// conversion.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(r) : "r"(two));
-  return r;
-}
-
 // int8: a byte b with its sign bit flipped, below the f16 exponent byte 0x64,
 // is the f16 number 1024 + (b + 128); subtracting 1152 leaves b.
 // `lo_sel` picks the two bytes: 0x4140 bytes 0 and 1, 0x4342 bytes 2 and 3.
@@ -77,7 +69,8 @@ __device__ __forceinline__ uint32_t int8x2_to_f16x2(uint32_t four_flipped, uint3
   return d;
 }
 
-// Four codes (one 32-bit word) to two packed f16 pairs.
+// Four codes (one 32-bit word) to two packed f16 pairs (exact for both types;
+// e4m3 by the hardware conversion).
 template <bool kInt8>
 __device__ __forceinline__ void codes4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
   if constexpr (kInt8) {
@@ -85,8 +78,11 @@ __device__ __forceinline__ void codes4_to_f16(uint32_t w, uint32_t& lo, uint32_t
     lo = int8x2_to_f16x2(f, 0x4140u);
     hi = int8x2_to_f16x2(f, 0x4342u);
   } else {
-    lo = e4m3x2_to_f16x2(w & 0xFFFFu);
-    hi = e4m3x2_to_f16x2(w >> 16);
+    // (the 16-bit halves are operands of the conversion as they are)
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
   }
 }
 
