@@ -27,7 +27,6 @@ Around them, for serving:
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from dataclasses import dataclass
 
@@ -79,24 +78,47 @@ def _check(code: int, where: str) -> None:
 
 
 def _ptr(t):
-    if t is None:
-        return None
-    return ctypes.c_void_p(t.data_ptr())
+    """An address argument (ctypes takes the integer as it is)."""
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream, device):
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    return ctypes.c_void_p(stream.cuda_stream)
+        return _raw_stream(device)
+    return stream.cuda_stream
+
+
+def _raw_stream(device):
+    """The current stream's handle, without a Stream object where torch offers it."""
+    index = device.index
+    if _current_raw_stream is None or index is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return _current_raw_stream(index)
+
+
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _host_ptr(a: np.ndarray) -> int:
+    return a.__array_interface__["data"][0]
 
 
 def _host_i64(a) -> np.ndarray:
+    if type(a) is np.ndarray and a.dtype == np.int64 and a.flags.c_contiguous:
+        return a
     if isinstance(a, torch.Tensor):
         a = a.detach().cpu().numpy()
     return np.ascontiguousarray(a, dtype=np.int64)
 
 
 def _require(t, dtype, name, device=None):
+    # the usual case in three calls; what is wrong is found out below
+    try:
+        if (t.dtype is dtype and t.is_contiguous() and
+                (t.is_cuda if device is None else t.device == device)):
+            return t
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -218,7 +240,7 @@ def sa_build_index(selected, cu_seqlens_q_host, cu_seqlens_q, used_kv_lens, max_
         index = allocate_index(tq, hkv, topk, max(batch, 1), max_pages, block_size, page_size,
                                dev)
     _check(_native.load().sa_build_index(
-        _ptr(selected), tq, hkv, topk, cu_h.ctypes.data_as(ctypes.c_void_p), _ptr(cu_seqlens_q),
+        _ptr(selected), tq, hkv, topk, _host_ptr(cu_h), _ptr(cu_seqlens_q),
         batch, _ptr(used_kv_lens), max_pages, block_size, page_size, split_edges,
         ctypes.byref(index.c), _stream(stream, dev)), "sa_build_index")
     return index
@@ -240,7 +262,7 @@ def sa_build_index_no_alloc(selected, cu_seqlens_q_host, cu_seqlens_q, used_kv_l
     if used_kv_lens is not None:
         _require(used_kv_lens, torch.int32, "used_kv_lens", dev)
     _check(_native.load().sa_build_index_no_alloc(
-        _ptr(selected), tq, hkv, topk, cu_h.ctypes.data_as(ctypes.c_void_p), _ptr(cu_seqlens_q),
+        _ptr(selected), tq, hkv, topk, _host_ptr(cu_h), _ptr(cu_seqlens_q),
         cu_h.size - 1, _ptr(used_kv_lens), max_pages, block_size, page_size, split_edges,
         ctypes.byref(index.c), _stream(stream, dev)), "sa_build_index_no_alloc")
     return index
@@ -383,9 +405,8 @@ def sa_forward(q, k_pages, v_pages, index: Index, block_tables, cu_seqlens_q, us
     if x is not None:
         if q_scratch is not None:
             raise ValueError("q_scratch does not apply to an 8-bit cache")
-        with _on(dev):
-            _check(L.sa_forward_scaled(*x.head(q, k_pages, v_pages, num_pages), *mid, ocode, *tail),
-                   "sa_forward_scaled")
+        _check(_on(dev, L.sa_forward_scaled, *x.head(q, k_pages, v_pages, num_pages), *mid, ocode,
+                   *tail), "sa_forward_scaled")
         return o_partial, m_partial, l_partial
     head = (_ptr(q), _ptr(k_pages), _ptr(v_pages), num_pages, kvd, *mid)
     if q_scratch is not None:
@@ -453,14 +474,13 @@ def sa_forward_combine(q, k_pages, v_pages, index: Index, selected, cu_seqlens_q
     num_pages = k_pages.numel() // page_elems if page_elems > 0 else 0
     o, m, l = partials
     L = _native.load()
-    mid = (ctypes.byref(c), _ptr(selected), cu_h.ctypes.data_as(ctypes.c_void_p),
+    mid = (ctypes.byref(c), _ptr(selected), _host_ptr(cu_h),
            _ptr(cu_seqlens_q), _ptr(used_kv_lens), _ptr(block_tables), hq, head_dim, block_size,
            page_size, softmax_scale, _causal(causal), split_edges)
     tail = (_ptr(o), _ptr(m), _ptr(l), _ptr(out), _ptr(lse), path, _stream(stream, dev))
     if x is not None:
-        with _on(dev):
-            _check(L.sa_forward_combine_scaled(*x.head(q, k_pages, v_pages, num_pages), *mid, ocode,
-                                               *tail), "sa_forward_combine_scaled")
+        _check(_on(dev, L.sa_forward_combine_scaled, *x.head(q, k_pages, v_pages, num_pages), *mid,
+                   ocode, *tail), "sa_forward_combine_scaled")
         return out, lse, partials
     head = (_ptr(q), _ptr(k_pages), _ptr(v_pages), num_pages, kvd, *mid)
     if ocode:
@@ -509,14 +529,13 @@ def sa_attention(q, k_pages, v_pages, selected, cu_seqlens_q_host, cu_seqlens_q,
     num_pages = k_pages.numel() // page_elems if page_elems > 0 else 0
     o, m, l = partials
     L = _native.load()
-    mid = (_ptr(selected), tq, topk, cu_h.ctypes.data_as(ctypes.c_void_p), _ptr(cu_seqlens_q),
+    mid = (_ptr(selected), tq, topk, _host_ptr(cu_h), _ptr(cu_seqlens_q),
            batch, _ptr(used_kv_lens), _ptr(block_tables), max_pages, hq, hkv, head_dim, block_size,
            page_size, softmax_scale, _causal(causal), split_edges, ctypes.byref(index.c))
     tail = (_ptr(o), _ptr(m), _ptr(l), _ptr(out), _ptr(lse), path, _stream(stream, dev))
     if x is not None:
-        with _on(dev):
-            _check(L.sa_attention_scaled(*x.head(q, k_pages, v_pages, num_pages), *mid, ocode,
-                                         *tail), "sa_attention_scaled")
+        _check(_on(dev, L.sa_attention_scaled, *x.head(q, k_pages, v_pages, num_pages), *mid, ocode,
+                   *tail), "sa_attention_scaled")
         return out, lse, index, partials
     head = (_ptr(q), _ptr(k_pages), _ptr(v_pages), num_pages, kvd, *mid)
     if ocode:
@@ -563,11 +582,12 @@ class AttentionGraph:
         return self.out, self.lse
 
 
-def _on(dev):
-    """The device of the call's tensors as the current one, where it is not."""
+def _on(dev, fn, *args) -> int:
+    """fn(*args) with the device of the call's tensors as the current one."""
     if dev.index is None or dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(dev)
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
 
 
 _CACHE_DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16,
@@ -594,7 +614,7 @@ def _scales(scales, pages, name):
     if scales is None:
         raise ValueError(f"{name} [num_pages, hkv] are needed with a {pages.dtype} cache")
     _require(scales, torch.float32, name, pages.device)
-    if tuple(scales.shape) != tuple(pages.shape[:2]):
+    if scales.shape != pages.shape[:2]:
         raise ValueError(f"{name} must be {tuple(pages.shape[:2])}, got {tuple(scales.shape)}")
     return scales
 
@@ -610,7 +630,7 @@ def _batch_args(cu_seqlens_q_host, cu_seqlens_q, used_kv_lens, tables, dev, name
                          "cu_seqlens_q_host")
     for t, n in zip(tables, name):
         _require(t, torch.int32, n, dev)
-        if t.dim() != 2 or t.shape[0] != batch:
+        if len(t.shape) != 2 or t.shape[0] != batch:
             raise ValueError(f"{n} must have a row for each of the {batch} sequences")
     return cu_h, batch
 
@@ -636,7 +656,7 @@ def sa_store_kv(k, v, k_pages, v_pages, block_tables, cu_seqlens_q_host, cu_seql
     _require(v_pages, k_pages.dtype, "v_pages", dev)
     if v_pages.shape != k_pages.shape:
         raise ValueError("k_pages and v_pages must have one shape")
-    num_pages, hkv, page_size, d = (int(x) for x in k_pages.shape)
+    num_pages, hkv, page_size, d = k_pages.shape
     for t, name in ((k, "k"), (v, "v")):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
@@ -644,25 +664,25 @@ def sa_store_kv(k, v, k_pages, v_pages, block_tables, cu_seqlens_q_host, cu_seql
             raise TypeError(f"{name} must be float32 or bfloat16 (both alike), got {t.dtype}")
         if t.device != dev:
             raise ValueError(f"{name} is on {t.device}, expected {dev}")
-        if t.dim() != 3 or tuple(t.shape) != (k.shape[0], hkv, d):
+        if t.shape != (k.shape[0], hkv, d):
             raise ValueError(f"{name} must be [tq, {hkv}, {d}], got {tuple(t.shape)}")
-        if t.numel() and t.stride(2) != 1:
+        if t.stride(2) != 1 and t.numel():
             raise ValueError(f"{name}: channels must be contiguous")
     ks, vs = _scales(k_scales, k_pages, "k_scales"), _scales(v_scales, v_pages, "v_scales")
     cu_h, batch = _batch_args(cu_seqlens_q_host, cu_seqlens_q, used_kv_lens, (block_tables,), dev,
                               ("block_tables",))
-    with _on(dev):
-        _check(_native.load().sa_store_kv(
-            _ptr(k), _ptr(v), _ACT_DTYPES[k.dtype], k.stride(0), k.stride(1), v.stride(0),
-            v.stride(1), _ptr(k_pages), _ptr(v_pages), _ptr(ks), _ptr(vs), num_pages, code,
-            _ptr(block_tables), int(block_tables.shape[1]), cu_h.ctypes.data_as(ctypes.c_void_p),
-            _ptr(cu_seqlens_q), batch, int(k.shape[0]), _ptr(used_kv_lens), hkv, d, page_size,
-            _status_word(status, dev), _stream(stream, dev)), "sa_store_kv")
+    ks0, ks1, _ = k.stride()
+    vs0, vs1, _ = v.stride()
+    _check(_on(dev, _native.load().sa_store_kv, k.data_ptr(), v.data_ptr(), _ACT_DTYPES[k.dtype],
+               ks0, ks1, vs0, vs1, k_pages.data_ptr(), v_pages.data_ptr(), _ptr(ks), _ptr(vs),
+               num_pages, code, block_tables.data_ptr(), block_tables.shape[1], _host_ptr(cu_h),
+               cu_seqlens_q.data_ptr(), batch, k.shape[0], used_kv_lens.data_ptr(), hkv, d,
+               page_size, _status_word(status, dev), _stream(stream, dev)), "sa_store_kv")
 
 
 def _check_bounds(bounds, hkv, d, dev):
     _require(bounds, torch.bfloat16, "bounds", dev)
-    if bounds.dim() != 4 or tuple(bounds.shape[1:]) != (hkv, 2, d):
+    if len(bounds.shape) != 4 or bounds.shape[1:] != (hkv, 2, d):
         raise ValueError(f"bounds must be [rows, {hkv}, 2, {d}], got {tuple(bounds.shape)}")
 
 
@@ -675,18 +695,17 @@ def sa_block_bounds(k_pages, block_tables, cu_seqlens_q_host, cu_seqlens_q, used
     code = _cache_dtype(k_pages, "k_pages")
     dev = k_pages.device
     _require(k_pages, k_pages.dtype, "k_pages", dev)
-    num_pages, hkv, page_size, d = (int(x) for x in k_pages.shape)
+    num_pages, hkv, page_size, d = k_pages.shape
     ks = _scales(k_scales, k_pages, "k_scales")
     _check_bounds(bounds, hkv, d, dev)
     cu_h, batch = _batch_args(cu_seqlens_q_host, cu_seqlens_q, used_kv_lens,
                               (block_tables, bound_tables), dev, ("block_tables", "bound_tables"))
-    with _on(dev):
-        _check(_native.load().sa_block_bounds(
-            _ptr(k_pages), _ptr(ks), num_pages, code, _ptr(block_tables),
-            int(block_tables.shape[1]), cu_h.ctypes.data_as(ctypes.c_void_p), _ptr(cu_seqlens_q),
-            batch, int(cu_h[-1]), _ptr(used_kv_lens), hkv, d, int(block_size), page_size,
-            _ptr(bound_tables), int(bound_tables.shape[1]), int(bounds.shape[0]), _ptr(bounds),
-            _status_word(status, dev), _stream(stream, dev)), "sa_block_bounds")
+    _check(_on(dev, _native.load().sa_block_bounds, k_pages.data_ptr(), _ptr(ks), num_pages, code,
+               block_tables.data_ptr(), block_tables.shape[1], _host_ptr(cu_h),
+               cu_seqlens_q.data_ptr(), batch, int(cu_h[-1]), used_kv_lens.data_ptr(), hkv, d,
+               block_size, page_size, bound_tables.data_ptr(), bound_tables.shape[1],
+               bounds.shape[0], bounds.data_ptr(), _status_word(status, dev),
+               _stream(stream, dev)), "sa_block_bounds")
     return bounds
 
 
@@ -715,17 +734,17 @@ def sa_select_blocks(q, bounds, bound_tables, cu_seqlens_q_host, cu_seqlens_q, u
     dev = q.device
     if q.dim() != 3 or not isinstance(bounds, torch.Tensor) or bounds.dim() != 4:
         raise ValueError("q must be [tq, hq, d], bounds [rows, hkv, 2, d]")
-    tq, hq, d = (int(x) for x in q.shape)
-    hkv = int(bounds.shape[1])
+    tq, hq, d = q.shape
+    hkv = bounds.shape[1]
     _check_bounds(bounds, hkv, d, dev)
     cu_h, batch = _batch_args(cu_seqlens_q_host, cu_seqlens_q, used_kv_lens, (bound_tables,), dev,
                               ("bound_tables",))
-    msb = int(bound_tables.shape[1])
+    msb = bound_tables.shape[1]
     if selected is None:
         selected = torch.empty((tq, hkv, int(topk)), dtype=torch.int32, device=dev)
     else:
         _require(selected, torch.int32, "selected", dev)
-        if tuple(selected.shape) != (tq, hkv, int(topk)):
+        if selected.shape != (tq, hkv, topk):
             raise ValueError(f"selected must be {(tq, hkv, int(topk))}, got {tuple(selected.shape)}")
     if workspace is None:
         workspace = allocate_select_workspace(tq, batch, hkv, d, msb, dev)
@@ -736,14 +755,12 @@ def sa_select_blocks(q, bounds, bound_tables, cu_seqlens_q_host, cu_seqlens_q, u
         _require(workspace, torch.uint8, "workspace", dev)
     base = workspace.data_ptr()
     aligned = (base + 255) & ~255
-    with _on(dev):
-        _check(_native.load().sa_select_blocks(
-            _ptr(q), _ACT_DTYPES[q.dtype], tq, hq, hkv, d, _ptr(bounds), int(bounds.shape[0]),
-            _ptr(bound_tables), msb, cu_h.ctypes.data_as(ctypes.c_void_p), _ptr(cu_seqlens_q),
-            batch, _ptr(used_kv_lens), int(block_size), int(topk), _causal(causal),
-            int(sink_blocks), int(local_blocks), _ptr(selected), ctypes.c_void_p(aligned),
-            max(workspace.numel() - (aligned - base), 0), _status_word(status, dev),
-            _stream(stream, dev)), "sa_select_blocks")
+    _check(_on(dev, _native.load().sa_select_blocks, q.data_ptr(), _ACT_DTYPES[q.dtype], tq, hq,
+               hkv, d, bounds.data_ptr(), bounds.shape[0], bound_tables.data_ptr(), msb,
+               _host_ptr(cu_h), cu_seqlens_q.data_ptr(), batch, used_kv_lens.data_ptr(), block_size,
+               topk, _causal(causal), sink_blocks, local_blocks, selected.data_ptr(), aligned,
+               max(workspace.numel() - (aligned - base), 0), _status_word(status, dev),
+               _stream(stream, dev)), "sa_select_blocks")
     return selected
 
 

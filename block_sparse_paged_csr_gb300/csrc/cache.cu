@@ -142,7 +142,7 @@ __device__ __forceinline__ void store8(void* pages, int64_t off, const float (&x
 // magnitude and the pass that writes codes, so a page of 64 x 128 is read
 // once.
 template <int kType, bool kSrcBf16, int kItemWarps>
-__global__ void __launch_bounds__(kThreads) store_kv_kernel(const StoreArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) store_kv_kernel(const StoreArgs a) {
   constexpr bool kCodes = kType == kE4m3 || kType == kInt8;
   constexpr int kT = kItemWarps * 32;                 // threads per item
   constexpr int kHeld = kItemWarps == 1 ? 2 : 4;
@@ -290,160 +290,203 @@ struct BoundsArgs {
 // Elements of a 16-byte piece.
 template <int kType> struct Piece { static constexpr int n = kType == kF32 ? 4 : kType == kBf16 ? 8 : 16; };
 
-// One CTA per (block, kv head).  A thread owns one 16-byte piece of a row (its
-// channels) and every kRows-th row of the block; the codes' minima and maxima
-// are kept as packed f16 (exact) and multiplied by the scale where the page
-// changes; threads of the same channels meet in shared memory.
+// The pieces of a row are spread over P lanes (the power of two that holds
+// them, at most 32), so a warp takes 32 / P rows side by side.
 template <int kType>
-__global__ void __launch_bounds__(kThreads) block_bounds_kernel(const BoundsArgs a) {
+__host__ __device__ constexpr int lanes_per_row(int head_dim) {
+  const int n = head_dim / Piece<kType>::n;
+  int p = 1;
+  while (p < n && p < 32) p *= 2;
+  return p;
+}
+
+__device__ __forceinline__ uint32_t min_bf16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+
+// One warp per (block, kv head): no barrier, no shared memory, and as many
+// blocks in flight as registers allow, which is what both ends of the range
+// need (single tokens: the chain of lookups before the first key; prompts:
+// bytes in flight).  A lane takes one 16-byte piece of every (32 / P)-th row,
+// four loads in flight.  Minima and maxima of codes are taken as packed f16
+// (exact) and meet the scale where the page changes; they are rounded outward to
+// bf16 before lanes of the same channels meet (rounding is monotonic: the
+// minimum of the rounded is the rounded minimum).  Reads each key once.
+template <int kType>
+__global__ void __launch_bounds__(kThreads, 3) block_bounds_kernel(const BoundsArgs a) {
   constexpr int kN = Piece<kType>::n;
   constexpr bool kCodes = kType == kE4m3 || kType == kInt8;
-  extern __shared__ float s_part[];                    // [groups][2][head_dim]
-  const int tid = threadIdx.x;
-  const int lane = tid & 31;
-  const int64_t u = blockIdx.x / a.hkv;
-  const int h = static_cast<int>(blockIdx.x - u * a.hkv);
+  constexpr int kBatch = 4;
+  const int lane = threadIdx.x & 31;
+  const unsigned item = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const unsigned u = item / static_cast<unsigned>(a.hkv);
+  const int h = static_cast<int>(item - u * static_cast<unsigned>(a.hkv));
+  if (u >= a.slots) return;
   const int b = warp_slot_sequence(a.cu, a.batch, a.block_size, u, lane);
   const NewRange nr = new_range(a.cu, a.used, b, a.tq);
-  const int64_t blk0 = nr.p0 / a.block_size;
-  const int64_t blk = blk0 + (u - slot_base(a.cu[b], b, a.block_size));
+  // (positions fit 32 bits: lengths are int32)
+  const unsigned blk0 = static_cast<unsigned>(nr.p0) / static_cast<unsigned>(a.block_size);
+  const int64_t blk = blk0 + (static_cast<int64_t>(u) - slot_base(nr.cu0, b, a.block_size));
   const int64_t base = blk * a.block_size;
   if (blk < blk0 || base >= nr.p1 || nr.p0 >= nr.p1 || blk >= a.msb) return;
-  const int row = a.bound_tables[static_cast<int64_t>(b) * a.msb + blk];
-  if (row < 0 || row >= a.num_bounds) {
-    if (row >= 0 && tid == 0) report(a.status, SA_ERR_SHAPE);
-    return;
-  }
   const int d = a.head_dim;
-  const int per_row = d / kN;                          // pieces of a row
-  const int groups = kThreads / per_row;               // rows taken at a time
-  const int c = tid % per_row;
-  const int g = tid / per_row;
-  const int keys = static_cast<int>(min(nr.p1 - base, static_cast<int64_t>(a.block_size)));
   const int ps = a.page_size;
+  const int ppb = a.block_size / ps;
+  const int keys = static_cast<int>(min(nr.p1 - base, static_cast<int64_t>(a.block_size)));
   const int32_t* bt = a.block_tables + static_cast<int64_t>(b) * a.max_pages;
-  const int64_t pg0 = blk * (a.block_size / ps);
+  const int row = a.bound_tables[static_cast<int64_t>(b) * a.msb + blk];
 
-  float lo[kN], hi[kN];
+  const int lanes = lanes_per_row<kType>(d);
+  const int piece = lane & (lanes - 1);
+  const int sub = lane / lanes;                        // the lane's row of a load
+  const int rows = 32 / lanes;                         // rows per load
+  const int lps = (ps & (ps - 1)) == 0 ? __ffs(ps) - 1 : -1;
+  uint32_t* out =
+      reinterpret_cast<uint32_t*>(a.bounds) + (static_cast<int64_t>(max(row, 0)) * a.hkv + h) * d;
+  for (int c0 = 0; c0 < d; c0 += lanes * kN) {         // (rows of more than 32 pieces: in parts)
+    const int ch = c0 + piece * kN;
+    const bool mine = ch < d;
+    uint32_t lo[kN / 2], hi[kN / 2];                   // bf16 pairs, rounded outward
 #pragma unroll
-  for (int i = 0; i < kN; ++i) {
-    lo[i] = INFINITY;
-    hi[i] = -INFINITY;
-  }
-  if (g < groups) {
-    // each group of threads takes a contiguous run of keys, so that pages
-    // change as rarely as possible
-    const int run = (a.block_size + groups - 1) / groups;
-    const int k1 = min((g + 1) * run, keys);
-    int k = g * run;
-    while (k < k1) {
-      const int p = k / ps;
-      const int end = min((p + 1) * ps, k1);
-      const int64_t pg = pg0 + p;
-      const int id = pg < a.max_pages ? bt[pg] : -1;
-      if (id < 0 || id >= a.num_pages) {
-        if (id >= 0 && c == 0) report(a.status, SA_ERR_SHAPE);
-        k = end;
-        continue;
+    for (int i = 0; i < kN / 2; ++i) {
+      lo[i] = 0x7F807F80u;
+      hi[i] = 0xFF80FF80u;
+    }
+    for (int pg0 = 0; pg0 * ps < keys; pg0 += 32) {
+      // 32 pages at a time: ids and scales, one per lane
+      const int64_t pg = blk * ppb + pg0 + lane;
+      int id_of = pg0 + lane < ppb && (pg0 + lane) * ps < keys && pg < a.max_pages ? bt[pg] : -1;
+      if (id_of >= a.num_pages) {
+        report(a.status, SA_ERR_SHAPE);
+        id_of = -1;
       }
-      const int64_t off = ((static_cast<int64_t>(id) * a.hkv + h) * ps + (k - p * ps)) * d + c * kN;
-      if constexpr (kCodes) {
-        const uint4* at = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.k_pages) + off);
-        const float s = a.k_scales[static_cast<int64_t>(id) * a.hkv + h];
-        __half2 l2[8], h2[8];
+      float sc_of = 0.f;
+      if constexpr (kCodes)
+        sc_of = id_of >= 0 ? a.k_scales[static_cast<int64_t>(id_of) * a.hkv + h] : 0.f;
+      const int r1 = min(keys, (pg0 + 32) * ps);
+      int cur = -1;                                    // the lane's page at hand
+      float sc = 0.f;
+      __half2 l2[8], h2[8];
+      auto open = [&]() {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           l2[i] = __half2half2(__ushort_as_half(0x7C00));
           h2[i] = __half2half2(__ushort_as_half(0xFC00));
         }
-        const int step = d / 16;
-#pragma unroll 4
-        for (int r = k; r < end; ++r, at += step) {
-          const uint4 w = __ldg(at);
-          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+      };
+      // (a NaN product, of a scale that is 0 and a channel with NaN keys only,
+      // counts as no key)
+      auto close = [&]() {
+        if constexpr (kCodes) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t f0, f1;
-            codes4_to_f16<kType == kInt8>(ww[i], f0, f1);
-            const __half2 x0 = *reinterpret_cast<const __half2*>(&f0);
-            const __half2 x1 = *reinterpret_cast<const __half2*>(&f1);
-            l2[2 * i] = __hmin2(l2[2 * i], x0);
-            h2[2 * i] = __hmax2(h2[2 * i], x0);
-            l2[2 * i + 1] = __hmin2(l2[2 * i + 1], x1);
-            h2[2 * i + 1] = __hmax2(h2[2 * i + 1], x1);
+          for (int i = 0; i < 8; ++i) {
+            const float2 l = __half22float2(l2[i]);
+            const float2 m = __half22float2(h2[i]);
+            lo[i] = min_bf16x2(lo[i], bf16_down(fminf(l.x * sc, INFINITY)) |
+                                          (bf16_down(fminf(l.y * sc, INFINITY)) << 16));
+            hi[i] = max_bf16x2(hi[i], bf16_up(fmaxf(m.x * sc, -INFINITY)) |
+                                          (bf16_up(fmaxf(m.y * sc, -INFINITY)) << 16));
           }
         }
-        // (a NaN product, of a scale that is 0 and a channel with NaN keys
-        // only, leaves the other operand)
+      };
+      if constexpr (kCodes) open();
+      for (int k0 = pg0 * ps; k0 < r1; k0 += kBatch * rows) {
+        uint4 w[kBatch];
+        int pw[kBatch];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 l = __half22float2(l2[i]);
-          const float2 m = __half22float2(h2[i]);
-          lo[2 * i] = fminf(lo[2 * i], l.x * s);
-          lo[2 * i + 1] = fminf(lo[2 * i + 1], l.y * s);
-          hi[2 * i] = fmaxf(hi[2 * i], m.x * s);
-          hi[2 * i + 1] = fmaxf(hi[2 * i + 1], m.y * s);
+        for (int t = 0; t < kBatch; ++t) {
+          const int r = k0 + t * rows + sub;
+          const int p = min(lps >= 0 ? r >> lps : r / ps, pg0 + 31);
+          const int page = __shfl_sync(0xffffffffu, id_of, p - pg0);
+          pw[t] = r < r1 && page >= 0 && mine ? p : -1;
+          w[t] = make_uint4(0u, 0u, 0u, 0u);
+          if (pw[t] >= 0)
+            w[t] = __ldg(reinterpret_cast<const uint4*>(
+                static_cast<const unsigned char*>(a.k_pages) +
+                (((static_cast<int64_t>(page) * a.hkv + h) * ps + (r - p * ps)) * d + ch) *
+                    (16 / kN)));
         }
-      } else if constexpr (kType == kBf16) {
-        const uint16_t* at = static_cast<const uint16_t*>(a.k_pages) + off;
-#pragma unroll 4
-        for (int r = k; r < end; ++r, at += d) {
-          const uint4 w = __ldg(reinterpret_cast<const uint4*>(at));
-          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float x0 = __uint_as_float(ww[i] << 16);
-            const float x1 = __uint_as_float(ww[i] & 0xFFFF0000u);
-            lo[2 * i] = fminf(lo[2 * i], x0);
-            hi[2 * i] = fmaxf(hi[2 * i], x0);
-            lo[2 * i + 1] = fminf(lo[2 * i + 1], x1);
-            hi[2 * i + 1] = fmaxf(hi[2 * i + 1], x1);
+        for (int t = 0; t < kBatch; ++t) {
+          const uint32_t ww[4] = {w[t].x, w[t].y, w[t].z, w[t].w};
+          if constexpr (kCodes) {
+            const float s_new = __shfl_sync(0xffffffffu, sc_of, max(pw[t] - pg0, 0));
+            if (pw[t] < 0) continue;
+            if (pw[t] != cur) {
+              if (cur >= 0) {
+                close();
+                open();
+              }
+              cur = pw[t];
+              sc = s_new;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t f0, f1;
+              codes4_to_f16<kType == kInt8>(ww[i], f0, f1);
+              const __half2 x0 = *reinterpret_cast<const __half2*>(&f0);
+              const __half2 x1 = *reinterpret_cast<const __half2*>(&f1);
+              l2[2 * i] = __hmin2(l2[2 * i], x0);
+              h2[2 * i] = __hmax2(h2[2 * i], x0);
+              l2[2 * i + 1] = __hmin2(l2[2 * i + 1], x1);
+              h2[2 * i + 1] = __hmax2(h2[2 * i + 1], x1);
+            }
+          } else if constexpr (kType == kBf16) {
+            if (pw[t] < 0) continue;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              lo[i] = min_bf16x2(lo[i], ww[i]);
+              hi[i] = max_bf16x2(hi[i], ww[i]);
+            }
+          } else {
+            if (pw[t] < 0) continue;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float x0 = __uint_as_float(ww[2 * i]), x1 = __uint_as_float(ww[2 * i + 1]);
+              // (NaN keys do not count)
+              lo[i] = min_bf16x2(lo[i], bf16_down(fminf(x0, INFINITY)) |
+                                            (bf16_down(fminf(x1, INFINITY)) << 16));
+              hi[i] = max_bf16x2(hi[i], bf16_up(fmaxf(x0, -INFINITY)) |
+                                            (bf16_up(fmaxf(x1, -INFINITY)) << 16));
+            }
           }
-        }
-      } else {
-        const float* at = static_cast<const float*>(a.k_pages) + off;
-#pragma unroll 4
-        for (int r = k; r < end; ++r, at += d) {
-          const float4 w = __ldg(reinterpret_cast<const float4*>(at));
-          lo[0] = fminf(lo[0], w.x);
-          hi[0] = fmaxf(hi[0], w.x);
-          lo[1] = fminf(lo[1], w.y);
-          hi[1] = fmaxf(hi[1], w.y);
-          lo[2] = fminf(lo[2], w.z);
-          hi[2] = fmaxf(hi[2], w.z);
-          lo[3] = fminf(lo[3], w.w);
-          hi[3] = fmaxf(hi[3], w.w);
         }
       }
-      k = end;
+      if constexpr (kCodes) {
+        if (cur >= 0) close();
+      }
     }
-    float* mine = s_part + static_cast<int64_t>(g) * 2 * d + c * kN;
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      mine[i] = lo[i];
-      mine[d + i] = hi[i];
+    for (int i = 0; i < kN / 2; ++i) {
+      for (int o = lanes; o < 32; o <<= 1) {
+        lo[i] = min_bf16x2(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
+        hi[i] = max_bf16x2(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
+      }
+    }
+    if (sub == 0 && mine && row >= 0 && row < a.num_bounds) {
+#pragma unroll
+      for (int i = 0; i < kN / 2; ++i) {
+        out[ch / 2 + i] = lo[i];
+        out[d / 2 + ch / 2 + i] = hi[i];
+      }
     }
   }
-  __syncthreads();
-  uint16_t* out = a.bounds + (static_cast<int64_t>(row) * a.hkv + h) * 2 * d;
-  for (int x = tid; x < 2 * d; x += kThreads) {
-    const bool is_hi = x >= d;
-    float v = s_part[x];
-    for (int g2 = 1; g2 < groups; ++g2) {
-      const float y = s_part[static_cast<int64_t>(g2) * 2 * d + x];
-      v = is_hi ? fmaxf(v, y) : fminf(v, y);
-    }
-    out[x] = static_cast<uint16_t>(is_hi ? bf16_up(v) : bf16_down(v));
-  }
+  if (row >= a.num_bounds && lane == 0) report(a.status, SA_ERR_SHAPE);
 }
 
 template <int kType>
 cudaError_t launch_bounds(const BoundsArgs& a, cudaStream_t stream) {
   const int64_t grid = a.slots * a.hkv;
   if (grid > 0x7FFFFFFF) return cudaErrorNotSupported;
-  const int groups = kThreads / (a.head_dim / Piece<kType>::n);
-  const size_t smem = static_cast<size_t>(groups) * 2 * a.head_dim * sizeof(float);
-  block_bounds_kernel<kType><<<static_cast<unsigned>(grid), kThreads, smem, stream>>>(a);
+  block_bounds_kernel<kType>
+      <<<static_cast<unsigned>((grid + kWarps - 1) / kWarps), kThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

@@ -1031,8 +1031,8 @@ cudaError_t launch_q8(const FusedQ8Args& a, cudaStream_t stream) {
   if (!encode_pool(b.k_pages, rows, kb, &maps.k) || !encode_pool(b.v_pages, rows, kb, &maps.v))
     return cudaErrorNotSupported;
   const void* fn = reinterpret_cast<const void*>(fused_dec_q8_kernel<kI8, R>);
-  cudaError_t err =
-      cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  static SmemLimit limit;
+  const cudaError_t err = limit.raise(fn, static_cast<int>(smem));
   if (err != cudaSuccess) return err;
   const int64_t n_pieces = b.whole_items + (b.tq * b.hkv - b.whole_items) * b.pieces;
   int64_t grid = device_sm_count();

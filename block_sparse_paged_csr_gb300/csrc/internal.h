@@ -1,6 +1,7 @@
 // Internal launch interfaces between the C ABI (api.cu) and the kernels.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
@@ -223,6 +224,28 @@ struct CombineArgs {
 cudaError_t launch_combine(const CombineArgs& a, cudaStream_t stream);
 
 int device_sm_count();
+
+// A kernel's dynamic shared-memory limit, raised once per device and size
+// instead of at every launch.  One static object per kernel; safe from several
+// host threads (a limit raised twice is the same limit).
+struct SmemLimit {
+  std::atomic<int> set[64] = {};
+  cudaError_t raise(const void* fn, int bytes) {
+    int dev = 0;
+    const cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    const bool known = dev >= 0 && dev < 64;
+    if (known && set[dev].load(std::memory_order_acquire) >= bytes) return cudaSuccess;
+    const cudaError_t e =
+        cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && known) {
+      int was = set[dev].load(std::memory_order_relaxed);
+      while (was < bytes && !set[dev].compare_exchange_weak(was, bytes)) {
+      }
+    }
+    return e;
+  }
+};
 
 // The fixed scratch array of sa_build_index_no_alloc on the current device
 // (no_alloc.cu): its device address and size.

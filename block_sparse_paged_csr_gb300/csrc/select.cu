@@ -1266,8 +1266,8 @@ cudaError_t launch_score(const SelectArgs& a, cudaStream_t s) {
   return by_q_type(a, [&](auto q16) {
     auto fn = block_score_kernel<kT, kNQ, decltype(q16)::value>;
     const int smem = kScoreWarps * score_ring(kT) * kGroup * score_row_bytes(a.head_dim);
-    const cudaError_t err =
-        cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static SmemLimit limit;
+    const cudaError_t err = limit.raise(reinterpret_cast<const void*>(fn), smem);
     if (err != cudaSuccess) return err;
     fn<<<static_cast<unsigned>(a.rows * a.chunks), kScoreThreads, smem, s>>>(a);
     return cudaGetLastError();
@@ -1291,9 +1291,9 @@ cudaError_t launch_tile(const SelectArgs& a, cudaStream_t s) {
     return 0;
   });
   block_maxima_kernel<<<static_cast<unsigned>(a.batch) * a.hkv * a.chunks, 1024, 0, s>>>(a);
+  static SmemLimit limit;
   const cudaError_t err =
-      cudaFuncSetAttribute(block_score_tile_kernel<kG>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, TileSmem<kG>::kTotal);
+      limit.raise(reinterpret_cast<const void*>(block_score_tile_kernel<kG>), TileSmem<kG>::kTotal);
   if (err != cudaSuccess) return err;
   block_score_tile_kernel<kG>
       <<<static_cast<unsigned>(grid), kTileThreads, TileSmem<kG>::kTotal, s>>>(a);
@@ -1301,18 +1301,20 @@ cudaError_t launch_tile(const SelectArgs& a, cudaStream_t s) {
 }
 
 template <int kWarps, int kKeys>
-cudaError_t launch_pick(const SelectArgs& a, cudaStream_t s) {
+cudaError_t launch_pick(const SelectArgs& a, bool behind_scores, cudaStream_t s) {
   constexpr int rows = pick_threads(kWarps) / (32 * kWarps);
   const size_t smem = rows * (static_cast<size_t>(2) * a.head_dim * 8 +
                               static_cast<size_t>(a.msb) * 8);
   return by_q_type(a, [&](auto q16) {
     auto fn = block_pick_kernel<kWarps, kKeys, decltype(q16)::value>;
     if (smem > 32 * 1024) {            // (the default limit counts the static part too)
-      const cudaError_t err = cudaFuncSetAttribute(
-          fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+      static SmemLimit limit;
+      const cudaError_t err =
+          limit.raise(reinterpret_cast<const void*>(fn), static_cast<int>(smem));
       if (err != cudaSuccess) return err;
     }
-    // (its prologue overlaps the end of the score kernel)
+    // Behind a score kernel its prologue overlaps that kernel's end.  (Behind
+    // another it would overlap work that may still write its inputs.)
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>((a.rows + rows - 1) / rows));
     cfg.blockDim = dim3(pick_threads(kWarps));
@@ -1322,7 +1324,7 @@ cudaError_t launch_pick(const SelectArgs& a, cudaStream_t s) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = behind_scores ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, fn, a);
   });
 }
@@ -1352,11 +1354,11 @@ cudaError_t launch_select(SelectArgs a, const SelectLayout& l, int64_t longest, 
                                   : launch_score_nq<16>(a, one, s);
       if (err != cudaSuccess) return err;
     }
-    if (a.msb <= 256) err = launch_pick<1, 8>(a, s);
-    else if (a.msb <= 512) err = launch_pick<1, 16>(a, s);
-    else if (a.msb <= 2048) err = launch_pick<8, 8>(a, s);
-    else if (a.msb <= 4096) err = launch_pick<8, 16>(a, s);
-    else err = launch_pick<8, 64>(a, s);
+    if (a.msb <= 256) err = launch_pick<1, 8>(a, a.msb > a.topk, s);
+    else if (a.msb <= 512) err = launch_pick<1, 16>(a, a.msb > a.topk, s);
+    else if (a.msb <= 2048) err = launch_pick<8, 8>(a, a.msb > a.topk, s);
+    else if (a.msb <= 4096) err = launch_pick<8, 16>(a, a.msb > a.topk, s);
+    else err = launch_pick<8, 64>(a, a.msb > a.topk, s);
     if (err != cudaSuccess) return err;
   }
   return cudaSuccess;

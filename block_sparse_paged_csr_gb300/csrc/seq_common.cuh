@@ -18,13 +18,23 @@ namespace sa {
 // least that much, so every touched piece has a slot although the lengths
 // live on the device; slots past a sequence's pieces stay idle.
 __host__ __device__ __forceinline__ int64_t slot_base(int64_t cu_b, int64_t b, int per) {
+#ifdef __CUDA_ARCH__
+  // (a 64-bit division costs some 100 instructions; token counts rarely need it)
+  if (cu_b >= 0 && cu_b < (int64_t{1} << 32))
+    return static_cast<int64_t>(static_cast<uint32_t>(cu_b) / static_cast<uint32_t>(per)) + 2 * b;
+#endif
   return cu_b / per + 2 * b;
 }
 
-// The sequence that owns slot u (the largest b with base(b) <= u); 32
-// candidates per round.  All lanes of the warp call it.
+// The sequence that owns slot u (the largest b with base(b) <= u): u / 2 where
+// few tokens precede it (decode batches: no search), else 32 candidates per
+// round.  All lanes of the warp call it.
 __device__ __forceinline__ int warp_slot_sequence(const int64_t* cu, int batch, int per,
                                                   int64_t u, int lane) {
+  const int guess = static_cast<int>(min(u / 2, static_cast<int64_t>(batch - 1)));
+  const int64_t g0 = cu[guess], g1 = cu[guess + 1];
+  if (slot_base(g0, guess, per) <= u && (guess + 1 == batch || u < slot_base(g1, guess + 1, per)))
+    return guess;
   int lo = 0, hi = batch;
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) / 32;
