@@ -61,8 +61,15 @@ __device__ __forceinline__ void load8(const void* src, int64_t off, float (&x)[8
   }
 }
 
-// Largest finite magnitude's bits (order-preserving as unsigned).
+// Largest magnitude's bits (they order like the magnitudes; infinities and NaN
+// above every number).
 __device__ __forceinline__ uint32_t amax_bits(uint32_t m, const float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  return m;
+}
+// The same without infinities and NaN.
+__device__ __forceinline__ uint32_t amax_finite(uint32_t m, const float (&x)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const uint32_t u = __float_as_uint(x[i]) & 0x7FFFFFFFu;
@@ -83,35 +90,60 @@ __device__ __forceinline__ float scale_of(uint32_t amax) {
 }
 
 // x / s for the page's scale: by the exact reciprocal where s is a power of
-// two (every scale this kernel makes), by division for a caller's own.
+// two (every scale this kernel makes), by division for a caller's own.  `plain`:
+// a power of two and numbers only, so that nothing has to be looked at per
+// element.
 struct Quant {
   float s, inv;
-  bool pow2;
-  __device__ __forceinline__ explicit Quant(float scale) : s(scale) {
+  bool pow2, plain;
+  __device__ __forceinline__ Quant(float scale, bool numbers) : s(scale) {
     const uint32_t u = __float_as_uint(scale);
     pow2 = (u & 0x7FFFFFu) == 0u && u != 0u;
     // 2^-e has the exponent field 254 - e; e = 254 (2^127) leaves the
     // subnormal 2^-127
     const uint32_t e = u >> 23;
     inv = pow2 ? (e < 254u ? __uint_as_float((254u - e) << 23) : __uint_as_float(0x00400000u)) : 0.f;
+    plain = pow2 && numbers;
   }
-  __device__ __forceinline__ float operator()(float x) const {
+  __device__ __forceinline__ float divided(float x) const {
     return s == 0.f ? (x == x ? 0.f : x) : (pow2 ? x * inv : __fdiv_rn(x, s));
   }
 };
 
-// Two values to codes, round to nearest even, beyond the range to its end;
+// Eight values to codes, round to nearest even, beyond the range to its end;
 // NaN stays NaN in e4m3 and becomes 0 in int8.
 template <int kType>
-__device__ __forceinline__ uint32_t to_code2(float x0, float x1) {
+__device__ __forceinline__ uint2 to_codes8(const float (&x)[8], const Quant& q) {
+  uint32_t c[4];
   if constexpr (kType == kE4m3) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(x1), "f"(x0));
-    return r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x0 = q.plain ? x[2 * i] * q.inv : q.divided(x[2 * i]);
+      const float x1 = q.plain ? x[2 * i + 1] * q.inv : q.divided(x[2 * i + 1]);
+      uint16_t r;
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(x1), "f"(x0));
+      c[i] = r;
+    }
+    return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
   } else {
-    const int a = __float2int_rn(fminf(fmaxf(x0 == x0 ? x0 : 0.f, -127.f), 127.f));
-    const int b = __float2int_rn(fminf(fmaxf(x1 == x1 ? x1 : 0.f, -127.f), 127.f));
-    return (static_cast<uint32_t>(a) & 0xFFu) | ((static_cast<uint32_t>(b) & 0xFFu) << 8);
+    // 1.5 * 2^23 + v has the integer nearest to v (|v| < 2^22) in its low bits;
+    // x inv is exact, so the one rounding is that of the addition
+    uint32_t b[8];
+    if (q.plain) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) b[i] = __float_as_uint(fmaf(x[i], q.inv, 12582912.f));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float v = q.divided(x[i]);
+        b[i] = __float_as_uint(fminf(fmaxf(v == v ? v : 0.f, -127.f), 127.f) + 12582912.f);
+      }
+    }
+    c[0] = __byte_perm(b[0], b[1], 0x0040);
+    c[1] = __byte_perm(b[2], b[3], 0x0040);
+    c[2] = __byte_perm(b[4], b[5], 0x0040);
+    c[3] = __byte_perm(b[6], b[7], 0x0040);
+    return make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
   }
 }
 
@@ -127,11 +159,7 @@ __device__ __forceinline__ void store8(void* pages, int64_t off, const float (&x
         make_uint4(pack_bf16x2_rn(x[0], x[1]), pack_bf16x2_rn(x[2], x[3]),
                    pack_bf16x2_rn(x[4], x[5]), pack_bf16x2_rn(x[6], x[7]));
   } else {
-    uint32_t c[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = to_code2<kType>(qz(x[2 * i]), qz(x[2 * i + 1]));
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(pages) + off) =
-        make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(pages) + off) = to_codes8<kType>(x, qz);
   }
 }
 
@@ -175,21 +203,34 @@ __global__ void __launch_bounds__(kThreads, 4) store_kv_kernel(const StoreArgs a
   const int64_t tok0 = nr.cu0 + (base + r0 - nr.p0);
   const int per_row = a.head_dim >> 3;                // 8-element pieces of a row
   const int n = (r1 - r0) * per_row;
+  // the thread's piece i: row r and piece c of it, without a division per piece
+  const int step_r = kT / per_row, step_c = kT - step_r * per_row;
+  const int first_r = t / per_row, first_c = t - first_r * per_row;
   const void* src = a.src[kv];
   const int64_t ts = a.token_stride[kv];
   const int64_t src0 = tok0 * ts + h * a.head_stride[kv];
   void* pages = a.pages[kv];
   const int64_t dst0 = ((static_cast<int64_t>(id) * a.hkv + h) * a.page_size + r0) * a.head_dim;
-  auto src_at = [&](int i) -> int64_t {
-    const int r = i / per_row;
-    return src0 + r * ts + (i - r * per_row) * 8;
+  auto advance = [&](int& r, int& c) {
+    r += step_r;
+    c += step_c;
+    if (c >= per_row) {
+      c -= per_row;
+      ++r;
+    }
   };
+  auto src_at = [&](int r, int c) -> int64_t { return src0 + r * ts + c * 8; };
 
   float held[kHeld][8];
   uint32_t m = 0;
+  int r = first_r, c = first_c;
 #pragma unroll
-  for (int j = 0; j < kHeld; ++j)
-    if (t + j * kT < n) load8<kSrcBf16>(src, src_at(t + j * kT), held[j]);
+  for (int j = 0; j < kHeld; ++j) {
+    if (t + j * kT < n) load8<kSrcBf16>(src, src_at(r, c), held[j]);
+    advance(r, c);
+  }
+  const int next_r = r, next_c = c;                    // the first piece not held
+  bool numbers = true;
   float* scale_at = nullptr;
   float s_old = 0.f;
   if constexpr (kCodes) {
@@ -198,38 +239,52 @@ __global__ void __launch_bounds__(kThreads, 4) store_kv_kernel(const StoreArgs a
       s_old = *scale_at;
       if (!(s_old > 0.f && s_old < INFINITY)) s_old = 0.f;
     }
+    auto amax = [&](bool finite_only) {
+      uint32_t v = 0;
 #pragma unroll
-    for (int j = 0; j < kHeld; ++j)
-      if (t + j * kT < n) m = amax_bits(m, held[j]);
-    for (int i = t + kHeld * kT; i < n; i += kT) {
-      float x[8];
-      load8<kSrcBf16>(src, src_at(i), x);
-      m = amax_bits(m, x);
-    }
-    m = __reduce_max_sync(0xffffffffu, m);
-    if constexpr (kItemWarps > 1) {
-      if (lane == 0) s_amax[warp] = m;
-      __syncthreads();
+      for (int j = 0; j < kHeld; ++j)
+        if (t + j * kT < n) v = finite_only ? amax_finite(v, held[j]) : amax_bits(v, held[j]);
+      int ar = next_r, ac = next_c;
+      for (int i = t + kHeld * kT; i < n; i += kT) {
+        float x[8];
+        load8<kSrcBf16>(src, src_at(ar, ac), x);
+        advance(ar, ac);
+        v = finite_only ? amax_finite(v, x) : amax_bits(v, x);
+      }
+      v = __reduce_max_sync(0xffffffffu, v);
+      if constexpr (kItemWarps > 1) {
+        __syncthreads();
+        if (lane == 0) s_amax[warp] = v;
+        __syncthreads();
 #pragma unroll
-      for (int w = 0; w < kItemWarps; ++w) m = max(m, s_amax[w]);
-    }
+        for (int w = 0; w < kItemWarps; ++w) v = max(v, s_amax[w]);
+      }
+      return v;
+    };
+    m = amax(false);
+    numbers = m < 0x7F800000u;
+    if (!numbers) m = amax(true);                      // (the same for the whole item)
   }
   const float s_new = kCodes ? fmaxf(s_old, scale_of<kType>(m)) : 1.f;
-  const Quant qz(s_new);
+  const Quant qz(s_new, numbers);
 #pragma unroll
   for (int j = 0; j < kHeld; ++j)
     if (t + j * kT < n)
       store8<kType>(pages, dst0 + static_cast<int64_t>(t + j * kT) * 8, held[j], qz);
+  r = next_r;
+  c = next_c;
   for (int i = t + kHeld * kT; i < n; i += kT) {
     float x[8];
-    load8<kSrcBf16>(src, src_at(i), x);
+    load8<kSrcBf16>(src, src_at(r, c), x);
+    advance(r, c);
     store8<kType>(pages, dst0 + static_cast<int64_t>(i) * 8, x, qz);
   }
   if constexpr (kCodes) {
     if (r0 > 0 && s_new > s_old) {
       // the page's earlier rows to the larger scale
       const float ratio = __fdiv_rn(s_old, s_new);
-      const Quant one(1.f);
+      // (NaN codes of e4m3 stay NaN; int8 codes are numbers)
+      const Quant one(1.f, true);
       uint8_t* old = static_cast<uint8_t*>(pages) + dst0 - static_cast<int64_t>(r0) * a.head_dim;
       for (int i = t; i < r0 * per_row; i += kT) {
         const uint2 w = *reinterpret_cast<const uint2*>(old + static_cast<int64_t>(i) * 8);
@@ -319,7 +374,47 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t x, uint32_t y) {
 // (exact) and meet the scale where the page changes; they are rounded outward to
 // bf16 before lanes of the same channels meet (rounding is monotonic: the
 // minimum of the rounded is the rounded minimum).  Reads each key once.
-template <int kType>
+// Codes' minima and maxima as f16 pairs (exact, two codes an instruction).  An
+// int8 code v is held as 1152 + v, whose f16 bits are 0x6400 above the byte
+// v + 128, until it is read.
+template <bool kI8>
+struct CodeRange {
+  uint32_t lo[8], hi[8];
+  __device__ __forceinline__ void reset() {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      lo[i] = 0x7C007C00u;
+      hi[i] = 0xFC00FC00u;
+    }
+  }
+  __device__ __forceinline__ void add(const uint4& w) {
+    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t f[2];
+      if constexpr (kI8) {
+        const uint32_t u = ww[i] ^ 0x80808080u;
+        f[0] = __byte_perm(u, 0x64646464u, 0x4140);
+        f[1] = __byte_perm(u, 0x64646464u, 0x4342);
+      } else {
+        codes4_to_f16<false>(ww[i], f[0], f[1]);
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {                    // (NaN codes do not count)
+        asm("min.f16x2 %0, %0, %1;" : "+r"(lo[2 * i + j]) : "r"(f[j]));
+        asm("max.f16x2 %0, %0, %1;" : "+r"(hi[2 * i + j]) : "r"(f[j]));
+      }
+    }
+  }
+  static __device__ __forceinline__ float2 value(uint32_t u) {
+    if constexpr (kI8) asm("sub.f16x2 %0, %0, %1;" : "+r"(u) : "r"(0x64806480u));
+    return f16x2_to_f32(u);
+  }
+};
+
+// kInPage: a batch of loads never leaves a page (page_size a multiple of its
+// rows), the usual case: one lookup per batch.
+template <int kType, bool kInPage>
 __global__ void __launch_bounds__(kThreads, 3) block_bounds_kernel(const BoundsArgs a) {
   constexpr int kN = Piece<kType>::n;
   constexpr bool kCodes = kType == kE4m3 || kType == kInt8;
@@ -373,89 +468,109 @@ __global__ void __launch_bounds__(kThreads, 3) block_bounds_kernel(const BoundsA
       const int r1 = min(keys, (pg0 + 32) * ps);
       int cur = -1;                                    // the lane's page at hand
       float sc = 0.f;
-      __half2 l2[8], h2[8];
-      auto open = [&]() {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          l2[i] = __half2half2(__ushort_as_half(0x7C00));
-          h2[i] = __half2half2(__ushort_as_half(0xFC00));
-        }
-      };
-      // (a NaN product, of a scale that is 0 and a channel with NaN keys only,
-      // counts as no key)
+      CodeRange<kType == kInt8> cr;
+      // The page's codes times its scale.  A code has at most 8 significant bits
+      // and lies in 2^-9 .. 448, so its product with a power of two of this
+      // range is a bf16 number; other products are rounded outward.  (A NaN
+      // product, of a scale that is 0 and a channel with NaN keys only, counts
+      // as no key.)
       auto close = [&]() {
         if constexpr (kCodes) {
+          const bool exact = (__float_as_uint(sc) & 0x7FFFFFu) == 0u && sc >= 0x1p-120f && sc <= 0x1p100f;
+          if (exact) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float2 l = __half22float2(l2[i]);
-            const float2 m = __half22float2(h2[i]);
-            lo[i] = min_bf16x2(lo[i], bf16_down(fminf(l.x * sc, INFINITY)) |
-                                          (bf16_down(fminf(l.y * sc, INFINITY)) << 16));
-            hi[i] = max_bf16x2(hi[i], bf16_up(fmaxf(m.x * sc, -INFINITY)) |
-                                          (bf16_up(fmaxf(m.y * sc, -INFINITY)) << 16));
+            for (int i = 0; i < 8; ++i) {
+              const float2 l = cr.value(cr.lo[i]);
+              const float2 m = cr.value(cr.hi[i]);
+              lo[i] = min_bf16x2(lo[i], __byte_perm(__float_as_uint(l.x * sc),
+                                                    __float_as_uint(l.y * sc), 0x7632));
+              hi[i] = max_bf16x2(hi[i], __byte_perm(__float_as_uint(m.x * sc),
+                                                    __float_as_uint(m.y * sc), 0x7632));
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float2 l = cr.value(cr.lo[i]);
+              const float2 m = cr.value(cr.hi[i]);
+              lo[i] = min_bf16x2(lo[i], bf16_down(fminf(l.x * sc, INFINITY)) |
+                                            (bf16_down(fminf(l.y * sc, INFINITY)) << 16));
+              hi[i] = max_bf16x2(hi[i], bf16_up(fmaxf(m.x * sc, -INFINITY)) |
+                                            (bf16_up(fmaxf(m.y * sc, -INFINITY)) << 16));
+            }
           }
         }
       };
-      if constexpr (kCodes) open();
+      // one load's keys; `page`, its page within the block, opens the page's range
+      auto open = [&](int page, float scale) {
+        if constexpr (kCodes) {
+          if (page == cur) return;
+          if (cur >= 0) close();
+          cr.reset();
+          cur = page;
+          sc = scale;
+        }
+      };
+      auto add = [&](const uint4& w) {
+        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+        if constexpr (kCodes) {
+          cr.add(w);
+        } else if constexpr (kType == kBf16) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            lo[i] = min_bf16x2(lo[i], ww[i]);
+            hi[i] = max_bf16x2(hi[i], ww[i]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float x0 = __uint_as_float(ww[2 * i]), x1 = __uint_as_float(ww[2 * i + 1]);
+            // (NaN keys do not count)
+            lo[i] = min_bf16x2(lo[i], bf16_down(fminf(x0, INFINITY)) |
+                                          (bf16_down(fminf(x1, INFINITY)) << 16));
+            hi[i] = max_bf16x2(hi[i], bf16_up(fmaxf(x0, -INFINITY)) |
+                                          (bf16_up(fmaxf(x1, -INFINITY)) << 16));
+          }
+        }
+      };
       for (int k0 = pg0 * ps; k0 < r1; k0 += kBatch * rows) {
         uint4 w[kBatch];
-        int pw[kBatch];
-#pragma unroll
-        for (int t = 0; t < kBatch; ++t) {
-          const int r = k0 + t * rows + sub;
-          const int p = min(lps >= 0 ? r >> lps : r / ps, pg0 + 31);
+        if constexpr (kInPage) {
+          const int p = lps >= 0 ? k0 >> lps : k0 / ps;
           const int page = __shfl_sync(0xffffffffu, id_of, p - pg0);
-          pw[t] = r < r1 && page >= 0 && mine ? p : -1;
-          w[t] = make_uint4(0u, 0u, 0u, 0u);
-          if (pw[t] >= 0)
+          const float scale = kCodes ? __shfl_sync(0xffffffffu, sc_of, p - pg0) : 0.f;
+          if (page < 0 || !mine) continue;
+          const unsigned char* at =
+              static_cast<const unsigned char*>(a.k_pages) +
+              (((static_cast<int64_t>(page) * a.hkv + h) * ps + (k0 - p * ps)) * d + ch) * (16 / kN);
+          const int last = r1 - 1 - k0;                // (behind it: a row that counts already)
+#pragma unroll
+          for (int t = 0; t < kBatch; ++t)
             w[t] = __ldg(reinterpret_cast<const uint4*>(
-                static_cast<const unsigned char*>(a.k_pages) +
-                (((static_cast<int64_t>(page) * a.hkv + h) * ps + (r - p * ps)) * d + ch) *
-                    (16 / kN)));
-        }
+                at + min(t * rows + sub, last) * (d * (16 / kN))));
+          open(p, scale);
 #pragma unroll
-        for (int t = 0; t < kBatch; ++t) {
-          const uint32_t ww[4] = {w[t].x, w[t].y, w[t].z, w[t].w};
-          if constexpr (kCodes) {
-            const float s_new = __shfl_sync(0xffffffffu, sc_of, max(pw[t] - pg0, 0));
+          for (int t = 0; t < kBatch; ++t) add(w[t]);
+        } else {
+          int pw[kBatch];
+#pragma unroll
+          for (int t = 0; t < kBatch; ++t) {
+            const int r = k0 + t * rows + sub;
+            const int p = min(lps >= 0 ? r >> lps : r / ps, pg0 + 31);
+            const int page = __shfl_sync(0xffffffffu, id_of, p - pg0);
+            pw[t] = r < r1 && page >= 0 && mine ? p : -1;
+            if (pw[t] >= 0)
+              w[t] = __ldg(reinterpret_cast<const uint4*>(
+                  static_cast<const unsigned char*>(a.k_pages) +
+                  (((static_cast<int64_t>(page) * a.hkv + h) * ps + (r - p * ps)) * d + ch) *
+                      (16 / kN)));
+          }
+#pragma unroll
+          for (int t = 0; t < kBatch; ++t) {
+            const float scale =
+                kCodes ? __shfl_sync(0xffffffffu, sc_of, max(pw[t] - pg0, 0)) : 0.f;
             if (pw[t] < 0) continue;
-            if (pw[t] != cur) {
-              if (cur >= 0) {
-                close();
-                open();
-              }
-              cur = pw[t];
-              sc = s_new;
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t f0, f1;
-              codes4_to_f16<kType == kInt8>(ww[i], f0, f1);
-              const __half2 x0 = *reinterpret_cast<const __half2*>(&f0);
-              const __half2 x1 = *reinterpret_cast<const __half2*>(&f1);
-              l2[2 * i] = __hmin2(l2[2 * i], x0);
-              h2[2 * i] = __hmax2(h2[2 * i], x0);
-              l2[2 * i + 1] = __hmin2(l2[2 * i + 1], x1);
-              h2[2 * i + 1] = __hmax2(h2[2 * i + 1], x1);
-            }
-          } else if constexpr (kType == kBf16) {
-            if (pw[t] < 0) continue;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              lo[i] = min_bf16x2(lo[i], ww[i]);
-              hi[i] = max_bf16x2(hi[i], ww[i]);
-            }
-          } else {
-            if (pw[t] < 0) continue;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float x0 = __uint_as_float(ww[2 * i]), x1 = __uint_as_float(ww[2 * i + 1]);
-              // (NaN keys do not count)
-              lo[i] = min_bf16x2(lo[i], bf16_down(fminf(x0, INFINITY)) |
-                                            (bf16_down(fminf(x1, INFINITY)) << 16));
-              hi[i] = max_bf16x2(hi[i], bf16_up(fmaxf(x0, -INFINITY)) |
-                                            (bf16_up(fmaxf(x1, -INFINITY)) << 16));
-            }
+            open(pw[t], scale);
+            add(w[t]);
           }
         }
       }
@@ -485,8 +600,11 @@ template <int kType>
 cudaError_t launch_bounds(const BoundsArgs& a, cudaStream_t stream) {
   const int64_t grid = a.slots * a.hkv;
   if (grid > 0x7FFFFFFF) return cudaErrorNotSupported;
-  block_bounds_kernel<kType>
-      <<<static_cast<unsigned>((grid + kWarps - 1) / kWarps), kThreads, 0, stream>>>(a);
+  const unsigned ctas = static_cast<unsigned>((grid + kWarps - 1) / kWarps);
+  if (a.page_size % (4 * 32 / lanes_per_row<kType>(a.head_dim)) == 0)
+    block_bounds_kernel<kType, true><<<ctas, kThreads, 0, stream>>>(a);
+  else
+    block_bounds_kernel<kType, false><<<ctas, kThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
