@@ -254,18 +254,21 @@ __device__ __forceinline__ uint32_t sw128_offset(int rows, int r, int k) {
   return static_cast<uint32_t>(panel * rows * 128 + r * 128 + ((chunk ^ (r & 7)) << 4) + within);
 }
 
-// Four K/V elements as packed bf16 (round to nearest even); 8-bit codes times
-// the scale of their page (exact in bf16 under a power-of-two scale).
+// Four 8-bit codes times the scale of their page as packed bf16 (exact under a
+// power-of-two scale, else rounded to nearest even).
+template <bool kInt8>
+__device__ __forceinline__ uint2 codes4_to_bf16(uint32_t w, float scale) {
+  uint32_t h0, h1;
+  codes4_to_f16<kInt8>(w, h0, h1);
+  const float2 x = f16x2_to_f32(h0), y = f16x2_to_f32(h1);
+  return make_uint2(pack_bf16x2_rn(x.x * scale, x.y * scale),
+                    pack_bf16x2_rn(y.x * scale, y.y * scale));
+}
+
+// Four K/V elements as packed bf16 (round to nearest even).
 template <int kT>
-__device__ __forceinline__ uint2 ld_kv4_bf16(const void* pages, int64_t elem_off, float scale) {
-  if constexpr (kT == SA_DTYPE_E4M3 || kT == SA_DTYPE_INT8) {
-    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(pages) + elem_off));
-    uint32_t h0, h1;
-    codes4_to_f16<kT == SA_DTYPE_INT8>(w, h0, h1);
-    const float2 x = f16x2_to_f32(h0), y = f16x2_to_f32(h1);
-    return make_uint2(pack_bf16x2_rn(x.x * scale, x.y * scale),
-                      pack_bf16x2_rn(y.x * scale, y.y * scale));
-  } else if constexpr (kT == SA_DTYPE_BF16) {
+__device__ __forceinline__ uint2 ld_kv4_bf16(const void* pages, int64_t elem_off) {
+  if constexpr (kT == SA_DTYPE_BF16) {
     return __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(pages) + elem_off));
   } else {
     const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(pages) + elem_off));
@@ -595,6 +598,46 @@ __device__ void tc_loader(const ForwardArgs& a, unsigned char* smem, const TcPla
           }
         }
       }
+    } else if constexpr (kT == SA_DTYPE_E4M3 || kT == SA_DTYPE_INT8) {
+      // 8-bit rows are 128 bytes: 16 codes per lane, four rows per load
+      // instruction, all of a warp's rows in flight together
+      constexpr int kQuads = (2 * BS / 4 + kLoaders - 1) / kLoaders;
+      const int pc = lane & 7;
+      uint4 w[kQuads];
+      float sc[kQuads];
+#pragma unroll
+      for (int q = 0; q < kQuads; ++q) {
+        const int r = (lw + q * kLoaders) * 4 + (lane >> 3);
+        const bool is_k = r < BS;
+        const int64_t off = r < 2 * BS ? koff[is_k ? r : r - BS] : -1;
+        w[q] = make_uint4(0u, 0u, 0u, 0u);
+        sc[q] = 0.f;
+        if (off >= 0) {
+          w[q] = __ldg(reinterpret_cast<const uint4*>(
+                           static_cast<const uint8_t*>(is_k ? a.k_pages : a.v_pages) + off) + pc);
+          // off / (page_size * 128) numbers the (page, kv head); a pool of
+          // 2^32 rows of 128 codes would not fit the device
+          sc[q] = __ldg((is_k ? a.k_scales : a.v_scales) +
+                        static_cast<uint32_t>(off >> 7) / static_cast<uint32_t>(a.page_size));
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < kQuads; ++q) {
+        const int r = (lw + q * kLoaders) * 4 + (lane >> 3);
+        if (r >= 2 * BS) continue;
+        const uint2 c0 = codes4_to_bf16<kT == SA_DTYPE_INT8>(w[q].x, sc[q]);
+        const uint2 c1 = codes4_to_bf16<kT == SA_DTYPE_INT8>(w[q].y, sc[q]);
+        const uint2 c2 = codes4_to_bf16<kT == SA_DTYPE_INT8>(w[q].z, sc[q]);
+        const uint2 c3 = codes4_to_bf16<kT == SA_DTYPE_INT8>(w[q].w, sc[q]);
+        unsigned char* dst = r < BS ? ks : vs;
+        const int key = r < BS ? r : r - BS;
+        // the lanes of the second 64 dims write their upper half first, so
+        // that the eight lanes of a row hit eight different bank groups
+        const uint4 lo = make_uint4(c0.x, c0.y, c1.x, c1.y), hi = make_uint4(c2.x, c2.y, c3.x, c3.y);
+        const bool sw = pc >= 4;
+        *reinterpret_cast<uint4*>(dst + sw128_offset(BS, key, 16 * pc + (sw ? 8 : 0))) = sw ? hi : lo;
+        *reinterpret_cast<uint4*>(dst + sw128_offset(BS, key, 16 * pc + (sw ? 0 : 8))) = sw ? lo : hi;
+      }
     } else {
       constexpr int kRows = (2 * BS + kLoaders - 1) / kLoaders;
 #pragma unroll
@@ -605,16 +648,8 @@ __device__ void tc_loader(const ForwardArgs& a, unsigned char* smem, const TcPla
           const int r = lw + (q0 + q) * kLoaders;
           const int key = r < BS ? r : r - BS;
           const int64_t off = q0 + q < kRows && r < 2 * BS ? koff[key] : -1;
-          float sc = 1.f;
-          if constexpr (kT == SA_DTYPE_E4M3 || kT == SA_DTYPE_INT8) {
-            // off / (page_size * 128) numbers the (page, kv head); a pool of
-            // 2^32 rows of 128 codes would not fit the device
-            if (off >= 0)
-              sc = __ldg((r < BS ? a.k_scales : a.v_scales) +
-                         static_cast<uint32_t>(off >> 7) / static_cast<uint32_t>(a.page_size));
-          }
           kr[q] = off >= 0
-                      ? ld_kv4_bf16<kT>(r < BS ? a.k_pages : a.v_pages, off + 4 * lane, sc)
+                      ? ld_kv4_bf16<kT>(r < BS ? a.k_pages : a.v_pages, off + 4 * lane)
                       : make_uint2(0u, 0u);
         }
 #pragma unroll
