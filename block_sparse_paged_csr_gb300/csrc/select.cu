@@ -605,6 +605,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) block_score_tile_kernel(const
   using L = TileSmem<kG>;
   extern __shared__ __align__(16) unsigned char s_raw[];
   int* ids = reinterpret_cast<int*>(s_raw + L::kIds);
+  __shared__ uint64_t s_bar[2];                        // the two buffers' bounds are there
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, c = lane & 3;
   const int d = a.head_dim;
@@ -626,37 +627,40 @@ __global__ void __launch_bounds__(kTileThreads, 2) block_score_tile_kernel(const
   const int j0 = chunk * kChunk;
   if (j0 >= nmax || nmax <= a.topk) return;
   const int j1 = min(j0 + kChunk, nmax);
-  for (int j = tid; j < kChunk; j += kTileThreads)
-    ids[j] = j0 + j < j1 ? bound_row(a, b, j0 + j) : -1;
+  if (tid < 2) mbar_init(s_bar + tid, kTileThreads / 32);
+  if (tid < 32) fence_mbar_init();
   bool all_rows = true;                                // every block of the chunk has its row
-  for (int j = tid; j < j1 - j0; j += kTileThreads) all_rows = all_rows && ids[j] >= 0;
+  for (int j = tid; j < kChunk; j += kTileThreads) {
+    const int id = j0 + j < j1 ? bound_row(a, b, j0 + j) : -1;
+    ids[j] = id;
+    all_rows = all_rows && (id >= 0 || j0 + j >= j1);
+  }
+  // channels past d: their weights are zero, so the bounds only have to be numbers
+  for (int x = tid; d < 32 * kG && x < 2 * kTileB * 8 * kG; x += kTileThreads) {
+    const int at = x % (8 * kG);
+    if (at % (4 * kG) * 8 >= d)
+      *reinterpret_cast<uint4*>(s_raw + x / (8 * kG) * L::kRow + at * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
   all_rows = __syncthreads_and(all_rows);
 
-  // a tile of bounds: 16-byte pieces, lo then hi, channels past d zero; a
-  // thread's piece of a row is always the same
-  constexpr int kPieces = 8 * kG;                      // per row (lo and hi)
-  constexpr int kRowStep = kTileThreads / kPieces;
-  const int p_row = tid / kPieces, p_at = tid % kPieces;
-  const int p_hi = p_at >= 4 * kG, p_ch = (p_at - p_hi * 4 * kG) * 8;
-  const uint16_t* p_src = a.bounds + static_cast<int64_t>(h) * 2 * d + p_hi * d + p_ch;
-  const int64_t id_step = static_cast<int64_t>(a.hkv) * 2 * d;
+  // A tile of bounds: a warp sends for 16 rows, a lane for the lo or the hi half
+  // of one.  Blocks without a row keep what the buffer holds: their scores are
+  // not taken from the MMA.
+  const uint32_t half_bytes = 2u * static_cast<uint32_t>(d);
   auto load_tile = [&](int t) {
-    unsigned char* dst = s_raw + (t & 1) * L::kBuf + p_row * L::kRow + p_at * 16;
-    const int* id_at = ids + t * kTileB + p_row;
-#pragma unroll
-    for (int r = 0; r < kTileB; r += kRowStep, dst += kRowStep * L::kRow) {
-      const int id = id_at[r];
-      if (id >= 0 && p_ch < d)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)),
-                     "l"(p_src + id * id_step)
-                     : "memory");
-      else
-        *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
+    const int r = 16 * warp + (lane & 15), hi = lane >> 4;
+    const int id = ids[t * kTileB + r];
+    const unsigned present = __ballot_sync(0xffffffffu, id >= 0);
+    uint64_t* bar = s_bar + (t & 1);
+    if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(present)) * half_bytes);
+    __syncwarp();
+    if (id >= 0)
+      bulk_g2s(s_raw + (t & 1) * L::kBuf + r * L::kRow + hi * 64 * kG,
+               a.bounds + ((static_cast<int64_t>(id) * a.hkv + h) * 2 + hi) * d, half_bytes, bar);
   };
   const int tiles = (j1 - j0 + kTileB - 1) / kTileB;
   load_tile(0);
+  if (tiles > 1) load_tile(1);
 
   // weights of queries i0 + 16 warp + g and + 8, channels 32 x + 8 c + 0..7
   uint32_t ahi[2][kG][2][4], alo[2][kG][2][4];         // [lo, hi bound][group][k-step][fragment]
@@ -695,14 +699,12 @@ __global__ void __launch_bounds__(kTileThreads, 2) block_score_tile_kernel(const
               static_cast<int64_t>(there ? (iq[rr] - w0) * a.hkv + h : 0) * a.stride;
   }
 
+  bool late = false;                                   // a wait ran out: send no more
   for (int t = 0; t < tiles; ++t) {
-    if (t + 1 < tiles) {
-      load_tile(t + 1);
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
-    } else {
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (!mbar_wait_bounded(s_bar + (t & 1), (t >> 1) & 1)) {
+      if (lane == 0) report(a.status, SA_ERR_DEVICE_TIMEOUT);
+      late = true;
     }
-    __syncthreads();
     const unsigned char* buf = s_raw + (t & 1) * L::kBuf;
 #pragma unroll 1
     for (int n = 0; n < kTileB / 16; ++n) {
@@ -763,40 +765,74 @@ __global__ void __launch_bounds__(kTileThreads, 2) block_score_tile_kernel(const
         }
       }
     }
-    __syncthreads();
+    if (__syncthreads_or(late)) {                      // (and the buffer is read)
+      // (the copies in flight end before the CTA does)
+      mbar_wait_bounded(s_bar + (t & 1), (t >> 1) & 1);
+      if (t + 1 < tiles) mbar_wait_bounded(s_bar + ((t + 1) & 1), ((t + 1) >> 1) & 1);
+      return;
+    }
+    if (t + 2 < tiles) load_tile(t + 2);
   }
-  // eps of the chunk for every query
+  // eps of the chunk for every query: the sum of |weight| times the largest
+  // |bound|.  M is never positive and P never negative, so it is the score of a
+  // block of those maxima, negated where they meet M: one more column.
   const uint16_t* mx =
       a.maxima + ((static_cast<int64_t>(b) * a.hkv + h) * a.chunks + chunk) * 2 * d;
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int half = 0; half < 2; ++half)
+#pragma unroll
+    for (int x = 0; x < kG; ++x) {
+      const int ch = 32 * x + 8 * c;
+      uint4 u = make_uint4(0u, 0u, 0u, 0u);
+      if (g == 0 && ch < d) {
+        const uint32_t sign = half == 0 ? 0x80008000u : 0u;
+        u = __ldg(reinterpret_cast<const uint4*>(mx + half * d + ch));
+        u = make_uint4(u.x ^ sign, u.y ^ sign, u.z ^ sign, u.w ^ sign);
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t b0 = k ? u.z : u.x, b1 = k ? u.w : u.y;
+        mma_bf16(sum, ahi[half][x][k][0], ahi[half][x][k][1], ahi[half][x][k][2],
+                 ahi[half][x][k][3], b0, b1);
+        mma_bf16(sum, alo[half][x][k][0], alo[half][x][k][1], alo[half][x][k][2],
+                 alo[half][x][k][3], b0, b1);
+      }
+    }
 #pragma unroll
   for (int rr = 0; rr < 2; ++rr) {
-    float l1 = 0.f;
-    bool huge = false;
+    // (column 0 is the first lane's; this sum's own error is below 2^-10)
+    float l1 = __shfl_sync(0xffffffffu, sum[2 * rr], lane & 28) * (1.f + 0x1p-10f);
+    if (__any_sync(0xffffffffu, !(l1 < INFINITY))) {
+      // weights that are not numbers or past bf16's range: channel by channel
+      l1 = 0.f;
+      bool huge = false;
 #pragma unroll
-    for (int half = 0; half < 2; ++half)
+      for (int half = 0; half < 2; ++half)
 #pragma unroll
-      for (int x = 0; x < kG; ++x) {
-        const int ch = 32 * x + 8 * c;
-        if (ch >= d) continue;
-        const uint4 m4 = __ldg(reinterpret_cast<const uint4*>(mx + half * d + ch));
-        const uint32_t m[4] = {m4.x, m4.y, m4.z, m4.w};
+        for (int x = 0; x < kG; ++x) {
+          const int ch = 32 * x + 8 * c;
+          if (ch >= d) continue;
+          const uint4 m4 = __ldg(reinterpret_cast<const uint4*>(mx + half * d + ch));
+          const uint32_t m[4] = {m4.x, m4.y, m4.z, m4.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t hi = ahi[half][x][e >> 1][2 * (e & 1) + rr];
-          const uint32_t lo = alo[half][x][e >> 1][2 * (e & 1) + rr];
-          const float a0 = fabsf(__uint_as_float(hi << 16) + __uint_as_float(lo << 16));
-          const float a1 = fabsf(__uint_as_float(hi & 0xFFFF0000u) +
-                                 __uint_as_float(lo & 0xFFFF0000u));
-          l1 += a0 < INFINITY ? a0 * __uint_as_float(m[e] << 16) : 0.f;
-          l1 += a1 < INFINITY ? a1 * __uint_as_float(m[e] & 0xFFFF0000u) : 0.f;
-          // (a weight past bf16's range has an infinite part and an infinite
-          // remainder of the other sign; an infinite weight's remainder is NaN)
-          huge = huge || huge_part(hi, lo) || huge_part(hi >> 16, lo >> 16);
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t hi = ahi[half][x][e >> 1][2 * (e & 1) + rr];
+            const uint32_t lo = alo[half][x][e >> 1][2 * (e & 1) + rr];
+            const float a0 = fabsf(__uint_as_float(hi << 16) + __uint_as_float(lo << 16));
+            const float a1 = fabsf(__uint_as_float(hi & 0xFFFF0000u) +
+                                   __uint_as_float(lo & 0xFFFF0000u));
+            l1 += a0 < INFINITY ? a0 * __uint_as_float(m[e] << 16) : 0.f;
+            l1 += a1 < INFINITY ? a1 * __uint_as_float(m[e] & 0xFFFF0000u) : 0.f;
+            // (a weight past bf16's range has an infinite part and an infinite
+            // remainder of the other sign; an infinite weight's remainder is NaN)
+            huge = huge || huge_part(hi, lo) || huge_part(hi >> 16, lo >> 16);
+          }
         }
-      }
-    if (huge) l1 = INFINITY;
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+      if (huge) l1 = INFINITY;
+      l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    }
     if (c == 0 && iq[rr] < c1 && iq[rr] >= w0 && iq[rr] < w1)
       a.eps[static_cast<int64_t>((iq[rr] - w0) * a.hkv + h) * a.chunks + chunk] =
           l1 * score_eps(4 * kG + 1, a.qhead, 0x1p-18f);
