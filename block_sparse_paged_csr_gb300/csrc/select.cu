@@ -31,6 +31,7 @@ namespace {
 constexpr int kScoreThreads = 256;
 constexpr int kScoreWarps = kScoreThreads / 32;
 constexpr int kChunk = 256;            // blocks per CTA of the score kernels
+constexpr int kSpan = 2;               // chunks per CTA of the score kernel
 constexpr int kTileQ = 64;             // queries per CTA of the tile kernel
 constexpr int kTileThreads = 128;
 constexpr int kTileB = 64;             // blocks in flight there
@@ -268,8 +269,9 @@ block_score_kernel(const SelectArgs a) {
   const int d = a.head_dim;
   // the CTA's first query (kNQ = 1: every query; else every kNQ-th of its
   // sequence), head and chunk
-  const unsigned unit = blockIdx.x / static_cast<unsigned>(a.chunks);
-  const int chunk = static_cast<int>(blockIdx.x - unit * static_cast<unsigned>(a.chunks));
+  const unsigned spans = static_cast<unsigned>((a.chunks + kSpan - 1) / kSpan);
+  const unsigned unit = blockIdx.x / spans;
+  const int chunk = static_cast<int>(blockIdx.x - unit * spans) * kSpan;
   const unsigned row = static_cast<unsigned>(a.row0) + unit;
   griddep_launch_dependents();
   if (tid < kScoreWarps * kRing) mbar_init(&s_bar[0][0] + tid, 1);
@@ -293,14 +295,15 @@ block_score_kernel(const SelectArgs a) {
   }
   // (a row that takes every block it sees needs no scores)
   if (j0 >= nmax || nmax <= a.topk) return;
-  const int j1 = min(j0 + kChunk, nmax);
+  const int j1 = min(j0 + kSpan * kChunk, nmax);
   // the warp's blocks: stage t holds blocks j0 + 8 (kScoreWarps t + warp) ..;
-  // lane l has the row of block l & 7 of stage l / 8
-  static_assert(kStages == 4, "a row id per lane");
-  int ids;
-  {
-    const int j = j0 + kGroup * (kScoreWarps * (lane >> 3) + warp) + (lane & 7);
-    ids = j < j1 ? bound_row(a, rv.b, j) : -1;
+  // lane l has the row of block l & 7 of stages l / 8 and l / 8 + 4
+  static_assert(kStages == 4, "a row id per lane and chunk");
+  int ids[kSpan];
+#pragma unroll
+  for (int x = 0; x < kSpan; ++x) {
+    const int j = j0 + kChunk * x + kGroup * (kScoreWarps * (lane >> 3) + warp) + (lane & 7);
+    ids[x] = j < j1 ? bound_row(a, rv.b, j) : -1;
   }
   const int row_bytes = score_row_bytes(d);
   unsigned char* mine = s_rows + warp * kRing * kGroup * row_bytes;
@@ -309,7 +312,8 @@ block_score_kernel(const SelectArgs a) {
   __syncthreads();                                     // the barriers are there
   // rows of stage t in flight
   auto send = [&](int t) {
-    const bool there = (lane >> 3) == t && ids >= 0;
+    const int id = t < kStages ? ids[0] : ids[1];
+    const bool there = (lane >> 3) == t % kStages && id >= 0;
     const unsigned present = __ballot_sync(0xffffffffu, there);
     uint64_t* bar = &s_bar[warp][t % kRing];
     if (lane == 0)
@@ -318,7 +322,7 @@ block_score_kernel(const SelectArgs a) {
     __syncwarp();
     if (there)
       bulk_g2s(mine + ((t % kRing) * kGroup + (lane & 7)) * row_bytes,
-               a.bounds + (static_cast<int64_t>(ids) * a.hkv + rv.h) * 2 * d,
+               a.bounds + (static_cast<int64_t>(id) * a.hkv + rv.h) * 2 * d,
                4u * static_cast<uint32_t>(d), bar);
   };
 #pragma unroll
@@ -425,8 +429,9 @@ block_score_kernel(const SelectArgs a) {
           mma_bf16(mag[k], a0, a1, a2, a3, v[2 * k], v[2 * k + 1]);
         }
       }
-      const int id0 = __shfl_sync(0xffffffffu, ids, 8 * st + 2 * c);
-      const int id1 = __shfl_sync(0xffffffffu, ids, 8 * st + 2 * c + 1);
+      const int id = st < kStages ? ids[0] : ids[1];
+      const int id0 = __shfl_sync(0xffffffffu, id, 8 * (st % kStages) + 2 * c);
+      const int id1 = __shfl_sync(0xffffffffu, id, 8 * (st % kStages) + 2 * c + 1);
       // a query's score: its three rows' sums, of columns 2 c and 2 c + 1
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -488,8 +493,9 @@ block_score_kernel(const SelectArgs a) {
   if (tid < nq) {
     float m = 0.f;
     for (int w = 0; w < kScoreWarps; ++w) m = fmaxf(m, s_l1[tid][w]);
-    a.eps[(static_cast<int64_t>(unit) + static_cast<int64_t>(tid) * a.hkv) * a.chunks + chunk] =
-        m * score_eps(kT + 2, a.qhead, 0x1p-24f);
+    for (int x = chunk; x < min(chunk + kSpan, a.chunks); ++x)
+      a.eps[(static_cast<int64_t>(unit) + static_cast<int64_t>(tid) * a.hkv) * a.chunks + x] =
+          m * score_eps(kT + 2, a.qhead, 0x1p-24f);
   }
 }
 
@@ -1305,7 +1311,8 @@ cudaError_t launch_score(const SelectArgs& a, cudaStream_t s) {
     static SmemLimit limit;
     const cudaError_t err = limit.raise(reinterpret_cast<const void*>(fn), smem);
     if (err != cudaSuccess) return err;
-    fn<<<static_cast<unsigned>(a.rows * a.chunks), kScoreThreads, smem, s>>>(a);
+    const int64_t spans = (a.chunks + kSpan - 1) / kSpan;
+    fn<<<static_cast<unsigned>(a.rows * spans), kScoreThreads, smem, s>>>(a);
     return cudaGetLastError();
   });
 }
