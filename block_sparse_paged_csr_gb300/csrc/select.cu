@@ -31,7 +31,6 @@ namespace {
 constexpr int kScoreThreads = 256;
 constexpr int kScoreWarps = kScoreThreads / 32;
 constexpr int kChunk = 256;            // blocks per CTA of the score kernels
-constexpr int kSpan = 2;               // chunks per CTA of the score kernel
 constexpr int kTileQ = 64;             // queries per CTA of the tile kernel
 constexpr int kTileThreads = 128;
 constexpr int kTileB = 64;             // blocks in flight there
@@ -253,7 +252,11 @@ __host__ __device__ constexpr int score_row_bytes(int d) { return (4 * d + 127) 
 // 128).
 __host__ __device__ constexpr int score_ring(int kT) { return kT <= 8 ? 3 : 2; }
 
-template <int kT, int kNQ, bool kQ16>
+//   kSpan: chunks per CTA.  A CTA's start (sequence, row ids, weights) takes about
+//   as long as a chunk's bounds, so two where there are CTAs enough: 128
+//   sequences of up to 131072 keys, 64-key blocks, 8 kv heads take 178 us instead
+//   of 197, but one of them 18.5 us instead of 14.4.
+template <int kT, int kNQ, int kSpan, bool kQ16>
 __global__ void __launch_bounds__(kScoreThreads, kT <= 8 && kNQ == 1 ? 2 : 1)
 block_score_kernel(const SelectArgs a) {
   constexpr int kHalves = kNQ > 2 ? 2 : 1;             // A rows 0-7, 8-15
@@ -297,8 +300,8 @@ block_score_kernel(const SelectArgs a) {
   if (j0 >= nmax || nmax <= a.topk) return;
   const int j1 = min(j0 + kSpan * kChunk, nmax);
   // the warp's blocks: stage t holds blocks j0 + 8 (kScoreWarps t + warp) ..;
-  // lane l has the row of block l & 7 of stages l / 8 and l / 8 + 4
-  static_assert(kStages == 4, "a row id per lane and chunk");
+  // lane l has the row of block l & 7 of stage l / 8 of each chunk
+  static_assert(kStages == 4 && kSpan <= 2, "a row id per lane and chunk");
   int ids[kSpan];
 #pragma unroll
   for (int x = 0; x < kSpan; ++x) {
@@ -312,7 +315,7 @@ block_score_kernel(const SelectArgs a) {
   __syncthreads();                                     // the barriers are there
   // rows of stage t in flight
   auto send = [&](int t) {
-    const int id = t < kStages ? ids[0] : ids[1];
+    const int id = ids[kSpan == 1 || t < kStages ? 0 : 1];
     const bool there = (lane >> 3) == t % kStages && id >= 0;
     const unsigned present = __ballot_sync(0xffffffffu, there);
     uint64_t* bar = &s_bar[warp][t % kRing];
@@ -429,7 +432,7 @@ block_score_kernel(const SelectArgs a) {
           mma_bf16(mag[k], a0, a1, a2, a3, v[2 * k], v[2 * k + 1]);
         }
       }
-      const int id = st < kStages ? ids[0] : ids[1];
+      const int id = ids[kSpan == 1 || st < kStages ? 0 : 1];
       const int id0 = __shfl_sync(0xffffffffu, id, 8 * (st % kStages) + 2 * c);
       const int id1 = __shfl_sync(0xffffffffu, id, 8 * (st % kStages) + 2 * c + 1);
       // a query's score: its three rows' sums, of columns 2 c and 2 c + 1
@@ -1303,10 +1306,10 @@ auto by_q_type(const SelectArgs& a, F f) {
   return a.q_bf16 ? f(std::true_type{}) : f(std::false_type{});
 }
 
-template <int kT, int kNQ>
+template <int kT, int kNQ, int kSpan>
 cudaError_t launch_score(const SelectArgs& a, cudaStream_t s) {
   return by_q_type(a, [&](auto q16) {
-    auto fn = block_score_kernel<kT, kNQ, decltype(q16)::value>;
+    auto fn = block_score_kernel<kT, kNQ, kSpan, decltype(q16)::value>;
     const int smem = kScoreWarps * score_ring(kT) * kGroup * score_row_bytes(a.head_dim);
     static SmemLimit limit;
     const cudaError_t err = limit.raise(reinterpret_cast<const void*>(fn), smem);
@@ -1319,7 +1322,10 @@ cudaError_t launch_score(const SelectArgs& a, cudaStream_t s) {
 
 template <int kT>
 cudaError_t launch_score_nq(const SelectArgs& a, bool one, cudaStream_t s) {
-  return one ? launch_score<kT, 1>(a, s) : launch_score<kT, 5>(a, s);
+  if (!one) return launch_score<kT, 5, 1>(a, s);
+  // (two CTAs per SM are there at a time)
+  return a.rows * a.chunks <= 2 * device_sm_count() ? launch_score<kT, 1, 1>(a, s)
+                                                    : launch_score<kT, 1, 2>(a, s);
 }
 
 template <int kG>
