@@ -170,7 +170,7 @@ __device__ __forceinline__ void store8(void* pages, int64_t off, const float (&x
 // magnitude and the pass that writes codes, so a page of 64 x 128 is read
 // once.
 template <int kType, bool kSrcBf16, int kItemWarps>
-__global__ void __launch_bounds__(kThreads, 4) store_kv_kernel(const StoreArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) store_kv_kernel(const StoreArgs a) {
   constexpr bool kCodes = kType == kE4m3 || kType == kInt8;
   constexpr int kT = kItemWarps * 32;                 // threads per item
   constexpr int kHeld = kItemWarps == 1 ? 2 : 4;

@@ -440,6 +440,16 @@ def test_select_many_blocks(n):
     run_select(*p, 16, 64)
 
 
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [8, 32, 64, 128, 256])
+def test_select_many_sequences(d, act):
+    """More (sequence, head, 256 blocks) units than are resident at a time, an
+    odd number of them per row, single queries."""
+    lens = [(700 * 16 - 37 * i) if i % 7 else 5 * i for i in range(90)]
+    p = problem([1] * 90, lens, 4, 2, d, 16, act, seed=d + 1)
+    run_select(*p, 16, 33)
+
+
 def test_select_missing_blocks_and_bad_rows():
     q, bounds, rows, cu, lens = problem([2, 1], [1600, 800], 4, 2, 64, 16, seed=11)
     rows[0, ::3] = -1
