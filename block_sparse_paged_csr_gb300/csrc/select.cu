@@ -1381,8 +1381,10 @@ cudaError_t launch_pick(const SelectArgs& a, bool behind_scores, cudaStream_t s)
 // `longest`: most queries of one sequence.
 cudaError_t launch_select(SelectArgs a, const SelectLayout& l, int64_t longest, cudaStream_t s) {
   cudaError_t err;
-  // the tile kernel from a quarter of a tile of queries on
-  const bool tile = longest >= kTileQ / 4 && a.head_dim <= 128;
+  // The tile kernel from 8 queries of a sequence on, where its weights fit in
+  // registers (16 sequences, 8 heads of 128 channels, 256 blocks: 4 queries 41 us
+  // with it, 31 us without; 8: 43 and 51; 32: 47 and 147).
+  const bool tile = longest >= kTileQ / 8 && a.head_dim <= 128;
   a.slots = slot_base(a.tq, a.batch, kTileQ);
   const int64_t all = a.tq * a.hkv;
   for (int64_t r0 = 0; r0 < all; r0 += l.rows) {
@@ -1403,6 +1405,9 @@ cudaError_t launch_select(SelectArgs a, const SelectLayout& l, int64_t longest, 
                                   : launch_score_nq<16>(a, one, s);
       if (err != cudaSuccess) return err;
     }
+    // A warp per row while a row's keys fit in its registers: 65536 rows of 256
+    // blocks take 93 us, 700 us with a CTA of eight warps per row; 32 rows of 512
+    // blocks the same time either way (13 and 14 us with their scores).
     if (a.msb <= 256) err = launch_pick<1, 8>(a, a.msb > a.topk, s);
     else if (a.msb <= 512) err = launch_pick<1, 16>(a, a.msb > a.topk, s);
     else if (a.msb <= 2048) err = launch_pick<8, 8>(a, a.msb > a.topk, s);

@@ -274,7 +274,8 @@ def outward(x, up):
 
 @pytest.mark.parametrize("kind", ["e4m3", "int8", "bf16", "f32"])
 @pytest.mark.parametrize("hkv,d,ps,bs", [(2, 32, 16, 32), (1, 128, 16, 64), (3, 64, 8, 128),
-                                         (1, 256, 32, 32), (2, 48, 12, 36), (1, 16, 4, 16)])
+                                         (1, 256, 32, 32), (2, 48, 12, 36), (1, 16, 4, 16),
+                                         (2, 48, 32, 64), (1, 128, 64, 128)])
 def test_bounds(kind, hkv, d, ps, bs):
     rng = np.random.default_rng(6)
     qo = [1, 0, 70, 5, 1, 200]
