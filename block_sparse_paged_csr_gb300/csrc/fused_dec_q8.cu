@@ -5,8 +5,8 @@
 // Work is cut as in the kernel for f32 and bf16 caches (fused_dec.cu): a
 // "piece" is a range of ranks of one (query, kv head) pair, normally all of
 // them; its kept blocks stream through shared memory, 128 keys a stage (two
-// chunks of at most 64 keys of one block), under one online softmax; pieces of a cut pair meet in a small global scratch and
-// the last one to finish merges them.
+// chunks of at most 64 keys of one block), under one online softmax; pieces of a
+// cut pair meet in a small global scratch and the last one to finish merges them.
 //
 // Half the bytes per key of a bf16 cache leave half the time per stage: what
 // bounds the kernel is no longer only HBM but how fast one SM can issue a
@@ -25,6 +25,11 @@
 //   * codes go from shared memory to the MMA's registers as they lie: see
 //     consumer().
 // Roles: warp 0 metadata, warps 1..NL loads, then merge, then consumers.
+// Measured, with the index build beside it: 128 sequences of 65536 to 131072 keys,
+// 64 blocks of 64, 64 heads on 8, pages of 16, e4m3 (970 MB): 200 us, 4.9 TB/s
+// (309 us with work cut as in the kernel for wider caches); 32 heads on 8, 64 sequences, 16
+// blocks (124 MB): 48 us.  About 1400 cycles of an SM per 128 keys, of which the
+// copies would need 800: conversions, softmax and MMA issue bound it.
 #include <cstdint>
 #include <cuda.h>
 
