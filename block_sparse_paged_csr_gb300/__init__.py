@@ -99,8 +99,16 @@ def _raw_stream(device):
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _host_ptr(a: np.ndarray) -> int:
-    return a.__array_interface__["data"][0]
+_HostWords = ctypes.c_int64 * 1
+
+
+def _host_ptr(a: np.ndarray):
+    """The address of a host array's data, as a pointer argument (a view of its
+    buffer where it gives one, which is the quicker way)."""
+    try:
+        return _HostWords.from_buffer(a)
+    except (TypeError, ValueError):      # read-only, or shorter than a word
+        return a.__array_interface__["data"][0]
 
 
 def _host_i64(a) -> np.ndarray:
@@ -130,6 +138,17 @@ def _require(t, dtype, name, device=None):
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     return t
+
+
+def _alike(index, dtype, *tensors) -> bool:
+    """Whether all are contiguous CUDA tensors of device ``index`` and ``dtype``:
+    the usual case of the checks below, in few calls (a decode step's call is
+    shorter on the GPU than its checks on the host).  Where not, the checks
+    one by one say what is wrong."""
+    for t in tensors:
+        if t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+            return False
+    return True
 
 
 def sa_status_string(code: int) -> str:
@@ -296,7 +315,8 @@ class _Scaled:
 def _scaled(q, k_pages, v_pages, k_scales, v_scales):
     """Checks of a call over an 8-bit cache; None for the other cache types,
     which take no scales."""
-    if k_pages.dtype not in (torch.float8_e4m3fn, torch.int8):
+    dtype = k_pages.dtype
+    if dtype is not torch.float8_e4m3fn and dtype is not torch.int8:
         if k_scales is not None or v_scales is not None:
             raise ValueError(f"a {k_pages.dtype} cache has no scales")
         return None
@@ -304,8 +324,9 @@ def _scaled(q, k_pages, v_pages, k_scales, v_scales):
     if q.dtype not in _ACT_DTYPES:
         raise TypeError(f"q must be float32 or bfloat16, got {q.dtype}")
     _require(q, q.dtype, "q")
-    _require(k_pages, k_pages.dtype, "k_pages", q.device)
-    _require(v_pages, k_pages.dtype, "v_pages", q.device)
+    if not _alike(q.get_device(), dtype, k_pages, v_pages):
+        _require(k_pages, dtype, "k_pages", q.device)
+        _require(v_pages, dtype, "v_pages", q.device)
     if v_pages.shape != k_pages.shape:
         raise ValueError("k_pages and v_pages must have one shape")
     ks, vs = _scales(k_scales, k_pages, "k_scales"), _scales(v_scales, v_pages, "v_scales")
@@ -508,10 +529,10 @@ def sa_attention(q, k_pages, v_pages, selected, cu_seqlens_q_host, cu_seqlens_q,
     else:
         _check_out(out, x.out_dtype)
     dev = q.device
-    tq, hkv_s, topk = (int(x) for x in selected.shape)
+    tq, hkv_s, topk = selected.shape
     cu_h = _host_i64(cu_seqlens_q_host)
     batch = cu_h.size - 1
-    max_pages = int(block_tables.shape[1])
+    max_pages = block_tables.shape[1]
     if index is None:
         index = allocate_index(tq, hkv_s, topk, max(batch, 1), max_pages, block_size, page_size,
                                dev)
@@ -584,10 +605,15 @@ class AttentionGraph:
 
 def _on(dev, fn, *args) -> int:
     """fn(*args) with the device of the call's tensors as the current one."""
-    if dev.index is None or dev.index == torch.cuda.current_device():
+    index = dev.index
+    if index is None or index == _current_device():
         return fn(*args)
     with torch.cuda.device(dev):
         return fn(*args)
+
+
+# (the tensors at hand are CUDA tensors, so CUDA is initialised)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 _CACHE_DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16,
@@ -607,12 +633,18 @@ def _cache_dtype(pages, name):
 
 def _scales(scales, pages, name):
     """The scales [num_pages, hkv] of an 8-bit cache (None for the others)."""
-    if pages.dtype not in (torch.float8_e4m3fn, torch.int8):
+    if pages.dtype is not torch.float8_e4m3fn and pages.dtype is not torch.int8:
         if scales is not None:
             raise ValueError(f"{name}: a {pages.dtype} cache has no scales")
         return None
     if scales is None:
         raise ValueError(f"{name} [num_pages, hkv] are needed with a {pages.dtype} cache")
+    try:
+        if (scales.shape == tuple(pages.shape)[:2] and
+                _alike(pages.get_device(), torch.float32, scales)):
+            return scales
+    except AttributeError:
+        pass
     _require(scales, torch.float32, name, pages.device)
     if scales.shape != pages.shape[:2]:
         raise ValueError(f"{name} must be {tuple(pages.shape[:2])}, got {tuple(scales.shape)}")
@@ -623,6 +655,14 @@ def _batch_args(cu_seqlens_q_host, cu_seqlens_q, used_kv_lens, tables, dev, name
     """Host prefix lengths after the checks that sequences and tables agree."""
     cu_h = _host_i64(cu_seqlens_q_host)
     batch = cu_h.size - 1
+    try:
+        if (_alike(dev.index, torch.int32, used_kv_lens, *tables) and
+                _alike(dev.index, torch.int64, cu_seqlens_q) and
+                cu_seqlens_q.numel() == batch + 1 and used_kv_lens.numel() == batch and
+                all([t.dim() == 2 and t.shape[0] == batch for t in tables])):
+            return cu_h, batch
+    except AttributeError:
+        pass
     _require(cu_seqlens_q, torch.int64, "cu_seqlens_q", dev)
     _require(used_kv_lens, torch.int32, "used_kv_lens", dev)
     if cu_seqlens_q.numel() != cu_h.size or used_kv_lens.numel() != batch:
@@ -650,13 +690,49 @@ def sa_store_kv(k, v, k_pages, v_pages, block_tables, cu_seqlens_q_host, cu_seql
     and ``v_scales`` [num_pages, hkv], renewed with the pages (powers of two;
     see sa.h).  ``status``: a zeroed int64 CUDA tensor that keeps the first
     device-detected error."""
-    code = _cache_dtype(k_pages, "k_pages")
+    if not _store_args_usual(k, v, k_pages, v_pages, k_scales, v_scales):
+        _check_store_args(k, v, k_pages, v_pages, k_scales, v_scales)
+    dev = k_pages.device
+    num_pages, hkv, page_size, d = k_pages.shape
+    cu_h, batch = _batch_args(cu_seqlens_q_host, cu_seqlens_q, used_kv_lens, (block_tables,), dev,
+                              ("block_tables",))
+    ks0, ks1, _ = k.stride()
+    vs0, vs1, _ = v.stride()
+    _check(_on(dev, _native.load().sa_store_kv, k.data_ptr(), v.data_ptr(), _ACT_DTYPES[k.dtype],
+               ks0, ks1, vs0, vs1, k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scales),
+               _ptr(v_scales), num_pages, _CACHE_DTYPES[k_pages.dtype], block_tables.data_ptr(),
+               block_tables.shape[1], _host_ptr(cu_h), cu_seqlens_q.data_ptr(), batch, k.shape[0],
+               used_kv_lens.data_ptr(), hkv, d, page_size, _status_word(status, dev),
+               _stream(stream, dev)), "sa_store_kv")
+
+
+def _store_args_usual(k, v, k_pages, v_pages, k_scales, v_scales) -> bool:
+    try:
+        dtype, act, shape, new = k_pages.dtype, k.dtype, k_pages.shape, k.shape
+        index = k_pages.get_device()
+        num_pages, hkv, _, d = shape
+        tq, heads, channels = new
+        if not (index >= 0 and act in _ACT_DTYPES and v.dtype is act and v.shape == new and
+                heads == hkv and channels == d and k.get_device() == index and
+                v.get_device() == index and k.stride(2) == 1 and v.stride(2) == 1 and
+                v_pages.shape == shape and _alike(index, dtype, k_pages, v_pages)):
+            return False
+        if dtype is torch.float8_e4m3fn or dtype is torch.int8:
+            return (k_scales.shape == (num_pages, hkv) and v_scales.shape == (num_pages, hkv) and
+                    _alike(index, torch.float32, k_scales, v_scales))
+        return dtype in _CACHE_DTYPES and k_scales is None and v_scales is None
+    except (AttributeError, TypeError, ValueError):
+        return False
+
+
+def _check_store_args(k, v, k_pages, v_pages, k_scales, v_scales) -> None:
+    _cache_dtype(k_pages, "k_pages")
     dev = k_pages.device
     _require(k_pages, k_pages.dtype, "k_pages", dev)
     _require(v_pages, k_pages.dtype, "v_pages", dev)
     if v_pages.shape != k_pages.shape:
         raise ValueError("k_pages and v_pages must have one shape")
-    num_pages, hkv, page_size, d = k_pages.shape
+    _, hkv, _, d = k_pages.shape
     for t, name in ((k, "k"), (v, "v")):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
@@ -668,16 +744,8 @@ def sa_store_kv(k, v, k_pages, v_pages, block_tables, cu_seqlens_q_host, cu_seql
             raise ValueError(f"{name} must be [tq, {hkv}, {d}], got {tuple(t.shape)}")
         if t.stride(2) != 1 and t.numel():
             raise ValueError(f"{name}: channels must be contiguous")
-    ks, vs = _scales(k_scales, k_pages, "k_scales"), _scales(v_scales, v_pages, "v_scales")
-    cu_h, batch = _batch_args(cu_seqlens_q_host, cu_seqlens_q, used_kv_lens, (block_tables,), dev,
-                              ("block_tables",))
-    ks0, ks1, _ = k.stride()
-    vs0, vs1, _ = v.stride()
-    _check(_on(dev, _native.load().sa_store_kv, k.data_ptr(), v.data_ptr(), _ACT_DTYPES[k.dtype],
-               ks0, ks1, vs0, vs1, k_pages.data_ptr(), v_pages.data_ptr(), _ptr(ks), _ptr(vs),
-               num_pages, code, block_tables.data_ptr(), block_tables.shape[1], _host_ptr(cu_h),
-               cu_seqlens_q.data_ptr(), batch, k.shape[0], used_kv_lens.data_ptr(), hkv, d,
-               page_size, _status_word(status, dev), _stream(stream, dev)), "sa_store_kv")
+    _scales(k_scales, k_pages, "k_scales")
+    _scales(v_scales, v_pages, "v_scales")
 
 
 def _check_bounds(bounds, hkv, d, dev):
@@ -694,7 +762,7 @@ def sa_block_bounds(k_pages, block_tables, cu_seqlens_q_host, cu_seqlens_q, used
     sequence b.  Returns ``bounds``."""
     code = _cache_dtype(k_pages, "k_pages")
     dev = k_pages.device
-    _require(k_pages, k_pages.dtype, "k_pages", dev)
+    _require(k_pages, k_pages.dtype, "k_pages")
     num_pages, hkv, page_size, d = k_pages.shape
     ks = _scales(k_scales, k_pages, "k_scales")
     _check_bounds(bounds, hkv, d, dev)

@@ -318,14 +318,14 @@ template <int kT>
 cudaError_t launch_cc(const ForwardArgs& a, cudaStream_t stream) {
   const SmemPlan p = plan_smem(a.block_size, a.head_dim, kT);
   const void* fn = reinterpret_cast<const void*>(forward_cc_kernel<kT>);
-  cudaError_t err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(p.total));
+  static SmemLimit limit;
+  static LaunchFacts facts;
+  cudaError_t err = limit.raise(fn, static_cast<int>(p.total));
   if (err != cudaSuccess) return err;
-  err = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout,
-                             cudaSharedmemCarveoutMaxShared);
+  err = facts.prefer_shared(fn);
   if (err != cudaSuccess) return err;
   int per_sm = 0;
-  err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, kThreads, p.total);
+  err = facts.per_sm(fn, kThreads, p.total, &per_sm);
   if (err != cudaSuccess) return err;
   if (per_sm < 1) per_sm = 1;
   int64_t grid = static_cast<int64_t>(device_sm_count()) * per_sm;

@@ -949,13 +949,14 @@ cudaError_t launch_build_index(const IndexArgs& a, int64_t chunks_per_head,
   int per_sm = 0;
   size_t smem = 16 * static_cast<size_t>(a.hkv) + 24 * (static_cast<size_t>(a.hkv) + 1);
   if (args.small) {
-    err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, index_kernel<true>, kThreads, smem);
+    static LaunchFacts facts;
+    const void* small_fn = reinterpret_cast<const void*>(index_kernel<true>);
+    err = facts.per_sm(small_fn, kThreads, smem, &per_sm);
     if (err != cudaSuccess) return err;
     if (seg_ctas > static_cast<int64_t>(per_sm) * sms) args.small = 0;
     // beside a fused decode kernel: an SM keeps one split of L1 and shared
     // memory for all its CTAs, so this kernel asks for the fused kernel's
-    err = cudaFuncSetAttribute(index_kernel<true>, cudaFuncAttributePreferredSharedMemoryCarveout,
-                               cudaSharedmemCarveoutMaxShared);
+    err = facts.prefer_shared(small_fn);
     if (err != cudaSuccess) return err;
   }
   const void* fn = reinterpret_cast<const void*>(index_kernel<true>);
@@ -967,12 +968,13 @@ cudaError_t launch_build_index(const IndexArgs& a, int64_t chunks_per_head,
     fn = reinterpret_cast<const void*>(index_kernel<false>);
     smem = index_smem_bytes(a.msb, a.batch, a.hkv);
     if (smem > 227 * 1024) return cudaErrorNotSupported;
+    static SmemLimit limit;
+    static LaunchFacts facts;
     if (smem > 48 * 1024) {
-      err = cudaFuncSetAttribute(index_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(smem));
+      err = limit.raise(fn, static_cast<int>(smem));
       if (err != cudaSuccess) return err;
     }
-    err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, index_kernel<false>, kThreads, smem);
+    err = facts.per_sm(fn, kThreads, smem, &per_sm);
     if (err != cudaSuccess) return err;
     if (per_sm < 1) return cudaErrorNotSupported;
     nch = chunks_per_head * a.hkv;

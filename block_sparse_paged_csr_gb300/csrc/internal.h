@@ -247,6 +247,42 @@ struct SmemLimit {
   }
 };
 
+// How many CTAs of a kernel fit on an SM at a dynamic shared-memory size, and its
+// wish for the largest share of shared memory: asked for once per device (and
+// size) instead of at every launch, about a microsecond of the host each.
+struct LaunchFacts {
+  std::atomic<uint64_t> blocks[64] = {};               // size + 1 above 16 bits of count
+  std::atomic<bool> carveout[64] = {};
+
+  cudaError_t per_sm(const void* fn, int threads, size_t smem, int* n) {
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    const bool known = dev >= 0 && dev < 64;
+    const uint64_t v = known ? blocks[dev].load(std::memory_order_acquire) : 0;
+    if ((v >> 16) == smem + 1) {
+      *n = static_cast<int>(v & 0xFFFFu);
+      return cudaSuccess;
+    }
+    err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, fn, threads, smem);
+    if (err == cudaSuccess && known)
+      blocks[dev].store((static_cast<uint64_t>(smem + 1) << 16) | static_cast<uint64_t>(*n),
+                        std::memory_order_release);
+    return err;
+  }
+  cudaError_t prefer_shared(const void* fn) {
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    const bool known = dev >= 0 && dev < 64;
+    if (known && carveout[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    err = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared);
+    if (err == cudaSuccess && known) carveout[dev].store(true, std::memory_order_release);
+    return err;
+  }
+};
+
 // The fixed scratch array of sa_build_index_no_alloc on the current device
 // (no_alloc.cu): its device address and size.
 sa_status static_index_scratch(void** ptr, size_t* bytes);
