@@ -244,3 +244,20 @@ def test_scaled_kernel_choice():
                                          sa.PATH_TENSOR_CORE) == "forward_tc_kernel"
         assert sa.sa_forward_kernel_name(80, 2, 8, 64, 128, 128, 64, kind,
                                          sa.PATH_CUDA_CORE) == "forward_cc_kernel"
+
+
+def test_host_pointers():
+    """Host prefix lengths reach the library by the address of their data,
+    writable or not, whatever they come as."""
+    import torch
+
+    import block_sparse_paged_csr_gb300 as sa
+
+    a = np.arange(5, dtype=np.int64)
+    p = sa._host_ptr(a)
+    assert ctypes.addressof(p) == a.ctypes.data
+    a.flags.writeable = False
+    assert sa._host_ptr(a) == a.ctypes.data
+    for x in ([0, 2, 5], np.array([0, 2, 5], np.int32), torch.tensor([0, 2, 5])):
+        h = sa._host_i64(x)
+        assert h.dtype == np.int64 and h.flags.c_contiguous and h.tolist() == [0, 2, 5]
