@@ -1003,44 +1003,36 @@ __device__ __forceinline__ void weights64(const SelectArgs& a, const RowView& rv
   }
 }
 
-// Threads of a CTA: two rows of a warp each (a row whose border has to be
-// settled in f64 takes several times as long, and should not hold others), or
-// one row of eight warps.
-__host__ __device__ constexpr int pick_threads(int warps) { return warps == 1 ? 64 : 32 * warps; }
-
 // The topk of one row: keys in registers (block t * threads + thread),
 // bisection over the keys' range until just k lie above (a dozen counts), the
 // border check against eps, f64 scores where it asks for them, and the ids
-// written in ascending order.  kWarps = 1: a warp per row; else a CTA per row.
+// written in ascending order.  A CTA of one or eight warps per row (two rows of a
+// warp each in a CTA take 92 us instead of 83 in the case below: a row whose border
+// has to be settled in f64 takes several times as long and holds the other's place).
 // What it costs is instructions and the latency of the counts, so the fewest
 // threads that hold a row's keys in registers take it.  65536 rows of 256 blocks,
-// 32 of them chosen: 92 us, of which the 9 % of rows that f32 leaves open take 32,
+// 32 of them chosen: 84 us, of which the 9 % of rows that f32 leaves open take 25,
 // the bisection 18, reading the scores 29; 512 rows of up to 512 blocks, 16
 // chosen: 17.5 us; 1024 rows of up to 2048, 64 chosen: 26 us.  (Cuts by
 // interpolation need as many counts as bisection; border scores four blocks at a
 // time are slower, since most open rows have two or three.)
 template <int kWarps, int kKeys, bool kQ16>
-__global__ void __launch_bounds__(pick_threads(kWarps)) block_pick_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(32 * kWarps) block_pick_kernel(const SelectArgs a) {
   constexpr int kThreads = 32 * kWarps;
-  constexpr int kRowsPerCta = pick_threads(kWarps) / kThreads;
   constexpr int kList = 32;
   extern __shared__ __align__(16) unsigned char s_raw[];
   __shared__ int s_red[2 * kWarps];
-  __shared__ int s_amb[kRowsPerCta][kList];
-  __shared__ int s_namb[kRowsPerCta];
+  __shared__ int s_amb[kList];
+  __shared__ int s_namb;
   __shared__ int s_cnt[kWarps == 1 ? 1 : kKeys * kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int tid = kWarps == 1 ? lane : static_cast<int>(threadIdx.x);
-  const int sub = kWarps == 1 ? warp : 0;              // the CTA's row
-  const int gw = kWarps == 1 ? 0 : warp;               // warp of the row's group
-  const int64_t lrow = static_cast<int64_t>(blockIdx.x) * kRowsPerCta + sub;
-  if (lrow >= a.rows) return;                          // (whole warps; a CTA has one row)
+  const int tid = static_cast<int>(threadIdx.x);
+  const int64_t lrow = blockIdx.x;
   RowGroup<kWarps> grp(s_red);
   const RowView rv = row_view(a, static_cast<unsigned>(a.row0 + lrow), lane);
   const int n = rv.nblk;
   int32_t* out = a.selected + (a.row0 + lrow) * a.topk;
-  const size_t per_row = static_cast<size_t>(2) * a.head_dim * 8 + static_cast<size_t>(a.msb) * 8;
-  double* w64 = reinterpret_cast<double*>(s_raw + sub * per_row);                 // [2 d]
+  double* w64 = reinterpret_cast<double*>(s_raw);                                 // [2 d]
   unsigned long long* key64 =
       reinterpret_cast<unsigned long long*>(w64 + 2 * a.head_dim);                // [msb]
 
@@ -1147,7 +1139,7 @@ __global__ void __launch_bounds__(pick_threads(kWarps)) block_pick_kernel(const 
       const bool exact_tie =
           s_k == s_next && e < INFINITY && (e == 0.f || s_k <= 1u || !(fabsf(fk) < INFINITY));
       int n_in = 0, n_amb = 0;
-      if (tid == 0) s_namb[sub] = 0;
+      if (tid == 0) s_namb = 0;
 #pragma unroll
       for (int t = 0; t < kKeys; ++t) {
         const uint32_t k = key[t];
@@ -1179,13 +1171,13 @@ __global__ void __launch_bounds__(pick_threads(kWarps)) block_pick_kernel(const 
           for (int x = 0; x < kKeys; ++x) kt = x == t ? key[x] : kt;
           unsigned m = __ballot_sync(0xffffffffu, kt == 1u);
           while (m) {
-            const int j = t * kThreads + gw * 32 + __ffs(m) - 1;
+            const int j = t * kThreads + warp * 32 + __ffs(m) - 1;
             m &= m - 1;
             const double sc = score64(a, rv, w64, j, lane);
             if (lane == 0) {
               key64[j] = score_key64(sc);
-              const int at = atomicAdd(&s_namb[sub], 1);
-              if (at < kList) s_amb[sub][at] = j;
+              const int at = atomicAdd(&s_namb, 1);
+              if (at < kList) s_amb[at] = j;
             }
           }
         }
@@ -1194,7 +1186,7 @@ __global__ void __launch_bounds__(pick_threads(kWarps)) block_pick_kernel(const 
       if (!exact_tie && n_amb <= kList) {
         // every warp ranks the list: a block comes in with fewer than `need`
         // better ones
-        const int j = lane < n_amb ? s_amb[sub][lane] : -1;
+        const int j = lane < n_amb ? s_amb[lane] : -1;
         const unsigned long long kj = j >= 0 ? key64[j] : 0ull;
         int rank = 0;
         for (int t = 0; t < n_amb; ++t) {
@@ -1372,8 +1364,8 @@ cudaError_t launch_tile(const SelectArgs& a, cudaStream_t s) {
   err = limit.raise(reinterpret_cast<const void*>(block_score_tile_kernel<kG>), TileSmem<kG>::kTotal);
   if (err != cudaSuccess) return err;
   // The maxima beside the weights, and the tiles' first bounds beside both
-  // (230 -> 219 us for the case above): the weights kernel starts after all earlier work, so the
-  // bounds that the others read meanwhile are there.
+  // (230 -> 219 us for the case of 8192 queries): the weights kernel starts after all
+  // earlier work, so the bounds that the others read meanwhile are there.
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1393,9 +1385,7 @@ cudaError_t launch_tile(const SelectArgs& a, cudaStream_t s) {
 
 template <int kWarps, int kKeys>
 cudaError_t launch_pick(const SelectArgs& a, bool behind_scores, cudaStream_t s) {
-  constexpr int rows = pick_threads(kWarps) / (32 * kWarps);
-  const size_t smem = rows * (static_cast<size_t>(2) * a.head_dim * 8 +
-                              static_cast<size_t>(a.msb) * 8);
+  const size_t smem = static_cast<size_t>(2) * a.head_dim * 8 + static_cast<size_t>(a.msb) * 8;
   return by_q_type(a, [&](auto q16) {
     auto fn = block_pick_kernel<kWarps, kKeys, decltype(q16)::value>;
     if (smem > 32 * 1024) {            // (the default limit counts the static part too)
@@ -1407,8 +1397,8 @@ cudaError_t launch_pick(const SelectArgs& a, bool behind_scores, cudaStream_t s)
     // Behind a score kernel its prologue overlaps that kernel's end.  (Behind
     // another it would overlap work that may still write its inputs.)
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>((a.rows + rows - 1) / rows));
-    cfg.blockDim = dim3(pick_threads(kWarps));
+    cfg.gridDim = dim3(static_cast<unsigned>(a.rows));
+    cfg.blockDim = dim3(32 * kWarps);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -1448,7 +1438,7 @@ cudaError_t launch_select(SelectArgs a, const SelectLayout& l, int64_t longest, 
       if (err != cudaSuccess) return err;
     }
     // A warp per row while a row's keys fit in its registers: 65536 rows of 256
-    // blocks take 93 us, 700 us with a CTA of eight warps per row; 32 rows of 512
+    // blocks take 84 us, 700 us with a CTA of eight warps per row; 32 rows of 512
     // blocks the same time either way (13 and 14 us with their scores).
     if (a.msb <= 256) err = launch_pick<1, 8>(a, a.msb > a.topk, s);
     else if (a.msb <= 512) err = launch_pick<1, 16>(a, a.msb > a.topk, s);
