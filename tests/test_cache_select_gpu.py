@@ -626,3 +626,40 @@ def test_on_another_stream_and_in_a_graph():
         assert torch.equal(sel, ref)
         for x, y in zip(state, want):
             assert torch.equal(x, y)
+
+
+def test_prompts_in_a_row_and_in_a_graph():
+    """Selection for prompts: calls that follow one another on one workspace
+    without a synchronisation, bounds rewritten in between, and a captured call
+    replayed with new queries and bounds."""
+    hkv, d, bs, topk = 2, 128, 16, 12
+    _, bounds, rows, cu, lens = problem([130, 0, 20, 300], [4000, 50, 5200, 9000], 8, hkv, d, bs,
+                                        seed=19)
+    a = (cuda_i(rows, np.int32), cu, cuda_i(cu, np.int64), cuda_i(lens, np.int32), bs, topk, True)
+    gen = torch.Generator(device="cuda").manual_seed(20)
+    n = 12
+    qs = [torch.randn((int(cu[-1]), 8, d), generator=gen, device="cuda") for _ in range(n)]
+    boxes = [make_bounds(bounds.shape[0], hkv, d, gen) for _ in range(n)]
+    ref = []
+    for q, box in zip(qs, boxes):
+        ref.append(sa.sa_select_blocks(q, box, *a))
+        torch.cuda.synchronize()
+    ws = sa.allocate_select_workspace(int(cu[-1]), 4, hkv, d, rows.shape[1], "cuda")
+    box = boxes[0].clone()
+    got = []
+    for q, new in zip(qs, boxes):
+        box.copy_(new)
+        got.append(sa.sa_select_blocks(q, box, *a, workspace=ws))
+    torch.cuda.synchronize()
+    for x, y in zip(got, ref):
+        assert torch.equal(x, y)
+    assert not torch.equal(ref[0], ref[1])
+    q, sel = qs[0].clone(), torch.empty_like(ref[0])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        sa.sa_select_blocks(q, box, *a, workspace=ws, selected=sel)
+    for i in range(n):
+        q.copy_(qs[i])
+        box.copy_(boxes[i])
+        g.replay()
+        assert torch.equal(sel, ref[i])
