@@ -695,12 +695,14 @@ sa_status sa_store_kv(const void* k, const void* v, sa_dtype src_dtype, int64_t 
   int64_t longest = 0;
   for (int32_t b = 0; b < batch; ++b)
     longest = std::max(longest, cu_seqlens_q_host[b + 1] - cu_seqlens_q_host[b]);
-  // A warp per item while an item is at most eight 8-element pieces a lane: 7000
+  // A warp per item while an item is at most sixteen 8-element pieces a lane: 7000
   // f32 rows of 8 heads of 128 to int8 take 18.5 us by warps and 61 us by CTAs with
-  // pages of 16, 20.5 and 22.6 us with pages of 64, 58 and 20.6 us with pages of
-  // 256; one prompt of 1000 rows and pages of 64 takes 16 us by warps, 6 by CTAs.
+  // pages of 16, 18 and 35 us with pages of 32, 20.5 and 22.6 us with pages of 64, 58
+  // and 20.6 us with pages of 256; 28000 rows 69 and 123 us with pages of 32, 90 and
+  // 74 us with pages of 64; one prompt of 1000 rows 10 and 8 us with pages of 32, 16
+  // and 6 us with pages of 64.
   const int64_t rows = std::min<int64_t>(longest, page_size);
-  const bool by_warp = rows * head_dim <= 32 * 8 * 8;
+  const bool by_warp = rows * head_dim <= 32 * 16 * 8;
   const bool bf = src_dtype == SA_DTYPE_BF16;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t err;
