@@ -195,7 +195,9 @@ __global__ void __launch_bounds__(kThreads, 3) store_kv_kernel(const StoreArgs a
   const int64_t page0 = nr.p0 / a.page_size;
   const int64_t pg = page0 + (u - slot_base(a.cu[b], b, a.page_size));
   const int64_t base = pg * a.page_size;
-  if (pg < page0 || base >= nr.p1 || pg >= a.max_pages) return;   // the same for the whole item
+  // (a sequence without new rows has p0 = p1, inside a page perhaps: another
+  // sequence may be writing that page and its scale)
+  if (nr.p0 >= nr.p1 || pg < page0 || base >= nr.p1 || pg >= a.max_pages) return;   // the whole item
   const int id = a.block_tables[static_cast<int64_t>(b) * a.max_pages + pg];
   if (id < 0 || id >= a.num_pages) {
     if (id >= 0 && t == 0) report(a.status, SA_ERR_SHAPE);

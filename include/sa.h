@@ -567,7 +567,8 @@ sa_status sa_attention_scaled(const void *q, sa_dtype q_dtype, const void *k_pag
  * behind the new ones are left as they were.  Two new positions of one call
  * must not share a page through different table entries (which of them ends
  * up in a shared row, or in the scale, is then unspecified; every access stays
- * in bounds).
+ * in bounds).  A sequence without new tokens touches no page and no scale, so
+ * one that appends may share its last page with others that do not.
  *
  * Supported: head_dim a multiple of 8 (16 for the 8-bit types), at most 256.
  * Checks, in order: HEAD_COUNT, BLOCK_PAGE, CU_SEQLENS, SHAPE

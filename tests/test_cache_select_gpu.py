@@ -260,6 +260,51 @@ def test_store_far_pages():
     assert torch.equal(bounds[1, :, 1].float(), vals.amax(1))
 
 
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+def test_store_leaves_pages_without_new_rows(kind):
+    """A sequence without new tokens whose length ends inside a page: the page
+    and its scale stay as they are, whatever the scale (0.3, negative, NaN)."""
+    hkv, d, ps = 2, 32, 16
+    lens, qo = [7, 23, 5, 9], [0, 0, 0, 1]
+    cu = np.concatenate([[0], np.cumsum(qo)]).astype(np.int64)
+    bt = np.array([[0, -1], [1, 2], [3, -1], [4, -1]], np.int32)
+    kp = torch.full((5, hkv, ps, d), 3, dtype=torch.uint8, device="cuda").view(TORCH[kind])
+    ks = torch.tensor([[-2.0, 0.3], [1.0, 1.0], [-0.5, math.nan], [math.inf, 0.0], [0.25, 0.25]],
+                      device="cuda")
+    vp, vs = kp.clone(), -ks
+    before = [t.clone() for t in (kp, vp, ks, vs)]
+    x = torch.ones((1, hkv, d), device="cuda")
+    sa.sa_store_kv(x, x, kp, vp, cuda_i(bt, np.int32), cu, cuda_i(cu, np.int64),
+                   cuda_i(lens, np.int32), k_scales=ks, v_scales=vs)
+    for t, was in zip((kp, vp, ks, vs), before):
+        np.testing.assert_array_equal(t[:4].cpu().view(torch.uint8).numpy(),
+                                      was[:4].cpu().view(torch.uint8).numpy())
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+def test_store_page_shared_with_an_idle_sequence(kind):
+    """Two sequences over one partly filled page, of which one appends a larger
+    row: the page takes the larger scale (many pairs, so that the two meet)."""
+    hkv, d, ps, n = 8, 64, 16, 300
+    order = np.random.default_rng(1).permutation(2 * n)
+    lens, qo = np.zeros(2 * n, np.int64), np.zeros(2 * n, np.int64)
+    bt = np.zeros((2 * n, 1), np.int32)
+    for i, s in enumerate(order):          # i < n: appends to page i; else idle on page i - n
+        lens[s], qo[s], bt[s, 0] = (8, 1, i) if i < n else (7, 0, i - n)
+    cu = np.concatenate([[0], np.cumsum(qo)]).astype(np.int64)
+    unit = 2.0 ** -6
+    for _ in range(5):
+        kp = torch.ones((n, hkv, ps, d), device="cuda").mul_(64).to(TORCH[kind])
+        ks = torch.full((n, hkv), unit, device="cuda")
+        vp, vs = kp.clone(), ks.clone()
+        x = torch.full((n, hkv, d), 64.0 * 16 * unit, device="cuda")
+        sa.sa_store_kv(x, x, kp, vp, cuda_i(bt, np.int32), cu, cuda_i(cu, np.int64),
+                       cuda_i(lens, np.int32), k_scales=ks, v_scales=vs)
+        for pages, scales in ((kp, ks), (vp, vs)):
+            v = pages.float() * scales[:, :, None, None]
+            assert (v[:, :, :7] == 64 * unit).all() and (v[:, :, 7] == 64 * 16 * unit).all()
+
+
 # ----------------------------------------------------------------------------- bounds
 
 def outward(x, up):
