@@ -312,7 +312,16 @@ class _Scaled:
                 self.kv_code)
 
 
-def _scaled(q, k_pages, v_pages, k_scales, v_scales):
+def _check_pool(k_pages, hkv, page_size, head_dim):
+    """The scales are looked up by page id, so an 8-bit pool has to be what the
+    call's sizes say: with other sizes an id inside the pool could lie past the
+    scales."""
+    if tuple(k_pages.shape[1:]) != (hkv, page_size, head_dim):
+        raise ValueError(f"k_pages must be [num_pages, {hkv}, {page_size}, {head_dim}], got "
+                         f"{tuple(k_pages.shape)}")
+
+
+def _scaled(q, k_pages, v_pages, k_scales, v_scales, hkv, page_size, head_dim):
     """Checks of a call over an 8-bit cache; None for the other cache types,
     which take no scales."""
     dtype = k_pages.dtype
@@ -321,6 +330,7 @@ def _scaled(q, k_pages, v_pages, k_scales, v_scales):
             raise ValueError(f"a {k_pages.dtype} cache has no scales")
         return None
     code = _cache_dtype(k_pages, "k_pages")
+    _check_pool(k_pages, hkv, page_size, head_dim)
     if q.dtype not in _ACT_DTYPES:
         raise TypeError(f"q must be float32 or bfloat16, got {q.dtype}")
     _require(q, q.dtype, "q")
@@ -398,7 +408,7 @@ def sa_forward(q, k_pages, v_pages, index: Index, block_tables, cu_seqlens_q, us
     tensor-core kernel gather Q from a bf16 copy (both: sa_forward_ex).  An
     8-bit cache needs ``k_scales`` and ``v_scales`` [num_pages, hkv]; ``q`` may
     then be bfloat16 (sa_forward_scaled)."""
-    x = _scaled(q, k_pages, v_pages, k_scales, v_scales)
+    x = _scaled(q, k_pages, v_pages, k_scales, v_scales, hkv, page_size, head_dim)
     if x is None:
         _require(q, torch.float32, "q")
         kvd = _kv_dtype(k_pages)
@@ -471,7 +481,7 @@ def sa_forward_combine(q, k_pages, v_pages, index: Index, selected, cu_seqlens_q
     applies).  Returns (out, lse, (o, m, l)).  ``partial_dtype="bf16"`` (or a
     bfloat16 o in ``partials``): 16-bit o partials.  ``k_scales``, ``v_scales``:
     see :func:`sa_attention`."""
-    x = _scaled(q, k_pages, v_pages, k_scales, v_scales)
+    x = _scaled(q, k_pages, v_pages, k_scales, v_scales, index.c.hkv, page_size, head_dim)
     if x is None:
         _require(q, torch.float32, "q")
         kvd = _kv_dtype(k_pages)
@@ -522,7 +532,7 @@ def sa_attention(q, k_pages, v_pages, selected, cu_seqlens_q_host, cu_seqlens_q,
     partials (sa_attention_ex).  A float8_e4m3fn or int8 cache needs
     ``k_scales`` and ``v_scales`` [num_pages, hkv] (see :func:`sa_store_kv`);
     ``q`` may then be bfloat16, and ``out`` has its type (sa_attention_scaled)."""
-    x = _scaled(q, k_pages, v_pages, k_scales, v_scales)
+    x = _scaled(q, k_pages, v_pages, k_scales, v_scales, hkv, page_size, head_dim)
     if x is None:
         _require(q, torch.float32, "q")
         kvd = _kv_dtype(k_pages)

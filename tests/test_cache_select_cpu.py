@@ -1,6 +1,7 @@
 """Host-side checks of the cache, bounds and selection entry points: every
 refusal comes before any device work."""
 import ctypes
+import types
 
 import numpy as np
 import pytest
@@ -261,3 +262,30 @@ def test_host_pointers():
     for x in ([0, 2, 5], np.array([0, 2, 5], np.int32), torch.tensor([0, 2, 5])):
         h = sa._host_i64(x)
         assert h.dtype == np.int64 and h.flags.c_contiguous and h.tolist() == [0, 2, 5]
+
+
+@pytest.mark.parametrize("shape", [(4, 2, 32, 128), (4, 1, 16, 128), (4, 2, 16, 64), (4, 4, 8, 128)])
+def test_pool_of_other_sizes(shape):
+    """An 8-bit pool whose shape is not what the call's sizes say is refused
+    before any pointer is taken: its scales would be read past their end."""
+    import torch
+
+    import block_sparse_paged_csr_gb300 as sa
+
+    codes = torch.zeros(shape, dtype=torch.int8)
+    scales = torch.ones(shape[:2])
+    q = torch.zeros((1, 4, 128))
+    with pytest.raises(ValueError, match="k_pages must be"):
+        sa._scaled(q, codes, codes, scales, scales, 2, 16, 128)
+    i32 = torch.zeros((1, 8), dtype=torch.int32)
+    sel = torch.zeros((1, 2, 1), dtype=torch.int32)
+    with pytest.raises(ValueError, match="k_pages must be"):
+        sa.sa_attention(q, codes, codes, sel, [0, 1], None, None, i32, 4, 2, 128, 64, 16, 0.1, True,
+                        k_scales=scales, v_scales=scales)
+    with pytest.raises(ValueError, match="k_pages must be"):
+        sa.sa_forward(q, codes, codes, None, i32, None, None, 4, 2, 128, 64, 16, 0.1, True,
+                      k_scales=scales, v_scales=scales)
+    index = sa._native.SaIndex(hkv=2, tq=1)
+    with pytest.raises(ValueError, match="k_pages must be"):
+        sa.sa_forward_combine(q, codes, codes, types.SimpleNamespace(c=index), sel, [0, 1], None, None,
+                              i32, 4, 128, 64, 16, 0.1, True, k_scales=scales, v_scales=scales)
