@@ -381,6 +381,44 @@ def test_bounds_without_keys_and_bad_ids():
     assert sa.sa_status_string(call([[9, 1, 2, 3]], [[2, 1]])) == "shape mismatch"
 
 
+def outward64(x, up):
+    """float64 -> the nearest bf16 value (as float64) at or beyond it."""
+    m, e = np.frexp(np.asarray(x, np.float64))
+    m = (np.ceil if up else np.floor)(m * 256.0)
+    return np.ldexp(m, e - 8)
+
+
+@pytest.mark.parametrize("ps,bs,d", [(16, 32, 32), (4, 16, 64), (64, 128, 128)])
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("scales", ["negative", "signs"])
+def test_bounds_scales_of_any_sign(kind, scales, ps, bs, d):
+    """Scales of a caller's own: negative ones turn smallest and largest round."""
+    rng = np.random.default_rng(8)
+    hkv, lens, qo = 2, [3 * bs + 5, bs, 2 * bs - 1], [3 * bs + 5, 2, bs]
+    cu = np.concatenate([[0], np.cumsum(qo)]).astype(np.int64)
+    bt, n = tables(lens, ps, rng)
+    cols = -(-bt.shape[1] * ps // bs)
+    bt = np.concatenate([bt, np.full((len(lens), cols * bs // ps - bt.shape[1]), -1, np.int32)], 1)
+    kh, _, kp, _ = make_pool(n, hkv, ps, d, kind, rng)
+    if scales == "negative":
+        s = -(2.0 ** rng.integers(-9, -3, (n, hkv)))
+    elif scales == "signs":
+        s = 2.0 ** rng.integers(-9, -3, (n, hkv)) * rng.choice([-1.0, 0.0, 1.0], (n, hkv))
+    s = s.astype(np.float32)
+    rows, nb = tables(lens, bs, rng, cols=cols)
+    out = torch.zeros((nb, hkv, 2, d), dtype=torch.bfloat16, device="cuda")
+    sa.sa_block_bounds(kp, cuda_i(bt, np.int32), cu, cuda_i(cu, np.int64), cuda_i(lens, np.int32),
+                       out, cuda_i(rows, np.int32), bs, k_scales=torch.from_numpy(s).cuda())
+    vals = kh * s.astype(np.float64)[:, :, None, None]
+    got = host(out)
+    for b, lk in enumerate(lens):
+        for j in range((lk - qo[b]) // bs, -(-lk // bs)):
+            k = np.stack([vals[bt[b, p // ps], :, p % ps] for p in range(j * bs, min((j + 1) * bs, lk))], 1)
+            lo, hi = got[rows[b, j], :, 0], got[rows[b, j], :, 1]
+            np.testing.assert_array_equal(lo, outward64(k.min(1), False))
+            np.testing.assert_array_equal(hi, outward64(k.max(1), True))
+
+
 # ----------------------------------------------------------------------------- selection
 
 def visible(cu, lens, causal, bs, msb):
