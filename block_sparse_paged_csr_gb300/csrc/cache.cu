@@ -485,10 +485,10 @@ __global__ void __launch_bounds__(kThreads, 3) block_bounds_kernel(const BoundsA
       CodeRange<kType == kInt8> cr;
       // The page's codes times its scale.  A code has at most 8 significant bits
       // and lies in 2^-9 .. 448, so its product with a power of two of this
-      // range is a bf16 number; other products are rounded outward.  A negative
-      // scale of a caller's own makes the largest code the smallest key.  (A NaN
-      // product, of a scale that is 0 and a channel with NaN keys only, counts as
-      // no key.)
+      // range is a bf16 number; other products are rounded outward, from f32
+      // rounded outward.  A negative scale of a caller's own makes the largest
+      // code the smallest key.  (A NaN product, of a scale that is 0 and a
+      // channel with NaN keys only, counts as no key.)
       auto close = [&]() {
         if constexpr (kCodes) {
           const bool exact = (__float_as_uint(sc) & 0x7FFFFFu) == 0u && sc >= 0x1p-120f && sc <= 0x1p100f;
@@ -508,10 +508,10 @@ __global__ void __launch_bounds__(kThreads, 3) block_bounds_kernel(const BoundsA
             for (int i = 0; i < 8; ++i) {
               const float2 l = cr.value(turned ? cr.hi[i] : cr.lo[i]);
               const float2 m = cr.value(turned ? cr.lo[i] : cr.hi[i]);
-              lo[i] = min_bf16x2(lo[i], bf16_down(fminf(l.x * sc, INFINITY)) |
-                                            (bf16_down(fminf(l.y * sc, INFINITY)) << 16));
-              hi[i] = max_bf16x2(hi[i], bf16_up(fmaxf(m.x * sc, -INFINITY)) |
-                                            (bf16_up(fmaxf(m.y * sc, -INFINITY)) << 16));
+              lo[i] = min_bf16x2(lo[i], bf16_down(fminf(__fmul_rd(l.x, sc), INFINITY)) |
+                                            (bf16_down(fminf(__fmul_rd(l.y, sc), INFINITY)) << 16));
+              hi[i] = max_bf16x2(hi[i], bf16_up(fmaxf(__fmul_ru(m.x, sc), -INFINITY)) |
+                                            (bf16_up(fmaxf(__fmul_ru(m.y, sc), -INFINITY)) << 16));
             }
           }
         }

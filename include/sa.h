@@ -593,7 +593,8 @@ sa_status sa_store_kv(const void *k, const void *v, sa_dtype src_dtype, int64_t 
  *
  *   bounds        [num_bounds, hkv, 2, head_dim] bf16: smallest, then largest,
  *                 rounded down and up (exact for bf16 keys and for 8-bit codes
- *                 under power-of-two scales)
+ *                 under power-of-two scales; under others, of either sign, they
+ *                 enclose the exact products code * scale)
  *   bound_tables  [batch, msb] int32: row of `bounds` for block j of sequence
  *                 b; -1: the block is skipped
  *   k_scales      [num_pages, hkv] for the 8-bit types, else ignored

@@ -390,7 +390,7 @@ def outward64(x, up):
 
 @pytest.mark.parametrize("ps,bs,d", [(16, 32, 32), (4, 16, 64), (64, 128, 128)])
 @pytest.mark.parametrize("kind", ["e4m3", "int8"])
-@pytest.mark.parametrize("scales", ["negative", "signs"])
+@pytest.mark.parametrize("scales", ["negative", "signs", "any"])
 def test_bounds_scales_of_any_sign(kind, scales, ps, bs, d):
     """Scales of a caller's own: negative ones turn smallest and largest round."""
     rng = np.random.default_rng(8)
@@ -404,6 +404,8 @@ def test_bounds_scales_of_any_sign(kind, scales, ps, bs, d):
         s = -(2.0 ** rng.integers(-9, -3, (n, hkv)))
     elif scales == "signs":
         s = 2.0 ** rng.integers(-9, -3, (n, hkv)) * rng.choice([-1.0, 0.0, 1.0], (n, hkv))
+    else:
+        s = rng.uniform(-0.1, 0.1, (n, hkv))
     s = s.astype(np.float32)
     rows, nb = tables(lens, bs, rng, cols=cols)
     out = torch.zeros((nb, hkv, 2, d), dtype=torch.bfloat16, device="cuda")
@@ -417,6 +419,27 @@ def test_bounds_scales_of_any_sign(kind, scales, ps, bs, d):
             lo, hi = got[rows[b, j], :, 0], got[rows[b, j], :, 1]
             np.testing.assert_array_equal(lo, outward64(k.min(1), False))
             np.testing.assert_array_equal(hi, outward64(k.max(1), True))
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+def test_bounds_enclose_the_exact_keys(kind):
+    """Products that lie just beside a bf16 number, where f32 would round to it:
+    the bounds enclose the exact product."""
+    codes = [c for c in range(1, 100 if kind == "int8" else 16)]
+    n, d = 2 * len(codes), 32
+    c = np.array(codes * 2, np.float32) * np.repeat([1, -1], len(codes)).astype(np.float32)
+    s = np.float32(1) / np.abs(c)
+    kp = torch.from_numpy(c).cuda()[:, None, None, None].expand(n, 1, 16, d).contiguous().to(TORCH[kind])
+    bt = np.arange(n, dtype=np.int32)[:, None]
+    cu = np.arange(n + 1, dtype=np.int64) * 16
+    out = torch.zeros((n, 1, 2, d), dtype=torch.bfloat16, device="cuda")
+    sa.sa_block_bounds(kp, cuda_i(bt, np.int32), cu, cuda_i(cu, np.int64),
+                       cuda_i(np.full(n, 16), np.int32), out, cuda_i(bt, np.int32), 16,
+                       k_scales=torch.from_numpy(s)[:, None].cuda())
+    exact = c.astype(np.float64) * s.astype(np.float64)
+    assert (exact != np.float32(exact)).any()              # (some are not f32 numbers)
+    for x, up in ((0, False), (1, True)):
+        np.testing.assert_array_equal(host(out)[:, 0, x], np.repeat(outward64(exact, up)[:, None], d, 1))
 
 
 # ----------------------------------------------------------------------------- selection
