@@ -157,9 +157,9 @@ __host__ __device__ constexpr float score_eps(int steps, int lanes, float split)
   return static_cast<float>(steps) * 0x1p-22f + static_cast<float>(lanes + 2) * 0x1p-24f + split;
 }
 
-// The bits of a score that is not finite, or of a block without a bounds row:
-// kNoBlock for the latter and for a block without keys (it holds lo = inf, hi =
-// -inf); else the sum over the channels by itself, since a part of a split
+// The bits of a score that is not finite, or of a block without a bounds row, or
+// with one that stands for no block (lo[0] > hi[0]: a block without keys holds
+// lo = inf, hi = -inf): kNoBlock for the last two; else the sum over the channels by itself, since a part of a split
 // weight that is 0 makes a NaN of an infinite bound; one NaN for all.
 __device__ __noinline__ uint32_t special_bits(const SelectArgs& a, int i, int h,
                                               const uint16_t* box, bool there) {
@@ -439,6 +439,10 @@ block_score_kernel(const SelectArgs a) {
       const int id = ids[kSpan == 1 || st < kStages ? 0 : 1];
       const int id0 = __shfl_sync(0xffffffffu, id, 8 * (st % kStages) + 2 * c);
       const int id1 = __shfl_sync(0xffffffffu, id, 8 * (st % kStages) + 2 * c + 1);
+      // whether this lane's column (2 c + (g & 1), see below) is a block: lo[0] <= hi[0]
+      const uint16_t* own = reinterpret_cast<const uint16_t*>(
+          mine + ((st % kRing) * kGroup + 2 * c + (g & 1)) * row_bytes);
+      const bool none = bf16_to_f32(own[0]) > bf16_to_f32(own[d]);
       // a query's score: its three rows' sums, of columns 2 c and 2 c + 1
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -475,7 +479,7 @@ block_score_kernel(const SelectArgs a) {
           if (g < 2 && j < min(j1, s_nblk[qi])) {
             const float sv = g == 0 ? s0 : s1;
             a.scores[(static_cast<int64_t>(unit) + static_cast<int64_t>(qi) * a.hkv) * a.stride + j] =
-                rj >= 0 && fabsf(sv) < INFINITY
+                rj >= 0 && !none && fabsf(sv) < INFINITY
                     ? __float_as_uint(sv)
                     : special_bits(a, rv.i + qi, rv.h,
                                    a.bounds + (static_cast<int64_t>(max(rj, 0)) * a.hkv + rv.h) * 2 * d,
@@ -739,6 +743,8 @@ __global__ void __launch_bounds__(kTileThreads, 2) block_score_tile_kernel(const
     const unsigned char* buf = s_raw + (t & 1) * L::kBuf;
 #pragma unroll 1
     for (int n = 0; n < kTileB / 16; ++n) {
+      float lo0[2];                                    // lo[0] (lanes c = 0)
+      bool none = false;                               // a row of these 16 with lo[0] > hi[0]
       float acc[2][2][4];
 #pragma unroll
       for (int x = 0; x < 2; ++x)
@@ -754,6 +760,11 @@ __global__ void __launch_bounds__(kTileThreads, 2) block_score_tile_kernel(const
           for (int n2 = 0; n2 < 2; ++n2) {
             const uint4 u = *reinterpret_cast<const uint4*>(
                 buf + (16 * n + 8 * n2 + g) * L::kRow + (half * 4 * kG + 4 * x + c) * 16);
+            if (x == 0) {
+              const float first = __uint_as_float(u.x << 16);
+              if (half == 0) lo0[n2] = first;
+              else none = none || (c == 0 && lo0[n2] > first);
+            }
             mma_bf16(acc[n2][0], ahi[half][x][0][0], ahi[half][x][0][1], ahi[half][x][0][2],
                      ahi[half][x][0][3], u.x, u.y);
             mma_bf16(acc[n2][1], alo[half][x][0][0], alo[half][x][0][1], alo[half][x][0][2],
@@ -771,7 +782,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) block_score_tile_kernel(const
           acc[n2][0][e] += acc[n2][1][e];
           big += fabsf(acc[n2][0][e]);
         }
-      const bool plain = all_rows && big < INFINITY;
+      const bool plain = !__any_sync(0xffffffffu, none) && all_rows && big < INFINITY;
 #pragma unroll
       for (int n2 = 0; n2 < 2; ++n2) {
         const int lj = t * kTileB + 16 * n + 8 * n2 + 2 * c;   // column of the chunk
@@ -782,11 +793,16 @@ __global__ void __launch_bounds__(kTileThreads, 2) block_score_tile_kernel(const
           uint2 bits = make_uint2(__float_as_uint(s0), __float_as_uint(s1));
           if (!plain) {
             const int id0 = ids[lj], id1 = ids[lj + 1];
-            if (id0 < 0 || !(fabsf(s0) < INFINITY))
+            const uint16_t* r0 = reinterpret_cast<const uint16_t*>(
+                buf + (16 * n + 8 * n2 + 2 * c) * L::kRow);
+            const uint16_t* r1 = r0 + L::kRow / 2;
+            if (id0 < 0 || !(fabsf(s0) < INFINITY) ||
+                bf16_to_f32(r0[0]) > bf16_to_f32(r0[32 * kG]))
               bits.x = special_bits(
                   a, iq[rr], h, a.bounds + (static_cast<int64_t>(max(id0, 0)) * a.hkv + h) * 2 * d,
                   id0 >= 0);
-            if (id1 < 0 || !(fabsf(s1) < INFINITY))
+            if (id1 < 0 || !(fabsf(s1) < INFINITY) ||
+                bf16_to_f32(r1[0]) > bf16_to_f32(r1[32 * kG]))
               bits.y = special_bits(
                   a, iq[rr], h, a.bounds + (static_cast<int64_t>(max(id1, 0)) * a.hkv + h) * 2 * d,
                   id1 >= 0);

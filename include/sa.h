@@ -625,7 +625,7 @@ sa_status sa_select_workspace_size(int64_t tq, int32_t batch, int32_t hkv, int32
  * lanes.  The candidates are the blocks with a key that query i may see
  * (causal as in sa_forward: 0 every block below the sequence's length, 1 up to
  * its own position right-aligned, 2 left-aligned) whose bounds row is there
- * and holds lo[0] <= hi[0].  The topk candidates with the highest scores are
+ * and does not hold lo[0] > hi[0], finite or not.  The topk candidates with the highest scores are
  * written in ascending order, then -1.  Ties go to the lower block; a score
  * that is NaN ranks behind all others.  The first sink_blocks and the last
  * local_blocks of the blocks in sight come in before any other (sink_blocks +

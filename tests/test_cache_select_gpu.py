@@ -633,6 +633,31 @@ def test_select_not_finite():
     run_select(q2, b2, rows, cu, lens, 16, 9)
 
 
+@pytest.mark.parametrize("d", [8, 32, 64, 128, 256])
+@pytest.mark.parametrize("qo", [1, 3, 40])
+@pytest.mark.parametrize("topk", [5, 90])
+def test_select_leaves_out_rows_of_no_block(qo, d, topk):
+    """A bounds row with lo[0] > hi[0] is no block, finite or not, however high
+    its score: with more blocks in sight than are taken and with fewer."""
+    q, bounds, rows, cu, lens = problem([qo, 1], [1600, 900], 4, 2, d, 16, seed=31 + d)
+    gen = np.random.default_rng(d)
+    for b in range(2):
+        n = -(-int(lens[b]) // 16)
+        for j in gen.permutation(n)[:n // 5]:
+            r, h = rows[b, j], int(gen.integers(2))
+            bounds[r, h, 0] = -50.0                    # wide, so high scores ..
+            bounds[r, h, 1] = 50.0
+            bounds[r, h, 0, 0] = 2.0 ** -7             # .. but for channel 0
+            bounds[r, h, 1, 0] = -2.0 ** -7
+    got = run_select(q, bounds, rows, cu, lens, 16, topk)
+    box = bounds.float().cpu().numpy()
+    seq = np.searchsorted(cu, np.arange(len(got)), side="right") - 1
+    for i in range(len(got)):
+        for h in range(2):
+            ids = got[i, h][got[i, h] >= 0]
+            assert (box[rows[seq[i], ids], h, 0, 0] <= box[rows[seq[i], ids], h, 1, 0]).all()
+
+
 def test_select_in_parts():
     """More scores than the workspace holds at a time."""
     qo, n, bs, topk = 1100, 16000, 16, 24
