@@ -147,14 +147,24 @@ __device__ __forceinline__ uint32_t finite_bf16x2(uint32_t u) {
 }
 
 // The error bound of a score, per unit of the sum of |weight| * largest |bound|
-// (which no block's sum of |terms| exceeds).  The products are summed by
-// the tensor cores in `steps` of 16, each of which may lose a unit in the 23rd
-// place of the running sum (products are exact, sums of a step are aligned and
-// cut, not rounded): 2^-22 a step; the weights' own sums over `lanes` f32 terms
-// lose 2^-24 each, and their split `split`.  (On the hardware the largest error
-// seen is a small part of this: see the tests.)
+// (which no block's sum of |terms| exceeds).  The tensor cores add 16 exact
+// products and the sum so far in one step: every addend is cut (not rounded) to
+// a multiple of 2^-25 of the power of two of the largest one, two bits below
+// f32's last, and the sum is cut to 24 bits.  The largest addend loses nothing,
+// each of the 16 others less than 2^-25, the sum less than 2^-23: 5 * 2^-23 a
+// step.  That is how GB300's tensor cores behave, found by measuring (one large
+// addend of either sign at every place beside 16 small ones of 2^-20 to 2^-32, and 2 million
+// sums of random exponents, of which the worst lost 3.5 * 2^-23 of its terms'
+// magnitudes), not a documented property.  Terms of 2^-25 beside two large
+// ones take scores 62 * 2^-23 off at head_dim 128; see the test of small terms.
+// The weights' own sums over `lanes` f32 terms and the sums of parts and chains
+// lose 2^-24 each, and the weights' split `split`; the last factor covers the
+// parts' magnitudes above their weight's and the error of the sum of magnitudes
+// itself.  (Products and parts below 2^-133 are lost besides: nothing, unless
+// all of a score's terms are below 2^-100 or so.)
 __host__ __device__ constexpr float score_eps(int steps, int lanes, float split) {
-  return static_cast<float>(steps) * 0x1p-22f + static_cast<float>(lanes + 2) * 0x1p-24f + split;
+  return (static_cast<float>(steps) * 0x5p-23f + static_cast<float>(lanes + 6) * 0x1p-24f + split) *
+         (1.f + 0x1p-6f);
 }
 
 // The bits of a score that is not finite, or of a block without a bounds row, or
@@ -506,7 +516,7 @@ block_score_kernel(const SelectArgs a) {
     for (int w = 0; w < kScoreWarps; ++w) m = fmaxf(m, s_l1[tid][w]);
     for (int x = chunk; x < min(chunk + kSpan, a.chunks); ++x)
       a.eps[(static_cast<int64_t>(unit) + static_cast<int64_t>(tid) * a.hkv) * a.chunks + x] =
-          m * score_eps(kT + 2, a.qhead, 0x1p-24f);
+          m * score_eps(kT, a.qhead, 0x1p-24f);
   }
 }
 
@@ -848,8 +858,8 @@ __global__ void __launch_bounds__(kTileThreads, 2) block_score_tile_kernel(const
     }
 #pragma unroll
   for (int rr = 0; rr < 2; ++rr) {
-    // (column 0 is the first lane's; this sum's own error is below 2^-10)
-    float l1 = __shfl_sync(0xffffffffu, sum[2 * rr], lane & 28) * (1.f + 0x1p-10f);
+    // (column 0 is the first lane's)
+    float l1 = __shfl_sync(0xffffffffu, sum[2 * rr], lane & 28);
     if (__any_sync(0xffffffffu, !(l1 < INFINITY))) {
       // weights that are not numbers or past bf16's range: channel by channel
       l1 = 0.f;
@@ -882,7 +892,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) block_score_tile_kernel(const
     }
     if (c == 0 && iq[rr] < c1 && iq[rr] >= w0 && iq[rr] < w1)
       a.eps[static_cast<int64_t>((iq[rr] - w0) * a.hkv + h) * a.chunks + chunk] =
-          l1 * score_eps(4 * kG + 1, a.qhead, 0x1p-18f);
+          l1 * score_eps(4 * kG, a.qhead, 0x1p-18f);
   }
 }
 

@@ -658,6 +658,44 @@ def test_select_leaves_out_rows_of_no_block(qo, d, topk):
             assert (box[rows[seq[i], ids], h, 0, 0] <= box[rows[seq[i], ids], h, 1, 0]).all()
 
 
+@pytest.mark.parametrize("qo", [1, 4, 16])
+@pytest.mark.parametrize("d", [32, 64, 128, 256])
+@pytest.mark.parametrize("big", [1.0, 1.9921875, -1.0])
+def test_select_small_terms_beside_large_ones(qo, d, big):
+    """Scores whose small terms a sum cuts off beside two large ones: half of
+    the blocks have all of them positive, the other half all of them negative
+    and one more term, smaller than the difference, that the sum keeps.  Which
+    half comes first turns on what was cut off.  Small terms of many sizes; all
+    products and all sums in 64 bits are exact."""
+    n, bs, topk = 600, 16, 300
+    q = torch.ones((qo, 2, d), device="cuda")
+    q[:, 1] = -1.0                                     # weights 1 and -1 in every channel
+    rng = np.random.default_rng(d)
+    rows = rng.permutation(n).astype(np.int32)[None]
+    cu = np.array([0, qo])
+    lens = np.array([n * bs])
+    for k in range(21, 31):
+        tiny = 1.9921875 * 2.0 ** -k
+        small = [c for c in range(2, d) if c not in (4, 5)]
+        for part in (0.3, 0.55, 0.65, 0.75, 0.9):
+            first = rng.permutation(n)[:n // 2]        # the half that should come in
+            sign = np.full((n, 1), -1.0)
+            sign[first] = 1.0
+            lo, hi = np.zeros((n, d)), np.zeros((n, d))
+            hi[:, small] = sign * tiny
+            lo[:, small] = -sign * tiny                # (times -1: the same again)
+            lo[:, 1] = lo[:, 4] = -big                 # times -1: among the first terms
+            kept = torch.tensor(part * 4 * len(small) * tiny).to(torch.bfloat16).item()
+            hi[sign[:, 0] < 0, 5] = kept
+            box = np.stack([lo, hi], 1)[:, None]
+            bounds = torch.from_numpy(box).to(torch.bfloat16)
+            assert torch.equal(bounds.double(), torch.from_numpy(box))
+            place = torch.empty_like(bounds)
+            place[torch.from_numpy(rows[0]).long()] = bounds
+            ref = np.tile(np.sort(first).astype(np.int32), (qo, 1, 1))
+            run_select(q, place.cuda(), rows, cu, lens, bs, topk, 0, ref=ref)
+
+
 def test_select_in_parts():
     """More scores than the workspace holds at a time."""
     qo, n, bs, topk = 1100, 16000, 16, 24
