@@ -52,12 +52,20 @@ constexpr int kNL = 2;               // load warps (with metadata and merge one 
 constexpr uint32_t kFirst = 1u, kLast = 2u, kDone = 4u;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-// The softmax's reference m is not the running maximum itself: P = 2^(s - m +
-// kShift) is formed with the m at hand, and only a score more than kSlack above
-// it (a P beyond 2^14, near f16's largest number) moves m up to the maximum.
-// So the products do not wait for a maximum over lanes, and o is rescaled a few
-// times per piece.  P's f16 parts resolve what lies 2^-30 below the largest.
-constexpr float kShift = 6.f, kSlack = 8.f;
+// The softmax's reference m is not the running maximum itself: P = 2^(s - m) is
+// formed with the m at hand, and only a score more than kSlack above it moves m
+// up, to the whole number above the maximum (so that rescaling is exact).  So the
+// products do not wait for a maximum over lanes.
+// What meets V's codes is P times their page's scale, and o keeps a reference n of
+// its own for that: it holds sums of P vs 2^(m - n).  A page whose scale is far
+// from the others' may carry nearly all of the softmax and little of the output,
+// or the other way round, so neither m nor the largest scale will do: n follows
+// the largest product.  It moves up (and o is rescaled), to where that product
+// counts 2^kTop, when m moves or when a page's vs 2^(m - n) is above kRoom: below it
+// no P of at most 2^kSlack makes a product above 2^15 (f16 ends at 2^16), so pages
+// of up to 2^4 times the scale of the one that set n cost nothing.  The f16 parts
+// of a product resolve 2^-22 of it or 2^-25, which is 2^-28 of the largest.
+constexpr float kSlack = 7.f, kTop = 4.f, kRoom = 256.f;
 
 // What differs with the number of query rows R: consumer groups, stages.
 template <int R> struct Q8Cfg;
@@ -82,12 +90,10 @@ struct Q8Maps {
 
 struct PieceDesc {
   int32_t item, k, i, h, lk, nr;
-  float vmax;                        // the largest |V scale| of the piece's pages
-  int32_t pad;
   int32_t blk[kMaxEP];               // blocks of the kept ranks, in rank order
   int32_t row[kMaxEP][kMaxPPB];      // first pool row of their pages (-1: absent)
   float ks[kMaxEP][kMaxPPB];         // their K scales
-  float vs[kMaxEP][kMaxPPB];         // their V scales over vmax
+  float vs[kMaxEP][kMaxPPB];         // their V scales
 };
 
 // One consumer warp's view of a stage: per chunk its 16 keys that exist (low
@@ -99,11 +105,10 @@ struct __align__(16) Rec {
 
 struct StageInfo {
   int32_t item, k;
-  float vmax;
 };
 
 struct Q8Layout {
-  uint32_t q, rec, info, mo, mm, ml, desc, bars, flag, total;
+  uint32_t q, rec, info, mo, mm, mn, ml, desc, bars, flag, total;
 };
 
 __host__ __device__ constexpr uint32_t up_to(uint32_t x, uint32_t a) { return (x + a - 1) / a * a; }
@@ -117,7 +122,8 @@ __host__ __device__ constexpr Q8Layout q8_layout() {
   L.info = L.rec + S * 4 * static_cast<uint32_t>(sizeof(Rec));
   L.mo = up_to(L.info + S * static_cast<uint32_t>(sizeof(StageInfo)), 16);
   L.mm = L.mo + NC * R * kD * 4;                               // merge rows [NC][R][128]
-  L.ml = L.mm + NC * R * 4;
+  L.mn = L.mm + NC * R * 4;
+  L.ml = L.mn + NC * R * 4;
   L.desc = up_to(L.ml + NC * R * 4, 16);
   L.bars = up_to(L.desc + kDescs * static_cast<uint32_t>(sizeof(PieceDesc)), 8);
   L.flag = L.bars + (2 * S + 2 * kDescs + 2) * 8;
@@ -132,11 +138,12 @@ struct Smem {
   Rec* rec;
   StageInfo* info;
   float* mo;
-  float* mm;
+  float* mm;            // l's reference
+  float* mn;            // o's
   float* ml;
   PieceDesc* desc;
   uint64_t *full, *empty, *dfull, *dempty;
-  uint64_t* mready;     // consumers -> merge warp: the piece's states are in mo/mm/ml
+  uint64_t* mready;     // consumers -> merge warp: the piece's states are in mo/mm/mn/ml
   uint64_t* mfree;      // merge warp -> consumers: the states have been read
   volatile int* minfo;  // item, k of the piece being merged (-1: no more pieces)
 };
@@ -224,7 +231,6 @@ __device__ void meta_warp(const FusedQ8Args& qa, const Smem& sm, int64_t n_piece
     // pages and scales, one (rank, page) per lane, four in flight
     const int ppb = a.pages_per_block;
     const int32_t* bt = a.block_tables + static_cast<int64_t>(b) * a.max_pages;
-    float vmax = 0.f;
 #pragma unroll 1
     for (int t0 = lane; t0 < nkept * ppb; t0 += 4 * 32) {
       int id[4], at[4];
@@ -258,24 +264,9 @@ __device__ void meta_warp(const FusedQ8Args& qa, const Smem& sm, int64_t n_piece
         if (at[x] >= 0) {
           (&d.ks[0][0])[at[x]] = ks[x];
           (&d.vs[0][0])[at[x]] = vs[x];
-          vmax = fmaxf(vmax, fabsf(vs[x]));
         }
     }
-    // V scales as fractions of the piece's largest: they go into P, so that all
-    // of the piece's products meet in one accumulator
-#pragma unroll
-    for (int off = 16; off; off >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
-    // (a power of two's reciprocal is exact; 2^-126 is the smallest it is taken
-    // of, and a smaller largest scale keeps its pages' values as they are)
-    const float inv = vmax >= 0x1p-126f ? __frcp_rn(vmax) : 1.f;
-    if (vmax < 0x1p-126f) vmax = 1.f;
-#pragma unroll 1
-    for (int t = lane; t < nkept * ppb; t += 32) {
-      const int pos = t / ppb;
-      d.vs[pos][t - pos * ppb] *= inv;     // this lane's own
-    }
     if (lane == 0) {
-      d.vmax = vmax;
       d.item = static_cast<int>(item);
       d.k = k;
       d.i = static_cast<int>(i);
@@ -346,7 +337,6 @@ __device__ void load_warp(const Q8Maps& maps, const FusedQ8Args& qa, const Smem&
     const uint32_t nst = need == 0 ? G : (need + G - 1) / G * G;
     if (mine < xs + nst) {
       const int lk = d.lk, h = d.h, i = d.i, kk = d.k;
-      const float vmax = d.vmax;
       uint32_t u = mine - xs;
       int ch = 2 * static_cast<int>(u) + half;    // the lane's chunk of the piece
       int j = ch / cpb, c = ch - j * cpb;
@@ -382,7 +372,7 @@ __device__ void load_warp(const Q8Maps& maps, const FusedQ8Args& qa, const Smem&
             r.flags = (u < G ? kFirst : 0u) | (u + G >= nst ? kLast : 0u);
           }
         } else if (lane == 16) {
-          sm.info[s] = StageInfo{item, kk, vmax};
+          sm.info[s] = StageInfo{item, kk};
         }
         __syncwarp();
         if (lane == 0)
@@ -427,6 +417,12 @@ __device__ __forceinline__ float ex2(float x) {
 
 // ------------------------------------------------------------------ piece end
 
+// 2^d for a whole number d up to 127 (0 below -126).
+__device__ __forceinline__ float pow2_of(float d) {
+  return d < -126.f ? 0.f
+                    : __uint_as_float(static_cast<uint32_t>(static_cast<int>(fminf(d, 127.f)) + 127) << 23);
+}
+
 __device__ __forceinline__ void write_row(const FusedQ8Args& qa, int64_t row, int d4, float m2,
                                           float l, float4 o) {
   const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -440,8 +436,8 @@ __device__ __forceinline__ void write_row(const FusedQ8Args& qa, int64_t row, in
 // on the same banks.
 __device__ __forceinline__ int merge_chunk(int c, int r) { return c ^ (c >> 3) ^ ((r & 1) << 2); }
 
-// The merge warp.  Per piece: merge the consumer warps' states (m in the log2
-// domain) row by row, lane = 4 channels; release the state buffer; then
+// The merge warp.  Per piece: merge the consumer warps' states (m and n in the
+// log2 domain) row by row, lane = 4 channels; release the state buffer; then
 // either write the output rows (one piece per pair) or the piece's scratch
 // rows, and if this piece is the pair's last to finish (a counter per pair),
 // merge the pair's scratch rows into the output.
@@ -465,16 +461,19 @@ __device__ void merge_warp(const FusedQ8Args& qa, const Smem& sm, int lane) {
     // scratch row of (pair, piece kk, lane r): (item * topk + kk) * qhead + r
     const int64_t prow = static_cast<int64_t>(item) * a.topk * qhead;
     for (int r = 0; r < qhead; ++r) {
-      float M = -INFINITY;
+      float M = -INFINITY, N = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < NC; ++w) M = fmaxf(M, sm.mm[w * R + r]);
+      for (int w = 0; w < NC; ++w) {
+        M = fmaxf(M, sm.mm[w * R + r]);
+        N = fmaxf(N, sm.mn[w * R + r]);
+      }
       float l = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
       if (M != -INFINITY) {
 #pragma unroll
         for (int w = 0; w < NC; ++w) {
-          const float e = ex2(sm.mm[w * R + r] - M);
-          l = fmaf(e, sm.ml[w * R + r], l);
+          l = fmaf(pow2_of(sm.mm[w * R + r] - M), sm.ml[w * R + r], l);
+          const float e = pow2_of(sm.mn[w * R + r] - N);
           const float4 v =
               reinterpret_cast<const float4*>(sm.mo + (w * R + r) * kD)[merge_chunk(lane, r)];
           o.x = fmaf(e, v.x, o.x);
@@ -482,6 +481,11 @@ __device__ void merge_warp(const FusedQ8Args& qa, const Smem& sm, int lane) {
           o.z = fmaf(e, v.z, o.z);
           o.w = fmaf(e, v.w, o.w);
         }
+        // from o's unit 2^N to l's, 2^M, in two halves: the values of a row with
+        // scales near the ends of f32's range stay inside it
+        const float half = truncf(0.5f * (N - M));
+        const float h0 = pow2_of(half), h1 = pow2_of(N - M - half);
+        o = make_float4(o.x * h0 * h1, o.y * h0 * h1, o.z * h0 * h1, o.w * h0 * h1);
       }
       if (P == 1) {
         write_row(qa, row0 + r, lane, M, l, o);
@@ -602,10 +606,8 @@ __device__ __forceinline__ void split2h(float x0, float x1, uint32_t& hi, uint32
 // Warp-level MMA (m16n8k16) on f16 operands.  Codes of both types are exact in
 // f16; Q (its row scaled by a power of two into f16's range) and P are split
 // into f16 high parts and remainders, so products lose no more than 2^-22.
-// The scale of a 16-key group's page meets K on the scores; that of V, as a
-// fraction of the largest of the piece, goes into P, and the largest into the
-// result: every product of the piece adds to one accumulator, and what a page
-// of a 2^n times smaller scale adds keeps 2^-(30 - n) of its size.
+// The scale of a 16-key group's page meets K on the scores and V on P (see kSlack):
+// every product of the piece adds to one accumulator.
 //
 // Codes need no transposition and no repacking through shared memory: a
 // fragment's k index may stand for any channel (scores) and its n index for
@@ -633,7 +635,8 @@ __device__ void consumer(const FusedQ8Args& qa, const Smem& sm, int warp, int la
   const uint32_t v_c0 = static_cast<uint32_t>((g ^ (2 * c)) << 4);
   const uint32_t v_c1 = v_c0 ^ 16u;
 
-  float m_run[NR];                   // the reference m, in the log2 domain
+  float m_run[NR], n_run[NR];        // the references m and n, in the log2 domain
+  float vfac[NR];                    // 2^(m - n)
   float l_part[NR], sfac[NR];
   float o[16][4];                    // [n-tile j][row g: columns 2c, 2c + 1 | row g + 8]
   uint32_t qf[8][4];                 // R = 8: high parts | remainders; R = 16: high parts
@@ -644,7 +647,8 @@ __device__ void consumer(const FusedQ8Args& qa, const Smem& sm, int warp, int la
     for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
-    m_run[r] = -INFINITY;
+    m_run[r] = n_run[r] = -INFINITY;
+    vfac[r] = 1.f;
     l_part[r] = 0.f;
     sfac[r] = 0.f;
   }
@@ -715,7 +719,8 @@ __device__ void consumer(const FusedQ8Args& qa, const Smem& sm, int warp, int la
             ql[j][2 + r] = l1;
           }
         }
-        m_run[r] = -INFINITY;
+        m_run[r] = n_run[r] = -INFINITY;
+        vfac[r] = 1.f;
         l_part[r] = 0.f;
       }
 #pragma unroll
@@ -768,10 +773,11 @@ __device__ void consumer(const FusedQ8Args& qa, const Smem& sm, int warp, int la
       bool beyond = false;
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
-        const float sub = kShift - m_run[r];             // +inf before the first keys
+        const float sub = -m_run[r];                     // +inf before the first keys
 #pragma unroll
         for (int hh = 0; hh < NH; ++hh) {
           const float f = sfac[r] * rec.ks[NH == 2 ? hh : h0];
+          beyond = beyond || fabsf(rec.vs[NH == 2 ? hh : h0] * vfac[r]) > kRoom;
 #pragma unroll
           for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
@@ -782,23 +788,24 @@ __device__ void consumer(const FusedQ8Args& qa, const Smem& sm, int warp, int la
                       (part[hh][nt][0][e + 2] + part[hh][nt][1][e + 2]);
               else
                 sum = part[hh][nt][0][e + 2 * r] + part[hh][nt][1][e + 2 * r];
-              // s q + kShift - m, kept apart from m's move below
               x[r][hh][nt][e] = fmaf(sum, f, sub);
               if (!whole && !((mk >> (16 * hh + 8 * nt + 2 * c + e)) & 1u))
                 x[r][hh][nt][e] = -INFINITY;
-              beyond = beyond || x[r][hh][nt][e] > kShift + kSlack;
+              beyond = beyond || x[r][hh][nt][e] > kSlack;
               part[hh][nt][0][e + (R == 8 ? 0 : 2 * r)] = sum;
             }
         }
       }
       if (__any_sync(0xffffffffu, beyond)) {
-        // a score well above the reference (the piece's first keys among them)
+        // a score well above the reference (the piece's first keys among them), or
+        // a page of a large V scale
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
-          float cm = -INFINITY;
+          float cm = -INFINITY, top = -INFINITY;         // largest score, largest product
 #pragma unroll
           for (int hh = 0; hh < NH; ++hh) {
             const float f = sfac[r] * rec.ks[NH == 2 ? hh : h0];
+            float chunk = -INFINITY;
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
@@ -806,26 +813,35 @@ __device__ void consumer(const FusedQ8Args& qa, const Smem& sm, int warp, int la
                 const bool live = (mk >> (16 * hh + 8 * nt + 2 * c + e)) & 1u;
                 const float v = part[hh][nt][0][e + (R == 8 ? 0 : 2 * r)] * f;
                 x[r][hh][nt][e] = live ? v : -INFINITY;
-                cm = fmaxf(cm, x[r][hh][nt][e]);
+                chunk = fmaxf(chunk, x[r][hh][nt][e]);
               }
+            cm = fmaxf(cm, chunk);
+            top = fmaxf(top, chunk + log2f(fabsf(rec.vs[NH == 2 ? hh : h0])));
           }
           cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, 1));
           cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, 2));
-          const float m_new = fmaxf(m_run[r], cm);       // finite: the warp has a key
-          const float alpha = ex2(m_run[r] - m_new);
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          // finite: the warp has a key
+          const float m_new = fmaxf(m_run[r], ceilf(cm));
+          l_part[r] *= pow2_of(m_run[r] - m_new);
           m_run[r] = m_new;
-          l_part[r] *= alpha;
+          // (pages of zeros only: the lowest n whose 2^(m - n) is a number)
+          const float n_new = fmaxf(fmaxf(n_run[r], ceilf(top) - kTop), m_new - 127.f);
+          const float beta = pow2_of(n_run[r] - n_new);
+          n_run[r] = n_new;
+          vfac[r] = pow2_of(m_new - n_new);
 #pragma unroll
           for (int hh = 0; hh < NH; ++hh)
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-              for (int e = 0; e < 2; ++e) x[r][hh][nt][e] += kShift - m_new;
+              for (int e = 0; e < 2; ++e) x[r][hh][nt][e] -= m_new;
 #pragma unroll
           for (int j = 0; j < 16; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (R == 8 || e / 2 == r) o[j][e] *= alpha;
+              if (R == 8 || e / 2 == r) o[j][e] *= beta;
         }
       }
 #pragma unroll
@@ -839,7 +855,7 @@ __device__ void consumer(const FusedQ8Args& qa, const Smem& sm, int warp, int la
 #pragma unroll
             for (int e = 0; e < 2; ++e) p[nt][e] = ex2(x[r][hh][nt][e]);
           lsum += (p[0][0] + p[0][1]) + (p[1][0] + p[1][1]);
-          const float vs = rec.vs[NH == 2 ? hh : h0];
+          const float vs = rec.vs[NH == 2 ? hh : h0] * vfac[r];
           if constexpr (R == 8) {
             split2h(p[0][0] * vs, p[0][1] * vs, pf[hh][0], pf[hh][1]);
             split2h(p[1][0] * vs, p[1][1] * vs, pf[hh][2], pf[hh][3]);
@@ -903,7 +919,7 @@ __device__ void consumer(const FusedQ8Args& qa, const Smem& sm, int warp, int la
         float4* dst = reinterpret_cast<float4*>(sm.mo + (warp * R + row) * kD);
         // (R = 8: the remainders' row joins its own)
         auto at = [&](int j, int e) {
-          return (R == 8 ? o[j][e] + o[j][e + 2] : o[j][2 * r + e]) * info.vmax;
+          return R == 8 ? o[j][e] + o[j][e + 2] : o[j][2 * r + e];
         };
 #pragma unroll
         for (int e = 0; e < 2; ++e)
@@ -912,7 +928,8 @@ __device__ void consumer(const FusedQ8Args& qa, const Smem& sm, int warp, int la
             dst[merge_chunk(8 * c + 4 * e + q, row)] =
                 make_float4(at(4 * q, e), at(4 * q + 1, e), at(4 * q + 2, e), at(4 * q + 3, e));
         if (c == 0) {
-          sm.mm[warp * R + row] = m_run[r] - kShift;
+          sm.mm[warp * R + row] = m_run[r];
+          sm.mn[warp * R + row] = n_run[r];
           sm.ml[warp * R + row] = l;
         }
       }
@@ -962,6 +979,7 @@ fused_dec_q8_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__
   sm.info = reinterpret_cast<StageInfo*>(base + L.info);
   sm.mo = reinterpret_cast<float*>(base + L.mo);
   sm.mm = reinterpret_cast<float*>(base + L.mm);
+  sm.mn = reinterpret_cast<float*>(base + L.mn);
   sm.ml = reinterpret_cast<float*>(base + L.ml);
   sm.desc = reinterpret_cast<PieceDesc*>(base + L.desc);
   sm.full = reinterpret_cast<uint64_t*>(base + L.bars);

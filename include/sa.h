@@ -489,8 +489,9 @@ sa_status sa_attention_ex(const float *q, const void *k_pages, const void *v_pag
  *
  * Kernels: batches of one query per sequence take the fused decode path under
  * the conditions given at sa_attention (8-bit: page_size a power of two of at
- * least 16, qhead <= 16), with products exact to 2^-21 and f32 sums; other
- * problems the tcgen05 kernel where it is supported (keys, values, queries and
+ * least 16, qhead <= 16), with q k products exact to 2^-21 of the row's largest
+ * q, p v products (scales included, whatever their spread) to 2^-21 or to 2^-28
+ * of the largest, and f32 sums; other problems the tcgen05 kernel where it is supported (keys, values, queries and
  * P rounded to bf16: code * scale is exact there under a power-of-two scale),
  * decode-shaped ones and the rest the general f32 FMA kernel.  SA_PATH_CUDA_CORE
  * means the general kernel.  head_dim: a multiple of 16, at most 256.  Codes

@@ -142,6 +142,89 @@ def test_fused_decode_scales(kind, scales, hq):
     check(w, t, vals, _gpu.TOL_F32, f"fused scales {scales} {kind}")
 
 
+def spread_workload(kind, hq, e, where, seed):
+    """A decode batch in which one page of each sequence takes nearly all of the
+    softmax (`where` "light") or as much of the output as the others (`where`
+    "even") while its V scale is 2^-e of theirs, or (`where` "heavy") has a share
+    of 2^-e of the softmax and a V scale of 2^e."""
+    hkv, d, ps, bs, topk = 2, 128, 16, 64, 6
+    w = inputs.gqa_decode(seed, batch=4, kv_min=500, kv_max=900, hq=hq, hkv=hkv, topk=topk)
+    rng = np.random.default_rng(seed)
+    sel = np.sort(np.argsort(rng.random((w.tq, hkv, 7)), axis=2)[:, :, :topk].astype(np.int32), axis=2)
+    w = replace(w, selected=sel)
+    t = _gpu.device_workload(replace(w, kv_dtype="f32"))
+    # every lane points along one direction of signs, the page's keys too
+    sign = rng.choice([-1.0, 1.0], (w.tq, hkv, d))
+    q = np.repeat(sign, hq // hkv, axis=1) * rng.uniform(0.9, 1.1, (w.tq, hq, 1))
+    t["q"] = torch.from_numpy(q.astype(np.float32)).cuda()
+    shape = (w.num_pages, hkv, ps, d)
+    k = rng.choice([-1.0, 0.0, 1.0], shape)
+    v = np.round(rng.standard_normal(shape) * 30).clip(-100, 100)
+    ks = np.full(shape[:2], 0.02)
+    vs = np.ones(shape[:2])
+    nat = e * math.log(2.0)
+    gain = {"light": nat + 20.0, "even": nat, "heavy": -nat}[where]
+    for i in range(w.tq):                     # (sequence i holds query i)
+        for h in range(hkv):
+            block = int(sel[i, h, rng.integers(topk)])
+            page = w.block_tables[i, block * (bs // ps) + int(rng.integers(bs // ps))]
+            c = 100.0
+            k[page, h] = sign[i, h] * c
+            # score gain = softmax_scale * d * c * ks
+            ks[page, h] = gain / (w.softmax_scale * d * c)
+            vs[page, h] = 2.0 ** (e if where == "heavy" else -e)
+    vals = {}
+    for name, x, s in (("k", k, ks), ("v", v, vs)):
+        codes = torch.from_numpy(x).cuda().to(torch.float32).to(TORCH[kind])
+        s = torch.from_numpy(s.astype(np.float32)).cuda()
+        t[name], t[name + "s"] = codes, s
+        vals[name] = (codes.double() * s.double()[:, :, None, None] if kind == "int8" else
+                      codes.float().double() * s.double()[:, :, None, None]).float().cpu().numpy()
+    return w, t, vals
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("hq", [8, 24])
+@pytest.mark.parametrize("where", ["light", "even", "heavy"])
+@pytest.mark.parametrize("e", [4, 12, 20, 28, 40, 60])
+def test_fused_decode_scales_far_apart(kind, hq, where, e):
+    """V scales up to 2^60 apart in one piece, the output from either end: what
+    a page adds keeps f32's class whatever the other pages' scales are, and
+    however the ranks are cut."""
+    w, t, vals = spread_workload(kind, hq, e, where, 71)
+    assert kernel(w, kind) == "fused_dec_kernel"
+    ref, ref_lse, _, _ = reference(w, t, vals)
+    size = np.abs(ref).max(axis=-1, keepdims=True)        # (no floor: outputs may be small)
+    for split in (0, 1, 4):
+        out, lse, _, _ = attend(w, t, split_edges=split)
+        got = out.cpu().numpy().astype(np.float64)
+        assert (np.abs(got - ref) / size).max() <= _gpu.TOL_F32
+        _gpu.compare_lse(lse.cpu().numpy(), ref_lse, 1e-4)
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("hq", [8, 24])
+@pytest.mark.parametrize("v_scale", [0.0, 2.0 ** -126, -(2.0 ** -60), 2.0 ** 100])
+def test_fused_decode_scales_at_the_ends(kind, hq, v_scale):
+    """V scales at the ends of f32's range, negative, and 0 for half of the pages
+    (their keys count in the softmax all the same)."""
+    w = inputs.gqa_decode(73, batch=3, kv_min=400, kv_max=700, hq=hq, hkv=2, topk=5)
+    t, vals = scaled_workload(w, kind, dirty=False)
+    s = torch.full_like(t["vs"], v_scale)
+    if v_scale == 0.0:
+        s[::2] = 0.5
+    vals["v"] = (t["v"].float() * s[:, :, None, None]).cpu().numpy()
+    t["vs"] = s
+    ref, ref_lse, _, _ = reference(w, t, vals)
+    size = np.abs(ref).max(axis=-1, keepdims=True)
+    for split in (0, 1):
+        out, lse, _, _ = attend(w, t, split_edges=split)
+        got = out.cpu().numpy().astype(np.float64)
+        # (outputs near 2^-126 are held in steps of 2^-149)
+        assert (np.abs(got - ref) <= _gpu.TOL_F32 * size + 2.0 ** -148).all()
+        _gpu.compare_lse(lse.cpu().numpy(), ref_lse, 1e-4)
+
+
 @pytest.mark.parametrize("split", [1, 3, 64])
 @pytest.mark.parametrize("partial", [None, "bf16"])
 def test_fused_decode_pieces(split, partial):
