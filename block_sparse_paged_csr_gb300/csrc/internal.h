@@ -4,6 +4,7 @@
 #include <atomic>
 #include <cstddef>
 #include <cstdint>
+#include <mutex>
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -226,23 +227,24 @@ cudaError_t launch_combine(const CombineArgs& a, cudaStream_t stream);
 int device_sm_count();
 
 // A kernel's dynamic shared-memory limit, raised once per device and size
-// instead of at every launch.  One static object per kernel; safe from several
-// host threads (a limit raised twice is the same limit).
+// instead of at every launch.  One static object per kernel.  Launches of
+// different sizes may meet on several host threads, and the attribute takes
+// whatever the last call gave it, so look, call and record are one step: a
+// smaller size never comes behind a larger one.
 struct SmemLimit {
   std::atomic<int> set[64] = {};
+  std::mutex raising;
   cudaError_t raise(const void* fn, int bytes) {
     int dev = 0;
     const cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
     const bool known = dev >= 0 && dev < 64;
     if (known && set[dev].load(std::memory_order_acquire) >= bytes) return cudaSuccess;
+    std::lock_guard<std::mutex> hold(raising);
+    if (known && set[dev].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
     const cudaError_t e =
         cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess && known) {
-      int was = set[dev].load(std::memory_order_relaxed);
-      while (was < bytes && !set[dev].compare_exchange_weak(was, bytes)) {
-      }
-    }
+    if (e == cudaSuccess && known) set[dev].store(bytes, std::memory_order_release);
     return e;
   }
 };
