@@ -45,10 +45,10 @@ __all__ = ["SAError", "Index", "sa_index_query_sizes", "sa_build_index",
            "sa_version", "allocate_index", "PATH_AUTO", "PATH_CUDA_CORE", "PATH_TENSOR_CORE",
            "PATH_TENSOR_CORE_TF32",
            "PATH_CUDA_CORE_GENERAL", "AttentionGraph", "sa_debug_stall", "sa_debug_cta_stats", "STALL_NONE",
-           "STALL_INDEX_BARRIER", "STALL_FUSED_COPIES"]
+           "STALL_INDEX_BARRIER", "STALL_FUSED_COPIES", "STALL_SELECT_COPIES"]
 
 #: sa_debug_stall sites (a test hook: see include/sa.h)
-STALL_NONE, STALL_INDEX_BARRIER, STALL_FUSED_COPIES = 0, 1, 2
+STALL_NONE, STALL_INDEX_BARRIER, STALL_FUSED_COPIES, STALL_SELECT_COPIES = 0, 1, 2, 3
 
 
 class SAError(RuntimeError):
@@ -855,7 +855,7 @@ def sa_clear_status(index: Index, stream=None) -> None:
 
 def sa_debug_stall(site: int, spin_limit: int = 0) -> None:
     """Test hook: make the bounded wait at ``site`` run out on every launch
-    from now on (STALL_INDEX_BARRIER, STALL_FUSED_COPIES), with ``spin_limit``
+    from now on (STALL_INDEX_BARRIER, STALL_FUSED_COPIES, STALL_SELECT_COPIES), with ``spin_limit``
     tries per wait (0 = the library default); STALL_NONE restores normal
     operation."""
     _check(_native.load().sa_debug_stall(int(site), int(spin_limit)), "sa_debug_stall")

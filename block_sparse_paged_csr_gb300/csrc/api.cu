@@ -937,7 +937,7 @@ sa_status sa_attention(const float* q, const void* k_pages, const void* v_pages,
 }
 
 sa_status sa_debug_stall(int32_t site, uint32_t spin_limit) {
-  if (site < sa::kStallNone || site > sa::kStallFusedCopies) return SA_ERR_INVALID_ARGUMENT;
+  if (site < sa::kStallNone || site > sa::kStallSelectCopies) return SA_ERR_INVALID_ARGUMENT;
   sa::g_stall_site.store(site, std::memory_order_relaxed);
   sa::g_spin_limit.store(spin_limit, std::memory_order_relaxed);
   return SA_OK;

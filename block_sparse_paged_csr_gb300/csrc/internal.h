@@ -51,7 +51,12 @@ int64_t index_hist_slot_bound(int64_t tq, int32_t topk);
 
 // Test hook (sa_debug_stall): a site whose bounded wait is made to run out,
 // and the tries a bounded wait takes before it gives up (0 = kSpinLimit).
-enum StallSite { kStallNone = 0, kStallIndexBarrier = 1, kStallFusedCopies = 2 };
+enum StallSite {
+  kStallNone = 0,
+  kStallIndexBarrier = 1,
+  kStallFusedCopies = 2,
+  kStallSelectCopies = 3
+};
 void debug_stall_setting(int* site, uint32_t* spin_limit);
 // Test hook (sa_debug_cta_stats): where the tensor-core forward adds up each
 // CTA's rows, units and busy cycles (NULL: nowhere), and its length in CTAs.

@@ -59,6 +59,8 @@ struct SelectArgs {
   int64_t stride;
   int32_t chunks;
   int64_t* status;
+  uint32_t spin;                       // tries of a bounded wait
+  int stall;                           // test hook: no copy is sent, so every wait on one runs out
 };
 
 // What a (query, kv head) row sees: its sequence and the number of blocks
@@ -329,6 +331,7 @@ block_score_kernel(const SelectArgs a) {
   __syncthreads();                                     // the barriers are there
   // rows of stage t in flight
   auto send = [&](int t) {
+    if (a.stall) return;
     const int id = ids[kSpan == 1 || t < kStages ? 0 : 1];
     const bool there = (lane >> 3) == t % kStages && id >= 0;
     const unsigned present = __ballot_sync(0xffffffffu, there);
@@ -417,8 +420,12 @@ block_score_kernel(const SelectArgs a) {
   for (int qi = 0; qi < kNQ; ++qi) l1[qi] = 0.f;
 #pragma unroll 1
   for (int st = 0; st < nst; ++st) {
-    if (!mbar_wait_bounded(&s_bar[warp][st % kRing], (st / kRing) & 1)) {
+    if (!mbar_wait_bounded(&s_bar[warp][st % kRing], (st / kRing) & 1, a.spin)) {
       if (lane == 0) report(a.status, SA_ERR_DEVICE_TIMEOUT);
+      // (the copies in flight end before the CTA does: stages up to st + kRing - 1
+      // have been sent)
+      for (int x = st; x < min(st + kRing, nst); ++x)
+        mbar_wait_bounded(&s_bar[warp][x % kRing], (x / kRing) & 1, a.spin);
       break;
     }
     {
@@ -691,6 +698,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) block_score_tile_kernel(const
   // not taken from the MMA.
   const uint32_t half_bytes = 2u * static_cast<uint32_t>(d);
   auto load_tile = [&](int t) {
+    if (a.stall) return;
     const int r = 16 * warp + (lane & 15), hi = lane >> 4;
     const int id = ids[t * kTileB + r];
     const unsigned present = __ballot_sync(0xffffffffu, id >= 0);
@@ -746,7 +754,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) block_score_tile_kernel(const
 
   bool late = false;                                   // a wait ran out: send no more
   for (int t = 0; t < tiles; ++t) {
-    if (!mbar_wait_bounded(s_bar + (t & 1), (t >> 1) & 1)) {
+    if (!mbar_wait_bounded(s_bar + (t & 1), (t >> 1) & 1, a.spin)) {
       if (lane == 0) report(a.status, SA_ERR_DEVICE_TIMEOUT);
       late = true;
     }
@@ -824,8 +832,8 @@ __global__ void __launch_bounds__(kTileThreads, 2) block_score_tile_kernel(const
     }
     if (__syncthreads_or(late)) {                      // (and the buffer is read)
       // (the copies in flight end before the CTA does)
-      mbar_wait_bounded(s_bar + (t & 1), (t >> 1) & 1);
-      if (t + 1 < tiles) mbar_wait_bounded(s_bar + ((t + 1) & 1), ((t + 1) >> 1) & 1);
+      mbar_wait_bounded(s_bar + (t & 1), (t >> 1) & 1, a.spin);
+      if (t + 1 < tiles) mbar_wait_bounded(s_bar + ((t + 1) & 1), ((t + 1) >> 1) & 1, a.spin);
       return;
     }
     if (t + 2 < tiles) load_tile(t + 2);
@@ -1557,6 +1565,10 @@ sa_status sa_select_blocks(const void* q, sa_dtype q_dtype, int64_t tq, int32_t 
   a.stride = l.stride;
   a.chunks = l.chunks;
   a.status = status;
+  int site = sa::kStallNone;
+  sa::debug_stall_setting(&site, &a.spin);
+  if (a.spin == 0) a.spin = sa::kSpinLimit;
+  a.stall = site == sa::kStallSelectCopies ? 1 : 0;
   int64_t longest = 0;
   for (int32_t b = 0; b < batch; ++b)
     longest = std::max(longest, cu_seqlens_q_host[b + 1] - cu_seqlens_q_host[b]);

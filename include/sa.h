@@ -668,6 +668,9 @@ sa_status sa_select_blocks(const void *q, sa_dtype q_dtype, int64_t tq, int32_t 
  *   site 2: the fused decode kernel's load warps issue no copy (its
  *           consumer, merge and metadata warps time out and return; no copy
  *           is ever in flight);
+ *   site 3: the score kernels of sa_select_blocks issue no copy of bounds
+ *           (the status goes to that call's status word; the selection is
+ *           unspecified);
  *   site 0: normal operation.
  * spin_limit: tries of each bounded wait from now on (0 = the library's
  * default, about a second).  Process-wide, read at every launch; not for

@@ -832,3 +832,20 @@ def test_prompts_in_a_row_and_in_a_graph():
         box.copy_(boxes[i])
         g.replay()
         assert torch.equal(sel, ref[i])
+
+
+@pytest.mark.parametrize("qo,d", [(1, 128), (3, 64), (20, 128), (3, 256)])
+def test_selection_waits_run_out(qo, d):
+    """Score kernels whose copies never come give up, wait (as long) for those
+    that may be in flight, report it and end; the next call is clean."""
+    q, bounds, rows, cu, lens = problem([qo, qo], [9000, 4000], 4, 2, d, 16, seed=41)
+    a = (q, bounds, cuda_i(rows, np.int32), cu, cuda_i(cu, np.int64), cuda_i(lens, np.int32), 16, 7, 1)
+    status = torch.zeros(1, dtype=torch.int64, device="cuda")
+    sa.sa_debug_stall(sa.STALL_SELECT_COPIES, 2000)
+    try:
+        sa.sa_select_blocks(*a, status=status)
+        torch.cuda.synchronize()
+    finally:
+        sa.sa_debug_stall(sa.STALL_NONE, 0)
+    assert int(status) == 9, sa.sa_status_string(int(status))
+    run_select(q, bounds, rows, cu, lens, 16, 7)
