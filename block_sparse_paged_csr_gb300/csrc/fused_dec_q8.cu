@@ -963,9 +963,10 @@ constexpr bool registers_fit() {
 }
 static_assert(registers_fit<8>() && registers_fit<16>(), "register shares");
 
+// (The name that sa_attention_kernel_name gives for the fused decode path.)
 template <bool kI8, int R>
 __global__ void __maxnreg__(Q8Regs<R>::kLaunch)
-fused_dec_q8_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ FusedQ8Args a) {
+fused_dec_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ FusedQ8Args a) {
   extern __shared__ unsigned char smem_raw[];
   constexpr Q8Layout L = q8_layout<R>();
   constexpr int S = Q8Cfg<R>::S, NC = 4 * Q8Cfg<R>::G;
@@ -1053,7 +1054,7 @@ cudaError_t launch_q8(const FusedQ8Args& a, cudaStream_t stream) {
   Q8Maps maps;
   if (!encode_pool(b.k_pages, rows, kb, &maps.k) || !encode_pool(b.v_pages, rows, kb, &maps.v))
     return cudaErrorNotSupported;
-  const void* fn = reinterpret_cast<const void*>(fused_dec_q8_kernel<kI8, R>);
+  const void* fn = reinterpret_cast<const void*>(fused_dec_kernel<kI8, R>);
   static SmemLimit limit;
   const cudaError_t err = limit.raise(fn, static_cast<int>(smem));
   if (err != cudaSuccess) return err;
@@ -1075,7 +1076,7 @@ cudaError_t launch_q8(const FusedQ8Args& a, cudaStream_t stream) {
   int site = kStallNone;
   debug_stall_setting(&site, &args.base.spin_limit);
   args.base.stall = site == kStallFusedCopies;
-  return cudaLaunchKernelEx(&cfg, fused_dec_q8_kernel<kI8, R>, maps, args);
+  return cudaLaunchKernelEx(&cfg, fused_dec_kernel<kI8, R>, maps, args);
 }
 
 }  // namespace

@@ -357,7 +357,8 @@ const char *sa_forward_kernel_name(int64_t tq, int32_t batch, int32_t hq, int32_
 /*
  * The kernel that sa_attention / sa_forward_combine run for steps 2 and 3
  * with this `causal` mode: "fused_dec_kernel" on the fused decode path (see
- * sa_attention), else the name sa_forward_kernel_name gives; NULL where the
+ * sa_attention; a kernel of that name for the f32 and bf16 caches and another
+ * for the 8-bit ones), else the name sa_forward_kernel_name gives; NULL where the
  * call would be refused.  Host only (reads cu_seqlens_q_host[0..batch]).
  */
 const char *sa_attention_kernel_name(int64_t tq, int32_t batch, const int64_t *cu_seqlens_q_host,

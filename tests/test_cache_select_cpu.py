@@ -289,3 +289,29 @@ def test_pool_of_other_sizes(shape):
     with pytest.raises(ValueError, match="k_pages must be"):
         sa.sa_forward_combine(q, codes, codes, types.SimpleNamespace(c=index), sel, [0, 1], None, None,
                               i32, 4, 128, 64, 16, 0.1, True, k_scales=scales, v_scales=scales)
+
+
+def test_kernel_names_are_kernels():
+    """What the name queries answer is the name of a kernel in the file that
+    serves the cache type (a profiling script filters by it)."""
+    import os
+    import re
+
+    import block_sparse_paged_csr_gb300 as sa
+
+    csrc = os.path.join(os.path.dirname(sa.__file__), "csrc")
+
+    def kernels(file):
+        with open(os.path.join(csrc, file)) as f:
+            return set(re.findall(r"__global__[^;{]*?\b(\w+)\(const|__global__[^;{]*?\b(\w+)\(ForwardArgs",
+                                  f.read()))
+
+    one, many = np.arange(5, dtype=np.int64), np.array([0, 40, 80], np.int64)
+    for kind in ("f32", "bf16", "e4m3", "int8"):
+        eight = kind in ("e4m3", "int8")
+        for cu, d, path, file in (
+                (one, 128, sa.PATH_AUTO, "fused_dec_q8.cu" if eight else "fused_dec.cu"),
+                (many, 128, sa.PATH_AUTO, "forward_tc.cu"),
+                (many, 64, sa.PATH_AUTO, "forward_cc.cu")):
+            name = sa.sa_attention_kernel_name(cu, 1000, 8, 32, d, 64, 16, kind, path=path)
+            assert name in {n for pair in kernels(file) for n in pair}, (kind, name, file)
