@@ -258,8 +258,9 @@ def sa_build_index(selected, cu_seqlens_q_host, cu_seqlens_q, used_kv_lens, max_
     if index is None:
         index = allocate_index(tq, hkv, topk, max(batch, 1), max_pages, block_size, page_size,
                                dev)
-    _check(_native.load().sa_build_index(
-        _ptr(selected), tq, hkv, topk, _host_ptr(cu_h), _ptr(cu_seqlens_q),
+    _check(_on(
+        dev, _native.load().sa_build_index, _ptr(selected), tq, hkv, topk, _host_ptr(cu_h),
+        _ptr(cu_seqlens_q),
         batch, _ptr(used_kv_lens), max_pages, block_size, page_size, split_edges,
         ctypes.byref(index.c), _stream(stream, dev)), "sa_build_index")
     return index
@@ -280,8 +281,9 @@ def sa_build_index_no_alloc(selected, cu_seqlens_q_host, cu_seqlens_q, used_kv_l
     _require(cu_seqlens_q, torch.int64, "cu_seqlens_q", dev)
     if used_kv_lens is not None:
         _require(used_kv_lens, torch.int32, "used_kv_lens", dev)
-    _check(_native.load().sa_build_index_no_alloc(
-        _ptr(selected), tq, hkv, topk, _host_ptr(cu_h), _ptr(cu_seqlens_q),
+    _check(_on(
+        dev, _native.load().sa_build_index_no_alloc, _ptr(selected), tq, hkv, topk, _host_ptr(cu_h),
+        _ptr(cu_seqlens_q),
         cu_h.size - 1, _ptr(used_kv_lens), max_pages, block_size, page_size, split_edges,
         ctypes.byref(index.c), _stream(stream, dev)), "sa_build_index_no_alloc")
     return index
@@ -445,9 +447,9 @@ def sa_forward(q, k_pages, v_pages, index: Index, block_tables, cu_seqlens_q, us
         if q_scratch.device != dev or q_scratch.numel() * q_scratch.element_size() < need:
             raise ValueError(f"q_scratch needs {need} bytes on {dev}")
     if ocode or q_scratch is not None:
-        _check(L.sa_forward_ex(*head, ocode, *tail, _ptr(q_scratch)), "sa_forward_ex")
+        _check(_on(dev, L.sa_forward_ex, *head, ocode, *tail, _ptr(q_scratch)), "sa_forward_ex")
     else:
-        _check(L.sa_forward(*head, *tail), "sa_forward")
+        _check(_on(dev, L.sa_forward, *head, *tail), "sa_forward")
     return o_partial, m_partial, l_partial
 
 
@@ -466,9 +468,9 @@ def sa_combine(index: Index, o_partial, m_partial, l_partial, hq, head_dim, out=
     tail = (_ptr(o_partial), _ptr(m_partial), _ptr(l_partial), hq, head_dim, _ptr(out), _ptr(lse),
             _stream(stream, dev))
     if ocode:
-        _check(L.sa_combine_ex(ctypes.byref(index.c), ocode, *tail), "sa_combine_ex")
+        _check(_on(dev, L.sa_combine_ex, ctypes.byref(index.c), ocode, *tail), "sa_combine_ex")
     else:
-        _check(L.sa_combine(ctypes.byref(index.c), *tail), "sa_combine")
+        _check(_on(dev, L.sa_combine, ctypes.byref(index.c), *tail), "sa_combine")
     return out, lse
 
 
@@ -515,9 +517,9 @@ def sa_forward_combine(q, k_pages, v_pages, index: Index, selected, cu_seqlens_q
         return out, lse, partials
     head = (_ptr(q), _ptr(k_pages), _ptr(v_pages), num_pages, kvd, *mid)
     if ocode:
-        _check(L.sa_forward_combine_ex(*head, ocode, *tail), "sa_forward_combine_ex")
+        _check(_on(dev, L.sa_forward_combine_ex, *head, ocode, *tail), "sa_forward_combine_ex")
     else:
-        _check(L.sa_forward_combine(*head, *tail), "sa_forward_combine")
+        _check(_on(dev, L.sa_forward_combine, *head, *tail), "sa_forward_combine")
     return out, lse, partials
 
 
@@ -570,9 +572,9 @@ def sa_attention(q, k_pages, v_pages, selected, cu_seqlens_q_host, cu_seqlens_q,
         return out, lse, index, partials
     head = (_ptr(q), _ptr(k_pages), _ptr(v_pages), num_pages, kvd, *mid)
     if ocode:
-        _check(L.sa_attention_ex(*head, ocode, *tail), "sa_attention_ex")
+        _check(_on(dev, L.sa_attention_ex, *head, ocode, *tail), "sa_attention_ex")
     else:
-        _check(L.sa_attention(*head, *tail), "sa_attention")
+        _check(_on(dev, L.sa_attention, *head, *tail), "sa_attention")
     return out, lse, index, partials
 
 
@@ -604,7 +606,7 @@ class AttentionGraph:
         if status != 0:
             raise SAError(status, "AttentionGraph (eager call)")
         self.graph = torch.cuda.CUDAGraph()
-        with torch.cuda.graph(self.graph):
+        with torch.cuda.device(q.device), torch.cuda.graph(self.graph):
             sa_attention(*args, index=self.index, partials=self.partials, out=self.out,
                          lse=self.lse, **kw)
 
@@ -844,13 +846,13 @@ def sa_select_blocks(q, bounds, bound_tables, cu_seqlens_q_host, cu_seqlens_q, u
 
 def sa_get_status(index: Index, stream=None) -> int:
     """Synchronise and return the device status code (0 = OK)."""
-    return int(_native.load().sa_get_status(ctypes.byref(index.c),
-                                            _stream(stream, index.device)))
+    return int(_on(index.device, _native.load().sa_get_status, ctypes.byref(index.c),
+                   _stream(stream, index.device)))
 
 
 def sa_clear_status(index: Index, stream=None) -> None:
-    _check(_native.load().sa_clear_status(ctypes.byref(index.c), _stream(stream, index.device)),
-           "sa_clear_status")
+    _check(_on(index.device, _native.load().sa_clear_status, ctypes.byref(index.c),
+               _stream(stream, index.device)), "sa_clear_status")
 
 
 def sa_debug_stall(site: int, spin_limit: int = 0) -> None:

@@ -432,3 +432,62 @@ def test_serving_steps(kind, act):
         assert _gpu.row_error(out.float().cpu().numpy(), ref) <= tol
         lens = lens + 1
         qo = np.ones(batch, np.int64)
+
+
+def test_every_launch_names_its_device(monkeypatch):
+    """Each call to the library that launches or synchronises is made with the
+    device of its tensors as the current one."""
+    w = inputs.small("gqa_decode", seed=63)
+    made = set()
+    on = sa._on
+
+    def record(dev, fn, *args):
+        assert dev == torch.device("cuda", 0)
+        made.add(fn.__name__)
+        return on(dev, fn, *args)
+
+    monkeypatch.setattr(sa, "_on", record)
+    wide = _gpu.device_workload(w)
+    eight, _ = scaled_workload(w, "int8")
+    for t, kw in ((wide, {}), (eight, dict(k_scales=eight["ks"], v_scales=eight["vs"]))):
+        for partial in (None, "bf16"):
+            args = (w.hq, w.hkv, w.head_dim, w.block_size, w.page_size, w.softmax_scale, w.causal)
+            idx = sa.sa_build_index(t["selected"], w.cu_seqlens_q, t["cu"], t["used"], w.max_pages,
+                                    w.block_size, w.page_size)
+            sa.sa_build_index_no_alloc(t["selected"], w.cu_seqlens_q, t["cu"], t["used"], idx,
+                                       w.max_pages, w.block_size, w.page_size)
+            o, m, l = sa.sa_forward(t["q"], t["k"], t["v"], idx, t["bt"], t["cu"], t["used"], *args,
+                                    partial_dtype=partial, **kw)
+            sa.sa_combine(idx, o, m, l, w.hq, w.head_dim)
+            sa.sa_forward_combine(t["q"], t["k"], t["v"], idx, t["selected"], w.cu_seqlens_q, t["cu"],
+                                  t["used"], t["bt"], args[0], *args[2:], partial_dtype=partial, **kw)
+            sa.sa_attention(t["q"], t["k"], t["v"], t["selected"], w.cu_seqlens_q, t["cu"], t["used"],
+                            t["bt"], *args, partial_dtype=partial, **kw)
+            assert sa.sa_get_status(idx) == 0
+            sa.sa_clear_status(idx)
+    assert made == {"sa_build_index", "sa_build_index_no_alloc", "sa_forward", "sa_forward_ex",
+                    "sa_forward_scaled", "sa_combine", "sa_combine_ex", "sa_forward_combine",
+                    "sa_forward_combine_ex", "sa_forward_combine_scaled", "sa_attention",
+                    "sa_attention_ex", "sa_attention_scaled", "sa_get_status", "sa_clear_status"}
+
+
+@pytest.mark.parametrize("current,device,switched", [(0, 0, False), (1, 0, True), (0, 1, True)])
+def test_device_switch(monkeypatch, current, device, switched):
+    """_on makes the tensors' device current where it is not (the devices are
+    names here: the call is a Python function)."""
+    seen = []
+
+    class Device:
+        def __init__(self, d):
+            self.d = d
+
+        def __enter__(self):
+            seen.append(("in", self.d.index))
+
+        def __exit__(self, *a):
+            seen.append(("out", self.d.index))
+
+    monkeypatch.setattr(sa, "_current_device", lambda: current)
+    monkeypatch.setattr(sa.torch.cuda, "device", Device)
+    assert sa._on(torch.device("cuda", device), lambda x: x + 1, 4) == 5
+    assert seen == ([("in", device), ("out", device)] if switched else [])
