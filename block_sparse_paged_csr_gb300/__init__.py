@@ -27,6 +27,7 @@ Around them, for serving:
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from dataclasses import dataclass
 
@@ -86,6 +87,16 @@ def _stream(stream, device):
     if stream is None:
         return _raw_stream(device)
     return stream.cuda_stream
+
+
+def _allocating(stream):
+    """Where a call makes its buffers: on the stream that is going to use them, so
+    that memory freed elsewhere and still in use there is not handed out (the
+    current stream where the call names none)."""
+    return _NOTHING if stream is None else torch.cuda.stream(stream)
+
+
+_NOTHING = contextlib.nullcontext()
 
 
 def _raw_stream(device):
@@ -256,8 +267,9 @@ def sa_build_index(selected, cu_seqlens_q_host, cu_seqlens_q, used_kv_lens, max_
     if used_kv_lens is not None:
         _require(used_kv_lens, torch.int32, "used_kv_lens", dev)
     if index is None:
-        index = allocate_index(tq, hkv, topk, max(batch, 1), max_pages, block_size, page_size,
-                               dev)
+        with _allocating(stream):
+            index = allocate_index(tq, hkv, topk, max(batch, 1), max_pages, block_size, page_size,
+                                   dev)
     _check(_on(
         dev, _native.load().sa_build_index, _ptr(selected), tq, hkv, topk, _host_ptr(cu_h),
         _ptr(cu_seqlens_q),
@@ -425,12 +437,13 @@ def sa_forward(q, k_pages, v_pages, index: Index, block_tables, cu_seqlens_q, us
     num_pages = k_pages.numel() // page_elems if page_elems > 0 else 0
     rows = partial_rows(index, hq) if hkv > 0 and hq % max(hkv, 1) == 0 else 1
     odt, ocode = _partial_dtype(partial_dtype, o_partial)
-    if o_partial is None:
-        o_partial = torch.empty((rows, head_dim), dtype=odt, device=dev)
-    if m_partial is None:
-        m_partial = torch.empty(rows, dtype=torch.float32, device=dev)
-    if l_partial is None:
-        l_partial = torch.empty(rows, dtype=torch.float32, device=dev)
+    with _allocating(stream):
+        if o_partial is None:
+            o_partial = torch.empty((rows, head_dim), dtype=odt, device=dev)
+        if m_partial is None:
+            m_partial = torch.empty(rows, dtype=torch.float32, device=dev)
+        if l_partial is None:
+            l_partial = torch.empty(rows, dtype=torch.float32, device=dev)
     L = _native.load()
     mid = (ctypes.byref(index.c), _ptr(block_tables), _ptr(cu_seqlens_q), _ptr(used_kv_lens), hq,
            hkv, head_dim, block_size, page_size, softmax_scale, _causal(causal))
@@ -460,10 +473,11 @@ def sa_combine(index: Index, o_partial, m_partial, l_partial, hq, head_dim, out=
     dev = o_partial.device
     tq = index.c.tq
     _, ocode = _partial_dtype(None, o_partial)
-    if out is None:
-        out = torch.empty((tq, hq, head_dim), dtype=torch.float32, device=dev)
-    if lse is None and with_lse:
-        lse = torch.empty((tq, hq), dtype=torch.float32, device=dev)
+    with _allocating(stream):
+        if out is None:
+            out = torch.empty((tq, hq, head_dim), dtype=torch.float32, device=dev)
+        if lse is None and with_lse:
+            lse = torch.empty((tq, hq), dtype=torch.float32, device=dev)
     L = _native.load()
     tail = (_ptr(o_partial), _ptr(m_partial), _ptr(l_partial), hq, head_dim, _ptr(out), _ptr(lse),
             _stream(stream, dev))
@@ -495,14 +509,15 @@ def sa_forward_combine(q, k_pages, v_pages, index: Index, selected, cu_seqlens_q
     cu_h = _host_i64(cu_seqlens_q_host)
     rows = partial_rows(index, hq) if hkv > 0 and hq % max(hkv, 1) == 0 else 1
     odt, ocode = _partial_dtype(partial_dtype, None if partials is None else partials[0])
-    if partials is None:
-        partials = (torch.empty((rows, head_dim), dtype=odt, device=dev),
-                    torch.empty(rows, dtype=torch.float32, device=dev),
-                    torch.empty(rows, dtype=torch.float32, device=dev))
-    if out is None:
-        out = torch.empty((c.tq, hq, head_dim), dtype=q.dtype, device=dev)
-    if lse is None and with_lse:
-        lse = torch.empty((c.tq, hq), dtype=torch.float32, device=dev)
+    with _allocating(stream):
+        if partials is None:
+            partials = (torch.empty((rows, head_dim), dtype=odt, device=dev),
+                        torch.empty(rows, dtype=torch.float32, device=dev),
+                        torch.empty(rows, dtype=torch.float32, device=dev))
+        if out is None:
+            out = torch.empty((c.tq, hq, head_dim), dtype=q.dtype, device=dev)
+        if lse is None and with_lse:
+            lse = torch.empty((c.tq, hq), dtype=torch.float32, device=dev)
     page_elems = hkv * page_size * head_dim
     num_pages = k_pages.numel() // page_elems if page_elems > 0 else 0
     o, m, l = partials
@@ -545,19 +560,20 @@ def sa_attention(q, k_pages, v_pages, selected, cu_seqlens_q_host, cu_seqlens_q,
     cu_h = _host_i64(cu_seqlens_q_host)
     batch = cu_h.size - 1
     max_pages = block_tables.shape[1]
-    if index is None:
-        index = allocate_index(tq, hkv_s, topk, max(batch, 1), max_pages, block_size, page_size,
-                               dev)
     rows = max(tq * hkv_s * topk * (hq // max(hkv_s, 1)), 1)
     odt, ocode = _partial_dtype(partial_dtype, None if partials is None else partials[0])
-    if partials is None:
-        partials = (torch.empty((rows, head_dim), dtype=odt, device=dev),
-                    torch.empty(rows, dtype=torch.float32, device=dev),
-                    torch.empty(rows, dtype=torch.float32, device=dev))
-    if out is None:
-        out = torch.empty((tq, hq, head_dim), dtype=q.dtype, device=dev)
-    if lse is None and with_lse:
-        lse = torch.empty((tq, hq), dtype=torch.float32, device=dev)
+    with _allocating(stream):
+        if index is None:
+            index = allocate_index(tq, hkv_s, topk, max(batch, 1), max_pages, block_size,
+                                   page_size, dev)
+        if partials is None:
+            partials = (torch.empty((rows, head_dim), dtype=odt, device=dev),
+                        torch.empty(rows, dtype=torch.float32, device=dev),
+                        torch.empty(rows, dtype=torch.float32, device=dev))
+        if out is None:
+            out = torch.empty((tq, hq, head_dim), dtype=q.dtype, device=dev)
+        if lse is None and with_lse:
+            lse = torch.empty((tq, hq), dtype=torch.float32, device=dev)
     page_elems = hkv * page_size * head_dim
     num_pages = k_pages.numel() // page_elems if page_elems > 0 else 0
     o, m, l = partials
@@ -821,16 +837,15 @@ def sa_select_blocks(q, bounds, bound_tables, cu_seqlens_q_host, cu_seqlens_q, u
                               ("bound_tables",))
     msb = bound_tables.shape[1]
     if selected is None:
-        selected = torch.empty((tq, hkv, int(topk)), dtype=torch.int32, device=dev)
+        with _allocating(stream):
+            selected = torch.empty((tq, hkv, int(topk)), dtype=torch.int32, device=dev)
     else:
         _require(selected, torch.int32, "selected", dev)
         if selected.shape != (tq, hkv, topk):
             raise ValueError(f"selected must be {(tq, hkv, int(topk))}, got {tuple(selected.shape)}")
     if workspace is None:
-        workspace = allocate_select_workspace(tq, batch, hkv, d, msb, dev)
-        if stream is not None:
-            workspace.record_stream(stream)
-            selected.record_stream(stream)
+        with _allocating(stream):
+            workspace = allocate_select_workspace(tq, batch, hkv, d, msb, dev)
     else:
         _require(workspace, torch.uint8, "workspace", dev)
     base = workspace.data_ptr()

@@ -491,3 +491,38 @@ def test_device_switch(monkeypatch, current, device, switched):
     monkeypatch.setattr(sa.torch.cuda, "device", Device)
     assert sa._on(torch.device("cuda", device), lambda x: x + 1, 4) == 5
     assert seen == ([("in", device), ("out", device)] if switched else [])
+
+
+def test_buffers_belong_to_the_stream_of_the_call():
+    """What a call allocates comes from the stream that it names, where memory
+    that the current stream freed and still uses is not handed out."""
+    w = inputs.small("gqa_decode", seed=65)
+    t, vals = scaled_workload(w, "int8")
+    ref, ref_lse, _, _ = reference(w, t, vals)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    out, lse, idx, parts = attend(w, t, stream=side)
+    bounds = torch.zeros((4, w.hkv, 2, w.head_dim), dtype=torch.bfloat16, device="cuda")
+    tables = torch.zeros((w.batch, 4), dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    sel = sa.sa_select_blocks(t["q"], bounds, tables, w.cu_seqlens_q, t["cu"], t["used"],
+                              w.block_size, 2, True, stream=side)
+    i2 = sa.sa_build_index(t["selected"], w.cu_seqlens_q, t["cu"], t["used"], w.max_pages,
+                           w.block_size, w.page_size, stream=side)
+    o, m, l = sa.sa_forward(t["q"], t["k"], t["v"], i2, t["bt"], t["cu"], t["used"], w.hq, w.hkv,
+                            w.head_dim, w.block_size, w.page_size, w.softmax_scale, w.causal,
+                            k_scales=t["ks"], v_scales=t["vs"], stream=side)
+    out2, lse2 = sa.sa_combine(i2, o, m, l, w.hq, w.head_dim, stream=side)
+    out3, lse3, p3 = sa.sa_forward_combine(
+        t["q"], t["k"], t["v"], i2, t["selected"], w.cu_seqlens_q, t["cu"], t["used"], t["bt"], w.hq,
+        w.head_dim, w.block_size, w.page_size, w.softmax_scale, w.causal, k_scales=t["ks"],
+        v_scales=t["vs"], stream=side)
+    side.synchronize()
+    for x in (out, out2, out3):
+        assert _gpu.row_error(x.cpu().numpy(), ref) <= _gpu.TOL_F32
+    segments = torch.cuda.memory_snapshot()
+    for x in (out, lse, *parts, idx.totals, idx.workspace, idx.edges, sel, i2.inv, o, m, l, out2, lse2,
+              out3, lse3, *p3):
+        of = [s["stream"] for s in segments
+              if s["address"] <= x.data_ptr() < s["address"] + s["total_size"]]
+        assert of == [side.cuda_stream]
