@@ -270,6 +270,8 @@ def sa_build_index(selected, cu_seqlens_q_host, cu_seqlens_q, used_kv_lens, max_
         with _allocating(stream):
             index = allocate_index(tq, hkv, topk, max(batch, 1), max_pages, block_size, page_size,
                                    dev)
+    else:
+        _check_index(index, tq, hkv, topk, batch, max_pages, block_size, page_size)
     _check(_on(
         dev, _native.load().sa_build_index, _ptr(selected), tq, hkv, topk, _host_ptr(cu_h),
         _ptr(cu_seqlens_q),
@@ -293,6 +295,7 @@ def sa_build_index_no_alloc(selected, cu_seqlens_q_host, cu_seqlens_q, used_kv_l
     _require(cu_seqlens_q, torch.int64, "cu_seqlens_q", dev)
     if used_kv_lens is not None:
         _require(used_kv_lens, torch.int32, "used_kv_lens", dev)
+    _check_index(index, tq, hkv, topk, cu_h.size - 1, max_pages, block_size, page_size)
     _check(_on(
         dev, _native.load().sa_build_index_no_alloc, _ptr(selected), tq, hkv, topk, _host_ptr(cu_h),
         _ptr(cu_seqlens_q),
@@ -312,20 +315,6 @@ def _kv_dtype(k):
 _DTYPE_NAMES = {"f32": DTYPE_F32, "bf16": DTYPE_BF16, "e4m3": DTYPE_E4M3, "int8": DTYPE_INT8}
 
 
-@dataclass
-class _Scaled:
-    """An 8-bit cache's part of a call: types and scale pointers."""
-
-    kv_code: int
-    q_code: int
-    out_dtype: torch.dtype
-    scales: tuple
-
-    def head(self, q, k_pages, v_pages, num_pages):
-        return (_ptr(q), self.q_code, _ptr(k_pages), _ptr(v_pages), *self.scales, num_pages,
-                self.kv_code)
-
-
 def _check_pool(k_pages, hkv, page_size, head_dim):
     """The scales are looked up by page id, so an 8-bit pool has to be what the
     call's sizes say: with other sizes an id inside the pool could lie past the
@@ -336,30 +325,104 @@ def _check_pool(k_pages, hkv, page_size, head_dim):
 
 
 def _scaled(q, k_pages, v_pages, k_scales, v_scales, hkv, page_size, head_dim):
-    """Checks of a call over an 8-bit cache; None for the other cache types,
-    which take no scales."""
+    """Checks of a call over an 8-bit cache: (q's type, the cache's, the scales'
+    addresses); None for the other cache types, which take no scales."""
     dtype = k_pages.dtype
     if dtype is not torch.float8_e4m3fn and dtype is not torch.int8:
         if k_scales is not None or v_scales is not None:
             raise ValueError(f"a {k_pages.dtype} cache has no scales")
         return None
-    code = _cache_dtype(k_pages, "k_pages")
+    code, act, index = _CACHE_DTYPES[dtype], _ACT_DTYPES.get(q.dtype), q.get_device()
+    try:
+        shape = k_pages.shape
+        pool = shape[:2]
+        if (act is not None and index >= 0 and q.is_contiguous() and
+                shape[1:] == (hkv, page_size, head_dim) and v_pages.shape == shape and
+                k_scales.shape == pool and v_scales.shape == pool and
+                _alike(index, dtype, k_pages, v_pages) and
+                _alike(index, torch.float32, k_scales, v_scales)):
+            return act, code, k_scales.data_ptr(), v_scales.data_ptr()
+    except AttributeError:
+        pass
+    _cache_dtype(k_pages, "k_pages")
     _check_pool(k_pages, hkv, page_size, head_dim)
-    if q.dtype not in _ACT_DTYPES:
+    if act is None:
         raise TypeError(f"q must be float32 or bfloat16, got {q.dtype}")
     _require(q, q.dtype, "q")
-    if not _alike(q.get_device(), dtype, k_pages, v_pages):
-        _require(k_pages, dtype, "k_pages", q.device)
-        _require(v_pages, dtype, "v_pages", q.device)
+    _require(k_pages, dtype, "k_pages", q.device)
+    _require(v_pages, dtype, "v_pages", q.device)
     if v_pages.shape != k_pages.shape:
         raise ValueError("k_pages and v_pages must have one shape")
     ks, vs = _scales(k_scales, k_pages, "k_scales"), _scales(v_scales, v_pages, "v_scales")
-    return _Scaled(code, _ACT_DTYPES[q.dtype], q.dtype, (_ptr(ks), _ptr(vs)))
+    return act, code, _ptr(ks), _ptr(vs)
 
 
-def _check_out(out, dtype):
-    if out is not None and out.dtype != dtype:
-        raise TypeError(f"out must be {dtype}, got {out.dtype}")
+def _scaled_head(x, q, k_pages, v_pages, num_pages):
+    """The first arguments of the entry points with scales."""
+    act, code, ks, vs = x
+    return (q.data_ptr(), act, k_pages.data_ptr(), v_pages.data_ptr(), ks, vs, num_pages, code)
+
+
+def _check_call(dev, q, q_elems, tables, batch, max_pages, cu_seqlens_q, used_kv_lens,
+                selected=None, shape=None):
+    """That the tensors of a call are of its device, dense, and as large as its
+    sizes say: the kernels take addresses and would read on past their ends."""
+    i32 = [tables] if selected is None else [tables, selected]
+    if used_kv_lens is not None:
+        i32.append(used_kv_lens)
+    try:
+        if (_alike(dev.index, torch.int32, *i32) and _alike(dev.index, torch.int64, cu_seqlens_q) and
+                q.numel() >= q_elems and tables.numel() >= batch * max_pages and
+                cu_seqlens_q.numel() > batch and
+                (used_kv_lens is None or used_kv_lens.numel() >= batch) and
+                (selected is None or selected.shape == shape)):
+            return
+    except AttributeError:
+        pass
+    _require(tables, torch.int32, "block_tables", dev)
+    _require(cu_seqlens_q, torch.int64, "cu_seqlens_q", dev)
+    if used_kv_lens is not None:
+        _require(used_kv_lens, torch.int32, "used_kv_lens", dev)
+        if used_kv_lens.numel() < batch:
+            raise ValueError(f"used_kv_lens needs {batch} values, has {used_kv_lens.numel()}")
+    if selected is not None:
+        _require(selected, torch.int32, "selected", dev)
+        if tuple(selected.shape) != shape:
+            raise ValueError(f"selected must be {shape}, got {tuple(selected.shape)}")
+    for t, n, name in ((q, q_elems, "q"), (tables, batch * max_pages, "block_tables"),
+                       (cu_seqlens_q, batch + 1, "cu_seqlens_q")):
+        if t.numel() < n:
+            raise ValueError(f"{name} needs {n} values, has {t.numel()}")
+
+
+def _check_room(dev, *buffers):
+    """That buffers handed in (tensor, dtype, elements, name) hold what the call
+    writes to them."""
+    index = dev.index
+    for t, dtype, n, name in buffers:
+        if t is not None and not (t.dtype is dtype and t.get_device() == index and
+                                  t.is_contiguous() and t.numel() >= n):
+            _require(t, dtype, name, dev)
+            raise ValueError(f"{name} needs {n} values, has {t.numel()}")
+
+
+def _check_partials(dev, partials, odt, rows, head_dim):
+    if partials is not None:
+        o, m, l = partials
+        _check_room(dev, (o, odt, rows * head_dim, "o_partial"),
+                    (m, torch.float32, rows, "m_partial"), (l, torch.float32, rows, "l_partial"))
+
+
+def _check_index(index, tq, hkv, topk, batch, max_pages, block_size, page_size):
+    """That an index handed in has room for one over these sizes (what the library
+    refuses is left to it)."""
+    if min(tq, hkv, topk, batch, block_size, page_size) <= 0 or block_size % page_size:
+        return
+    z, n = index.sizes, tq * hkv * topk
+    nbs = batch * (max_pages // (block_size // page_size))
+    if (z["edges"] < 2 * n or z["inv"] < n or z["splits"] < 4 * n or z["sel_slots"] < hkv * nbs or
+            z["sel_offsets"] < hkv * (nbs + 1) or z["num_sel"] < hkv):
+        raise ValueError("index was allocated for a smaller problem")
 
 
 def sa_forward_kernel_name(tq, batch, hkv, hq, head_dim, block_size, page_size, kv_dtype="f32",
@@ -392,6 +455,8 @@ def _partial_dtype(partial_dtype, o_partial):
     given (float32 or bfloat16), else ``partial_dtype`` ("f32" default, or
     "bf16": 16-bit o partials, an opt-in the pages do not have)."""
     if o_partial is not None:
+        if partial_dtype is None and o_partial.dtype in _ACT_DTYPES:
+            return o_partial.dtype, _ACT_DTYPES[o_partial.dtype]
         for name, (dt, code) in _PARTIAL_DTYPES.items():
             if o_partial.dtype == dt:
                 if partial_dtype not in (None, name):
@@ -429,14 +494,14 @@ def sa_forward(q, k_pages, v_pages, index: Index, block_tables, cu_seqlens_q, us
     dev = q.device
     _require(k_pages, k_pages.dtype, "k_pages", dev)
     _require(v_pages, k_pages.dtype, "v_pages", dev)
-    _require(block_tables, torch.int32, "block_tables", dev)
-    _require(cu_seqlens_q, torch.int64, "cu_seqlens_q", dev)
-    if used_kv_lens is not None:
-        _require(used_kv_lens, torch.int32, "used_kv_lens", dev)
+    c = index.c
+    _check_call(dev, q, c.tq * hq * head_dim, block_tables, c.batch, c.max_pages, cu_seqlens_q,
+                used_kv_lens)
     page_elems = hkv * page_size * head_dim
     num_pages = k_pages.numel() // page_elems if page_elems > 0 else 0
     rows = partial_rows(index, hq) if hkv > 0 and hq % max(hkv, 1) == 0 else 1
     odt, ocode = _partial_dtype(partial_dtype, o_partial)
+    _check_partials(dev, (o_partial, m_partial, l_partial), odt, rows, head_dim)
     with _allocating(stream):
         if o_partial is None:
             o_partial = torch.empty((rows, head_dim), dtype=odt, device=dev)
@@ -451,8 +516,8 @@ def sa_forward(q, k_pages, v_pages, index: Index, block_tables, cu_seqlens_q, us
     if x is not None:
         if q_scratch is not None:
             raise ValueError("q_scratch does not apply to an 8-bit cache")
-        _check(_on(dev, L.sa_forward_scaled, *x.head(q, k_pages, v_pages, num_pages), *mid, ocode,
-                   *tail), "sa_forward_scaled")
+        _check(_on(dev, L.sa_forward_scaled, *_scaled_head(x, q, k_pages, v_pages, num_pages),
+                   *mid, ocode, *tail), "sa_forward_scaled")
         return o_partial, m_partial, l_partial
     head = (_ptr(q), _ptr(k_pages), _ptr(v_pages), num_pages, kvd, *mid)
     if q_scratch is not None:
@@ -473,6 +538,8 @@ def sa_combine(index: Index, o_partial, m_partial, l_partial, hq, head_dim, out=
     dev = o_partial.device
     tq = index.c.tq
     _, ocode = _partial_dtype(None, o_partial)
+    _check_room(dev, (out, torch.float32, tq * hq * head_dim, "out"),
+                (lse, torch.float32, tq * hq, "lse"))
     with _allocating(stream):
         if out is None:
             out = torch.empty((tq, hq, head_dim), dtype=torch.float32, device=dev)
@@ -501,14 +568,20 @@ def sa_forward_combine(q, k_pages, v_pages, index: Index, selected, cu_seqlens_q
     if x is None:
         _require(q, torch.float32, "q")
         kvd = _kv_dtype(k_pages)
-    else:
-        _check_out(out, x.out_dtype)
     dev = q.device
     c = index.c
     hkv = c.hkv
+    if x is None:
+        _require(k_pages, k_pages.dtype, "k_pages", dev)
+        _require(v_pages, k_pages.dtype, "v_pages", dev)
     cu_h = _host_i64(cu_seqlens_q_host)
+    _check_call(dev, q, c.tq * hq * head_dim, block_tables, c.batch, c.max_pages, cu_seqlens_q,
+                used_kv_lens, selected, (c.tq, c.hkv, c.topk))
     rows = partial_rows(index, hq) if hkv > 0 and hq % max(hkv, 1) == 0 else 1
     odt, ocode = _partial_dtype(partial_dtype, None if partials is None else partials[0])
+    _check_partials(dev, partials, odt, rows, head_dim)
+    _check_room(dev, (out, q.dtype, c.tq * hq * head_dim, "out"),
+                (lse, torch.float32, c.tq * hq, "lse"))
     with _allocating(stream):
         if partials is None:
             partials = (torch.empty((rows, head_dim), dtype=odt, device=dev),
@@ -527,8 +600,8 @@ def sa_forward_combine(q, k_pages, v_pages, index: Index, selected, cu_seqlens_q
            page_size, softmax_scale, _causal(causal), split_edges)
     tail = (_ptr(o), _ptr(m), _ptr(l), _ptr(out), _ptr(lse), path, _stream(stream, dev))
     if x is not None:
-        _check(_on(dev, L.sa_forward_combine_scaled, *x.head(q, k_pages, v_pages, num_pages), *mid,
-                   ocode, *tail), "sa_forward_combine_scaled")
+        _check(_on(dev, L.sa_forward_combine_scaled, *_scaled_head(x, q, k_pages, v_pages, num_pages),
+                   *mid, ocode, *tail), "sa_forward_combine_scaled")
         return out, lse, partials
     head = (_ptr(q), _ptr(k_pages), _ptr(v_pages), num_pages, kvd, *mid)
     if ocode:
@@ -553,15 +626,22 @@ def sa_attention(q, k_pages, v_pages, selected, cu_seqlens_q_host, cu_seqlens_q,
     if x is None:
         _require(q, torch.float32, "q")
         kvd = _kv_dtype(k_pages)
-    else:
-        _check_out(out, x.out_dtype)
     dev = q.device
+    if x is None:
+        _require(k_pages, k_pages.dtype, "k_pages", dev)
+        _require(v_pages, k_pages.dtype, "v_pages", dev)
     tq, hkv_s, topk = selected.shape
     cu_h = _host_i64(cu_seqlens_q_host)
     batch = cu_h.size - 1
     max_pages = block_tables.shape[1]
+    _check_call(dev, q, tq * hq * head_dim, block_tables, batch, max_pages, cu_seqlens_q,
+                used_kv_lens, selected, (tq, hkv_s if hkv <= 0 else hkv, topk))
     rows = max(tq * hkv_s * topk * (hq // max(hkv_s, 1)), 1)
     odt, ocode = _partial_dtype(partial_dtype, None if partials is None else partials[0])
+    _check_partials(dev, partials, odt, rows, head_dim)
+    _check_room(dev, (out, q.dtype, tq * hq * head_dim, "out"), (lse, torch.float32, tq * hq, "lse"))
+    if index is not None:
+        _check_index(index, tq, hkv, topk, batch, max_pages, block_size, page_size)
     with _allocating(stream):
         if index is None:
             index = allocate_index(tq, hkv_s, topk, max(batch, 1), max_pages, block_size,
@@ -583,8 +663,8 @@ def sa_attention(q, k_pages, v_pages, selected, cu_seqlens_q_host, cu_seqlens_q,
            page_size, softmax_scale, _causal(causal), split_edges, ctypes.byref(index.c))
     tail = (_ptr(o), _ptr(m), _ptr(l), _ptr(out), _ptr(lse), path, _stream(stream, dev))
     if x is not None:
-        _check(_on(dev, L.sa_attention_scaled, *x.head(q, k_pages, v_pages, num_pages), *mid, ocode,
-                   *tail), "sa_attention_scaled")
+        _check(_on(dev, L.sa_attention_scaled, *_scaled_head(x, q, k_pages, v_pages, num_pages),
+                   *mid, ocode, *tail), "sa_attention_scaled")
         return out, lse, index, partials
     head = (_ptr(q), _ptr(k_pages), _ptr(v_pages), num_pages, kvd, *mid)
     if ocode:

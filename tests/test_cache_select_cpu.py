@@ -315,3 +315,16 @@ def test_kernel_names_are_kernels():
                 (many, 64, sa.PATH_AUTO, "forward_cc.cu")):
             name = sa.sa_attention_kernel_name(cu, 1000, 8, 32, d, 64, 16, kind, path=path)
             assert name in {n for pair in kernels(file) for n in pair}, (kind, name, file)
+
+
+def test_index_of_a_smaller_problem():
+    """An index handed in has to hold one over the call's sizes."""
+    import block_sparse_paged_csr_gb300 as sa
+
+    small = types.SimpleNamespace(sizes=sa.sa_index_query_sizes(4, 2, 3, 4, 16, 64, 16))
+    sa._check_index(small, 4, 2, 3, 4, 16, 64, 16)
+    sa._check_index(small, 2, 2, 3, 2, 16, 64, 16)          # larger than needed
+    sa._check_index(small, 4, 2, 3, 4, 16, 24, 16)          # the library refuses these sizes
+    for sizes in ((5, 2, 3, 4, 16), (4, 4, 3, 4, 16), (4, 2, 4, 4, 16), (4, 2, 3, 5, 16), (4, 2, 3, 4, 20)):
+        with pytest.raises(ValueError, match="smaller problem"):
+            sa._check_index(small, *sizes, 64, 16)

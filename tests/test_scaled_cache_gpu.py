@@ -526,3 +526,71 @@ def test_buffers_belong_to_the_stream_of_the_call():
         of = [s["stream"] for s in segments
               if s["address"] <= x.data_ptr() < s["address"] + s["total_size"]]
         assert of == [side.cuda_stream]
+
+
+@pytest.mark.parametrize("kind", ["f32", "int8"])
+def test_tensors_smaller_than_the_call(kind):
+    """Tables, lengths, queries and buffers that are too small, of another layout
+    or type are refused before any launch."""
+    w = inputs.small("gqa_decode", seed=67)
+    if kind == "f32":
+        t = _gpu.device_workload(w)
+        kw = {}
+    else:
+        t, _ = scaled_workload(w, kind)
+        kw = dict(k_scales=t["ks"], v_scales=t["vs"])
+    sizes = (w.hq, w.hkv, w.head_dim, w.block_size, w.page_size, w.softmax_scale, w.causal)
+
+    def attention(t, **more):
+        return sa.sa_attention(t["q"], t["k"], t["v"], t["selected"], w.cu_seqlens_q, t["cu"],
+                               t["used"], t["bt"], *sizes, **kw, **more)
+
+    def steps(t, **more):
+        return sa.sa_forward_combine(t["q"], t["k"], t["v"], idx, t["selected"], w.cu_seqlens_q,
+                                     t["cu"], t["used"], t["bt"], w.hq, *sizes[2:], **kw, **more)
+
+    def forward(t, **more):
+        return sa.sa_forward(t["q"], t["k"], t["v"], idx, t["bt"], t["cu"], t["used"], *sizes, **kw,
+                             **more)
+
+    out, lse, idx, parts = attention(t)
+    bad = dict(q=t["q"][:-1], cu=t["cu"][:-1], used=t["used"][:-1], bt=t["bt"].t().contiguous().t())
+    short = dict(bt=t["bt"][:-1], selected=t["selected"][:-1])
+    for call in (attention, steps, forward):
+        for name, x in {**bad, "bt": short["bt"]}.items():
+            if call is attention and name == "bt":
+                continue
+            with pytest.raises(ValueError):
+                call({**t, name: x})
+        with pytest.raises(ValueError):
+            call({**t, "bt": bad["bt"]})
+        with pytest.raises(TypeError):
+            call({**t, "bt": t["bt"].long()})
+        with pytest.raises(TypeError):
+            call({**t, "cu": t["cu"].int()})
+    for call in (attention, steps):
+        with pytest.raises(ValueError):
+            call({**t, "selected": t["selected"][:, :1].contiguous()})
+        with pytest.raises(ValueError):
+            call(t, out=out[:-1])
+        with pytest.raises(ValueError):
+            call(t, lse=lse[:-1])
+        with pytest.raises(TypeError):
+            call(t, lse=lse.double())
+        for i in range(3):
+            with pytest.raises(ValueError):
+                call(t, partials=tuple(p[:-1] if i == x else p for x, p in enumerate(parts)))
+    with pytest.raises(ValueError):
+        attention({**t, "bt": short["bt"]})
+    with pytest.raises(ValueError):
+        forward(t, m_partial=parts[1][:-1])
+    small = sa.allocate_index(w.tq, w.hkv, w.topk - 1, w.batch, w.max_pages, w.block_size, w.page_size,
+                              "cuda")
+    with pytest.raises(ValueError):
+        attention(t, index=small)
+    with pytest.raises(ValueError):
+        sa.sa_build_index(t["selected"], w.cu_seqlens_q, t["cu"], t["used"], w.max_pages, w.block_size,
+                          w.page_size, index=small)
+    with pytest.raises(ValueError):
+        sa.sa_combine(idx, *parts, w.hq, w.head_dim, out=out[:-1].float())
+    torch.cuda.synchronize()
