@@ -254,8 +254,18 @@ __device__ __forceinline__ uint32_t sw128_offset(int rows, int r, int k) {
   return static_cast<uint32_t>(panel * rows * 128 + r * 128 + ((chunk ^ (r & 7)) << 4) + within);
 }
 
-// Four 8-bit codes times the scale of their page as packed bf16 (exact under a
-// power-of-two scale, else rounded to nearest even).
+// A page's scale as a power of two and a factor of +-[1, 2).  A code times the
+// power of two is a bf16 number; the factor, 1 for the scales that sa_store_kv
+// makes, meets S (K) and P (V) in f32 instead of rounding every key and value.
+// (0 and subnormal scales are taken as they are.)
+__device__ __forceinline__ float2 scale_parts(float s) {
+  const uint32_t u = __float_as_uint(s);
+  if ((u & 0x7F800000u) == 0u) return make_float2(s, 1.f);
+  return make_float2(__uint_as_float(u & 0x7F800000u),
+                     __uint_as_float((u & 0x807FFFFFu) | 0x3F800000u));
+}
+
+// Four 8-bit codes times a power of two as packed bf16 (exact).
 template <bool kInt8>
 __device__ __forceinline__ uint2 codes4_to_bf16(uint32_t w, float scale) {
   uint32_t h0, h1;
@@ -322,13 +332,13 @@ struct UnitInfo {
 };
 
 // Shared memory: KVB unit buffers (K, V), NX tile buffers (Q), key
-// positions and unit info per unit buffer, the scheduler's ring of unit
+// positions, unit info and scale factors per unit buffer, the scheduler's ring of unit
 // slots, the epilogue's staging tiles, barriers, the TMEM address and
 // per-head unit bases.
 struct TcPlan {
   size_t kv_bytes;      // one unit buffer: K [BS][128] + V [BS][128] bf16
   size_t slot_bytes;    // one unit slot (UnitSlot layout below)
-  size_t kv, x, kpos, info, ring, stage, bars, misc, total;
+  size_t kv, x, kpos, info, factors, ring, stage, bars, misc, total;
 };
 
 // A unit slot of the scheduler ring: the unit's info, then per key its
@@ -358,7 +368,8 @@ __host__ __device__ inline TcPlan tc_plan() {
   p.kpos = tc_up(p.x + nx * static_cast<size_t>(kM) * kD * C::E, 128);  // int32 [kvb][BS]
   p.info = tc_up(p.kpos + kvb * static_cast<size_t>(bs) * 4, 128);      // UnitInfo [kvb]
   p.slot_bytes = bs == 128 ? SlotLayout<128>::bytes : SlotLayout<64>::bytes;
-  p.ring = tc_up(p.info + kvb * sizeof(UnitInfo), 128);                 // slots [kRing]
+  p.factors = tc_up(p.info + kvb * sizeof(UnitInfo), 128);              // f32 [kvb][2][BS]
+  p.ring = tc_up(p.factors + kvb * static_cast<size_t>(bs) * 8, 128);   // slots [kRing]
   p.stage = tc_up(p.ring + kRing * p.slot_bytes, 1024);                 // f32 [8][sb][32][16]
   p.bars = tc_up(p.stage + 8 * sb * 32 * 16 * 4, 128);                  // uint64 [32]
   p.misc = tc_up(p.bars + 32 * 8, 128);                                 // TMEM slot, unit bases
@@ -605,6 +616,7 @@ __device__ void tc_loader(const ForwardArgs& a, unsigned char* smem, const TcPla
       // 789 with a row per load and four codes per lane)
       constexpr int kQuads = (2 * BS / 4 + kLoaders - 1) / kLoaders;
       const int pc = lane & 7;
+      float* factors = reinterpret_cast<float*>(smem + P.factors) + kvb * 2 * BS;
       uint4 w[kQuads];
       float sc[kQuads];
 #pragma unroll
@@ -627,10 +639,12 @@ __device__ void tc_loader(const ForwardArgs& a, unsigned char* smem, const TcPla
       for (int q = 0; q < kQuads; ++q) {
         const int r = (lw + q * kLoaders) * 4 + (lane >> 3);
         if (r >= 2 * BS) continue;
-        const uint2 c0 = codes4_to_bf16<kT == SA_DTYPE_INT8>(w[q].x, sc[q]);
-        const uint2 c1 = codes4_to_bf16<kT == SA_DTYPE_INT8>(w[q].y, sc[q]);
-        const uint2 c2 = codes4_to_bf16<kT == SA_DTYPE_INT8>(w[q].z, sc[q]);
-        const uint2 c3 = codes4_to_bf16<kT == SA_DTYPE_INT8>(w[q].w, sc[q]);
+        const float2 parts = scale_parts(sc[q]);
+        if (pc == 0) factors[r] = parts.y;             // K's, then V's
+        const uint2 c0 = codes4_to_bf16<kT == SA_DTYPE_INT8>(w[q].x, parts.x);
+        const uint2 c1 = codes4_to_bf16<kT == SA_DTYPE_INT8>(w[q].y, parts.x);
+        const uint2 c2 = codes4_to_bf16<kT == SA_DTYPE_INT8>(w[q].z, parts.x);
+        const uint2 c3 = codes4_to_bf16<kT == SA_DTYPE_INT8>(w[q].w, parts.x);
         unsigned char* dst = r < BS ? ks : vs;
         const int key = r < BS ? r : r - BS;
         // the lanes of the second 64 dims write their upper half first, so
@@ -899,9 +913,63 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   return d;
 }
 
+template <int BS> struct KeyMask { uint32_t m[BS / 32]; };
+
+// The softmax of one row of a tile of 8-bit keys with factors: scores times K's
+// factors, P times V's, 32 keys per TMEM load.  P goes where the paths in
+// tc_softmax put it (128-key blocks: the upper half first, each half's 32
+// columns at its first S column, all of them read by then).  Returns m (log2
+// domain) and l.  Rarely called, so kept out of the other path's way.
+template <int BS>
+__device__ __noinline__ float2 factored_tile(uint32_t t_s, const float* factors, KeyMask<BS> keys,
+                                             int jlim, float qscale) {
+  auto live_of = [&](int c) -> uint32_t {
+    const int cut = jlim - c * 32;
+    const uint32_t inside = cut >= 31 ? 0xffffffffu : (cut < 0 ? 0u : ((2u << cut) - 1u));
+    uint32_t m = 0u;
+#pragma unroll
+    for (int x = 0; x < BS / 32; ++x) m = x == c ? keys.m[x] : m;
+    return m & inside;
+  };
+  float m2 = -INFINITY, l = 0.f;
+#pragma unroll 1
+  for (int c = 0; c < BS / 32; ++c) {
+    float v[32];
+    tmem_ld32(t_s + c * 32, v);
+    tmem_ld_wait();
+    const uint32_t live = live_of(c);
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if ((live >> i) & 1u) m2 = fmaxf(m2, v[i] * (factors[c * 32 + i] * qscale));
+  }
+  const float msub = m2 == -INFINITY ? 0.f : m2;
+#pragma unroll 1
+  for (int cc = 0; cc < BS / 32; ++cc) {
+    const int c = TcWarps<BS>::kWideS ? cc ^ 2 : cc;
+    float v[32];
+    tmem_ld32(t_s + c * 32, v);
+    tmem_ld_wait();
+    const uint32_t live = live_of(c);
+    uint32_t pk[16];
+#pragma unroll
+    for (int i2 = 0; i2 < 16; ++i2) {
+      const int i = 2 * i2, key = c * 32 + i;
+      const float p0 =
+          ((live >> i) & 1u) ? ex2_fast(fmaf(v[i], factors[key] * qscale, -msub)) : 0.f;
+      const float p1 =
+          ((live >> (i + 1)) & 1u) ? ex2_fast(fmaf(v[i + 1], factors[key + 1] * qscale, -msub)) : 0.f;
+      l += p0 + p1;
+      pk[i2] = pack_bf16x2_rn(p0 * factors[BS + key], p1 * factors[BS + key + 1]);
+    }
+    tmem_st16(t_s + (TcWarps<BS>::kWideS ? (c >> 1) * 64 + (c & 1) * 16 : c * 16), pk);
+  }
+  return make_float2(m2, l);
+}
+
 // Softmax warpgroup g (0 or 1) takes the tiles whose running index has
-// parity g, and with them TMEM buffers S[g], O[g].
-template <int BS, bool kTf32>
+// parity g, and with them TMEM buffers S[g], O[g].  kQ8: K/V in 8 bits, whose
+// keys may bring factors of their own (scale_parts).
+template <int BS, bool kTf32, bool kQ8>
 __device__ void tc_softmax(const ForwardArgs& a, const CUtensorMap* omap, unsigned char* smem,
                            const TcPlan& P, const TcBars& B, uint32_t tmem, int warp,
                            int lane) {
@@ -1045,7 +1113,16 @@ __device__ void tc_softmax(const ForwardArgs& a, const CUtensorMap* omap, unsign
     uint32_t vmask[BS / 32];
 #pragma unroll
     for (int c = 0; c < BS / 32; ++c) vmask[c] = __ballot_sync(0xffffffffu, kpos[c * 32 + lane] >= 0);
-    mbar_arrive(B.kv_empty + kvb);                      // info and keys read
+    // whether a key's factors have to be applied; the buffer is then needed until
+    // the unit's last P is formed
+    const float* const factors = reinterpret_cast<const float*>(smem + P.factors) + kvb * 2 * BS;
+    bool factored = false;
+    if constexpr (kQ8) {
+#pragma unroll
+      for (int c = 0; c < 2 * BS / 32; ++c) factored = factored || factors[c * 32 + lane] != 1.f;
+      factored = __any_sync(0xffffffffu, factored);
+    }
+    if (!factored) mbar_arrive(B.kv_empty + kvb);       // info and keys read
     const int tiles = (info.rows + kM - 1) / kM;
     for (int tt = 0; tt < tiles; ++tt, ++T) {
       if ((T & 1u) != g) continue;                      // the other warpgroup's tile
@@ -1081,7 +1158,14 @@ __device__ void tc_softmax(const ForwardArgs& a, const CUtensorMap* omap, unsign
       const uint32_t t_s = tmem + 128 * sb + lane_base;
       uint64_t l2 = f32x2(0.f, 0.f);          // two partial sums of p
       float m2;
-      if constexpr (TcWarps<BS>::kWideS) {
+      if (kQ8 && factored) {
+        KeyMask<BS> keys;
+#pragma unroll
+        for (int c = 0; c < BS / 32; ++c) keys.m[c] = vmask[c];
+        const float2 ml = factored_tile<BS>(t_s, factors, keys, jlim, qscale);
+        m2 = ml.x;
+        l2 = f32x2(ml.y, 0.f);
+      } else if constexpr (TcWarps<BS>::kWideS) {
       // S in halves of 64 keys, each read with one TMEM load (one round trip):
       // pass 1 takes the row maximum of qscale * s over live keys, as qscale
       // times the largest (qscale >= 0) or smallest raw score (rounding is
@@ -1256,6 +1340,7 @@ __device__ void tc_softmax(const ForwardArgs& a, const CUtensorMap* omap, unsign
       prev_m = m2;
       prev_l = l;
     }
+    if (factored) mbar_arrive(B.kv_empty + kvb);
     // The unit's last tile before the next unit's keys.
     if (prev && !epilogue(prevT, prev_prow, prev_m, prev_l)) {
       if (lane == 0) report(status, SA_ERR_DEVICE_TIMEOUT);
@@ -1344,7 +1429,7 @@ forward_tc_kernel(const __grid_constant__ CUtensorMap omap, ForwardArgs a) {
   const uint32_t tmem = *tmem_slot;
   const int64_t n_units = unit_base[a.hkv];
   if (warp >= W::kSoftmaxWarp0) {
-    tc_softmax<BS, kTf32>(a, &omap, smem, P, B, tmem, warp, lane);
+    tc_softmax<BS, kTf32, kT == SA_DTYPE_E4M3 || kT == SA_DTYPE_INT8>(a, &omap, smem, P, B, tmem, warp, lane);
     // box stores issued by this thread have landed before the CTA leaves
     bulk_wait_all();
   } else {

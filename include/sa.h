@@ -492,8 +492,10 @@ sa_status sa_attention_ex(const float *q, const void *k_pages, const void *v_pag
  * the conditions given at sa_attention (8-bit: page_size a power of two of at
  * least 16, qhead <= 16), with q k products exact to 2^-21 of the row's largest
  * q, p v products (scales included, whatever their spread) to 2^-21 or to 2^-28
- * of the largest, and f32 sums; other problems the tcgen05 kernel where it is supported (keys, values, queries and
- * P rounded to bf16: code * scale is exact there under a power-of-two scale),
+ * of the largest, and f32 sums; other problems the tcgen05 kernel where it is
+ * supported (P is rounded to bf16, and so are f32 queries: codes and scales are
+ * not, whatever the scales; SA_PATH_TENSOR_CORE_TF32 means SA_PATH_TENSOR_CORE
+ * here, and f32 queries lose nothing with SA_PATH_CUDA_CORE),
  * decode-shaped ones and the rest the general f32 FMA kernel.  SA_PATH_CUDA_CORE
  * means the general kernel.  head_dim: a multiple of 16, at most 256.  Codes
  * behind a sequence's length or on absent pages are never used, whatever they

@@ -305,6 +305,31 @@ def test_tensor_cores_odd_lengths(kind):
     check(w, t, vals, tc_tol(vals), f"odd {kind}")
 
 
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("scales", ["pow2", "any", "signs"])
+@pytest.mark.parametrize("bs,qo,lens", [(64, 37, (1999, 1003, 64)), (128, 300, (1999, 300, 777))])
+def test_tensor_cores_scales_lose_nothing(kind, scales, bs, qo, lens):
+    """With bf16 queries, whatever the scales, what the tensor-core kernel rounds
+    is P and the output, half a step of bf16 (2^-8) each: an element is off by at
+    most 2^-8 sum p |v| / sum p + 2^-8 |out|, besides the sums' f32 class."""
+    make = inputs.skewed if bs == 64 else inputs.chunked_prefill
+    w = make(75, batch=3, qo_len=qo, kv_len=1999, hq=16, hkv=2, topk=6, block_size=bs)
+    w = replace(w, used_kv_lens=np.array(lens, np.int32))
+    assert kernel(w, kind) == "forward_tc_kernel"
+    t, vals = scaled_workload(w, kind, "bf16", scales="any" if scales == "signs" else scales)
+    if scales == "signs":
+        for name in ("ks", "vs"):
+            sign = torch.from_numpy(np.random.default_rng(len(name)).choice([-1.0, 1.0], t[name].shape))
+            t[name] = t[name] * sign.float().cuda()
+            vals[name[0]] = vals[name[0]] * sign.numpy()[:, :, None, None].astype(np.float32)
+    out, lse, _, _ = attend(w, t)
+    ref, ref_lse, _, _ = reference(w, t, vals)
+    size, _, _, _ = reference(w, t, dict(k=vals["k"], v=np.abs(vals["v"])))
+    err = np.abs(out.float().cpu().numpy().astype(np.float64) - ref)
+    assert (err <= (HALF_BF16 + _gpu.TOL_F32) * size + HALF_BF16 * np.abs(ref)).all()
+    _gpu.compare_lse(lse.cpu().numpy(), ref_lse, _gpu.TOL_F32)
+
+
 @pytest.mark.parametrize("path", [sa.PATH_AUTO, sa.PATH_CUDA_CORE])
 def test_steps_one_by_one(path):
     """sa_forward and sa_combine, and sa_forward_combine, on a built index."""
