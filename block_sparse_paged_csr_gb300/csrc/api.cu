@@ -62,7 +62,7 @@ int device_sm_count() {
 
 namespace {
 
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+using sa::aligned16;
 
 enum class FwdKernel { kNone, kGeneral, kDecode, kDecodeMma, kTensor };
 
@@ -75,12 +75,10 @@ struct KvExtra {
   sa_dtype q_dtype = SA_DTYPE_F32;
 };
 
-bool kv_eight_bit(sa_dtype t) { return t == SA_DTYPE_E4M3 || t == SA_DTYPE_INT8; }
-
 // The types a call may have: 8-bit K/V exactly where scales come with it.
 bool types_ok(sa_dtype kv_dtype, const KvExtra& x) {
   if (!x.scaled) return kv_dtype == SA_DTYPE_F32 || kv_dtype == SA_DTYPE_BF16;
-  return kv_eight_bit(kv_dtype) && (x.q_dtype == SA_DTYPE_F32 || x.q_dtype == SA_DTYPE_BF16);
+  return sa::eight_bit(kv_dtype) && (x.q_dtype == SA_DTYPE_F32 || x.q_dtype == SA_DTYPE_BF16);
 }
 
 // The forward kernel a call takes.  Decode-shaped problems (tq at most twice
@@ -146,13 +144,6 @@ const char* forward_kernel_name(FwdKernel k) {
     case FwdKernel::kGeneral: return "forward_cc_kernel";
     default: return nullptr;
   }
-}
-
-sa_status validate_cu_host(const int64_t* cu, int32_t batch) {
-  if (cu == nullptr || batch < 1 || cu[0] != 0) return SA_ERR_CU_SEQLENS;
-  for (int32_t b = 1; b <= batch; ++b)
-    if (cu[b] < cu[b - 1]) return SA_ERR_CU_SEQLENS;
-  return SA_OK;
 }
 
 sa_status check_geometry(int64_t tq, int32_t hkv, int32_t topk, int32_t batch, int32_t max_pages,
@@ -280,7 +271,7 @@ sa_status build_index_impl(const int32_t* selected, int64_t tq, int32_t hkv, int
   if (forked != nullptr) *forked = false;
   if (block_size <= 0 || page_size <= 0 || block_size % page_size != 0) return SA_ERR_BLOCK_PAGE;
   if (tq == 0 || hkv == 0 || topk == 0) return SA_ERR_EMPTY;
-  sa_status st = validate_cu_host(cu_seqlens_q_host, batch);
+  sa_status st = sa::check_lengths(cu_seqlens_q_host, batch);
   if (st != SA_OK) return st;
   if (cu_seqlens_q_host[batch] != tq) return SA_ERR_SHAPE;
   int64_t msb = 0, nbs = 0;
@@ -553,7 +544,7 @@ const char* sa_attention_kernel_name(int64_t tq, int32_t batch, const int64_t* c
   const int kv_type = static_cast<int>(kv_dtype);
   if ((path == SA_PATH_AUTO || path == SA_PATH_FUSED_DECODE) && causal != 2) {
     if (hkv > 0 && hq > 0 && hq % hkv == 0 && head_dim > 0 && block_size > 0 && page_size > 0 &&
-        block_size % page_size == 0 && validate_cu_host(cu_seqlens_q_host, batch) == SA_OK &&
+        block_size % page_size == 0 && sa::check_lengths(cu_seqlens_q_host, batch) == SA_OK &&
         cu_seqlens_q_host[batch] == tq &&
         fused_eligible(tq, batch, cu_seqlens_q_host, num_pages, hq, hkv, head_dim, block_size,
                        page_size, kv_type))
@@ -646,7 +637,7 @@ sa_status forward_combine_impl(const void* q, const void* k_pages, const void* v
   bool fused = false;
   if (path == SA_PATH_AUTO || path == SA_PATH_FUSED_DECODE) {
     // (left-aligned causal masks a lone query's keys: not the fused path's case)
-    if (causal != 2 && validate_cu_host(cu_seqlens_q_host, batch) == SA_OK &&
+    if (causal != 2 && sa::check_lengths(cu_seqlens_q_host, batch) == SA_OK &&
         cu_seqlens_q_host[batch] == tq)
       fused = fused_eligible(tq, batch, cu_seqlens_q_host, num_pages, hq, hkv, head_dim,
                              block_size, page_size, kv_type);
@@ -817,7 +808,7 @@ sa_status attention_impl(const void* q, const void* k_pages, const void* v_pages
   // Shape checks of the forward step, before any device work.
   bool fused = false;
   if (path == SA_PATH_AUTO || path == SA_PATH_FUSED_DECODE) {
-    if (causal != 2 && tq > 0 && validate_cu_host(cu_seqlens_q_host, batch) == SA_OK)
+    if (causal != 2 && tq > 0 && sa::check_lengths(cu_seqlens_q_host, batch) == SA_OK)
       fused = fused_eligible(tq, batch, cu_seqlens_q_host, num_pages, hq, hkv, head_dim,
                              block_size, page_size, kv_type);
     if (path == SA_PATH_FUSED_DECODE && !fused) return SA_ERR_UNSUPPORTED;

@@ -626,18 +626,7 @@ cudaError_t launch_bounds(const BoundsArgs& a, cudaStream_t stream) {
 
 // ------------------------------------------------------------------ checks
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 bool known_type(sa_dtype t) { return t >= SA_DTYPE_F32 && t <= SA_DTYPE_INT8; }
-
-bool eight_bit(sa_dtype t) { return t == SA_DTYPE_E4M3 || t == SA_DTYPE_INT8; }
-
-sa_status check_lengths(const int64_t* cu_host, int32_t batch, int64_t tq) {
-  if (cu_host == nullptr || batch < 1 || cu_host[0] != 0) return SA_ERR_CU_SEQLENS;
-  for (int32_t b = 1; b <= batch; ++b)
-    if (cu_host[b] < cu_host[b - 1]) return SA_ERR_CU_SEQLENS;
-  return cu_host[batch] == tq ? SA_OK : SA_ERR_SHAPE;
-}
 
 }  // namespace
 

@@ -150,22 +150,6 @@ struct Smem {
 
 // ------------------------------------------------------------------ metadata
 
-// Sequence b of query i: the largest b with cu[b] <= i; 32 candidates a round.
-__device__ __forceinline__ int warp_batch_of(const int64_t* cu, int batch, int64_t i, int lane) {
-  int lo = 0, hi = batch;
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32;
-    const int cand = lo + lane * step;
-    const bool le = cand < hi && cu[cand] <= i;
-    const unsigned bal = __ballot_sync(0xffffffffu, le);   // lane 0 (cand = lo) always set
-    const int last = bal ? 31 - __clz(bal) : 0;
-    const int nlo = lo + last * step;
-    hi = min(nlo + step, hi);
-    lo = nlo;
-  }
-  return lo;
-}
-
 __device__ void meta_warp(const FusedQ8Args& qa, const Smem& sm, int64_t n_pieces, int lane) {
   const FusedDecArgs& a = qa.base;
   uint32_t n = 0;
@@ -211,7 +195,7 @@ __device__ void meta_warp(const FusedQ8Args& qa, const Smem& sm, int64_t n_piece
     const int64_t c0 = a.cu[b], c1 = a.cu[b + 1];
     int lk = a.used ? a.used[b] : a.msb * a.block_size;
     if (c0 > i || c1 <= i) {
-      b = warp_batch_of(a.cu, a.batch, i, lane);
+      b = warp_search(a.batch, lane, [&](int x) { return a.cu[x] <= i; });
       if (a.used) lk = a.used[b];
     }
     lk = max(lk, 0);

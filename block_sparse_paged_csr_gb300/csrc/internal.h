@@ -12,6 +12,24 @@
 
 namespace sa {
 
+// Checks that several entry points make.
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+inline bool eight_bit(sa_dtype t) { return t == SA_DTYPE_E4M3 || t == SA_DTYPE_INT8; }
+
+// Prefix lengths on the host: from 0 on, never falling.
+inline sa_status check_lengths(const int64_t* cu_host, int32_t batch) {
+  if (cu_host == nullptr || batch < 1 || cu_host[0] != 0) return SA_ERR_CU_SEQLENS;
+  for (int32_t b = 1; b <= batch; ++b)
+    if (cu_host[b] < cu_host[b - 1]) return SA_ERR_CU_SEQLENS;
+  return SA_OK;
+}
+// ... that end at tq.
+inline sa_status check_lengths(const int64_t* cu_host, int32_t batch, int64_t tq) {
+  const sa_status st = check_lengths(cu_host, batch);
+  return st != SA_OK ? st : cu_host[batch] == tq ? SA_OK : SA_ERR_SHAPE;
+}
+
 // Entries of one (kv head, sequence) segment handled by one CTA of the index
 // kernel at a time.
 constexpr int kChunkEntries = 4096;

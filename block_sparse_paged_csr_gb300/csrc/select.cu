@@ -95,21 +95,10 @@ __device__ __forceinline__ RowView row_view(const SelectArgs& a, unsigned row, i
   v.c1 = static_cast<int>(a.cu[v.b + 1]);
   v.lk = a.used[v.b];
   if (v.c0 > v.i || v.c1 <= v.i) {
-    int lo = 0, hi = a.batch;
-    while (hi - lo > 1) {
-      const int step = (hi - lo + 31) / 32;
-      const int cand = lo + lane * step;
-      const bool le = cand < hi && a.cu[cand] <= v.i;
-      const unsigned bal = __ballot_sync(0xffffffffu, le);
-      const int last = bal ? 31 - __clz(bal) : 0;
-      const int nlo = lo + last * step;
-      hi = min(nlo + step, hi);
-      lo = nlo;
-    }
-    v.b = lo;
-    v.c0 = static_cast<int>(a.cu[lo]);
-    v.c1 = static_cast<int>(a.cu[lo + 1]);
-    v.lk = a.used[lo];
+    v.b = warp_search(a.batch, lane, [&](int b) { return a.cu[b] <= v.i; });
+    v.c0 = static_cast<int>(a.cu[v.b]);
+    v.c1 = static_cast<int>(a.cu[v.b + 1]);
+    v.lk = a.used[v.b];
   }
   v.lk = max(v.lk, 0);
   v.nblk = blocks_in_sight(a, v.i, v.c0, v.c1, v.lk);
@@ -1484,8 +1473,6 @@ cudaError_t launch_select(SelectArgs a, const SelectLayout& l, int64_t longest, 
   return cudaSuccess;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 }  // namespace
 
 }  // namespace sa
@@ -1516,11 +1503,8 @@ sa_status sa_select_blocks(const void* q, sa_dtype q_dtype, int64_t tq, int32_t 
   if (head_dim <= 0 || block_size <= 0) return SA_ERR_BLOCK_PAGE;
   if (tq == 0 || topk == 0) return SA_ERR_EMPTY;
   if (tq < 0 || topk < 0 || msb < 0 || num_bounds < 0) return SA_ERR_SHAPE;
-  if (cu_seqlens_q_host == nullptr || batch < 1 || cu_seqlens_q_host[0] != 0)
-    return SA_ERR_CU_SEQLENS;
-  for (int32_t b = 1; b <= batch; ++b)
-    if (cu_seqlens_q_host[b] < cu_seqlens_q_host[b - 1]) return SA_ERR_CU_SEQLENS;
-  if (cu_seqlens_q_host[batch] != tq) return SA_ERR_SHAPE;
+  const sa_status st = sa::check_lengths(cu_seqlens_q_host, batch, tq);
+  if (st != SA_OK) return st;
   if (q_dtype != SA_DTYPE_F32 && q_dtype != SA_DTYPE_BF16) return SA_ERR_INVALID_ARGUMENT;
   if (causal < 0 || causal > 2) return SA_ERR_INVALID_ARGUMENT;
   if (sink_blocks < 0 || local_blocks < 0 ||

@@ -26,20 +26,15 @@ __host__ __device__ __forceinline__ int64_t slot_base(int64_t cu_b, int64_t b, i
   return cu_b / per + 2 * b;
 }
 
-// The sequence that owns slot u (the largest b with base(b) <= u): u / 2 where
-// few tokens precede it (decode batches: no search), else 32 candidates per
-// round.  All lanes of the warp call it.
-__device__ __forceinline__ int warp_slot_sequence(const int64_t* cu, int batch, int per,
-                                                  int64_t u, int lane) {
-  const int guess = static_cast<int>(min(u / 2, static_cast<int64_t>(batch - 1)));
-  const int64_t g0 = cu[guess], g1 = cu[guess + 1];
-  if (slot_base(g0, guess, per) <= u && (guess + 1 == batch || u < slot_base(g1, guess + 1, per)))
-    return guess;
-  int lo = 0, hi = batch;
+// The largest b in [0, n) with before(b), which holds for 0 and up to some b: 32
+// candidates per round.  All lanes of the warp call it.
+template <typename F>
+__device__ __forceinline__ int warp_search(int n, int lane, F before) {
+  int lo = 0, hi = n;
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) / 32;
     const int cand = lo + lane * step;
-    const bool le = cand < hi && slot_base(cu[cand], cand, per) <= u;
+    const bool le = cand < hi && before(cand);
     const unsigned bal = __ballot_sync(0xffffffffu, le);   // lane 0 (cand = lo) always set
     const int last = bal ? 31 - __clz(bal) : 0;
     const int nlo = lo + last * step;
@@ -47,6 +42,18 @@ __device__ __forceinline__ int warp_slot_sequence(const int64_t* cu, int batch, 
     lo = nlo;
   }
   return lo;
+}
+
+// The sequence that owns slot u (the largest b with base(b) <= u): u / 2 where
+// few tokens precede it (decode batches: no search), else a search.  All lanes of
+// the warp call it.
+__device__ __forceinline__ int warp_slot_sequence(const int64_t* cu, int batch, int per,
+                                                  int64_t u, int lane) {
+  const int guess = static_cast<int>(min(u / 2, static_cast<int64_t>(batch - 1)));
+  const int64_t g0 = cu[guess], g1 = cu[guess + 1];
+  if (slot_base(g0, guess, per) <= u && (guess + 1 == batch || u < slot_base(g1, guess + 1, per)))
+    return guess;
+  return warp_search(batch, lane, [&](int b) { return slot_base(cu[b], b, per) <= u; });
 }
 
 // The new positions [p0, p1) of sequence b: right-aligned at its length lk
