@@ -30,6 +30,7 @@
 // (309 us with work cut as in the kernel for wider caches); 32 heads on 8, 64 sequences, 16
 // blocks (124 MB): 48 us.  About 1400 cycles of an SM per 128 keys, of which the
 // copies would need 800: conversions, softmax and MMA issue bound it.
+#include <cfloat>
 #include <cstdint>
 #include <cuda.h>
 
@@ -839,7 +840,10 @@ __device__ void consumer(const FusedQ8Args& qa, const Smem& sm, int warp, int la
 #pragma unroll
             for (int e = 0; e < 2; ++e) p[nt][e] = ex2(x[r][hh][nt][e]);
           lsum += (p[0][0] + p[0][1]) + (p[1][0] + p[1][1]);
-          const float vs = rec.vs[NH == 2 ? hh : h0] * vfac[r];
+          // (a number: a page far above the others' scales may pass f32's range where
+          // its keys' P is 0)
+          const float vs =
+              fminf(fmaxf(rec.vs[NH == 2 ? hh : h0] * vfac[r], -FLT_MAX), FLT_MAX);
           if constexpr (R == 8) {
             split2h(p[0][0] * vs, p[0][1] * vs, pf[hh][0], pf[hh][1]);
             split2h(p[1][0] * vs, p[1][1] * vs, pf[hh][2], pf[hh][3]);

@@ -195,7 +195,7 @@ def test_fused_decode_scales_far_apart(kind, hq, where, e):
     assert kernel(w, kind) == "fused_dec_kernel"
     ref, ref_lse, _, _ = reference(w, t, vals)
     size = np.abs(ref).max(axis=-1, keepdims=True)        # (no floor: outputs may be small)
-    for split in (0, 1, 4):
+    for split in (0, 1, 4, 64):
         out, lse, _, _ = attend(w, t, split_edges=split)
         got = out.cpu().numpy().astype(np.float64)
         assert (np.abs(got - ref) / size).max() <= _gpu.TOL_F32
@@ -217,11 +217,46 @@ def test_fused_decode_scales_at_the_ends(kind, hq, v_scale):
     t["vs"] = s
     ref, ref_lse, _, _ = reference(w, t, vals)
     size = np.abs(ref).max(axis=-1, keepdims=True)
-    for split in (0, 1):
+    for split in (0, 1, 64):
         out, lse, _, _ = attend(w, t, split_edges=split)
         got = out.cpu().numpy().astype(np.float64)
         # (outputs near 2^-126 are held in steps of 2^-149)
         assert (np.abs(got - ref) <= _gpu.TOL_F32 * size + 2.0 ** -148).all()
+        _gpu.compare_lse(lse.cpu().numpy(), ref_lse, 1e-4)
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("hq", [8, 24])
+@pytest.mark.parametrize("page_size", [16, 64])
+def test_fused_decode_scale_beyond_reach(kind, hq, page_size):
+    """A page whose V scale is 2^160 times the others' and whose keys have 2^-250
+    of the softmax adds nothing, and no NaN (0 times infinity) either, whether
+    it comes first, where the sequence ends inside it, or last."""
+    w = inputs.gqa_decode(77, batch=3, kv_min=400, kv_max=700, hq=hq, hkv=2, topk=5,
+                          page_size=page_size)
+    t, vals = scaled_workload(w, kind, dirty=False)
+    shape = (w.num_pages, 2, page_size, 128)
+    sign = np.random.default_rng(7).choice([-1.0, 1.0], 128)
+    t["q"] = torch.from_numpy(np.tile(sign, (w.tq, hq, 1)).astype(np.float32)).cuda()
+    k = np.random.default_rng(8).choice([-1.0, 0.0, 1.0], shape)
+    ks, vs = np.full(shape[:2], 0.02), np.full(shape[:2], 2.0 ** -60)
+    for b in range(3):
+        for h in range(2):                   # head 0: the first rank's last page; head 1: the last rank's
+            last = (int(w.used_kv_lens[b]) - 1) // page_size
+            page = w.block_tables[b, last if h == 0 else w.selected[b, h, -1] * (64 // page_size)]
+            k[page, h] = sign * 100.0
+            ks[page, h] = -250 * math.log(2.0) / (w.softmax_scale * 128 * 100.0)
+            vs[page, h] = 2.0 ** 100
+    for name, x, s in (("k", torch.from_numpy(k).float(), ks), ("v", t["v"].float().cpu(), vs)):
+        codes = x.cuda().to(TORCH[kind])
+        t[name], t[name + "s"] = codes, torch.from_numpy(s.astype(np.float32)).cuda()
+        vals[name] = (codes.float() * t[name + "s"][:, :, None, None]).cpu().numpy()
+    ref, ref_lse, _, _ = reference(w, t, vals)
+    size = np.abs(ref).max(axis=-1, keepdims=True)
+    for split in (0, 1, 64):                 # (64: one piece of all ranks)
+        out, lse, _, _ = attend(w, t, split_edges=split)
+        got = out.cpu().numpy().astype(np.float64)
+        assert (np.abs(got - ref) <= _gpu.TOL_F32 * size).all()
         _gpu.compare_lse(lse.cpu().numpy(), ref_lse, 1e-4)
 
 
