@@ -93,7 +93,7 @@ def _allocating(stream):
     """Where a call makes its buffers: on the stream that is going to use them, so
     that memory freed elsewhere and still in use there is not handed out (the
     current stream where the call names none)."""
-    return _NOTHING if stream is None else torch.cuda.stream(stream)
+    return torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else _NOTHING
 
 
 _NOTHING = contextlib.nullcontext()

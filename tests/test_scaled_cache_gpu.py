@@ -654,3 +654,17 @@ def test_tensors_smaller_than_the_call(kind):
     with pytest.raises(ValueError):
         sa.sa_combine(idx, *parts, w.hq, w.head_dim, out=out[:-1].float())
     torch.cuda.synchronize()
+
+
+def test_stream_by_its_handle():
+    """A stream that is not torch's own, known by its handle only."""
+    import types
+
+    w = inputs.small("gqa_decode", seed=69)
+    t, vals = scaled_workload(w, "int8")
+    ref, _, _, _ = reference(w, t, vals)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    out, _, idx, _ = attend(w, t, stream=types.SimpleNamespace(cuda_stream=side.cuda_stream))
+    torch.cuda.synchronize()
+    assert _gpu.row_error(out.cpu().numpy(), ref) <= _gpu.TOL_F32
