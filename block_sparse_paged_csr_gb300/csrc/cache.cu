@@ -170,10 +170,12 @@ __device__ __forceinline__ void store8(void* pages, int64_t off, const float (&x
 // magnitude and the pass that writes codes, so a page of 64 x 128 is read
 // once.
 //
-// Bound by instructions (the largest magnitude, the conversion) more than by
-// memory: 7000 f32 rows of 8 heads of 128, K and V, to int8 (73 MB) take 22.6 us,
-// 3.2 TB/s; three CTAs per SM, as four leave too few registers for the pieces
-// (23.6 us).  Single bf16 rows of 128 sequences to e4m3: 6 us, latency.
+// 7000 f32 rows of 8 heads of 128, K and V, to int8 (73 MB) take 22.6 us, 3.2 TB/s.
+// Neither memory (33 %) nor the issue slots (48 %) are full: at 80 registers a third
+// of the warps is resident, and they wait for their rows (long scoreboard first)
+// and for the maximum before they may write.  Three CTAs per SM, as four leave
+// too few registers for the pieces (23.6 us).  Single bf16 rows of 64 sequences
+// (128 rows of K and V, 8 heads) to e4m3: 6 us, latency.
 template <int kType, bool kSrcBf16, int kItemWarps>
 __global__ void __launch_bounds__(kThreads, 3) store_kv_kernel(const StoreArgs a) {
   constexpr bool kCodes = kType == kE4m3 || kType == kInt8;
@@ -422,11 +424,12 @@ struct CodeRange {
 //   kInPage: a batch of loads never leaves a page (page_size a multiple of its
 // rows), the usual case: one lookup per batch instead of one per load.
 //
-// Bound by instructions, not by memory: every code passes a conversion and two
-// comparisons (108 MB of int8 keys, 64-key pages, 128-key blocks: 33 us, 3.3
-// TB/s, 60 us with a lookup per load and rounding at every page; two loads in
-// flight 46 us, eight 33 us but slower single tokens).  A block of 64 keys for
-// each of 128 sequences, 8 heads, e4m3: 10 us, latency.
+// 108 MB of int8 keys, 64-key pages, 128-key blocks: 33 us, 3.3 TB/s (60 us with a
+// lookup per load and rounding at every page; two loads in flight 46 us, eight 33 us
+// but slower single tokens).  Neither memory (43 %) nor the issue slots (52 %) are
+// full: a third of the warps is resident (80 registers), four loads each, and long
+// scoreboard is the first of their stalls.  A block of 64 keys for each of 128
+// sequences, 8 heads, e4m3: 10 us, latency.
 constexpr int kBatch = 4;
 
 template <int kType, bool kInPage>

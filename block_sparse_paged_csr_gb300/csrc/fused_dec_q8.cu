@@ -26,10 +26,15 @@
 //     consumer().
 // Roles: warp 0 metadata, warps 1..NL loads, then merge, then consumers.
 // Measured, with the index build beside it: 128 sequences of 65536 to 131072 keys,
-// 64 blocks of 64, 64 heads on 8, pages of 16, e4m3 (970 MB): 200 us, 4.9 TB/s
-// (309 us with work cut as in the kernel for wider caches); 32 heads on 8, 64 sequences, 16
-// blocks (124 MB): 48 us.  About 1400 cycles of an SM per 128 keys, of which the
-// copies would need 800: conversions, softmax and MMA issue bound it.
+// 64 blocks of 64, 64 heads on 8, pages of 16, e4m3 (970 MB): 205 us, 4.7 TB/s
+// (309 us with work cut as in the kernel for wider caches); 32 heads on 8, 64
+// sequences, 16 blocks (124 MB): 49 us.  From 8 to 64 blocks a query, each 16 more take
+// 43 us (268 MB, 6.2 TB/s of the 6.8 that a copy reaches: 0.8 us for an SM's 128
+// keys, 32 KB); with cold caches a call takes 42 us besides, for its start
+// (selected ids -> page ids -> scales -> keys), its changes of piece and its end, and
+// 64 us where 768 pieces make five rounds of the SMs and a short sixth.  int8 takes 6 %
+// longer than e4m3 (a quarter more instructions: its conversion), f32 queries as
+// long as bf16 ones.
 #include <cfloat>
 #include <cstdint>
 #include <cuda.h>

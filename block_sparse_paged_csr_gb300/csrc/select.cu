@@ -521,7 +521,7 @@ block_score_kernel(const SelectArgs a) {
 // is lost, which eps counts): reads q, coalesced, at the speed of memory; the
 // largest |bound| per channel of every (sequence, kv head, chunk), for eps; and
 // the products, tile by tile.  For 8192 queries, 64 heads of 128 channels on 8 kv
-// heads, 256 blocks: 48 us (302 MB, 6.2 TB/s), 7.5 us and 75 us.
+// heads, 256 blocks: 48 us (302 MB, 6.2 TB/s), 7.5 us and 77 us.
 //   weights: [rows][part][2 head_dim] bf16, M (lo channels) then P (hi)
 template <bool kQ16>
 __global__ void __launch_bounds__(256) block_weights_kernel(const SelectArgs a) {
@@ -1030,11 +1030,11 @@ __device__ __forceinline__ void weights64(const SelectArgs& a, const RowView& rv
 // bisection over the keys' range until just k lie above (a dozen counts), the
 // border check against eps, f64 scores where it asks for them, and the ids
 // written in ascending order.  A CTA of one or eight warps per row (two rows of a
-// warp each in a CTA take 92 us instead of 83 in the case below: a row whose border
+// warp each in a CTA are a tenth slower in the case below: a row whose border
 // has to be settled in f64 takes several times as long and holds the other's place).
 // What it costs is instructions and the latency of the counts, so the fewest
 // threads that hold a row's keys in registers take it.  65536 rows of 256 blocks,
-// 32 of them chosen: 84 us, of which the 9 % of rows that f32 leaves open take 25,
+// 32 of them chosen: 101 us, of which the 15 % of rows that f32 leaves open take 40,
 // the bisection 18, reading the scores 29; 512 rows of up to 512 blocks, 16
 // chosen: 17.5 us; 1024 rows of up to 2048, 64 chosen: 26 us.  (Cuts by
 // interpolation need as many counts as bisection; border scores four blocks at a
@@ -1387,7 +1387,7 @@ cudaError_t launch_tile(const SelectArgs& a, cudaStream_t s) {
   err = limit.raise(reinterpret_cast<const void*>(block_score_tile_kernel<kG>), TileSmem<kG>::kTotal);
   if (err != cudaSuccess) return err;
   // The maxima beside the weights, and the tiles' first bounds beside both
-  // (230 -> 219 us for the case of 8192 queries): the weights kernel starts after all
+  // (11 us less for the case of 8192 queries): the weights kernel starts after all
   // earlier work, so the bounds that the others read meanwhile are there.
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1461,7 +1461,7 @@ cudaError_t launch_select(SelectArgs a, const SelectLayout& l, int64_t longest, 
       if (err != cudaSuccess) return err;
     }
     // A warp per row while a row's keys fit in its registers: 65536 rows of 256
-    // blocks take 84 us, 700 us with a CTA of eight warps per row; 32 rows of 512
+    // blocks take 101 us, some 700 us with a CTA of eight warps per row; 32 rows of 512
     // blocks the same time either way (13 and 14 us with their scores).
     if (a.msb <= 256) err = launch_pick<1, 8>(a, a.msb > a.topk, s);
     else if (a.msb <= 512) err = launch_pick<1, 16>(a, a.msb > a.topk, s);

@@ -635,7 +635,8 @@ sa_status sa_select_workspace_size(int64_t tq, int32_t batch, int32_t hkv, int32
  * local_blocks of the blocks in sight come in before any other (sink_blocks +
  * local_blocks <= topk).  The result is that of exactly computed scores: f32
  * decides where its error cannot matter, f64 elsewhere (the bound of that error
- * rests on how GB300's tensor cores cut their sums, as measured there).
+ * rests on how GB300's tensor cores cut their sums, as measured there; scores
+ * whose terms add up to less than 2^-90 in magnitude may order otherwise).
  *
  *   q             [tq, hq, head_dim] of q_dtype (f32 or bf16), 16-byte aligned
  *   bounds, bound_tables, msb, num_bounds   as for sa_block_bounds
