@@ -143,11 +143,12 @@ __device__ __forceinline__ uint32_t finite_bf16x2(uint32_t u) {
 // a multiple of 2^-25 of the power of two of the largest one, two bits below
 // f32's last, and the sum is cut to 24 bits.  The largest addend loses nothing,
 // each of the 16 others less than 2^-25, the sum less than 2^-23: 5 * 2^-23 a
-// step.  That is how GB300's tensor cores behave, found by measuring (one large
-// addend of either sign at every place beside 16 small ones of 2^-20 to 2^-32, and 2 million
-// sums of random exponents, of which the worst lost 3.5 * 2^-23 of its terms'
-// magnitudes), not a documented property.  Terms of 2^-25 beside two large
-// ones take scores 62 * 2^-23 off at head_dim 128; see the test of small terms.
+// step.  That is how GB300's tensor cores behave, found by measuring (a large
+// addend of either sign, first or last product or the sum so far, beside small ones
+// of 2^-20 to 2^-32, and 2 million sums of random exponents, of which the worst lost
+// 3.5 * 2^-23 of its terms' magnitudes), not a documented property.  Terms just
+// below 2^-25 beside two large ones take scores 62 * 2^-23 off at head_dim 128; see
+// the test of small terms.
 // The weights' own sums over `lanes` f32 terms and the sums of parts and chains
 // lose 2^-24 each, and the weights' split `split`; the last factor covers the
 // parts' magnitudes above their weight's and the error of the sum of magnitudes
@@ -160,8 +161,9 @@ __host__ __device__ constexpr float score_eps(int steps, int lanes, float split)
 
 // The bits of a score that is not finite, or of a block without a bounds row, or
 // with one that stands for no block (lo[0] > hi[0]: a block without keys holds
-// lo = inf, hi = -inf): kNoBlock for the last two; else the sum over the channels by itself, since a part of a split
-// weight that is 0 makes a NaN of an infinite bound; one NaN for all.
+// lo = inf, hi = -inf): kNoBlock for the last two; else the sum over the channels
+// by itself, since a part of a split weight that is 0 makes a NaN of an infinite
+// bound; one NaN for all.
 __device__ __noinline__ uint32_t special_bits(const SelectArgs& a, int i, int h,
                                               const uint16_t* box, bool there) {
   if (!there) return kNoBlock;
