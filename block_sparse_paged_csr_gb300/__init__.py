@@ -23,7 +23,12 @@ Around them, for serving:
 * :func:`sa_block_bounds` - the smallest and largest key per channel of the
   blocks that got new tokens;
 * :func:`sa_select_blocks` - each query's topk blocks by those bounds: the
-  ``selected`` of the steps above.
+  ``selected`` of the steps above;
+* :func:`sa_norm_rope` - before the store: head norms and position rotation of
+  the new queries and keys;
+* :func:`sa_decode_attention` - one new token per sequence over its whole cache
+  or a window of it, without a selection;
+* :func:`sa_load_kv` - rows of the cache read back.
 """
 from __future__ import annotations
 
@@ -42,7 +47,8 @@ __all__ = ["SAError", "Index", "sa_index_query_sizes", "sa_build_index",
            "sa_build_index_no_alloc", "sa_forward", "sa_forward_combine", "sa_forward_kernel_name",
            "sa_attention_kernel_name", "PATH_FUSED_DECODE",
            "sa_combine", "sa_attention", "sa_store_kv", "sa_block_bounds", "sa_select_blocks",
-           "allocate_select_workspace", "sa_get_status", "sa_clear_status", "sa_status_string",
+           "allocate_select_workspace", "sa_norm_rope", "sa_load_kv", "sa_decode_attention",
+           "allocate_decode_workspace", "sa_get_status", "sa_clear_status", "sa_status_string",
            "sa_version", "allocate_index", "PATH_AUTO", "PATH_CUDA_CORE", "PATH_TENSOR_CORE",
            "PATH_TENSOR_CORE_TF32",
            "PATH_CUDA_CORE_GENERAL", "AttentionGraph", "sa_debug_stall", "sa_debug_cta_stats", "STALL_NONE",
@@ -937,6 +943,231 @@ def sa_select_blocks(q, bounds, bound_tables, cu_seqlens_q_host, cu_seqlens_q, u
                max(workspace.numel() - (aligned - base), 0), _status_word(status, dev),
                _stream(stream, dev)), "sa_select_blocks")
     return selected
+
+
+def sa_norm_rope(q, k, q_weight, k_weight, inv_freq, positions=None, cu_seqlens_q_host=None,
+                 cu_seqlens_q=None, used_kv_lens=None, eps=1e-6, freq_axes=None, interleaved=False,
+                 q_out=None, k_out=None, out_dtype=None, status=None, stream=None):
+    """RMS norm of each head of new tokens' ``q`` [tq, hq, d] and ``k`` [tq, hkv, d]
+    (float32 or bfloat16, channels contiguous; either may be None) with the
+    weights ``q_weight`` / ``k_weight`` [d] (None: no norm), then rotation of the
+    first ``2 * inv_freq.numel()`` channels (``inv_freq`` float32, None: none) by
+    the token's position: pairs (i, i + half), or (2 i, 2 i + 1) where
+    ``interleaved``.  ``positions`` int32 [tq] or [axes, tq], with ``freq_axes``
+    int32 (per pair, its axis) in the latter case; without positions each
+    sequence's last positions, as :func:`sa_store_kv` takes them from the same
+    ``cu_seqlens_q_host``, ``cu_seqlens_q`` and ``used_kv_lens``.  Returns
+    (q_out, k_out), of ``out_dtype`` (default: the input's type); an output handed
+    in may be its input."""
+    given = q if q is not None else k
+    src = _heads(given, "k" if q is None else "q")
+    dev, (tq, _, d) = given.device, given.shape
+    for t, name in ((q, "q"), (k, "k")):
+        if t is not None and (_heads(t, name) != src or t.device != dev or t.shape[0] != tq or
+                              t.shape[2] != d):
+            raise ValueError("q and k must have one type, device, number of tokens and of channels")
+    made = []
+    for t, out, name in ((q, q_out, "q_out"), (k, k_out, "k_out")):
+        if t is None:
+            if out is not None:
+                raise ValueError(f"{name} without its input")
+        elif out is None:
+            with _allocating(stream):
+                out = torch.empty(t.shape, dtype=out_dtype or t.dtype, device=dev)
+            _heads(out, name)
+        else:
+            _heads(out, name)
+            if out.shape != t.shape or out.device != dev:
+                raise ValueError(f"{name} must be {tuple(t.shape)} on {dev}")
+            if out_dtype is not None and out.dtype != out_dtype:
+                raise TypeError(f"{name} must be {out_dtype}, got {out.dtype}")
+            if (t.numel() and out.data_ptr() == t.data_ptr() and
+                    (out.dtype != t.dtype or out.stride() != t.stride())):
+                raise ValueError(f"{name} in its input's place must have its type and strides")
+        made.append(out)
+    q_out, k_out = made
+    if q_out is not None and k_out is not None and q_out.dtype != k_out.dtype:
+        raise TypeError("q_out and k_out must have one type")
+    out = q_out if q_out is not None else k_out
+    wt = None
+    for w, t, name in ((q_weight, q, "q_weight"), (k_weight, k, "k_weight")):
+        if w is not None:
+            if not isinstance(w, torch.Tensor) or w.dtype not in _ACT_DTYPES:
+                raise TypeError(f"{name} must be a float32 or bfloat16 tensor")
+            wt = wt or w.dtype
+            _require(w, wt, name, dev)
+            if w.numel() != d:
+                raise ValueError(f"{name} must have {d} values")
+    rot, axes, axis_stride, cu_h, batch = 0, 0, 0, None, 0
+    if inv_freq is not None:
+        _require(inv_freq, torch.float32, "inv_freq", dev)
+        rot = 2 * inv_freq.numel()
+    if positions is not None:
+        _require(positions, torch.int32, "positions", dev)
+        if positions.dim() not in (1, 2) or positions.shape[-1] != tq:
+            raise ValueError(f"positions must be [{tq}] or [axes, {tq}]")
+        axes, axis_stride = (1 if positions.dim() == 1 else positions.shape[0]), tq
+    elif rot:
+        if cu_seqlens_q_host is None or cu_seqlens_q is None or used_kv_lens is None:
+            raise ValueError("positions, or cu_seqlens_q_host, cu_seqlens_q and used_kv_lens, are needed")
+        cu_h, batch = _batch_args(cu_seqlens_q_host, cu_seqlens_q, used_kv_lens, (), dev, ())
+    if freq_axes is not None:
+        _require(freq_axes, torch.int32, "freq_axes", dev)
+        if freq_axes.numel() * 2 != rot:
+            raise ValueError(f"freq_axes must have {rot // 2} values")
+    q_st, k_st, qo_st, ko_st = [(0, 0) if t is None else t.stride()[:2]
+                                for t in (q, k, q_out, k_out)]
+    _check(_on(dev, _native.load().sa_norm_rope, _ptr(q), _ptr(k), _ACT_DTYPES[given.dtype], *q_st,
+               *k_st, _ptr(q_weight if q is not None else None),
+               _ptr(k_weight if k is not None else None), _ACT_DTYPES[wt or torch.float32], eps,
+               _ptr(inv_freq), rot, _ptr(freq_axes), int(bool(interleaved)), _ptr(positions), axes,
+               axis_stride, None if cu_h is None else _host_ptr(cu_h),
+               None if cu_h is None else cu_seqlens_q.data_ptr(), batch,
+               None if cu_h is None else used_kv_lens.data_ptr(), tq,
+               0 if q is None else q.shape[1], 0 if k is None else k.shape[1], d, _ptr(q_out),
+               _ptr(k_out), _ACT_DTYPES[out.dtype], *qo_st, *ko_st, _status_word(status, dev),
+               _stream(stream, dev)), "sa_norm_rope")
+    return q_out, k_out
+
+
+def _heads(t, name):
+    """The type of a [tokens, heads, channels] activation, after its checks."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _ACT_DTYPES:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, channels]")
+    if t.numel() and t.stride(2) != 1 and t.shape[2] != 1:
+        raise ValueError(f"{name}: channels must be contiguous")
+    return t.dtype
+
+
+def _pool(k_pages, v_pages, k_scales, v_scales):
+    """Checks of a cache of any type: its type's code."""
+    code = _CACHE_DTYPES.get(getattr(k_pages, "dtype", None))
+    try:
+        shape, index = k_pages.shape, k_pages.get_device()
+        if code is not None and index >= 0 and len(shape) == 4 and v_pages.shape == shape and (
+                _alike(index, k_pages.dtype, k_pages, v_pages)):
+            if code != DTYPE_E4M3 and code != DTYPE_INT8:
+                if k_scales is None and v_scales is None:
+                    return code
+            elif (k_scales.shape == shape[:2] and v_scales.shape == shape[:2] and
+                  _alike(index, torch.float32, k_scales, v_scales)):
+                return code
+    except AttributeError:
+        pass
+    code = _cache_dtype(k_pages, "k_pages")
+    _require(k_pages, k_pages.dtype, "k_pages")
+    _require(v_pages, k_pages.dtype, "v_pages", k_pages.device)
+    if v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages and v_pages must have one shape")
+    _scales(k_scales, k_pages, "k_scales")
+    _scales(v_scales, v_pages, "v_scales")
+    return code
+
+
+def sa_load_kv(k_pages, v_pages, block_tables, cu_seqlens_host, cu_seqlens, used_kv_lens, k=None,
+               v=None, dtype=None, k_scales=None, v_scales=None, status=None, stream=None):
+    """Read rows of the cache back: with the lengths of a :func:`sa_store_kv` call the
+    rows that it stored, each sequence's last ``cu_seqlens`` positions below
+    ``used_kv_lens`` (the whole sequence where both agree).  Returns (k, v) [rows,
+    hkv, d] of ``dtype`` (float32 or bfloat16; default: that of ``k``, else the
+    cache's, bfloat16 for 8 bits); ``k`` / ``v`` handed in may be strided.  Rows that the
+    cache does not hold become 0."""
+    code = _pool(k_pages, v_pages, k_scales, v_scales)
+    dev = k_pages.device
+    num_pages, hkv, page_size, d = k_pages.shape
+    cu_h, batch = _batch_args(cu_seqlens_host, cu_seqlens, used_kv_lens, (block_tables,), dev,
+                              ("block_tables",))
+    rows = int(cu_h[-1]) if cu_h.size else 0
+    if dtype is None:
+        some = k if k is not None else v
+        dtype = some.dtype if some is not None else (
+            torch.float32 if k_pages.dtype is torch.float32 else torch.bfloat16)
+    if dtype not in _ACT_DTYPES:
+        raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
+    shape = (max(rows, 0), hkv, d)
+    made = []
+    for t, name in ((k, "k"), (v, "v")):
+        if t is None:
+            with _allocating(stream):
+                t = torch.empty(shape, dtype=dtype, device=dev)
+        elif (_heads(t, name) != dtype or t.shape != shape or t.device != dev):
+            raise ValueError(f"{name} must be {shape} of {dtype} on {dev}")
+        made.append(t)
+    k, v = made
+    ks0, ks1, _ = k.stride()
+    vs0, vs1, _ = v.stride()
+    _check(_on(dev, _native.load().sa_load_kv, k_pages.data_ptr(), v_pages.data_ptr(),
+               _ptr(k_scales), _ptr(v_scales), num_pages, code, block_tables.data_ptr(),
+               block_tables.shape[1], _host_ptr(cu_h), cu_seqlens.data_ptr(), batch, rows,
+               used_kv_lens.data_ptr(), hkv, d, page_size, k.data_ptr(), v.data_ptr(),
+               _ACT_DTYPES[dtype], ks0, ks1, vs0, vs1, _status_word(status, dev),
+               _stream(stream, dev)), "sa_load_kv")
+    return k, v
+
+
+def allocate_decode_workspace(batch, hq, hkv, head_dim, device) -> torch.Tensor:
+    """Scratch for :func:`sa_decode_attention` over these sizes, to be kept from call
+    to call."""
+    n = ctypes.c_size_t(0)
+    _check(_native.load().sa_decode_workspace_size(batch, hq, hkv, head_dim, ctypes.byref(n)),
+           "sa_decode_workspace_size")
+    return torch.empty(n.value + 256, dtype=torch.uint8, device=device)
+
+
+def sa_decode_attention(q, k_pages, v_pages, block_tables, used_kv_lens, softmax_scale, window=0,
+                        k_scales=None, v_scales=None, out=None, lse=None, with_lse=True,
+                        workspace=None, status=None, stream=None):
+    """One new token per sequence over its whole cache: query b of ``q`` [batch, hq, d]
+    (float32 or bfloat16) attends over the positions below ``used_kv_lens[b]``, the
+    last ``window`` of them where that is not 0.  Any cache type (with ``k_scales`` and
+    ``v_scales`` for 8 bits) and any hq / hkv.  Returns (out, lse): out of q's type, lse
+    [batch, hq] float32; a sequence of length 0 gets 0 and -inf."""
+    code = _pool(k_pages, v_pages, k_scales, v_scales)
+    dev = k_pages.device
+    num_pages, hkv, page_size, d = k_pages.shape
+    act = _ACT_DTYPES.get(getattr(q, "dtype", None))
+    if act is None:
+        raise TypeError("q must be a float32 or bfloat16 tensor")
+    _require(q, q.dtype, "q", dev)
+    if q.dim() != 3 or q.shape[2] != d:
+        raise ValueError(f"q must be [batch, hq, {d}], got {tuple(q.shape)}")
+    batch, hq, _ = q.shape
+    try:
+        usual = (_alike(dev.index, torch.int32, block_tables, used_kv_lens) and
+                 block_tables.dim() == 2 and block_tables.shape[0] == batch and
+                 used_kv_lens.numel() == batch)
+    except AttributeError:
+        usual = False
+    if not usual:
+        _require(block_tables, torch.int32, "block_tables", dev)
+        _require(used_kv_lens, torch.int32, "used_kv_lens", dev)
+        if block_tables.dim() != 2 or block_tables.shape[0] != batch or used_kv_lens.numel() != batch:
+            raise ValueError(f"block_tables and used_kv_lens must have a row for each of the {batch} sequences")
+    _check_room(dev, (out, q.dtype, batch * hq * d, "out"), (lse, torch.float32, batch * hq, "lse"))
+    if out is None or workspace is None or (lse is None and with_lse):
+        with _allocating(stream):
+            if out is None:
+                out = torch.empty((batch, hq, d), dtype=q.dtype, device=dev)
+            if lse is None and with_lse:
+                lse = torch.empty((batch, hq), dtype=torch.float32, device=dev)
+            if workspace is None:
+                workspace = allocate_decode_workspace(batch, hq, hkv, d, dev)
+    _require(workspace, torch.uint8, "workspace", dev)
+    base = workspace.data_ptr()
+    aligned = (base + 255) & ~255
+    _check(_on(dev, _native.load().sa_decode_attention, q.data_ptr(), act, k_pages.data_ptr(),
+               v_pages.data_ptr(), _ptr(k_scales), _ptr(v_scales), num_pages, code,
+               block_tables.data_ptr(), block_tables.shape[1], used_kv_lens.data_ptr(), batch, hq,
+               hkv, d, page_size, softmax_scale, window, out.data_ptr(), _ptr(lse), aligned,
+               max(workspace.numel() - (aligned - base), 0), _status_word(status, dev),
+               _stream(stream, dev)), "sa_decode_attention")
+    return out, lse
 
 
 def sa_get_status(index: Index, stream=None) -> int:

@@ -26,7 +26,8 @@ EXPORTS = ("sa_status_string", "sa_version", "sa_index_query_sizes", "sa_index_w
            "sa_combine", "sa_combine_ex", "sa_attention", "sa_attention_ex", "sa_get_status",
            "sa_clear_status", "sa_forward_scaled", "sa_forward_combine_scaled",
            "sa_attention_scaled", "sa_store_kv", "sa_block_bounds", "sa_select_workspace_size",
-           "sa_select_blocks", "sa_debug_stall", "sa_debug_cta_stats")
+           "sa_select_blocks", "sa_norm_rope", "sa_load_kv", "sa_decode_workspace_size",
+           "sa_decode_attention", "sa_debug_stall", "sa_debug_cta_stats")
 
 
 class SaIndex(ctypes.Structure):
@@ -148,6 +149,18 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.sa_select_blocks.argtypes = [p, st, i64, i32, i32, i32, p, i64, p, i32, p, p, i32, p, i32,
                                      i32, i32, i32, i32, p, p, ctypes.c_size_t, p, p]
     lib.sa_select_blocks.restype = st
+    lib.sa_norm_rope.argtypes = [p, p, st, i64, i64, i64, i64, p, p, st, f32, p, i32, p, i32, p, i32,
+                                 i64, p, p, i32, p, i64, i32, i32, i32, p, p, st, i64, i64, i64,
+                                 i64, p, p]
+    lib.sa_norm_rope.restype = st
+    lib.sa_load_kv.argtypes = [p, p, p, p, i64, st, p, i32, p, p, i32, i64, p, i32, i32, i32, p, p,
+                               st, i64, i64, i64, i64, p, p]
+    lib.sa_load_kv.restype = st
+    lib.sa_decode_workspace_size.argtypes = [i32, i32, i32, i32, ctypes.POINTER(ctypes.c_size_t)]
+    lib.sa_decode_workspace_size.restype = st
+    lib.sa_decode_attention.argtypes = [p, st, p, p, p, p, i64, st, p, i32, p, i32, i32, i32, i32,
+                                        i32, f32, i32, p, p, p, ctypes.c_size_t, p, p]
+    lib.sa_decode_attention.restype = st
     lib.sa_debug_stall.argtypes = [i32, ctypes.c_uint32]
     lib.sa_debug_stall.restype = st
     lib.sa_debug_cta_stats.argtypes = [p, i32]

@@ -661,6 +661,128 @@ sa_status sa_select_blocks(const void *q, sa_dtype q_dtype, int64_t tq, int32_t 
                            size_t workspace_bytes, int64_t *status, void *stream);
 
 /*
+ * Head norms and position rotation of new tokens' queries and keys in one pass,
+ * what comes before sa_store_kv.  Per (token, head) row x of head_dim channels:
+ *
+ *   y = x / sqrt(mean(x^2) + eps) * weight        (y = x where weight is NULL)
+ *   (y_a, y_b) = (y_a cos t - y_b sin t, y_a sin t + y_b cos t),
+ *   t = position(token, axis(i)) * inv_freq[i],  i < rot_dim / 2,
+ *
+ * with (a, b) = (i, i + rot_dim / 2), or (2 i, 2 i + 1) where `interleaved` is not 0;
+ * channels from rot_dim on are not rotated.  Sums are f32, angles exact to 2^-31
+ * turns at any 32-bit position, and each output is rounded once.
+ *
+ *   q, k          [tq, hq, head_dim], [tq, hkv, head_dim] of src_dtype (f32 or
+ *                 bf16); channels contiguous, tokens and heads at the given
+ *                 strides (elements).  hq or hkv may be 0 (pointers unused).
+ *   q_weight,
+ *   k_weight      [head_dim] of weight_dtype (f32 or bf16), each may be NULL
+ *   inv_freq      [rot_dim / 2] f32, finite
+ *   positions     [n_axes] rows of tq int32, axis_stride elements apart; with
+ *                 n_axes = 0 none: then token t of sequence b stands at lk_b - qo_b + t (at t where
+ *                 lk_b < qo_b), the positions that sa_store_kv gives its key
+ *                 with the same lengths, and cu_seqlens_q_host [batch + 1],
+ *                 cu_seqlens_q and used_kv_lens [batch] are required
+ *   freq_axes     [rot_dim / 2] int32 in [0, n_axes): the axis whose position
+ *                 turns pair i (needs positions; NULL: axis 0)
+ *   q_out, k_out  as q and k, of out_dtype (f32 or bf16), strides of their own.
+ *                 An output may be its input (same address, type and strides);
+ *                 other overlaps are not allowed.
+ *   status        as for sa_store_kv
+ *
+ * Supported: head_dim <= 256, any strides and alignment (fastest where head_dim
+ * is a multiple of 8, rot_dim of 16, and every row starts on 16 bytes).  Checks,
+ * in order: HEAD_COUNT (hq + hkv = 0), HEAD_DIM (rot_dim odd or above head_dim),
+ * SHAPE (tq, n_axes), CU_SEQLENS and SHAPE (n_axes = 0), INVALID_ARGUMENT (types, eps
+ * negative or NaN, freq_axes without positions), UNSUPPORTED, INVALID_ARGUMENT
+ * (NULL); on device: SHAPE (an axis outside [0, n_axes), taken as axis 0).
+ */
+sa_status sa_norm_rope(const void *q, const void *k, sa_dtype src_dtype, int64_t q_token_stride,
+                       int64_t q_head_stride, int64_t k_token_stride, int64_t k_head_stride,
+                       const void *q_weight, const void *k_weight, sa_dtype weight_dtype,
+                       float eps, const float *inv_freq, int32_t rot_dim,
+                       const int32_t *freq_axes, int32_t interleaved, const int32_t *positions,
+                       int32_t n_axes, int64_t axis_stride, const int64_t *cu_seqlens_q_host,
+                       const int64_t *cu_seqlens_q, int32_t batch, const int32_t *used_kv_lens,
+                       int64_t tq, int32_t hq, int32_t hkv, int32_t head_dim, void *q_out,
+                       void *k_out, sa_dtype out_dtype, int64_t q_out_token_stride,
+                       int64_t q_out_head_stride, int64_t k_out_token_stride,
+                       int64_t k_out_head_stride, int64_t *status, void *stream);
+
+/*
+ * Reading rows of the paged cache back: with the arguments of a sa_store_kv call
+ * the rows that it stored, i.e. for sequence b its positions lk_b - qo_b .. lk_b - 1
+ * (0 .. qo_b - 1 where lk_b < qo_b), qo_b from cu_seqlens and lk_b =
+ * used_kv_lens[b].  qo_b = lk_b reads a whole sequence, lk_b = n a prefix of n.
+ *
+ *   k, v          [tq, hkv, head_dim] of dst_dtype (f32 or bf16), written;
+ *                 channels contiguous, tokens and heads at the given strides
+ *                 (elements; multiples of 16 bytes)
+ *
+ * Other arguments as for sa_store_kv.  Values of 8-bit caches are code * scale in
+ * f32, rounded to nearest even for bf16 (scales that sa_store_kv made are powers
+ * of two: then exact in both).  Rows that the cache does not hold (a page id
+ * below 0 or past the table, positions from lk_b on) become 0.
+ *
+ * Checks, in order: HEAD_COUNT, BLOCK_PAGE, CU_SEQLENS, SHAPE, INVALID_ARGUMENT
+ * (types), UNSUPPORTED (head_dim not a multiple of 8, or 16 for the 8-bit types, or
+ * above 256), INVALID_ARGUMENT (NULL, alignment, strides); on device: SHAPE
+ * (page id >= num_pages, taken as absent).
+ */
+sa_status sa_load_kv(const void *k_pages, const void *v_pages, const float *k_scales,
+                     const float *v_scales, int64_t num_pages, sa_dtype kv_dtype,
+                     const int32_t *block_tables, int32_t max_pages,
+                     const int64_t *cu_seqlens_host, const int64_t *cu_seqlens, int32_t batch,
+                     int64_t tq, const int32_t *used_kv_lens, int32_t hkv, int32_t head_dim,
+                     int32_t page_size, void *k, void *v, sa_dtype dst_dtype,
+                     int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                     int64_t v_head_stride, int64_t *status, void *stream);
+
+/*
+ * Attention of one new token per sequence over its whole cache, without a
+ * selection: what layers without block selection run beside the others.  Query
+ * b attends over positions max(0, lk_b - window) .. lk_b - 1 of sequence b (window
+ * = 0: all; lk_b = used_kv_lens[b], the length WITH the new token), at most the
+ * max_pages * page_size positions that its table has columns for:
+ *
+ *   out = softmax(softmax_scale q K^T) V,   lse = log sum exp(softmax_scale q K^T).
+ *
+ * A sequence without keys in sight gets out = 0 and lse = -inf.
+ *
+ *   q             [batch, hq, head_dim] of q_dtype (f32 or bf16); q-heads
+ *                 h * hq / hkv .. of kv head h
+ *   k_pages, v_pages, k_scales, v_scales, num_pages, kv_dtype, block_tables,
+ *   max_pages     as for sa_store_kv; keys of pages with an id below 0 do not exist
+ *   out           [batch, hq, head_dim] of q_dtype
+ *   lse           [batch, hq] f32, or NULL
+ *   workspace     device memory of sa_decode_workspace_size bytes, 16-byte
+ *                 aligned; nothing is kept in it from call to call, and calls that
+ *                 overlap on the GPU need one each
+ *   status        as for sa_store_kv
+ *
+ * Nothing that stands at other positions of the pages is read into a result
+ * (infinities and NaN there do not matter); a key or value in sight that is not finite
+ * makes its rows' results unspecified.  Results do not depend on timing: the
+ * same call gives the same bits.
+ *
+ * Checks, in order: HEAD_COUNT, HEAD_DIM, SHAPE (batch < 0), BLOCK_PAGE, SHAPE,
+ * INVALID_ARGUMENT (types), UNSUPPORTED (head_dim not a multiple of 8, or 16 for the
+ * 8-bit types, or above 256; batch * hq >= 2^31), INVALID_ARGUMENT (NULL, alignment, workspace);
+ * on device: SHAPE (page id >= num_pages, taken as absent).
+ */
+sa_status sa_decode_workspace_size(int32_t batch, int32_t hq, int32_t hkv, int32_t head_dim,
+                                   size_t *bytes);
+
+sa_status sa_decode_attention(const void *q, sa_dtype q_dtype, const void *k_pages,
+                              const void *v_pages, const float *k_scales, const float *v_scales,
+                              int64_t num_pages, sa_dtype kv_dtype, const int32_t *block_tables,
+                              int32_t max_pages, const int32_t *used_kv_lens, int32_t batch,
+                              int32_t hq, int32_t hkv, int32_t head_dim, int32_t page_size,
+                              float softmax_scale, int32_t window, void *out, float *lse,
+                              void *workspace, size_t workspace_bytes, int64_t *status,
+                              void *stream);
+
+/*
  * Test hook for the bounded device waits (the pages have no counterpart:
  * their GpuRuntimeError stands for any device failure).  Every wait inside
  * the kernels gives up after a bounded number of tries, records
