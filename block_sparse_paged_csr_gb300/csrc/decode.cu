@@ -1,121 +1,27 @@
-// Attention of one new token per sequence over its whole paged cache (or the last
-// `window` keys of it).
+// Entry point of the attention of one new token per sequence over its whole cache; the
+// kernels are in decode_split.cuh.
+#include <algorithm>
 #include <cstdint>
 
 #include "internal.h"
-#include "seq_common.cuh"
 
 namespace sa {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+int padded_dim(int head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256; }
 
-struct DecodeArgs {
-  const void* q;
-  const void* k_pages;
-  const void* v_pages;
-  const float* k_scales;
-  const float* v_scales;
-  int64_t num_pages;
-  const int32_t* block_tables;
-  const int32_t* used;
-  int32_t batch, hq, hkv, qhead, head_dim, page_size, max_pages, window, q_bf16, kv_type;
-  float scale;
-  void* out;
-  float* lse;
-  int64_t* status;
+// Bytes of the workspace's regions, each a multiple of 256.
+struct Workspace {
+  size_t firsts, parts, joins;
+  size_t total() const { return firsts + parts + joins; }
 };
-
-__device__ __forceinline__ float cached(const void* p, int64_t at, int type) {
-  if (type == SA_DTYPE_F32) return static_cast<const float*>(p)[at];
-  if (type == SA_DTYPE_BF16) return bf16_to_f32(static_cast<const uint16_t*>(p)[at]);
-  const uint32_t w = static_cast<const uint8_t*>(p)[at];
-  uint32_t lo, hi;
-  if (type == SA_DTYPE_INT8)
-    codes4_to_f16<true>(w, lo, hi);
-  else
-    codes4_to_f16<false>(w, lo, hi);
-  return f16x2_to_f32(lo).x;
-}
-
-// A CTA per (sequence, q-head): a key per warp at a time, a lane holding channels
-// lane, lane + 32, ..; the warps' states meet in shared memory.
-__global__ void __launch_bounds__(kThreads) decode_attention_kernel(const DecodeArgs a) {
-  __shared__ float s_m[kWarps], s_l[kWarps], s_o[kWarps][256];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t row = blockIdx.x;
-  const int b = static_cast<int>(row / a.hq);
-  const int h = static_cast<int>(row - static_cast<int64_t>(b) * a.hq) / a.qhead;
-  const int64_t lk = min(static_cast<int64_t>(max(a.used[b], 0)),
-                         static_cast<int64_t>(a.max_pages) * a.page_size);
-  const int64_t first = a.window > 0 ? max(static_cast<int64_t>(a.used[b]) - a.window, int64_t{0}) : 0;
-  const bool eight = a.kv_type == SA_DTYPE_E4M3 || a.kv_type == SA_DTYPE_INT8;
-  float q[8], o[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int c = lane + 32 * i;
-    o[i] = 0.f;
-    q[i] = c >= a.head_dim ? 0.f
-           : a.q_bf16 ? bf16_to_f32(static_cast<const uint16_t*>(a.q)[row * a.head_dim + c])
-                      : static_cast<const float*>(a.q)[row * a.head_dim + c];
-  }
-  float m = -INFINITY, l = 0.f;
-  for (int64_t key = first + warp; key < lk; key += kWarps) {
-    const int64_t pg = key / a.page_size;
-    const int id = a.block_tables[static_cast<int64_t>(b) * a.max_pages + pg];
-    if (id >= a.num_pages && lane == 0) report(a.status, SA_ERR_SHAPE);
-    if (id < 0 || id >= a.num_pages) continue;
-    const int64_t at =
-        ((static_cast<int64_t>(id) * a.hkv + h) * a.page_size + (key - pg * a.page_size)) *
-        a.head_dim;
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (lane + 32 * i < a.head_dim)
-        s = fmaf(q[i], cached(a.k_pages, at + lane + 32 * i, a.kv_type), s);
-#pragma unroll
-    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= a.scale;
-    float vs = 1.f;
-    if (eight) {
-      s *= a.k_scales[static_cast<int64_t>(id) * a.hkv + h];
-      vs = a.v_scales[static_cast<int64_t>(id) * a.hkv + h];
-    }
-    const float top = fmaxf(m, s);
-    const float e = m == top ? 1.f : expf(m - top), p = expf(s - top);
-    m = top;
-    l = l * e + p;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (lane + 32 * i < a.head_dim)
-        o[i] = o[i] * e + p * vs * cached(a.v_pages, at + lane + 32 * i, a.kv_type);
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) s_o[warp][lane + 32 * i] = o[i];
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-  }
-  __syncthreads();
-  float top = -INFINITY, sum = 0.f, acc = 0.f;
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w]);
-  const int c = threadIdx.x;
-  for (int w = 0; w < kWarps; ++w) {
-    const float e = s_l[w] == 0.f ? 0.f : expf(s_m[w] - top);
-    sum += e * s_l[w];
-    acc += e * s_o[w][c];
-  }
-  if (c < a.head_dim) {
-    const float y = sum == 0.f ? 0.f : acc / sum;
-    if (a.q_bf16)
-      static_cast<uint16_t*>(a.out)[row * a.head_dim + c] =
-          static_cast<uint16_t>(pack_bf16x2_rn(y, 0.f) & 0xFFFFu);
-    else
-      static_cast<float*>(a.out)[row * a.head_dim + c] = y;
-  }
-  if (c == 0 && a.lse) a.lse[row] = sum == 0.f ? -INFINITY : top + logf(sum);
+Workspace decode_workspace(int qhead, int head_dim) {
+  const size_t state = sizeof(float) * decode_state_floats(padded_dim(std::min(head_dim, 256)),
+                                                           qhead <= 8 ? 8 : 16);
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  return {up(kDecodeCtas * kDecodeMaxWarps * state), up(kDecodeCtas * 2 * state),
+          up(kDecodeCtas * sizeof(int2))};
 }
 
 }  // namespace
@@ -130,7 +36,7 @@ sa_status sa_decode_workspace_size(int32_t batch, int32_t hq, int32_t hkv, int32
   if (head_dim <= 0) return SA_ERR_HEAD_DIM;
   if (batch < 0) return SA_ERR_SHAPE;
   if (bytes == nullptr) return SA_ERR_INVALID_ARGUMENT;
-  *bytes = 16;
+  *bytes = sa::decode_workspace(hq / hkv, head_dim).total();
   return SA_OK;
 }
 
@@ -162,32 +68,55 @@ sa_status sa_decode_attention(const void* q, sa_dtype q_dtype, const void* k_pag
   if (!sa::aligned16(q) || !sa::aligned16(out) || !sa::aligned16(k_pages) ||
       !sa::aligned16(v_pages) || !sa::aligned16(workspace) || workspace_bytes < need)
     return SA_ERR_INVALID_ARGUMENT;
+  const int qhead = hq / hkv;
+  // Query rows of a tile: 16 where a kv head has more than 8 q-heads (f32 caches keep 8: their
+  // operands come in two parts each, which fill the rows), in several groups where
+  // 16 are not enough.
+  const int r = qhead <= 8 || kv_dtype == SA_DTYPE_F32 ? 8 : 16;
+  const sa::Workspace ws = sa::decode_workspace(qhead, head_dim);
+  unsigned char* base = static_cast<unsigned char*>(workspace);
   sa::DecodeArgs a{};
   a.q = q;
-  a.k_pages = k_pages;
-  a.v_pages = v_pages;
-  a.k_scales = k_scales;
-  a.v_scales = v_scales;
+  // (copies of rows that are not there name the pools' start and read nothing: some address)
+  a.k_pages = num_pages > 0 ? k_pages : workspace;
+  a.v_pages = num_pages > 0 ? v_pages : workspace;
+  a.k_scales = num_pages > 0 ? k_scales : static_cast<const float*>(workspace);
+  a.v_scales = num_pages > 0 ? v_scales : static_cast<const float*>(workspace);
   a.num_pages = num_pages;
   a.block_tables = block_tables;
   a.used = used_kv_lens;
   a.batch = batch;
   a.hq = hq;
   a.hkv = hkv;
-  a.qhead = hq / hkv;
+  a.qhead = qhead;
+  a.groups = (qhead + r - 1) / r;
+  a.items_per_seq = hkv * a.groups;
   a.head_dim = head_dim;
+  a.row_bytes = head_dim * (kv_dtype == SA_DTYPE_F32 ? 4 : kv_dtype == SA_DTYPE_BF16 ? 2 : 1);
   a.page_size = page_size;
+  a.page_shift = (page_size & (page_size - 1)) == 0 ? __builtin_ctz(page_size) : -1;
   a.max_pages = max_pages;
+  a.capacity = static_cast<int32_t>(
+      std::min<int64_t>(static_cast<int64_t>(max_pages) * page_size, 0x7FFFFF00));
   a.window = window;
-  a.q_bf16 = q_dtype == SA_DTYPE_BF16;
-  a.kv_type = kv_dtype;
+  a.act_bf16 = q_dtype == SA_DTYPE_BF16;
   a.scale = softmax_scale;
   a.out = out;
   a.lse = lse;
   a.status = status;
-  sa::decode_attention_kernel<<<static_cast<unsigned>(batch * hq), sa::kThreads, 0,
-                                static_cast<cudaStream_t>(stream)>>>(a);
-  return cudaGetLastError() == cudaSuccess ? SA_OK : SA_ERR_CUDA;
+  a.firsts = reinterpret_cast<float*>(base);
+  a.parts = reinterpret_cast<float*>(base + ws.firsts);
+  a.joins = reinterpret_cast<int2*>(base + ws.firsts + ws.parts);
+  const int dp = sa::padded_dim(head_dim);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t err;
+  switch (kv_dtype) {
+    case SA_DTYPE_F32: err = sa::launch_decode_f32(a, dp, r, s); break;
+    case SA_DTYPE_BF16: err = sa::launch_decode_bf16(a, dp, r, s); break;
+    case SA_DTYPE_E4M3: err = sa::launch_decode_e4m3(a, dp, r, s); break;
+    default: err = sa::launch_decode_int8(a, dp, r, s); break;
+  }
+  return err == cudaSuccess ? SA_OK : SA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -231,6 +231,44 @@ struct FusedQ8Args {
 bool fused_dec_q8_supported(int head_dim, int block_size, int page_size, int qhead);
 cudaError_t launch_fused_dec_q8(const FusedQ8Args& a, cudaStream_t stream);
 
+// Attention of one new token per sequence over its whole cache (decode_split.cuh).
+constexpr int kDecodeCtas = 160;      // CTAs of a launch at most (one per SM)
+constexpr int kDecodeMaxWarps = 8;    // warps of a CTA at most
+// f32 numbers of a warp's state: o, and m, n and l of each query row (dp: head_dim
+// rounded up to 64, 128 or 256; r: query rows of a tile).
+constexpr int decode_state_floats(int dp, int r) { return r * dp + 3 * r; }
+
+struct DecodeArgs {
+  const void* q;            // f32, or bf16 when act_bf16 (out too)
+  const void* k_pages;
+  const void* v_pages;
+  const float* k_scales;    // [num_pages, hkv], 8-bit K/V only
+  const float* v_scales;
+  int64_t num_pages;
+  const int32_t* block_tables;
+  const int32_t* used;
+  int32_t batch, hq, hkv, qhead;
+  int32_t groups;           // lane groups of a kv head
+  int32_t items_per_seq;    // hkv * groups
+  int32_t head_dim, row_bytes, page_size;
+  int32_t page_shift;       // log2(page_size), or -1
+  int32_t max_pages, capacity;   // capacity: max_pages * page_size, at most 2^31 - 256
+  int32_t window, act_bf16;
+  float scale;
+  void* out;
+  float* lse;               // nullable
+  int64_t* status;          // nullable
+  float* firsts;            // workspace: [CTA][warp] states of the pieces that warps began with
+  float* parts;             // [CTA][2] states of a CTA's first and last pair
+  int2* joins;              // [CTA] the pair that its first part goes on from the CTA before
+                            // (-1: none), and whether it ends there
+};
+// dp: head_dim rounded up, r: query rows of a tile (8 or 16; 8 for f32 caches).
+cudaError_t launch_decode_f32(const DecodeArgs& a, int dp, int r, cudaStream_t stream);
+cudaError_t launch_decode_bf16(const DecodeArgs& a, int dp, int r, cudaStream_t stream);
+cudaError_t launch_decode_e4m3(const DecodeArgs& a, int dp, int r, cudaStream_t stream);
+cudaError_t launch_decode_int8(const DecodeArgs& a, int dp, int r, cudaStream_t stream);
+
 struct CombineArgs {
   const int32_t* inv;
   const int64_t* edge_head_base;
