@@ -17,10 +17,14 @@ struct Workspace {
   size_t total() const { return firsts + parts + joins; }
 };
 Workspace decode_workspace(int qhead, int head_dim) {
-  const size_t state = sizeof(float) * decode_state_floats(padded_dim(std::min(head_dim, 256)),
-                                                           qhead <= 8 ? 8 : 16);
+  const int dp = padded_dim(std::min(head_dim, 256));
+  // (the larger of what the two row counts need: f32 caches keep 8 rows)
+  auto bytes = [&](int r) {
+    return sizeof(float) * static_cast<size_t>(decode_max_warps(dp, r)) * decode_state_floats(dp, r);
+  };
+  const size_t state = sizeof(float) * decode_state_floats(dp, qhead <= 8 ? 8 : 16);
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  return {up(kDecodeCtas * kDecodeMaxWarps * state), up(kDecodeCtas * 2 * state),
+  return {up(kDecodeCtas * std::max(bytes(8), qhead <= 8 ? 0 : bytes(16))), up(kDecodeCtas * 2 * state),
           up(kDecodeCtas * sizeof(int2))};
 }
 
@@ -57,7 +61,10 @@ sa_status sa_decode_attention(const void* q, sa_dtype q_dtype, const void* k_pag
   if (kv_dtype < SA_DTYPE_F32 || kv_dtype > SA_DTYPE_INT8) return SA_ERR_INVALID_ARGUMENT;
   if (head_dim % (sa::eight_bit(kv_dtype) ? 16 : 8) != 0 || head_dim > 256)
     return SA_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(batch) * hq > 0x7FFFFFFF) return SA_ERR_UNSUPPORTED;
+  // (row numbers of the pools are 32-bit)
+  if (static_cast<int64_t>(batch) * hq > 0x7FFFFFFF ||
+      (num_pages > 0 && num_pages > int64_t{0xFFFFFFFE} / page_size / hkv))
+    return SA_ERR_UNSUPPORTED;
   if (batch == 0) return SA_OK;
   // (a cache without pages or columns may have no memory either)
   if (!q || !out || !used_kv_lens || !workspace || (max_pages > 0 && !block_tables) ||

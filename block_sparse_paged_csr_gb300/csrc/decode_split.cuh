@@ -37,6 +37,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 // kRoom no P of at most 2^kSlack makes a product above 2^15; f16 ends at 2^16).
 constexpr float kSlack = 7.f, kTop = 4.f, kRoom = 256.f;
 
+constexpr int kInfos = 4;            // tiles that are copied or in use at a time, at most
+
 template <int T> struct TypeOf;
 template <> struct TypeOf<SA_DTYPE_F32> { static constexpr int size = 4; };
 template <> struct TypeOf<SA_DTYPE_BF16> { static constexpr int size = 2; };
@@ -44,43 +46,59 @@ template <> struct TypeOf<SA_DTYPE_E4M3> { static constexpr int size = 1; };
 template <> struct TypeOf<SA_DTYPE_INT8> { static constexpr int size = 1; };
 
 // T: the cache's type.  DP: head_dim rounded up to 64, 128 or 256 (channels behind it
-// are zeros).  R: query rows of a tile, 8 or 16.
-template <int T, int DP, int R>
+// are zeros).  R: query rows of a tile, 8 or 16.  B: bf16 queries, whose operands have one part (for
+// the instances where that saves shared memory or products; the others take both types).
+template <int T, int DP, int R, bool B>
 struct Cfg {
   static constexpr int kSize = TypeOf<T>::size;
   static constexpr bool kF32 = T == SA_DTYPE_F32;
   static constexpr bool k8 = kSize == 1;
   static constexpr int kRow = DP * kSize;                       // bytes of a row in the ring
   // keys of a tile: 4 KB of K where that is 8 to 32 keys
-  static constexpr int kKT = kF32 ? (DP == 64 ? 16 : 8) : k8 ? (DP == 256 ? 16 : 32) : (DP == 64 ? 32 : 16);
+  static constexpr int kKT = 4096 / kRow < 8 ? 8 : 4096 / kRow > 32 ? 32 : 4096 / kRow;
   static constexpr int kEntry = kKT * kRow;                     // bytes of a tile's K (or V)
-  static constexpr int kST = 2;                                 // tiles of the ring
   static constexpr int kNCH = kRow / 16;                        // 16-byte chunks of a row
   static constexpr int kLCH = kNCH / 4;                         // chunks of a row that a lane reads for S
   static constexpr int kEC = 16 / kSize;                        // elements of a chunk
   static constexpr int kKPC = k8 ? 4 : 2;                       // k-steps of a chunk
   static constexpr int kKS = kLCH * kKPC;                       // k-steps of a row
   static constexpr int kNT = kKT / 8;                           // n-tiles of S
-  static constexpr int kKK = kF32 ? 8 : 16;                     // keys of one P V k-step
+  static constexpr int kKK = kF32 || kKT == 8 ? 8 : 16;         // keys of one P V k-step
   static constexpr int kVP = DP * kSize / 8 < 16 ? 8 : 16;      // bytes of V that a lane reads of a row at a time
   static constexpr int kEP = kVP / kSize;                       // .. channels
   static constexpr int kNS = DP / (8 * kEP);                    // .. times
   static constexpr int kNJ = DP / 8;                            // n-tiles of o
   static constexpr int kNR = R / 8;                             // query rows of a lane
-  // operands of Q kept per k-step (see load_q)
-  static constexpr int kQP = kF32 ? 1 : k8 ? (R == 8 ? 1 : 2) : (R == 8 ? 2 : 3);
+  // operands of Q kept per k-step (see load_q), and of P
+  static constexpr int kQP = kF32 ? 1 : k8 ? (R == 8 || B ? 1 : 2) : B ? 1 : R == 8 ? 2 : 3;
+  static constexpr int kPP = kF32 ? 1 : k8 ? (R == 8 || B ? 1 : 2) : R == 8 ? (B ? 1 : 2) : (B ? 2 : 3);
   static constexpr int kQBytes = kKS * kQP * 512;
-  static constexpr int kScales = k8 ? 2 * kST * kKT * 4 : 0;
-  static constexpr int kPerWarp = 2 * kST * kEntry + kQBytes + kScales + kST * 16;
-  static constexpr int kMost = 220 * 1024;
-  static constexpr int kW = kMost / kPerWarp < 8 ? kMost / kPerWarp : 8;   // warps
+  static constexpr int kScales = k8 ? kKT * 4 : 0;              // bytes of an entry's scales
+  // The ring's entries hold K and V in turn.  Three are least (one in use, two in
+  // flight); a fourth is taken where it costs no warp.  Warps are worth more than a longer
+  // ring (e4m3, 64 sequences of 20000 to 50000 keys: 12 warps of 3 entries 760 us, 8 of 4
+  // 830), since an instruction's latency shows with 2 of them on a scheduler; their
+  // number is a multiple of 4, as their ranges are equal and the four schedulers share
+  // them (10 warps of 4 entries: 1130 us).
+  static constexpr int warp_bytes(int ne) {
+    return ne * (kEntry + kScales) + kQBytes + kInfos * 16;
+  }
+  static constexpr int warps_of(int ne) {
+    return kMost / warp_bytes(ne) / 4 * 4 < decode_max_warps(DP, R)
+               ? kMost / warp_bytes(ne) / 4 * 4
+               : decode_max_warps(DP, R);
+  }
+  static constexpr int kMost = 220 * 1024;                       // (of 227 KB, some of them static)
+  static constexpr int kNE = warps_of(4) == warps_of(3) ? 4 : 3;
+  static constexpr int kPerWarp = warp_bytes(kNE);
+  static constexpr int kW = warps_of(kNE);                      // warps
   static constexpr int kThreads = 32 * kW;
   static constexpr int kSmem = kW * kPerWarp;
   // a state: o in the order of the accumulators, then m, n and l of each row
   static constexpr int kNel = R * DP;
   static constexpr int kState = kNel + 3 * R;
-  static_assert(kState * 4 <= 2 * kST * kEntry + kQBytes, "a warp's last state replaces its ring");
-  static_assert(kW >= 2 && kW <= kDecodeMaxWarps && kState <= decode_state_floats(DP, R), "workspace");
+  static_assert(kState * 4 <= kNE * kEntry + kQBytes, "a warp's last state replaces its ring");
+  static_assert(kW >= 2 && kState <= decode_state_floats(DP, R), "workspace");
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -129,6 +147,14 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint4& a, uint32_t b0, 
         "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+
+// The same over 8 keys for bf16 (m16n8k8).
+__device__ __forceinline__ void mma_k8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+      "{%4, %5}, {%6}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(b0));
 }
 
 // f32 as a tf32 high part (cut) and the rest, rounded to tf32's 11 bits: 2^-21 of x
@@ -189,15 +215,15 @@ __device__ __forceinline__ Item item_of(const DecodeArgs& a, int item) {
           min(R, a.qhead - grp * R)};
 }
 
-template <int T, int DP, int R>
+template <int T, int DP, int R, bool B>
 struct Worker {
-  using C = Cfg<T, DP, R>;
+  using C = Cfg<T, DP, R, B>;
 
   const DecodeArgs& a;
-  unsigned char* ring;           // this warp's [2 kST][kEntry]: K, V of a tile in turn
+  unsigned char* ring;           // this warp's [kNE][kEntry]
   unsigned char* qf;             // Q's operands
-  float* sc;                     // [2 kST][kKT] scales
-  uint4* info;                   // [kST]: item, live keys, flags
+  float* sc;                     // [kNE][kKT] scales
+  uint4* info;                   // [kInfos]: item, live keys, flags
   int lane, g, c;
 
   // ---- the tile to come: where it lies
@@ -210,6 +236,7 @@ struct Worker {
   // ---- state of the piece at hand
   float o[C::kNJ][4];
   float m_run[C::kNR], n_run[C::kNR], l_part[C::kNR], vfac[C::kNR], sfac[C::kNR];
+  bool clamp;                    // some V scale is beyond kRoom
 
   __device__ __forceinline__ void seek(int b0, int64_t in_seq) {
     b = b0;
@@ -252,26 +279,32 @@ struct Worker {
     return p;
   }
 
-  // Copies of one tile's K (kV false) or V rows; off: the lane's row (key `lane`) in
-  // bytes of the pool, negative where there is none; so: its scale's index.
+  // Copies of one tile's K (kV false) or V rows into entry e; row: the lane's (key
+  // `lane`) row of the pool, kNone where there is none (the pools have fewer rows).
+  static constexpr uint32_t kNone = 0xFFFFFFFFu;
   template <bool kV>
-  __device__ __forceinline__ void copy_rows(int slot, int64_t off, int64_t so) {
-    unsigned char* dst = ring + (2 * slot + (kV ? 1 : 0)) * C::kEntry;
+  __device__ __forceinline__ void copy_rows(int e, uint32_t row, uint32_t scale_at) {
     const unsigned char* pool = static_cast<const unsigned char*>(kV ? a.v_pages : a.k_pages);
-    const uint32_t d0 = smem_u32(dst);
+    const uint32_t d0 = smem_u32(ring + e * C::kEntry);
+    // a lane copies chunk lane % kNCH (and + 32 ..) of rows that are 32 / kNCH apart
+    constexpr int kPer = C::kNCH < 32 ? C::kNCH : 32;
+    const int ch0 = lane & (kPer - 1);
 #pragma unroll
     for (int i = 0; i < C::kKT * C::kNCH / 32; ++i) {
-      const int idx = 32 * i + lane;
-      const int row = idx / C::kNCH, ch = idx & (C::kNCH - 1);
-      const int64_t at = __shfl_sync(0xffffffffu, off, row);
-      const bool there = at >= 0 && 16 * ch < a.row_bytes;
-      const int phys = C::kNCH >= 8 ? ch ^ (row & 7) : ch ^ ((row >> 1) & 3);
-      copy16(d0 + row * C::kRow + phys * 16, pool + (there ? at + 16 * ch : 0), there);
+      const int r = C::kNCH <= 32 ? i * (32 / kPer) + lane / kPer : i / (C::kNCH / 32);
+      const int ch = C::kNCH <= 32 ? ch0 : ch0 + 32 * (i % (C::kNCH / 32));
+      const uint32_t at = __shfl_sync(0xffffffffu, row, r);
+      const bool there = at != kNone && 16 * ch < a.row_bytes;
+      const int phys = C::kNCH >= 8 ? ch ^ (r & 7) : ch ^ ((r >> 1) & 3);
+      const unsigned char* src =
+          pool + (there ? static_cast<uint64_t>(at) * static_cast<uint32_t>(a.row_bytes) + 16u * ch : 0);
+      copy16(d0 + r * C::kRow + phys * 16, src, there);
     }
     if constexpr (C::k8) {
       if (C::kKT == 32 || lane < C::kKT) {
-        const float* s = kV ? a.v_scales : a.k_scales;
-        copy4(smem_u32(sc + (2 * slot + (kV ? 1 : 0)) * C::kKT + lane), s + (off >= 0 ? so : 0), off >= 0);
+        const bool there = row != kNone;
+        copy4(smem_u32(sc + e * C::kKT + lane), (kV ? a.v_scales : a.k_scales) + (there ? scale_at : 0u),
+              there);
       }
     }
   }
@@ -345,7 +378,7 @@ struct Worker {
             if constexpr (C::kQP == 2) at[32] = make_uint4(lo[0][0], 0u, lo[0][1], 0u);
           } else {
             at[0] = make_uint4(hi[0][0], hi[1][0], hi[0][1], hi[1][1]);
-            at[32] = make_uint4(mid[0][0], mid[1][0], mid[0][1], mid[1][1]);
+            if constexpr (C::kQP >= 2) at[32] = make_uint4(mid[0][0], mid[1][0], mid[0][1], mid[1][1]);
             if constexpr (C::kQP == 3) at[64] = make_uint4(lo[0][0], lo[1][0], lo[0][1], lo[1][1]);
           }
         }
@@ -366,28 +399,29 @@ struct Worker {
       vfac[r] = 1.f;
       l_part[r] = 0.f;
     }
+    clamp = false;
 #pragma unroll
     for (int j = 0; j < C::kNJ; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
   }
 
-  // S = Q K^T of a tile: acc[nt][e] (row g: keys 8 nt + 2 c, + 1; then row g + 8).
-  // A fragment's k index may stand for any channel as long as both operands agree,
-  // so K's rows go from the ring to the MMA as they lie.
-  __device__ __forceinline__ void scores(int slot, float (&acc)[C::kNT][4]) {
-    const unsigned char* kt = ring + 2 * slot * C::kEntry + g * C::kRow;
+  // S = Q K^T of the tile in entry e: acc[nt][i] (row g: keys 8 nt + 2 c, + 1; then row g +
+  // 8).  A fragment's k index may stand for any channel as long as both operands agree,
+  // so K's rows go from the ring to the MMA as they lie.  kf: the keys' scales.
+  __device__ __forceinline__ void scores(int e, float (&acc)[C::kNT][4], float2 (&kf)[C::kNT]) {
+    const unsigned char* kt = ring + e * C::kEntry + g * C::kRow;
     const uint4* q = reinterpret_cast<const uint4*>(qf) + lane;
     float low[C::kF32 ? C::kNT : 1][4];
 #pragma unroll
     for (int n = 0; n < C::kNT; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+      for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
     if constexpr (C::kF32) {
 #pragma unroll
       for (int n = 0; n < C::kNT; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) low[n][e] = 0.f;
+        for (int i = 0; i < 4; ++i) low[n][i] = 0.f;
     }
 #pragma unroll
     for (int l = 0; l < C::kLCH; ++l) {
@@ -406,25 +440,21 @@ struct Worker {
 #pragma unroll
         for (int n = 0; n < C::kNT; ++n) {
           const uint32_t w[4] = {kr[n].x, kr[n].y, kr[n].z, kr[n].w};
+          uint32_t b0, b1;
           if constexpr (C::k8) {
-            uint32_t b0, b1;
             codes4_to_f16<T == SA_DTYPE_INT8>(w[s], b0, b1);
-            mma<T>(acc[n], q0, b0, b1);
-            if constexpr (C::kQP == 2)
-              if (!a.act_bf16) mma<T>(acc[n], q1, b0, b1);     // (bf16 has no remainder in f16)
           } else if constexpr (C::kF32) {
-            uint32_t h0, l0, h1, l1;
-            split_tf32(__uint_as_float(w[2 * s]), h0, l0);
-            split_tf32(__uint_as_float(w[2 * s + 1]), h1, l1);
-            mma<T>(acc[n], q0, h0, h1);
+            uint32_t l0, l1;
+            split_tf32(__uint_as_float(w[2 * s]), b0, l0);
+            split_tf32(__uint_as_float(w[2 * s + 1]), b1, l1);
             mma<T>(low[n], q0, l0, l1);
           } else {
-            mma<T>(acc[n], q0, w[2 * s], w[2 * s + 1]);
-            if (!a.act_bf16) {
-              mma<T>(acc[n], q1, w[2 * s], w[2 * s + 1]);
-              if constexpr (C::kQP == 3) mma<T>(acc[n], q2, w[2 * s], w[2 * s + 1]);
-            }
+            b0 = w[2 * s];
+            b1 = w[2 * s + 1];
           }
+          mma<T>(acc[n], q0, b0, b1);
+          if constexpr (C::kQP >= 2) mma<T>(acc[n], q1, b0, b1);
+          if constexpr (C::kQP >= 3) mma<T>(acc[n], q2, b0, b1);
         }
       }
     }
@@ -432,59 +462,82 @@ struct Worker {
 #pragma unroll
       for (int n = 0; n < C::kNT; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[n][e] += low[n][e];
+        for (int i = 0; i < 4; ++i) acc[n][i] += low[n][i];
     }
     if constexpr (C::k8) {
-      const float* ks = sc + 2 * slot * C::kKT;
 #pragma unroll
-      for (int n = 0; n < C::kNT; ++n) {
-        const float2 f = *reinterpret_cast<const float2*>(ks + 8 * n + 2 * c);
-        acc[n][0] *= f.x;
-        acc[n][1] *= f.y;
-        acc[n][2] *= f.x;
-        acc[n][3] *= f.y;
-      }
+      for (int n = 0; n < C::kNT; ++n)
+        kf[n] = *reinterpret_cast<const float2*>(sc + e * C::kKT + 8 * n + 2 * c);
     }
   }
 
-  // The online softmax of a tile: acc becomes p (row g + 8 r, key 8 n + 2 c + e:
-  // acc[n][2 r + e]).  mask: which of the tile's keys there are (others count 0).
-  __device__ __forceinline__ void softmax(int slot, uint32_t mask, float (&acc)[C::kNT][4]) {
-    const float* vs = sc + (2 * slot + 1) * C::kKT;
+  // The online softmax of a tile whose V is in entry e: p (row g + 8 r, key 8 n + 2 c + i:
+  // p[n][2 r + i]) from acc.  mask: which of the tile's keys there are (others count 0).
+  __device__ __forceinline__ void softmax(int e, uint32_t mask, float (&acc)[C::kNT][4],
+                                          const float2 (&kf)[C::kNT], float (&p)[C::kNT][2 * C::kNR]) {
+    const float* vs = sc + e * C::kKT;
     constexpr uint32_t kAll = C::kKT == 32 ? 0xFFFFFFFFu : (1u << (C::kKT & 31)) - 1u;
-    const bool whole = mask == kAll;
-    bool beyond = false;
+    float most = -INFINITY;
+    if constexpr (R == 8) {
 #pragma unroll
-    for (int n = 0; n < C::kNT; ++n) {
-#pragma unroll
-      for (int r = 0; r < C::kNR; ++r)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          // (R = 8: the remainders' row joins its own)
-          float x = (R == 8 ? acc[n][e] + acc[n][e + 2] : acc[n][2 * r + e]) * sfac[r];
-          if (!whole && !((mask >> (8 * n + 2 * c + e)) & 1u)) x = -INFINITY;
-          beyond = beyond || x - m_run[r] > kSlack;           // (m = -inf before the first keys)
-          acc[n][2 * r + e] = x;
-        }
-      if constexpr (C::k8) {
-        const float2 vf = *reinterpret_cast<const float2*>(vs + 8 * n + 2 * c);
-        const float most = fmaxf(fabsf(vf.x), fabsf(vf.y));
-#pragma unroll
-        for (int r = 0; r < C::kNR; ++r) beyond = beyond || most * vfac[r] > kRoom;
+      for (int n = 0; n < C::kNT; ++n) {                     // the remainders' row joins its own
+        acc[n][0] += acc[n][2];
+        acc[n][1] += acc[n][3];
       }
     }
+    auto factor = [&](int n, int i) {
+      const float f = sfac[i >> 1];
+      if constexpr (C::k8) return f * (i & 1 ? kf[n].y : kf[n].x);
+      return f;
+    };
+    auto missing = [&]() {
+      if (mask != kAll) {
+#pragma unroll
+        for (int n = 0; n < C::kNT; ++n)
+#pragma unroll
+          for (int i = 0; i < 2 * C::kNR; ++i)
+            if (!((mask >> (8 * n + 2 * c + (i & 1))) & 1u)) p[n][i] = -INFINITY;
+      }
+    };
+#pragma unroll
+    for (int n = 0; n < C::kNT; ++n)
+#pragma unroll
+      for (int i = 0; i < 2 * C::kNR; ++i)
+        p[n][i] = fmaf(acc[n][i], factor(n, i), -m_run[i >> 1]);   // (m = -inf before the first keys)
+    missing();
+#pragma unroll
+    for (int n = 0; n < C::kNT; ++n)
+#pragma unroll
+      for (int i = 0; i < 2 * C::kNR; ++i) most = fmaxf(most, p[n][i]);
+    bool beyond = most > kSlack;
+    if constexpr (C::k8) {
+      float vm = 0.f, vf = vfac[0];
+#pragma unroll
+      for (int n = 0; n < C::kNT; ++n) {
+        const float2 v = *reinterpret_cast<const float2*>(vs + 8 * n + 2 * c);
+        vm = fmaxf(vm, fmaxf(fabsf(v.x), fabsf(v.y)));
+      }
+#pragma unroll
+      for (int r = 1; r < C::kNR; ++r) vf = fmaxf(vf, vfac[r]);
+      beyond = beyond || vm * vf > kRoom;
+    }
+    clamp = false;
     if (__any_sync(0xffffffffu, beyond)) {
+      clamp = true;
+#pragma unroll
+      for (int n = 0; n < C::kNT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2 * C::kNR; ++i) p[n][i] = acc[n][i] * factor(n, i);
+      missing();
 #pragma unroll
       for (int r = 0; r < C::kNR; ++r) {
         float cm = -INFINITY, top = -INFINITY;               // largest score, largest product
 #pragma unroll
         for (int n = 0; n < C::kNT; ++n) {
-          cm = fmaxf(cm, fmaxf(acc[n][2 * r], acc[n][2 * r + 1]));
+          cm = fmaxf(cm, fmaxf(p[n][2 * r], p[n][2 * r + 1]));
           if constexpr (C::k8) {
-            const float2 vf = *reinterpret_cast<const float2*>(vs + 8 * n + 2 * c);
-            // (a key that is not there: its score is -inf, its scale 0)
-            top = fmaxf(top, fmaxf(acc[n][2 * r] + log2f(fabsf(vf.x)),
-                                   acc[n][2 * r + 1] + log2f(fabsf(vf.y))));
+            const float2 v = *reinterpret_cast<const float2*>(vs + 8 * n + 2 * c);
+            top = fmaxf(top, fmaxf(p[n][2 * r] + log2f(fabsf(v.x)), p[n][2 * r + 1] + log2f(fabsf(v.y))));
           }
         }
         cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, 1));
@@ -505,8 +558,13 @@ struct Worker {
 #pragma unroll
         for (int j = 0; j < C::kNJ; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (R == 8 || e / 2 == r) o[j][e] *= beta;
+          for (int i = 0; i < 4; ++i)
+            if (R == 8 || i / 2 == r) o[j][i] *= beta;
+#pragma unroll
+        for (int n = 0; n < C::kNT; ++n) {
+          p[n][2 * r] -= m_new;
+          p[n][2 * r + 1] -= m_new;
+        }
       }
     }
 #pragma unroll
@@ -515,9 +573,9 @@ struct Worker {
 #pragma unroll
       for (int n = 0; n < C::kNT; ++n)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          acc[n][2 * r + e] = ex2(acc[n][2 * r + e] - m_run[r]);
-          sum += acc[n][2 * r + e];
+        for (int i = 0; i < 2; ++i) {
+          p[n][2 * r + i] = ex2(p[n][2 * r + i]);
+          sum += p[n][2 * r + i];
         }
       l_part[r] += sum;
     }
@@ -525,43 +583,49 @@ struct Worker {
 
   // o += P V.  V's rows too go to the MMA as they lie: n index of n-tile kEP s + i stands
   // for channel 8 kEP s + kEP n + i.
-  __device__ __forceinline__ void values(int slot, const float (&p)[C::kNT][4]) {
-    const unsigned char* vt = ring + (2 * slot + 1) * C::kEntry;
-    const float* vs = sc + (2 * slot + 1) * C::kKT;
+  __device__ __forceinline__ void values(int e, const float (&p)[C::kNT][2 * C::kNR]) {
+    const unsigned char* vt = ring + e * C::kEntry;
+    const float* vs = sc + e * C::kKT;
 #pragma unroll
     for (int kt = 0; kt < C::kKT / C::kKK; ++kt) {
-      uint4 a0, a1, a2;
+      uint4 pa[C::kPP];
       if constexpr (C::kF32) {
-        split_tf32(p[kt][0], a0.x, a0.y);
-        split_tf32(p[kt][1], a0.z, a0.w);
+        split_tf32(p[kt][0], pa[0].x, pa[0].y);
+        split_tf32(p[kt][1], pa[0].z, pa[0].w);
       } else {
-        uint32_t hi[C::kNR][2], mid[C::kNR][2], lo[C::kNR][2];
+        constexpr int kX = C::kKK / 8;
+        uint32_t hi[C::kNR][2] = {}, mid[C::kNR][2] = {}, lo[C::kNR][2] = {};
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int n = 2 * kt + x;
+        for (int x = 0; x < kX; ++x) {
+          const int n = kX * kt + x;
           float2 vf = make_float2(1.f, 1.f);
           if constexpr (C::k8) vf = *reinterpret_cast<const float2*>(vs + 8 * n + 2 * c);
 #pragma unroll
           for (int r = 0; r < C::kNR; ++r) {
             float p0 = p[n][2 * r], p1 = p[n][2 * r + 1];
             if constexpr (C::k8) {
-              // (a number: a page far above the others' scales may pass f32's range where its
-              // keys' P is 0)
-              p0 *= fminf(fmaxf(vf.x * vfac[r], -FLT_MAX), FLT_MAX);
-              p1 *= fminf(fmaxf(vf.y * vfac[r], -FLT_MAX), FLT_MAX);
-              split_f16(p0, p1, hi[r][x], mid[r][x]);
+              float f0 = vf.x * vfac[r], f1 = vf.y * vfac[r];
+              if (clamp) {
+                // (numbers: a page far above the others' scales may pass f32's range where its keys'
+                // P is 0)
+                f0 = fminf(fmaxf(f0, -FLT_MAX), FLT_MAX);
+                f1 = fminf(fmaxf(f1, -FLT_MAX), FLT_MAX);
+              }
+              split_f16(p0 * f0, p1 * f1, hi[r][x], mid[r][x]);
             } else {
               split_bf16(p0, p1, hi[r][x], mid[r][x], lo[r][x]);
             }
           }
         }
+        // bf16 queries over 8 bits with R = 16: one f16 part (2^-12 of P, an eighth of the output's
+        // step); over bf16 two parts (16 bits)
         if constexpr (R == 8) {
-          a0 = make_uint4(hi[0][0], mid[0][0], hi[0][1], mid[0][1]);
-          if constexpr (!C::k8) a1 = make_uint4(lo[0][0], 0u, lo[0][1], 0u);
+          pa[0] = make_uint4(hi[0][0], mid[0][0], hi[0][1], mid[0][1]);
+          if constexpr (C::kPP == 2) pa[1] = make_uint4(lo[0][0], 0u, lo[0][1], 0u);
         } else {
-          a0 = make_uint4(hi[0][0], hi[1][0], hi[0][1], hi[1][1]);
-          a1 = make_uint4(mid[0][0], mid[1][0], mid[0][1], mid[1][1]);
-          if constexpr (!C::k8) a2 = make_uint4(lo[0][0], lo[1][0], lo[0][1], lo[1][1]);
+          pa[0] = make_uint4(hi[0][0], hi[1][0], hi[0][1], hi[1][1]);
+          if constexpr (C::kPP >= 2) pa[1] = make_uint4(mid[0][0], mid[1][0], mid[0][1], mid[1][1]);
+          if constexpr (C::kPP >= 3) pa[2] = make_uint4(lo[0][0], lo[1][0], lo[0][1], lo[1][1]);
         }
       }
 #pragma unroll
@@ -583,21 +647,29 @@ struct Worker {
           }
         };
         uint32_t y0[4], y1[4];
+        read(C::kKK * kt + 2 * c, y0);
+        read(C::kKK * kt + 2 * c + 1, y1);
         if constexpr (C::kF32) {
-          read(8 * kt + 2 * c, y0);
-          read(8 * kt + 2 * c + 1, y1);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint32_t h0, l0, h1, l1;
             split_tf32(__uint_as_float(y0[i]), h0, l0);
             split_tf32(__uint_as_float(y1[i]), h1, l1);
-            mma<T>(o[4 * s + i], a0, h0, h1);
-            mma<T>(o[4 * s + i], a0, l0, l1);
+            mma<T>(o[4 * s + i], pa[0], h0, h1);
+            mma<T>(o[4 * s + i], pa[0], l0, l1);
+          }
+        } else if constexpr (C::kKK == 8) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t b0 = __byte_perm(y0[q], y1[q], 0x5410), b1 = __byte_perm(y0[q], y1[q], 0x7632);
+#pragma unroll
+            for (int x = 0; x < C::kPP; ++x) {
+              mma_k8(o[C::kEP * s + 2 * q], pa[x].x, pa[x].y, b0);
+              mma_k8(o[C::kEP * s + 2 * q + 1], pa[x].x, pa[x].y, b1);
+            }
           }
         } else {
           uint32_t y2[4], y3[4];
-          read(16 * kt + 2 * c, y0);
-          read(16 * kt + 2 * c + 1, y1);
           read(16 * kt + 2 * c + 8, y2);
           read(16 * kt + 2 * c + 9, y3);
 #pragma unroll
@@ -617,19 +689,10 @@ struct Worker {
               b[1][1] = __byte_perm(y2[q], y3[q], 0x7632);
             }
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-              const int j = C::kEP * s + kPer * q + i;
-              mma<T>(o[j], a0, b[i][0], b[i][1]);
-              if constexpr (R == 16 && C::k8) {
-                // bf16 out: one f16 part of P (2^-12 of it, an eighth of the output's step)
-                if (!a.act_bf16) mma<T>(o[j], a1, b[i][0], b[i][1]);
-              } else if constexpr (R == 16) {
-                mma<T>(o[j], a1, b[i][0], b[i][1]);
-                if (!a.act_bf16) mma<T>(o[j], a2, b[i][0], b[i][1]);
-              } else if constexpr (!C::k8) {
-                if (!a.act_bf16) mma<T>(o[j], a1, b[i][0], b[i][1]);
-              }
-            }
+            for (int i = 0; i < kPer; ++i)
+#pragma unroll
+              for (int x = 0; x < C::kPP; ++x)
+                mma<T>(o[C::kEP * s + kPer * q + i], pa[x], b[i][0], b[i][1]);
           }
         }
       }
@@ -682,6 +745,23 @@ struct Worker {
     return l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
   }
 
+  // One element of a merged row: lane ln's, of n-tile and column je = (j, e).
+  static __device__ __forceinline__ void write_element(const DecodeArgs& a, int64_t row, int ln, int je,
+                                                       float sum, float m, float n, float l) {
+    const int j = je >> 1, e = je & 1;
+    const int ch = 8 * C::kEP * (j / C::kEP) + C::kEP * (2 * (ln & 3) + e) + j % C::kEP;
+    const float2 f = out_factors(m, n, l);
+    if (ch < a.head_dim) {
+      const int64_t to = row * a.head_dim + ch;
+      const float y = sum * f.x * f.y;
+      if (a.act_bf16)
+        static_cast<uint16_t*>(a.out)[to] = static_cast<uint16_t>(pack_bf16x2_rn(y, 0.f) & 0xFFFFu);
+      else
+        static_cast<float*>(a.out)[to] = y;
+    }
+    if ((ln & 3) == 0 && je == 0 && a.lse) a.lse[row] = row_lse(m, l);
+  }
+
   // The state for a later merge.
   __device__ __forceinline__ void dump(float* to) const {
 #pragma unroll
@@ -708,14 +788,18 @@ struct PieceInfo {
   int starts, ends;              // the pair's first, last tile is in it
 };
 
-template <int T, int DP, int R>
-__global__ void __launch_bounds__(Cfg<T, DP, R>::kThreads, 1)
+template <int T, int DP, int R, bool B>
+__global__ void __launch_bounds__(Cfg<T, DP, R, B>::kThreads, 1)
 decode_split_kernel(const __grid_constant__ DecodeArgs a) {
-  using C = Cfg<T, DP, R>;
+  using C = Cfg<T, DP, R, B>;
+  using W = Worker<T, DP, R, B>;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int64_t s_scan[C::kThreads];
   __shared__ int64_t s_warp[C::kW];
   __shared__ PieceInfo s_piece[2 * C::kW];     // of warp w: [2 w] the one it began with, [2 w + 1] its last
+  __shared__ float s_weight[2 * C::kW][R];     // of a group's pieces
+  __shared__ float s_m[R], s_n[R], s_l[R];
+  __shared__ int s_list[2 * C::kW];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   griddep_launch_dependents();
 
@@ -782,12 +866,12 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
   }
 
   // ---- the warp's tiles
-  Worker<T, DP, R> w{a};
+  W w{a};
   unsigned char* own = smem + warp * C::kPerWarp;
   w.ring = own;
-  w.qf = own + 2 * C::kST * C::kEntry;
+  w.qf = own + C::kNE * C::kEntry;
   w.info = reinterpret_cast<uint4*>(w.qf + C::kQBytes);
-  w.sc = reinterpret_cast<float*>(w.qf + C::kQBytes + C::kST * 16);
+  w.sc = reinterpret_cast<float*>(w.qf + C::kQBytes + kInfos * 16);
   w.lane = lane;
   w.g = lane >> 2;
   w.c = lane & 3;
@@ -795,64 +879,82 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
   if (lane < 2) s_piece[2 * warp + lane] = {-1, 0, 0};
   __syncwarp();
   if (n > 0) {
-    using Pend = typename Worker<T, DP, R>::Pend;
     w.seek(b0, in_seq);
-    Pend pend[C::kST], ahead{};
-    int64_t off = -1, so = 0;
-    // K of a tile: what the consumer needs to know of it beside
-    auto issue_k = [&](Pend& p, int slot) {
-      if (p.pid >= a.num_pages) {
-        report(a.status, SA_ERR_SHAPE);
-        p.pid = -1;
+    const int h0 = w.h;
+    typename W::Pend ahead = w.take();           // of the tile whose K is next to be copied
+    uint32_t row = W::kNone, scale_at = 0;       // of the tile whose V is
+    int next_k = 0, next_v = 0, ne = 0;          // tiles asked for so far; the entry for the next copies
+    auto end_group = [&]() {                     // (also where nothing was left to copy)
+      copies_commit();
+      if (++ne == C::kNE) ne = 0;
+    };
+    // K of a tile, and what its consumer has to know of it; then its V.
+    auto issue_k = [&]() {
+      if (next_k < n) {
+        if (ahead.pid >= a.num_pages) {
+          report(a.status, SA_ERR_SHAPE);
+          ahead.pid = -1;
+        }
+        scale_at = static_cast<uint32_t>(ahead.pid) * static_cast<uint32_t>(a.hkv) + ahead.h;
+        row = ahead.pid >= 0 ? scale_at * static_cast<uint32_t>(a.page_size) + ahead.row : W::kNone;
+        const unsigned mask =
+            __ballot_sync(0xffffffffu, (C::kKT == 32 || lane < C::kKT) && row != W::kNone);
+        if (lane == 0)
+          w.info[next_k % kInfos] = make_uint4(static_cast<uint32_t>(ahead.item), mask, ahead.flags, 0u);
+        w.template copy_rows<false>(ne, row, scale_at);
       }
-      so = static_cast<int64_t>(p.pid) * a.hkv + p.h;
-      off = p.pid >= 0 ? (so * a.page_size + p.row) * a.row_bytes : -1;
-      const unsigned mask = __ballot_sync(0xffffffffu, (C::kKT == 32 || lane < C::kKT) && off >= 0);
-      if (lane == 0) w.info[slot] = make_uint4(static_cast<uint32_t>(p.item), mask, p.flags, 0u);
-      w.template copy_rows<false>(slot, off, so);
+      ++next_k;
+      end_group();
+    };
+    auto issue_v = [&]() {
+      if (next_v < n) {
+        w.template copy_rows<true>(ne, row, scale_at);
+        if (next_k < n) ahead = w.take();
+      }
+      ++next_v;
+      end_group();
     };
 #pragma unroll
-    for (int i = 0; i < C::kST; ++i)
-      if (i < n) pend[i] = w.take();
-    if (C::kST < n) ahead = w.take();
-#pragma unroll
-    for (int i = 0; i < C::kST; ++i) {
-      if (i < n) issue_k(pend[i], i);
-      copies_commit();
-      if (i < n) w.template copy_rows<true>(i, off, so);
-      copies_commit();
-    }
-    int item = -1;
+    for (int i = 0; i < C::kNE; ++i)
+      if (i & 1)
+        issue_v();
+      else
+        issue_k();
+    // (Q of the first piece beside the first copies)
+    int item = b0 * a.items_per_seq + h0;
+    w.begin();
+    w.load_q(item);
     uint32_t flags = 0;
     bool started = false;          // the piece at hand holds its pair's first tile
-    int slot = 0;
+    int e = 0;
     for (int i = 0; i < n; ++i) {
-      copies_wait<2 * C::kST - 1>();
+      copies_wait<C::kNE - 1>();
       __syncwarp();
-      const uint4 inf = w.info[slot];
+      const uint4 inf = w.info[i % kInfos];
       flags = inf.z;
-      if (i == 0 || (flags & 1u)) {
-        item = static_cast<int>(inf.x);
-        started = (flags & 1u) != 0;
-        w.begin();
-        w.load_q(item);
+      if (flags & 1u) {
+        started = true;
+        if (i > 0) {
+          item = static_cast<int>(inf.x);
+          w.begin();
+          w.load_q(item);
+        }
       }
-      float acc[C::kNT][4];
-      if (inf.y) w.scores(slot, acc);
+      float acc[C::kNT][4], p[C::kNT][2 * C::kNR];
+      float2 kf[C::kNT];
+      if (inf.y) w.scores(e, acc, kf);
       __syncwarp();
-      const bool more = i + C::kST < n;
-      if (more) issue_k(ahead, slot);
-      copies_commit();
-      copies_wait<2 * C::kST - 1>();
+      if constexpr (C::kNE & 1) issue_v(); else issue_k();
+      if (++e == C::kNE) e = 0;
+      copies_wait<C::kNE - 1>();
       __syncwarp();
       if (inf.y) {
-        w.softmax(slot, inf.y, acc);
-        w.values(slot, acc);
+        w.softmax(e, inf.y, acc, kf, p);
+        w.values(e, p);
       }
       __syncwarp();
-      if (more) w.template copy_rows<true>(slot, off, so);
-      copies_commit();
-      if (i + C::kST + 1 < n) ahead = w.take();
+      if constexpr (C::kNE & 1) issue_k(); else issue_v();
+      if (++e == C::kNE) e = 0;
       if (flags & 2u) {
         if (started) {
           w.write_out(item);
@@ -861,7 +963,6 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
           if (lane == 0) s_piece[2 * warp] = {item, 0, 1};
         }
       }
-      if (++slot == C::kST) slot = 0;
     }
     copies_wait<0>();
     __syncwarp();
@@ -872,73 +973,75 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
   }
   __syncthreads();
 
-  // ---- pieces of pairs that this CTA's warps cut, in the order of the keys
+  // ---- pieces of pairs that this CTA's warps cut, in the order of the keys: groups of
+  // one pair, merged row by row (a lane per piece), then element by element
+  static_assert(2 * C::kW <= 32, "a lane per piece");
+  auto state = [&](int x) -> const float* {
+    return x & 1 ? reinterpret_cast<const float*>(smem + (x >> 1) * C::kPerWarp)
+                 : a.firsts + (static_cast<int64_t>(cta) * C::kW + (x >> 1)) * C::kState;
+  };
+  PieceInfo my{-1, 0, 0};
+  if (lane < 2 * C::kW) my = s_piece[lane];
+  unsigned left = __ballot_sync(0xffffffffu, my.item >= 0);
   bool joined = false;             // the CTA's first piece goes on from the CTA before
   int first_item = -1, first_ends = 0;
-  for (int p = 0; p < 2 * C::kW;) {
-    const PieceInfo head = s_piece[p];
-    if (head.item < 0) {
-      ++p;
-      continue;
-    }
-    int q = p, ends = head.ends;
-    while (q + 1 < 2 * C::kW && (s_piece[q + 1].item < 0 || s_piece[q + 1].item == head.item)) {
-      ++q;
-      if (s_piece[q].item >= 0) ends = s_piece[q].ends;
-    }
-    auto state = [&](int x) -> const float* {
-      return x & 1 ? reinterpret_cast<const float*>(smem + (x >> 1) * C::kPerWarp)
-                   : a.firsts + (static_cast<int64_t>(cta) * C::kW + (x >> 1)) * C::kState;
-    };
-    const bool all = head.starts && ends;
-    if (!head.starts) {
+  while (left) {
+    const int p = __ffs(left) - 1, item = __shfl_sync(0xffffffffu, my.item, p);
+    const unsigned group = __ballot_sync(0xffffffffu, my.item == item);
+    const int starts = __shfl_sync(0xffffffffu, my.starts, p);
+    const int ends = __shfl_sync(0xffffffffu, my.ends, 31 - __clz(group));
+    left &= ~group;
+    if (!starts) {
       joined = true;
-      first_item = head.item;
+      first_item = item;
       first_ends = ends;
     }
-    float* to = a.parts + (static_cast<int64_t>(cta) * 2 + (head.starts ? 1 : 0)) * C::kState;
-    const Item it = item_of<R>(a, head.item);
+    const bool in = (group >> lane) & 1u;
+    const int place = __popc(group & ((1u << lane) - 1u));
+    if (warp == 0 && in) s_list[place] = lane;
+    for (int row = warp; row < R; row += C::kW) {
+      const float* s = state(lane) + C::kNel + row;
+      const float m = in ? s[0] : -INFINITY, n = in ? s[R] : -INFINITY;
+      float mm = m, nn = n;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+        nn = fmaxf(nn, __shfl_xor_sync(0xffffffffu, nn, o));
+      }
+      float l = in ? pow2_of(m - mm) * s[2 * R] : 0.f;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      if (in) s_weight[place][row] = pow2_of(n - nn);
+      if (lane == 0) {
+        s_m[row] = mm;
+        s_n[row] = nn;
+        s_l[row] = l;
+      }
+    }
+    __syncthreads();
+    const int pieces = __popc(group);
+    const bool all = starts && ends;
+    float* to = a.parts + (static_cast<int64_t>(cta) * 2 + (starts ? 1 : 0)) * C::kState;
+    const Item it = item_of<R>(a, item);
     for (int idx = tid; idx < C::kNel; idx += C::kThreads) {
       const int ln = idx & 31, rest = idx >> 5;
       const int r = rest % C::kNR, je = rest / C::kNR;
       const int row = (ln >> 2) + 8 * r;
-      float m = -INFINITY, nn = -INFINITY;
-      for (int x = p; x <= q; ++x)
-        if (s_piece[x].item >= 0) {
-          m = fmaxf(m, state(x)[C::kNel + row]);
-          nn = fmaxf(nn, state(x)[C::kNel + R + row]);
-        }
-      float sum = 0.f, l = 0.f;
-      for (int x = p; x <= q; ++x)
-        if (s_piece[x].item >= 0) {
-          const float* s = state(x);
-          sum = fmaf(pow2_of(s[C::kNel + R + row] - nn), s[idx], sum);
-          l = fmaf(pow2_of(s[C::kNel + row] - m), s[C::kNel + 2 * R + row], l);
-        }
+      float sum = 0.f;
+#pragma unroll 4
+      for (int x = 0; x < pieces; ++x) sum = fmaf(s_weight[x][row], state(s_list[x])[idx], sum);
       if (!all) {
         to[idx] = sum;
         if ((ln & 3) == 0 && je == 0) {
-          to[C::kNel + row] = m;
-          to[C::kNel + R + row] = nn;
-          to[C::kNel + 2 * R + row] = l;
+          to[C::kNel + row] = s_m[row];
+          to[C::kNel + R + row] = s_n[row];
+          to[C::kNel + 2 * R + row] = s_l[row];
         }
       } else if (row < it.rows) {
-        const int j = je >> 1, e = je & 1;
-        const int ch = 8 * C::kEP * (j / C::kEP) + C::kEP * (2 * (ln & 3) + e) + j % C::kEP;
-        const float2 f = Worker<T, DP, R>::out_factors(m, nn, l);
-        if (ch < a.head_dim) {
-          const int64_t at = (it.row0 + row) * a.head_dim + ch;
-          if (a.act_bf16)
-            static_cast<uint16_t*>(a.out)[at] =
-                static_cast<uint16_t>(pack_bf16x2_rn(sum * f.x * f.y, 0.f) & 0xFFFFu);
-          else
-            static_cast<float*>(a.out)[at] = sum * f.x * f.y;
-        }
-        if ((ln & 3) == 0 && je == 0 && a.lse)
-          a.lse[it.row0 + row] = Worker<T, DP, R>::row_lse(m, l);
+        W::write_element(a, it.row0 + row, ln, je, sum, s_m[row], s_n[row], s_l[row]);
       }
     }
-    p = q + 1;
+    __syncthreads();               // (the lists and weights are the next group's)
   }
   if (tid == 0) a.joins[cta] = make_int2(joined ? first_item : -1, first_ends);
 }
@@ -946,9 +1049,10 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
 // Pairs whose parts lie in several CTAs.  CTA x of `joins` says which pair its first piece
 // continues (-1: none) and whether it ends it; block x merges the pair that CTA x - 1
 // began (its second part) and x, x + 1, .. continue (their first).
-template <int T, int DP, int R>
+template <int T, int DP, int R, bool B>
 __global__ void __launch_bounds__(256) decode_join_kernel(const __grid_constant__ DecodeArgs a) {
-  using C = Cfg<T, DP, R>;
+  using C = Cfg<T, DP, R, B>;
+  using W = Worker<T, DP, R, B>;
   __shared__ int2 s_join[kDecodeCtas];
   __shared__ float s_wo[R][kDecodeCtas + 1];
   __shared__ float s_m[R], s_n[R], s_l[R];
@@ -1000,30 +1104,18 @@ __global__ void __launch_bounds__(256) decode_join_kernel(const __grid_constant_
   float sum = 0.f;
 #pragma unroll 8
   for (int p = 0; p < pieces; ++p) sum = fmaf(s_wo[row][p], __ldcg(state(p) + idx), sum);
-  const int j = je >> 1, e = je & 1;
-  const int ch = 8 * C::kEP * (j / C::kEP) + C::kEP * (2 * (ln & 3) + e) + j % C::kEP;
-  const float2 f = Worker<T, DP, R>::out_factors(s_m[row], s_n[row], s_l[row]);
-  if (ch < a.head_dim) {
-    const int64_t at = (it.row0 + row) * a.head_dim + ch;
-    if (a.act_bf16)
-      static_cast<uint16_t*>(a.out)[at] =
-          static_cast<uint16_t>(pack_bf16x2_rn(sum * f.x * f.y, 0.f) & 0xFFFFu);
-    else
-      static_cast<float*>(a.out)[at] = sum * f.x * f.y;
-  }
-  if ((ln & 3) == 0 && je == 0 && a.lse)
-    a.lse[it.row0 + row] = Worker<T, DP, R>::row_lse(s_m[row], s_l[row]);
+  W::write_element(a, it.row0 + row, ln, je, sum, s_m[row], s_n[row], s_l[row]);
 }
 
-template <int T, int DP, int R>
+template <int T, int DP, int R, bool B>
 cudaError_t launch(const DecodeArgs& a, cudaStream_t stream) {
-  using C = Cfg<T, DP, R>;
-  const void* fn = reinterpret_cast<const void*>(decode_split_kernel<T, DP, R>);
+  using C = Cfg<T, DP, R, B>;
+  const void* fn = reinterpret_cast<const void*>(decode_split_kernel<T, DP, R, B>);
   static SmemLimit limit;
   cudaError_t err = limit.raise(fn, C::kSmem);
   if (err != cudaSuccess) return err;
   const int ctas = device_sm_count() < kDecodeCtas ? device_sm_count() : kDecodeCtas;
-  decode_split_kernel<T, DP, R><<<ctas, C::kThreads, C::kSmem, stream>>>(a);
+  decode_split_kernel<T, DP, R, B><<<ctas, C::kThreads, C::kSmem, stream>>>(a);
   err = cudaGetLastError();
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg{};
@@ -1035,18 +1127,26 @@ cudaError_t launch(const DecodeArgs& a, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_join_kernel<T, DP, R>, a);
+  return cudaLaunchKernelEx(&cfg, decode_join_kernel<T, DP, R, B>, a);
+}
+
+template <int T, int DP>
+cudaError_t launch_dim(const DecodeArgs& a, int r, cudaStream_t s) {
+  if constexpr (T == SA_DTYPE_F32) {
+    return launch<T, DP, 8, false>(a, s);
+  } else if constexpr (T == SA_DTYPE_BF16) {
+    if (r == 8) return a.act_bf16 ? launch<T, DP, 8, true>(a, s) : launch<T, DP, 8, false>(a, s);
+  } else {
+    if (r == 8) return launch<T, DP, 8, false>(a, s);
+  }
+  if constexpr (T != SA_DTYPE_F32)
+    return a.act_bf16 ? launch<T, DP, 16, true>(a, s) : launch<T, DP, 16, false>(a, s);
 }
 
 template <int T>
 cudaError_t launch_type(const DecodeArgs& a, int dp, int r, cudaStream_t s) {
-  if constexpr (T != SA_DTYPE_F32) {
-    if (r == 16)
-      return dp == 64 ? launch<T, 64, 16>(a, s) : dp == 128 ? launch<T, 128, 16>(a, s)
-                                                            : launch<T, 256, 16>(a, s);
-  }
-  return dp == 64 ? launch<T, 64, 8>(a, s) : dp == 128 ? launch<T, 128, 8>(a, s)
-                                                       : launch<T, 256, 8>(a, s);
+  return dp == 64 ? launch_dim<T, 64>(a, r, s) : dp == 128 ? launch_dim<T, 128>(a, r, s)
+                                                           : launch_dim<T, 256>(a, r, s);
 }
 
 }  // namespace dec1

@@ -233,7 +233,10 @@ cudaError_t launch_fused_dec_q8(const FusedQ8Args& a, cudaStream_t stream);
 
 // Attention of one new token per sequence over its whole cache (decode_split.cuh).
 constexpr int kDecodeCtas = 160;      // CTAs of a launch at most (one per SM)
-constexpr int kDecodeMaxWarps = 8;    // warps of a CTA at most
+// Warps of a CTA at most: 16, 12 or 8, as their registers (128, 168 or 255 a thread) allow.
+constexpr int decode_max_warps(int dp, int r) {
+  return dp == 256 ? 8 : r == 16 ? (dp == 64 ? 12 : 8) : (dp == 64 ? 16 : 12);
+}
 // f32 numbers of a warp's state: o, and m, n and l of each query row (dp: head_dim
 // rounded up to 64, 128 or 256; r: query rows of a tile).
 constexpr int decode_state_floats(int dp, int r) { return r * dp + 3 * r; }
