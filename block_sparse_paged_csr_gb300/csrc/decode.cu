@@ -61,8 +61,9 @@ sa_status sa_decode_attention(const void* q, sa_dtype q_dtype, const void* k_pag
   if (kv_dtype < SA_DTYPE_F32 || kv_dtype > SA_DTYPE_INT8) return SA_ERR_INVALID_ARGUMENT;
   if (head_dim % (sa::eight_bit(kv_dtype) ? 16 : 8) != 0 || head_dim > 256)
     return SA_ERR_UNSUPPORTED;
-  // (row numbers of the pools are 32-bit)
+  // (row numbers of the pools are 32-bit, as are the tiles of 32 sequences)
   if (static_cast<int64_t>(batch) * hq > 0x7FFFFFFF ||
+      static_cast<int64_t>(max_pages) * page_size > (int64_t{1} << 29) ||
       (num_pages > 0 && num_pages > int64_t{0xFFFFFFFE} / page_size / hkv))
     return SA_ERR_UNSUPPORTED;
   if (batch == 0) return SA_OK;
@@ -103,8 +104,7 @@ sa_status sa_decode_attention(const void* q, sa_dtype q_dtype, const void* k_pag
   a.page_size = page_size;
   a.page_shift = (page_size & (page_size - 1)) == 0 ? __builtin_ctz(page_size) : -1;
   a.max_pages = max_pages;
-  a.capacity = static_cast<int32_t>(
-      std::min<int64_t>(static_cast<int64_t>(max_pages) * page_size, 0x7FFFFF00));
+  a.capacity = max_pages * page_size;
   a.window = window;
   a.act_bf16 = q_dtype == SA_DTYPE_BF16;
   a.scale = softmax_scale;

@@ -184,22 +184,14 @@ struct Keys {
 };
 __device__ __forceinline__ Keys keys_of(const DecodeArgs& a, int used) {
   Keys k;
-  k.end = min(max(used, 0), a.capacity);
-  k.first = a.window > 0 ? max(used - a.window, 0) : 0;      // (used < 0: end = 0 takes all)
+  used = max(used, 0);
+  k.end = min(used, a.capacity);
+  k.first = a.window > 0 ? max(used - a.window, 0) : 0;
   return k;
 }
 template <int KT>
 __device__ __forceinline__ int tiles_of(const Keys& k) {
   return max((k.end - k.first + KT - 1) / KT, 1);             // a sequence without keys has one, of none
-}
-
-// Four channels of query row `row` (zeros behind head_dim).
-__device__ __forceinline__ float4 load_q4(const DecodeArgs& a, int64_t row, int ch, bool there) {
-  if (!there || ch >= a.head_dim) return make_float4(0.f, 0.f, 0.f, 0.f);
-  if (a.act_bf16)
-    return bf16x4_to_f32(*reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) +
-                                                         row * a.head_dim + ch));
-  return *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + row * a.head_dim + ch);
 }
 
 // An item: (sequence b, kv head h, lane group).  Its first query row and their number.
@@ -314,75 +306,103 @@ struct Worker {
   //   8 bits: the row, scaled by a power of two into f16's range, as f16 high
   //     parts and remainders; bf16: three bf16 parts (bf16 queries: the first says all);
   //     f32: tf32 parts.
-  //   R = 8: rows g + 8 of the MMA's tile carry the second parts of rows g, so that they cost no product.
-  __device__ __forceinline__ void load_q(int item) {
+  //   R = 8: rows g + 8 of the MMA's tile carry the second parts of rows g, so that they
+  //     cost no product.
+  // fetch_q asks for the rows, keep_q lays them out: between them other loads start.
+  static constexpr int kQ4 = C::kLCH * C::kEC / 4;  // groups of 4 channels of a row that a lane holds
+  struct Rows {
+    uint4 x[C::kNR][kQ4];                           // f32, or bf16 in the first two words
+  };
+  __device__ __forceinline__ int q_channel(int i) const {
+    return chunk(i / (C::kEC / 4)) * C::kEC + 4 * (i % (C::kEC / 4));
+  }
+  __device__ __forceinline__ void fetch_q(int item, Rows& q) const {
     const Item it = item_of<R>(a, item);
-    uint4* out = reinterpret_cast<uint4*>(qf) + lane;
 #pragma unroll
-    for (int r = 0; r < C::kNR; ++r) sfac[r] = a.scale * kLog2e;
-    float f[C::kNR];
-    if constexpr (C::k8) {
+    for (int r = 0; r < C::kNR; ++r) {
+      const bool there = g + 8 * r < it.rows;
+      const int64_t at = (it.row0 + g + 8 * r) * a.head_dim;
 #pragma unroll
-      for (int r = 0; r < C::kNR; ++r) {
-        const int row = g + 8 * r;
+      for (int i = 0; i < kQ4; ++i) {
+        q.x[r][i] = make_uint4(0u, 0u, 0u, 0u);
+        if (there && q_channel(i) < a.head_dim) {
+          if (a.act_bf16) {
+            const uint2 u =
+                *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) + at + q_channel(i));
+            q.x[r][i].x = u.x;
+            q.x[r][i].y = u.y;
+          } else {
+            q.x[r][i] =
+                *reinterpret_cast<const uint4*>(static_cast<const float*>(a.q) + at + q_channel(i));
+          }
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void keep_q(const Rows& q) {
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < C::kNR; ++r) {
+      float4 x[kQ4];
+#pragma unroll
+      for (int i = 0; i < kQ4; ++i)
+        x[i] = a.act_bf16 ? bf16x4_to_f32(make_uint2(q.x[r][i].x, q.x[r][i].y))
+                          : make_float4(__uint_as_float(q.x[r][i].x), __uint_as_float(q.x[r][i].y),
+                                        __uint_as_float(q.x[r][i].z), __uint_as_float(q.x[r][i].w));
+      float f = 1.f;
+      sfac[r] = a.scale * kLog2e;
+      if constexpr (C::k8) {
         float am = 0.f;
 #pragma unroll
-        for (int l = 0; l < C::kLCH; ++l)
-#pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            const float4 x = load_q4(a, it.row0 + row, chunk(l) * 16 + 4 * s, row < it.rows);
-            am = fmaxf(am, fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))));
-          }
+        for (int i = 0; i < kQ4; ++i)
+          am = fmaxf(am, fmaxf(fmaxf(fabsf(x[i].x), fabsf(x[i].y)), fmaxf(fabsf(x[i].z), fabsf(x[i].w))));
         am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
         am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
         // largest magnitude to [2^10, 2^11): f and 1 / f kept normal
         const int ex = min(max(static_cast<int>(__float_as_uint(am) >> 23), 11), 253);
-        f[r] = __uint_as_float(static_cast<uint32_t>(264 - ex) << 23);
+        f = __uint_as_float(static_cast<uint32_t>(264 - ex) << 23);
         sfac[r] *= __uint_as_float(static_cast<uint32_t>(ex - 10) << 23);
       }
-    }
-    __syncwarp();
+      uint4* out = reinterpret_cast<uint4*>(qf) + lane;
 #pragma unroll
-    for (int l = 0; l < C::kLCH; ++l)
-#pragma unroll
-      for (int s = 0; s < C::kEC / 4; ++s) {
-        const int ch = chunk(l) * C::kEC + 4 * s;
-        float4 x[C::kNR];
-#pragma unroll
-        for (int r = 0; r < C::kNR; ++r)
-          x[r] = load_q4(a, it.row0 + g + 8 * r, ch, g + 8 * r < it.rows);
+      for (int i = 0; i < kQ4; ++i) {
         if constexpr (C::kF32) {
           uint4 u, v;
-          split_tf32(x[0].x, u.x, u.y);
-          split_tf32(x[0].y, u.z, u.w);
-          split_tf32(x[0].z, v.x, v.y);
-          split_tf32(x[0].w, v.z, v.w);
-          out[32 * (2 * l)] = u;
-          out[32 * (2 * l + 1)] = v;
+          split_tf32(x[i].x, u.x, u.y);
+          split_tf32(x[i].y, u.z, u.w);
+          split_tf32(x[i].z, v.x, v.y);
+          split_tf32(x[i].w, v.z, v.w);
+          out[32 * 2 * i] = u;
+          out[32 * (2 * i + 1)] = v;
         } else {
-          uint4* at = out + 32 * C::kQP * (l * C::kKPC + s);
-          uint32_t hi[C::kNR][2], mid[C::kNR][2], lo[C::kNR][2];
-#pragma unroll
-          for (int r = 0; r < C::kNR; ++r) {
-            if constexpr (C::k8) {
-              split_f16(x[r].x * f[r], x[r].y * f[r], hi[r][0], mid[r][0]);
-              split_f16(x[r].z * f[r], x[r].w * f[r], hi[r][1], mid[r][1]);
-              lo[r][0] = lo[r][1] = 0u;
-            } else {
-              split_bf16(x[r].x, x[r].y, hi[r][0], mid[r][0], lo[r][0]);
-              split_bf16(x[r].z, x[r].w, hi[r][1], mid[r][1], lo[r][1]);
-            }
+          uint4* to = out + 32 * C::kQP * i;
+          uint32_t hi[2], mid[2], lo[2] = {0u, 0u};
+          if constexpr (C::k8) {
+            split_f16(x[i].x * f, x[i].y * f, hi[0], mid[0]);
+            split_f16(x[i].z * f, x[i].w * f, hi[1], mid[1]);
+          } else {
+            split_bf16(x[i].x, x[i].y, hi[0], mid[0], lo[0]);
+            split_bf16(x[i].z, x[i].w, hi[1], mid[1], lo[1]);
           }
           if constexpr (R == 8) {
-            at[0] = make_uint4(hi[0][0], mid[0][0], hi[0][1], mid[0][1]);
-            if constexpr (C::kQP == 2) at[32] = make_uint4(lo[0][0], 0u, lo[0][1], 0u);
+            to[0] = make_uint4(hi[0], mid[0], hi[1], mid[1]);
+            if constexpr (C::kQP == 2) to[32] = make_uint4(lo[0], 0u, lo[1], 0u);
           } else {
-            at[0] = make_uint4(hi[0][0], hi[1][0], hi[0][1], hi[1][1]);
-            if constexpr (C::kQP >= 2) at[32] = make_uint4(mid[0][0], mid[1][0], mid[0][1], mid[1][1]);
-            if constexpr (C::kQP == 3) at[64] = make_uint4(lo[0][0], lo[1][0], lo[0][1], lo[1][1]);
+            uint32_t* w = reinterpret_cast<uint32_t*>(to) + r;
+            w[0] = hi[0];
+            w[2] = hi[1];
+            if constexpr (C::kQP >= 2) {
+              w[128] = mid[0];
+              w[130] = mid[1];
+            }
+            if constexpr (C::kQP >= 3) {
+              w[256] = lo[0];
+              w[258] = lo[1];
+            }
           }
         }
       }
+    }
     __syncwarp();
   }
 
@@ -794,29 +814,35 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
   using C = Cfg<T, DP, R, B>;
   using W = Worker<T, DP, R, B>;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ int64_t s_scan[C::kThreads];
-  __shared__ int64_t s_warp[C::kW];
+  constexpr int kChunks = 64;
+  __shared__ int64_t s_chunk[kChunks];         // tiles (of one item) of pieces of the batch
   __shared__ PieceInfo s_piece[2 * C::kW];     // of warp w: [2 w] the one it began with, [2 w + 1] its last
-  __shared__ float s_weight[2 * C::kW][R];     // of a group's pieces
-  __shared__ float s_m[R], s_n[R], s_l[R];
-  __shared__ int s_list[2 * C::kW];
+  __shared__ float s_weight[2 * C::kW][R];     // of a piece's o in its group
+  __shared__ float s_stat[2 * C::kW][3][R];    // m, n, l of a group
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   griddep_launch_dependents();
 
   // ---- the plan: tiles of all sequences, this warp's range and where it begins
-  int64_t mine = 0;
-  for (int b = tid; b < a.batch; b += C::kThreads) mine += tiles_of<C::kKT>(keys_of(a, a.used[b]));
-#pragma unroll
-  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) s_warp[warp] = mine;
+  const int per_chunk = (a.batch + 32 * kChunks - 1) / (32 * kChunks) * 32;    // sequences
+  const int chunks = (a.batch + per_chunk - 1) / per_chunk;
+  auto tiles_at = [&](int b, int most) -> unsigned {
+    return b < most ? static_cast<unsigned>(tiles_of<C::kKT>(keys_of(a, a.used[b]))) : 0u;
+  };
+#pragma unroll 1
+  for (int k = warp; k < chunks; k += C::kW) {
+    int64_t sum = 0;
+#pragma unroll 1
+    for (int i = lane; i < per_chunk; i += 32)
+      sum += __reduce_add_sync(0xffffffffu, tiles_at(k * per_chunk + i, a.batch));
+    if (lane == 0) s_chunk[k] = sum;
+  }
   __syncthreads();
   int64_t total = 0;
-#pragma unroll
-  for (int w = 0; w < C::kW; ++w) total += s_warp[w];
+#pragma unroll 1
+  for (int k = 0; k < chunks; ++k) total += s_chunk[k];
   total *= a.items_per_seq;
-  // CTAs that take part: as many as have kMinTiles tiles for each of their warps
-  constexpr int kMinTiles = 1;
-  const int64_t want = (total + C::kW * kMinTiles - 1) / (C::kW * kMinTiles);
+  // CTAs that take part: as many as have a tile for each of their warps
+  const int64_t want = (total + C::kW - 1) / C::kW;
   const int ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), want));
   const int cta = static_cast<int>(blockIdx.x);
   if (cta >= ctas) {
@@ -826,42 +852,31 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
   const int64_t workers = static_cast<int64_t>(ctas) * C::kW;
   const int64_t me = static_cast<int64_t>(cta) * C::kW + warp;
   const int64_t t0 = total * me / workers, t1 = total * (me + 1) / workers;
-  int b0 = -1;
-  int64_t in_seq = 0;
-  {
-    int64_t before = 0;                        // tiles of the sequences before `base`, of one item
-    for (int base = 0; base < a.batch; base += C::kThreads) {
-      const int b = base + tid;
-      const int64_t n = b < a.batch ? tiles_of<C::kKT>(keys_of(a, a.used[b])) : 0;
-      int64_t x = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      __syncthreads();                         // (the last round's readers)
-      if (lane == 31) s_warp[warp] = x;
-      __syncthreads();
-      int64_t seg = 0;
-#pragma unroll
-      for (int w = 0; w < C::kW; ++w) {
-        if (w < warp) x += s_warp[w];
-        seg += s_warp[w];
-      }
-      s_scan[tid] = x;
-      __syncthreads();
-      if (b0 < 0 && t0 < (before + seg) * a.items_per_seq) {
-        for (int i = 0; i < C::kThreads && b0 < 0; i += 32) {
-          const bool past = (before + s_scan[i + lane]) * a.items_per_seq > t0;
-          const unsigned bal = __ballot_sync(0xffffffffu, past);
-          if (bal) {
-            const int at = i + __ffs(bal) - 1;
-            b0 = base + at;
-            in_seq = t0 - (before + (at ? s_scan[at - 1] : 0)) * a.items_per_seq;
-          }
+  int b0 = 0;
+  int64_t in_seq = t0;                         // tiles of the sequence before t0
+  if (t0 < t1) {
+    int k = 0;
+#pragma unroll 1
+    for (; in_seq >= s_chunk[k] * a.items_per_seq; ++k) in_seq -= s_chunk[k] * a.items_per_seq;
+#pragma unroll 1
+    for (int i = k * per_chunk;; i += 32) {
+      const unsigned n = tiles_at(i + lane, a.batch);
+      const int64_t all = static_cast<int64_t>(__reduce_add_sync(0xffffffffu, n)) * a.items_per_seq;
+      if (in_seq < all) {
+        unsigned x = n;                        // tiles of the 32 sequences up to the lane's
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) {
+          const unsigned y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
         }
+        const unsigned past =
+            __ballot_sync(0xffffffffu, static_cast<int64_t>(x) * a.items_per_seq > in_seq);
+        const int at = __ffs(past) - 1;
+        b0 = i + at;
+        in_seq -= static_cast<int64_t>(__shfl_sync(0xffffffffu, x - n, at)) * a.items_per_seq;
+        break;
       }
-      before += seg;
+      in_seq -= all;
     }
   }
 
@@ -880,7 +895,9 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
   __syncwarp();
   if (n > 0) {
     w.seek(b0, in_seq);
-    const int h0 = w.h;
+    int item = b0 * a.items_per_seq + w.h;
+    typename W::Rows q;
+    w.fetch_q(item, q);
     typename W::Pend ahead = w.take();           // of the tile whose K is next to be copied
     uint32_t row = W::kNone, scale_at = 0;       // of the tile whose V is
     int next_k = 0, next_v = 0, ne = 0;          // tiles asked for so far; the entry for the next copies
@@ -920,10 +937,9 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
         issue_v();
       else
         issue_k();
-    // (Q of the first piece beside the first copies)
-    int item = b0 * a.items_per_seq + h0;
+    // (Q of the first piece came beside the first copies)
+    w.keep_q(q);
     w.begin();
-    w.load_q(item);
     uint32_t flags = 0;
     bool started = false;          // the piece at hand holds its pair's first tile
     int e = 0;
@@ -936,8 +952,9 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
         started = true;
         if (i > 0) {
           item = static_cast<int>(inf.x);
+          w.fetch_q(item, q);
+          w.keep_q(q);
           w.begin();
-          w.load_q(item);
         }
       }
       float acc[C::kNT][4], p[C::kNT][2 * C::kNR];
@@ -982,128 +999,196 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
   };
   PieceInfo my{-1, 0, 0};
   if (lane < 2 * C::kW) my = s_piece[lane];
-  unsigned left = __ballot_sync(0xffffffffu, my.item >= 0);
-  bool joined = false;             // the CTA's first piece goes on from the CTA before
-  int first_item = -1, first_ends = 0;
-  while (left) {
-    const int p = __ffs(left) - 1, item = __shfl_sync(0xffffffffu, my.item, p);
+  const unsigned there = __ballot_sync(0xffffffffu, my.item >= 0);
+  unsigned left = there;
+  int turn = warp;                 // (group, row) pairs go to the warps in turn
+#pragma unroll 1
+  for (int k = 0; left; ++k) {
+    const int item = __shfl_sync(0xffffffffu, my.item, __ffs(left) - 1);
     const unsigned group = __ballot_sync(0xffffffffu, my.item == item);
-    const int starts = __shfl_sync(0xffffffffu, my.starts, p);
-    const int ends = __shfl_sync(0xffffffffu, my.ends, 31 - __clz(group));
     left &= ~group;
-    if (!starts) {
-      joined = true;
-      first_item = item;
-      first_ends = ends;
-    }
     const bool in = (group >> lane) & 1u;
-    const int place = __popc(group & ((1u << lane) - 1u));
-    if (warp == 0 && in) s_list[place] = lane;
-    for (int row = warp; row < R; row += C::kW) {
-      const float* s = state(lane) + C::kNel + row;
-      const float m = in ? s[0] : -INFINITY, n = in ? s[R] : -INFINITY;
+#pragma unroll 1
+    for (; turn < R; turn += C::kW) {
+      const float* s = state(lane) + C::kNel + turn;
+      float m = -INFINITY, n = -INFINITY, l = 0.f;
+      if (in) {
+        m = s[0];
+        n = s[R];
+        l = s[2 * R];
+      }
       float mm = m, nn = n;
-#pragma unroll
+#pragma unroll 1
       for (int o = 16; o; o >>= 1) {
         mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
         nn = fmaxf(nn, __shfl_xor_sync(0xffffffffu, nn, o));
       }
-      float l = in ? pow2_of(m - mm) * s[2 * R] : 0.f;
-#pragma unroll
+      if (in) {
+        l *= pow2_of(m - mm);
+        s_weight[lane][turn] = pow2_of(n - nn);
+      }
+#pragma unroll 1
       for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-      if (in) s_weight[place][row] = pow2_of(n - nn);
       if (lane == 0) {
-        s_m[row] = mm;
-        s_n[row] = nn;
-        s_l[row] = l;
+        s_stat[k][0][turn] = mm;
+        s_stat[k][1][turn] = nn;
+        s_stat[k][2][turn] = l;
       }
     }
-    __syncthreads();
-    const int pieces = __popc(group);
-    const bool all = starts && ends;
+    turn -= R;
+  }
+  __syncthreads();
+  auto row_of = [](int idx) {      // the query row of element idx of a state
+    return ((idx & 31) >> 2) + (C::kNR == 2 ? 8 * ((idx >> 5) & 1) : 0);
+  };
+  int2 join = make_int2(-1, 0);    // the pair that goes on from the CTA before, and whether it ends here
+  left = there;
+#pragma unroll 1
+  for (int k = 0; left; ++k) {
+    const int p = __ffs(left) - 1;
+    const int item = __shfl_sync(0xffffffffu, my.item, p);
+    const unsigned group = __ballot_sync(0xffffffffu, my.item == item);
+    const int starts = __shfl_sync(0xffffffffu, my.starts, p);
+    const int ends = __shfl_sync(0xffffffffu, my.ends, 31 - __clz(group));
+    left &= ~group;
+    if (!starts) join = make_int2(item, ends);
     float* to = a.parts + (static_cast<int64_t>(cta) * 2 + (starts ? 1 : 0)) * C::kState;
     const Item it = item_of<R>(a, item);
-    for (int idx = tid; idx < C::kNel; idx += C::kThreads) {
-      const int ln = idx & 31, rest = idx >> 5;
-      const int r = rest % C::kNR, je = rest / C::kNR;
-      const int row = (ln >> 2) + 8 * r;
-      float sum = 0.f;
-#pragma unroll 4
-      for (int x = 0; x < pieces; ++x) sum = fmaf(s_weight[x][row], state(s_list[x])[idx], sum);
-      if (!all) {
-        to[idx] = sum;
+    // a thread's elements, all at once for a piece (the warp's lanes hold the same columns)
+    constexpr int kMine = (C::kNel + C::kThreads - 1) / C::kThreads;
+    float sum[kMine];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) sum[i] = 0.f;
+#pragma unroll 1
+    for (unsigned bits = group; bits; bits &= bits - 1) {
+      const int at = __ffs(bits) - 1;
+      const float* s = state(at);
+      float v[kMine];
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int idx = tid + i * C::kThreads;
+        v[i] = idx < C::kNel ? s[idx] : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < kMine; ++i)
+        sum[i] = fmaf(s_weight[at][row_of(tid + i * C::kThreads)], v[i], sum[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int idx = tid + i * C::kThreads;
+      if (idx >= C::kNel) break;
+      const int ln = idx & 31, je = (idx >> 5) / C::kNR, row = row_of(idx);
+      const float m = s_stat[k][0][row], n = s_stat[k][1][row], l = s_stat[k][2][row];
+      if (!(starts && ends)) {
+        to[idx] = sum[i];
         if ((ln & 3) == 0 && je == 0) {
-          to[C::kNel + row] = s_m[row];
-          to[C::kNel + R + row] = s_n[row];
-          to[C::kNel + 2 * R + row] = s_l[row];
+          to[C::kNel + row] = m;
+          to[C::kNel + R + row] = n;
+          to[C::kNel + 2 * R + row] = l;
         }
       } else if (row < it.rows) {
-        W::write_element(a, it.row0 + row, ln, je, sum, s_m[row], s_n[row], s_l[row]);
+        W::write_element(a, it.row0 + row, ln, je, sum[i], m, n, l);
       }
     }
-    __syncthreads();               // (the lists and weights are the next group's)
   }
-  if (tid == 0) a.joins[cta] = make_int2(joined ? first_item : -1, first_ends);
+  if (tid == 0) a.joins[cta] = join;
 }
 
 // Pairs whose parts lie in several CTAs.  CTA x of `joins` says which pair its first piece
 // continues (-1: none) and whether it ends it; block x merges the pair that CTA x - 1
-// began (its second part) and x, x + 1, .. continue (their first).
+// began (its second part) and x, x + 1, .. continue (their first).  blockIdx.y: which elements.
 template <int T, int DP, int R, bool B>
 __global__ void __launch_bounds__(256) decode_join_kernel(const __grid_constant__ DecodeArgs a) {
   using C = Cfg<T, DP, R, B>;
   using W = Worker<T, DP, R, B>;
-  __shared__ int2 s_join[kDecodeCtas];
-  __shared__ float s_wo[R][kDecodeCtas + 1];
+  constexpr int kLanes = kDecodeCtas / 32;     // pieces of a lane at most
+  static_assert(kDecodeCtas % 32 == 0, "pieces by lanes");
+  __shared__ float s_weight[R][kDecodeCtas];
   __shared__ float s_m[R], s_n[R], s_l[R];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ctas = static_cast<int>(gridDim.x);
   const int x = static_cast<int>(blockIdx.x);
+  if (x == 0) return;
   griddep_wait();
-  for (int i = tid; i < ctas; i += 256) s_join[i] = __ldcg(a.joins + i);
-  __syncthreads();
-  const int item = s_join[x].x;
-  if (x == 0 || item < 0 || s_join[x - 1].x == item) return;
-  int z = x;
-  while (!s_join[z].y && z + 1 < ctas) ++z;
+  // the pair's last CTA: the first from x on that ends it
+  const int2 before = __ldcg(a.joins + x - 1);
+  int z = x, item = -1;
+#pragma unroll 1
+  for (int i = x;; i += 32) {
+    const int2 j = i + lane < ctas ? __ldcg(a.joins + i + lane) : make_int2(-1, 1);
+    if (i == x) {
+      item = __shfl_sync(0xffffffffu, j.x, 0);
+      if (item < 0 || before.x == item) return;
+    }
+    const unsigned ends = __ballot_sync(0xffffffffu, j.y != 0);
+    if (ends) {
+      z = min(i + __ffs(ends) - 1, ctas - 1);
+      break;
+    }
+  }
   const int pieces = z - x + 2;
   auto state = [&](int p) -> const float* {
     return a.parts + (static_cast<int64_t>(x - 1 + p) * 2 + (p == 0 ? 1 : 0)) * C::kState;
   };
+  // the first pieces' elements beside what they are weighted by
+  constexpr int kEarly = 20;
+  const int idx = static_cast<int>(blockIdx.y) * 256 + tid;
+  float v[kEarly];
+#pragma unroll
+  for (int p = 0; p < kEarly; ++p) v[p] = p < pieces ? __ldcg(state(p) + idx) : 0.f;
+#pragma unroll 1
   for (int row = warp; row < R; row += 8) {
-    float m = -INFINITY, n = -INFINITY;
-    for (int p = lane; p < pieces; p += 32) {
-      m = fmaxf(m, __ldcg(state(p) + C::kNel + row));
-      n = fmaxf(n, __ldcg(state(p) + C::kNel + R + row));
+    float m[kLanes], n[kLanes], l[kLanes], mm = -INFINITY, nn = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kLanes; ++i) {
+      const int p = lane + 32 * i;
+      m[i] = n[i] = -INFINITY;
+      l[i] = 0.f;
+      if (p < pieces) {
+        const float* s = state(p) + C::kNel + row;
+        m[i] = __ldcg(s);
+        n[i] = __ldcg(s + R);
+        l[i] = __ldcg(s + 2 * R);
+      }
     }
 #pragma unroll
+    for (int i = 0; i < kLanes; ++i) {
+      mm = fmaxf(mm, m[i]);
+      nn = fmaxf(nn, n[i]);
+    }
+#pragma unroll 1
     for (int o = 16; o; o >>= 1) {
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, o));
-    }
-    float l = 0.f;
-    for (int p = lane; p < pieces; p += 32) {
-      s_wo[row][p] = pow2_of(__ldcg(state(p) + C::kNel + R + row) - n);
-      l = fmaf(pow2_of(__ldcg(state(p) + C::kNel + row) - m), __ldcg(state(p) + C::kNel + 2 * R + row), l);
+      mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+      nn = fmaxf(nn, __shfl_xor_sync(0xffffffffu, nn, o));
     }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    for (int i = 0; i < kLanes; ++i) {
+      const int p = lane + 32 * i;
+      if (p < pieces) {
+        s_weight[row][p] = pow2_of(n[i] - nn);
+        sum = fmaf(pow2_of(m[i] - mm), l[i], sum);
+      }
+    }
+#pragma unroll 1
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) {
-      s_m[row] = m;
-      s_n[row] = n;
-      s_l[row] = l;
+      s_m[row] = mm;
+      s_n[row] = nn;
+      s_l[row] = sum;
     }
   }
   __syncthreads();
   const Item it = item_of<R>(a, item);
-  const int idx = static_cast<int>(blockIdx.y) * 256 + tid;
   const int ln = idx & 31, rest = idx >> 5;
   const int r = rest % C::kNR, je = rest / C::kNR;
   const int row = (ln >> 2) + 8 * r;
   if (row >= it.rows) return;
   float sum = 0.f;
+#pragma unroll
+  for (int p = 0; p < kEarly; ++p)
+    if (p < pieces) sum = fmaf(s_weight[row][p], v[p], sum);
 #pragma unroll 8
-  for (int p = 0; p < pieces; ++p) sum = fmaf(s_wo[row][p], __ldcg(state(p) + idx), sum);
+  for (int p = kEarly; p < pieces; ++p) sum = fmaf(s_weight[row][p], __ldcg(state(p) + idx), sum);
   W::write_element(a, it.row0 + row, ln, je, sum, s_m[row], s_n[row], s_l[row]);
 }
 

@@ -255,7 +255,7 @@ struct DecodeArgs {
   int32_t items_per_seq;    // hkv * groups
   int32_t head_dim, row_bytes, page_size;
   int32_t page_shift;       // log2(page_size), or -1
-  int32_t max_pages, capacity;   // capacity: max_pages * page_size, at most 2^31 - 256
+  int32_t max_pages, capacity;   // capacity: max_pages * page_size, at most 2^29
   int32_t window, act_bf16;
   float scale;
   void* out;

@@ -767,8 +767,8 @@ sa_status sa_load_kv(const void *k_pages, const void *v_pages, const float *k_sc
  *
  * Checks, in order: HEAD_COUNT, HEAD_DIM, SHAPE (batch < 0), BLOCK_PAGE, SHAPE,
  * INVALID_ARGUMENT (types), UNSUPPORTED (head_dim not a multiple of 8, or 16 for the
- * 8-bit types, or above 256; batch * hq >= 2^31; num_pages * hkv * page_size >= 2^32 -
- * 1), INVALID_ARGUMENT (NULL, alignment, workspace);
+ * 8-bit types, or above 256; batch * hq >= 2^31; max_pages * page_size > 2^29;
+ * num_pages * hkv * page_size >= 2^32 - 1), INVALID_ARGUMENT (NULL, alignment, workspace);
  * on device: SHAPE (page id >= num_pages, taken as absent).
  */
 sa_status sa_decode_workspace_size(int32_t batch, int32_t hq, int32_t hkv, int32_t head_dim,
