@@ -72,7 +72,7 @@ struct Cfg {
   // operands of Q kept per k-step (see load_q), and of P
   static constexpr int kQP = kF32 ? 1 : k8 ? (R == 8 || B ? 1 : 2) : B ? 1 : R == 8 ? 2 : 3;
   static constexpr int kPP = kF32 ? 1 : k8 ? (R == 8 || B ? 1 : 2) : R == 8 ? (B ? 1 : 2) : (B ? 2 : 3);
-  static constexpr int kQBytes = kKS * kQP * 512;
+  static constexpr int kQBytes = (kF32 ? kKS / 2 : kKS * kQP) * 512;
   static constexpr int kScales = k8 ? kKT * 4 : 0;              // bytes of an entry's scales
   // The ring's entries hold K and V in turn.  Three are least (one in use, two in
   // flight); a fourth is taken where it costs no warp.  Warps are worth more than a longer
@@ -194,6 +194,11 @@ __device__ __forceinline__ int tiles_of(const Keys& k) {
   return max((k.end - k.first + KT - 1) / KT, 1);             // a sequence without keys has one, of none
 }
 
+// x / y for x >= 0 (a 64-bit division is long, and rarely needed).
+__device__ __forceinline__ int64_t divide(int64_t x, unsigned y) {
+  return (x >> 32) == 0 ? static_cast<int64_t>(static_cast<unsigned>(x) / y) : x / y;
+}
+
 // An item: (sequence b, kv head h, lane group).  Its first query row and their number.
 struct Item {
   int64_t row0;
@@ -236,7 +241,7 @@ struct Worker {
     first = k.first;
     end = k.end;
     nt = tiles_of<C::kKT>(k);
-    h = static_cast<int>(in_seq / nt);
+    h = static_cast<int>(divide(in_seq, static_cast<unsigned>(nt)));
     t = static_cast<int>(in_seq - static_cast<int64_t>(h) * nt);
     next_used = b + 1 < a.batch ? a.used[b + 1] : 0;
   }
@@ -305,7 +310,8 @@ struct Worker {
   // holds row g (and g + 8) at the channels of the chunks that it reads of K's rows.
   //   8 bits: the row, scaled by a power of two into f16's range, as f16 high
   //     parts and remainders; bf16: three bf16 parts (bf16 queries: the first says all);
-  //     f32: tf32 parts.
+  //     f32: as they are, split into tf32 parts where they are used (12 operations per 16
+  //     products, and half the room, which lets 12 warps in instead of 8).
   //   R = 8: rows g + 8 of the MMA's tile carry the second parts of rows g, so that they
   //     cost no product.
   // fetch_q asks for the rows, keep_q lays them out: between them other loads start.
@@ -367,13 +373,8 @@ struct Worker {
 #pragma unroll
       for (int i = 0; i < kQ4; ++i) {
         if constexpr (C::kF32) {
-          uint4 u, v;
-          split_tf32(x[i].x, u.x, u.y);
-          split_tf32(x[i].y, u.z, u.w);
-          split_tf32(x[i].z, v.x, v.y);
-          split_tf32(x[i].w, v.z, v.w);
-          out[32 * 2 * i] = u;
-          out[32 * (2 * i + 1)] = v;
+          out[32 * i] = make_uint4(__float_as_uint(x[i].x), __float_as_uint(x[i].y),
+                                   __float_as_uint(x[i].z), __float_as_uint(x[i].w));
         } else {
           uint4* to = out + 32 * C::kQP * i;
           uint32_t hi[2], mid[2], lo[2] = {0u, 0u};
@@ -446,15 +447,21 @@ struct Worker {
 #pragma unroll
     for (int l = 0; l < C::kLCH; ++l) {
       const int phys = C::kNCH >= 8 ? chunk(l) ^ g : chunk(l) ^ ((g >> 1) & 3);
-      uint4 kr[C::kNT];
+      uint4 kr[C::kNT], qr;
 #pragma unroll
       for (int n = 0; n < C::kNT; ++n)
         kr[n] = *reinterpret_cast<const uint4*>(kt + n * 8 * C::kRow + phys * 16);
 #pragma unroll
       for (int s = 0; s < C::kKPC; ++s) {
+        uint4 q0, q1, q2;
         const uint4* at = q + 32 * C::kQP * (l * C::kKPC + s);
-        const uint4 q0 = at[0];
-        uint4 q1, q2;
+        if constexpr (C::kF32) {
+          if (s == 0) qr = q[32 * l];
+          split_tf32(__uint_as_float(s ? qr.z : qr.x), q0.x, q0.y);
+          split_tf32(__uint_as_float(s ? qr.w : qr.y), q0.z, q0.w);
+        } else {
+          q0 = at[0];
+        }
         if constexpr (C::kQP >= 2) q1 = at[32];
         if constexpr (C::kQP >= 3) q2 = at[64];
 #pragma unroll
@@ -849,9 +856,13 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
     if (tid == 0) a.joins[cta] = make_int2(-1, 0);
     return;
   }
-  const int64_t workers = static_cast<int64_t>(ctas) * C::kW;
-  const int64_t me = static_cast<int64_t>(cta) * C::kW + warp;
-  const int64_t t0 = total * me / workers, t1 = total * (me + 1) / workers;
+  // worker w of n: tiles floor(total w / n) on
+  const unsigned workers = static_cast<unsigned>(ctas) * C::kW;
+  const unsigned me = static_cast<unsigned>(cta) * C::kW + warp;
+  const int64_t each = divide(total, workers);
+  const unsigned rest = static_cast<unsigned>(total - each * workers);
+  const int64_t t0 = each * me + rest * me / workers;
+  const int64_t t1 = each * (me + 1) + rest * (me + 1) / workers;
   int b0 = 0;
   int64_t in_seq = t0;                         // tiles of the sequence before t0
   if (t0 < t1) {
