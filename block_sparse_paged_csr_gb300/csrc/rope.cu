@@ -84,49 +84,38 @@ __device__ __forceinline__ int axis_position(const RopeArgs& a, int64_t tok, int
   return a.positions[axis * a.axis_stride + tok];
 }
 
-template <bool kBf16>
-__device__ __forceinline__ void load8f(const void* p, int64_t off, float* x) {
-  if constexpr (kBf16) {
-    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + off);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  } else {
-    const float4* v = reinterpret_cast<const float4*>(static_cast<const float*>(p) + off);
-    const float4 l = v[0], h = v[1];
-    x[0] = l.x; x[1] = l.y; x[2] = l.z; x[3] = l.w;
-    x[4] = h.x; x[5] = h.y; x[6] = h.z; x[7] = h.w;
+// Four channels as they lie, and as values.
+template <bool kBf16> struct Raw4;
+template <> struct Raw4<true> {
+  uint2 u;
+  __device__ __forceinline__ void load(const void* p, int64_t off) {
+    u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + off);
   }
-}
-
-template <bool kBf16>
-__device__ __forceinline__ void store8f(void* p, int64_t off, const float* x) {
-  if constexpr (kBf16) {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + off) =
-        make_uint4(pack_bf16x2_rn(x[0], x[1]), pack_bf16x2_rn(x[2], x[3]),
-                   pack_bf16x2_rn(x[4], x[5]), pack_bf16x2_rn(x[6], x[7]));
-  } else {
-    float4* v = reinterpret_cast<float4*>(static_cast<float*>(p) + off);
-    v[0] = make_float4(x[0], x[1], x[2], x[3]);
-    v[1] = make_float4(x[4], x[5], x[6], x[7]);
+  __device__ __forceinline__ void zero() { u = make_uint2(0u, 0u); }
+  __device__ __forceinline__ float4 values() const { return bf16x4_to_f32(u); }
+};
+template <> struct Raw4<false> {
+  float4 u;
+  __device__ __forceinline__ void load(const void* p, int64_t off) {
+    u = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + off);
   }
-}
+  __device__ __forceinline__ void zero() { u = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ float4 values() const { return u; }
+};
 
-// A row is spread over kLanes lanes, a lane holding 16 channels in two pieces of 8
-// that hold whole pairs: channels 8 u and rot / 2 + 8 u on (or 16 u on, where pairs
-// are adjacent), so that the rotation needs no other lane.  Either way the pieces'
-// pairs are 8 u .. 8 u + 7.  A group of kLanes lanes keeps one token and walks over
-// its heads: angles are made once per token and pair, by the CTA, and stay in
-// registers, as the weights do.
+// A row is spread over kLanes lanes, a lane holding 8 channels in two pieces of 4 that
+// hold whole pairs: channels 4 u and rot / 2 + 4 u on (or 8 u on, where pairs are
+// adjacent), so that the rotation needs no other lane.  Either way the pieces' pairs are
+// 4 u .. 4 u + 3.  A group of kLanes lanes keeps one token and walks over its heads, kRows of them
+// at a time, all asked for before the first is used: angles are made once per
+// token and pair, by the CTA, and stay in registers, as the weights do.
 template <bool kSrcBf16, bool kDstBf16, int kLanes>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
 norm_rope_kernel(const RopeArgs a, int log_tokens, int heads_per_cta) {
   constexpr int kGroups = kThreads / kLanes;
+  constexpr int kRows = 3;
   __shared__ int s_pos[kMaxTokens];
-  __shared__ float2 s_turn[kMaxTokens * 128];
+  __shared__ __align__(16) float2 s_turn[kMaxTokens * 128];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int tokens = 1 << log_tokens;
   const int64_t tok0 = static_cast<int64_t>(blockIdx.x) << log_tokens;
@@ -134,27 +123,49 @@ norm_rope_kernel(const RopeArgs a, int log_tokens, int heads_per_cta) {
   const int group = tid / kLanes, u = tid % kLanes;
   const int64_t tok = tok0 + (group & (tokens - 1));
   const int step = kGroups >> log_tokens;              // heads between a group's rows
-  const int head0 = static_cast<int>(blockIdx.y) * heads_per_cta + (group >> log_tokens);
   const int total = a.heads[0] + a.heads[1];
   const int end = min(total, static_cast<int>(blockIdx.y + 1) * heads_per_cta);
-  const int rot_units = a.rot >> 4;
+  int head = static_cast<int>(blockIdx.y) * heads_per_cta + (group >> log_tokens);
+  const int rot_units = a.rot >> 3;
   const bool rotated = u < rot_units;
-  const int ca = rotated ? (a.interleaved ? 16 * u : 8 * u) : a.rot + 16 * (u - rot_units);
-  const int cb = rotated && !a.interleaved ? n_pairs + 8 * u : ca + 8;
-  const bool has_a = ca < a.head_dim, has_b = has_a && cb < a.head_dim;
-
-  float x[16];
-  auto load_row = [&](int h, float (&v)[16]) {
-    const int kind = h >= a.heads[0] ? 1 : 0;
-    const int64_t at = tok * a.token_stride[kind] +
-                       static_cast<int64_t>(h - (kind ? a.heads[0] : 0)) * a.head_stride[kind];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = 0.f;
-    if (has_a) load8f<kSrcBf16>(a.src[kind], at + ca, v);
-    if (has_b) load8f<kSrcBf16>(a.src[kind], at + cb, v + 8);
-  };
+  const int ca = rotated ? (a.interleaved ? 8 * u : 4 * u) : 8 * u;
+  const int cb = rotated && !a.interleaved ? n_pairs + 4 * u : ca + 4;
+  const bool mine = 8 * u < a.head_dim;
   const bool live = tok < a.tq;
-  if (live && head0 < end) load_row(head0, x);
+
+  Raw4<kSrcBf16> xa[kRows], xb[kRows];
+  auto load_rows = [&]() {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int h = head + i * step;
+      xa[i].zero();
+      xb[i].zero();
+      if (live && mine && h < end) {
+        const int kind = h >= a.heads[0] ? 1 : 0;
+        const int64_t at = tok * a.token_stride[kind] +
+                           static_cast<int64_t>(h - (kind ? a.heads[0] : 0)) * a.head_stride[kind];
+        xa[i].load(a.src[kind], at + ca);
+        xb[i].load(a.src[kind], at + cb);
+      }
+    }
+  };
+  load_rows();
+  float4 w[2][2];                                      // of q and k: both pieces
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    w[k][0] = w[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (a.weight[k] != nullptr && mine) {
+      if (a.weight_bf16) {
+        const uint16_t* p = static_cast<const uint16_t*>(a.weight[k]);
+        w[k][0] = bf16x4_to_f32(*reinterpret_cast<const uint2*>(p + ca));
+        w[k][1] = bf16x4_to_f32(*reinterpret_cast<const uint2*>(p + cb));
+      } else {
+        const float* p = static_cast<const float*>(a.weight[k]);
+        w[k][0] = *reinterpret_cast<const float4*>(p + ca);
+        w[k][1] = *reinterpret_cast<const float4*>(p + cb);
+      }
+    }
+  }
 
   if (n_pairs > 0) {
     if (a.positions == nullptr) {
@@ -174,71 +185,70 @@ norm_rope_kernel(const RopeArgs a, int log_tokens, int heads_per_cta) {
     __syncthreads();
   }
   if (!live) return;
-  float co[8], si[8];
+  float co[4], si[4];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    co[j] = 1.f;
-    si[j] = 0.f;
-    if (rotated) {
-      const float2 t = s_turn[(group & (tokens - 1)) * n_pairs + 8 * u + j];
-      co[j] = t.x;
-      si[j] = t.y;
-    }
+  for (int j = 0; j < 4; j += 2) {
+    float4 t = make_float4(1.f, 0.f, 1.f, 0.f);
+    if (rotated)
+      t = *reinterpret_cast<const float4*>(s_turn + (group & (tokens - 1)) * n_pairs + 4 * u + j);
+    co[j] = t.x;
+    si[j] = t.y;
+    co[j + 1] = t.z;
+    si[j + 1] = t.w;
   }
-  float w[16];
-  int have = -1;                                       // whose weights w holds
-  for (int h = head0; h < end; h += step) {
-    float next[16];
-    if (h + step < end) load_row(h + step, next);
-    const int kind = h >= a.heads[0] ? 1 : 0;
-    // (the same for all lanes of a group, and a group's lanes lie in one warp)
-    if (a.weight[kind] != nullptr) {
-      if (have != kind) {
-        have = kind;
+  const unsigned mask = kLanes == 32 ? 0xffffffffu
+                                     : ((1u << (kLanes & 31)) - 1u) << ((lane / kLanes) * kLanes);
+  for (; head < end; head += kRows * step) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = 0.f;
-        if (a.weight_bf16) {
-          if (has_a) load8f<true>(a.weight[kind], ca, w);
-          if (has_b) load8f<true>(a.weight[kind], cb, w + 8);
+    for (int i = 0; i < kRows; ++i) {
+      const int h = head + i * step;
+      if (h >= end) break;
+      const int kind = h >= a.heads[0] ? 1 : 0;
+      const float4 p4 = xa[i].values(), q4 = xb[i].values();
+      float x[8] = {p4.x, p4.y, p4.z, p4.w, q4.x, q4.y, q4.z, q4.w};
+      // (the same for all lanes of a group, and a group's lanes lie in one warp)
+      if (a.weight[kind] != nullptr) {
+        float ss = 0.f;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) ss = fmaf(x[c], x[c], ss);
+#pragma unroll
+        for (int o = kLanes / 2; o; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
+        const float r = rsqrtf(ss / static_cast<float>(a.head_dim) + a.eps);
+        const float4 wa = kind ? w[1][0] : w[0][0], wb = kind ? w[1][1] : w[0][1];
+        const float ww[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
+#pragma unroll
+        for (int c = 0; c < 8; ++c) x[c] = x[c] * r * ww[c];
+      }
+      if (rotated) {
+        if (a.interleaved) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float p = x[2 * j], q = x[2 * j + 1];
+            x[2 * j] = p * co[j] - q * si[j];
+            x[2 * j + 1] = p * si[j] + q * co[j];
+          }
         } else {
-          if (has_a) load8f<false>(a.weight[kind], ca, w);
-          if (has_b) load8f<false>(a.weight[kind], cb, w + 8);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float p = x[j], q = x[4 + j];
+            x[j] = p * co[j] - q * si[j];
+            x[4 + j] = p * si[j] + q * co[j];
+          }
         }
       }
-      float ss = 0.f;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
-      const unsigned mask = kLanes == 32 ? 0xffffffffu
-                                         : ((1u << kLanes) - 1u) << ((lane / kLanes) * kLanes);
-#pragma unroll
-      for (int o = kLanes / 2; o; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
-      const float r = rsqrtf(ss / static_cast<float>(a.head_dim) + a.eps);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = x[i] * r * w[i];
-    }
-    if (rotated) {
-      if (a.interleaved) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float p = x[2 * j], q = x[2 * j + 1];
-          x[2 * j] = p * co[j] - q * si[j];
-          x[2 * j + 1] = p * si[j] + q * co[j];
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float p = x[j], q = x[8 + j];
-          x[j] = p * co[j] - q * si[j];
-          x[8 + j] = p * si[j] + q * co[j];
-        }
+      if (mine) {
+        const int64_t at =
+            tok * a.dst_token_stride[kind] +
+            static_cast<int64_t>(h - (kind ? a.heads[0] : 0)) * a.dst_head_stride[kind];
+        store_o4(a.dst[kind], kDstBf16, at + ca, make_float4(x[0], x[1], x[2], x[3]));
+        store_o4(a.dst[kind], kDstBf16, at + cb, make_float4(x[4], x[5], x[6], x[7]));
       }
     }
-    const int64_t at = tok * a.dst_token_stride[kind] +
-                       static_cast<int64_t>(h - (kind ? a.heads[0] : 0)) * a.dst_head_stride[kind];
-    if (has_a) store8f<kDstBf16>(a.dst[kind], at + ca, x);
-    if (has_b) store8f<kDstBf16>(a.dst[kind], at + cb, x + 8);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = next[i];
+    if (head + kRows * step < end) {
+      head += kRows * step;
+      load_rows();
+      head -= kRows * step;
+    }
   }
 }
 
@@ -334,8 +344,8 @@ cudaError_t launch_rope(const RopeArgs& a, bool wide, cudaStream_t stream) {
         <<<static_cast<unsigned>(ctas), kThreads, 0, stream>>>(a);
     return cudaGetLastError();
   }
-  const int units = (a.head_dim + 15) / 16;
-  const int lanes = units <= 4 ? 4 : units <= 8 ? 8 : 16;
+  const int units = a.head_dim / 8;
+  const int lanes = units <= 4 ? 4 : units <= 8 ? 8 : units <= 16 ? 16 : 32;
   const int groups = kThreads / lanes;
   // Prompts: four tokens a CTA.  Few tokens: one, and its heads over several CTAs,
   // so that a row is all that a group does.
@@ -347,15 +357,15 @@ cudaError_t launch_rope(const RopeArgs& a, bool wide, cudaStream_t stream) {
   const int64_t gy = (total + heads_per_cta - 1) / heads_per_cta;
   if (gx > 0x7FFFFFFF || gy > 65535) return cudaErrorNotSupported;
   const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy));
+  auto go = [&](auto kernel) { kernel<<<grid, kThreads, 0, stream>>>(a, log_tokens, heads_per_cta); };
   if (lanes == 4)
-    norm_rope_kernel<kSrcBf16, kDstBf16, 4>
-        <<<grid, kThreads, 0, stream>>>(a, log_tokens, heads_per_cta);
+    go(norm_rope_kernel<kSrcBf16, kDstBf16, 4>);
   else if (lanes == 8)
-    norm_rope_kernel<kSrcBf16, kDstBf16, 8>
-        <<<grid, kThreads, 0, stream>>>(a, log_tokens, heads_per_cta);
+    go(norm_rope_kernel<kSrcBf16, kDstBf16, 8>);
+  else if (lanes == 16)
+    go(norm_rope_kernel<kSrcBf16, kDstBf16, 16>);
   else
-    norm_rope_kernel<kSrcBf16, kDstBf16, 16>
-        <<<grid, kThreads, 0, stream>>>(a, log_tokens, heads_per_cta);
+    go(norm_rope_kernel<kSrcBf16, kDstBf16, 32>);
   return cudaGetLastError();
 }
 
@@ -427,16 +437,16 @@ extern "C" sa_status sa_norm_rope(
   a.rot = rot_dim;
   a.interleaved = interleaved != 0;
   a.status = status;
-  // 16-byte loads and stores of 8-channel pieces: everything a multiple of them
-  const int64_t src_unit = src_dtype == SA_DTYPE_BF16 ? 8 : 4;
-  const int64_t dst_unit = out_dtype == SA_DTYPE_BF16 ? 8 : 4;
-  bool wide = head_dim % 8 == 0 && rot_dim % 16 == 0;
+  // loads and stores of 4-channel pieces (8 or 16 bytes): everything a multiple of them
+  auto whole = [](const void* p, sa_dtype type) {
+    return (reinterpret_cast<uintptr_t>(p) & (type == SA_DTYPE_BF16 ? 7u : 15u)) == 0;
+  };
+  bool wide = head_dim % 8 == 0 && rot_dim % 8 == 0;
   for (int i = 0; i < 2; ++i) {
     if (a.heads[i] == 0) continue;
-    wide = wide && sa::aligned16(a.src[i]) && sa::aligned16(a.dst[i]) &&
-           (a.weight[i] == nullptr || sa::aligned16(a.weight[i])) &&
-           a.token_stride[i] % src_unit == 0 && a.head_stride[i] % src_unit == 0 &&
-           a.dst_token_stride[i] % dst_unit == 0 && a.dst_head_stride[i] % dst_unit == 0;
+    wide = wide && whole(a.src[i], src_dtype) && whole(a.dst[i], out_dtype) &&
+           whole(a.weight[i], weight_dtype) &&
+           ((a.token_stride[i] | a.head_stride[i] | a.dst_token_stride[i] | a.dst_head_stride[i]) & 3) == 0;
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t err;

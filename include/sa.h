@@ -691,7 +691,7 @@ sa_status sa_select_blocks(const void *q, sa_dtype q_dtype, int64_t tq, int32_t 
  *   status        as for sa_store_kv
  *
  * Supported: head_dim <= 256, any strides and alignment (fastest where head_dim
- * is a multiple of 8, rot_dim of 16, and every row starts on 16 bytes).  Checks,
+ * and rot_dim are multiples of 8 and every row starts on 4 channels).  Checks,
  * in order: HEAD_COUNT (hq + hkv = 0), HEAD_DIM (rot_dim odd or above head_dim),
  * SHAPE (tq, n_axes), CU_SEQLENS and SHAPE (n_axes = 0), INVALID_ARGUMENT (types, eps
  * negative or NaN, freq_axes without positions), UNSUPPORTED, INVALID_ARGUMENT
