@@ -959,6 +959,67 @@ def sa_norm_rope(q, k, q_weight, k_weight, inv_freq, positions=None, cu_seqlens_
     ``cu_seqlens_q_host``, ``cu_seqlens_q`` and ``used_kv_lens``.  Returns
     (q_out, k_out), of ``out_dtype`` (default: the input's type); an output handed
     in may be its input."""
+    x = _rope_usual(q, k, q_weight, k_weight, inv_freq, q_out, k_out, out_dtype)
+    if x is None:
+        q_out, k_out, x = _check_rope(q, k, q_weight, k_weight, inv_freq, q_out, k_out, out_dtype,
+                                      stream)
+    dev, tq, hq, hkv, d, src, wt, out, strides = x
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    cu_h = used = None
+    axes = batch = 0
+    if positions is not None:
+        _require(positions, torch.int32, "positions", dev)
+        if positions.dim() not in (1, 2) or positions.shape[-1] != tq:
+            raise ValueError(f"positions must be [{tq}] or [axes, {tq}]")
+        axes = 1 if positions.dim() == 1 else positions.shape[0]
+        positions = positions.data_ptr()
+    elif rot:
+        if cu_seqlens_q_host is None or cu_seqlens_q is None or used_kv_lens is None:
+            raise ValueError("positions, or cu_seqlens_q_host, cu_seqlens_q and used_kv_lens, are needed")
+        cu, batch = _batch_args(cu_seqlens_q_host, cu_seqlens_q, used_kv_lens, (), dev, ())
+        cu_h, cu_d, used = _host_ptr(cu), cu_seqlens_q.data_ptr(), used_kv_lens.data_ptr()
+    if cu_h is None:
+        cu_d = None
+    if freq_axes is not None:
+        _require(freq_axes, torch.int32, "freq_axes", dev)
+        if freq_axes.numel() * 2 != rot:
+            raise ValueError(f"freq_axes must have {rot // 2} values")
+    q_st, k_st, qo_st, ko_st = strides
+    _check(_on(dev, _native.load().sa_norm_rope, _ptr(q), _ptr(k), _ACT_DTYPES[src], q_st[0],
+               q_st[1], k_st[0], k_st[1], None if q is None else _ptr(q_weight),
+               None if k is None else _ptr(k_weight), _ACT_DTYPES[wt], eps, _ptr(inv_freq), rot,
+               _ptr(freq_axes), 1 if interleaved else 0, positions, axes, tq, cu_h, cu_d, batch,
+               used, tq, hq, hkv, d, _ptr(q_out), _ptr(k_out), _ACT_DTYPES[out], qo_st[0], qo_st[1],
+               ko_st[0], ko_st[1], _status_word(status, dev), _stream(stream, dev)), "sa_norm_rope")
+    return q_out, k_out
+
+
+def _rope_usual(q, k, q_weight, k_weight, inv_freq, q_out, k_out, out_dtype):
+    """What a call needs to know of its tensors where all are given and as they should
+    be; None where not (:func:`_check_rope` then says what is wrong, or makes outputs)."""
+    try:
+        src, out, shape, kshape = q.dtype, q_out.dtype, q.shape, k.shape
+        index, wt = q.get_device(), q_weight.dtype
+        tq, hq, d = shape
+        tk, hkv, dk = kshape
+        strides = q.stride(), k.stride(), q_out.stride(), k_out.stride()
+        if (index >= 0 and src in _ACT_DTYPES and out in _ACT_DTYPES and wt in _ACT_DTYPES and
+                k.dtype is src and k_out.dtype is out and (out_dtype is None or out_dtype is out) and
+                tk == tq and dk == d and q_out.shape == shape and k_out.shape == kshape and
+                strides[0][2] == 1 and strides[1][2] == 1 and strides[2][2] == 1 and
+                strides[3][2] == 1 and k.get_device() == index and q_out.get_device() == index and
+                k_out.get_device() == index and
+                (q.data_ptr() != q_out.data_ptr() or (src is out and strides[0] == strides[2])) and
+                (k.data_ptr() != k_out.data_ptr() or (src is out and strides[1] == strides[3])) and
+                _alike(index, wt, q_weight, k_weight) and q_weight.numel() == d and
+                k_weight.numel() == d and _alike(index, torch.float32, inv_freq)):
+            return q.device, tq, hq, hkv, d, src, wt, out, strides
+    except (AttributeError, ValueError):
+        pass
+    return None
+
+
+def _check_rope(q, k, q_weight, k_weight, inv_freq, q_out, k_out, out_dtype, stream):
     given = q if q is not None else k
     src = _heads(given, "k" if q is None else "q")
     dev, (tq, _, d) = given.device, given.shape
@@ -972,9 +1033,10 @@ def sa_norm_rope(q, k, q_weight, k_weight, inv_freq, positions=None, cu_seqlens_
             if out is not None:
                 raise ValueError(f"{name} without its input")
         elif out is None:
+            if (out_dtype or t.dtype) not in _ACT_DTYPES:
+                raise TypeError(f"out_dtype must be float32 or bfloat16, got {out_dtype}")
             with _allocating(stream):
                 out = torch.empty(t.shape, dtype=out_dtype or t.dtype, device=dev)
-            _heads(out, name)
         else:
             _heads(out, name)
             if out.shape != t.shape or out.device != dev:
@@ -988,9 +1050,8 @@ def sa_norm_rope(q, k, q_weight, k_weight, inv_freq, positions=None, cu_seqlens_
     q_out, k_out = made
     if q_out is not None and k_out is not None and q_out.dtype != k_out.dtype:
         raise TypeError("q_out and k_out must have one type")
-    out = q_out if q_out is not None else k_out
     wt = None
-    for w, t, name in ((q_weight, q, "q_weight"), (k_weight, k, "k_weight")):
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if w is not None:
             if not isinstance(w, torch.Tensor) or w.dtype not in _ACT_DTYPES:
                 raise TypeError(f"{name} must be a float32 or bfloat16 tensor")
@@ -998,36 +1059,12 @@ def sa_norm_rope(q, k, q_weight, k_weight, inv_freq, positions=None, cu_seqlens_
             _require(w, wt, name, dev)
             if w.numel() != d:
                 raise ValueError(f"{name} must have {d} values")
-    rot, axes, axis_stride, cu_h, batch = 0, 0, 0, None, 0
     if inv_freq is not None:
         _require(inv_freq, torch.float32, "inv_freq", dev)
-        rot = 2 * inv_freq.numel()
-    if positions is not None:
-        _require(positions, torch.int32, "positions", dev)
-        if positions.dim() not in (1, 2) or positions.shape[-1] != tq:
-            raise ValueError(f"positions must be [{tq}] or [axes, {tq}]")
-        axes, axis_stride = (1 if positions.dim() == 1 else positions.shape[0]), tq
-    elif rot:
-        if cu_seqlens_q_host is None or cu_seqlens_q is None or used_kv_lens is None:
-            raise ValueError("positions, or cu_seqlens_q_host, cu_seqlens_q and used_kv_lens, are needed")
-        cu_h, batch = _batch_args(cu_seqlens_q_host, cu_seqlens_q, used_kv_lens, (), dev, ())
-    if freq_axes is not None:
-        _require(freq_axes, torch.int32, "freq_axes", dev)
-        if freq_axes.numel() * 2 != rot:
-            raise ValueError(f"freq_axes must have {rot // 2} values")
-    q_st, k_st, qo_st, ko_st = [(0, 0) if t is None else t.stride()[:2]
-                                for t in (q, k, q_out, k_out)]
-    _check(_on(dev, _native.load().sa_norm_rope, _ptr(q), _ptr(k), _ACT_DTYPES[given.dtype], *q_st,
-               *k_st, _ptr(q_weight if q is not None else None),
-               _ptr(k_weight if k is not None else None), _ACT_DTYPES[wt or torch.float32], eps,
-               _ptr(inv_freq), rot, _ptr(freq_axes), int(bool(interleaved)), _ptr(positions), axes,
-               axis_stride, None if cu_h is None else _host_ptr(cu_h),
-               None if cu_h is None else cu_seqlens_q.data_ptr(), batch,
-               None if cu_h is None else used_kv_lens.data_ptr(), tq,
-               0 if q is None else q.shape[1], 0 if k is None else k.shape[1], d, _ptr(q_out),
-               _ptr(k_out), _ACT_DTYPES[out.dtype], *qo_st, *ko_st, _status_word(status, dev),
-               _stream(stream, dev)), "sa_norm_rope")
-    return q_out, k_out
+    strides = [(0, 0, 1) if t is None else t.stride() for t in (q, k, q_out, k_out)]
+    out = q_out if q_out is not None else k_out
+    return q_out, k_out, (dev, tq, 0 if q is None else q.shape[1], 0 if k is None else k.shape[1], d,
+                          src, wt or torch.float32, out.dtype, strides)
 
 
 def _heads(t, name):
@@ -1084,31 +1121,47 @@ def sa_load_kv(k_pages, v_pages, block_tables, cu_seqlens_host, cu_seqlens, used
     cu_h, batch = _batch_args(cu_seqlens_host, cu_seqlens, used_kv_lens, (block_tables,), dev,
                               ("block_tables",))
     rows = int(cu_h[-1]) if cu_h.size else 0
+    shape = (rows, hkv, d)
+    try:
+        ks0, ks1, ks2 = k.stride()
+        vs0, vs1, vs2 = v.stride()
+        out, index = k.dtype, dev.index
+        usual = (out in _ACT_DTYPES and v.dtype is out and (dtype is None or dtype is out) and
+                 k.shape == shape and v.shape == shape and ks2 == 1 and vs2 == 1 and
+                 k.get_device() == index and v.get_device() == index)
+    except (AttributeError, ValueError):
+        usual = False
+    if not usual:
+        k, v, out = _check_rows(k, v, dtype, (max(rows, 0), hkv, d), k_pages, stream)
+        ks0, ks1, _ = k.stride()
+        vs0, vs1, _ = v.stride()
+    _check(_on(dev, _native.load().sa_load_kv, k_pages.data_ptr(), v_pages.data_ptr(),
+               _ptr(k_scales), _ptr(v_scales), num_pages, code, block_tables.data_ptr(),
+               block_tables.shape[1], _host_ptr(cu_h), cu_seqlens.data_ptr(), batch, rows,
+               used_kv_lens.data_ptr(), hkv, d, page_size, k.data_ptr(), v.data_ptr(),
+               _ACT_DTYPES[out], ks0, ks1, vs0, vs1, _status_word(status, dev),
+               _stream(stream, dev)), "sa_load_kv")
+    return k, v
+
+
+def _check_rows(k, v, dtype, shape, k_pages, stream):
+    """The outputs of a :func:`sa_load_kv` call, made where not given, and their type."""
+    dev = k_pages.device
     if dtype is None:
         some = k if k is not None else v
         dtype = some.dtype if some is not None else (
             torch.float32 if k_pages.dtype is torch.float32 else torch.bfloat16)
     if dtype not in _ACT_DTYPES:
         raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
-    shape = (max(rows, 0), hkv, d)
     made = []
     for t, name in ((k, "k"), (v, "v")):
         if t is None:
             with _allocating(stream):
                 t = torch.empty(shape, dtype=dtype, device=dev)
-        elif (_heads(t, name) != dtype or t.shape != shape or t.device != dev):
+        elif _heads(t, name) != dtype or t.shape != shape or t.device != dev:
             raise ValueError(f"{name} must be {shape} of {dtype} on {dev}")
         made.append(t)
-    k, v = made
-    ks0, ks1, _ = k.stride()
-    vs0, vs1, _ = v.stride()
-    _check(_on(dev, _native.load().sa_load_kv, k_pages.data_ptr(), v_pages.data_ptr(),
-               _ptr(k_scales), _ptr(v_scales), num_pages, code, block_tables.data_ptr(),
-               block_tables.shape[1], _host_ptr(cu_h), cu_seqlens.data_ptr(), batch, rows,
-               used_kv_lens.data_ptr(), hkv, d, page_size, k.data_ptr(), v.data_ptr(),
-               _ACT_DTYPES[dtype], ks0, ks1, vs0, vs1, _status_word(status, dev),
-               _stream(stream, dev)), "sa_load_kv")
-    return k, v
+    return made[0], made[1], dtype
 
 
 def allocate_decode_workspace(batch, hq, hkv, head_dim, device) -> torch.Tensor:

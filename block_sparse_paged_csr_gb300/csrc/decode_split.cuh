@@ -46,8 +46,8 @@ template <> struct TypeOf<SA_DTYPE_E4M3> { static constexpr int size = 1; };
 template <> struct TypeOf<SA_DTYPE_INT8> { static constexpr int size = 1; };
 
 // T: the cache's type.  DP: head_dim rounded up to 64, 128 or 256 (channels behind it
-// are zeros).  R: query rows of a tile, 8 or 16.  B: bf16 queries, whose operands have one part (for
-// the instances where that saves shared memory or products; the others take both types).
+// are zeros).  R: query rows of a tile, 8 or 16.  B: bf16 queries, whose operands have
+// fewer parts (f32 caches take both types as they come).
 template <int T, int DP, int R, bool B>
 struct Cfg {
   static constexpr int kSize = TypeOf<T>::size;
@@ -69,10 +69,15 @@ struct Cfg {
   static constexpr int kNS = DP / (8 * kEP);                    // .. times
   static constexpr int kNJ = DP / 8;                            // n-tiles of o
   static constexpr int kNR = R / 8;                             // query rows of a lane
+  // bf16 queries: o stays in the tensor cores' accumulators (see values)
+  static constexpr bool kDirect = B;
+  static constexpr int kOW = kDirect ? 4 : 2 * kNR;             // numbers of o of an n-tile
   // operands of Q kept per k-step (see load_q), and of P
   static constexpr int kQP = kF32 ? 1 : k8 ? (R == 8 || B ? 1 : 2) : B ? 1 : R == 8 ? 2 : 3;
   static constexpr int kPP = kF32 ? 1 : k8 ? (R == 8 || B ? 1 : 2) : R == 8 ? (B ? 1 : 2) : (B ? 2 : 3);
-  static constexpr int kQBytes = (kF32 ? kKS / 2 : kKS * kQP) * 512;
+  // (the third parts of R = 8 leave half of their operand zero, which is not stored)
+  static constexpr bool kHalfQ = !kF32 && !k8 && R == 8 && !B;
+  static constexpr int kQBytes = kF32 ? kKS / 2 * 512 : kHalfQ ? kKS * 768 : kKS * kQP * 512;
   static constexpr int kScales = k8 ? kKT * 4 : 0;              // bytes of an entry's scales
   // The ring's entries hold K and V in turn.  Three are least (one in use, two in
   // flight); a fourth is taken where it costs no warp.  Warps are worth more than a longer
@@ -157,6 +162,14 @@ __device__ __forceinline__ void mma_k8(float (&d)[4], uint32_t a0, uint32_t a1, 
       : "r"(a0), "r"(a1), "r"(b0));
 }
 
+// (x, y) += (a, b), one instruction.
+__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
+      "add.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+
 // f32 as a tf32 high part (cut) and the rest, rounded to tf32's 11 bits: 2^-21 of x
 // is lost at most.
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
@@ -231,7 +244,7 @@ struct Worker {
   };
 
   // ---- state of the piece at hand
-  float o[C::kNJ][4];
+  float o[C::kNJ][C::kOW];       // columns 2 c, + 1 of row g, then of row g + 8 (R = 8: its second parts)
   float m_run[C::kNR], n_run[C::kNR], l_part[C::kNR], vfac[C::kNR], sfac[C::kNR];
   bool clamp;                    // some V scale is beyond kRoom
 
@@ -386,8 +399,12 @@ struct Worker {
             split_bf16(x[i].z, x[i].w, hi[1], mid[1], lo[1]);
           }
           if constexpr (R == 8) {
-            to[0] = make_uint4(hi[0], mid[0], hi[1], mid[1]);
-            if constexpr (C::kQP == 2) to[32] = make_uint4(lo[0], 0u, lo[1], 0u);
+            if constexpr (C::kHalfQ) {
+              out[32 * i] = make_uint4(hi[0], mid[0], hi[1], mid[1]);
+              reinterpret_cast<uint2*>(qf + C::kKS * 512)[32 * i + lane] = make_uint2(lo[0], lo[1]);
+            } else {
+              to[0] = make_uint4(hi[0], mid[0], hi[1], mid[1]);
+            }
           } else {
             uint32_t* w = reinterpret_cast<uint32_t*>(to) + r;
             w[0] = hi[0];
@@ -424,7 +441,7 @@ struct Worker {
 #pragma unroll
     for (int j = 0; j < C::kNJ; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
+      for (int e = 0; e < C::kOW; ++e) o[j][e] = 0.f;
   }
 
   // S = Q K^T of the tile in entry e: acc[nt][i] (row g: keys 8 nt + 2 c, + 1; then row g +
@@ -459,10 +476,14 @@ struct Worker {
           if (s == 0) qr = q[32 * l];
           split_tf32(__uint_as_float(s ? qr.z : qr.x), q0.x, q0.y);
           split_tf32(__uint_as_float(s ? qr.w : qr.y), q0.z, q0.w);
+        } else if constexpr (C::kHalfQ) {
+          q0 = q[32 * (l * C::kKPC + s)];
+          const uint2 low = reinterpret_cast<const uint2*>(qf + C::kKS * 512)[32 * (l * C::kKPC + s) + lane];
+          q1 = make_uint4(low.x, 0u, low.y, 0u);
         } else {
           q0 = at[0];
         }
-        if constexpr (C::kQP >= 2) q1 = at[32];
+        if constexpr (C::kQP >= 2 && !C::kHalfQ) q1 = at[32];
         if constexpr (C::kQP >= 3) q2 = at[64];
 #pragma unroll
         for (int n = 0; n < C::kNT; ++n) {
@@ -505,7 +526,7 @@ struct Worker {
     const float* vs = sc + e * C::kKT;
     constexpr uint32_t kAll = C::kKT == 32 ? 0xFFFFFFFFu : (1u << (C::kKT & 31)) - 1u;
     float most = -INFINITY;
-    if constexpr (R == 8) {
+    if constexpr (R == 8 && !B) {
 #pragma unroll
       for (int n = 0; n < C::kNT; ++n) {                     // the remainders' row joins its own
         acc[n][0] += acc[n][2];
@@ -585,7 +606,7 @@ struct Worker {
 #pragma unroll
         for (int j = 0; j < C::kNJ; ++j)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < C::kOW; ++i)
             if (R == 8 || i / 2 == r) o[j][i] *= beta;
 #pragma unroll
         for (int n = 0; n < C::kNT; ++n) {
@@ -610,116 +631,148 @@ struct Worker {
 
   // o += P V.  V's rows too go to the MMA as they lie: n index of n-tile kEP s + i stands
   // for channel 8 kEP s + kEP n + i.
+  // f32 queries: a tile's products are summed by the tensor cores from zero and added to
+  // o by rounding additions.  The tensor cores cut a sum to 24 bits, so that an o that runs
+  // through them loses 2^-25 of itself on average at every step, always towards zero: 1.4e-5 over 64
+  // sequences of 4096 to 32768 keys (6e-7 with the additions, which cost up to 7 %
+  // over 8 bits).  With bf16 queries o does run through them: n steps of one warp (16
+  // keys each) make n 2^-26, an eighth of the output's half step after 500,000 keys.
   __device__ __forceinline__ void values(int e, const float (&p)[C::kNT][2 * C::kNR]) {
+    // k-steps summed together (those of o one by one: fewer registers at a time)
+    constexpr int kK = C::kDirect ? 1 : C::kKT / C::kKK;
     const unsigned char* vt = ring + e * C::kEntry;
     const float* vs = sc + e * C::kKT;
 #pragma unroll
-    for (int kt = 0; kt < C::kKT / C::kKK; ++kt) {
-      uint4 pa[C::kPP];
-      if constexpr (C::kF32) {
-        split_tf32(p[kt][0], pa[0].x, pa[0].y);
-        split_tf32(p[kt][1], pa[0].z, pa[0].w);
-      } else {
-        constexpr int kX = C::kKK / 8;
-        uint32_t hi[C::kNR][2] = {}, mid[C::kNR][2] = {}, lo[C::kNR][2] = {};
+    for (int k0 = 0; k0 < C::kKT / C::kKK; k0 += kK) {
+      uint4 pa[kK][C::kPP];
 #pragma unroll
-        for (int x = 0; x < kX; ++x) {
-          const int n = kX * kt + x;
-          float2 vf = make_float2(1.f, 1.f);
-          if constexpr (C::k8) vf = *reinterpret_cast<const float2*>(vs + 8 * n + 2 * c);
+      for (int kt = 0; kt < kK; ++kt) {
+        if constexpr (C::kF32) {
+          split_tf32(p[k0 + kt][0], pa[kt][0].x, pa[kt][0].y);
+          split_tf32(p[k0 + kt][1], pa[kt][0].z, pa[kt][0].w);
+        } else {
+          constexpr int kX = C::kKK / 8;
+          uint32_t hi[C::kNR][2] = {}, mid[C::kNR][2] = {}, lo[C::kNR][2] = {};
 #pragma unroll
-          for (int r = 0; r < C::kNR; ++r) {
-            float p0 = p[n][2 * r], p1 = p[n][2 * r + 1];
-            if constexpr (C::k8) {
-              float f0 = vf.x * vfac[r], f1 = vf.y * vfac[r];
-              if (clamp) {
-                // (numbers: a page far above the others' scales may pass f32's range where its keys'
-                // P is 0)
-                f0 = fminf(fmaxf(f0, -FLT_MAX), FLT_MAX);
-                f1 = fminf(fmaxf(f1, -FLT_MAX), FLT_MAX);
+          for (int x = 0; x < kX; ++x) {
+            const int n = kX * (k0 + kt) + x;
+            float2 vf = make_float2(1.f, 1.f);
+            if constexpr (C::k8) vf = *reinterpret_cast<const float2*>(vs + 8 * n + 2 * c);
+#pragma unroll
+            for (int r = 0; r < C::kNR; ++r) {
+              float p0 = p[n][2 * r], p1 = p[n][2 * r + 1];
+              if constexpr (C::k8) {
+                float f0 = vf.x * vfac[r], f1 = vf.y * vfac[r];
+                if (clamp) {
+                  // (numbers: a page far above the others' scales may pass f32's range where its keys'
+                  // P is 0)
+                  f0 = fminf(fmaxf(f0, -FLT_MAX), FLT_MAX);
+                  f1 = fminf(fmaxf(f1, -FLT_MAX), FLT_MAX);
+                }
+                if constexpr (B)
+                  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(hi[r][x]) : "f"(p1 * f1), "f"(p0 * f0));
+                else
+                  split_f16(p0 * f0, p1 * f1, hi[r][x], mid[r][x]);
+              } else {
+                split_bf16(p0, p1, hi[r][x], mid[r][x], lo[r][x]);
               }
-              split_f16(p0 * f0, p1 * f1, hi[r][x], mid[r][x]);
-            } else {
-              split_bf16(p0, p1, hi[r][x], mid[r][x], lo[r][x]);
             }
           }
-        }
-        // bf16 queries over 8 bits with R = 16: one f16 part (2^-12 of P, an eighth of the output's
-        // step); over bf16 two parts (16 bits)
-        if constexpr (R == 8) {
-          pa[0] = make_uint4(hi[0][0], mid[0][0], hi[0][1], mid[0][1]);
-          if constexpr (C::kPP == 2) pa[1] = make_uint4(lo[0][0], 0u, lo[0][1], 0u);
-        } else {
-          pa[0] = make_uint4(hi[0][0], hi[1][0], hi[0][1], hi[1][1]);
-          if constexpr (C::kPP >= 2) pa[1] = make_uint4(mid[0][0], mid[1][0], mid[0][1], mid[1][1]);
-          if constexpr (C::kPP >= 3) pa[2] = make_uint4(lo[0][0], lo[1][0], lo[0][1], lo[1][1]);
+          // bf16 queries over 8 bits: one f16 part (2^-12 of P, an eighth of the output's half
+          // step); over bf16 two parts (16 bits)
+          if constexpr (R == 8) {
+            pa[kt][0] = make_uint4(hi[0][0], mid[0][0], hi[0][1], mid[0][1]);
+            if constexpr (C::kPP == 2) pa[kt][1] = make_uint4(lo[0][0], 0u, lo[0][1], 0u);
+          } else {
+            pa[kt][0] = make_uint4(hi[0][0], hi[1][0], hi[0][1], hi[1][1]);
+            if constexpr (C::kPP >= 2) pa[kt][1] = make_uint4(mid[0][0], mid[1][0], mid[0][1], mid[1][1]);
+            if constexpr (C::kPP >= 3) pa[kt][2] = make_uint4(lo[0][0], lo[1][0], lo[0][1], lo[1][1]);
+          }
         }
       }
+      // rows of V that a lane reads per k-step
+      constexpr int kVR = C::kKK == 16 ? 4 : 2;
+      constexpr int kWords = C::kVP / 4;
 #pragma unroll
       for (int s = 0; s < C::kNS; ++s) {
-        auto read = [&](int row, uint32_t (&w)[4]) {
-          const int sw = C::kNCH >= 8 ? row & 7 : (row >> 1) & 3;
-          if constexpr (C::kVP == 16) {
-            const uint4 u = *reinterpret_cast<const uint4*>(vt + row * C::kRow + (((8 * s + g) ^ sw) << 4));
-            w[0] = u.x;
-            w[1] = u.y;
-            w[2] = u.z;
-            w[3] = u.w;
-          } else {
-            const uint2 u = *reinterpret_cast<const uint2*>(vt + row * C::kRow + (((g >> 1) ^ sw) << 4) +
-                                                            8 * (g & 1));
-            w[0] = u.x;
-            w[1] = u.y;
-            w[2] = w[3] = 0u;
-          }
-        };
-        uint32_t y0[4], y1[4];
-        read(C::kKK * kt + 2 * c, y0);
-        read(C::kKK * kt + 2 * c + 1, y1);
-        if constexpr (C::kF32) {
+        uint32_t y[kK][kVR][kWords];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t h0, l0, h1, l1;
-            split_tf32(__uint_as_float(y0[i]), h0, l0);
-            split_tf32(__uint_as_float(y1[i]), h1, l1);
-            mma<T>(o[4 * s + i], pa[0], h0, h1);
-            mma<T>(o[4 * s + i], pa[0], l0, l1);
-          }
-        } else if constexpr (C::kKK == 8) {
+        for (int kt = 0; kt < kK; ++kt)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t b0 = __byte_perm(y0[q], y1[q], 0x5410), b1 = __byte_perm(y0[q], y1[q], 0x7632);
-#pragma unroll
-            for (int x = 0; x < C::kPP; ++x) {
-              mma_k8(o[C::kEP * s + 2 * q], pa[x].x, pa[x].y, b0);
-              mma_k8(o[C::kEP * s + 2 * q + 1], pa[x].x, pa[x].y, b1);
-            }
-          }
-        } else {
-          uint32_t y2[4], y3[4];
-          read(16 * kt + 2 * c + 8, y2);
-          read(16 * kt + 2 * c + 9, y3);
-#pragma unroll
-          for (int q = 0; q < C::kVP / 4; ++q) {
-            constexpr int kPer = C::k8 ? 4 : 2;              // channels of a word
-            uint32_t b[kPer][2];
-            if constexpr (C::k8) {
-              constexpr bool kI8 = T == SA_DTYPE_INT8;
-              codes4_to_f16<kI8>(__byte_perm(y0[q], y1[q], 0x5140), b[0][0], b[1][0]);
-              codes4_to_f16<kI8>(__byte_perm(y0[q], y1[q], 0x7362), b[2][0], b[3][0]);
-              codes4_to_f16<kI8>(__byte_perm(y2[q], y3[q], 0x5140), b[0][1], b[1][1]);
-              codes4_to_f16<kI8>(__byte_perm(y2[q], y3[q], 0x7362), b[2][1], b[3][1]);
+          for (int x = 0; x < kVR; ++x) {
+            const int row = C::kKK * (k0 + kt) + 2 * c + (x & 1) + 8 * (x >> 1);
+            const int sw = C::kNCH >= 8 ? row & 7 : (row >> 1) & 3;
+            if constexpr (C::kVP == 16) {
+              const uint4 u = *reinterpret_cast<const uint4*>(vt + row * C::kRow + (((8 * s + g) ^ sw) << 4));
+              y[kt][x][0] = u.x;
+              y[kt][x][1] = u.y;
+              y[kt][x][2] = u.z;
+              y[kt][x][3] = u.w;
             } else {
-              b[0][0] = __byte_perm(y0[q], y1[q], 0x5410);
-              b[1][0] = __byte_perm(y0[q], y1[q], 0x7632);
-              b[0][1] = __byte_perm(y2[q], y3[q], 0x5410);
-              b[1][1] = __byte_perm(y2[q], y3[q], 0x7632);
+              const uint2 u = *reinterpret_cast<const uint2*>(vt + row * C::kRow + (((g >> 1) ^ sw) << 4) +
+                                                              8 * (g & 1));
+              y[kt][x][0] = u.x;
+              y[kt][x][1] = u.y;
             }
+          }
 #pragma unroll
-            for (int i = 0; i < kPer; ++i)
+        for (int q = 0; q < kWords; ++q) {
+          constexpr int kPer = C::k8 ? 4 : C::kF32 ? 1 : 2;      // channels of a word
+          float sum[kPer][4];
 #pragma unroll
-              for (int x = 0; x < C::kPP; ++x)
-                mma<T>(o[C::kEP * s + kPer * q + i], pa[x], b[i][0], b[i][1]);
+          for (int i = 0; i < kPer; ++i)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              sum[i][x] = C::kDirect ? o[C::kEP * s + kPer * q + i][x % C::kOW] : 0.f;
+#pragma unroll
+          for (int kt = 0; kt < kK; ++kt) {
+            const auto& v = y[kt];
+            if constexpr (C::kF32) {
+              uint32_t h0, l0, h1, l1;
+              split_tf32(__uint_as_float(v[0][q]), h0, l0);
+              split_tf32(__uint_as_float(v[1][q]), h1, l1);
+              mma<T>(sum[0], pa[kt][0], l0, l1);
+              mma<T>(sum[0], pa[kt][0], h0, h1);
+            } else {
+              uint32_t b[kPer][2];
+              if constexpr (C::k8) {
+                constexpr bool kI8 = T == SA_DTYPE_INT8;
+                codes4_to_f16<kI8>(__byte_perm(v[0][q], v[1][q], 0x5140), b[0][0], b[1][0]);
+                codes4_to_f16<kI8>(__byte_perm(v[0][q], v[1][q], 0x7362), b[2][0], b[3][0]);
+                codes4_to_f16<kI8>(__byte_perm(v[2][q], v[3][q], 0x5140), b[0][1], b[1][1]);
+                codes4_to_f16<kI8>(__byte_perm(v[2][q], v[3][q], 0x7362), b[2][1], b[3][1]);
+              } else {
+                b[0][0] = __byte_perm(v[0][q], v[1][q], 0x5410);
+                b[1][0] = __byte_perm(v[0][q], v[1][q], 0x7632);
+                if constexpr (kVR == 4) {
+                  b[0][1] = __byte_perm(v[2][q], v[3][q], 0x5410);
+                  b[1][1] = __byte_perm(v[2][q], v[3][q], 0x7632);
+                }
+              }
+#pragma unroll
+              for (int x = C::kPP - 1; x >= 0; --x)              // (small parts first)
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                  if constexpr (C::kKK == 8)
+                    mma_k8(sum[i], pa[kt][x].x, pa[kt][x].y, b[i][0]);
+                  else
+                    mma<T>(sum[i], pa[kt][x], b[i][0], b[i][1]);
+                }
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            const int j = C::kEP * s + kPer * q + i;
+            if constexpr (C::kDirect) {
+#pragma unroll
+              for (int x = 0; x < 4; ++x) o[j][x] = sum[i][x];
+            } else if constexpr (R == 8) {                       // the remainders' row joins its own
+              add2(sum[i][0], sum[i][1], sum[i][2], sum[i][3]);
+              add2(o[j][0], o[j][1], sum[i][0], sum[i][1]);
+            } else {
+              add2(o[j][0], o[j][1], sum[i][0], sum[i][1]);
+              add2(o[j][2], o[j][3], sum[i][2], sum[i][3]);
+            }
           }
         }
       }
@@ -727,7 +780,7 @@ struct Worker {
   }
 
   __device__ __forceinline__ float at(int j, int r, int e) const {
-    return R == 8 ? o[j][e] + o[j][e + 2] : o[j][2 * r + e];
+    return C::kDirect && R == 8 ? o[j][e] + o[j][C::kOW - 2 + e] : o[j][2 * r + e];
   }
   __device__ __forceinline__ float row_sum(int r) const {
     float l = l_part[r];
@@ -1230,13 +1283,10 @@ template <int T, int DP>
 cudaError_t launch_dim(const DecodeArgs& a, int r, cudaStream_t s) {
   if constexpr (T == SA_DTYPE_F32) {
     return launch<T, DP, 8, false>(a, s);
-  } else if constexpr (T == SA_DTYPE_BF16) {
-    if (r == 8) return a.act_bf16 ? launch<T, DP, 8, true>(a, s) : launch<T, DP, 8, false>(a, s);
   } else {
-    if (r == 8) return launch<T, DP, 8, false>(a, s);
-  }
-  if constexpr (T != SA_DTYPE_F32)
+    if (r == 8) return a.act_bf16 ? launch<T, DP, 8, true>(a, s) : launch<T, DP, 8, false>(a, s);
     return a.act_bf16 ? launch<T, DP, 16, true>(a, s) : launch<T, DP, 16, false>(a, s);
+  }
 }
 
 template <int T>

@@ -303,3 +303,39 @@ def test_refusals():
     no(TypeError, workspace=torch.empty(800, device="cuda"))
     out, lse = sa.sa_decode_attention(q[:0], *c.pages, c.table[:0], c.used[:0], 0.1, **c.kw())
     assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_long_sums_do_not_drift(kind):
+    """Sums over many tiles by one warp: 256 sequences of 65536 keys that share their pages, all
+    values near 1, so that a sum which is cut at every step (2^-25 of it on average) shows as an output
+    below the true one.  A warp adds 256 * 2 * 65536 / (1824 * 32) = 575 tiles or more of 32 keys:
+    cut, they would leave 575 2^-26 = 9e-6 missing (16 keys a tile: 1.7e-5).  What may be
+    missing: a tile's own products are cut at most 3 times, 3 2^-24 = 2e-7; rounding
+    errors of the additions have no sign, at most half a step each, and their mean over 4096 x 64
+    outputs vanishes beside it.  ex2 is off by 2^-22 in numerator and denominator alike.  1e-6."""
+    batch, hkv, g, n, d, ps = 256, 2, 2, 65536, 64, 64
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    shape = (n // ps, hkv, ps, d)
+    k = torch.randn(shape, generator=gen, device="cuda")
+    v = 1 + 0.05 * torch.randn(shape, generator=gen, device="cuda")
+    kw = {}
+    if kind in ("e4m3", "int8"):
+        k, v = (k * 30).to(TORCH[kind]), (v * 64).to(TORCH[kind])
+        s = torch.full((n // ps, hkv), 2.0 ** -6, device="cuda")
+        kw = dict(k_scales=s, v_scales=s)
+    else:
+        k, v = k.to(TORCH[kind]), v.to(TORCH[kind])
+    kx, vx = (x.float().double() * (2.0 ** -6 if kw else 1) for x in (k, v))
+    table = torch.arange(n // ps, dtype=torch.int32, device="cuda").repeat(batch, 1)
+    q = torch.randn((batch, hkv * g, d), generator=gen, device="cuda")
+    out, lse = sa.sa_decode_attention(q, k, v, table, torch.full((batch,), n, dtype=torch.int32, device="cuda"),
+                                      0.125, **kw)
+    for h in range(hkv):
+        keys, vals = (x[:, h].reshape(n, d) for x in (kx, vx))
+        x = q[:, h * g:(h + 1) * g].double().reshape(-1, d) @ keys.T * 0.125
+        ref = torch.softmax(x, 1) @ vals
+        got = out[:, h * g:(h + 1) * g].double().reshape(-1, d)
+        assert abs(float(((got - ref) / ref).mean())) <= 1e-6
+        # (rounding: 575 additions of half a step, 2^-25, at random: 24 2^-25, six of them)
+        assert float(((got - ref).norm() / ref.norm())) <= 6 * 24 * 2.0 ** -25
