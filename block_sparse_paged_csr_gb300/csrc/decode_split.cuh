@@ -69,8 +69,8 @@ struct Cfg {
   static constexpr int kNS = DP / (8 * kEP);                    // .. times
   static constexpr int kNJ = DP / 8;                            // n-tiles of o
   static constexpr int kNR = R / 8;                             // query rows of a lane
-  // bf16 queries: o stays in the tensor cores' accumulators (see values)
-  static constexpr bool kDirect = B;
+  // bf16 queries over 8 bits: o stays in the tensor cores' accumulators (see values)
+  static constexpr bool kDirect = B && k8;
   static constexpr int kOW = kDirect ? 4 : 2 * kNR;             // numbers of o of an n-tile
   // operands of Q kept per k-step (see load_q), and of P
   static constexpr int kQP = kF32 ? 1 : k8 ? (R == 8 || B ? 1 : 2) : B ? 1 : R == 8 ? 2 : 3;
@@ -79,24 +79,20 @@ struct Cfg {
   static constexpr bool kHalfQ = !kF32 && !k8 && R == 8 && !B;
   static constexpr int kQBytes = kF32 ? kKS / 2 * 512 : kHalfQ ? kKS * 768 : kKS * kQP * 512;
   static constexpr int kScales = k8 ? kKT * 4 : 0;              // bytes of an entry's scales
-  // The ring's entries hold K and V in turn.  Three are least (one in use, two in
-  // flight); a fourth is taken where it costs no warp.  Warps are worth more than a longer
-  // ring (e4m3, 64 sequences of 20000 to 50000 keys: 12 warps of 3 entries 760 us, 8 of 4
-  // 830), since an instruction's latency shows with 2 of them on a scheduler; their
-  // number is a multiple of 4, as their ranges are equal and the four schedulers share
-  // them (10 warps of 4 entries: 1130 us).
-  static constexpr int warp_bytes(int ne) {
-    return ne * (kEntry + kScales) + kQBytes + kInfos * 16;
-  }
-  static constexpr int warps_of(int ne) {
-    return kMost / warp_bytes(ne) / 4 * 4 < decode_max_warps(DP, R)
-               ? kMost / warp_bytes(ne) / 4 * 4
-               : decode_max_warps(DP, R);
-  }
-  static constexpr int kMost = 220 * 1024;                       // (of 227 KB, some of them static)
-  static constexpr int kNE = warps_of(4) == warps_of(3) ? 4 : 3;
-  static constexpr int kPerWarp = warp_bytes(kNE);
-  static constexpr int kW = warps_of(kNE);                      // warps
+  // The ring's entries hold K and V in turn: one in use, two in flight.  (A fourth costs
+  // warps, and where it costs none it gains nothing: bf16, 32 sequences of 20000 to 50000 keys, 8
+  // warps: 719 us with three, 736 with four.)
+  static constexpr int kNE = 3;
+  static constexpr int kPerWarp = kNE * (kEntry + kScales) + kQBytes + kInfos * 16;
+  static constexpr int kMost = 220 * 1024;                      // (of 227 KB, some of them static)
+  // Warps hide the instructions' latencies from each other (e4m3, 64 sequences: 12 warps 735
+  // us, 8 warps 830).  Their number is a multiple of 4, as their ranges are equal and
+  // the four schedulers share them (10 warps: 1130 us).  bf16 keys under bf16
+  // queries ask for few instructions; there more copies at a time only cost (12 warps 750 us, 8
+  // 719: 6.8 TB/s).
+  static constexpr int kWarpsMost = T == SA_DTYPE_BF16 && B ? 8 : decode_max_warps(DP, R);
+  static constexpr int kWarpsSmem = kMost / kPerWarp / 4 * 4;
+  static constexpr int kW = kWarpsSmem < kWarpsMost ? kWarpsSmem : kWarpsMost;      // warps
   static constexpr int kThreads = 32 * kW;
   static constexpr int kSmem = kW * kPerWarp;
   // a state: o in the order of the accumulators, then m, n and l of each row
@@ -254,8 +250,9 @@ struct Worker {
     first = k.first;
     end = k.end;
     nt = tiles_of<C::kKT>(k);
-    h = static_cast<int>(divide(in_seq, static_cast<unsigned>(nt)));
-    t = static_cast<int>(in_seq - static_cast<int64_t>(h) * nt);
+    h = static_cast<int>(min(divide(in_seq, static_cast<unsigned>(nt)),
+                             static_cast<int64_t>(a.items_per_seq - 1)));
+    t = min(static_cast<int>(in_seq - static_cast<int64_t>(h) * nt), nt - 1);
     next_used = b + 1 < a.batch ? a.used[b + 1] : 0;
   }
 
@@ -283,6 +280,8 @@ struct Worker {
           end = k.end;
           nt = tiles_of<C::kKT>(k);
           if (b + 1 < a.batch) next_used = a.used[b + 1];
+        } else {
+          b = a.batch - 1;         // (only if the lengths change under the call: stay in bounds)
         }
       }
     }
@@ -631,12 +630,13 @@ struct Worker {
 
   // o += P V.  V's rows too go to the MMA as they lie: n index of n-tile kEP s + i stands
   // for channel 8 kEP s + kEP n + i.
-  // f32 queries: a tile's products are summed by the tensor cores from zero and added to
-  // o by rounding additions.  The tensor cores cut a sum to 24 bits, so that an o that runs
-  // through them loses 2^-25 of itself on average at every step, always towards zero: 1.4e-5 over 64
-  // sequences of 4096 to 32768 keys (6e-7 with the additions, which cost up to 7 %
-  // over 8 bits).  With bf16 queries o does run through them: n steps of one warp (16
-  // keys each) make n 2^-26, an eighth of the output's half step after 500,000 keys.
+  // A tile's products are summed by the tensor cores from zero and added to o by rounding
+  // additions.  The tensor cores cut a sum to 24 bits, so that an o that runs through
+  // them loses 2^-25 of itself on average at every step, always towards zero: 1.4e-5 over 64
+  // sequences of 4096 to 32768 bf16 keys (6e-7 with the additions).  Over 8 bits, where
+  // instructions count, the additions cost 7 %; bf16 queries do without: n steps of
+  // one warp (16 keys each) make n 2^-26, a quarter of the output's half step after
+  // 500,000 keys.
   __device__ __forceinline__ void values(int e, const float (&p)[C::kNT][2 * C::kNR]) {
     // k-steps summed together (those of o one by one: fewer registers at a time)
     constexpr int kK = C::kDirect ? 1 : C::kKT / C::kKK;
@@ -921,9 +921,11 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
   if (t0 < t1) {
     int k = 0;
 #pragma unroll 1
-    for (; in_seq >= s_chunk[k] * a.items_per_seq; ++k) in_seq -= s_chunk[k] * a.items_per_seq;
+    for (; in_seq >= s_chunk[k] * a.items_per_seq; ++k) in_seq -= s_chunk[k] * a.items_per_seq;   // (t0 < total)
+    // (lengths that change under the call may leave it without an answer: then the last sequence's)
+    b0 = a.batch - 1;
 #pragma unroll 1
-    for (int i = k * per_chunk;; i += 32) {
+    for (int i = k * per_chunk; i < a.batch; i += 32) {
       const unsigned n = tiles_at(i + lane, a.batch);
       const int64_t all = static_cast<int64_t>(__reduce_add_sync(0xffffffffu, n)) * a.items_per_seq;
       if (in_seq < all) {
@@ -995,12 +997,10 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
       ++next_v;
       end_group();
     };
-#pragma unroll
-    for (int i = 0; i < C::kNE; ++i)
-      if (i & 1)
-        issue_v();
-      else
-        issue_k();
+    static_assert(C::kNE == 3, "a V follows a K's place");
+    issue_k();
+    issue_v();
+    issue_k();
     // (Q of the first piece came beside the first copies)
     w.keep_q(q);
     w.begin();
@@ -1025,7 +1025,7 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
       float2 kf[C::kNT];
       if (inf.y) w.scores(e, acc, kf);
       __syncwarp();
-      if constexpr (C::kNE & 1) issue_v(); else issue_k();
+      issue_v();
       if (++e == C::kNE) e = 0;
       copies_wait<C::kNE - 1>();
       __syncwarp();
@@ -1034,7 +1034,7 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
         w.values(e, p);
       }
       __syncwarp();
-      if constexpr (C::kNE & 1) issue_k(); else issue_v();
+      issue_k();
       if (++e == C::kNE) e = 0;
       if (flags & 2u) {
         if (started) {
