@@ -1179,7 +1179,8 @@ def sa_decode_attention(q, k_pages, v_pages, block_tables, used_kv_lens, softmax
     """One new token per sequence over its whole cache: query b of ``q`` [batch, hq, d]
     (float32 or bfloat16) attends over the positions below ``used_kv_lens[b]``, the
     last ``window`` of them where that is not 0.  Any cache type (with ``k_scales`` and
-    ``v_scales`` for 8 bits) and any hq / hkv.  Returns (out, lse): out of q's type, lse
+    ``v_scales`` for 8 bits) and any hq / hkv.  ``workspace``: see
+    :func:`allocate_decode_workspace`; calls that overlap need one each.  Returns (out, lse): out of q's type, lse
     [batch, hq] float32; a sequence of length 0 gets 0 and -inf."""
     code = _pool(k_pages, v_pages, k_scales, v_scales)
     dev = k_pages.device
@@ -1212,9 +1213,11 @@ def sa_decode_attention(q, k_pages, v_pages, block_tables, used_kv_lens, softmax
             if workspace is None:
                 workspace = allocate_decode_workspace(batch, hq, hkv, d, dev)
     _require(workspace, torch.uint8, "workspace", dev)
-    base = workspace.data_ptr()
+    base, at = workspace.data_ptr(), q.data_ptr()
     aligned = (base + 255) & ~255
-    _check(_on(dev, _native.load().sa_decode_attention, q.data_ptr(), act, k_pages.data_ptr(),
+    if at == out.data_ptr() and batch:
+        raise ValueError("out must not be q")
+    _check(_on(dev, _native.load().sa_decode_attention, at, act, k_pages.data_ptr(),
                v_pages.data_ptr(), _ptr(k_scales), _ptr(v_scales), num_pages, code,
                block_tables.data_ptr(), block_tables.shape[1], used_kv_lens.data_ptr(), batch, hq,
                hkv, d, page_size, softmax_scale, window, out.data_ptr(), _ptr(lse), aligned,

@@ -56,6 +56,7 @@ struct Cfg {
   static constexpr int kRow = DP * kSize;                       // bytes of a row in the ring
   // keys of a tile: 4 KB of K where that is 8 to 32 keys
   static constexpr int kKT = 4096 / kRow < 8 ? 8 : 4096 / kRow > 32 ? 32 : 4096 / kRow;
+  static constexpr int kRun = kKT < 16 ? kKT : 16;              // rows that mostly lie in one page
   static constexpr int kEntry = kKT * kRow;                     // bytes of a tile's K (or V)
   static constexpr int kNCH = kRow / 16;                        // 16-byte chunks of a row
   static constexpr int kLCH = kNCH / 4;                         // chunks of a row that a lane reads for S
@@ -85,14 +86,17 @@ struct Cfg {
   static constexpr int kNE = 3;
   static constexpr int kPerWarp = kNE * (kEntry + kScales) + kQBytes + kInfos * 16;
   static constexpr int kMost = 220 * 1024;                      // (of 227 KB, some of them static)
-  // Warps hide the instructions' latencies from each other (e4m3, 64 sequences: 12 warps 735
-  // us, 8 warps 830).  Their number is a multiple of 4, as their ranges are equal and
-  // the four schedulers share them (10 warps: 1130 us).  bf16 keys under bf16
-  // queries ask for few instructions; there more copies at a time only cost (12 warps 750 us, 8
-  // 719: 6.8 TB/s).
-  static constexpr int kWarpsMost = T == SA_DTYPE_BF16 && B ? 8 : decode_max_warps(DP, R);
+  // Warps hide the instructions' latencies from each other (int8, 32 sequences of 20000 to
+  // 50000 keys: 12 warps 392 us, 8 warps 430; e4m3 with heads of 64: 16 warps 408, 12 454, 8 555).
+  // Their number is a multiple of 4, as their ranges are equal and the four schedulers
+  // share them (10 warps instead of 12: 1130 instead of 750 us).  bf16 keys ask for
+  // few instructions; there more copies at a time only cost (12 warps 757 us, 8 719).
+  static constexpr int kWarpsMost = T == SA_DTYPE_BF16 ? 8 : decode_max_warps(DP, R);
   static constexpr int kWarpsSmem = kMost / kPerWarp / 4 * 4;
   static constexpr int kW = kWarpsSmem < kWarpsMost ? kWarpsSmem : kWarpsMost;      // warps
+  // An SM does best with some 64 KB in flight.  Where two entries a warp would be more, V's copies
+  // wait until the tile before is done with (e4m3, 64 sequences, 12 warps: 736 us, at once 761).
+  static constexpr bool kLate = 2 * kW * kEntry > 64 * 1024;
   static constexpr int kThreads = 32 * kW;
   static constexpr int kSmem = kW * kPerWarp;
   // a state: o in the order of the accumulators, then m, n and l of each row
@@ -118,6 +122,9 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there
   const int n = there ? 16 : 0;
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
                : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool there) {
   const int n = there ? 4 : 0;
@@ -234,9 +241,10 @@ struct Worker {
 
   // ---- the tile to come: where it lies
   int b, h, t, nt, first, end, next_used;     // cursor
+  bool runs;                     // pages hold whole runs of kRun rows, and rows are not padded
   struct Pend {
     int pid, row, h, item;
-    uint32_t flags;              // 1: the pair's first tile, 2: its last
+    uint32_t flags;              // 1: the pair's first tile, 2: its last, 4: runs of rows lie in a page
   };
 
   // ---- state of the piece at hand
@@ -269,7 +277,7 @@ struct Worker {
     }
     p.h = a.groups == 1 ? h : h / a.groups;
     p.item = b * a.items_per_seq + h;
-    p.flags = (t == 0 ? 1u : 0u) | (t + 1 == nt ? 2u : 0u);
+    p.flags = (t == 0 ? 1u : 0u) | (t + 1 == nt ? 2u : 0u) | (runs && first % C::kRun == 0 ? 4u : 0u);
     if (++t == nt) {
       t = 0;
       if (++h == a.items_per_seq) {
@@ -290,14 +298,37 @@ struct Worker {
 
   // Copies of one tile's K (kV false) or V rows into entry e; row: the lane's (key
   // `lane`) row of the pool, kNone where there is none (the pools have fewer rows).
+  // whole: all rows are there, and every kRun of them lie side by side, so that one address serves
+  // a run (a tenth of a tile's instructions less).
   static constexpr uint32_t kNone = 0xFFFFFFFFu;
   template <bool kV>
-  __device__ __forceinline__ void copy_rows(int e, uint32_t row, uint32_t scale_at) {
+  __device__ __forceinline__ void copy_rows(int e, uint32_t row, uint32_t scale_at, bool whole) {
     const unsigned char* pool = static_cast<const unsigned char*>(kV ? a.v_pages : a.k_pages);
     const uint32_t d0 = smem_u32(ring + e * C::kEntry);
     // a lane copies chunk lane % kNCH (and + 32 ..) of rows that are 32 / kNCH apart
     constexpr int kPer = C::kNCH < 32 ? C::kNCH : 32;
     const int ch0 = lane & (kPer - 1);
+    if (whole) {
+      constexpr int kCopies = C::kRun * C::kNCH / 32;          // of a run
+#pragma unroll
+      for (int run = 0; run < C::kKT / C::kRun; ++run) {
+        const uint32_t at = __shfl_sync(0xffffffffu, row, run * C::kRun);
+        const unsigned char* src = pool + static_cast<uint64_t>(at) * C::kRow + 16 * lane;
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) {
+          const int j = run * kCopies + i;
+          const int r = C::kNCH <= 32 ? j * (32 / kPer) + lane / kPer : j / (C::kNCH / 32);
+          const int ch = C::kNCH <= 32 ? ch0 : ch0 + 32 * (j % (C::kNCH / 32));
+          const int phys = C::kNCH >= 8 ? ch ^ (r & 7) : ch ^ ((r >> 1) & 3);
+          copy16(d0 + r * C::kRow + phys * 16, src + 512 * i);
+        }
+      }
+      if constexpr (C::k8) {
+        if (C::kKT == 32 || lane < C::kKT)
+          copy4(smem_u32(sc + e * C::kKT + lane), (kV ? a.v_scales : a.k_scales) + scale_at, true);
+      }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < C::kKT * C::kNCH / 32; ++i) {
       const int r = C::kNCH <= 32 ? i * (32 / kPer) + lane / kPer : i / (C::kNCH / 32);
@@ -960,12 +991,14 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
   if (lane < 2) s_piece[2 * warp + lane] = {-1, 0, 0};
   __syncwarp();
   if (n > 0) {
+    w.runs = a.head_dim == DP && a.page_size % C::kRun == 0;
     w.seek(b0, in_seq);
     int item = b0 * a.items_per_seq + w.h;
     typename W::Rows q;
     w.fetch_q(item, q);
     typename W::Pend ahead = w.take();           // of the tile whose K is next to be copied
     uint32_t row = W::kNone, scale_at = 0;       // of the tile whose V is
+    bool whole = false;
     int next_k = 0, next_v = 0, ne = 0;          // tiles asked for so far; the entry for the next copies
     auto end_group = [&]() {                     // (also where nothing was left to copy)
       copies_commit();
@@ -984,14 +1017,16 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
             __ballot_sync(0xffffffffu, (C::kKT == 32 || lane < C::kKT) && row != W::kNone);
         if (lane == 0)
           w.info[next_k % kInfos] = make_uint4(static_cast<uint32_t>(ahead.item), mask, ahead.flags, 0u);
-        w.template copy_rows<false>(ne, row, scale_at);
+        constexpr uint32_t kAll = C::kKT == 32 ? 0xFFFFFFFFu : (1u << (C::kKT & 31)) - 1u;
+        whole = mask == kAll && (ahead.flags & 4u);
+        w.template copy_rows<false>(ne, row, scale_at, whole);
       }
       ++next_k;
       end_group();
     };
     auto issue_v = [&]() {
       if (next_v < n) {
-        w.template copy_rows<true>(ne, row, scale_at);
+        w.template copy_rows<true>(ne, row, scale_at, whole);
         if (next_k < n) ahead = w.take();
       }
       ++next_v;
@@ -1008,7 +1043,7 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
     bool started = false;          // the piece at hand holds its pair's first tile
     int e = 0;
     for (int i = 0; i < n; ++i) {
-      copies_wait<C::kNE - 1>();
+      copies_wait<2>();
       __syncwarp();
       const uint4 inf = w.info[i % kInfos];
       flags = inf.z;
@@ -1025,15 +1060,16 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
       float2 kf[C::kNT];
       if (inf.y) w.scores(e, acc, kf);
       __syncwarp();
-      issue_v();
+      if constexpr (!C::kLate) issue_v();
       if (++e == C::kNE) e = 0;
-      copies_wait<C::kNE - 1>();
+      copies_wait<C::kLate ? 1 : 2>();
       __syncwarp();
       if (inf.y) {
         w.softmax(e, inf.y, acc, kf, p);
         w.values(e, p);
       }
       __syncwarp();
+      if constexpr (C::kLate) issue_v();
       issue_k();
       if (++e == C::kNE) e = 0;
       if (flags & 2u) {

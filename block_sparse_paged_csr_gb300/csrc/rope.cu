@@ -19,7 +19,7 @@ namespace sa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 8;                 // tokens per CTA
+constexpr int kMaxTokens = 4;                 // tokens per CTA
 
 struct RopeArgs {
   const void* src[2];                         // q, k
@@ -418,8 +418,8 @@ extern "C" sa_status sa_norm_rope(
   a.dst_token_stride[1] = k_out_token_stride;
   a.dst_head_stride[0] = q_out_head_stride;
   a.dst_head_stride[1] = k_out_head_stride;
-  a.weight[0] = q_weight;
-  a.weight[1] = k_weight;
+  a.weight[0] = hq > 0 ? q_weight : nullptr;
+  a.weight[1] = hkv > 0 ? k_weight : nullptr;
   a.heads[0] = hq;
   a.heads[1] = hkv;
   a.weight_bf16 = weight_dtype == SA_DTYPE_BF16;

@@ -669,8 +669,9 @@ sa_status sa_select_blocks(const void *q, sa_dtype q_dtype, int64_t tq, int32_t 
  *   t = position(token, axis(i)) * inv_freq[i],  i < rot_dim / 2,
  *
  * with (a, b) = (i, i + rot_dim / 2), or (2 i, 2 i + 1) where `interleaved` is not 0;
- * channels from rot_dim on are not rotated.  Sums are f32, angles exact to 2^-31
- * turns at any 32-bit position, and each output is rounded once.
+ * channels from rot_dim on are not rotated.  Sums are f32 (a row with magnitudes
+ * beyond 1e18 overflows its sum of squares), angles exact to 2^-31 turns at any
+ * 32-bit position, and each output is rounded once.
  *
  *   q, k          [tq, hq, head_dim], [tq, hkv, head_dim] of src_dtype (f32 or
  *                 bf16); channels contiguous, tokens and heads at the given
@@ -753,7 +754,7 @@ sa_status sa_load_kv(const void *k_pages, const void *v_pages, const float *k_sc
  *                 h * hq / hkv .. of kv head h
  *   k_pages, v_pages, k_scales, v_scales, num_pages, kv_dtype, block_tables,
  *   max_pages     as for sa_store_kv; keys of pages with an id below 0 do not exist
- *   out           [batch, hq, head_dim] of q_dtype
+ *   out           [batch, hq, head_dim] of q_dtype, apart from q
  *   lse           [batch, hq] f32, or NULL
  *   workspace     device memory of sa_decode_workspace_size bytes, 16-byte
  *                 aligned; nothing is kept in it from call to call, and calls that
@@ -762,8 +763,11 @@ sa_status sa_load_kv(const void *k_pages, const void *v_pages, const float *k_sc
  *
  * Nothing that stands at other positions of the pages is read into a result
  * (infinities and NaN there do not matter); a key or value in sight that is not finite
- * makes its rows' results unspecified.  Results do not depend on timing: the
- * same call gives the same bits.
+ * makes its rows' results unspecified.  Scores, softmax sums and outputs are
+ * summed in f32.  f32 queries keep 22 bits or more of every operand; bf16 queries
+ * take P in 11 (8-bit caches) or 16 bits (bf16), below the output's rounding.
+ * Results do not depend on timing: the same call on the same GPU gives the same bits.
+ * Enqueues two kernels and allocates nothing.
  *
  * Checks, in order: HEAD_COUNT, HEAD_DIM, SHAPE (batch < 0), BLOCK_PAGE, SHAPE,
  * INVALID_ARGUMENT (types), UNSUPPORTED (head_dim not a multiple of 8, or 16 for the

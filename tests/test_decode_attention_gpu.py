@@ -301,6 +301,7 @@ def test_refusals():
     no(ValueError, lse=torch.empty(7, device="cuda"))
     no(sa.SAError, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
     no(TypeError, workspace=torch.empty(800, device="cuda"))
+    no(ValueError, out=q)
     out, lse = sa.sa_decode_attention(q[:0], *c.pages, c.table[:0], c.used[:0], 0.1, **c.kw())
     assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
 
@@ -339,3 +340,37 @@ def test_long_sums_do_not_drift(kind):
         assert abs(float(((got - ref) / ref).mean())) <= 1e-6
         # (rounding: 575 additions of half a step, 2^-25, at random: 24 2^-25, six of them)
         assert float(((got - ref).norm() / ref.norm())) <= 6 * 24 * 2.0 ** -25
+
+
+@pytest.mark.parametrize("kind,d", [("bf16", 128), ("f32", 64), ("int8", 256)])
+def test_pages_far_into_a_pool(kind, d):
+    """Pages whose bytes, and whose elements, lie beyond 2^32 from the pool's start."""
+    hkv, ps = 8, 64
+    per = hkv * ps * d
+    n = 2 ** 32 // per + 300
+    pools = [torch.zeros((n, hkv, ps, d), dtype=TORCH[kind], device="cuda") for _ in range(2)]
+    kw = {}
+    if kind == "int8":
+        scales = torch.full((n, hkv), 2.0 ** -5, device="cuda")
+        kw = dict(k_scales=scales, v_scales=scales)
+    ids = torch.tensor([n - 1, n - 200, 3, n - 77], device="cuda")
+    for p in pools:
+        x = torch.randn((4, hkv, ps, d), device="cuda")
+        p[ids] = ((x * 40).round().clamp(-127, 127) if kind == "int8" else x).to(TORCH[kind])
+    table = ids.to(torch.int32).view(2, 2).contiguous()
+    used = on_gpu([100, 128], np.int32)
+    q = torch.randn((2, 16, d), device="cuda")
+    out, lse = sa.sa_decode_attention(q, *pools, table, used, d ** -0.5, **kw)
+    small = [p[ids] for p in pools]
+    if kw:
+        kw = dict(k_scales=scales[ids], v_scales=scales[ids])
+    near = torch.arange(4, dtype=torch.int32, device="cuda").view(2, 2)
+    same, slse = sa.sa_decode_attention(q, *small, near, used, d ** -0.5, **kw)
+    assert torch.equal(out, same) and torch.equal(lse, slse) and float(out.abs().max()) > 0
+    cu = np.array([0, 100, 228])
+    if kw:
+        kw = dict(k_scales=scales, v_scales=scales)
+    k, v = sa.sa_load_kv(*pools, table, cu, on_gpu(cu, np.int64), used, dtype=torch.float32, **kw)
+    for got, p in ((k, small[0]), (v, small[1])):
+        rows = torch.cat([p[:2].transpose(1, 2).reshape(-1, hkv, d)[:100], p[2:].transpose(1, 2).reshape(-1, hkv, d)])
+        assert torch.equal(got, rows.float() * (2.0 ** -5 if kw else 1))

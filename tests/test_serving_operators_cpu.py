@@ -99,6 +99,8 @@ def test_decode_checks(lib):
     assert decode(lib, act=INT8) == 11 and decode(lib, kind=4) == 11
     assert decode(lib, d=72) == 10 and decode(lib, d=272) == 10 and decode(lib, d=60, kind=F32) == 10
     assert decode(lib, batch=1 << 20, hq=1 << 12) == 10
+    assert decode(lib, cols=1 << 20, ps=1024) == 10            # positions of a sequence: 2^29
+    assert decode(lib, n=1 << 27, hkv=2, ps=16) == 10           # rows of the pool: below 2^32 - 1
     for name in ("q", "kp", "vp", "ks", "vs", "bt", "used", "out", "ws"):
         assert decode(lib, **{name: None}) == 11, name
     for name in ("q", "kp", "vp", "out", "ws"):
@@ -115,6 +117,11 @@ def test_decode_workspace(lib):
     assert lib.sa_decode_workspace_size(2, 4, 2, 0, ctypes.byref(n)) == 6
     assert lib.sa_decode_workspace_size(-1, 4, 2, 64, ctypes.byref(n)) == 4
     assert lib.sa_decode_workspace_size(2, 4, 2, 64, None) == 11
+    # (what the kernels keep: never less with more heads or channels)
+    last = 0
+    for hq, d in ((8, 64), (16, 64), (16, 128), (32, 128), (32, 256)):
+        assert lib.sa_decode_workspace_size(1, hq, 2, d, ctypes.byref(n)) == 0 and n.value >= last
+        last = n.value
     # the same for every batch: it grows with the machine, not with the work
     sizes = set()
     for batch in (0, 1, 100, 10 ** 6):
