@@ -1185,26 +1185,18 @@ def sa_decode_attention(q, k_pages, v_pages, block_tables, used_kv_lens, softmax
     code = _pool(k_pages, v_pages, k_scales, v_scales)
     dev = k_pages.device
     num_pages, hkv, page_size, d = k_pages.shape
-    act = _ACT_DTYPES.get(getattr(q, "dtype", None))
-    if act is None:
-        raise TypeError("q must be a float32 or bfloat16 tensor")
-    _require(q, q.dtype, "q", dev)
-    if q.dim() != 3 or q.shape[2] != d:
-        raise ValueError(f"q must be [batch, hq, {d}], got {tuple(q.shape)}")
-    batch, hq, _ = q.shape
     try:
-        usual = (_alike(dev.index, torch.int32, block_tables, used_kv_lens) and
-                 block_tables.dim() == 2 and block_tables.shape[0] == batch and
-                 used_kv_lens.numel() == batch)
-    except AttributeError:
+        index, dtype = dev.index, q.dtype
+        batch, hq, channels = q.shape
+        usual = (dtype in _ACT_DTYPES and channels == d and _alike(index, dtype, q, out) and
+                 out.shape == q.shape and _alike(index, torch.float32, lse) and
+                 lse.shape == (batch, hq) and _alike(index, torch.int32, block_tables, used_kv_lens) and
+                 used_kv_lens.shape == (batch,) and block_tables.dim() == 2 and
+                 block_tables.shape[0] == batch and _alike(index, torch.uint8, workspace))
+    except (AttributeError, TypeError, ValueError):
         usual = False
     if not usual:
-        _require(block_tables, torch.int32, "block_tables", dev)
-        _require(used_kv_lens, torch.int32, "used_kv_lens", dev)
-        if block_tables.dim() != 2 or block_tables.shape[0] != batch or used_kv_lens.numel() != batch:
-            raise ValueError(f"block_tables and used_kv_lens must have a row for each of the {batch} sequences")
-    _check_room(dev, (out, q.dtype, batch * hq * d, "out"), (lse, torch.float32, batch * hq, "lse"))
-    if out is None or workspace is None or (lse is None and with_lse):
+        batch, hq = _check_decode(q, d, dev, block_tables, used_kv_lens, out, lse, workspace)
         with _allocating(stream):
             if out is None:
                 out = torch.empty((batch, hq, d), dtype=q.dtype, device=dev)
@@ -1212,18 +1204,36 @@ def sa_decode_attention(q, k_pages, v_pages, block_tables, used_kv_lens, softmax
                 lse = torch.empty((batch, hq), dtype=torch.float32, device=dev)
             if workspace is None:
                 workspace = allocate_decode_workspace(batch, hq, hkv, d, dev)
-    _require(workspace, torch.uint8, "workspace", dev)
-    base, at = workspace.data_ptr(), q.data_ptr()
+    base, at, to = workspace.data_ptr(), q.data_ptr(), out.data_ptr()
     aligned = (base + 255) & ~255
-    if at == out.data_ptr() and batch:
+    if at == to and batch:
         raise ValueError("out must not be q")
-    _check(_on(dev, _native.load().sa_decode_attention, at, act, k_pages.data_ptr(),
-               v_pages.data_ptr(), _ptr(k_scales), _ptr(v_scales), num_pages, code,
+    _check(_on(dev, _native.load().sa_decode_attention, at, _ACT_DTYPES[q.dtype],
+               k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scales), _ptr(v_scales), num_pages, code,
                block_tables.data_ptr(), block_tables.shape[1], used_kv_lens.data_ptr(), batch, hq,
-               hkv, d, page_size, softmax_scale, window, out.data_ptr(), _ptr(lse), aligned,
+               hkv, d, page_size, softmax_scale, window, to, _ptr(lse), aligned,
                max(workspace.numel() - (aligned - base), 0), _status_word(status, dev),
                _stream(stream, dev)), "sa_decode_attention")
     return out, lse
+
+
+def _check_decode(q, d, dev, block_tables, used_kv_lens, out, lse, workspace):
+    """What is wrong with a :func:`sa_decode_attention` call's tensors, if anything is:
+    else (batch, hq)."""
+    if getattr(q, "dtype", None) not in _ACT_DTYPES:
+        raise TypeError("q must be a float32 or bfloat16 tensor")
+    _require(q, q.dtype, "q", dev)
+    if q.dim() != 3 or q.shape[2] != d:
+        raise ValueError(f"q must be [batch, hq, {d}], got {tuple(q.shape)}")
+    batch, hq, _ = q.shape
+    _require(block_tables, torch.int32, "block_tables", dev)
+    _require(used_kv_lens, torch.int32, "used_kv_lens", dev)
+    if block_tables.dim() != 2 or block_tables.shape[0] != batch or used_kv_lens.numel() != batch:
+        raise ValueError(f"block_tables and used_kv_lens must have a row for each of the {batch} sequences")
+    _check_room(dev, (out, q.dtype, batch * hq * d, "out"), (lse, torch.float32, batch * hq, "lse"))
+    if workspace is not None:
+        _require(workspace, torch.uint8, "workspace", dev)
+    return batch, hq
 
 
 def sa_get_status(index: Index, stream=None) -> int:

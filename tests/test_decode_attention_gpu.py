@@ -275,6 +275,53 @@ def test_equals_sparse_attention_over_all_blocks():
     torch.testing.assert_close(lse, rlse, rtol=1e-5, atol=1e-5)
 
 
+def test_no_pool_and_no_columns():
+    """A cache without a page, a table without a column: nobody has keys."""
+    q = torch.randn((2, 4, 64), device="cuda")
+    none = torch.empty((0, 2, 16, 64), device="cuda")
+    for table in (torch.zeros((2, 3), dtype=torch.int32, device="cuda"),
+                  torch.zeros((2, 0), dtype=torch.int32, device="cuda")):
+        out, lse = sa.sa_decode_attention(q, none, none, table, on_gpu([0, 40], np.int32), 0.1)
+        assert (out == 0).all() and torch.isneginf(lse).all()
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+def test_scales_of_zero_and_at_the_ends(kind):
+    """Rows of zeros have scale 0: all keys count alike.  Values at both ends of f32."""
+    c = Cache([90], kind, 1, 64, 16, poison=False)
+    c.scales[0].zero_()
+    q = torch.randn((1, 2, 64), device="cuda")
+    out, lse = sa.sa_decode_attention(q, *c.pages, c.table, c.used, 0.1, **c.kw())
+    v, _ = c.rows(0, list(range(90)), 1)
+    # f32 sums of 90 products with p = 1, at most 90 half steps; codes of up to 448 scales
+    np.testing.assert_allclose(f64(out)[0, 0], v.mean(0)[0], atol=90 * 2.0 ** -24 * 448 * 2.0 ** -4)
+    assert abs(float(lse[0, 0]) - math.log(90)) < 1e-5
+    for e in (-126, -60, 60, 116):
+        c.scales[1].fill_(2.0 ** e)
+        big, _ = sa.sa_decode_attention(q, *c.pages, c.table, c.used, 0.1, **c.kw())
+        c.scales[1].fill_(1.0)
+        one, _ = sa.sa_decode_attention(q, *c.pages, c.table, c.used, 0.1, **c.kw())
+        # (a power of two: the same codes times it; at 2^-126 results leave f32's normal range)
+        np.testing.assert_allclose(f64(big), f64(one) * 2.0 ** e, rtol=2.0 ** -20, atol=2.0 ** -148)
+    c.scales[1].zero_()
+    out, _ = sa.sa_decode_attention(q, *c.pages, c.table, c.used, 0.1, **c.kw())
+    assert (out == 0).all()
+
+
+def test_a_query_that_is_no_number_stays_its_own():
+    """NaN in one row leaves the others, whole pairs and merged ones alike, and comes out."""
+    for lens in ([5, 40], [5, 60000]):
+        c = Cache(lens, "bf16", 1, 64, 16, poison=False)
+        q = torch.randn((2, 4, 64), device="cuda")
+        ref, rlse = sa.sa_decode_attention(q, *c.pages, c.table, c.used, 0.1)
+        q[1, 2, 7] = math.nan
+        out, lse = sa.sa_decode_attention(q, *c.pages, c.table, c.used, 0.1)
+        assert torch.isnan(out[1, 2]).all() and torch.isnan(lse[1, 2])
+        keep = torch.ones((2, 4), dtype=torch.bool, device="cuda")
+        keep[1, 2] = False
+        assert torch.equal(out[keep], ref[keep]) and torch.equal(lse[keep], rlse[keep])
+
+
 def test_refusals():
     c = Cache([30, 7], "int8", 2, 64, 16)
     q = torch.randn((2, 4, 64), device="cuda")
