@@ -1,6 +1,6 @@
 // Attention of one new token per sequence over its whole paged cache, split over the
 // cache's length.  Instances per cache type are in decode_f32.cu, decode_bf16.cu,
-// decode_e4m3.cu and decode_int8.cu; decode.cu holds the entry point and the join.
+// decode_e4m3.cu and decode_int8.cu; decode.cu holds the entry point.
 //
 // One query row per q-head against n keys: every byte of K and V is used once for the
 // few lanes of its kv head, so the floor is the cache's bytes.  The work is a flat

@@ -99,6 +99,16 @@ def test_heads(kind, g):
         check(Cache([70, 301], kind, 3, 64, 16, seed=g), 3 * g, act)
 
 
+@pytest.mark.parametrize("d", [128, 200, 256])
+@pytest.mark.parametrize("g", [9, 16, 20])
+@pytest.mark.parametrize("kind", KINDS)
+def test_many_heads_of_other_dims(kind, g, d):
+    """Every instance with 16 query rows, whole pairs and cut ones."""
+    d = d if kind in ("f32", "bf16") else d // 16 * 16
+    for act in ("f32", "bf16"):
+        check(Cache([41, 0, 700], kind, 2, d, 16, seed=g), 2 * g, act)
+
+
 @pytest.mark.parametrize("d", [16, 32, 48, 64, 80, 96, 112, 128, 144, 192, 240, 256])
 @pytest.mark.parametrize("kind", KINDS)
 def test_head_dims(kind, d):
