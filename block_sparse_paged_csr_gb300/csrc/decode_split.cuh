@@ -1211,8 +1211,8 @@ __global__ void __launch_bounds__(256) decode_join_kernel(const __grid_constant_
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ctas = static_cast<int>(gridDim.x);
   const int x = static_cast<int>(blockIdx.x);
-  if (x == 0) return;
   griddep_wait();
+  if (x == 0) return;
   // the pair's last CTA: the first from x on that ends it
   const int2 before = __ldcg(a.joins + x - 1);
   int z = x, item = -1;

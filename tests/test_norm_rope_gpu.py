@@ -207,6 +207,22 @@ def test_many_sequences_of_one_token():
     assert torch.equal(got, same)
 
 
+@pytest.mark.parametrize("rot", [128, 20])
+def test_tokens_far_into_a_tensor(rot):
+    """Elements beyond 2^31 from the tensor's start, by both kernels."""
+    tq, hq, d = 140001, 128, 128
+    q = torch.empty((tq, hq, d), dtype=torch.bfloat16, device="cuda")
+    q[-5:].normal_()
+    q[:-5].zero_()
+    f = on_gpu(freqs(rot), np.float32)
+    pos = torch.arange(tq, dtype=torch.int32, device="cuda")
+    w = torch.ones(d, device="cuda")
+    got, _ = sa.sa_norm_rope(q, None, w, None, f, positions=pos)
+    same, _ = sa.sa_norm_rope(q[-5:].contiguous(), None, w, None, f, positions=pos[-5:].contiguous())
+    assert torch.equal(got[-5:], same) and float(same.abs().max()) > 0
+    assert not got[:1000].any()
+
+
 def test_an_axis_outside_is_reported():
     x = torch.randn((3, 1, 32), device="cuda")
     f = on_gpu(freqs(32), np.float32)
