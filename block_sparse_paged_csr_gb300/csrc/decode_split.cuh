@@ -856,6 +856,33 @@ struct Worker {
     return l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
   }
 
+  // The state joined by another piece's (see dump).
+  __device__ __forceinline__ void absorb(const float* from) {
+    float f_own[C::kNR], f_other[C::kNR];
+#pragma unroll
+    for (int r = 0; r < C::kNR; ++r) {
+      const float* s = from + C::kNel + g + 8 * r;
+      const float m = s[0], n = s[R], l = s[2 * R];
+      const float mm = fmaxf(m_run[r], m), nn = fmaxf(n_run[r], n);
+      f_own[r] = pow2_of(n_run[r] - nn);
+      f_other[r] = pow2_of(n - nn);
+      l_part[r] = l_part[r] * pow2_of(m_run[r] - mm) + (c == 0 ? l * pow2_of(m - mm) : 0.f);
+      m_run[r] = mm;
+      n_run[r] = nn;
+    }
+#pragma unroll
+    for (int j = 0; j < C::kNJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int r = 0; r < C::kNR; ++r) {
+          const float v = from[((2 * j + e) * C::kNR + r) * 32 + lane];
+          const float sum = fmaf(f_other[r], v, f_own[r] * at(j, r, e));
+          if constexpr (C::kDirect && R == 8) o[j][C::kOW - 2 + e] = 0.f;
+          o[j][2 * r + e] = sum;
+        }
+  }
+
   // One element of a merged row: lane ln's, of n-tile and column je = (j, e).
   static __device__ __forceinline__ void write_element(const DecodeArgs& a, int64_t row, int ln, int je,
                                                        float sum, float m, float n, float l) {
@@ -908,7 +935,10 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
   constexpr int kChunks = 64;
   __shared__ int64_t s_chunk[kChunks];         // tiles (of one item) of pieces of the batch
   __shared__ PieceInfo s_piece[2 * C::kW];     // of warp w: [2 w] the one it began with, [2 w + 1] its last
-  __shared__ float s_weight[2 * C::kW][R];     // of a piece's o in its group
+  __shared__ int s_order[2 * C::kW];           // pieces that there are, in order
+  __shared__ int4 s_group[2 * C::kW];          // groups: item, its pieces in that order, their number, 1 starts | 2 ends
+  __shared__ int s_groups;
+  __shared__ float s_weight[2 * C::kW][R];     // of a piece's o in its group, in that order
   __shared__ float s_stat[2 * C::kW][3][R];    // m, n, l of a group
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   griddep_launch_dependents();
@@ -993,10 +1023,13 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
   const int n = static_cast<int>(t1 - t0);
   if (lane < 2) s_piece[2 * warp + lane] = {-1, 0, 0};
   __syncwarp();
+  int item = -1;
+  bool open = false;               // the warp's range ended inside a pair
+  bool started = false;            // the piece at hand holds its pair's first tile
   if (n > 0) {
     w.runs = a.head_dim == DP && a.page_size % C::kRun == 0;
     w.seek(b0, in_seq);
-    int item = b0 * a.items_per_seq + w.h;
+    item = b0 * a.items_per_seq + w.h;
     typename W::Rows q;
     w.fetch_q(item, q);
     typename W::Pend ahead = w.take();           // of the tile whose K is next to be copied
@@ -1043,7 +1076,6 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
     w.keep_q(q);
     w.begin();
     uint32_t flags = 0;
-    bool started = false;          // the piece at hand holds its pair's first tile
     int e = 0;
     for (int i = 0; i < n; ++i) {
       copies_wait<2>();
@@ -1086,115 +1118,151 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
     }
     copies_wait<0>();
     __syncwarp();
-    if (!(flags & 2u)) {
+    open = !(flags & 2u);
+    if (open && lane == 0) s_piece[2 * warp + 1] = {item, started ? 1 : 0, 0};
+  }
+  __syncthreads();
+  // Most pairs that are cut are cut once: a warp's last piece and the next warp's first make a
+  // whole, which the warp writes from its registers.  Other last pieces go where the ring was.
+  if (open) {
+    if (started && warp + 1 < C::kW && s_piece[2 * warp + 2].item == item) {
+      w.absorb(a.firsts + (static_cast<int64_t>(cta) * C::kW + warp + 1) * C::kState);
+      w.write_out(item);
+      __syncwarp();
+      if (lane < 2) s_piece[2 * warp + 1 + lane].item = -1;
+    } else {
       w.dump(reinterpret_cast<float*>(own));
-      if (lane == 0) s_piece[2 * warp + 1] = {item, started ? 1 : 0, 0};
     }
   }
   __syncthreads();
 
-  // ---- pieces of pairs that this CTA's warps cut, in the order of the keys: groups of
-  // one pair, merged row by row (a lane per piece), then element by element
+  // ---- pieces of pairs that this CTA's warps cut, in the order of the keys.  Pieces of one pair are
+  // a group; groups are merged side by side: their statistics by a warp each (a lane
+  // per row and piece), their elements by all warps in turn.
   static_assert(2 * C::kW <= 32, "a lane per piece");
   auto state = [&](int x) -> const float* {
     return x & 1 ? reinterpret_cast<const float*>(smem + (x >> 1) * C::kPerWarp)
                  : a.firsts + (static_cast<int64_t>(cta) * C::kW + (x >> 1)) * C::kState;
   };
-  PieceInfo my{-1, 0, 0};
-  if (lane < 2 * C::kW) my = s_piece[lane];
-  const unsigned there = __ballot_sync(0xffffffffu, my.item >= 0);
-  unsigned left = there;
-  int turn = warp;                 // (group, row) pairs go to the warps in turn
+  if (warp == 0) {
+    PieceInfo my{-1, 0, 0};
+    if (lane < 2 * C::kW) my = s_piece[lane];
+    unsigned left = __ballot_sync(0xffffffffu, my.item >= 0);
+    if (my.item >= 0) s_order[__popc(left & ((1u << lane) - 1u))] = lane;
+    int at = 0, k = 0;
 #pragma unroll 1
-  for (int k = 0; left; ++k) {
-    const int item = __shfl_sync(0xffffffffu, my.item, __ffs(left) - 1);
-    const unsigned group = __ballot_sync(0xffffffffu, my.item == item);
-    left &= ~group;
-    const bool in = (group >> lane) & 1u;
+    for (; left; ++k) {
+      const int p = __ffs(left) - 1, item = __shfl_sync(0xffffffffu, my.item, p);
+      const unsigned group = __ballot_sync(0xffffffffu, my.item == item);
+      const int starts = __shfl_sync(0xffffffffu, my.starts, p);
+      const int ends = __shfl_sync(0xffffffffu, my.ends, 31 - __clz(group));
+      if (lane == 0) s_group[k] = make_int4(item, at, __popc(group), starts | (ends << 1));
+      at += __popc(group);
+      left &= ~group;
+    }
+    if (lane == 0) s_groups = k;
+  }
+  __syncthreads();
+  const int groups = s_groups;
+  {
+    constexpr int kSlots = 32 / R, kMost = (2 * C::kW + kSlots - 1) / kSlots;    // pieces: of a lane
+    const int row = lane % R, slot = lane / R;
 #pragma unroll 1
-    for (; turn < R; turn += C::kW) {
-      const float* s = state(lane) + C::kNel + turn;
-      float m = -INFINITY, n = -INFINITY, l = 0.f;
-      if (in) {
-        m = s[0];
-        n = s[R];
-        l = s[2 * R];
+    for (int k = warp; k < groups; k += C::kW) {
+      const int4 group = s_group[k];
+      float m[kMost], n[kMost], l[kMost], mm = -INFINITY, nn = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < kMost; ++i) {
+        const int x = slot + kSlots * i;
+        m[i] = n[i] = -INFINITY;
+        l[i] = 0.f;
+        if (x < group.z) {
+          const float* s = state(s_order[group.y + x]) + C::kNel + row;
+          m[i] = s[0];
+          n[i] = s[R];
+          l[i] = s[2 * R];
+        }
       }
-      float mm = m, nn = n;
-#pragma unroll 1
-      for (int o = 16; o; o >>= 1) {
+#pragma unroll
+      for (int i = 0; i < kMost; ++i) {
+        mm = fmaxf(mm, m[i]);
+        nn = fmaxf(nn, n[i]);
+      }
+#pragma unroll
+      for (int o = R; o < 32; o <<= 1) {
         mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
         nn = fmaxf(nn, __shfl_xor_sync(0xffffffffu, nn, o));
       }
-      if (in) {
-        l *= pow2_of(m - mm);
-        s_weight[lane][turn] = pow2_of(n - nn);
+#pragma unroll
+      for (int i = 0; i < kMost; ++i) {
+        const int x = slot + kSlots * i;
+        if (x < group.z) {
+          s_weight[group.y + x][row] = pow2_of(n[i] - nn);
+          sum = fmaf(pow2_of(m[i] - mm), l[i], sum);
+        }
       }
-#pragma unroll 1
-      for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-      if (lane == 0) {
-        s_stat[k][0][turn] = mm;
-        s_stat[k][1][turn] = nn;
-        s_stat[k][2][turn] = l;
+#pragma unroll
+      for (int o = R; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (slot == 0) {
+        s_stat[k][0][row] = mm;
+        s_stat[k][1][row] = nn;
+        s_stat[k][2][row] = sum;
       }
     }
-    turn -= R;
   }
   __syncthreads();
   auto row_of = [](int idx) {      // the query row of element idx of a state
     return ((idx & 31) >> 2) + (C::kNR == 2 ? 8 * ((idx >> 5) & 1) : 0);
   };
-  int2 join = make_int2(-1, 0);    // the pair that goes on from the CTA before, and whether it ends here
-  left = there;
+  // 128 elements of a group a warp at a time, four pieces in flight
+  constexpr int kCols = 4, kUnits = C::kNel / (32 * kCols);
 #pragma unroll 1
-  for (int k = 0; left; ++k) {
-    const int p = __ffs(left) - 1;
-    const int item = __shfl_sync(0xffffffffu, my.item, p);
-    const unsigned group = __ballot_sync(0xffffffffu, my.item == item);
-    const int starts = __shfl_sync(0xffffffffu, my.starts, p);
-    const int ends = __shfl_sync(0xffffffffu, my.ends, 31 - __clz(group));
-    left &= ~group;
-    if (!starts) join = make_int2(item, ends);
-    float* to = a.parts + (static_cast<int64_t>(cta) * 2 + (starts ? 1 : 0)) * C::kState;
-    const Item it = item_of<R>(a, item);
-    // a thread's elements, all at once for a piece (the warp's lanes hold the same columns)
-    constexpr int kMine = (C::kNel + C::kThreads - 1) / C::kThreads;
-    float sum[kMine];
-#pragma unroll
-    for (int i = 0; i < kMine; ++i) sum[i] = 0.f;
+  for (int u = warp; u < groups * kUnits; u += C::kW) {
+    const int k = u / kUnits, idx0 = (u - k * kUnits) * 32 * kCols + lane;
+    const int4 group = s_group[k];
+    float sum[kCols] = {};
 #pragma unroll 1
-    for (unsigned bits = group; bits; bits &= bits - 1) {
-      const int at = __ffs(bits) - 1;
-      const float* s = state(at);
-      float v[kMine];
+    for (int x0 = 0; x0 < group.z; x0 += 4) {
+      float v[4][kCols];
 #pragma unroll
-      for (int i = 0; i < kMine; ++i) {
-        const int idx = tid + i * C::kThreads;
-        v[i] = idx < C::kNel ? s[idx] : 0.f;
+      for (int x = 0; x < 4; ++x) {
+        const bool in = x0 + x < group.z;
+        const float* s = state(s_order[group.y + (in ? x0 + x : 0)]) + idx0;
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) v[x][i] = in ? s[32 * i] : 0.f;
       }
 #pragma unroll
-      for (int i = 0; i < kMine; ++i)
-        sum[i] = fmaf(s_weight[at][row_of(tid + i * C::kThreads)], v[i], sum[i]);
-    }
+      for (int x = 0; x < 4; ++x)
+        if (x0 + x < group.z) {
 #pragma unroll
-    for (int i = 0; i < kMine; ++i) {
-      const int idx = tid + i * C::kThreads;
-      if (idx >= C::kNel) break;
-      const int ln = idx & 31, je = (idx >> 5) / C::kNR, row = row_of(idx);
+          for (int i = 0; i < kCols; ++i)
+            sum[i] = fmaf(s_weight[group.y + x0 + x][row_of(idx0 + 32 * i)], v[x][i], sum[i]);
+        }
+    }
+    const bool starts = group.w & 1, all = group.w == 3;
+    float* to = a.parts + (static_cast<int64_t>(cta) * 2 + (starts ? 1 : 0)) * C::kState;
+    const Item it = item_of<R>(a, group.x);
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) {
+      const int idx = idx0 + 32 * i, je = (idx >> 5) / C::kNR, row = row_of(idx);
       const float m = s_stat[k][0][row], n = s_stat[k][1][row], l = s_stat[k][2][row];
-      if (!(starts && ends)) {
+      if (!all) {
         to[idx] = sum[i];
-        if ((ln & 3) == 0 && je == 0) {
+        if ((lane & 3) == 0 && je == 0) {
           to[C::kNel + row] = m;
           to[C::kNel + R + row] = n;
           to[C::kNel + 2 * R + row] = l;
         }
       } else if (row < it.rows) {
-        W::write_element(a, it.row0 + row, ln, je, sum[i], m, n, l);
+        W::write_element(a, it.row0 + row, lane, je, sum[i], m, n, l);
       }
     }
   }
-  if (tid == 0) a.joins[cta] = join;
+  // the pair that goes on from the CTA before (-1: none), and whether it ends here
+  if (tid == 0) {
+    const int4 first = s_group[0];
+    a.joins[cta] = groups > 0 && !(first.w & 1) ? make_int2(first.x, first.w >> 1) : make_int2(-1, 0);
+  }
 }
 
 // Pairs whose parts lie in several CTAs.  CTA x of `joins` says which pair its first piece
