@@ -73,7 +73,7 @@ struct Cfg {
   // bf16 queries over 8 bits: o stays in the tensor cores' accumulators (see values)
   static constexpr bool kDirect = B && k8;
   static constexpr int kOW = kDirect ? 4 : 2 * kNR;             // numbers of o of an n-tile
-  // operands of Q kept per k-step (see load_q), and of P
+  // operands of Q kept per k-step (see keep_q), and of P
   static constexpr int kQP = kF32 ? 1 : k8 ? (R == 8 || B ? 1 : 2) : B ? 1 : R == 8 ? 2 : 3;
   static constexpr int kPP = kF32 ? 1 : k8 ? (R == 8 || B ? 1 : 2) : R == 8 ? (B ? 1 : 2) : (B ? 2 : 3);
   // (the third parts of R = 8 leave half of their operand zero, which is not stored)

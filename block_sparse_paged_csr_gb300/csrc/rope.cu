@@ -253,7 +253,8 @@ norm_rope_kernel(const RopeArgs a, int log_tokens, int heads_per_cta) {
 }
 
 // Any sizes, strides and alignment: a warp per row, a lane per pair (and per
-// channel behind the rotated ones), angles made where they are used.
+// channel behind the rotated ones), angles made where they are used (8192 tokens of 64 + 8
+// heads in f32 whose rows start off 16 bytes: 411 us, the other kernel 100).
 template <bool kSrcBf16, bool kDstBf16>
 __global__ void __launch_bounds__(kThreads) norm_rope_any_kernel(const RopeArgs a) {
   constexpr int kPairs = 4, kRest = 8;                 // of a lane: head_dim <= 256
@@ -347,10 +348,15 @@ cudaError_t launch_rope(const RopeArgs& a, bool wide, cudaStream_t stream) {
   const int units = a.head_dim / 8;
   const int lanes = units <= 4 ? 4 : units <= 8 ? 8 : units <= 16 ? 16 : 32;
   const int groups = kThreads / lanes;
-  // Prompts: four tokens a CTA.  Few tokens: one, and its heads over several CTAs,
-  // so that a row is all that a group does.
-  const int64_t sms = device_sm_count();
-  const bool few = a.tq * total <= 4 * sms * groups;
+  // Prompts: four tokens a CTA, whose groups walk over the heads in `turns` turns of kRows.  Few
+  // tokens: one, and its heads over several CTAs, so that a row is all that a group does.  A turn
+  // takes about half as long as a round of CTAs: 32 + 8 heads of 128 in bf16, four tokens / one token
+  // a CTA: 64 tokens (4 turns, 1 round) 7.4 / 3.5 us, 256 (2 rounds) 7.7 / 6.2, 400 (3 rounds) 7.6 /
+  // 8.1, 2000 19.7 / 31.8; 8 + 1 heads (1 turn): 500 tokens (2 rounds) 4.2 / 5.8.
+  const int64_t slots = 3ll * device_sm_count();
+  const int64_t rounds = (a.tq * ((total + groups - 1) / groups) + slots - 1) / slots;
+  const int64_t turns = (4ll * total + 3 * groups - 1) / (3 * groups);
+  const bool few = 2 * rounds <= turns + 1;
   const int log_tokens = few ? 0 : 2;
   const int heads_per_cta = few ? groups : total;
   const int64_t gx = (a.tq + (int64_t{1} << log_tokens) - 1) >> log_tokens;
