@@ -20,6 +20,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxTokens = 4;                 // tokens per CTA
+constexpr int kRows = 3;                      // rows that a lane has in flight
+constexpr int kMinCtas = 3;                   // CTAs per SM that the registers have to leave room for
 
 struct RopeArgs {
   const void* src[2];                         // q, k
@@ -84,38 +86,95 @@ __device__ __forceinline__ int axis_position(const RopeArgs& a, int64_t tok, int
   return a.positions[axis * a.axis_stride + tok];
 }
 
-// Four channels as they lie, and as values.
-template <bool kBf16> struct Raw4;
-template <> struct Raw4<true> {
-  uint2 u;
+// Two f32 numbers side by side, and operations on both at once.
+using pair_t = unsigned long long;
+__device__ __forceinline__ pair_t make_pair(float lo, float hi) {
+  pair_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 both(pair_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ pair_t mul2(pair_t x, pair_t y) {
+  pair_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+__device__ __forceinline__ pair_t fma2(pair_t x, pair_t y, pair_t z) {
+  pair_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+  return r;
+}
+
+// kC channels of a row as they lie (8 or 16 bytes of bf16, 16 of f32), and as values.
+template <bool kBf16, int kC>
+struct Raw {
+  static constexpr int kWords = kC * (kBf16 ? 2 : 4) / 4;
+  uint32_t w[kWords];
   __device__ __forceinline__ void load(const void* p, int64_t off) {
-    u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + off);
+    const unsigned char* at = static_cast<const unsigned char*>(p) + off * (kBf16 ? 2 : 4);
+    if constexpr (kWords == 4) {
+      const uint4 u = *reinterpret_cast<const uint4*>(at);
+      w[0] = u.x;
+      w[1] = u.y;
+      w[2] = u.z;
+      w[3] = u.w;
+    } else {
+      const uint2 u = *reinterpret_cast<const uint2*>(at);
+      w[0] = u.x;
+      w[1] = u.y;
+    }
   }
-  __device__ __forceinline__ void zero() { u = make_uint2(0u, 0u); }
-  __device__ __forceinline__ float4 values() const { return bf16x4_to_f32(u); }
-};
-template <> struct Raw4<false> {
-  float4 u;
-  __device__ __forceinline__ void load(const void* p, int64_t off) {
-    u = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + off);
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0u;
   }
-  __device__ __forceinline__ void zero() { u = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ float4 values() const { return u; }
+  __device__ __forceinline__ pair_t pair(int i) const {          // channels 2 i, 2 i + 1
+    if constexpr (kBf16)
+      return make_pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+    else
+      return make_pair(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+  }
 };
 
-// A row is spread over kLanes lanes, a lane holding 8 channels in two pieces of 4 that
-// hold whole pairs: channels 4 u and rot / 2 + 4 u on (or 8 u on, where pairs are
+template <bool kBf16, int kC>
+__device__ __forceinline__ void store_piece(void* p, int64_t off, const pair_t (&x)[kC / 2]) {
+  float2 v[kC / 2];
+#pragma unroll
+  for (int i = 0; i < kC / 2; ++i) v[i] = both(x[i]);
+  if constexpr (kBf16 && kC == 8) {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + off) =
+        make_uint4(pack_bf16x2_rn(v[0].x, v[0].y), pack_bf16x2_rn(v[1].x, v[1].y),
+                   pack_bf16x2_rn(v[2].x, v[2].y), pack_bf16x2_rn(v[3].x, v[3].y));
+  } else {
+#pragma unroll
+    for (int i = 0; i < kC / 4; ++i)
+      store_o4(p, kBf16, off + 4 * i, make_float4(v[2 * i].x, v[2 * i].y, v[2 * i + 1].x, v[2 * i + 1].y));
+  }
+}
+
+// A row is spread over kLanes lanes, a lane holding 2 kC channels in two pieces of kC that
+// hold whole pairs: channels kC u and rot / 2 + kC u on (or 2 kC u on, where pairs are
 // adjacent), so that the rotation needs no other lane.  Either way the pieces' pairs are
-// 4 u .. 4 u + 3.  A group of kLanes lanes keeps one token and walks over its heads, kRows of them
+// kC u on.  A group of kLanes lanes keeps one token and walks over its heads, kRows of them
 // at a time, all asked for before the first is used: angles are made once per
-// token and pair, by the CTA, and stay in registers, as the weights do.
-template <bool kSrcBf16, bool kDstBf16, int kLanes>
-__global__ void __launch_bounds__(kThreads, 3)
+// token and pair, by the CTA, and stay in registers; weights come from shared memory.
+//
+// Bound by memory from some thousand tokens on: 8192 of 64 + 8 heads of 128 in f32 (604 MB) 99.5 us,
+// 6.1 TB/s; 32768 in bf16 (1.2 GB) 210 us, 5.7 TB/s.  bf16 is bound by instructions as soon as
+// they are not few: 4 channels a piece and one number an operation took 288 us there, 8 and two
+// numbers take 210.  What counts besides is rows in flight against registers (bf16, 32768 tokens):
+// 3 rows and 3 CTAs an SM 211 us, 2 and 3 221, 2 and 4 211, 3 and 2 248, 4 and 2 247.
+template <bool kSrcBf16, bool kDstBf16, int kC, int kLanes>
+__global__ void __launch_bounds__(kThreads, kMinCtas)
 norm_rope_kernel(const RopeArgs a, int log_tokens, int heads_per_cta) {
   constexpr int kGroups = kThreads / kLanes;
-  constexpr int kRows = 3;
   __shared__ int s_pos[kMaxTokens];
-  __shared__ __align__(16) float2 s_turn[kMaxTokens * 128];
+  __shared__ __align__(16) float s_cos[kMaxTokens * 128], s_sin[kMaxTokens * 128];
+  __shared__ __align__(16) float s_w[2][256];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int tokens = 1 << log_tokens;
   const int64_t tok0 = static_cast<int64_t>(blockIdx.x) << log_tokens;
@@ -126,18 +185,17 @@ norm_rope_kernel(const RopeArgs a, int log_tokens, int heads_per_cta) {
   const int total = a.heads[0] + a.heads[1];
   const int end = min(total, static_cast<int>(blockIdx.y + 1) * heads_per_cta);
   int head = static_cast<int>(blockIdx.y) * heads_per_cta + (group >> log_tokens);
-  const int rot_units = a.rot >> 3;
-  const bool rotated = u < rot_units;
-  const int ca = rotated ? (a.interleaved ? 8 * u : 4 * u) : 8 * u;
-  const int cb = rotated && !a.interleaved ? n_pairs + 4 * u : ca + 4;
-  const bool mine = 8 * u < a.head_dim;
+  const bool rotated = u < a.rot / (2 * kC);
+  const int ca = rotated && !a.interleaved ? kC * u : 2 * kC * u;
+  const int cb = rotated && !a.interleaved ? n_pairs + kC * u : ca + kC;
+  const bool mine = 2 * kC * u < a.head_dim;
   const bool live = tok < a.tq;
 
-  Raw4<kSrcBf16> xa[kRows], xb[kRows];
-  auto load_rows = [&]() {
+  Raw<kSrcBf16, kC> xa[kRows], xb[kRows];
+  auto load_rows = [&](int first) {
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      const int h = head + i * step;
+      const int h = first + i * step;
       xa[i].zero();
       xb[i].zero();
       if (live && mine && h < end) {
@@ -149,23 +207,12 @@ norm_rope_kernel(const RopeArgs a, int log_tokens, int heads_per_cta) {
       }
     }
   };
-  load_rows();
-  float4 w[2][2];                                      // of q and k: both pieces
+  load_rows(head);
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    w[k][0] = w[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (a.weight[k] != nullptr && mine) {
-      if (a.weight_bf16) {
-        const uint16_t* p = static_cast<const uint16_t*>(a.weight[k]);
-        w[k][0] = bf16x4_to_f32(*reinterpret_cast<const uint2*>(p + ca));
-        w[k][1] = bf16x4_to_f32(*reinterpret_cast<const uint2*>(p + cb));
-      } else {
-        const float* p = static_cast<const float*>(a.weight[k]);
-        w[k][0] = *reinterpret_cast<const float4*>(p + ca);
-        w[k][1] = *reinterpret_cast<const float4*>(p + cb);
-      }
-    }
-  }
+  for (int k = 0; k < 2; ++k)
+    if (a.weight[k] != nullptr && tid < a.head_dim)
+      s_w[k][tid] = a.weight_bf16 ? bf16_to_f32(static_cast<const uint16_t*>(a.weight[k])[tid])
+                                  : static_cast<const float*>(a.weight[k])[tid];
 
   if (n_pairs > 0) {
     if (a.positions == nullptr) {
@@ -179,60 +226,85 @@ norm_rope_kernel(const RopeArgs a, int log_tokens, int heads_per_cta) {
       const int t = i / n_pairs, pair = i - t * n_pairs;
       if (tok0 + t < a.tq) {
         const int p = a.positions ? axis_position(a, tok0 + t, pair) : s_pos[t];
-        s_turn[i] = cos_sin(turn_fraction(a.inv_freq[pair]), p);
+        const float2 turn = cos_sin(turn_fraction(a.inv_freq[pair]), p);
+        s_cos[i] = turn.x;
+        s_sin[i] = turn.y;
       }
     }
-    __syncthreads();
   }
+  __syncthreads();
   if (!live) return;
-  float co[4], si[4];
+  pair_t co[kC / 2], si[kC / 2];                       // of the lane's pairs, two by two
 #pragma unroll
-  for (int j = 0; j < 4; j += 2) {
-    float4 t = make_float4(1.f, 0.f, 1.f, 0.f);
-    if (rotated)
-      t = *reinterpret_cast<const float4*>(s_turn + (group & (tokens - 1)) * n_pairs + 4 * u + j);
-    co[j] = t.x;
-    si[j] = t.y;
-    co[j + 1] = t.z;
-    si[j + 1] = t.w;
+  for (int j = 0; j < kC / 2; ++j) {
+    co[j] = make_pair(1.f, 1.f);
+    si[j] = make_pair(0.f, 0.f);
+    if (rotated) {
+      const int at = (group & (tokens - 1)) * n_pairs + kC * u + 2 * j;
+      co[j] = *reinterpret_cast<const pair_t*>(s_cos + at);
+      si[j] = *reinterpret_cast<const pair_t*>(s_sin + at);
+    }
   }
   const unsigned mask = kLanes == 32 ? 0xffffffffu
                                      : ((1u << (kLanes & 31)) - 1u) << ((lane / kLanes) * kLanes);
-  for (; head < end; head += kRows * step) {
+  for (;;) {
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       const int h = head + i * step;
-      if (h >= end) break;
+      if (h >= end) return;
       const int kind = h >= a.heads[0] ? 1 : 0;
-      const float4 p4 = xa[i].values(), q4 = xb[i].values();
-      float x[8] = {p4.x, p4.y, p4.z, p4.w, q4.x, q4.y, q4.z, q4.w};
+      pair_t x[kC / 2], y[kC / 2];
+#pragma unroll
+      for (int c = 0; c < kC / 2; ++c) {
+        x[c] = xa[i].pair(c);
+        y[c] = xb[i].pair(c);
+      }
       // (the same for all lanes of a group, and a group's lanes lie in one warp)
       if (a.weight[kind] != nullptr) {
-        float ss = 0.f;
+        pair_t ss2 = make_pair(0.f, 0.f);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) ss = fmaf(x[c], x[c], ss);
+        for (int c = 0; c < kC / 2; ++c) ss2 = fma2(y[c], y[c], fma2(x[c], x[c], ss2));
+        float ss = both(ss2).x + both(ss2).y;
 #pragma unroll
         for (int o = kLanes / 2; o; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
         const float r = rsqrtf(ss / static_cast<float>(a.head_dim) + a.eps);
-        const float4 wa = kind ? w[1][0] : w[0][0], wb = kind ? w[1][1] : w[0][1];
-        const float ww[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
+        const pair_t rr = make_pair(r, r);
+        if (mine) {
+          const ulonglong2* wa = reinterpret_cast<const ulonglong2*>(s_w[kind] + ca);
+          const ulonglong2* wb = reinterpret_cast<const ulonglong2*>(s_w[kind] + cb);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) x[c] = x[c] * r * ww[c];
+          for (int c = 0; c < kC / 4; ++c) {
+            const ulonglong2 p = wa[c], q = wb[c];
+            x[2 * c] = mul2(mul2(x[2 * c], rr), p.x);
+            x[2 * c + 1] = mul2(mul2(x[2 * c + 1], rr), p.y);
+            y[2 * c] = mul2(mul2(y[2 * c], rr), q.x);
+            y[2 * c + 1] = mul2(mul2(y[2 * c + 1], rr), q.y);
+          }
+        }
       }
       if (rotated) {
         if (a.interleaved) {
+          // x[c] is pair kC u + c, y[c] pair kC u + kC / 2 + c
+          auto turn = [](pair_t& v, float co1, float si1) {
+            const float2 p = both(v);
+            v = make_pair(p.x * co1 - p.y * si1, p.x * si1 + p.y * co1);
+          };
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float p = x[2 * j], q = x[2 * j + 1];
-            x[2 * j] = p * co[j] - q * si[j];
-            x[2 * j + 1] = p * si[j] + q * co[j];
+          for (int c = 0; c < kC / 4; ++c) {
+            const float2 c0 = both(co[c]), s0 = both(si[c]);
+            const float2 c1 = both(co[kC / 4 + c]), s1 = both(si[kC / 4 + c]);
+            turn(x[2 * c], c0.x, s0.x);
+            turn(x[2 * c + 1], c0.y, s0.y);
+            turn(y[2 * c], c1.x, s1.x);
+            turn(y[2 * c + 1], c1.y, s1.y);
           }
         } else {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float p = x[j], q = x[4 + j];
-            x[j] = p * co[j] - q * si[j];
-            x[4 + j] = p * si[j] + q * co[j];
+          for (int c = 0; c < kC / 2; ++c) {
+            const pair_t minus = si[c] ^ 0x8000000080000000ull;
+            const pair_t p = x[c];
+            x[c] = fma2(y[c], minus, mul2(p, co[c]));
+            y[c] = fma2(p, si[c], mul2(y[c], co[c]));
           }
         }
       }
@@ -240,15 +312,12 @@ norm_rope_kernel(const RopeArgs a, int log_tokens, int heads_per_cta) {
         const int64_t at =
             tok * a.dst_token_stride[kind] +
             static_cast<int64_t>(h - (kind ? a.heads[0] : 0)) * a.dst_head_stride[kind];
-        store_o4(a.dst[kind], kDstBf16, at + ca, make_float4(x[0], x[1], x[2], x[3]));
-        store_o4(a.dst[kind], kDstBf16, at + cb, make_float4(x[4], x[5], x[6], x[7]));
+        store_piece<kDstBf16, kC>(a.dst[kind], at + ca, x);
+        store_piece<kDstBf16, kC>(a.dst[kind], at + cb, y);
       }
     }
-    if (head + kRows * step < end) {
-      head += kRows * step;
-      load_rows();
-      head -= kRows * step;
-    }
+    head += kRows * step;
+    load_rows(head);
   }
 }
 
@@ -335,27 +404,22 @@ __global__ void __launch_bounds__(kThreads) norm_rope_any_kernel(const RopeArgs 
   }
 }
 
-template <bool kSrcBf16, bool kDstBf16>
-cudaError_t launch_rope(const RopeArgs& a, bool wide, cudaStream_t stream) {
+template <bool kSrcBf16, bool kDstBf16, int kC>
+cudaError_t launch_wide(const RopeArgs& a, cudaStream_t stream) {
   const int total = a.heads[0] + a.heads[1];
-  if (!wide) {
-    const int64_t ctas = (a.tq * total + kThreads / 32 - 1) / (kThreads / 32);
-    if (ctas > 0x7FFFFFFF) return cudaErrorNotSupported;
-    norm_rope_any_kernel<kSrcBf16, kDstBf16>
-        <<<static_cast<unsigned>(ctas), kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
-  }
-  const int units = a.head_dim / 8;
+  const int units = a.head_dim / (2 * kC);
   const int lanes = units <= 4 ? 4 : units <= 8 ? 8 : units <= 16 ? 16 : 32;
   const int groups = kThreads / lanes;
   // Prompts: four tokens a CTA, whose groups walk over the heads in `turns` turns of kRows.  Few
   // tokens: one, and its heads over several CTAs, so that a row is all that a group does.  A turn
-  // takes about half as long as a round of CTAs: 32 + 8 heads of 128 in bf16, four tokens / one token
-  // a CTA: 64 tokens (4 turns, 1 round) 7.4 / 3.5 us, 256 (2 rounds) 7.7 / 6.2, 400 (3 rounds) 7.6 /
-  // 8.1, 2000 19.7 / 31.8; 8 + 1 heads (1 turn): 500 tokens (2 rounds) 4.2 / 5.8.
-  const int64_t slots = 3ll * device_sm_count();
+  // takes about half as long as a round of CTAs: 32 + 8 heads of 128 in f32, four tokens / one token
+  // a CTA: 64 tokens (4 turns, 1 round) 7.9 / 3.9 us, 256 (2 rounds) 8.0 / 6.0, 400 (3 rounds) 8.0 /
+  // 8.3, 2000 23.3 / 34.5; in bf16 (2 turns) 64 (1 round) 5.6 / 3.5, 256 (2 rounds) 5.8 / 6.0, 800
+  // 7.3 / 10.9; 8 + 1 heads (1 turn): 500 tokens (2 rounds) 4.3 / 5.8.  Eight tokens
+  // in place of four, bf16: 800 tokens 9.1, 5000 27.9 against 27.3.
+  const int64_t slots = static_cast<int64_t>(kMinCtas) * device_sm_count();
   const int64_t rounds = (a.tq * ((total + groups - 1) / groups) + slots - 1) / slots;
-  const int64_t turns = (4ll * total + 3 * groups - 1) / (3 * groups);
+  const int64_t turns = (4ll * total + kRows * groups - 1) / (kRows * groups);
   const bool few = 2 * rounds <= turns + 1;
   const int log_tokens = few ? 0 : 2;
   const int heads_per_cta = few ? groups : total;
@@ -365,14 +429,32 @@ cudaError_t launch_rope(const RopeArgs& a, bool wide, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy));
   auto go = [&](auto kernel) { kernel<<<grid, kThreads, 0, stream>>>(a, log_tokens, heads_per_cta); };
   if (lanes == 4)
-    go(norm_rope_kernel<kSrcBf16, kDstBf16, 4>);
+    go(norm_rope_kernel<kSrcBf16, kDstBf16, kC, 4>);
   else if (lanes == 8)
-    go(norm_rope_kernel<kSrcBf16, kDstBf16, 8>);
+    go(norm_rope_kernel<kSrcBf16, kDstBf16, kC, 8>);
   else if (lanes == 16)
-    go(norm_rope_kernel<kSrcBf16, kDstBf16, 16>);
-  else
-    go(norm_rope_kernel<kSrcBf16, kDstBf16, 32>);
+    go(norm_rope_kernel<kSrcBf16, kDstBf16, kC, 16>);
+  else if constexpr (kC == 4)
+    go(norm_rope_kernel<kSrcBf16, kDstBf16, kC, 32>);
   return cudaGetLastError();
+}
+
+// piece: channels of a piece that sizes, strides and alignment allow (8, 4, or 0: none).
+template <bool kSrcBf16, bool kDstBf16>
+cudaError_t launch_rope(const RopeArgs& a, int piece, cudaStream_t stream) {
+  if (piece == 0) {
+    const int64_t rows = a.tq * (a.heads[0] + a.heads[1]);
+    const int64_t ctas = (rows + kThreads / 32 - 1) / (kThreads / 32);
+    if (ctas > 0x7FFFFFFF) return cudaErrorNotSupported;
+    norm_rope_any_kernel<kSrcBf16, kDstBf16>
+        <<<static_cast<unsigned>(ctas), kThreads, 0, stream>>>(a);
+    return cudaGetLastError();
+  }
+  // 4 channels of f32 fill the 16 bytes of an access: 8 would make two half-filled ones of each (3900
+  // tokens of 28 + 4 heads, bf16 to f32: 20.7 us with 4, 24.4 with 8)
+  if constexpr (kSrcBf16 && kDstBf16)
+    if (piece == 8) return launch_wide<kSrcBf16, kDstBf16, 8>(a, stream);
+  return launch_wide<kSrcBf16, kDstBf16, 4>(a, stream);
 }
 
 bool activation_type(sa_dtype t) { return t == SA_DTYPE_F32 || t == SA_DTYPE_BF16; }
@@ -443,25 +525,29 @@ extern "C" sa_status sa_norm_rope(
   a.rot = rot_dim;
   a.interleaved = interleaved != 0;
   a.status = status;
-  // loads and stores of 4-channel pieces (8 or 16 bytes): everything a multiple of them
-  auto whole = [](const void* p, sa_dtype type) {
-    return (reinterpret_cast<uintptr_t>(p) & (type == SA_DTYPE_BF16 ? 7u : 15u)) == 0;
+  // loads and stores of pieces of 4 or 8 channels, at most 16 bytes: everything a multiple of them
+  auto fits = [&](int c) {
+    auto whole = [&](const void* p, sa_dtype type) {
+      const uintptr_t bytes = c * (type == SA_DTYPE_BF16 ? 2 : 4);
+      return (reinterpret_cast<uintptr_t>(p) & ((bytes < 16 ? bytes : 16) - 1)) == 0;
+    };
+    bool ok = head_dim % (2 * c) == 0 && rot_dim % (2 * c) == 0;
+    for (int i = 0; i < 2; ++i)
+      ok = ok && (a.heads[i] == 0 ||
+                  (whole(a.src[i], src_dtype) && whole(a.dst[i], out_dtype) &&
+                   ((a.token_stride[i] | a.head_stride[i] | a.dst_token_stride[i] | a.dst_head_stride[i]) &
+                    (c - 1)) == 0));
+    return ok;
   };
-  bool wide = head_dim % 8 == 0 && rot_dim % 8 == 0;
-  for (int i = 0; i < 2; ++i) {
-    if (a.heads[i] == 0) continue;
-    wide = wide && whole(a.src[i], src_dtype) && whole(a.dst[i], out_dtype) &&
-           whole(a.weight[i], weight_dtype) &&
-           ((a.token_stride[i] | a.head_stride[i] | a.dst_token_stride[i] | a.dst_head_stride[i]) & 3) == 0;
-  }
+  const int piece = fits(8) ? 8 : fits(4) ? 4 : 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t err;
   if (src_dtype == SA_DTYPE_BF16)
-    err = out_dtype == SA_DTYPE_BF16 ? sa::launch_rope<true, true>(a, wide, s)
-                                     : sa::launch_rope<true, false>(a, wide, s);
+    err = out_dtype == SA_DTYPE_BF16 ? sa::launch_rope<true, true>(a, piece, s)
+                                     : sa::launch_rope<true, false>(a, piece, s);
   else
-    err = out_dtype == SA_DTYPE_BF16 ? sa::launch_rope<false, true>(a, wide, s)
-                                     : sa::launch_rope<false, false>(a, wide, s);
+    err = out_dtype == SA_DTYPE_BF16 ? sa::launch_rope<false, true>(a, piece, s)
+                                     : sa::launch_rope<false, false>(a, piece, s);
   if (err == cudaErrorNotSupported) return SA_ERR_UNSUPPORTED;
   return err == cudaSuccess ? SA_OK : SA_ERR_CUDA;
 }

@@ -98,6 +98,18 @@ def test_head_sizes(d, rot, interleaved):
     run(11, 5, 3, d, rot, "bf16", "f32", interleaved, seed=1)
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("d,rot", [(16, 16), (64, 32), (80, 48), (256, 256), (256, 16), (144, 0),
+                                   (48, 24), (24, 24), (200, 192)])
+def test_head_sizes_of_bf16(d, rot, interleaved):
+    """Pieces of 8 channels and of 4, the latter also where only the start or a stride forbids 8; more
+    than one turn of a group over its heads."""
+    run(11, 5, 3, d, rot, "bf16", "bf16", interleaved, seed=4)
+    run(11, 5, 3, d, rot, "bf16", "bf16", interleaved, offset=4, seed=5)
+    run(9, 5, 3, d, rot, "bf16", "bf16", interleaved, norm=False, seed=6)
+    run(501, 70, 3, d, rot, "bf16", "bf16", interleaved, seed=7)
+
+
 @pytest.mark.parametrize("tq,hq,hkv", [(1, 1, 1), (1, 64, 8), (3, 1, 0), (5, 0, 2), (700, 7, 1),
                                        (1025, 40, 8), (4, 300, 5)])
 def test_counts(tq, hq, hkv):
