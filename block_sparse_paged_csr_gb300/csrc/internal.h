@@ -241,6 +241,16 @@ constexpr int decode_max_warps(int dp, int r) {
 // rounded up to 64, 128 or 256; r: query rows of a tile).
 constexpr int decode_state_floats(int dp, int r) { return r * dp + 3 * r; }
 
+// Whether rows of head_dim channels at these strides (elements) certainly share elements: what
+// no output may do.  (A stride that nothing is multiplied by does not count.)
+inline bool rows_overlap(int64_t tokens, int64_t heads, int64_t head_dim, int64_t token_stride,
+                         int64_t head_stride) {
+  auto short_of = [&](int64_t n, int64_t stride) { return n > 1 && stride > -head_dim && stride < head_dim; };
+  return tokens > 0 && heads > 0 &&
+         (short_of(tokens, token_stride) || short_of(heads, head_stride));
+}
+
+
 struct DecodeArgs {
   const void* q;            // f32, or bf16 when act_bf16 (out too)
   const void* k_pages;

@@ -216,9 +216,15 @@ extern "C" sa_status sa_load_kv(const void* k_pages, const void* v_pages, const 
   if (sa::eight_bit(kv_dtype) && (!k_scales || !v_scales)) return SA_ERR_INVALID_ARGUMENT;
   if (!sa::aligned16(k) || !sa::aligned16(v) || !sa::aligned16(k_pages) || !sa::aligned16(v_pages))
     return SA_ERR_INVALID_ARGUMENT;
+  // (with one token or one head its stride says nothing, and may be anything)
+  if (tq == 1) k_token_stride = v_token_stride = 0;
+  if (hkv == 1) k_head_stride = v_head_stride = 0;
   const int64_t unit = dst_dtype == SA_DTYPE_BF16 ? 8 : 4;      // elements of 16 bytes
   if (k_token_stride % unit || k_head_stride % unit || v_token_stride % unit ||
       v_head_stride % unit)
+    return SA_ERR_INVALID_ARGUMENT;
+  if (sa::rows_overlap(tq, hkv, head_dim, k_token_stride, k_head_stride) ||
+      sa::rows_overlap(tq, hkv, head_dim, v_token_stride, v_head_stride))
     return SA_ERR_INVALID_ARGUMENT;
 
   sa::LoadArgs a{};

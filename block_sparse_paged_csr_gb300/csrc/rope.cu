@@ -492,6 +492,9 @@ extern "C" sa_status sa_norm_rope(
   if ((hq > 0 && (!q || !q_out)) || (hkv > 0 && (!k || !k_out)) || (rot_dim > 0 && !inv_freq) ||
       (rot_dim > 0 && n_axes > 0 && !positions) || (by_lengths && (!cu_seqlens_q || !used_kv_lens)))
     return SA_ERR_INVALID_ARGUMENT;
+  if (sa::rows_overlap(tq, hq, head_dim, q_out_token_stride, q_out_head_stride) ||
+      sa::rows_overlap(tq, hkv, head_dim, k_out_token_stride, k_out_head_stride))
+    return SA_ERR_INVALID_ARGUMENT;
 
   sa::RopeArgs a{};
   a.src[0] = q;

@@ -688,15 +688,16 @@ sa_status sa_select_blocks(const void *q, sa_dtype q_dtype, int64_t tq, int32_t 
  *                 turns pair i (needs positions; NULL: axis 0)
  *   q_out, k_out  as q and k, of out_dtype (f32 or bf16), strides of their own.
  *                 An output may be its input (same address, type and strides);
- *                 other overlaps are not allowed.
+ *                 other overlaps are not allowed, of an output's own rows neither.
  *   status        as for sa_store_kv
  *
  * Supported: head_dim <= 256, any strides and alignment (fastest where head_dim
- * and rot_dim are multiples of 8 and every row starts on 4 channels).  Checks,
+ * and rot_dim are multiples of 8 and every row starts on 4 channels; in bf16 to
+ * bf16 of 16, and on 8 channels).  Checks,
  * in order: HEAD_COUNT (hq + hkv = 0), HEAD_DIM (rot_dim odd or above head_dim),
  * SHAPE (tq, n_axes), CU_SEQLENS and SHAPE (n_axes = 0), INVALID_ARGUMENT (types, eps
  * negative or NaN, freq_axes without positions), UNSUPPORTED, INVALID_ARGUMENT
- * (NULL); on device: SHAPE (an axis outside [0, n_axes), taken as axis 0).
+ * (NULL; strides of an output below head_dim, of more than one token or head); on device: SHAPE (an axis outside [0, n_axes), taken as axis 0).
  */
 sa_status sa_norm_rope(const void *q, const void *k, sa_dtype src_dtype, int64_t q_token_stride,
                        int64_t q_head_stride, int64_t k_token_stride, int64_t k_head_stride,
@@ -718,7 +719,8 @@ sa_status sa_norm_rope(const void *q, const void *k, sa_dtype src_dtype, int64_t
  *
  *   k, v          [tq, hkv, head_dim] of dst_dtype (f32 or bf16), written;
  *                 channels contiguous, tokens and heads at the given strides
- *                 (elements; multiples of 16 bytes)
+ *                 (elements; multiples of 16 bytes, head_dim at least, where
+ *                 there is more than one token or head)
  *
  * Other arguments as for sa_store_kv.  Values of 8-bit caches are code * scale in
  * f32, rounded to nearest even for bf16 (scales that sa_store_kv made are powers

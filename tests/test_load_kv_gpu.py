@@ -119,6 +119,21 @@ def test_graph():
     assert torch.equal(k, k2) and torch.equal(v, v2)
 
 
+def test_strides_of_a_single_row_say_nothing():
+    """One row of one head out of a tensor of odd sizes."""
+    c = Cache([30], "bf16", 1, 64, 16)
+    cu = np.array([0, 1])
+    wide = torch.zeros((3, 3, 65), device="cuda")
+    k, v = (wide[i:i + 1].as_strided((1, 1, 64), (195, 65, 1), 256 * i) for i in (0, 1))
+    sa.sa_load_kv(*c.pages, c.table, cu, on_gpu(cu, np.int64), c.used, k=k, v=v)
+    for which, g in enumerate((k, v)):
+        np.testing.assert_array_equal(f64(g), c.rows(0, [29], which)[0])
+    rows = torch.zeros((1, 1, 64), device="cuda").expand(2, 1, 64)
+    cu = np.array([0, 2])
+    with pytest.raises(sa.SAError):
+        sa.sa_load_kv(*c.pages, c.table, cu, on_gpu(cu, np.int64), c.used, k=rows, v=rows)
+
+
 def test_refusals():
     c = Cache([30], "int8", 2, 64, 16)
     cu = np.array([0, 30])

@@ -84,6 +84,17 @@ def test_load_checks(lib):
     assert load(lib, cu=np.array([0, 0, 0], np.int64), tq=0, k=None, v=None) == 0
 
 
+def test_rows_of_an_output_that_share_elements(lib):
+    for st in ((0, 64, 128, 64), (128, 0, 128, 64), (128, 64, 60, 64), (128, 64, 128, -32)):
+        assert load(lib, st=st) == 11, st
+
+    def rope_out(*st):
+        return lib.sa_norm_rope(P, P, F32, 256, 64, 128, 64, P, P, F32, 1e-6, P, 64, None, 0, P, 1, 5, None,
+                                None, 0, None, 5, 4, 2, 64, P, P, F32, *st, None, None)
+    for st in ((0, 64, 128, 64), (256, 63, 128, 64), (256, 64, -1, 64), (256, 64, 128, 0)):
+        assert rope_out(*st) == 11, st
+
+
 def decode(lib, q=P, act=F32, kp=P, vp=P, ks=P, vs=P, n=4, kind=INT8, bt=P, cols=2, used=P, batch=2,
            hq=4, hkv=2, d=64, ps=16, window=0, out=P, lse=P, ws=P, nbytes=1 << 30):
     return lib.sa_decode_attention(q, act, kp, vp, ks, vs, n, kind, bt, cols, used, batch, hq, hkv, d, ps,
