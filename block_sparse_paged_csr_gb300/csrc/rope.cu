@@ -20,8 +20,12 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxTokens = 4;                 // tokens per CTA
-constexpr int kRows = 3;                      // rows that a lane has in flight
-constexpr int kMinCtas = 3;                   // CTAs per SM that the registers have to leave room for
+// Rows that a lane has in flight, and CTAs per SM that the registers have to leave room for, by the
+// source's type and the channels of a piece.
+template <bool kSrcBf16, int kC>
+constexpr int kRowsOf = kSrcBf16 && kC == 4 ? 4 : 3;
+template <int kC>
+constexpr int kMinCtas = kC == 8 ? 3 : 4;
 
 struct RopeArgs {
   const void* src[2];                         // q, k
@@ -163,15 +167,19 @@ __device__ __forceinline__ void store_piece(void* p, int64_t off, const pair_t (
 // at a time, all asked for before the first is used: angles are made once per
 // token and pair, by the CTA, and stay in registers; weights come from shared memory.
 //
-// Bound by memory from some thousand tokens on: 8192 of 64 + 8 heads of 128 in f32 (604 MB) 99.5 us,
-// 6.1 TB/s; 32768 in bf16 (1.2 GB) 210 us, 5.7 TB/s.  bf16 is bound by instructions as soon as
-// they are not few: 4 channels a piece and one number an operation took 288 us there, 8 and two
-// numbers take 210.  What counts besides is rows in flight against registers (bf16, 32768 tokens):
-// 3 rows and 3 CTAs an SM 211 us, 2 and 3 221, 2 and 4 211, 3 and 2 248, 4 and 2 247.
+// Bound by memory from some thousand tokens on: 8192 of 64 + 8 heads of 128 in f32 (604 MB) 97 us,
+// 6.2 TB/s, 32768 356 us, 6.8; 32768 in bf16 (1.2 GB) 210 us, 5.7 TB/s.  bf16 is bound by instructions
+// as soon as they are not few: 4 channels a piece and one number an operation took 288 us there, 8
+// and two numbers take 210.  What counts besides is rows in flight against CTAs an SM:
+//   bf16, 8 channels, 32768 tokens: 3 rows and 3 CTAs 211 us, 2 and 3 221, 2 and 4 211, 3 and 2 248;
+//   f32, 2048 tokens / 8192: 3 and 4 29.7 / 97.5, 3 and 3 37.4 / 99.7, 2 and 4 29.5 / 100.5, 2 and
+//   5 (spilling) 30.6 / 98.2, 4 and 3 36.7 / 98.6;
+//   bf16 to f32, 4 channels, 32768: 4 and 4 282, 3 and 4 292, 2 and 4 313.
 template <bool kSrcBf16, bool kDstBf16, int kC, int kLanes>
-__global__ void __launch_bounds__(kThreads, kMinCtas)
+__global__ void __launch_bounds__(kThreads, kMinCtas<kC>)
 norm_rope_kernel(const RopeArgs a, int log_tokens, int heads_per_cta) {
   constexpr int kGroups = kThreads / kLanes;
+  constexpr int kRows = kRowsOf<kSrcBf16, kC>;
   __shared__ int s_pos[kMaxTokens];
   __shared__ __align__(16) float s_cos[kMaxTokens * 128], s_sin[kMaxTokens * 128];
   __shared__ __align__(16) float s_w[2][256];
@@ -410,14 +418,15 @@ cudaError_t launch_wide(const RopeArgs& a, cudaStream_t stream) {
   const int units = a.head_dim / (2 * kC);
   const int lanes = units <= 4 ? 4 : units <= 8 ? 8 : units <= 16 ? 16 : 32;
   const int groups = kThreads / lanes;
+  constexpr int kRows = kRowsOf<kSrcBf16, kC>;
   // Prompts: four tokens a CTA, whose groups walk over the heads in `turns` turns of kRows.  Few
   // tokens: one, and its heads over several CTAs, so that a row is all that a group does.  A turn
   // takes about half as long as a round of CTAs: 32 + 8 heads of 128 in f32, four tokens / one token
-  // a CTA: 64 tokens (4 turns, 1 round) 7.9 / 3.9 us, 256 (2 rounds) 8.0 / 6.0, 400 (3 rounds) 8.0 /
-  // 8.3, 2000 23.3 / 34.5; in bf16 (2 turns) 64 (1 round) 5.6 / 3.5, 256 (2 rounds) 5.8 / 6.0, 800
-  // 7.3 / 10.9; 8 + 1 heads (1 turn): 500 tokens (2 rounds) 4.3 / 5.8.  Eight tokens
-  // in place of four, bf16: 800 tokens 9.1, 5000 27.9 against 27.3.
-  const int64_t slots = static_cast<int64_t>(kMinCtas) * device_sm_count();
+  // a CTA: 64 tokens (4 turns, 1 round) 7.6 / 3.8 us, 256 (2 rounds) 8.0 / 6.2, 400 (2 rounds) 7.8 /
+  // 6.8, 800 (4 rounds) 11.0 / 12.2, 2000 17.7 / 29.2; in bf16 (2 turns) 64 (1 round) 5.6 / 3.5, 256
+  // (2 rounds) 5.8 / 6.0, 800 7.3 / 10.9; 8 + 1 heads (1 turn): 500 tokens (2 rounds) 4.3 / 5.8.  Eight
+  // tokens in place of four, bf16: 800 tokens 9.1, 5000 27.9 against 27.3.
+  const int64_t slots = static_cast<int64_t>(kMinCtas<kC>) * device_sm_count();
   const int64_t rounds = (a.tq * ((total + groups - 1) / groups) + slots - 1) / slots;
   const int64_t turns = (4ll * total + kRows * groups - 1) / (kRows * groups);
   const bool few = 2 * rounds <= turns + 1;
