@@ -26,6 +26,13 @@ template <bool kSrcBf16, int kC>
 constexpr int kRowsOf = kSrcBf16 && kC == 4 ? 4 : 3;
 template <int kC>
 constexpr int kMinCtas = kC == 8 ? 3 : 4;
+// Tokens of a CTA that walks over their heads, as a power of two: more of them make fewer CTAs with
+// longer tails, fewer of them fewer rows after the angles.  1 / 2 / 4 tokens, heads of 128, us: f32 8192
+// tokens of 64 + 8 heads 93.1 / 93.3 / 97.8, 800 of 32 + 8 10.5 / 8.5 / 11.3, 5000 44.4 / 38.6 / 40.5;
+// bf16 to f32 8192 of 64 + 8 80.4 / 76.4 / 79.4; bf16 70.6 / 66.1 / 59.1, 5000 of 32 + 8 41.4 / 33.5 /
+// 27.2, 800 7.7 / 6.2 / 7.1 (8 tokens: 27.9 and 9.1).
+template <int kC>
+constexpr int kLogTokens = kC == 8 ? 2 : 1;
 
 struct RopeArgs {
   const void* src[2];                         // q, k
@@ -167,11 +174,12 @@ __device__ __forceinline__ void store_piece(void* p, int64_t off, const pair_t (
 // at a time, all asked for before the first is used: angles are made once per
 // token and pair, by the CTA, and stay in registers; weights come from shared memory.
 //
-// Bound by memory from some thousand tokens on: 8192 of 64 + 8 heads of 128 in f32 (604 MB) 97 us,
-// 6.2 TB/s, 32768 356 us, 6.8; 32768 in bf16 (1.2 GB) 210 us, 5.7 TB/s.  bf16 is bound by instructions
+// Bound by memory from some thousand tokens on: 8192 of 64 + 8 heads of 128 in f32 (604 MB) 93 us,
+// 6.5 TB/s, 32768 350 us, 6.9; 32768 in bf16 (1.2 GB) 210 us, 5.7 TB/s.  bf16 is bound by instructions
 // as soon as they are not few: 4 channels a piece and one number an operation took 288 us there, 8
 // and two numbers take 210.  What counts besides is rows in flight against CTAs an SM:
 //   bf16, 8 channels, 32768 tokens: 3 rows and 3 CTAs 211 us, 2 and 3 221, 2 and 4 211, 3 and 2 248;
+// and, with four tokens a CTA,
 //   f32, 2048 tokens / 8192: 3 and 4 29.7 / 97.5, 3 and 3 37.4 / 99.7, 2 and 4 29.5 / 100.5, 2 and
 //   5 (spilling) 30.6 / 98.2, 4 and 3 36.7 / 98.6;
 //   bf16 to f32, 4 channels, 32768: 4 and 4 282, 3 and 4 292, 2 and 4 313.
@@ -419,18 +427,17 @@ cudaError_t launch_wide(const RopeArgs& a, cudaStream_t stream) {
   const int lanes = units <= 4 ? 4 : units <= 8 ? 8 : units <= 16 ? 16 : 32;
   const int groups = kThreads / lanes;
   constexpr int kRows = kRowsOf<kSrcBf16, kC>;
-  // Prompts: four tokens a CTA, whose groups walk over the heads in `turns` turns of kRows.  Few
-  // tokens: one, and its heads over several CTAs, so that a row is all that a group does.  A turn
-  // takes about half as long as a round of CTAs: 32 + 8 heads of 128 in f32, four tokens / one token
-  // a CTA: 64 tokens (4 turns, 1 round) 7.6 / 3.8 us, 256 (2 rounds) 8.0 / 6.2, 400 (2 rounds) 7.8 /
-  // 6.8, 800 (4 rounds) 11.0 / 12.2, 2000 17.7 / 29.2; in bf16 (2 turns) 64 (1 round) 5.6 / 3.5, 256
-  // (2 rounds) 5.8 / 6.0, 800 7.3 / 10.9; 8 + 1 heads (1 turn): 500 tokens (2 rounds) 4.3 / 5.8.  Eight
-  // tokens in place of four, bf16: 800 tokens 9.1, 5000 27.9 against 27.3.
+  // Prompts: two or four tokens a CTA, whose groups walk over the heads in `turns` turns of kRows.
+  // Few tokens: one, and its heads over several CTAs, so that a row is all that a group does.  A turn
+  // takes about half as long as a round of CTAs: 32 + 8 heads of 128, several tokens / one token a
+  // CTA, us: f32 64 tokens (2 turns, 1 round) 5.2 / 3.8, 128 (1 round) 5.4 / 4.2, 256 (2 rounds) 5.7 /
+  // 6.2, 800 (4 rounds) 8.7 / 12.3; bf16 (2 turns) 64 (1 round) 5.6 / 3.5, 256 (2 rounds) 5.8 / 6.0,
+  // 800 7.3 / 10.9; 8 + 1 heads (1 turn): bf16 500 tokens (2 rounds) 4.3 / 5.8.
   const int64_t slots = static_cast<int64_t>(kMinCtas<kC>) * device_sm_count();
   const int64_t rounds = (a.tq * ((total + groups - 1) / groups) + slots - 1) / slots;
-  const int64_t turns = (4ll * total + kRows * groups - 1) / (kRows * groups);
+  const int64_t turns = ((static_cast<int64_t>(total) << kLogTokens<kC>) + kRows * groups - 1) / (kRows * groups);
   const bool few = 2 * rounds <= turns + 1;
-  const int log_tokens = few ? 0 : 2;
+  const int log_tokens = few ? 0 : kLogTokens<kC>;
   const int heads_per_cta = few ? groups : total;
   const int64_t gx = (a.tq + (int64_t{1} << log_tokens) - 1) >> log_tokens;
   const int64_t gy = (total + heads_per_cta - 1) / heads_per_cta;
