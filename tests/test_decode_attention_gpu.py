@@ -332,6 +332,62 @@ def test_a_query_that_is_no_number_stays_its_own():
         assert torch.equal(out[keep], ref[keep]) and torch.equal(lse[keep], rlse[keep])
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_a_key_or_value_that_is_no_number_stays_its_own(kind):
+    """NaN in one row of K comes out for its sequence and kv head, in one row of V for its channel,
+    whole pairs and merged ones alike; all else keeps its bits."""
+    for lens, b, at in (([5, 40, 33], 1, 17), ([5, 60000, 33], 1, 41234)):
+        c = Cache(lens, kind, 2, 64, 16, poison=False)
+        q = torch.randn((3, 8, 64), device="cuda")
+        ref, rlse = sa.sa_decode_attention(q, *c.pages, c.table, c.used, 0.1)
+        page = int(c.bt[b, at // 16])
+        old = c.pages[1][page, 1, at % 16, 3].clone()
+        c.pages[1][page, 1, at % 16, 3] = math.nan
+        out, lse = sa.sa_decode_attention(q, *c.pages, c.table, c.used, 0.1)
+        hit = torch.zeros((3, 8, 64), dtype=torch.bool, device="cuda")
+        hit[b, 4:, 3] = True
+        assert torch.isnan(out[hit]).all() and torch.equal(out[~hit], ref[~hit])
+        assert torch.equal(lse, rlse)
+        c.pages[1][page, 1, at % 16, 3] = old
+        c.pages[0][page, 1, at % 16, 3] = math.nan
+        out, lse = sa.sa_decode_attention(q, *c.pages, c.table, c.used, 0.1)
+        hit[b, 4:] = True
+        assert torch.isnan(out[hit]).all() and torch.equal(out[~hit], ref[~hit])
+        rows = hit.any(2)
+        assert torch.isnan(lse[rows]).all() and torch.equal(lse[~rows], rlse[~rows])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("window", [1, 15, 100])
+def test_rows_before_a_window_are_not_read(kind, window):
+    """No numbers in the rows before it, within the tile where it starts too, nor in the scales of
+    pages that lie before it as a whole."""
+    lens, ps = [90, 257, 300, 31], 16
+    c = Cache(lens, kind, 2, 64, ps, seed=window)
+    for b, n in enumerate(lens):
+        for p in range(max(n - window, 0)):
+            page = int(c.bt[b, p // ps])
+            for x in c.pages:
+                if kind == "int8":
+                    x[page, :, p % ps] = -128
+                elif kind == "e4m3":
+                    x.view(torch.uint8)[page, :, p % ps] = 0x7F
+                else:
+                    x[page, :, p % ps] = math.nan
+            if c.eight and p % ps == ps - 1:
+                for s in c.scales:
+                    s[page] = math.nan
+    for act in ("f32", "bf16"):
+        check(c, 6, act, window=window)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_softmax_scales_of_any_sign(kind):
+    c = Cache([0, 40, 300], kind, 2, 64, 16)
+    for scale in (0.0, -0.125, 2.0 ** -60, 1.5):
+        check(c, 6, scale=scale)
+
+
 def test_refusals():
     c = Cache([30, 7], "int8", 2, 64, 16)
     q = torch.randn((2, 4, 64), device="cuda")
