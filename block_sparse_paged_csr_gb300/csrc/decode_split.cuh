@@ -202,7 +202,9 @@ __device__ __forceinline__ Keys keys_of(const DecodeArgs& a, int used) {
   Keys k;
   used = max(used, 0);
   k.end = min(used, a.capacity);
-  k.first = a.window > 0 ? max(used - a.window, 0) : 0;
+  // (a length may stand far past the table: a window that begins behind it holds no keys, and
+  // positions stay far from 2^31)
+  k.first = a.window > 0 ? min(max(used - a.window, 0), k.end) : 0;
   return k;
 }
 template <int KT>

@@ -214,6 +214,34 @@ def test_lengths_past_the_table():
     assert (out == 0).all() and torch.isneginf(lse).all()
 
 
+@pytest.mark.parametrize("d", [64, 256])
+@pytest.mark.parametrize("kind", KINDS)
+def test_windows_of_lengths_up_to_the_largest(kind, d):
+    """A window behind the table's columns holds no keys, wherever it begins: its positions, rounded up
+    to tiles, would pass 2^31.  One that reaches back into the table holds what is there."""
+    top = 2 ** 31 - 1
+    c = Cache([40, 40, 33, 40, 7], kind, 2, d, 16, seed=d)
+    q = torch.randn((5, 4, d), device="cuda")
+    for window in (1, 2, 7, 16, 30, 31, 32, 100):
+        used = on_gpu([top, top - 1, 33, top - 15, 7], np.int32)
+        status = torch.zeros(1, dtype=torch.int64, device="cuda")
+        out, lse = sa.sa_decode_attention(q, *c.pages, c.table, used, 0.1, window=window, status=status,
+                                          **c.kw())
+        # (sequences without keys cut the work alike)
+        same, slse = sa.sa_decode_attention(q, *c.pages, c.table, on_gpu([0, 0, 33, 0, 7], np.int32), 0.1,
+                                            window=window, **c.kw())
+        assert int(status) == 0 and torch.equal(out, same) and torch.equal(lse, slse)
+        assert (out[[0, 1, 3]] == 0).all() and torch.isneginf(lse[[0, 1, 3]]).all()
+    c = Cache([48, 40, 33, 48, 7], kind, 2, d, 16, seed=d, poison=False)
+    for far, window, near, short in (([top, 40, 33, top, 7], top, c.lens, 0),
+                                     ([1000, 18, 17, 1000, 7], 970, [48, 18, 17, 48, 7], 18)):
+        out, lse = sa.sa_decode_attention(q, *c.pages, c.table, on_gpu(far, np.int32), 0.1, window=window,
+                                          **c.kw())
+        same, slse = sa.sa_decode_attention(q, *c.pages, c.table, on_gpu(near, np.int32), 0.1,
+                                            window=short, **c.kw())
+        assert torch.equal(out, same) and torch.equal(lse, slse)
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_repeats_and_shared_workspace(kind):
     """The same bits again; one workspace for calls of other sizes, whatever it holds."""
