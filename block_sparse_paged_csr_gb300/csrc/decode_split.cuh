@@ -70,9 +70,7 @@ struct Cfg {
   static constexpr int kNS = DP / (8 * kEP);                    // .. times
   static constexpr int kNJ = DP / 8;                            // n-tiles of o
   static constexpr int kNR = R / 8;                             // query rows of a lane
-  // bf16 queries over 8 bits: o stays in the tensor cores' accumulators (see values)
-  static constexpr bool kDirect = B && k8;
-  static constexpr int kOW = kDirect ? 4 : 2 * kNR;             // numbers of o of an n-tile
+  static constexpr int kOW = 2 * kNR;                           // numbers of o of an n-tile
   // operands of Q kept per k-step (see keep_q), and of P
   static constexpr int kQP = kF32 ? 1 : k8 ? (R == 8 || B ? 1 : 2) : B ? 1 : R == 8 ? 2 : 3;
   static constexpr int kPP = kF32 ? 1 : k8 ? (R == 8 || B ? 1 : 2) : R == 8 ? (B ? 1 : 2) : (B ? 2 : 3);
@@ -250,7 +248,7 @@ struct Worker {
   };
 
   // ---- state of the piece at hand
-  float o[C::kNJ][C::kOW];       // columns 2 c, + 1 of row g, then of row g + 8 (R = 8: its second parts)
+  float o[C::kNJ][C::kOW];       // columns 2 c, + 1 of row g, then of row g + 8
   float m_run[C::kNR], n_run[C::kNR], l_part[C::kNR], vfac[C::kNR], sfac[C::kNR];
   bool clamp;                    // some V scale is beyond kRoom
 
@@ -639,7 +637,7 @@ struct Worker {
         for (int j = 0; j < C::kNJ; ++j)
 #pragma unroll
           for (int i = 0; i < C::kOW; ++i)
-            if (R == 8 || i / 2 == r) o[j][i] *= beta;
+            if (i / 2 == r) o[j][i] *= beta;
 #pragma unroll
         for (int n = 0; n < C::kNT; ++n) {
           p[n][2 * r] -= m_new;
@@ -665,14 +663,13 @@ struct Worker {
   // for channel 8 kEP s + kEP n + i.
   // A tile's products are summed by the tensor cores from zero and added to o by rounding
   // additions.  The tensor cores cut a sum to 24 bits, so that an o that runs through
-  // them loses 2^-25 of itself on average at every step, always towards zero: 1.4e-5 over 64
-  // sequences of 4096 to 32768 bf16 keys (6e-7 with the additions).  Over 8 bits, where
-  // instructions count, the additions cost 7 %; bf16 queries do without: n steps of
-  // one warp (16 keys each) make n 2^-26, a quarter of the output's half step after
-  // 500,000 keys.
+  // them is cut at every step, always towards zero: 1.4e-5 over 64 sequences of 4096 to 32768
+  // bf16 keys (6e-7 with the additions), 2.4e-4 over 1700 tiles of 8 bits a warp.  Over 8 bits, where
+  // instructions count, the additions cost 4 to 8 % (bf16 queries, 8 q-heads a kv head, 32 sequences of
+  // 20000 to 50000 keys: e4m3 394 -> 409 us, int8 405 -> 437).
   __device__ __forceinline__ void values(int e, const float (&p)[C::kNT][2 * C::kNR]) {
     // k-steps summed together (those of o one by one: fewer registers at a time)
-    constexpr int kK = C::kDirect ? 1 : C::kKT / C::kKK;
+    constexpr int kK = C::kKT / C::kKK;
     const unsigned char* vt = ring + e * C::kEntry;
     const float* vs = sc + e * C::kKT;
 #pragma unroll
@@ -756,50 +753,54 @@ struct Worker {
           for (int i = 0; i < kPer; ++i)
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-              sum[i][x] = C::kDirect ? o[C::kEP * s + kPer * q + i][x % C::kOW] : 0.f;
+              sum[i][x] = 0.f;
+          if constexpr (C::kF32) {
 #pragma unroll
-          for (int kt = 0; kt < kK; ++kt) {
-            const auto& v = y[kt];
-            if constexpr (C::kF32) {
+            for (int kt = 0; kt < kK; ++kt) {
+              const auto& v = y[kt];
               uint32_t h0, l0, h1, l1;
               split_tf32(__uint_as_float(v[0][q]), h0, l0);
               split_tf32(__uint_as_float(v[1][q]), h1, l1);
               mma<T>(sum[0], pa[kt][0], l0, l1);
               mma<T>(sum[0], pa[kt][0], h0, h1);
-            } else {
-              uint32_t b[kPer][2];
+            }
+          } else {
+            uint32_t b[kK][kPer][2];
+#pragma unroll
+            for (int kt = 0; kt < kK; ++kt) {
+              const auto& v = y[kt];
               if constexpr (C::k8) {
                 constexpr bool kI8 = T == SA_DTYPE_INT8;
-                codes4_to_f16<kI8>(__byte_perm(v[0][q], v[1][q], 0x5140), b[0][0], b[1][0]);
-                codes4_to_f16<kI8>(__byte_perm(v[0][q], v[1][q], 0x7362), b[2][0], b[3][0]);
-                codes4_to_f16<kI8>(__byte_perm(v[2][q], v[3][q], 0x5140), b[0][1], b[1][1]);
-                codes4_to_f16<kI8>(__byte_perm(v[2][q], v[3][q], 0x7362), b[2][1], b[3][1]);
+                codes4_to_f16<kI8>(__byte_perm(v[0][q], v[1][q], 0x5140), b[kt][0][0], b[kt][1][0]);
+                codes4_to_f16<kI8>(__byte_perm(v[0][q], v[1][q], 0x7362), b[kt][2][0], b[kt][3][0]);
+                codes4_to_f16<kI8>(__byte_perm(v[2][q], v[3][q], 0x5140), b[kt][0][1], b[kt][1][1]);
+                codes4_to_f16<kI8>(__byte_perm(v[2][q], v[3][q], 0x7362), b[kt][2][1], b[kt][3][1]);
               } else {
-                b[0][0] = __byte_perm(v[0][q], v[1][q], 0x5410);
-                b[1][0] = __byte_perm(v[0][q], v[1][q], 0x7632);
+                b[kt][0][0] = __byte_perm(v[0][q], v[1][q], 0x5410);
+                b[kt][1][0] = __byte_perm(v[0][q], v[1][q], 0x7632);
                 if constexpr (kVR == 4) {
-                  b[0][1] = __byte_perm(v[2][q], v[3][q], 0x5410);
-                  b[1][1] = __byte_perm(v[2][q], v[3][q], 0x7632);
+                  b[kt][0][1] = __byte_perm(v[2][q], v[3][q], 0x5410);
+                  b[kt][1][1] = __byte_perm(v[2][q], v[3][q], 0x7632);
                 }
               }
+            }
 #pragma unroll
-              for (int x = C::kPP - 1; x >= 0; --x)              // (small parts first)
+            for (int x = C::kPP - 1; x >= 0; --x) {              // (small parts first)
+#pragma unroll
+              for (int kt = 0; kt < kK; ++kt)
 #pragma unroll
                 for (int i = 0; i < kPer; ++i) {
                   if constexpr (C::kKK == 8)
-                    mma_k8(sum[i], pa[kt][x].x, pa[kt][x].y, b[i][0]);
+                    mma_k8(sum[i], pa[kt][x].x, pa[kt][x].y, b[kt][i][0]);
                   else
-                    mma<T>(sum[i], pa[kt][x], b[i][0], b[i][1]);
+                    mma<T>(sum[i], pa[kt][x], b[kt][i][0], b[kt][i][1]);
                 }
             }
           }
 #pragma unroll
           for (int i = 0; i < kPer; ++i) {
             const int j = C::kEP * s + kPer * q + i;
-            if constexpr (C::kDirect) {
-#pragma unroll
-              for (int x = 0; x < 4; ++x) o[j][x] = sum[i][x];
-            } else if constexpr (R == 8) {                       // the remainders' row joins its own
+            if constexpr (R == 8) {                              // the remainders' row joins its own
               add2(sum[i][0], sum[i][1], sum[i][2], sum[i][3]);
               add2(o[j][0], o[j][1], sum[i][0], sum[i][1]);
             } else {
@@ -813,7 +814,7 @@ struct Worker {
   }
 
   __device__ __forceinline__ float at(int j, int r, int e) const {
-    return C::kDirect && R == 8 ? o[j][e] + o[j][C::kOW - 2 + e] : o[j][2 * r + e];
+    return o[j][2 * r + e];
   }
   __device__ __forceinline__ float row_sum(int r) const {
     float l = l_part[r];
@@ -880,7 +881,6 @@ struct Worker {
         for (int r = 0; r < C::kNR; ++r) {
           const float v = from[((2 * j + e) * C::kNR + r) * 32 + lane];
           const float sum = fmaf(f_other[r], v, f_own[r] * at(j, r, e));
-          if constexpr (C::kDirect && R == 8) o[j][C::kOW - 2 + e] = 0.f;
           o[j][2 * r + e] = sum;
         }
   }
