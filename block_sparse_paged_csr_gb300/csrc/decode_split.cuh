@@ -73,7 +73,7 @@ struct Cfg {
   static constexpr int kOW = 2 * kNR;                           // numbers of o of an n-tile
   // operands of Q kept per k-step (see keep_q), and of P
   static constexpr int kQP = kF32 ? 1 : k8 ? (R == 8 || B ? 1 : 2) : B ? 1 : R == 8 ? 2 : 3;
-  static constexpr int kPP = kF32 ? 1 : k8 ? (R == 8 || B ? 1 : 2) : R == 8 ? (B ? 1 : 2) : (B ? 2 : 3);
+  static constexpr int kPP = kF32 ? 1 : k8 ? (R == 8 ? 1 : 2) : R == 8 ? (B ? 1 : 2) : (B ? 2 : 3);
   // (the third parts of R = 8 leave half of their operand zero, which is not stored)
   static constexpr bool kHalfQ = !kF32 && !k8 && R == 8 && !B;
   static constexpr int kQBytes = kF32 ? kKS / 2 * 512 : kHalfQ ? kKS * 768 : kKS * kQP * 512;
@@ -665,8 +665,8 @@ struct Worker {
   // additions.  The tensor cores cut a sum to 24 bits, so that an o that runs through
   // them is cut at every step, always towards zero: 1.4e-5 over 64 sequences of 4096 to 32768
   // bf16 keys (6e-7 with the additions), 2.4e-4 over 1700 tiles of 8 bits a warp.  Over 8 bits, where
-  // instructions count, the additions cost 4 to 8 % (bf16 queries, 8 q-heads a kv head, 32 sequences of
-  // 20000 to 50000 keys: e4m3 394 -> 409 us, int8 405 -> 437).
+  // instructions count, the additions and P's second part cost 2 to 3 % (bf16 queries, 8 q-heads a kv head, 32 sequences of
+  // 20000 to 50000 keys: e4m3 394 -> 400 us, int8 405 -> 413).
   __device__ __forceinline__ void values(int e, const float (&p)[C::kNT][2 * C::kNR]) {
     // k-steps summed together (those of o one by one: fewer registers at a time)
     constexpr int kK = C::kKT / C::kKK;
@@ -699,17 +699,14 @@ struct Worker {
                   f0 = fminf(fmaxf(f0, -FLT_MAX), FLT_MAX);
                   f1 = fminf(fmaxf(f1, -FLT_MAX), FLT_MAX);
                 }
-                if constexpr (B)
-                  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(hi[r][x]) : "f"(p1 * f1), "f"(p0 * f0));
-                else
-                  split_f16(p0 * f0, p1 * f1, hi[r][x], mid[r][x]);
+                split_f16(p0 * f0, p1 * f1, hi[r][x], mid[r][x]);
               } else {
                 split_bf16(p0, p1, hi[r][x], mid[r][x], lo[r][x]);
               }
             }
           }
-          // bf16 queries over 8 bits: one f16 part (2^-12 of P, an eighth of the output's half
-          // step); over bf16 two parts (16 bits)
+          // over 8 bits two f16 parts, which with 8 rows cost no product (rows g + 8); bf16 queries over
+          // bf16: two parts (16 bits)
           if constexpr (R == 8) {
             pa[kt][0] = make_uint4(hi[0][0], mid[0][0], hi[0][1], mid[0][1]);
             if constexpr (C::kPP == 2) pa[kt][1] = make_uint4(lo[0][0], 0u, lo[0][1], 0u);

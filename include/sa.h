@@ -767,7 +767,7 @@ sa_status sa_load_kv(const void *k_pages, const void *v_pages, const float *k_sc
  * (infinities and NaN there do not matter); a key or value in sight that is not finite
  * makes its rows' results unspecified.  Scores, softmax sums and outputs are
  * summed in f32.  f32 queries keep 22 bits or more of every operand; bf16 queries
- * take P in 11 (8-bit caches) or 16 bits (bf16), below the output's rounding.
+ * over a bf16 cache take P in 16 bits, below the output's rounding.
  * Results do not depend on timing: the same call on the same GPU gives the same bits.
  * Enqueues two kernels and allocates nothing.
  *

@@ -38,6 +38,36 @@ def half_step(x):
     return torch.exp2(torch.floor(torch.log2(x.clamp(min=1e-30))) - 8)
 
 
+@pytest.mark.parametrize("g", [4, 12])
+@pytest.mark.parametrize("kind", ["f32", "e4m3", "int8"])
+def test_bf16_outputs_are_the_formulas_rounded_once(kind, g):
+    """bf16 queries: what comes out is the formula's value rounded once, but for the f32 arithmetic
+    before it.  Three keys a sequence (one tile, no merges) with scores near 0, so that this arithmetic
+    is known closely: a score of at most big = sum |q k| scale is off by 2 (d + 16) 2^-24 big (d
+    roundings, 16 more for operands in parts, doubled for the tensor cores' cuts) and 3 2^-24 in base 2;
+    numerator and denominator have it both, with 2^-22 of ex2; P's parts and V's (f32) leave 2^-21
+    each, sums and the quotient some 10 roundings.  All of it relative to sum p |v|: signs that cancel make it
+    large beside the output's own half step."""
+    n, d, hkv, batch = 3, 64, 4, 1500
+    gen = torch.Generator(device="cuda").manual_seed(g)
+    (kp, vp), (k, v), kw = pools((batch, hkv, n, d), kind, gen)
+    q = (0.002 * torch.randn((batch, hkv * g, d), generator=gen, device="cuda")).bfloat16()
+    table = torch.randperm(batch, generator=gen, device="cuda").to(torch.int32)[:, None].contiguous()
+    used = torch.full((batch,), n, dtype=torch.int32, device="cuda")
+    out, _ = sa.sa_decode_attention(q, kp, vp, table, used, 0.125, **kw)
+    at = table[:, 0].long()
+    x = q.double().view(batch, hkv, g, d) * 0.125
+    big = float((x.abs() @ k[at].abs().transpose(2, 3)).max())
+    p = torch.softmax(x @ k[at].transpose(2, 3), 3)
+    ref, size = p @ v[at], p @ v[at].abs()
+    part = 2 * (2 * (d + 16) * U * big + 3 * U) + 2 * 2.0 ** -22 + 2 * 2.0 ** -21 + 10 * U
+    assert part < 2.0 ** -18
+    off = part * size
+    err = (out.double().view_as(ref) - ref).abs()
+    wrong = int((~(err <= off + half_step(ref.abs() + off))).sum())
+    assert wrong == 0, f"{wrong} of {err.numel()}"
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_long_sums_of_bf16_queries_do_not_drift(kind):
     """Sums over many tiles by one warp, 1024 sequences of 65536 keys that share their pages: at least
