@@ -171,6 +171,14 @@ __device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
       : "f"(a), "f"(b));
 }
 
+// (x, y) += (a, b) f, one instruction.
+__device__ __forceinline__ void fma2(float& x, float& y, float a, float b, float f) {
+  asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
+      "mov.b64 r, {%4, %4};\n\tfma.rn.f32x2 p, q, r, p;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b), "f"(f));
+}
+
 // f32 as a tf32 high part (cut) and the rest, rounded to tf32's 11 bits: 2^-21 of x
 // is lost at most.
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
@@ -182,6 +190,16 @@ __device__ __forceinline__ void split_f16(float x0, float x1, uint32_t& hi, uint
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(x1), "f"(x0));
   const float2 h = f16x2_to_f32(hi);
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(x1 - h.y), "f"(x0 - h.x));
+}
+// The same with the remainders times 1 / kRest: they stay in f16's normal range as long as the value
+// is above 2^-25, and end at 2^-36 of the unit instead of 2^-25.
+constexpr float kRest = 0x1p-11f;
+__device__ __forceinline__ void split_f16_apart(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(x1), "f"(x0));
+  const float2 h = f16x2_to_f32(hi);
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;"
+      : "=r"(lo)
+      : "f"((x1 - h.y) * (1.f / kRest)), "f"((x0 - h.x) * (1.f / kRest)));
 }
 // Two values as three bf16 parts (24 bits together).
 __device__ __forceinline__ void split_bf16(float x0, float x1, uint32_t& hi, uint32_t& mid,
@@ -666,7 +684,9 @@ struct Worker {
   // them is cut at every step, always towards zero: 1.4e-5 over 64 sequences of 4096 to 32768
   // bf16 keys (6e-7 with the additions), 2.4e-4 over 1700 tiles of 8 bits a warp.  Over 8 bits, where
   // instructions count, the additions and P's second part cost 2 to 3 % (bf16 queries, 8 q-heads a kv head, 32 sequences of
-  // 20000 to 50000 keys: e4m3 394 -> 400 us, int8 405 -> 413).
+  // 20000 to 50000 keys: e4m3 394 -> 400 us, int8 405 -> 416).
+  // Over 8 bits what P vs loses to f16 stays in a second part, 2^11 times as large (see split_f16_apart): with
+  // 8 rows in rows g + 8, with 16 in products of its own, made first and scaled before the others join.
   __device__ __forceinline__ void values(int e, const float (&p)[C::kNT][2 * C::kNR]) {
     // k-steps summed together (those of o one by one: fewer registers at a time)
     constexpr int kK = C::kKT / C::kKK;
@@ -699,14 +719,13 @@ struct Worker {
                   f0 = fminf(fmaxf(f0, -FLT_MAX), FLT_MAX);
                   f1 = fminf(fmaxf(f1, -FLT_MAX), FLT_MAX);
                 }
-                split_f16(p0 * f0, p1 * f1, hi[r][x], mid[r][x]);
+                split_f16_apart(p0 * f0, p1 * f1, hi[r][x], mid[r][x]);
               } else {
                 split_bf16(p0, p1, hi[r][x], mid[r][x], lo[r][x]);
               }
             }
           }
-          // over 8 bits two f16 parts, which with 8 rows cost no product (rows g + 8); bf16 queries over
-          // bf16: two parts (16 bits)
+          // bf16 queries over bf16: two parts (16 bits)
           if constexpr (R == 8) {
             pa[kt][0] = make_uint4(hi[0][0], mid[0][0], hi[0][1], mid[0][1]);
             if constexpr (C::kPP == 2) pa[kt][1] = make_uint4(lo[0][0], 0u, lo[0][1], 0u);
@@ -792,13 +811,24 @@ struct Worker {
                   else
                     mma<T>(sum[i], pa[kt][x], b[kt][i][0], b[kt][i][1]);
                 }
+              if constexpr (C::k8) {
+                if (x > 0) {
+#pragma unroll
+                  for (int i = 0; i < kPer; ++i)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) sum[i][k] *= kRest;
+                }
+              }
             }
           }
 #pragma unroll
           for (int i = 0; i < kPer; ++i) {
             const int j = C::kEP * s + kPer * q + i;
             if constexpr (R == 8) {                              // the remainders' row joins its own
-              add2(sum[i][0], sum[i][1], sum[i][2], sum[i][3]);
+              if constexpr (C::k8)
+                fma2(sum[i][0], sum[i][1], sum[i][2], sum[i][3], kRest);
+              else
+                add2(sum[i][0], sum[i][1], sum[i][2], sum[i][3]);
               add2(o[j][0], o[j][1], sum[i][0], sum[i][1]);
             } else {
               add2(o[j][0], o[j][1], sum[i][0], sum[i][1]);

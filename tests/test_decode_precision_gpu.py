@@ -68,6 +68,59 @@ def test_bf16_outputs_are_the_formulas_rounded_once(kind, g):
     assert wrong == 0, f"{wrong} of {err.numel()}"
 
 
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("g", [4, 12])
+@pytest.mark.parametrize("kind", KINDS)
+def test_a_key_that_takes_nearly_all_leaves_the_others_their_bits(kind, g, act):
+    """One key among 32768 holds all but some 2^-13 of the softmax, its V row is 0 (and shares its page
+    with ordinary rows), so that the output is the others' alone: products of 2^-28 of the largest.
+    Tolerance, relative to their sum p |v|: twice the scores' errors (theirs are small; the large one's
+    is common to all in l: 2 (d + 16) 2^-24 of its size), and over 8 bits the parts' last unit: the
+    remainder of a product keeps 2^-36 of a unit of which the largest counts 2^3 or more, 2^-39 of the
+    largest P vs a key, times its code.  These roundings are independent: their sum over the keys has
+    a deviation below sqrt(n) 2^-39 128 (448) and is taken six times.  (In f16 without the remainders'
+    own scale 2^-28 a key: that is as large as the products.)"""
+    n, d, hkv, ps, batch = 32768, 64, 2, 64, 1300
+    gen = torch.Generator(device="cuda").manual_seed(g)
+    (kp, vp), _, kw = pools((n // ps, hkv, ps, d), kind, gen)
+    for name in kw:
+        kw[name].fill_(2.0 ** -6)
+    # channel 0 is the large key's: 8 in the queries, 1 in its row, 0 in the other keys'
+    page, row = 11, 37
+    kp.view(torch.uint8).view(*kp.shape, -1)[..., 0, :] = 0
+    key = torch.zeros((hkv, d), device="cuda")
+    key[:, 0] = 64.0 if kw else 1.0
+    kp[page, :, row] = key.to(TORCH[kind])
+    vp[page, :, row] = torch.zeros((hkv, d), device="cuda").to(TORCH[kind])
+    scale = (math.log(n) + 13 * math.log(2.0)) / 8.0        # its score: 19.4
+    q = torch.randn((batch, hkv * g, d), generator=gen, device="cuda") * 0.1 / scale
+    q[..., 0] = 8.0                                         # (the others' scores: some 0.1 sqrt(d))
+    q = q.to(TORCH[act])
+    # (the sequences share their pages, so that a warp has the large key and many others in one piece)
+    table = torch.randperm(n // ps, generator=gen, device="cuda").to(torch.int32).repeat(batch, 1)
+    used = torch.full((batch,), n, dtype=torch.int32, device="cuda")
+    out, _ = sa.sa_decode_attention(q, kp, vp, table, used, scale, **kw)
+    kk, vv = ((x.float().double() * (2.0 ** -6 if kw else 1)).transpose(0, 1).reshape(hkv, n, d) for x in (kp, vp))
+    for b in range(0, batch, 29):
+        x = q[b].double().view(hkv, g, d) * scale
+        p = torch.softmax(x @ kk.transpose(1, 2), 2)
+        ref, size = p @ vv, p @ vv.abs()
+        held = p[:, :, page * ps + row]
+        assert 2.0 ** -15 < float((1 - held).min()) and float((1 - held).max()) < 2.0 ** -11
+        big = (x.abs() @ kk.abs().transpose(1, 2)).amax(2)[..., None]
+        tol = (2 * 2 * (d + 16) * U * (big + 1) + 3 * U * (big + 1)) * size
+        if kw:
+            tol = tol + 6 * math.sqrt(n) * 2.0 ** -39 * held[..., None] * 2.0 ** -6 * (
+                128 if kind == "int8" else 448)
+        # what the tolerance leaves of the others' part
+        assert float((tol / size).median()) < 2.0 ** -8
+        if act == "bf16":
+            tol = tol + half_step(ref.abs() + tol)
+        err = (out[b].double().view_as(ref) - ref).abs()
+        worst = float((err / tol).nan_to_num(nan=math.inf).max())
+        assert worst <= 1
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_long_sums_of_bf16_queries_do_not_drift(kind):
     """Sums over many tiles by one warp, 1024 sequences of 65536 keys that share their pages: at least
