@@ -73,7 +73,7 @@ struct Cfg {
   static constexpr int kOW = 2 * kNR;                           // numbers of o of an n-tile
   // operands of Q kept per k-step (see keep_q), and of P
   static constexpr int kQP = kF32 ? 1 : k8 ? (R == 8 || B ? 1 : 2) : B ? 1 : R == 8 ? 2 : 3;
-  static constexpr int kPP = kF32 ? 1 : k8 ? (R == 8 ? 1 : 2) : R == 8 ? (B ? 1 : 2) : (B ? 2 : 3);
+  static constexpr int kPP = kF32 ? 1 : k8 ? (R == 8 ? 1 : 2) : R == 8 ? 2 : 3;
   // (the third parts of R = 8 leave half of their operand zero, which is not stored)
   static constexpr bool kHalfQ = !kF32 && !k8 && R == 8 && !B;
   static constexpr int kQBytes = kF32 ? kKS / 2 * 512 : kHalfQ ? kKS * 768 : kKS * kQP * 512;
@@ -684,7 +684,7 @@ struct Worker {
   // them is cut at every step, always towards zero: 1.4e-5 over 64 sequences of 4096 to 32768
   // bf16 keys (6e-7 with the additions), 2.4e-4 over 1700 tiles of 8 bits a warp.  Over 8 bits, where
   // instructions count, the additions and P's second part cost 2 to 3 % (bf16 queries, 8 q-heads a kv head, 32 sequences of
-  // 20000 to 50000 keys: e4m3 394 -> 400 us, int8 405 -> 416).
+  // 20000 to 50000 keys: e4m3 394 -> 400 us, int8 405 -> 415).
   // Over 8 bits what P vs loses to f16 stays in a second part, 2^11 times as large (see split_f16_apart): with
   // 8 rows in rows g + 8, with 16 in products of its own, made first and scaled before the others join.
   __device__ __forceinline__ void values(int e, const float (&p)[C::kNT][2 * C::kNR]) {
@@ -725,7 +725,6 @@ struct Worker {
               }
             }
           }
-          // bf16 queries over bf16: two parts (16 bits)
           if constexpr (R == 8) {
             pa[kt][0] = make_uint4(hi[0][0], mid[0][0], hi[0][1], mid[0][1]);
             if constexpr (C::kPP == 2) pa[kt][1] = make_uint4(lo[0][0], 0u, lo[0][1], 0u);

@@ -766,9 +766,8 @@ sa_status sa_load_kv(const void *k_pages, const void *v_pages, const float *k_sc
  * Nothing that stands at other positions of the pages is read into a result
  * (infinities and NaN there do not matter); a key or value in sight that is not finite
  * makes its rows' results unspecified.  Scores, softmax sums and outputs are
- * summed in f32, from operands in parts that keep 22 bits or more (bf16 queries over a
- * bf16 cache take P in 16 bits, below the output's rounding).  Over 8 bits these are parts
- * of f16: 2^-35 of a query row's largest channel may be lost, and of a weight
+ * summed in f32, from operands in parts that keep 22 bits or more.  Over 8 bits these are
+ * parts of f16: 2^-35 of a query row's largest channel may be lost, and of a weight
  * times the V scale of its page 2^-39 of the largest such product of the row.
  * Results do not depend on timing: the same call on the same GPU gives the same bits.
  * Enqueues two kernels and allocates nothing.

@@ -39,7 +39,7 @@ def half_step(x):
 
 
 @pytest.mark.parametrize("g", [4, 12])
-@pytest.mark.parametrize("kind", ["f32", "e4m3", "int8"])
+@pytest.mark.parametrize("kind", KINDS)
 def test_bf16_outputs_are_the_formulas_rounded_once(kind, g):
     """bf16 queries: what comes out is the formula's value rounded once, but for the f32 arithmetic
     before it.  Three keys a sequence (one tile, no merges) with scores near 0, so that this arithmetic
