@@ -7,8 +7,9 @@
 //
 // Angles: f32 products p f lose the angle (p = 131072 leaves 2^-7 radians), so
 // f / (2 pi) is taken as a 64-bit fraction of a turn.  Its product with the integer p
-// wraps at whole turns by itself; the error is |p| 2^-64 turns, and the upper 32 bits
-// of the product go to sincospif.
+// wraps at whole turns by itself; the error is |p| (1 + |f| / 256) 2^-64 turns.  What lies beyond the
+// nearest quarter of a turn, an eighth at most, goes to sincospif in f32 (2^-28 turns; a
+// whole turn in f32 would be rounded by 2^-26), and the quarters turn its results.
 #include <cstdint>
 
 #include "internal.h"
@@ -57,24 +58,27 @@ struct RopeArgs {
 };
 
 // f / (2 pi) as a fraction of a turn, times 2^64 (whole turns dropped).  With f = M
-// 2^(e - 150) and C = 2^66 / (2 pi): M C 2^(e - 152), formed as the upper half of
-// (M 2^40) C, shifted by e - 128.
+// 2^(e - 150) and C = 2^66 / (2 pi) (the 64 bits kept are 2^-6 off): M C 2^(e - 152), formed as the
+// upper half of (M 2^40) C, shifted by e - 128; a shift up (f of 2 and more) brings in the lower half.
 __device__ __forceinline__ uint64_t turn_fraction(float f) {
   const uint32_t u = __float_as_uint(f);
   const int e = static_cast<int>((u >> 23) & 0xFFu);
   const uint64_t m = (u & 0x7FFFFFu) | (e ? 0x800000u : 0u);
-  const uint64_t hi = __umul64hi(m << 40, 0xA2F9836E4E44152Aull);
+  constexpr uint64_t kC = 0xA2F9836E4E44152Aull;
+  const uint64_t hi = __umul64hi(m << 40, kC), lo = (m << 40) * kC;
   const int s = (e ? e : 1) - 128;
-  const uint64_t v = s <= -64 || s >= 64 ? 0ull : s < 0 ? hi >> -s : hi << s;
+  const uint64_t v = s <= -64 || s >= 64 ? 0ull : s < 0 ? hi >> -s : s == 0 ? hi : hi << s | lo >> (64 - s);
   return (u >> 31) ? 0ull - v : v;
 }
 
 __device__ __forceinline__ float2 cos_sin(uint64_t turns, int pos) {
   const uint64_t t = turns * static_cast<uint64_t>(static_cast<int64_t>(pos));
-  const int half_turns = static_cast<int>(static_cast<int64_t>(t) >> 32);
-  float2 r;
-  sincospif(__int2float_rn(half_turns) * 0x1p-31f, &r.y, &r.x);
-  return r;
+  const uint64_t quarters = (t + (1ull << 61)) >> 62;
+  float s, c;
+  sincospif(__ll2float_rn(static_cast<int64_t>(t - (quarters << 62))) * 0x1p-63f, &s, &c);
+  const float x = quarters & 1 ? s : c, y = quarters & 1 ? c : s;
+  // (cosine's sign turns in the second and third quarter, sine's in the third and fourth)
+  return make_float2((quarters + 1) & 2 ? -x : x, quarters & 2 ? -y : y);
 }
 
 // Position of token `tok` where the call gives lengths: its sequence's last tokens

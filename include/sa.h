@@ -670,8 +670,8 @@ sa_status sa_select_blocks(const void *q, sa_dtype q_dtype, int64_t tq, int32_t 
  *
  * with (a, b) = (i, i + rot_dim / 2), or (2 i, 2 i + 1) where `interleaved` is not 0;
  * channels from rot_dim on are not rotated.  Sums are f32 (a row with magnitudes
- * beyond 1e18 overflows its sum of squares), angles exact to 2^-31 turns at any
- * 32-bit position, and each output is rounded once.
+ * beyond 1e18 overflows its sum of squares), angles within 2^-27 turns at any 32-bit
+ * position (frequencies up to 256), and each output is rounded once.
  *
  *   q, k          [tq, hq, head_dim], [tq, hkv, head_dim] of src_dtype (f32 or
  *                 bf16); channels contiguous, tokens and heads at the given

@@ -173,6 +173,42 @@ def test_frequencies_of_any_size():
     assert (err[ok] <= 40 * 2.0 ** -24 * size[ok]).all()
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_angles_near_quarter_turns(interleaved):
+    """The angle's own error, seen where cosine or sine is small: rows (1, 0) come out as both.  The angle
+    is rounded to f32 within an eighth of a turn of the nearest quarter, 2^-28 turns, after products that
+    are 2^-32 off (frequencies up to 256); sincospi's results are 2 ulp off, 2 2^-23 relative.  (Rounded
+    as a part of a whole turn it would be 2^-26 off, and from frequencies of 4 on, without the product's
+    lower bits, more.)  Positions whose turns lie near a quarter are looked for."""
+    from decimal import Decimal, getcontext
+    getcontext().prec = 60
+    two_pi = Decimal("6.28318530717958647692528676655900576839433879875021164194989")
+    f = np.array([1.0, 0.7, 0.01, 1e-4, -0.3, 5.0, 100.0, 250.0], np.float32)
+    rng = np.random.default_rng(1)
+    pos, turns = [], []
+    for fi in f:
+        x = np.concatenate([rng.integers(0, 2 ** 31, 20000), rng.integers(0, 4000, 500),
+                            [0, 1, 2 ** 31 - 1, -2 ** 31]])
+        t = x.astype(np.longdouble) * np.longdouble(fi) * 4 / (2 * np.pi)
+        x = x[np.argsort(np.abs(t - np.rint(t)))[:60]]
+        pos.append(x)
+        turns.append([float((Decimal(int(p)) * Decimal(float(fi)) / two_pi) % 1) for p in x])
+    pos = np.concatenate(pos)                       # [8 * 60] tokens, each for one of the pairs
+    own = np.repeat(np.arange(8), 60)
+    x = torch.zeros((len(pos), 1, 16), device="cuda")
+    a, b = (slice(0, 16, 2), slice(1, 16, 2)) if interleaved else (slice(0, 8), slice(8, 16))
+    x[..., a] = 1
+    got, _ = sa.sa_norm_rope(x, None, None, None, on_gpu(f, np.float32), positions=on_gpu(pos, np.int32),
+                             interleaved=interleaved)
+    i = np.arange(len(pos))
+    cos, sin = f64(got)[i, 0, a][i, own], f64(got)[i, 0, b][i, own]
+    t = 2 * np.pi * np.concatenate(turns)
+    angle = 2 * np.pi * (2.0 ** -28 + 2.0 ** -32)
+    for y, ref, slope in ((cos, np.cos(t), np.sin(t)), (sin, np.sin(t), np.cos(t))):
+        err, tol = np.abs(y - ref), angle * np.abs(slope) + 2.0 ** -22 * np.abs(ref) + 2.0 ** -50
+        assert (err <= tol).all(), (err / tol).max()
+
+
 def test_in_place_and_other_strides():
     run(21, 4, 2, 128, 128, "bf16", "bf16", inplace=True)
     run(21, 4, 2, 36, 20, "f32", "f32", True, inplace=True)
