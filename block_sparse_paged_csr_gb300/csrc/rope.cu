@@ -512,6 +512,10 @@ extern "C" sa_status sa_norm_rope(
   if ((hq > 0 && (!q || !q_out)) || (hkv > 0 && (!k || !k_out)) || (rot_dim > 0 && !inv_freq) ||
       (rot_dim > 0 && n_axes > 0 && !positions) || (by_lengths && (!cu_seqlens_q || !used_kv_lens)))
     return SA_ERR_INVALID_ARGUMENT;
+  // (with one token or one head its stride says nothing, and may be anything)
+  if (tq == 1) q_token_stride = k_token_stride = q_out_token_stride = k_out_token_stride = 0;
+  if (hq == 1) q_head_stride = q_out_head_stride = 0;
+  if (hkv == 1) k_head_stride = k_out_head_stride = 0;
   if (sa::rows_overlap(tq, hq, head_dim, q_out_token_stride, q_out_head_stride) ||
       sa::rows_overlap(tq, hkv, head_dim, k_out_token_stride, k_out_head_stride))
     return SA_ERR_INVALID_ARGUMENT;

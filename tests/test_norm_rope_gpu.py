@@ -224,6 +224,25 @@ def test_in_place_and_other_strides():
     assert torch.equal(out.transpose(0, 1), same)
 
 
+@pytest.mark.parametrize("tq,hq,hkv", [(1, 40, 8), (300, 1, 1), (1, 1, 1)])
+@pytest.mark.parametrize("src,out", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32")])
+def test_strides_that_nothing_is_multiplied_by(src, out, tq, hq, hkv):
+    """Of a single token or a single head: whatever they are, the same bits by the same kernel."""
+    d = 128
+    gen = torch.Generator(device="cuda").manual_seed(tq + hq)
+    q, k = (torch.randn((tq, h, d), generator=gen, device="cuda").to(TORCH[src]) for h in (hq, hkv))
+    w = torch.rand(d, generator=gen, device="cuda").to(TORCH[src])
+    f = on_gpu(freqs(d), np.float32)
+    pos = torch.arange(tq, dtype=torch.int32, device="cuda") + 100
+
+    def odd(x):
+        return x.as_strided(x.shape, (777 if tq == 1 else x.stride(0), 3 if x.shape[1] == 1 else d, 1))
+    a, b = sa.sa_norm_rope(q, k, w, w, f, positions=pos, out_dtype=TORCH[out])
+    qo, ko = (torch.empty(x.shape, dtype=TORCH[out], device="cuda") for x in (q, k))
+    c, e = sa.sa_norm_rope(odd(q), odd(k), w, w, f, positions=pos, q_out=odd(qo), k_out=odd(ko))
+    assert torch.equal(a, c) and torch.equal(b, e)
+
+
 def test_positions_from_lengths():
     """The new tokens end at the sequence's length; sequences without new tokens, one
     shorter than its new tokens; both kernels; rows behind the last one stay."""
