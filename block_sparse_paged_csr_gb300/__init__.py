@@ -972,6 +972,8 @@ def sa_norm_rope(q, k, q_weight, k_weight, inv_freq, positions=None, cu_seqlens_
         if positions.dim() not in (1, 2) or positions.shape[-1] != tq:
             raise ValueError(f"positions must be [{tq}] or [axes, {tq}]")
         axes = 1 if positions.dim() == 1 else positions.shape[0]
+        if axes > 1 and rot and freq_axes is None:
+            raise ValueError(f"freq_axes must say which of the {axes} axes turns each pair")
         positions = positions.data_ptr()
     elif rot:
         if cu_seqlens_q_host is None or cu_seqlens_q is None or used_kv_lens is None:

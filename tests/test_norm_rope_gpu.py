@@ -361,3 +361,19 @@ def test_refusals():
        used_kv_lens=on_gpu([5, 5], np.int32))
     empty, none = sa.sa_norm_rope(x[:0], None, None, None, f, positions=pos[:0])
     assert empty.shape == (0, 2, 32) and none is None
+
+
+def test_several_axes_need_freq_axes():
+    """Without them every pair would be turned by the first axis, and nobody asked for that."""
+    x = torch.randn((4, 2, 32), device="cuda")
+    f = on_gpu(freqs(32), np.float32)
+    pos = torch.arange(12, dtype=torch.int32, device="cuda").view(3, 4)
+    for kw in (dict(), dict(q_out=torch.empty_like(x))):
+        with pytest.raises(ValueError, match="freq_axes"):
+            sa.sa_norm_rope(x, None, None, None, f, positions=pos, **kw)
+    # one axis, however it is written, and no rotation at all
+    a, _ = sa.sa_norm_rope(x, None, None, None, f, positions=pos[:1])
+    b, _ = sa.sa_norm_rope(x, None, None, None, f, positions=pos[0].contiguous())
+    assert torch.equal(a, b)
+    a, _ = sa.sa_norm_rope(x, None, None, None, None, positions=pos)
+    assert torch.equal(a, x)
