@@ -5,6 +5,7 @@
 #include <cstddef>
 #include <cstdint>
 #include <mutex>
+#include <utility>
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -241,15 +242,28 @@ constexpr int decode_max_warps(int dp, int r) {
 // rounded up to 64, 128 or 256; r: query rows of a tile).
 constexpr int decode_state_floats(int dp, int r) { return r * dp + 3 * r; }
 
-// Whether rows of head_dim channels at these strides (elements) certainly share elements: what
-// no output may do.  (A stride that nothing is multiplied by does not count.)
+// Whether rows of head_dim channels at these strides (elements) share elements: what no
+// output may do.  (A stride that nothing is multiplied by does not count.)
 inline bool rows_overlap(int64_t tokens, int64_t heads, int64_t head_dim, int64_t token_stride,
                          int64_t head_stride) {
-  auto short_of = [&](int64_t n, int64_t stride) { return n > 1 && stride > -head_dim && stride < head_dim; };
-  return tokens > 0 && heads > 0 &&
-         (short_of(tokens, token_stride) || short_of(heads, head_stride));
+  if (tokens <= 0 || heads <= 0) return false;
+  // two rows lie |x a - y b| or x a + y b apart, x < tokens, y < heads
+  using wide = __int128;
+  wide n = tokens, m = heads, a = token_stride, b = head_stride;
+  if (a < 0) a = -a;
+  if (b < 0) b = -b;
+  if ((n > 1 && a < head_dim) || (m > 1 && b < head_dim)) return true;
+  if (n == 1 || m == 1 || a >= (m - 1) * b + head_dim || b >= (n - 1) * a + head_dim) return false;
+  if (n < m) {                     // (y over the smaller count)
+    std::swap(n, m);
+    std::swap(a, b);
+  }
+  for (wide y = 1; y < m; ++y) {
+    const wide x = y * b / a;      // the nearest multiples of a below and above
+    if ((x < n && y * b - x * a < head_dim) || (x + 1 < n && (x + 1) * a - y * b < head_dim)) return true;
+  }
+  return false;
 }
-
 
 struct DecodeArgs {
   const void* q;            // f32, or bf16 when act_bf16 (out too)

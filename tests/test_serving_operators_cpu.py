@@ -95,6 +95,34 @@ def test_rows_of_an_output_that_share_elements(lib):
         assert rope_out(*st) == 11, st
 
 
+def test_rows_of_an_output_that_meet_at_wide_strides(lib):
+    """Token and head strides of a row or more each that still put one row's elements on another's, against
+    all elements counted.  (Pages of 2^31 - 1 rows are refused after the strides: nothing is launched.)"""
+    rng = np.random.default_rng(0)
+    seen = [0, 0]
+    for _ in range(2000):
+        tokens, heads = int(rng.integers(1, 8)), int(rng.integers(8, 12))
+        ts, hs = (int(x) * 64 * int(rng.choice([-1, 1])) for x in rng.integers(4, 60, 2))
+        at = np.arange(tokens)[:, None] * ts + np.arange(heads) * hs
+        meet = len(np.unique(at[..., None] + np.arange(256))) < at.size * 256
+        for st in ((ts, hs, 1 << 20, 256), (1 << 20, 256, ts, hs)):
+            got = load(lib, hkv=heads, d=256, ps=2 ** 31 - 1, cu=np.array([0, 0, tokens], np.int64), tq=tokens,
+                       kind=F32, st=st)
+            assert got == (11 if meet else 10), (tokens, heads, st)
+        seen[meet] += 1
+    assert min(seen) > 200
+    # far strides: sums beyond 64 bits
+    for st in ((2 ** 62, 2 ** 62, 4096, 256), (-(2 ** 63), 2 ** 62, 4096, 256)):
+        assert load(lib, hkv=8, d=256, ps=2 ** 31 - 1, kind=F32, st=st) == 11
+    assert load(lib, hkv=8, d=256, ps=2 ** 31 - 1, kind=F32, st=(2 ** 62, 256, 4096, 256)) == 10
+
+    def rope_out(*st):
+        return lib.sa_norm_rope(P, P, F32, 256, 64, 128, 64, P, P, F32, 1e-6, P, 64, None, 0, P, 1, 5, None,
+                                None, 0, None, 5, 4, 2, 64, P, P, F32, *st, None, None)
+    for st in ((64, 64, 128, 64), (128, 64, 128, 64), (256, 64, 100, 100), (90, 270, 128, 64)):
+        assert rope_out(*st) == 11, st
+
+
 def decode(lib, q=P, act=F32, kp=P, vp=P, ks=P, vs=P, n=4, kind=INT8, bt=P, cols=2, used=P, batch=2,
            hq=4, hkv=2, d=64, ps=16, window=0, out=P, lse=P, ws=P, nbytes=1 << 30):
     return lib.sa_decode_attention(q, act, kp, vp, ks, vs, n, kind, bt, cols, used, batch, hq, hkv, d, ps,
