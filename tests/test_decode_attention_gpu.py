@@ -515,3 +515,60 @@ def test_pages_far_into_a_pool(kind, d):
     for got, p in ((k, small[0]), (v, small[1])):
         rows = torch.cat([p[:2].transpose(1, 2).reshape(-1, hkv, d)[:100], p[2:].transpose(1, 2).reshape(-1, hkv, d)])
         assert torch.equal(got, rows.float() * (2.0 ** -5 if kw else 1))
+
+
+@pytest.mark.parametrize("g", [5, 12])
+@pytest.mark.parametrize("kind", KINDS)
+def test_one_long_sequence_of_bf16_queries_is_split(kind, g):
+    """As above for bf16 queries, with 8 and 16 rows a tile: parts of differing references joined."""
+    check(Cache([30011], kind, 1, 64, 64, poison=False, free_scales=True), g, "bf16", qscale=4.0)
+
+
+def test_calls_side_by_side_from_two_threads():
+    """Two host threads, a stream and a workspace each, calls of all three operators that overlap on the
+    GPU: the bits of calls made alone."""
+    import threading
+
+    def work(i):
+        kind, act = (("int8", torch.bfloat16), ("bf16", torch.float32))[i]
+        c = Cache([3000, 5, 900], kind, 2, 128, 16, poison=False, seed=i)
+        gen = torch.Generator(device="cuda").manual_seed(i)
+        x = torch.randn((3, 10, 128), generator=gen, device="cuda").to(act)
+        f = on_gpu(10000.0 ** (-np.arange(64) / 64), np.float32)
+        cu = np.arange(4)
+        cud, status = on_gpu(cu, np.int64), torch.zeros(1, dtype=torch.int64, device="cuda")
+        stream, ws = torch.cuda.Stream(), sa.allocate_decode_workspace(3, 8, 2, 128, "cuda")
+
+        def step(stream=None):
+            q, _ = sa.sa_norm_rope(x[:, :8], x[:, 8:], None, None, f, cu_seqlens_q_host=cu, cu_seqlens_q=cud,
+                                   used_kv_lens=c.used, status=status, stream=stream)
+            out, lse = sa.sa_decode_attention(q, *c.pages, c.table, c.used, 0.1, workspace=ws, status=status,
+                                              stream=stream, **c.kw())
+            k, v = sa.sa_load_kv(*c.pages, c.table, cu, cud, c.used, status=status, stream=stream, **c.kw())
+            return q, out, lse, k, v
+        return step, stream, status
+
+    both = [work(i) for i in range(2)]
+    alone = [[t.clone() for t in step()] for step, _, _ in both]
+    torch.cuda.synchronize()
+    got, errors = [[], []], []
+
+    def loop(i):
+        try:
+            step, stream, _ = both[i]
+            for _ in range(40):
+                got[i].append(step(stream))
+        except Exception as e:          # (told by the main thread)
+            errors.append(e)
+
+    threads = [threading.Thread(target=loop, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+    for i in range(2):
+        assert len(got[i]) == 40 and int(both[i][2]) == 0
+        for one in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(one, alone[i]))
