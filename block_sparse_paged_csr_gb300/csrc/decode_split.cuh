@@ -73,7 +73,7 @@ struct Cfg {
   static constexpr int kOW = 2 * kNR;                           // numbers of o of an n-tile
   // operands of Q kept per k-step (see keep_q), and of P
   static constexpr int kQP = kF32 ? 1 : k8 ? (R == 8 || B ? 1 : 2) : B ? 1 : R == 8 ? 2 : 3;
-  static constexpr int kPP = kF32 ? 1 : k8 ? (R == 8 ? 1 : 2) : R == 8 ? 2 : 3;
+  static constexpr int kPP = kF32 ? 1 : k8 || kKK == 8 ? R / 8 : R == 8 ? 2 : 3;
   // (the third parts of R = 8 leave half of their operand zero, which is not stored)
   static constexpr bool kHalfQ = !kF32 && !k8 && R == 8 && !B;
   static constexpr int kQBytes = kF32 ? kKS / 2 * 512 : kHalfQ ? kKS * 768 : kKS * kQP * 512;
@@ -680,159 +680,170 @@ struct Worker {
   // o += P V.  V's rows too go to the MMA as they lie: n index of n-tile kEP s + i stands
   // for channel 8 kEP s + kEP n + i.
   // A tile's products are summed by the tensor cores from zero and added to o by rounding
-  // additions.  The tensor cores cut a sum to 24 bits, so that an o that runs through
-  // them is cut at every step, always towards zero: 1.4e-5 over 64 sequences of 4096 to 32768
-  // bf16 keys (6e-7 with the additions), 2.4e-4 over 1700 tiles of 8 bits a warp.  Over 8 bits, where
-  // instructions count, the additions and P's second part cost 2 to 3 % (bf16 queries, 8 q-heads a kv head, 32 sequences of
-  // 20000 to 50000 keys: e4m3 394 -> 400 us, int8 405 -> 415).
-  // Over 8 bits what P vs loses to f16 stays in a second part, 2^11 times as large (see split_f16_apart): with
-  // 8 rows in rows g + 8, with 16 in products of its own, made first and scaled before the others join.
+  // additions.  The tensor cores cut a sum to 24 bits, so that an o that runs through them is
+  // cut at every step, always towards zero: 1.4e-5 over 64 sequences of 4096 to 32768 bf16 keys
+  // (6e-7 with the additions), 2.4e-4 over 1700 tiles of 8 bits a warp.
+  // Over 8 bits what P vs loses to f16 stays in a second part, 2^11 times as large (see
+  // split_f16_apart): with 8 rows in rows g + 8, with 16 in products of its own, made first and
+  // scaled before the others join.  Together with the additions this costs bf16 queries, whose output
+  // hides less, 2 % with 8 q-heads a kv head and 27 % with 16 (32 sequences of 20000 to 50000 keys, without /
+  // with: e4m3 394 / 400 and 419 / 534 us, int8 405 / 415 and 475 / 601).
   __device__ __forceinline__ void values(int e, const float (&p)[C::kNT][2 * C::kNR]) {
-    // k-steps summed together (those of o one by one: fewer registers at a time)
-    constexpr int kK = C::kKT / C::kKK;
+    constexpr int kK = C::kKT / C::kKK;            // k-steps of the tile
     const unsigned char* vt = ring + e * C::kEntry;
     const float* vs = sc + e * C::kKT;
+    uint4 pa[kK][C::kPP];
 #pragma unroll
-    for (int k0 = 0; k0 < C::kKT / C::kKK; k0 += kK) {
-      uint4 pa[kK][C::kPP];
+    for (int kt = 0; kt < kK; ++kt) {
+      if constexpr (C::kF32) {
+        split_tf32(p[kt][0], pa[kt][0].x, pa[kt][0].y);
+        split_tf32(p[kt][1], pa[kt][0].z, pa[kt][0].w);
+      } else {
+        constexpr int kX = C::kKK / 8;
+        uint32_t hi[C::kNR][2] = {}, mid[C::kNR][2] = {}, lo[C::kNR][2] = {};
 #pragma unroll
-      for (int kt = 0; kt < kK; ++kt) {
-        if constexpr (C::kF32) {
-          split_tf32(p[k0 + kt][0], pa[kt][0].x, pa[kt][0].y);
-          split_tf32(p[k0 + kt][1], pa[kt][0].z, pa[kt][0].w);
-        } else {
-          constexpr int kX = C::kKK / 8;
-          uint32_t hi[C::kNR][2] = {}, mid[C::kNR][2] = {}, lo[C::kNR][2] = {};
+        for (int x = 0; x < kX; ++x) {
+          const int n = kX * kt + x;
+          float2 vf = make_float2(1.f, 1.f);
+          if constexpr (C::k8) vf = *reinterpret_cast<const float2*>(vs + 8 * n + 2 * c);
 #pragma unroll
-          for (int x = 0; x < kX; ++x) {
-            const int n = kX * (k0 + kt) + x;
-            float2 vf = make_float2(1.f, 1.f);
-            if constexpr (C::k8) vf = *reinterpret_cast<const float2*>(vs + 8 * n + 2 * c);
-#pragma unroll
-            for (int r = 0; r < C::kNR; ++r) {
-              float p0 = p[n][2 * r], p1 = p[n][2 * r + 1];
-              if constexpr (C::k8) {
-                float f0 = vf.x * vfac[r], f1 = vf.y * vfac[r];
-                if (clamp) {
-                  // (numbers: a page far above the others' scales may pass f32's range where its keys'
-                  // P is 0)
-                  f0 = fminf(fmaxf(f0, -FLT_MAX), FLT_MAX);
-                  f1 = fminf(fmaxf(f1, -FLT_MAX), FLT_MAX);
-                }
-                split_f16_apart(p0 * f0, p1 * f1, hi[r][x], mid[r][x]);
-              } else {
-                split_bf16(p0, p1, hi[r][x], mid[r][x], lo[r][x]);
+          for (int r = 0; r < C::kNR; ++r) {
+            float p0 = p[n][2 * r], p1 = p[n][2 * r + 1];
+            if constexpr (C::k8) {
+              float f0 = vf.x * vfac[r], f1 = vf.y * vfac[r];
+              if (clamp) {
+                // (numbers: a page far above the others' scales may pass f32's range where its keys'
+                // P is 0)
+                f0 = fminf(fmaxf(f0, -FLT_MAX), FLT_MAX);
+                f1 = fminf(fmaxf(f1, -FLT_MAX), FLT_MAX);
               }
+              split_f16_apart(p0 * f0, p1 * f1, hi[r][x], mid[r][x]);
+            } else {
+              split_bf16(p0, p1, hi[r][x], mid[r][x], lo[r][x]);
             }
-          }
-          if constexpr (R == 8) {
-            pa[kt][0] = make_uint4(hi[0][0], mid[0][0], hi[0][1], mid[0][1]);
-            if constexpr (C::kPP == 2) pa[kt][1] = make_uint4(lo[0][0], 0u, lo[0][1], 0u);
-          } else {
-            pa[kt][0] = make_uint4(hi[0][0], hi[1][0], hi[0][1], hi[1][1]);
-            if constexpr (C::kPP >= 2) pa[kt][1] = make_uint4(mid[0][0], mid[1][0], mid[0][1], mid[1][1]);
-            if constexpr (C::kPP >= 3) pa[kt][2] = make_uint4(lo[0][0], lo[1][0], lo[0][1], lo[1][1]);
           }
         }
-      }
-      // rows of V that a lane reads per k-step
-      constexpr int kVR = C::kKK == 16 ? 4 : 2;
-      constexpr int kWords = C::kVP / 4;
-#pragma unroll
-      for (int s = 0; s < C::kNS; ++s) {
-        uint32_t y[kK][kVR][kWords];
-#pragma unroll
-        for (int kt = 0; kt < kK; ++kt)
-#pragma unroll
-          for (int x = 0; x < kVR; ++x) {
-            const int row = C::kKK * (k0 + kt) + 2 * c + (x & 1) + 8 * (x >> 1);
-            const int sw = C::kNCH >= 8 ? row & 7 : (row >> 1) & 3;
-            if constexpr (C::kVP == 16) {
-              const uint4 u = *reinterpret_cast<const uint4*>(vt + row * C::kRow + (((8 * s + g) ^ sw) << 4));
-              y[kt][x][0] = u.x;
-              y[kt][x][1] = u.y;
-              y[kt][x][2] = u.z;
-              y[kt][x][3] = u.w;
-            } else {
-              const uint2 u = *reinterpret_cast<const uint2*>(vt + row * C::kRow + (((g >> 1) ^ sw) << 4) +
-                                                              8 * (g & 1));
-              y[kt][x][0] = u.x;
-              y[kt][x][1] = u.y;
-            }
-          }
-#pragma unroll
-        for (int q = 0; q < kWords; ++q) {
-          constexpr int kPer = C::k8 ? 4 : C::kF32 ? 1 : 2;      // channels of a word
-          float sum[kPer][4];
-#pragma unroll
-          for (int i = 0; i < kPer; ++i)
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              sum[i][x] = 0.f;
-          if constexpr (C::kF32) {
-#pragma unroll
-            for (int kt = 0; kt < kK; ++kt) {
-              const auto& v = y[kt];
-              uint32_t h0, l0, h1, l1;
-              split_tf32(__uint_as_float(v[0][q]), h0, l0);
-              split_tf32(__uint_as_float(v[1][q]), h1, l1);
-              mma<T>(sum[0], pa[kt][0], l0, l1);
-              mma<T>(sum[0], pa[kt][0], h0, h1);
-            }
+        if constexpr (C::kKK == 8) {
+          // a step of 8 keys fills half the depth of the MMA: two parts of P lie side by side in it, over
+          // the same rows of V (48 sequences, 4096 keys of 2 heads of 256: 84 us, with a product of
+          // its own for the third part 93)
+          if constexpr (R == 8) {
+            pa[kt][0] = make_uint4(hi[0][0], mid[0][0], lo[0][0], 0u);
           } else {
-            uint32_t b[kK][kPer][2];
+            pa[kt][0] = make_uint4(hi[0][0], hi[1][0], 0u, 0u);
+            pa[kt][1] = make_uint4(mid[0][0], mid[1][0], lo[0][0], lo[1][0]);
+          }
+        } else if constexpr (R == 8) {
+          pa[kt][0] = make_uint4(hi[0][0], mid[0][0], hi[0][1], mid[0][1]);
+          if constexpr (C::kPP == 2) pa[kt][1] = make_uint4(lo[0][0], 0u, lo[0][1], 0u);
+        } else {
+          pa[kt][0] = make_uint4(hi[0][0], hi[1][0], hi[0][1], hi[1][1]);
+          if constexpr (C::kPP >= 2) pa[kt][1] = make_uint4(mid[0][0], mid[1][0], mid[0][1], mid[1][1]);
+          if constexpr (C::kPP >= 3) pa[kt][2] = make_uint4(lo[0][0], lo[1][0], lo[0][1], lo[1][1]);
+        }
+      }
+    }
+    // rows of V that a lane reads per k-step
+    constexpr int kVR = C::kKK == 16 ? 4 : 2;
+    constexpr int kWords = C::kVP / 4;
 #pragma unroll
-            for (int kt = 0; kt < kK; ++kt) {
-              const auto& v = y[kt];
-              if constexpr (C::k8) {
-                constexpr bool kI8 = T == SA_DTYPE_INT8;
-                codes4_to_f16<kI8>(__byte_perm(v[0][q], v[1][q], 0x5140), b[kt][0][0], b[kt][1][0]);
-                codes4_to_f16<kI8>(__byte_perm(v[0][q], v[1][q], 0x7362), b[kt][2][0], b[kt][3][0]);
-                codes4_to_f16<kI8>(__byte_perm(v[2][q], v[3][q], 0x5140), b[kt][0][1], b[kt][1][1]);
-                codes4_to_f16<kI8>(__byte_perm(v[2][q], v[3][q], 0x7362), b[kt][2][1], b[kt][3][1]);
-              } else {
-                b[kt][0][0] = __byte_perm(v[0][q], v[1][q], 0x5410);
-                b[kt][1][0] = __byte_perm(v[0][q], v[1][q], 0x7632);
-                if constexpr (kVR == 4) {
-                  b[kt][0][1] = __byte_perm(v[2][q], v[3][q], 0x5410);
-                  b[kt][1][1] = __byte_perm(v[2][q], v[3][q], 0x7632);
-                }
-              }
-            }
+    for (int s = 0; s < C::kNS; ++s) {
+      uint32_t y[kK][kVR][kWords];
 #pragma unroll
-            for (int x = C::kPP - 1; x >= 0; --x) {              // (small parts first)
+      for (int kt = 0; kt < kK; ++kt)
 #pragma unroll
-              for (int kt = 0; kt < kK; ++kt)
+        for (int x = 0; x < kVR; ++x) {
+          const int row = C::kKK * kt + 2 * c + (x & 1) + 8 * (x >> 1);
+          const int sw = C::kNCH >= 8 ? row & 7 : (row >> 1) & 3;
+          if constexpr (C::kVP == 16) {
+            const uint4 u = *reinterpret_cast<const uint4*>(vt + row * C::kRow + (((8 * s + g) ^ sw) << 4));
+            y[kt][x][0] = u.x;
+            y[kt][x][1] = u.y;
+            y[kt][x][2] = u.z;
+            y[kt][x][3] = u.w;
+          } else {
+            const uint2 u = *reinterpret_cast<const uint2*>(vt + row * C::kRow + (((g >> 1) ^ sw) << 4) +
+                                                            8 * (g & 1));
+            y[kt][x][0] = u.x;
+            y[kt][x][1] = u.y;
+          }
+        }
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) {
-                  if constexpr (C::kKK == 8)
-                    mma_k8(sum[i], pa[kt][x].x, pa[kt][x].y, b[kt][i][0]);
-                  else
-                    mma<T>(sum[i], pa[kt][x], b[kt][i][0], b[kt][i][1]);
-                }
-              if constexpr (C::k8) {
-                if (x > 0) {
+      for (int q = 0; q < kWords; ++q) {
+        constexpr int kPer = C::k8 ? 4 : C::kF32 ? 1 : 2;      // channels of a word
+        float sum[kPer][4];
 #pragma unroll
-                  for (int i = 0; i < kPer; ++i)
+        for (int i = 0; i < kPer; ++i)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) sum[i][k] *= kRest;
-                }
+          for (int x = 0; x < 4; ++x)
+            sum[i][x] = 0.f;
+        if constexpr (C::kF32) {
+#pragma unroll
+          for (int kt = 0; kt < kK; ++kt) {
+            const auto& v = y[kt];
+            uint32_t h0, l0, h1, l1;
+            split_tf32(__uint_as_float(v[0][q]), h0, l0);
+            split_tf32(__uint_as_float(v[1][q]), h1, l1);
+            mma<T>(sum[0], pa[kt][0], l0, l1);
+            mma<T>(sum[0], pa[kt][0], h0, h1);
+          }
+        } else {
+          uint32_t b[kK][kPer][2];
+#pragma unroll
+          for (int kt = 0; kt < kK; ++kt) {
+            const auto& v = y[kt];
+            if constexpr (C::k8) {
+              constexpr bool kI8 = T == SA_DTYPE_INT8;
+              codes4_to_f16<kI8>(__byte_perm(v[0][q], v[1][q], 0x5140), b[kt][0][0], b[kt][1][0]);
+              codes4_to_f16<kI8>(__byte_perm(v[0][q], v[1][q], 0x7362), b[kt][2][0], b[kt][3][0]);
+              codes4_to_f16<kI8>(__byte_perm(v[2][q], v[3][q], 0x5140), b[kt][0][1], b[kt][1][1]);
+              codes4_to_f16<kI8>(__byte_perm(v[2][q], v[3][q], 0x7362), b[kt][2][1], b[kt][3][1]);
+            } else {
+              b[kt][0][0] = __byte_perm(v[0][q], v[1][q], 0x5410);
+              b[kt][1][0] = __byte_perm(v[0][q], v[1][q], 0x7632);
+              if constexpr (kVR == 4) {
+                b[kt][0][1] = __byte_perm(v[2][q], v[3][q], 0x5410);
+                b[kt][1][1] = __byte_perm(v[2][q], v[3][q], 0x7632);
               }
             }
           }
 #pragma unroll
-          for (int i = 0; i < kPer; ++i) {
-            const int j = C::kEP * s + kPer * q + i;
-            if constexpr (R == 8) {                              // the remainders' row joins its own
-              if constexpr (C::k8)
-                fma2(sum[i][0], sum[i][1], sum[i][2], sum[i][3], kRest);
-              else
-                add2(sum[i][0], sum[i][1], sum[i][2], sum[i][3]);
-              add2(o[j][0], o[j][1], sum[i][0], sum[i][1]);
-            } else {
-              add2(o[j][0], o[j][1], sum[i][0], sum[i][1]);
-              add2(o[j][2], o[j][3], sum[i][2], sum[i][3]);
+          for (int x = C::kPP - 1; x >= 0; --x) {              // (small parts first)
+#pragma unroll
+            for (int kt = 0; kt < kK; ++kt)
+#pragma unroll
+              for (int i = 0; i < kPer; ++i) {
+                if constexpr (C::kKK == 8 && R == 16) {
+                  if (x == 0)
+                    mma_k8(sum[i], pa[kt][0].x, pa[kt][0].y, b[kt][i][0]);
+                  else
+                    mma<T>(sum[i], pa[kt][x], b[kt][i][0], b[kt][i][0]);
+                } else {
+                  mma<T>(sum[i], pa[kt][x], b[kt][i][0], b[kt][i][C::kKK == 8 ? 0 : 1]);
+                }
+              }
+            if constexpr (C::k8) {
+              if (x > 0) {
+#pragma unroll
+                for (int i = 0; i < kPer; ++i)
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) sum[i][k] *= kRest;
+              }
             }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int j = C::kEP * s + kPer * q + i;
+          if constexpr (R == 8) {                              // the remainders' row joins its own
+            if constexpr (C::k8)
+              fma2(sum[i][0], sum[i][1], sum[i][2], sum[i][3], kRest);
+            else
+              add2(sum[i][0], sum[i][1], sum[i][2], sum[i][3]);
+            add2(o[j][0], o[j][1], sum[i][0], sum[i][1]);
+          } else {
+            add2(o[j][0], o[j][1], sum[i][0], sum[i][1]);
+            add2(o[j][2], o[j][3], sum[i][2], sum[i][3]);
           }
         }
       }
