@@ -192,14 +192,15 @@ __device__ __forceinline__ void split_f16(float x0, float x1, uint32_t& hi, uint
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(x1 - h.y), "f"(x0 - h.x));
 }
 // The same with the remainders times 1 / kRest: they stay in f16's normal range as long as the value
-// is above 2^-25, and end at 2^-36 of the unit instead of 2^-25.
+// is above 2^-25 (and below 2^15), and end at 2^-36 of the unit instead of 2^-25.
 constexpr float kRest = 0x1p-11f;
 __device__ __forceinline__ void split_f16_apart(float x0, float x1, uint32_t& hi, uint32_t& lo) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(x1), "f"(x0));
   const float2 h = f16x2_to_f32(hi);
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;"
-      : "=r"(lo)
-      : "f"((x1 - h.y) * (1.f / kRest)), "f"((x0 - h.x) * (1.f / kRest)));
+  float a = x0, b = x1, c = 0.f, d = 0.f;
+  fma2(a, b, h.x, h.y, -1.f);
+  fma2(c, d, a, b, 1.f / kRest);
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(d), "f"(c));
 }
 // Two values as three bf16 parts (24 bits together).
 __device__ __forceinline__ void split_bf16(float x0, float x1, uint32_t& hi, uint32_t& mid,
@@ -684,10 +685,10 @@ struct Worker {
   // cut at every step, always towards zero: 1.4e-5 over 64 sequences of 4096 to 32768 bf16 keys
   // (6e-7 with the additions), 2.4e-4 over 1700 tiles of 8 bits a warp.
   // Over 8 bits what P vs loses to f16 stays in a second part, 2^11 times as large (see
-  // split_f16_apart): with 8 rows in rows g + 8, with 16 in products of its own, made first and
-  // scaled before the others join.  Together with the additions this costs bf16 queries, whose output
-  // hides less, 2 % with 8 q-heads a kv head and 27 % with 16 (32 sequences of 20000 to 50000 keys, without /
-  // with: e4m3 394 / 400 and 419 / 534 us, int8 405 / 415 and 475 / 601).
+  // split_f16_apart): with 8 rows in rows g + 8, with 16 in products of its own.  Together with the
+  // additions this costs bf16 queries, whose output hides less, 0 to 4 % with 8 q-heads a kv head and
+  // 21 to 24 % with 16 (32 sequences of 20000 to 50000 keys, heads of 128, without / with:
+  // e4m3 374 / 373 and 401 / 498 us, int8 388 / 405 and 463 / 561).
   __device__ __forceinline__ void values(int e, const float (&p)[C::kNT][2 * C::kNR]) {
     constexpr int kK = C::kKT / C::kKK;            // k-steps of the tile
     const unsigned char* vt = ring + e * C::kEntry;
@@ -771,12 +772,11 @@ struct Worker {
 #pragma unroll
       for (int q = 0; q < kWords; ++q) {
         constexpr int kPer = C::k8 ? 4 : C::kF32 ? 1 : 2;      // channels of a word
-        float sum[kPer][4];
+        float sum[kPer][4], rest[kPer][4];                     // (rest: over 8 bits with 16 rows)
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            sum[i][x] = 0.f;
+          for (int x = 0; x < 4; ++x) sum[i][x] = rest[i][x] = 0.f;
         if constexpr (C::kF32) {
 #pragma unroll
           for (int kt = 0; kt < kK; ++kt) {
@@ -807,30 +807,28 @@ struct Worker {
               }
             }
           }
+          // products of one channel after the other where the remainders ride along (32 sequences, heads of
+          // 64, e4m3 under f32 queries: 443 us, the other way 463), of a word's channels side by side where
+          // they have their own (16 q-heads a kv head, e4m3 under bf16 queries: 498 us, 523)
+          constexpr int kSide = R == 16 ? kPer : 1;
 #pragma unroll
-          for (int x = C::kPP - 1; x >= 0; --x) {              // (small parts first)
+          for (int i0 = 0; i0 < kPer; i0 += kSide)
 #pragma unroll
-            for (int kt = 0; kt < kK; ++kt)
+            for (int x = C::kPP - 1; x >= 0; --x)                // (small parts first)
 #pragma unroll
-              for (int i = 0; i < kPer; ++i) {
-                if constexpr (C::kKK == 8 && R == 16) {
-                  if (x == 0)
-                    mma_k8(sum[i], pa[kt][0].x, pa[kt][0].y, b[kt][i][0]);
-                  else
-                    mma<T>(sum[i], pa[kt][x], b[kt][i][0], b[kt][i][0]);
-                } else {
-                  mma<T>(sum[i], pa[kt][x], b[kt][i][0], b[kt][i][C::kKK == 8 ? 0 : 1]);
+              for (int kt = 0; kt < kK; ++kt)
+#pragma unroll
+                for (int i = i0; i < i0 + kSide; ++i) {
+                  float (&to)[4] = C::k8 && x > 0 ? rest[i] : sum[i];
+                  if constexpr (C::kKK == 8 && R == 16) {
+                    if (x == 0)
+                      mma_k8(to, pa[kt][0].x, pa[kt][0].y, b[kt][i][0]);
+                    else
+                      mma<T>(to, pa[kt][x], b[kt][i][0], b[kt][i][0]);
+                  } else {
+                    mma<T>(to, pa[kt][x], b[kt][i][0], b[kt][i][C::kKK == 8 ? 0 : 1]);
+                  }
                 }
-              }
-            if constexpr (C::k8) {
-              if (x > 0) {
-#pragma unroll
-                for (int i = 0; i < kPer; ++i)
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) sum[i][k] *= kRest;
-              }
-            }
-          }
         }
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
@@ -842,6 +840,10 @@ struct Worker {
               add2(sum[i][0], sum[i][1], sum[i][2], sum[i][3]);
             add2(o[j][0], o[j][1], sum[i][0], sum[i][1]);
           } else {
+            if constexpr (C::k8) {
+              fma2(sum[i][0], sum[i][1], rest[i][0], rest[i][1], kRest);
+              fma2(sum[i][2], sum[i][3], rest[i][2], rest[i][3], kRest);
+            }
             add2(o[j][0], o[j][1], sum[i][0], sum[i][1]);
             add2(o[j][2], o[j][3], sum[i][2], sum[i][3]);
           }
