@@ -46,8 +46,8 @@ template <> struct TypeOf<SA_DTYPE_E4M3> { static constexpr int size = 1; };
 template <> struct TypeOf<SA_DTYPE_INT8> { static constexpr int size = 1; };
 
 // T: the cache's type.  DP: head_dim rounded up to 64, 128 or 256 (channels behind it
-// are zeros).  R: query rows of a tile, 8 or 16.  B: bf16 queries, whose operands have
-// fewer parts (f32 caches take both types as they come).
+// are zeros).  R: query rows of a tile, 8 or 16.  B: bf16 queries, whose Q has fewer
+// parts (f32 caches take both types as they come).
 template <int T, int DP, int R, bool B>
 struct Cfg {
   static constexpr int kSize = TypeOf<T>::size;
@@ -65,7 +65,7 @@ struct Cfg {
   static constexpr int kKS = kLCH * kKPC;                       // k-steps of a row
   static constexpr int kNT = kKT / 8;                           // n-tiles of S
   static constexpr int kKK = kF32 || kKT == 8 ? 8 : 16;         // keys of one P V k-step
-  static constexpr int kVP = DP * kSize / 8 < 16 ? 8 : 16;      // bytes of V that a lane reads of a row at a time
+  static constexpr int kVP = DP * kSize / 8 < 16 ? 8 : 16;      // bytes of a V row that a lane reads at a time
   static constexpr int kEP = kVP / kSize;                       // .. channels
   static constexpr int kNS = DP / (8 * kEP);                    // .. times
   static constexpr int kNJ = DP / 8;                            // n-tiles of o
@@ -84,16 +84,16 @@ struct Cfg {
   static constexpr int kNE = 3;
   static constexpr int kPerWarp = kNE * (kEntry + kScales) + kQBytes + kInfos * 16;
   static constexpr int kMost = 220 * 1024;                      // (of 227 KB, some of them static)
-  // Warps hide the instructions' latencies from each other (int8, 32 sequences of 20000 to
-  // 50000 keys: 12 warps 392 us, 8 warps 430; e4m3 with heads of 64: 16 warps 408, 12 454, 8 555).
+  // Warps hide the instructions' latencies from each other (bf16 queries, int8, 32 sequences of 20000
+  // to 50000 keys: 12 warps 405 us, 8 warps 446; e4m3 with heads of 64: 16 warps 426, 12 475, 8 575).
   // Their number is a multiple of 4, as their ranges are equal and the four schedulers
   // share them (10 warps instead of 12: 1130 instead of 750 us).  bf16 keys ask for
-  // few instructions; there more copies at a time only cost (12 warps 757 us, 8 719).
+  // few instructions; there more copies at a time only cost (64 sequences: 12 warps 732 us, 8 726).
   static constexpr int kWarpsMost = T == SA_DTYPE_BF16 ? 8 : decode_max_warps(DP, R);
   static constexpr int kWarpsSmem = kMost / kPerWarp / 4 * 4;
   static constexpr int kW = kWarpsSmem < kWarpsMost ? kWarpsSmem : kWarpsMost;      // warps
   // An SM does best with some 64 KB in flight.  Where two entries a warp would be more, V's copies
-  // wait until the tile before is done with (e4m3, 64 sequences, 12 warps: 736 us, at once 761).
+  // wait until the tile before is done with (e4m3, 64 sequences, 12 warps: 743 us, at once 755).
   static constexpr bool kLate = 2 * kW * kEntry > 64 * 1024;
   static constexpr int kThreads = 32 * kW;
   static constexpr int kSmem = kW * kPerWarp;
@@ -977,7 +977,7 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
   __shared__ int64_t s_chunk[kChunks];         // tiles (of one item) of pieces of the batch
   __shared__ PieceInfo s_piece[2 * C::kW];     // of warp w: [2 w] the one it began with, [2 w + 1] its last
   __shared__ int s_order[2 * C::kW];           // pieces that there are, in order
-  __shared__ int4 s_group[2 * C::kW];          // groups: item, its pieces in that order, their number, 1 starts | 2 ends
+  __shared__ int4 s_group[2 * C::kW];          // groups: item, first piece, their number, 1 starts | 2 ends
   __shared__ int s_groups;
   __shared__ float s_weight[2 * C::kW][R];     // of a piece's o in its group, in that order
   __shared__ float s_stat[2 * C::kW][3][R];    // m, n, l of a group
@@ -1026,7 +1026,8 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
   if (t0 < t1) {
     int k = 0;
 #pragma unroll 1
-    for (; in_seq >= s_chunk[k] * a.items_per_seq; ++k) in_seq -= s_chunk[k] * a.items_per_seq;   // (t0 < total)
+    for (; in_seq >= s_chunk[k] * a.items_per_seq; ++k)        // (t0 < total)
+      in_seq -= s_chunk[k] * a.items_per_seq;
     // (lengths that change under the call may leave it without an answer: then the last sequence's)
     b0 = a.batch - 1;
 #pragma unroll 1

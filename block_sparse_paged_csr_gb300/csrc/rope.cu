@@ -179,9 +179,10 @@ __device__ __forceinline__ void store_piece(void* p, int64_t off, const pair_t (
 // token and pair, by the CTA, and stay in registers; weights come from shared memory.
 //
 // Bound by memory from some thousand tokens on: 8192 of 64 + 8 heads of 128 in f32 (604 MB) 93 us,
-// 6.5 TB/s, 32768 350 us, 6.9; 32768 in bf16 (1.2 GB) 210 us, 5.7 TB/s.  bf16 is bound by instructions
-// as soon as they are not few: 4 channels a piece and one number an operation took 288 us there, 8
-// and two numbers take 210.  What counts besides is rows in flight against CTAs an SM:
+// 6.5 TB/s, 32768 350 us, 6.9; 32768 in bf16 (1.2 GB) 210 us, 5.7 TB/s.  bf16 stands between: 8192
+// tokens keep issue and DRAM 55 % busy each, with 80 registers and a third of the warps; fewer
+// instructions helped (4 channels a piece and one number an operation: 288 us for 32768, 8 and two
+// numbers 210), what is left is latency.  Rows in flight against CTAs an SM:
 //   bf16, 8 channels, 32768 tokens: 3 rows and 3 CTAs 211 us, 2 and 3 221, 2 and 4 211, 3 and 2 248;
 // and, with four tokens a CTA,
 //   f32, 2048 tokens / 8192: 3 and 4 29.7 / 97.5, 3 and 3 37.4 / 99.7, 2 and 4 29.5 / 100.5, 2 and
@@ -343,7 +344,7 @@ norm_rope_kernel(const RopeArgs a, int log_tokens, int heads_per_cta) {
 
 // Any sizes, strides and alignment: a warp per row, a lane per pair (and per
 // channel behind the rotated ones), angles made where they are used (8192 tokens of 64 + 8
-// heads in f32 whose rows start off 16 bytes: 411 us, the other kernel 100).
+// heads in f32 whose rows start off 16 bytes: 411 us, the other kernel 93).
 template <bool kSrcBf16, bool kDstBf16>
 __global__ void __launch_bounds__(kThreads) norm_rope_any_kernel(const RopeArgs a) {
   constexpr int kPairs = 4, kRest = 8;                 // of a lane: head_dim <= 256
@@ -439,7 +440,8 @@ cudaError_t launch_wide(const RopeArgs& a, cudaStream_t stream) {
   // 800 7.3 / 10.9; 8 + 1 heads (1 turn): bf16 500 tokens (2 rounds) 4.3 / 5.8.
   const int64_t slots = static_cast<int64_t>(kMinCtas<kC>) * device_sm_count();
   const int64_t rounds = (a.tq * ((total + groups - 1) / groups) + slots - 1) / slots;
-  const int64_t turns = ((static_cast<int64_t>(total) << kLogTokens<kC>) + kRows * groups - 1) / (kRows * groups);
+  const int64_t turns =
+      ((static_cast<int64_t>(total) << kLogTokens<kC>) + kRows * groups - 1) / (kRows * groups);
   const bool few = 2 * rounds <= turns + 1;
   const int log_tokens = few ? 0 : kLogTokens<kC>;
   const int heads_per_cta = few ? groups : total;

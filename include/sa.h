@@ -697,7 +697,8 @@ sa_status sa_select_blocks(const void *q, sa_dtype q_dtype, int64_t tq, int32_t 
  * in order: HEAD_COUNT (hq + hkv = 0), HEAD_DIM (rot_dim odd or above head_dim),
  * SHAPE (tq, n_axes), CU_SEQLENS and SHAPE (n_axes = 0), INVALID_ARGUMENT (types, eps
  * negative or NaN, freq_axes without positions), UNSUPPORTED, INVALID_ARGUMENT
- * (NULL; strides of an output below head_dim, of more than one token or head); on device: SHAPE (an axis outside [0, n_axes), taken as axis 0).
+ * (NULL; strides at which an output's rows share elements); on device: SHAPE (an
+ * axis outside [0, n_axes), taken as axis 0).
  */
 sa_status sa_norm_rope(const void *q, const void *k, sa_dtype src_dtype, int64_t q_token_stride,
                        int64_t q_head_stride, int64_t k_token_stride, int64_t k_head_stride,
@@ -719,8 +720,8 @@ sa_status sa_norm_rope(const void *q, const void *k, sa_dtype src_dtype, int64_t
  *
  *   k, v          [tq, hkv, head_dim] of dst_dtype (f32 or bf16), written;
  *                 channels contiguous, tokens and heads at the given strides
- *                 (elements; multiples of 16 bytes, head_dim at least, where
- *                 there is more than one token or head)
+ *                 (elements; multiples of 16 bytes where there is more than one
+ *                 token or head), at which no rows share elements
  *
  * Other arguments as for sa_store_kv.  Values of 8-bit caches are code * scale in
  * f32, rounded to nearest even for bf16 (scales that sa_store_kv made are powers
